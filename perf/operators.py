@@ -377,7 +377,7 @@ def _plan(s):
     """The state's plan: taken once, and bound to the state's request where it has one."""
     if "plan" not in s:
         from broadcast_gemm_attention_gb300 import binding
-        plan = _idle.pop() if _idle else binding.Plan(4096, 8192, 32)
+        plan = _idle.pop() if _idle else binding.Plan(65536, 8192, 32)
         c = s["case"]
         if "map" in s:
             plan.plan(s["map"], c["users"], c["H"], c.get("Lq", 8))
