@@ -746,8 +746,10 @@ __device__ void att_softmax(const AttnParams& p, const AttSmem& s, uint32_t tmem
         if (!__all_sync(0xffffffffu, (cw & 0xFFu) == (g & 0xFFu)) && !chain_wait(p, s, ln.r, g, mprev)) return;
         if (jt == 0) mprev = -INFINITY;
         // tcgen05.ld/st are warp-collective: the rescale decision must be
-        // uniform across the warp, so any row that needs it moves all 32
-        const bool rescale = __any_sync(0xffffffffu, mx > mprev + RESCALE_THRESHOLD);
+        // uniform across the warp, so any row that needs it moves all 32.  Rows
+        // behind the tile's last candidate (Lq does not divide 128) hold whatever
+        // shared memory held: they have no vote, or results would not repeat
+        const bool rescale = __any_sync(0xffffffffu, row_in_tile && mx > mprev + RESCALE_THRESHOLD);
         const float mj = rescale ? chain_value(fmaxf(mprev, mx)) : mprev;
         chain_post(s, ln.r, g + 1, mj);
         if (mj != mref) {  // this group's sum follows the reference (l = 0 on its first tile)
