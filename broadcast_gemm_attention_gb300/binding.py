@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libikbo.so")
 
 STATUS_NAMES = {0: "IKBO_OK", 1: "IKBO_ERR_INVALID_ARG", 2: "IKBO_ERR_UNSUPPORTED", 3: "IKBO_ERR_CUDA",
                 4: "IKBO_ERR_MAP_OUT_OF_RANGE", 5: "IKBO_ERR_TIMEOUT", 6: "IKBO_ERR_NOT_PLANNED",
-                7: "IKBO_ERR_INTERNAL"}
+                7: "IKBO_ERR_INTERNAL", 8: "IKBO_ERR_OUT_OF_PAGES", 9: "IKBO_ERR_CACHE"}
 IKBO_OK = 0
 IKBO_ERR_INVALID_ARG = 1
 IKBO_ERR_UNSUPPORTED = 2
@@ -29,11 +29,13 @@ IKBO_ERR_MAP_OUT_OF_RANGE = 4
 IKBO_ERR_TIMEOUT = 5
 IKBO_ERR_NOT_PLANNED = 6
 IKBO_ERR_INTERNAL = 7
+IKBO_ERR_OUT_OF_PAGES = 8
+IKBO_ERR_CACHE = 9
 DEBUG_WITHHOLD_USER_PARTIAL = 1
 DEBUG_NO_COOPERATIVE = 2
 
 # every function the header declares: name -> (restype, argtypes)
-_vp, _i, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64
+_vp, _i, _u64, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_double
 SIGNATURES = {
     "ikbo_plan_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i]),
     "ikbo_plan": (_i, [_vp, _vp, _i, _i, _i, _i, _vp]),
@@ -49,6 +51,17 @@ SIGNATURES = {
     "ikbo_attn_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, ctypes.c_float,
                                 _vp]),
     "ikbo_attn_self_target_forward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, ctypes.c_float, _vp]),
+    "ikbo_rope_frequencies": (_i, [_vp, _i, _f64, _i, _f64, _f64, _f64, _f64]),
+    "ikbo_rope_create": (_i, [ctypes.POINTER(_vp), _i, _vp, _i, ctypes.c_float]),
+    "ikbo_rope_destroy": (None, [_vp]),
+    "ikbo_rope_forward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
+    "ikbo_rope_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
+    "ikbo_qcache_bytes": (_u64, [_i, _i, _i]),
+    "ikbo_qcache_resize": (_i, [_vp, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp]),
+    "ikbo_qcache_append": (_i, [_vp, _vp, _vp, ctypes.c_int64, _vp, _i, _i, _i, _vp, _i, _i, _vp]),
+    "ikbo_qcache_load": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp]),
+    "ikbo_attn_qcache_forward": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _i, ctypes.c_float,
+                                      _vp]),
     "ikbo_plan_get_status": (_i, [_vp, _vp]),
     "ikbo_plan_set_debug": (_i, [_vp, ctypes.c_uint]),
     "ikbo_plan_set_timeout_ns": (_i, [_vp, _u64]),
@@ -335,6 +348,196 @@ def ikbo_attn_self_target_forward(plan: int, Q: torch.Tensor, Q_user: torch.Tens
            "ikbo_attn_self_target_forward")
 
 
+# ------------------------------------------------- rotary positions, 4-bit cache
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "turns": 3}
+ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+QCACHE_BLOCK_BYTES = 2560  # 16 tokens of one head
+QCACHE_MAX_USERS = 8192
+
+
+def _here(t: torch.Tensor, dtype, name: str) -> int:
+    """_dev, and the tensor lies on the current device (where the call launches)."""
+    ptr = _dev(t, dtype, name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return ptr
+
+
+def ikbo_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                          original_len: float = 1.0, low_turns: float = 0.0, high_turns: float = 1.0):
+    """The rot_dim / 2 frequencies (radians per position, floats) of a rotation:
+    scaling "none", "linear", "base" or "turns"."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = (ctypes.c_double * max(1, rot_dim // 2))()
+    _check(load().ikbo_rope_frequencies(ctypes.addressof(out), rot_dim, base, ROPE_SCALINGS[scaling], factor,
+                                        original_len, low_turns, high_turns), "ikbo_rope_frequencies")
+    return list(out)
+
+
+def ikbo_rope_create(rot_dim: int, freqs, interleaved: bool = False, magnitude: float = 1.0) -> int:
+    if len(freqs) != rot_dim // 2:
+        raise ValueError(f"freqs must hold rot_dim / 2 = {rot_dim // 2} values")
+    table = (ctypes.c_double * max(1, len(freqs)))(*freqs)
+    h = ctypes.c_void_p()
+    _check(load().ikbo_rope_create(ctypes.byref(h), rot_dim, ctypes.addressof(table), int(interleaved), magnitude),
+           "ikbo_rope_create")
+    return h.value
+
+
+def ikbo_rope_destroy(rope: int) -> None:
+    load().ikbo_rope_destroy(rope)
+
+
+def _rope(name: str, plan: int, rope: int, X: torch.Tensor, Y: torch.Tensor, start, broadcast: bool, stream) -> None:
+    for t, what in ((X, "input"), (Y, "output")):
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{what} is on {t.device}, not on the current device")
+    if X.dtype not in ROPE_DTYPES or Y.dtype != X.dtype:
+        raise ValueError("input and output must share a dtype: bfloat16, float16 or float32")
+    if X.shape != Y.shape or X.dim() not in (3, 4):
+        raise ValueError("input and output must share a shape [n, H, L, d] or [rows, H, d]")
+    if X.shape[-1] > 1 and (X.stride(-1) != 1 or Y.stride(-1) != 1):
+        raise ValueError("the last dimension must be contiguous")
+    if X.dim() == 4:
+        n, H, L, d = X.shape
+        xs, ys = X.stride()[:3], Y.stride()[:3]
+    else:
+        n, H, d = X.shape
+        L, xs, ys = 1, X.stride()[:2] + (0,), Y.stride()[:2] + (0,)
+    sptr = None
+    if start is not None:
+        sptr = _here(start, torch.int32, "start")
+        if start.dim() != 1 or (not broadcast and start.numel() != n):
+            raise ValueError("start must be [n], or [n_users] with broadcast")
+    i64x3 = ctypes.c_int64 * 3
+    cx, cy = i64x3(*xs), i64x3(*ys)
+    _check(getattr(load(), name)(plan, rope, X.data_ptr(), ctypes.addressof(cx), Y.data_ptr(), ctypes.addressof(cy),
+                                 sptr, int(broadcast), ROPE_DTYPES[X.dtype], n, H, L, d, _stream(stream)), name)
+
+
+def ikbo_rope_forward(plan: int, rope: int, X: torch.Tensor, Y: torch.Tensor, start: Optional[torch.Tensor] = None,
+                      broadcast: bool = False, stream=None) -> None:
+    """Y = X [n, H, L, d] (or [rows, H, d]: one token each) with its pairs rotated by the
+    angles of positions start[i] + l; with broadcast start[map[i]] + l of the planned
+    request (start then holds one position per user).  Y may be X."""
+    _rope("ikbo_rope_forward", plan, rope, X, Y, start, broadcast, stream)
+
+
+def ikbo_rope_backward(plan: int, rope: int, dY: torch.Tensor, dX: torch.Tensor, start: Optional[torch.Tensor] = None,
+                       broadcast: bool = False, stream=None) -> None:
+    """Gradient of ikbo_rope_forward: dX from dY."""
+    _rope("ikbo_rope_backward", plan, rope, dY, dX, start, broadcast, stream)
+
+
+def ikbo_qcache_bytes(n_pages: int, page: int, H: int) -> int:
+    """Bytes of a cache's data (0 for sizes outside the limits)."""
+    return int(load().ikbo_qcache_bytes(n_pages, page, H))
+
+
+def _qcache(data: torch.Tensor, page: int):
+    ptr = _here(data, torch.uint8, "data")
+    if data.dim() != 4 or page < 16 or data.shape[2] * 16 != page or data.shape[3] != QCACHE_BLOCK_BYTES:
+        raise ValueError(f"data must be [n_pages, H, page // 16, {QCACHE_BLOCK_BYTES}]")
+    return ptr, data.shape[0], data.shape[1]
+
+
+def _qtable(table: torch.Tensor, lens: torch.Tensor):
+    tptr, lptr = _here(table, torch.int32, "table"), _here(lens, torch.int32, "lens")
+    if table.dim() != 2 or lens.dim() != 1 or lens.numel() != table.shape[0]:
+        raise ValueError("table must be [n_users, max_blocks] and lens [n_users]")
+    return tptr, lptr, table.shape[0], table.shape[1]
+
+
+def ikbo_qcache_resize(plan: int, lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor, page: int,
+                       free: torch.Tensor, n_free: torch.Tensor, slots: torch.Tensor, slot_offsets: torch.Tensor,
+                       positions: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Set every user's length: pages are taken from and given back to the free list,
+    and each added token gets its slot (and position).  lens, table, free and n_free
+    change in place; all or nothing."""
+    tptr, lptr, n_users, max_blocks = _qtable(table, lens)
+    if new_lens.shape != lens.shape or tuple(slot_offsets.shape) != (n_users + 1,) or n_free.numel() != 1 or \
+            free.dim() != 1 or slots.dim() != 1 or (positions is not None and positions.shape != slots.shape):
+        raise ValueError("inconsistent cache shapes")
+    i32 = torch.int32
+    _check(load().ikbo_qcache_resize(plan, lptr, _here(new_lens, i32, "new_lens"), n_users, tptr, max_blocks, page,
+                                     _here(free, i32, "free"), _here(n_free, i32, "n_free"), free.numel(),
+                                     _here(slots, i32, "slots"), _here(slot_offsets, i32, "slot_offsets"),
+                                     None if positions is None else _here(positions, i32, "positions"), slots.numel(),
+                                     _stream(stream)), "ikbo_qcache_resize")
+
+
+def ikbo_qcache_append(plan: int, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, data: torch.Tensor,
+                       page: int, stream=None) -> None:
+    """Quantise row r of K and V ([n_rows, H, 128] bf16; rows may be strided, both
+    alike) into slot slots[r] of the cache (-1: skipped)."""
+    dptr, n_pages, H = _qcache(data, page)
+    for t, name in ((K, "K"), (V, "V")):
+        if not t.is_cuda or t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be a CUDA tensor of bfloat16")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if K.dim() != 3 or K.shape != V.shape or K.shape[1] != H or tuple(slots.shape) != (K.shape[0],):
+        raise ValueError("K and V must be [n_rows, H, d] and slots [n_rows]")
+    n, _, d = K.shape
+    strides = {(t.stride(0) if n > 1 else max(t.stride(0), H * d)) for t in (K, V)}
+    for t in (K, V):
+        if n and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+            raise ValueError("the heads of a row must be contiguous")
+    if n > 1 and len(strides) != 1:
+        raise ValueError("K and V must have the same row stride")
+    stride = max(strides) if n > 1 else (H * d + 7) // 8 * 8
+    _check(load().ikbo_qcache_append(plan, K.data_ptr(), V.data_ptr(), stride, _here(slots, torch.int32, "slots"), n,
+                                     H, d, dptr, n_pages, page, _stream(stream)), "ikbo_qcache_append")
+
+
+def ikbo_qcache_load(plan: int, data: torch.Tensor, page: int, table: torch.Tensor, lens: torch.Tensor,
+                     kv_offsets: torch.Tensor, K: Optional[torch.Tensor], V: Optional[torch.Tensor],
+                     stream=None) -> None:
+    """Read histories back as jagged bf16 rows: token t of user u to row
+    kv_offsets[u] + t of K and V [rows, H, 128] (either may be None)."""
+    dptr, n_pages, H = _qcache(data, page)
+    tptr, lptr, n_users, max_blocks = _qtable(table, lens)
+    if tuple(kv_offsets.shape) != (n_users + 1,):
+        raise ValueError("kv_offsets must be [n_users + 1]")
+    some = K if K is not None else V
+    if some is None:
+        raise ValueError("K, V or both must be given")
+    for t in (K, V):
+        if t is not None and (t.dim() != 3 or t.shape != some.shape or t.shape[1] != H):
+            raise ValueError("K and V must be [rows, H, d]")
+    kptr = None if K is None else _here(K, torch.bfloat16, "K")
+    vptr = None if V is None else _here(V, torch.bfloat16, "V")
+    _check(load().ikbo_qcache_load(plan, dptr, n_pages, page, H, some.shape[2], tptr, max_blocks, lptr, n_users,
+                                   _here(kv_offsets, torch.int32, "kv_offsets"), kptr, vptr, some.shape[0],
+                                   _stream(stream)), "ikbo_qcache_load")
+
+
+def ikbo_attn_qcache_forward(plan: int, Q: torch.Tensor, data: torch.Tensor, page: int, table: torch.Tensor,
+                             lens: torch.Tensor, O: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                             Lkv: Optional[int] = None, scale: Optional[float] = None, stream=None) -> None:
+    """ikbo_attn_forward's definition over the cache: user u's keys are the lens[u]
+    tokens of its pages.  Lkv: a bound on the sum of the lengths (default: what the
+    table can hold); the call's workspace goes by it."""
+    dptr, n_pages, H_kv = _qcache(data, page)
+    tptr, lptr, n_users, max_blocks = _qtable(table, lens)
+    if Q.dim() != 4 or O.shape != Q.shape or Q.shape[1] % H_kv != 0 or \
+            (lse is not None and tuple(lse.shape) != tuple(Q.shape[:3])):
+        raise ValueError("inconsistent attention shapes")
+    d = Q.shape[-1]
+    if Lkv is None:
+        Lkv = min(n_users * max_blocks * page, 2**31 - 1)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    bf = torch.bfloat16
+    _check(load().ikbo_attn_qcache_forward(plan, _here(Q, bf, "Q"), dptr, n_pages, page, H_kv, tptr, max_blocks, lptr,
+                                           _here(O, bf, "O"), None if lse is None else _here(lse, torch.float32, "lse"),
+                                           max(1, int(Lkv)), d, float(scale), _stream(stream)),
+           "ikbo_attn_qcache_forward")
+
+
 def ikbo_plan_get_status(plan: int, stream=None) -> int:
     """Synchronises the stream; returns the device-detected status code (and clears it)."""
     return int(load().ikbo_plan_get_status(plan, _stream(stream)))
@@ -363,6 +566,7 @@ class Plan:
 
     def __init__(self, max_cand: int, max_users: int, max_heads: int = 1):
         self._map = None
+        self._request = None  # (n_cand, n_users, H, Lq) of the last plan()
         self.handle = ikbo_plan_create(max_cand, max_users, max_heads)
 
     def __enter__(self):
@@ -388,6 +592,7 @@ class Plan:
         # the plan borrows the map for every later call of this request: hold
         # the tensor so that a temporary passed here stays allocated
         self._map = map_
+        self._request = (map_.numel(), n_users, H, Lq)
 
     def lce_forward(self, U, C, Wu, Wc, b, Y, stream=None):
         ikbo_lce_forward(self.handle, U, C, Wu, Wc, b, Y, stream)
@@ -410,6 +615,27 @@ class Plan:
     def attn_self_target_forward(self, Q, Q_user, K, V, kv_offsets, O, O_user, scale=None, stream=None):
         ikbo_attn_self_target_forward(self.handle, Q, Q_user, K, V, kv_offsets, O, O_user, scale, stream)
 
+    def rope_forward(self, rope, X, Y, start=None, broadcast=False, stream=None):
+        ikbo_rope_forward(self.handle, rope.handle, X, Y, start, broadcast, stream)
+
+    def rope_backward(self, rope, dY, dX, start=None, broadcast=False, stream=None):
+        ikbo_rope_backward(self.handle, rope.handle, dY, dX, start, broadcast, stream)
+
+    def qcache_resize(self, lens, new_lens, table, page, free, n_free, slots, slot_offsets, positions=None, stream=None):
+        ikbo_qcache_resize(self.handle, lens, new_lens, table, page, free, n_free, slots, slot_offsets, positions, stream)
+
+    def qcache_append(self, K, V, slots, data, page, stream=None):
+        ikbo_qcache_append(self.handle, K, V, slots, data, page, stream)
+
+    def qcache_load(self, data, page, table, lens, kv_offsets, K, V, stream=None):
+        ikbo_qcache_load(self.handle, data, page, table, lens, kv_offsets, K, V, stream)
+
+    def attn_qcache_forward(self, Q, data, page, table, lens, O, lse=None, Lkv=None, scale=None, stream=None):
+        if self._request is not None and (Q.dim() != 4 or (Q.shape[0],) + tuple(Q.shape[1:3]) != self._request[:1] +
+                                          self._request[2:] or lens.numel() != self._request[1]):
+            raise ValueError("Q and lens must have the sizes of the planned request")
+        ikbo_attn_qcache_forward(self.handle, Q, data, page, table, lens, O, lse, Lkv, scale, stream)
+
     def status(self, stream=None) -> int:
         return ikbo_plan_get_status(self.handle, stream)
 
@@ -429,6 +655,24 @@ class Plan:
         w, n, cpu, mu = ikbo_plan_worklist(self.handle)
         n_units = int(_copy_i32(n, 1)[0])
         return _copy_i32(w, 4 * n_units).view(n_units, 4), cpu
+
+
+class Rope:
+    """Owns one ikbo_rope_t: the first rot_dim elements of a head, rotated by freqs
+    (radians per position; ikbo_rope_frequencies makes the usual ones)."""
+
+    def __init__(self, rot_dim: int, freqs=None, interleaved: bool = False, magnitude: float = 1.0):
+        self.handle = None
+        self.handle = ikbo_rope_create(rot_dim, ikbo_rope_frequencies(rot_dim) if freqs is None else freqs, interleaved,
+                                       magnitude)
+
+    def __del__(self):
+        try:
+            if self.handle:
+                ikbo_rope_destroy(self.handle)
+                self.handle = None
+        except Exception:
+            pass
 
 
 class _DeviceArray:

@@ -13,6 +13,7 @@
 
 #include "ikbo.h"
 #include "bwd_internal.h"
+#include "plan_internal.h"
 
 namespace ikbo {
 cudaError_t launch_seg_build(const SegParams& p, cudaStream_t s);
@@ -46,60 +47,6 @@ cudaError_t launch_attn_backward(const CUtensorMap& tmQ, const CUtensorMap& tmDO
 }  // namespace ikbo
 
 using namespace ikbo;
-
-struct ikbo_plan_s {
-  int device = 0;
-  int num_sms = 0;
-  size_t max_smem = 0;
-  int max_cand = 0, max_users = 0, max_heads = 0;
-  // the bound request
-  bool planned = false;
-  const int32_t* d_map = nullptr;
-  int n_cand = 0, n_users = 0, H = 0, Lq = 0, cands_per_unit = 0;
-  // plan-owned device memory
-  int32_t* d_counts = nullptr;
-  int32_t* d_offsets = nullptr;
-  int32_t* d_runs = nullptr;
-  int32_t* d_perm = nullptr;
-  int32_t* d_work = nullptr;
-  int32_t* d_n_units = nullptr;
-  int64_t max_units = 0;
-  uint32_t* d_status = nullptr;  // [0] status bits, [1] LCE flag-timeout word, [2] LCE finished-CTA count
-  float* d_partial = nullptr;
-  size_t partial_elems = 0;
-  uint32_t* d_flags = nullptr;
-  size_t flags_elems = 0;
-  // LCE backward workspaces (grown on first use)
-  float* d_bwd_S = nullptr;
-  size_t bwd_S_elems = 0;
-  uint16_t* d_bwd_Sb = nullptr;
-  size_t bwd_Sb_elems = 0;
-  float* d_bwd_seg = nullptr;
-  size_t bwd_seg_elems = 0;
-  float* d_bwd_wpart = nullptr;
-  size_t bwd_wpart_elems = 0;
-  float* d_bwd_spart = nullptr;  // candidate pass: S partials of each CTA's first and last run
-  size_t bwd_spart_elems = 0;
-  float* d_bwd_dbcta = nullptr;  // candidate pass: each CTA's share of db
-  size_t bwd_dbcta_elems = 0;
-  uint32_t* d_bwd_ctrl = nullptr;  // candidate pass: grid barrier counts
-  size_t bwd_ctrl_elems = 0;
-  // a second stream (created on first use) on which dW_u runs beside dU
-  cudaStream_t side = nullptr;
-  cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
-  // attention backward workspaces
-  float* d_abwd_lse = nullptr;
-  size_t abwd_lse_elems = 0;
-  float* d_abwd_drow = nullptr;
-  size_t abwd_drow_elems = 0;
-  int32_t* d_abwd_blk = nullptr;
-  size_t abwd_blk_elems = 0;
-  bool lce_flags_dirty = false;  // an LCE launch failed: its flags may still be set
-  uint32_t debug = 0;
-  uint64_t timeout_ns = 2000000000ull;
-  int lce_schedule = LCE_SCHEDULE_AUTO;
-  std::atomic<uint64_t> launches{0};
-};
 
 namespace {
 
@@ -139,8 +86,6 @@ bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Grows a plan workspace to `need` elements.  New memory is zeroed on
 // `stream`, the stream of the call that will use it, so the clear is ordered
@@ -183,6 +128,11 @@ void free_plan(ikbo_plan_t p) {
   cudaFree(p->d_abwd_lse);
   cudaFree(p->d_abwd_drow);
   cudaFree(p->d_abwd_blk);
+  cudaFree(p->d_qa_part);
+  cudaFree(p->d_qa_tickets);
+  cudaFree(p->d_qa_kv);
+  cudaFree(p->d_qa_ranges);
+  for (int i = 0; i < p->n_retired; ++i) cudaFree(p->retired[i]);
   delete p;
 }
 
@@ -260,12 +210,16 @@ ikbo_status_t lce_launch(ikbo_plan_t p, const void* U, const void* C, const void
 }
 }  // namespace
 
-namespace {
-// Both attention entry points: the work list's (target) units, plus, when
-// Q_user is given, n_users * H * ceil(Lq_u / 128) self units in the same launch.
-ikbo_status_t attn_launch(ikbo_plan_t p, const void* Q, const void* Q_user, const void* K, const void* V,
-                          const int32_t* d_kv_offsets, void* O, void* O_user, float* lse, int Lq_u, int Lkv, int d,
-                          float scale, cudaStream_t stream) {
+namespace ikbo {
+// Every attention forward: the work list's (target) units, plus, when Q_user
+// is given, n_users * H * ceil(Lq_u / 128) self units in the same launch.
+ikbo_status_t attn_launch(ikbo_plan_s* p, const AttnCall& c, cudaStream_t stream) {
+  const void *Q = c.Q, *Q_user = c.Q_user, *K = c.K, *V = c.V;
+  const int32_t* d_kv_offsets = c.kv_offsets;
+  void *O = c.O, *O_user = c.O_user;
+  float* lse = c.lse;
+  const int Lq_u = c.Lq_u, Lkv = c.Lkv, d = c.d;
+  const float scale = c.scale;
   if (!p) return IKBO_ERR_INVALID_ARG;
   if (!p->planned) return IKBO_ERR_NOT_PLANNED;
   const bool self = Q_user != nullptr;
@@ -287,6 +241,8 @@ ikbo_status_t attn_launch(ikbo_plan_t p, const void* Q, const void* Q_user, cons
   ap.work = p->d_work;
   ap.n_units = p->d_n_units;
   ap.kv_offsets = d_kv_offsets;
+  ap.kv_lens = c.kv_lens;
+  ap.kv_group = p->H / c.H_kv;
   ap.O = static_cast<uint16_t*>(O);
   ap.lse = lse;
   ap.status = p->d_status;
@@ -322,8 +278,9 @@ ikbo_status_t attn_launch(ikbo_plan_t p, const void* Q, const void* Q_user, cons
     tmQu = tmQ;  // not read without self units
   }
   if (d_kv_offsets) {
-    const uint64_t kd[3] = {ATT_D, H, static_cast<uint64_t>(Lkv)};
-    const uint64_t ks[2] = {ATT_D * 2, H * ATT_D * 2};
+    const uint64_t Hk = static_cast<uint64_t>(c.H_kv);
+    const uint64_t kd[3] = {ATT_D, Hk, static_cast<uint64_t>(Lkv)};
+    const uint64_t ks[2] = {ATT_D * 2, Hk * ATT_D * 2};
     const uint32_t kbox[3] = {64, 1, ATT_BN};
     if (!encode_bf16(&tmK, K, 3, kd, ks, kbox) || !encode_bf16(&tmV, V, 3, kd, ks, kbox)) return IKBO_ERR_CUDA;
   } else {
@@ -337,7 +294,7 @@ ikbo_status_t attn_launch(ikbo_plan_t p, const void* Q, const void* Q_user, cons
   p->launches++;
   return IKBO_OK;
 }
-}  // namespace
+}  // namespace ikbo
 
 namespace {
 ikbo_status_t attn_backward_launch(ikbo_plan_t p, const void* Q, const void* K, const void* V, const void* O,
@@ -435,6 +392,8 @@ const char* ikbo_status_string(ikbo_status_t s) {
     case IKBO_ERR_TIMEOUT: return "device wait timed out";
     case IKBO_ERR_NOT_PLANNED: return "no request planned";
     case IKBO_ERR_INTERNAL: return "internal error (work list)";
+    case IKBO_ERR_OUT_OF_PAGES: return "not enough free cache pages";
+    case IKBO_ERR_CACHE: return "inconsistent cache lengths, pages or slots";
   }
   return "unknown status";
 }
@@ -575,6 +534,8 @@ ikbo_status_t ikbo_plan_get_status(ikbo_plan_t p, cudaStream_t stream) {
   if (word && cudaMemset(p->d_status, 0, sizeof(uint32_t)) != cudaSuccess) return IKBO_ERR_CUDA;
   if (word & DEV_ERR_MAP_RANGE) return IKBO_ERR_MAP_OUT_OF_RANGE;
   if (word & (DEV_ERR_FLAG_TIMEOUT | DEV_ERR_PIPE_TIMEOUT)) return IKBO_ERR_TIMEOUT;
+  if (word & DEV_ERR_OUT_OF_PAGES) return IKBO_ERR_OUT_OF_PAGES;
+  if (word & DEV_ERR_CACHE) return IKBO_ERR_CACHE;
   if (word & (DEV_ERR_BAD_WORK | DEV_ERR_SMEM_LAYOUT)) return IKBO_ERR_INTERNAL;
   return IKBO_OK;
 }
@@ -794,21 +755,23 @@ ikbo_status_t ikbo_lce_backward(ikbo_plan_t p, const void* U, const void* C, con
 ikbo_status_t ikbo_attn_forward(ikbo_plan_t p, const void* Q, const void* K, const void* V,
                                 const int32_t* d_kv_offsets, void* O, int Lkv, int d, float scale,
                                 cudaStream_t stream) {
-  return attn_launch(p, Q, nullptr, K, V, d_kv_offsets, O, nullptr, nullptr, 0, Lkv, d, scale, stream);
+  if (!p) return IKBO_ERR_INVALID_ARG;
+  return attn_launch(p, {Q, nullptr, K, V, d_kv_offsets, nullptr, O, nullptr, nullptr, 0, Lkv, d, p->H, scale}, stream);
 }
 
 ikbo_status_t ikbo_attn_forward_lse(ikbo_plan_t p, const void* Q, const void* K, const void* V,
                                     const int32_t* d_kv_offsets, void* O, float* lse, int Lkv, int d, float scale,
                                     cudaStream_t stream) {
   if (!lse || (reinterpret_cast<uintptr_t>(lse) & 3u)) return IKBO_ERR_INVALID_ARG;
-  return attn_launch(p, Q, nullptr, K, V, d_kv_offsets, O, nullptr, lse, 0, Lkv, d, scale, stream);
+  if (!p) return IKBO_ERR_INVALID_ARG;
+  return attn_launch(p, {Q, nullptr, K, V, d_kv_offsets, nullptr, O, nullptr, lse, 0, Lkv, d, p->H, scale}, stream);
 }
 
 ikbo_status_t ikbo_attn_self_target_forward(ikbo_plan_t p, const void* Q, const void* Q_user, const void* K,
                                             const void* V, const int32_t* d_kv_offsets, void* O, void* O_user,
                                             int Lq_u, int Lkv, int d, float scale, cudaStream_t stream) {
-  if (!Q_user) return IKBO_ERR_INVALID_ARG;
-  return attn_launch(p, Q, Q_user, K, V, d_kv_offsets, O, O_user, nullptr, Lq_u, Lkv, d, scale, stream);
+  if (!p || !Q_user) return IKBO_ERR_INVALID_ARG;
+  return attn_launch(p, {Q, Q_user, K, V, d_kv_offsets, nullptr, O, O_user, nullptr, Lq_u, Lkv, d, p->H, scale}, stream);
 }
 
 }  // extern "C"

@@ -197,7 +197,7 @@ __device__ __forceinline__ Unit decode(const AttnParams& p, int4 w) {
   }
   if (p.kv_offsets) {
     x.kv0 = p.kv_offsets[x.u];
-    x.L = p.kv_offsets[x.u + 1] - x.kv0;
+    x.L = p.kv_lens ? p.kv_lens[x.u] : p.kv_offsets[x.u + 1] - x.kv0;
     if (x.L < 0) x.L = 0;
   } else {
     x.kv0 = 0;
@@ -293,8 +293,9 @@ __device__ __forceinline__ void load_slots(const AttnParams& p, const Unit& x, Q
 __device__ __forceinline__ void load_kv_tile(const AttnParams& p, const CUtensorMap* tm, uint8_t* dst, uint64_t* bar,
                                              const Unit& x, int jt) {
   if (p.kv_offsets) {
-    tma_load_3d(dst, tm, bar, 0, x.h, x.kv0 + jt * ATT_BN);
-    tma_load_3d(dst + HALF_TILE, tm, bar, 64, x.h, x.kv0 + jt * ATT_BN);
+    const int hk = p.kv_group == 1 ? x.h : x.h / p.kv_group;
+    tma_load_3d(dst, tm, bar, 0, hk, x.kv0 + jt * ATT_BN);
+    tma_load_3d(dst + HALF_TILE, tm, bar, 64, hk, x.kv0 + jt * ATT_BN);
   } else {
     tma_load_4d(dst, tm, bar, 0, jt * ATT_BN, x.h, x.u);
     tma_load_4d(dst + HALF_TILE, tm, bar, 64, jt * ATT_BN, x.h, x.u);

@@ -18,6 +18,8 @@ enum : uint32_t {
   DEV_ERR_PIPE_TIMEOUT = 1u << 2,  // an mbarrier wait inside a kernel ran out
   DEV_ERR_BAD_WORK = 1u << 3,      // inconsistent attention work unit
   DEV_ERR_SMEM_LAYOUT = 1u << 4,   // dynamic shared memory too misaligned for the tile layout
+  DEV_ERR_OUT_OF_PAGES = 1u << 5,  // a resize wanted more pages than are free
+  DEV_ERR_CACHE = 1u << 6,         // a cache length, page, slot or offset out of range
 };
 
 // Debug switches (ikbo_plan_set_debug).
@@ -149,11 +151,13 @@ struct AttnParams {
   const int32_t* work;       // [n_units][4]: user, head, perm start, count
   const int32_t* n_units;    // device scalar written by the segment builder
   const int32_t* kv_offsets; // [n_users+1] or null (dense)
+  const int32_t* kv_lens;    // [n_users] or null: the keys of a user whose rows are followed by others' padding
   uint16_t* O;               // [n_cand][H][Lq][d]
   float* lse;                // [n_cand][H][Lq] natural-log row log-sum-exp, or null (not written)
   uint32_t* status;
   int n_cand, n_users, H, Lq, Lkv;  // Lkv: dense length (ignored when jagged)
   int cands_per_tile;        // floor(128 / Lq)
+  int kv_group;              // query heads that share a K/V head
   float scale_log2;          // scale * log2(e)
   uint64_t timeout_ns;
   // self units (users' own queries against the same K/V), after the work

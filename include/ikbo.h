@@ -9,11 +9,16 @@
  * and a candidate->user map, and never materialises the user tensors
  * replicated to n_cand -- not in memory, not on the bus, not in cache.
  *
- * Two operators are provided:
+ * Two operators and their gradients are provided:
  *   - Linear Compression Embedding (LCE, Type I, decomposable):
  *       Y[i] = W_u^T U[map[i]] + W_c^T C[i] + b
  *   - broadcast attention (Type II, broadcast inside the kernel):
  *       O[i,h] = softmax(Q[i,h] K[map[i],h]^T * scale) V[map[i],h]
+ * and, for users whose histories are kept between requests, what broadcast
+ * attention needs around it: rotary positions of queries and keys
+ * (ikbo_rope_*), a paged cache of 4-bit keys and values (ikbo_qcache_*) and
+ * the attention that reads it (ikbo_attn_qcache_forward).  The write-ups have
+ * no counterpart to these.
  *
  * Conventions for every entry point:
  *   - All tensor arguments are DEVICE pointers to row-major, contiguous
@@ -49,12 +54,17 @@ typedef enum {
   IKBO_ERR_MAP_OUT_OF_RANGE = 4,  /* device-detected: some map[i] outside [0, n_users) */
   IKBO_ERR_TIMEOUT = 5,           /* device-detected: a bounded wait inside a kernel gave up */
   IKBO_ERR_NOT_PLANNED = 6,       /* forward called before ikbo_plan */
-  IKBO_ERR_INTERNAL = 7           /* device-detected: inconsistent work list */
+  IKBO_ERR_INTERNAL = 7,          /* device-detected: inconsistent work list */
+  IKBO_ERR_OUT_OF_PAGES = 8,      /* device-detected: a cache resize wanted more pages than are free */
+  IKBO_ERR_CACHE = 9              /* device-detected: a cache length, page, slot or offset out of range */
 } ikbo_status_t;
 
 /* Opaque plan: owns the segment arrays, the attention work list, the fp32
  * user-partial workspace of LCE, its readiness flags and the status word. */
 typedef struct ikbo_plan_s* ikbo_plan_t;
+
+/* Opaque rotation (see ikbo_rope_create). */
+typedef struct ikbo_rope_s* ikbo_rope_t;
 
 /* Create a plan for requests of at most max_cand candidates, max_users users
  * and max_heads attention heads (each >= 1; max_users <= 8192).  Allocates
@@ -286,9 +296,171 @@ ikbo_status_t ikbo_attn_backward(ikbo_plan_t p, const void* Q, const void* K, co
                                  const void* dO, const float* lse, const int32_t* d_kv_offsets, void* dQ, void* dK,
                                  void* dV, int Lkv, int d, float scale, cudaStream_t stream);
 
+/* Rotary positions.  An ikbo_rope_t holds one rotation: which elements of a
+ * head pair up, each pair's frequency, and a factor on the result.  It is
+ * host memory only (its table travels with each launch), may be used by any
+ * number of plans and streams, and may be destroyed once the calls that use
+ * it have returned. */
+typedef enum { IKBO_BF16 = 0, IKBO_FP16 = 1, IKBO_FP32 = 2 } ikbo_dtype_t;
+
+typedef enum {
+  IKBO_ROPE_PLAIN = 0,  /* f_j = base^(-2j / rot_dim) */
+  IKBO_ROPE_LINEAR = 1, /* f_j / factor: positions interpolated */
+  IKBO_ROPE_BASE = 2,   /* base * factor^(rot_dim / (rot_dim - 2)) in place of base (rot_dim > 2, else plain) */
+  IKBO_ROPE_TURNS = 3   /* by the turns t_j = original_len f_j / 2 pi a pair makes over the original context: f_j from
+                           high_turns up, f_j / factor up to low_turns, linear in t_j between */
+} ikbo_rope_scaling_t;
+
+/* The frequencies (radians per position) of a rotation, freqs[rot_dim / 2] in
+ * host memory.  rot_dim even, 2..512; base, factor finite and > 0;
+ * original_len, low_turns and high_turns are read by IKBO_ROPE_TURNS alone
+ * (finite, original_len > 0, 0 <= low_turns < high_turns). */
+ikbo_status_t ikbo_rope_frequencies(double* freqs, int rot_dim, double base, int scaling, double factor,
+                                    double original_len, double low_turns, double high_turns);
+
+/* A rotation of the first rot_dim elements of a head (even, 2..512) by the
+ * given frequencies (radians per position, host memory, any finite values).
+ * interleaved 0: pair j is elements j and j + rot_dim/2; 1: elements 2j and
+ * 2j + 1.  magnitude (finite, non-zero; usually 1) multiplies the rotated
+ * elements.  *out is NULL on failure. */
+ikbo_status_t ikbo_rope_create(ikbo_rope_t* out, int rot_dim, const double* freqs, int interleaved, float magnitude);
+void ikbo_rope_destroy(ikbo_rope_t r);
+
+/* Y = X with pair j of row (i, h, l) rotated by the angle (start + l) f_j,
+ *   (x, y) -> magnitude (x cos - y sin, y cos + x sin);
+ * elements from rot_dim on are copied.  start = d_start[i], or with broadcast
+ * != 0 d_start[map[i]] with the map of the last ikbo_plan (then n must be its
+ * n_cand): a user's position serves all of its candidates, as its K/V does.
+ * d_start (int32, 4-byte aligned; any value, negative ones too) may be NULL: 0.
+ *   X, Y  [n][H][L][d] of dtype (ikbo_dtype_t), d <= 512, rot_dim <= d; the
+ *         last dimension is contiguous, the others have the element strides
+ *         x_strides / y_strides (host, 3 values: i, h, l), NULL: contiguous.
+ *         So Q is as it is for ikbo_attn_forward, jagged K has L = 1, H and
+ *         one d_start per row, and a slice of a wider projection needs no copy.
+ *         Aligned to their element size; 16-byte alignment of pointers and
+ *         strides with rot_dim a multiple of 16 and d of 8 runs faster.
+ *   Y may be X itself with the same strides (in place); other overlaps of X
+ *   and Y, and strides that make rows of Y overlap, are not allowed.
+ * Angles are exact to 2^-32 of a turn at any position (a position times a
+ * frequency is formed in 64-bit fixed point, where whole turns drop out);
+ * fp32 arithmetic, one rounding to dtype.  A candidate whose map value is out
+ * of range keeps its rows of Y and is reported by the plan's status.
+ * The plan need not be planned unless broadcast is set.  n = 0 launches
+ * nothing (X and Y may then be NULL). */
+ikbo_status_t ikbo_rope_forward(ikbo_plan_t p, ikbo_rope_t r, const void* X, const int64_t* x_strides, void* Y,
+                                const int64_t* y_strides, const int32_t* d_start, int broadcast, int dtype, int n,
+                                int H, int L, int d, cudaStream_t stream);
+
+/* Gradient of ikbo_rope_forward: dX from dY, the transposed rotation (by the
+ * opposite angle, with the same magnitude).  Arguments as there. */
+ikbo_status_t ikbo_rope_backward(ikbo_plan_t p, ikbo_rope_t r, const void* dY, const int64_t* dy_strides, void* dX,
+                                 const int64_t* dx_strides, const int32_t* d_start, int broadcast, int dtype, int n,
+                                 int H, int L, int d, cudaStream_t stream);
+
+/* A paged cache of users' keys and values in 4 bits.  All of its memory is
+ * the caller's:
+ *   data   uint8 [n_pages][H][page / 16][2560]: a page holds `page` tokens
+ *          (16, 32, .., 1024, a power of two) of H heads of 128 elements.
+ *          The 2560 bytes of 16 tokens of one head: keys' codes [16][64]
+ *          (element j in nibble j, low nibble first), keys' pairs (s, z)
+ *          [16][4] of two bf16, one pair for each group of 32 elements, then
+ *          codes and pairs of the values.  A code c stands for
+ *            bf16( z + (16 + c) s )
+ *          i.e. 5 bits an element.  (16 + c is what the bits 0x4180 | c << 3
+ *          are as a bf16, so decoding is one logic operation and one FMA.)
+ *   table  int32 [n_users][max_blocks]: user u's token t is in page
+ *          table[u][t / page], at t % page; slot = page number * page + place
+ *   lens   int32 [n_users]: tokens user u holds
+ * n_pages * page <= 2^31 - 1; data 16-byte, int32 arrays 4-byte aligned.
+ * The calls below take a plan for its status word, workspace and launch
+ * count; except for the attention it need not be planned.  Lengths outside
+ * [0, max_blocks * page], pages outside [0, n_pages), slots outside
+ * [0, n_pages * page) are skipped without being used and reported as
+ * IKBO_ERR_CACHE by ikbo_plan_get_status. */
+
+/* Bytes of `data` for these sizes (0 for sizes outside the limits). */
+uint64_t ikbo_qcache_bytes(int n_pages, int page, int H);
+
+/* Set every user's length, taking and giving back pages, on the device:
+ *   lens[u] -> new_lens[u] (which may be smaller, 0 included)
+ *   need_u = ceil(new_lens[u] / page), have_u = ceil(lens[u] / page)
+ * d_free int32 [n_pages] holds the free pages in its first *d_n_free places.
+ * Pages are taken from its end, users ascending and blocks ascending: the
+ * k-th page taken in the call is d_free[n_free - 1 - k].  Blocks given up
+ * (users ascending, blocks ascending) are then added to the end and become -1
+ * in the table.  d_lens, d_table, d_free and d_n_free are updated in place.
+ * Tokens added (users ascending, positions ascending; N in all) are numbered:
+ *   d_slots         int32 [max_new]: their slots; -1 from N on
+ *   d_slot_offsets  int32 [n_users + 1]: first token of each user; [n_users] = N
+ *   d_positions     int32 [max_new] or NULL: their positions in the history
+ *                   (the d_start of ikbo_rope_forward for their keys); 0 from N on
+ * so a call that gives every row of K and V its slot needs nothing from the
+ * host.  All or nothing: where the free pages do not suffice
+ * (IKBO_ERR_OUT_OF_PAGES), or a length, *d_n_free, or N > max_new is out of
+ * range (IKBO_ERR_CACHE), lengths, table and free list stay as they were,
+ * every slot is -1 and every offset 0.  Integer work, bit-exact.  n_users <=
+ * 8192; the arrays must not overlap.  One launch. */
+ikbo_status_t ikbo_qcache_resize(ikbo_plan_t p, int32_t* d_lens, const int32_t* d_new_lens, int n_users,
+                                 int32_t* d_table, int max_blocks, int page, int32_t* d_free, int32_t* d_n_free,
+                                 int n_pages, int32_t* d_slots, int32_t* d_slot_offsets, int32_t* d_positions,
+                                 int max_new, cudaStream_t stream);
+
+/* Quantise row r of K and V into slot d_slots[r] (-1: the row is skipped).
+ *   K, V  bf16 [n_rows][H][128], heads contiguous, rows row_stride elements
+ *         apart (>= H * 128, a multiple of 8; 16-byte aligned pointers), so
+ *         both may be slices of one projection
+ * Per group of 32 elements, lo and hi the smallest and largest:
+ *   s = bf16((hi/2 - lo/2) / 7.5),  z = bf16(lo - 16 s),
+ *   c = min(max(round((x - z) / s) - 16, 0), 15),   0 where s = 0
+ * in fp32, rounded to nearest even at each step; s = z = NaN for a group that
+ * holds an infinity or NaN or whose s or z overflows bf16, so that all of its
+ * values read as NaN.  Slots must be distinct (a slot given twice ends up with
+ * a mixture of the rows).  n_rows >= 0; one launch, none for 0 rows. */
+ikbo_status_t ikbo_qcache_append(ikbo_plan_t p, const void* K, const void* V, int64_t row_stride,
+                                 const int32_t* d_slots, int n_rows, int H, int d, void* data, int n_pages, int page,
+                                 cudaStream_t stream);
+
+/* Read histories back as the jagged bf16 K/V that the attention entry points
+ * take (for those that have no form over the cache):
+ *   token t of user u -> row kv_offsets[u] + t of K and V, bf16 [n_rows][H][128]
+ * d_kv_offsets int32 [n_users + 1], values in [0, n_rows], ascending; a
+ * history longer than its kv_offsets[u + 1] - kv_offsets[u] rows is cut there
+ * and reported (IKBO_ERR_CACHE).  Other rows are left as they are.  Blocks
+ * whose page is out of range are left out.  K or V may be NULL.  One launch. */
+ikbo_status_t ikbo_qcache_load(ikbo_plan_t p, const void* data, int n_pages, int page, int H, int d,
+                               const int32_t* d_table, int max_blocks, const int32_t* d_lens, int n_users,
+                               const int32_t* d_kv_offsets, void* K, void* V, int n_rows, cudaStream_t stream);
+
+/* Broadcast attention over the cache: ikbo_attn_forward's definition with
+ * K[u], V[u] the lens[u] tokens of user u in the cache,
+ *   O[i,h,q,:] = sum_j softmax_j(scale Q[i,h,q,:].K[u,g,j,:]) V[u,g,j,:],
+ *   u = map[i], g = h / (H / H_kv)
+ * with the map, n_cand, n_users, H and Lq of the last ikbo_plan; the table
+ * and lens hold that n_users.  H_kv heads in the cache, a divisor of H.
+ *   Q, O  bf16 [n_cand][H][Lq][128];  lse fp32 [n_cand][H][Lq] or NULL (natural log)
+ *   Lkv   >= 1, a bound on the sum of the lengths (any; it sizes a workspace).
+ *         A larger sum is reported as IKBO_ERR_CACHE; O is then not defined.
+ * Rows of a user with no tokens get O = 0, lse = -inf; a candidate whose map
+ * value is out of range keeps its rows; rows of a user with a page out of
+ * range are not defined (the page is not touched).  What lies in a page behind a history's end is never
+ * used.  fp32 scores and softmax, P rounded to bf16 for P.V, fp32
+ * accumulation.  Results repeat bit for bit.
+ * Workspaces are the plan's, grown by the first call that needs more (which
+ * allocates; under stream capture that call fails with IKBO_ERR_CUDA and
+ * allocates nothing, so make one eager call of the largest size first; a
+ * captured call stays valid when later ones grow them).  Two variants, chosen
+ * from the sizes: with few query rows per user and head the 4-bit blocks are
+ * decoded in registers and nothing else is written; with many, histories are
+ * decoded once into the workspace (512 bytes per token, head and the 128 rows
+ * a history is padded to) and the kernel of ikbo_attn_forward reads that. */
+ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void* data, int n_pages, int page,
+                                       int H_kv, const int32_t* d_table, int max_blocks, const int32_t* d_lens,
+                                       void* O, float* lse, int Lkv, int d, float scale, cudaStream_t stream);
+
 /* Synchronise `stream`, then return (and clear) the first device-detected
  * error recorded since the last call: IKBO_ERR_MAP_OUT_OF_RANGE,
- * IKBO_ERR_TIMEOUT, IKBO_ERR_INTERNAL, or IKBO_OK. */
+ * IKBO_ERR_TIMEOUT, IKBO_ERR_OUT_OF_PAGES, IKBO_ERR_CACHE,
+ * IKBO_ERR_INTERNAL, or IKBO_OK. */
 ikbo_status_t ikbo_plan_get_status(ikbo_plan_t p, cudaStream_t stream);
 
 /* Debug and robustness knobs.  flags: bit 0 = LCE user tiles compute but do
