@@ -23,8 +23,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libikbo.so")
 SOURCES = ["seg.cu", "lce.cu", "lce_noalloc.cu", "lce_bwd.cu", "attn.cu", "attn_bwd.cu", "rope.cu",
-           "qcache.cu", "qattn.cu", "api.cu", "qcache_api.cu"]
-HEADERS = ["ptx.cuh", "ikbo_internal.h", "bwd_internal.h", "plan_internal.h", "qcache_internal.h"]
+           "qcache.cu", "qattn.cu", "qattn_tile.cu", "api.cu", "qcache_api.cu"]
+HEADERS = ["ptx.cuh", "ikbo_internal.h", "bwd_internal.h", "plan_internal.h", "qcache_internal.h",
+           "attn_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

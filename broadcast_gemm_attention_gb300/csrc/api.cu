@@ -131,6 +131,7 @@ void free_plan(ikbo_plan_t p) {
   cudaFree(p->d_qa_part);
   cudaFree(p->d_qa_tickets);
   cudaFree(p->d_qa_kv);
+  cudaFree(p->d_qa_list);
   cudaFree(p->d_qa_ranges);
   for (int i = 0; i < p->n_retired; ++i) cudaFree(p->retired[i]);
   delete p;

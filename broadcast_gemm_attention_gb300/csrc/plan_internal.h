@@ -68,6 +68,8 @@ struct ikbo_plan_s {
   size_t qa_part_elems = 0;
   uint32_t* d_qa_tickets = nullptr;  // splits of a tile that have finished (zero between calls)
   size_t qa_tickets_elems = 0;
+  int4* d_qa_list = nullptr;  // work items
+  size_t qa_list_elems = 0;
   uint16_t* d_qa_kv = nullptr;  // decoded K rows, then V rows
   size_t qa_kv_elems = 0;
   int32_t* d_qa_ranges = nullptr;  // each user's first decoded row, then each user's length

@@ -1,0 +1,894 @@
+// qattn_tile.cu -- broadcast attention from the 4-bit cache on the 5th-gen
+// tensor cores, for more query rows per user and K/V head than a few.
+//
+//   O[i,h] = softmax(Q[i,h] K[map[i],g]^T * scale) V[map[i],g]
+//
+// A tile is 128 rows of one (user u, K/V head g): the queries of u's
+// candidates, of all heads that share g, in order.  The history never exists
+// as bf16 outside shared memory: eight warps decode each 128-token tile of
+// codes into the operand tiles of the products while the tile before is
+// multiplied, so the tile's 128 rows share one decode.  The rest follows
+// attn.cu: S and P.V issuers, two softmax groups that take turns at the key
+// tiles, and a chain of reference maxima between them.
+//
+// Per CTA (persistent, one per SM, 20 warps):
+//   warp 1       S issuer and TMEM owner;  warp 2  P.V issuer
+//   warp 3       Q: 128 gathered rows by 16-byte asynchronous copies
+//   warps 4-11   softmax and epilogue (as in attn.cu)
+//   warps 12-19  decode: one AND-OR and one FMA for two elements.  A word's
+//                codes come out as elements (0,4) (1,5) (2,6) (3,7); instead of
+//                putting them in order, Q's elements are put in the same order
+//                once per tile (an inner product does not care), and V's
+//                columns are, which the epilogue undoes by its choice of names.
+//
+// Work: items (user, K/V head, split, tile) are listed by every CTA for itself
+// (a scan over the users); histories are split over CTAs where tiles alone do
+// not fill the GPU.  A split leaves its unnormalised O, [column][row], with
+// each row's reference and sum; the last warp to finish a 32-row, 64-column
+// piece of a tile adds that piece's splits in order, so results repeat bit for
+// bit whichever CTA that is.
+//
+// What bounds it: the softmax warps and the decode share the four issue slots
+// (about 640 and 500 cycles of each per key tile; the products take 1024
+// cycles of the tensor pipe).
+#include <cuda_bf16.h>
+
+#include "attn_common.cuh"
+#include "qcache_internal.h"
+
+namespace ikbo {
+namespace {
+
+constexpr int TL_THREADS = 640;
+constexpr int SOFTMAX_WARP0 = 4, DECODE_WARP0 = 12;
+constexpr int SOFTMAX_THREADS = 256, GROUP_THREADS = 128;
+constexpr int DECODE_WARPS = 4;  // of each kind
+constexpr int CTRL_REGS = 56, SOFTMAX_REGS = 120, DECODE_REGS = 88;
+constexpr int LAUNCH_REGS = 96;  // 65536 / 640, in eights
+static_assert(128 * CTRL_REGS + SOFTMAX_THREADS * SOFTMAX_REGS + 64 * DECODE_WARPS * DECODE_REGS <= TL_THREADS * LAUNCH_REGS,
+              "register split exceeds the launch's registers");
+constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
+constexpr int TL_ITEM_TILES = 14;           // what an item costs beside its key tiles, in key tiles
+constexpr int TL_JOIN_TILES = 1;           // and each split of a tile
+constexpr int TL_MIN_TILES = 4;            // key tiles of a split, at least
+constexpr int TL_PART = ATT_BM * ATT_D + 4 * ATT_BM;  // floats of a split's partial rows: O, and m and l per half
+constexpr int S_BUFS = 3;
+constexpr uint32_t TM_S = 0, TM_O = 384;  // S_b at TM_S + 128 b, its P in its first 64 columns
+
+constexpr int STAGE_BYTES = 1024;  // of O, per softmax warp: 32 rows x 16 elements
+constexpr uint32_t K_AT = 2 * ATT_Q_TILE_BYTES, V_AT = K_AT + 2 * ATT_KV_STAGE_BYTES;
+constexpr uint32_t OUT_AT = V_AT + 2 * ATT_KV_STAGE_BYTES;
+constexpr uint32_t AUX_AT = OUT_AT + 8 * STAGE_BYTES;
+constexpr int NUM_BARS = 6 + 3 * S_BUFS + 8 + 8;
+
+constexpr int LIST_NEAR = 64;  // of a CTA's items, kept in shared memory
+
+struct Aux {
+  int4 list[3 * LIST_NEAR];
+  uint64_t bars[NUM_BARS];
+  float xval[2 * 2 * ATT_BM];
+  uint32_t chain[ATT_BM];
+  int64_t red[QA_ROUNDS][TL_THREADS / 32];
+  uint32_t tmem_slot, abort, n_tiles;
+};
+constexpr uint32_t SMEM_USED = AUX_AT + sizeof(Aux);
+constexpr uint32_t SMEM_ALLOC = 227 * 1024;
+static_assert(SMEM_USED <= SMEM_ALLOC, "tiles do not fit in shared memory");
+static_assert(2 * sizeof(int32_t) * (SEG_MAX_USERS + 1) <= AUX_AT, "the users' prefixes do not fit");
+
+struct Smem {
+  uint8_t *q, *k, *v, *out;
+  uint64_t *q_full, *q_empty, *s_full, *p_full, *pv_done, *o_full, *o_empty, *k_full, *k_empty, *v_full,
+      *v_empty, *xbar;
+  Aux* x;
+};
+
+__device__ __forceinline__ Smem carve(uint8_t* base) {
+  Smem s;
+  s.q = base;
+  s.k = base + K_AT;
+  s.v = base + V_AT;
+  s.out = base + OUT_AT;
+  s.x = reinterpret_cast<Aux*>(base + AUX_AT);
+  uint64_t* b = s.x->bars;
+  s.q_full = b;
+  s.q_empty = b + 2;
+  s.o_full = b + 4;
+  s.o_empty = b + 5;
+  s.s_full = b + 6;
+  s.p_full = s.s_full + S_BUFS;
+  s.pv_done = s.p_full + S_BUFS;
+  s.k_full = s.pv_done + S_BUFS;
+  s.k_empty = s.k_full + 2;
+  s.v_full = s.k_empty + 2;
+  s.v_empty = s.v_full + 2;
+  s.xbar = s.v_empty + 2;
+  return s;
+}
+
+// ------------------------------------------------------------------- items
+// An item of the list (48 bytes).
+struct Item {
+  int u, hk, seg, n_rows;     // user, K/V head, the user's first place in perm, rows that read this history
+  int row0, len, t0, nt;      // the tile's first row; tokens of the history; the split's key tiles t0 .. t0 + nt - 1
+  int ns, slot, first, step;  // splits of the tile; this split's slot for partial rows, the first split's, the step between them
+};
+
+__device__ __forceinline__ int4 ld_int4(const int4* p) {  // written by this CTA in this launch: not the read-only path
+  int4 r;
+  asm volatile("ld.global.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
+// This CTA's items: the first ones in shared memory, the others in list entries
+// b, b + grid, .. of CTA b.
+struct List {
+  const int4* near;
+  const int4* far;
+  int count;
+};
+__device__ __forceinline__ int4 item_part(const List& l, int k, int i) {
+  if (k < LIST_NEAR) return l.near[3 * k + i];
+  return ld_int4(l.far + 3 * (static_cast<int64_t>(blockIdx.x) + static_cast<int64_t>(k) * gridDim.x) + i);
+}
+__device__ __forceinline__ int item_tiles(const List& l, int k) { return item_part(l, k, 1).w; }
+__device__ __forceinline__ Item load_item(const List& l, int k) {
+  const int4 a = item_part(l, k, 0), b = item_part(l, k, 1), c = item_part(l, k, 2);
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+}
+
+__device__ __forceinline__ QcUserWork user_work(const QcAttnParams& p, int u, int64_t most, bool& bad) {
+  QcUserWork w;
+  const int count = __ldg(p.offsets + u + 1) - __ldg(p.offsets + u);
+  w.len = qc_length(p.lens, u, most, bad);
+  w.tiles = static_cast<int>((static_cast<int64_t>(count) * p.group * p.Lq + ATT_BM - 1) / ATT_BM);
+  w.units = (w.len + ATT_BN - 1) / ATT_BN;
+  return w;
+}
+
+// Writes this CTA's entries of the list; sm: [2 * n_users] ints of scratch.
+// Returns how many (-1: the sizes do not add up).
+__device__ int make_list(const QcAttnParams& p, int32_t* sm, Aux& x) {
+  const int tid = threadIdx.x, n = p.n_users;
+  int32_t* item0 = sm;
+  int32_t* part0 = sm + n;
+  const int64_t most = (static_cast<int64_t>(p.max_blocks) << p.blocks_log2) * QC_ROWS;
+  const QcItems it = qc_items<TL_THREADS, TL_MIN_TILES, TL_ITEM_TILES, TL_JOIN_TILES>(
+      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, item0, part0, x.red);
+  if (it.items > p.max_items || it.slots > QA_MOST_SPLITS * static_cast<int64_t>(p.ctas)) return -1;
+  bool ignored = false;
+  const int n_items = static_cast<int>(it.items), grid = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
+  const int count = n_items > b ? (n_items - b + grid - 1) / grid : 0;
+  int tiles = 0;
+  for (int k = tid; k < count; k += TL_THREADS) {
+    const int i = b + k * grid;
+    const int u = qc_find(item0, n, i);
+    const QcUserWork w = user_work(p, u, most, ignored);
+    const int ns = qc_splits(w.units, it.chunk);
+    int local = i - item0[u];
+    const int tile = local % w.tiles;
+    local /= w.tiles;
+    const int split = local % ns, hk = local / ns;
+    const int t0 = qc_split_start(w.units, ns, split);
+    const int t1 = qc_split_start(w.units, ns, split + 1);
+    const int first = part0[u] + hk * ns * w.tiles + tile;
+    int4* e = k < LIST_NEAR ? x.list + 3 * k : p.list + 3 * static_cast<int64_t>(i);
+    const int seg = __ldg(p.offsets + u);
+    e[0] = make_int4(u, hk, seg, (__ldg(p.offsets + u + 1) - seg) * p.group * p.Lq);
+    e[1] = make_int4(tile * ATT_BM, w.len, t0, t1 - t0);
+    e[2] = make_int4(ns, first + split * w.tiles, first, w.tiles);
+    tiles += t1 - t0;
+  }
+  if (tiles) atomicAdd(&x.n_tiles, static_cast<uint32_t>(tiles));
+  __syncthreads();  // the entries are visible to the CTA, the scratch is free
+  return count;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Smem& s, const QcAttnParams& p) {
+  const bool ok = mbar_wait(bar, parity, &s.x->abort, p.timeout_ns, 1);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// ------------------------------------------------------------------ decode
+// Place in the CTA's sequence of key tiles.
+struct Cursor {
+  int k, t, nt, t0, len;
+  const int32_t* table;
+  const uint8_t* data;  // the cache, at the item's K/V head and the warp's half
+  int page;             // of block lane & 1 (of the warp's two) of tile (t & ~15) + lane / 2
+};
+
+// To the first tile of the next item with any; k == count: the end.
+__device__ __forceinline__ void cursor_item(const QcAttnParams& p, const List& l, Cursor& c, int half) {
+  for (; c.k < l.count; ++c.k) {
+    const int4 b = item_part(l, c.k, 1);
+    if (b.w == 0) continue;
+    const int4 a = item_part(l, c.k, 0);
+    c.table = p.table + static_cast<int64_t>(a.x) * p.max_blocks;
+    c.data = p.data + ((static_cast<int64_t>(a.y) << p.blocks_log2) * QC_BLOCK_BYTES + half);
+    c.len = b.y;
+    c.t0 = b.z;
+    c.nt = b.w;
+    c.t = 0;
+    return;
+  }
+}
+
+// A warp's share of a half tile, in registers: 2 blocks of 16 tokens, of which
+// a lane has 4 chunks of 16 code bytes (one token's group of 32 elements) with
+// their pairs.  A zero pair makes a chunk of zeros, whatever its codes.
+struct Raw {
+  uint4 c[4];
+  uint32_t sz[4];
+};
+
+// Four warps turn the keys' half tiles, four the values', so that one kind's
+// waits lie beside the other's work.  The codes come straight from global
+// memory into registers, a warp reading 512 contiguous bytes, and each chunk's
+// registers are loaded again (for the next tile) as soon as it is decoded; the
+// lines of the tiles after that are asked for in L2.  (Codes that passed
+// through shared memory by bulk copies cost a producer warp over a thousand
+// cycles a tile to issue.)  A quarter warp's 16-byte stores (2 tokens x 4
+// groups) hit all banks because the second 64 elements' pieces lie two places
+// further (place ^ 2): like the order within a piece, Q's elements and the
+// epilogue follow that.
+__device__ void decode_warps(const QcAttnParams& p, const Smem& s, const List& l) {
+  const bool values = threadIdx.x >= 32 * (DECODE_WARP0 + DECODE_WARPS);  // one code for both kinds
+  const int lane = static_cast<int>(lane_id()), dw = static_cast<int>(threadIdx.x >> 5) & (DECODE_WARPS - 1);
+  const int grp = lane & 3, tok8 = lane >> 2;
+  uint8_t* const ring = (values ? s.v : s.k) + (dw * 32 + tok8) * 128;
+  uint64_t* const full = values ? s.v_full : s.k_full;
+  uint64_t* const empty = values ? s.v_empty : s.k_empty;
+  const int half = values ? QC_HALF_BYTES : 0;
+  uint32_t place[4];  // of the group's four pieces in a row of the tile
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    place[k] = (grp >> 1) * HALF_TILE + (((((grp & 1) * 4 + k) ^ (grp & 2)) ^ tok8) << 4);
+  const uint32_t tiles = s.x->n_tiles;
+  const int64_t page_bytes = (static_cast<int64_t>(p.H_kv) << p.blocks_log2) * QC_BLOCK_BYTES;
+
+  Cursor c = {};
+  cursor_item(p, l, c, half);
+  Raw raw;
+  const uint8_t* src[2];  // the warp's two blocks of the cursor's tile
+  int left = 0;           // tokens of the history from the warp's first one on
+  // the cursor's tile becomes the one that fetch() reads, and the cursor moves on
+  const auto point = [&]() {
+    if ((c.t & 15) == 0) {
+      const int blk = (c.t0 + c.t + (lane >> 1)) * 8 + dw * 2 + (lane & 1);
+      c.page = 0;
+      if (c.t + (lane >> 1) < c.nt && blk * QC_ROWS < c.len) {
+        c.page = __ldg(c.table + (blk >> p.blocks_log2));
+        if (c.page < 0 || c.page >= p.n_pages) {
+          atomicOr(p.status, DEV_ERR_CACHE);
+          c.page = 0;
+        }
+      }
+    }
+    const int blk = (c.t0 + c.t) * 8 + dw * 2;
+    left = c.len - blk * QC_ROWS;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int page = __shfl_sync(0xffffffffu, c.page, ((c.t & 15) << 1) | b);
+      src[b] = c.data + page * page_bytes + ((blk + b) & ((1 << p.blocks_log2) - 1)) * QC_BLOCK_BYTES;
+    }
+    // the lines of the warp's blocks two tiles on (of this item)
+    if (c.t + 2 < c.nt) {
+      const int at = ((c.t & 15) + 2) * 2 + (lane >= 10);
+      const int page = __shfl_sync(0xffffffffu, c.page, at & 31);
+      if (lane < 20 && at < 32) {
+        const uint8_t* line = c.data + page * page_bytes +
+                              ((blk + 16 + (lane >= 10)) & ((1 << p.blocks_log2) - 1)) * QC_BLOCK_BYTES +
+                              (lane >= 10 ? lane - 10 : lane) * 128;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+      }
+    }
+    if (++c.t == c.nt) {
+      ++c.k;
+      cursor_item(p, l, c, half);
+    }
+  };
+  // Unconditional (blocks that do not exist have page 0's address), so that the
+  // loads stay in flight: nothing touches their registers before the next tile.
+  const auto fetch = [&](int i) {
+    const uint8_t* blk = src[i >> 1];
+    raw.c[i] = __ldg(reinterpret_cast<const uint4*>(blk) + ((i & 1) * 32 + lane));
+    raw.sz[i] = __ldg(reinterpret_cast<const uint32_t*>(blk + QC_CODE_BYTES) + ((i & 1) * 32 + lane));
+  };
+  if (tiles > 0) {
+    point();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fetch(i);
+  }
+#pragma unroll 1
+  for (uint32_t g = 0; g < tiles; ++g) {
+    const int valid = left - tok8;  // > 8 i: the lane's token of chunk i exists
+    if (g + 1 < tiles) point();
+    if (!warp_wait(empty + (g & 1u), ((g >> 1) & 1u) ^ 1u, s, p)) return;
+    uint8_t* dst = ring + (g & 1u) * ATT_KV_STAGE_BYTES;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t sz = valid > 8 * i ? raw.sz[i] : 0u;
+      const uint32_t s2 = __byte_perm(sz, 0, 0x1010), z2 = __byte_perm(sz, 0, 0x3232);
+      const uint32_t w[4] = {raw.c[i].x, raw.c[i].y, raw.c[i].z, raw.c[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 o = make_uint4(qc_decode<0>(w[k], s2, z2), qc_decode<1>(w[k], s2, z2), qc_decode<2>(w[k], s2, z2),
+                                   qc_decode<3>(w[k], s2, z2));
+        *reinterpret_cast<uint4*>(dst + i * 1024 + place[k]) = o;
+      }
+      fetch(i);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full + (g & 1u));
+  }
+}
+
+// ---------------------------------------------------------------- Q loader
+// Rows of the tile into a Q buffer: asynchronous copies (rows behind the last
+// become zeros), then each eight elements into the decoded codes' order.
+__device__ __forceinline__ int64_t row_index(const QcAttnParams& p, const Item& x, int r, int rows_per_cand) {
+  const int slot = r / rows_per_cand;
+  return (static_cast<int64_t>(__ldg(p.perm + x.seg + slot)) * p.H + x.hk * p.group) * p.Lq + (r - slot * rows_per_cand);
+}
+
+__device__ void q_loader(const QcAttnParams& p, const Smem& s, const List& l) {
+  const int lane = static_cast<int>(lane_id());
+  const int rows_per_cand = p.group * p.Lq;
+  uint32_t qc = 0;
+  for (int k = 0; k < l.count; ++k) {
+    const Item x = load_item(l, k);
+    if (x.nt == 0) continue;
+    int64_t at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = x.row0 + i * 32 + lane;
+      at[i] = r < x.n_rows ? row_index(p, x, r, rows_per_cand) * ATT_D : -1;
+    }
+    const uint32_t qb = qc & 1u;
+    if (!warp_wait(&s.q_empty[qb], ((qc >> 1) & 1u) ^ 1u, s, p)) return;
+    ++qc;
+    uint8_t* q = s.q + qb * ATT_Q_TILE_BYTES;
+    const int chunk = lane & 15;
+    const uint32_t col = static_cast<uint32_t>((chunk >> 3) * HALF_TILE);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll 4
+      for (int j = 0; j < 16; ++j) {
+        const int r = 2 * j + (lane >> 4);
+        const int64_t a = __shfl_sync(0xffffffffu, at[i], r);
+        const uint32_t dst = smem_u32(q) + col + (i * 32 + r) * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+        const uint16_t* src = p.Q + (a < 0 ? 0 : a + (chunk ^ ((chunk >> 2) & 2)) * 8);  // places 8.. of a row: ^ 2
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(a < 0 ? 0 : 16) : "memory");
+      }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+#pragma unroll 8
+    for (int j = 0; j < 64; ++j) {  // any order of the tile's 2048 pieces
+      uint4* at16 = reinterpret_cast<uint4*>(q) + j * 32 + lane;
+      const uint4 v = *at16;
+      *at16 = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                         __byte_perm(v.y, v.w, 0x7632));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.q_full[qb]);
+  }
+}
+
+// ----------------------------------------------------------------- issuers
+__device__ void s_issuer(const QcAttnParams& p, const Smem& s, uint32_t tmem, const List& l) {
+  uint32_t g = 0, qu = 0;
+  for (int k = 0; k < l.count; ++k) {
+    const int nt = item_tiles(l, k);
+    if (nt == 0) continue;
+    const uint32_t qb = qu & 1u;
+    const uint32_t q_base = smem_u32(s.q + qb * ATT_Q_TILE_BYTES);
+    for (int jt = 0; jt < nt; ++jt, ++g) {
+      const uint32_t b = g & 1u, sb = g % S_BUFS;
+      if (!warp_wait(&s.k_full[b], (g >> 1) & 1u, s, p)) return;
+      if (g >= S_BUFS && !warp_wait(&s.pv_done[sb], (g / S_BUFS - 1) & 1u, s, p)) return;
+      if (jt == 0 && !warp_wait(&s.q_full[qb], (qu >> 1) & 1u, s, p)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_qk_ss(tmem + TM_S + sb * 128, q_base, smem_u32(s.k + b * ATT_KV_STAGE_BYTES));
+        mma_commit(&s.s_full[sb]);
+        mma_commit(&s.k_empty[b]);
+        if (jt + 1 == nt) mma_commit(&s.q_empty[qb]);
+      }
+      __syncwarp();
+    }
+    ++qu;
+  }
+}
+
+__device__ void pv_issuer(const QcAttnParams& p, const Smem& s, uint32_t tmem, const List& l) {
+  uint32_t g = 0, ou = 0;
+  for (int k = 0; k < l.count; ++k) {
+    const int nt = item_tiles(l, k);
+    for (int jt = 0; jt < nt; ++jt, ++g) {
+      const uint32_t b = g & 1u, sb = g % S_BUFS;
+      if (!warp_wait(&s.p_full[sb], (g / S_BUFS) & 1u, s, p)) return;
+      if (!warp_wait(&s.v_full[b], (g >> 1) & 1u, s, p)) return;
+      if (jt == 0 && !warp_wait(s.o_empty, (ou & 1u) ^ 1u, s, p)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_pv(tmem + TM_O, tmem + TM_S + sb * 128, smem_u32(s.v + b * ATT_KV_STAGE_BYTES), jt > 0);
+        mma_commit(&s.pv_done[sb]);
+        mma_commit(&s.v_empty[b]);
+        if (jt + 1 == nt) mma_commit(s.o_full);
+      }
+      __syncwarp();
+      if (jt + 1 == nt) ++ou;
+    }
+  }
+}
+
+// ---------------------------------------------------- softmax and epilogue
+struct Lane {
+  int quarter, half, r;  // half: the warp's group (its key tiles) and its d half of O
+  uint32_t xc;           // exchanges done with the partner warp
+};
+
+__device__ __forceinline__ bool pair_exchange(const QcAttnParams& p, const Smem& s, Lane& ln, float mine, float& theirs) {
+  const uint32_t buf = ln.xc & 1u;
+  s.x->xval[buf * 256 + ln.half * 128 + ln.r] = mine;
+  uint64_t* bar = &s.xbar[ln.quarter * 2 + buf];
+  mbar_arrive(bar);
+  if (!mbar_wait(bar, (ln.xc >> 1) & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
+  theirs = s.x->xval[buf * 256 + (ln.half ^ 1) * 128 + ln.r];
+  ++ln.xc;
+  return true;
+}
+
+// The chain of reference maxima through the tiles of both groups (attn.cu
+// describes it): the high 24 bits of the value, the tile's tag below.
+__device__ __forceinline__ float chain_value(float m) { return __uint_as_float(__float_as_uint(m) & 0xFFFFFF00u); }
+__device__ __forceinline__ void chain_post(const Smem& s, int r, uint32_t tag, float m) {
+  const uint32_t w = (__float_as_uint(m) & 0xFFFFFF00u) | (tag & 0xFFu);
+  asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(smem_u32(s.x->chain + r)), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint32_t chain_load(const Smem& s, int r) {
+  uint32_t w;
+  asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(w) : "r"(smem_u32(s.x->chain + r)) : "memory");
+  return w;
+}
+__device__ __forceinline__ bool chain_wait(const QcAttnParams& p, const Smem& s, int r, uint32_t tag, float& m) {
+  tag &= 0xFFu;
+  uint32_t w = chain_load(s, r);
+  bool ok = true;
+  if ((w & 0xFFu) != tag) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+      w = chain_load(s, r);
+      if ((w & 0xFFu) == tag) break;
+      if ((it & 63u) == 0) {
+        volatile uint32_t* abort = &s.x->abort;
+        if (*abort) {
+          ok = false;
+          break;
+        }
+        if (globaltimer_ns() - t0 > p.timeout_ns) {
+          *abort = 1;
+          ok = false;
+          break;
+        }
+      }
+    }
+  }
+  m = __uint_as_float(w & 0xFFFFFF00u);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Scores of columns from n on: none.
+__device__ __forceinline__ void mask_columns(uint32_t (&v)[32], int n) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j >= n) v[j] = __float_as_uint(-INFINITY);
+}
+
+// The running maximum of 32 columns' scores, of which n exist.
+__device__ __forceinline__ void row_max(uint32_t (&v)[32], int n, float& mx) {
+  if (n < 32) mask_columns(v, n);
+  float mx0 = mx, mx1 = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    mx0 = fmax3(mx0, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+    mx1 = fmax3(mx1, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+  }
+  mx = fmaxf(mx0, mx1);
+}
+
+// p = 2^(s sl - m) of 32 columns, summed into l0, l1, and as bf16 pairs to TMEM.
+__device__ __forceinline__ void row_exp(const uint32_t (&v)[32], float sl, float m, float& l0, float& l1, uint32_t to) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float t0, t1;
+    fma2(t0, t1, __uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), sl, -m);
+    const float p0 = ex2(t0);
+    const float p1 = ex2(t1);
+    add2(l0, l1, p0, p1);
+    pk[j] = pack_bf16x2(p0, p1);
+  }
+  tmem_st16(to, pk);
+}
+
+struct RowOut {
+  bool pending;    // a finished item whose O has not been read out yet
+  bool rows_here;  // any of the warp's rows exists
+  int64_t row;     // this thread's row of O (in rows), or -1
+  float l, m;      // this group's row sum, its last reference (-inf: no tile)
+  int ns, slot, first, step;
+};
+
+// 16 columns (the c-th of four in the warp's 64) of the finished rows, scaled,
+// in element order, to global memory: through 1 KB of shared memory, so that
+// every store fills whole 32-byte sectors.  Column 8k + j holds element
+// 8 (k ^ 2 half) + (j >> 1) + 4 (j & 1) of the warp's half.
+__device__ __forceinline__ void store_columns(const QcAttnParams& p, uint8_t* stage, const Lane& ln, int64_t row, int c,
+                                              const float* o, float inv) {
+  const int lane = static_cast<int>(lane_id());
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float* e = o + 8 * k;
+    uint4 w;
+    w.x = pack_bf16x2(e[0] * inv, e[2] * inv);
+    w.y = pack_bf16x2(e[4] * inv, e[6] * inv);
+    w.z = pack_bf16x2(e[1] * inv, e[3] * inv);
+    w.w = pack_bf16x2(e[5] * inv, e[7] * inv);
+    *reinterpret_cast<uint4*>(stage + lane * 32 + ((k ^ ((lane >> 2) & 1)) << 4)) = w;
+  }
+  __syncwarp();
+  const int piece = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 16 * i + (lane >> 1);
+    const int64_t at = __shfl_sync(0xffffffffu, row, r);
+    const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 32 + ((piece ^ ((r >> 2) & 1)) << 4));
+    if (at >= 0) reinterpret_cast<uint4*>(p.O + at * ATT_D + ln.half * 64)[(2 * c + piece) ^ (2 * ln.half)] = w;
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l); }
+__device__ __forceinline__ void store_lse(const QcAttnParams& p, int64_t row, float m, float l) {
+  p.lse[row] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+}
+
+// A split's piece of O (this warp's 32 rows x 64 columns) to its slot; the
+// warp that completes the tile's piece adds the splits in order and stores it.
+__device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, const RowOut& ro, const Lane& ln, float mf,
+                                            float l, uint8_t* stage, uint64_t* o_empty) {
+  const int lane = static_cast<int>(lane_id());
+  // slot: [half][64 columns][128 rows], then [half][m, l][128 rows]
+  constexpr int64_t SLOT = TL_PART;
+  const int64_t in = static_cast<int64_t>(ln.half) * 64 * ATT_BM + ln.r;
+  const int64_t ml = 2 * 64 * ATT_BM + ln.half * 2 * ATT_BM + ln.r;
+  float* mine = p.part + ro.slot * SLOT;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t o[32];
+    tmem_ld32(Ot + c * 32, o);
+    tmem_ld_wait(o);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) __stcg(mine + in + (c * 32 + j) * ATT_BM, __uint_as_float(o[j]));
+  }
+  __stcg(mine + ml, mf);
+  __stcg(mine + ml + ATT_BM, l);
+  tc_fence_before();
+  mbar_arrive(o_empty);
+  __threadfence();
+  __syncwarp();
+  uint32_t last = 0;
+  if (lane == 0) {
+    uint32_t* t = p.tickets + static_cast<int64_t>(ro.first) * 8 + ln.quarter * 2 + ln.half;
+    last = atomicAdd(t, 1u) + 1 == static_cast<uint32_t>(ro.ns);
+    if (last) *t = 0;  // zero again for the next call
+  }
+  last = __shfl_sync(0xffffffffu, last, 0);
+  if (!last) return;
+  __threadfence();
+  const float* first = p.part + ro.first * SLOT;
+  const int64_t stride = ro.step * SLOT;
+  float M = -INFINITY;
+  for (int k = 0; k < ro.ns; ++k) M = fmaxf(M, __ldcg(first + k * stride + ml));
+  float L = 0.f;
+  for (int k = 0; k < ro.ns; ++k) {
+    const float m = __ldcg(first + k * stride + ml);
+    L += (m == -INFINITY ? 0.f : ex2(m - M)) * __ldcg(first + k * stride + ml + ATT_BM);
+  }
+  const float inv = inverse(L);
+  if (p.lse && ro.row >= 0 && ln.half == 0) store_lse(p, ro.row, M, L);
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float acc[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < ro.ns; ++k) {
+      const float* sp = first + k * stride;
+      const float m = __ldcg(sp + ml);
+      const float f = m == -INFINITY ? 0.f : ex2(m - M);
+      float x[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = __ldcg(sp + in + (c * 16 + j) * ATT_BM);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[j] = fmaf(x[j], f, acc[j]);
+    }
+    store_columns(p, stage, ln, ro.row, c, acc, inv);
+  }
+}
+
+// An item's epilogue: the groups' row sums joined, O out of TMEM to global
+// memory (or through the partial rows of a split item).
+__device__ __forceinline__ bool epilogue(const QcAttnParams& p, const Smem& s, uint32_t Ot, const RowOut& ro, Lane& ln,
+                                         uint32_t& ou) {
+  if (!ro.rows_here) {  // both warps of the quarter skip
+    if (!mbar_wait(s.o_full, ou & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
+    ++ou;
+    mbar_arrive(s.o_empty);
+    return true;
+  }
+  float mp, lp;
+  if (!pair_exchange(p, s, ln, ro.m, mp)) return false;
+  const float mf = fmaxf(ro.m, mp);
+  const float lm = ro.m == -INFINITY ? ro.l : ro.l * ex2(ro.m - mf);  // without a reference: 0, or NaN
+  if (!pair_exchange(p, s, ln, lm, lp)) return false;
+  const float l = lm + lp;
+  if (!mbar_wait(s.o_full, ou & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
+  ++ou;
+  tc_fence_after();
+  uint8_t* stage = s.out + (ln.quarter * 2 + ln.half) * STAGE_BYTES;
+  if (ro.ns > 1) {
+    join_splits(p, Ot, ro, ln, mf, l, stage, s.o_empty);
+    return true;
+  }
+  if (p.lse && ro.row >= 0 && ln.half == 0) store_lse(p, ro.row, mf, l);
+  const float inv = inverse(l);
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t o[32];
+    tmem_ld32(Ot + c * 32, o);
+    tmem_ld_wait(o);
+    if (c == 1) {
+      tc_fence_before();
+      mbar_arrive(s.o_empty);
+    }
+    store_columns(p, stage, ln, ro.row, 2 * c, reinterpret_cast<const float*>(o), inv);
+    store_columns(p, stage, ln, ro.row, 2 * c + 1, reinterpret_cast<const float*>(o) + 16, inv);
+  }
+  return true;
+}
+
+__device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tmem, const List& l_) {
+  const int warp = threadIdx.x >> 5;
+  Lane ln;
+  ln.quarter = warp & 3;
+  ln.half = (warp - SOFTMAX_WARP0) >> 2;
+  ln.r = (ln.quarter << 5) + static_cast<int>(lane_id());
+  ln.xc = 0;
+  const int grp = ln.half;
+  const uint32_t lane_base = static_cast<uint32_t>(ln.quarter * 32) << 16;
+  const uint32_t Oall = tmem + lane_base + TM_O;
+  const uint32_t Ot = Oall + grp * 64;
+  const float sl = p.scale_log2;
+  const int rows_per_cand = p.group * p.Lq;
+  uint32_t g = 0, ou = 0;
+  RowOut prev = {};
+
+  for (int k = 0; k < l_.count; ++k) {
+    const Item x = load_item(l_, k);
+    const int rr = x.row0 + ln.r;
+    const int64_t row = rr < x.n_rows ? row_index(p, x, rr, rows_per_cand) : -1;
+    const bool rows_here = x.row0 + ln.quarter * 32 < x.n_rows;
+    if (x.nt == 0) {  // no tokens: O = 0, LSE = -inf
+      if (row >= 0) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(p.O + row * ATT_D + grp * 64)[c] = z;
+        if (p.lse && grp == 0) p.lse[row] = -INFINITY;
+      }
+      continue;
+    }
+    bool epi = prev.pending;  // the previous item's epilogue is still to come
+    float mref = -INFINITY, l = 0.f;
+    const uint32_t g0 = g;
+    for (int jt = static_cast<int>((static_cast<uint32_t>(grp) - g0) & 1u); jt < x.nt; jt += 2) {
+      g = g0 + static_cast<uint32_t>(jt);
+      const uint32_t sb = g % S_BUFS;
+      const uint32_t St = tmem + lane_base + TM_S + sb * 128;
+      if (!mbar_wait(&s.s_full[sb], (g / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1)) return;
+      tc_fence_after();
+      if (!rows_here) {  // none of the warp's 32 rows exists: keep the hand-shakes in step, nothing else
+        float ignored;
+        if (!chain_wait(p, s, ln.r, g, ignored)) return;
+        chain_post(s, ln.r, g + 1, 0.f);
+        tc_fence_before();
+        mbar_arrive(&s.p_full[sb]);
+        if (epi && !epilogue(p, s, Ot, prev, ln, ou)) return;
+        epi = false;
+        continue;
+      }
+      // two passes over the row, 32 columns at a time with the next ones on
+      // their way from TMEM (whole rows in registers, unrolled, are too much for
+      // the instruction cache that the SM's 20 warps share); the first pass goes
+      // down so that the second begins with what it ended on
+      const int ncols = min(ATT_BN, x.len - (x.t0 + jt) * ATT_BN);
+      uint32_t va[32], vb[32];
+      float mx = -INFINITY;
+      tmem_ld32p(St + 96, va);
+      tmem_ld_wait();
+      reg_fence32(va);
+      tmem_ld32p(St + 64, vb);
+      row_max(va, ncols - 96, mx);
+      tmem_ld_wait();
+      reg_fence32(vb);
+      tmem_ld32p(St + 32, va);
+      row_max(vb, ncols - 64, mx);
+      tmem_ld_wait();
+      reg_fence32(va);
+      tmem_ld32p(St, vb);
+      row_max(va, ncols - 32, mx);
+      tmem_ld_wait();
+      reg_fence32(vb);
+      row_max(vb, ncols, mx);
+      mx *= sl;
+      const uint32_t cw = chain_load(s, ln.r);
+      float mprev = __uint_as_float(cw & 0xFFFFFF00u);
+      if (!__all_sync(0xffffffffu, (cw & 0xFFu) == (g & 0xFFu)) && !chain_wait(p, s, ln.r, g, mprev)) return;
+      if (jt == 0) mprev = -INFINITY;
+      const bool rescale = __any_sync(0xffffffffu, mx > mprev + RESCALE_THRESHOLD);
+      const float mj = rescale ? chain_value(fmaxf(mprev, mx)) : mprev;
+      chain_post(s, ln.r, g + 1, mj);
+      if (mj != mref) {
+        l *= ex2(mref - mj);
+        mref = mj;
+      }
+      float l0 = 0.f, l1 = 0.f;
+      // P takes the place of the scores already read
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        tmem_ld32p(St + 64 * h + 32, va);
+        row_exp(vb, sl, mj, l0, l1, St + 32 * h);
+        tmem_ld_wait();
+        reg_fence32(va);
+        if (h == 0) tmem_ld32p(St + 64, vb);
+        if (ncols < 64 * h + 64) mask_columns(va, ncols - 64 * h - 32);
+        row_exp(va, sl, mj, l0, l1, St + 32 * h + 16);
+        tmem_ld_wait();
+        reg_fence32(vb);
+        if (ncols < 96) mask_columns(vb, ncols - 64);
+      }
+      l += l0 + l1;
+      if (rescale && jt > 0) {
+        // O must hold only this item's P.V: the previous item's is read out first
+        if (epi && !epilogue(p, s, Ot, prev, ln, ou)) return;
+        epi = false;
+        const uint32_t gp = g - 1;
+        if (!mbar_wait(&s.pv_done[gp % S_BUFS], (gp / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1)) return;
+        tc_fence_after();
+        const float alpha = ex2(mprev - mj);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(Oall + c * 32, o);
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+          tmem_st32(Oall + c * 32, o);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&s.p_full[sb]);
+      if (epi && !epilogue(p, s, Ot, prev, ln, ou)) return;  // after the group's first tile of the next item
+      epi = false;
+    }
+    g = g0 + static_cast<uint32_t>(x.nt);
+    if (epi && !epilogue(p, s, Ot, prev, ln, ou)) return;
+    prev.pending = true;
+    prev.row = row;
+    prev.rows_here = rows_here;
+    prev.l = l;
+    prev.m = mref;
+    prev.ns = x.ns;
+    prev.slot = x.slot;
+    prev.first = x.first;
+    prev.step = x.step;
+  }
+  if (prev.pending) epilogue(p, s, Ot, prev, ln, ou);
+}
+
+__global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  if (pad + SMEM_USED > SMEM_ALLOC) {
+    if (threadIdx.x == 0) atomicOr(p.status, DEV_ERR_SMEM_LAYOUT);
+    return;
+  }
+  const Smem s = carve(smem_raw + pad);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S_BUFS; ++i) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], GROUP_THREADS);
+      mbar_init(&s.pv_done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.q_full[i], 1);
+      mbar_init(&s.q_empty[i], 1);
+      mbar_init(&s.k_full[i], DECODE_WARPS);
+      mbar_init(&s.k_empty[i], 1);
+      mbar_init(&s.v_full[i], DECODE_WARPS);
+      mbar_init(&s.v_empty[i], 1);
+    }
+    mbar_init(s.o_full, 1);
+    mbar_init(s.o_empty, SOFTMAX_THREADS);
+    for (int i = 0; i < 8; ++i) mbar_init(&s.xbar[i], 64);
+    for (int r = 0; r < ATT_BM; ++r) s.x->chain[r] = 0;
+    s.x->abort = 0;
+    s.x->n_tiles = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(&s.x->tmem_slot, 512);
+    tmem_relinquish();
+  }
+  List l;
+  l.near = s.x->list;
+  l.far = p.list;
+  l.count = make_list(p, reinterpret_cast<int32_t*>(smem_raw + pad), *s.x);
+  if (l.count < 0) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(p.status, DEV_ERR_BAD_WORK);
+    l.count = 0;
+  }
+  fence_proxy_async_smem();  // the scratch of the list lay where bulk copies go
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.x->tmem_slot;
+
+  if (warp < SOFTMAX_WARP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
+    if (warp == 1) s_issuer(p, s, tmem, l);
+    else if (warp == 2) pv_issuer(p, s, tmem, l);
+    else if (warp == 3) q_loader(p, s, l);
+  } else if (warp < DECODE_WARP0) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
+    softmax_warps(p, s, tmem, l);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DECODE_REGS));
+    decode_warps(p, s, l);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (s.x->abort && threadIdx.x == 0) atomicOr(p.status, DEV_ERR_PIPE_TIMEOUT);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+size_t qattn_tile_smem() { return SMEM_ALLOC; }
+size_t qattn_tile_part_elems(int num_sms) { return static_cast<size_t>(QA_MOST_SPLITS) * num_sms * TL_PART; }
+// Items of a request: one per tile, and at most QA_MOST_SPLITS splits per CTA.
+int64_t qattn_tile_items(int64_t rows, int n_users, int H_kv, int num_sms) {
+  return (rows / ATT_BM + n_users) * H_kv + QA_MOST_SPLITS * static_cast<int64_t>(num_sms);
+}
+
+cudaError_t launch_qattn_tile(const QcAttnParams& p, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(qattn_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(SMEM_ALLOC));
+  if (e != cudaSuccess) return e;
+  qattn_tile_kernel<<<p.ctas, TL_THREADS, SMEM_ALLOC, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace ikbo

@@ -14,9 +14,13 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, int num_sms, cudaStream_
 cudaError_t launch_qc_resize(const QcResizeParams& p, cudaStream_t s);
 cudaError_t launch_qc_append(const QcAppendParams& p, cudaStream_t s);
 cudaError_t launch_qc_load(const QcLoadParams& p, int num_sms, cudaStream_t s);
-int qattn_target(int num_sms);
+int qattn_ctas(int num_sms);
 size_t qattn_part_elems(int num_sms);
-cudaError_t launch_qattn(const QcAttnParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_qattn(const QcAttnParams& p, cudaStream_t s);
+size_t qattn_tile_smem();
+size_t qattn_tile_part_elems(int num_sms);
+int64_t qattn_tile_items(int64_t rows, int n_users, int H_kv, int num_sms);
+cudaError_t launch_qattn_tile(const QcAttnParams& p, cudaStream_t s);
 }  // namespace ikbo
 
 using namespace ikbo;
@@ -53,6 +57,31 @@ ikbo_status_t check_table(const int32_t* table, const int32_t* lens, int max_blo
     return IKBO_ERR_INVALID_ARG;
   if (n_users > SEG_MAX_USERS || static_cast<int64_t>(max_blocks) * page > INT32_LIMIT) return IKBO_ERR_UNSUPPORTED;
   return IKBO_OK;
+}
+
+// The attention's variant, from the average number of query rows that read a
+// history's K/V head, R = rows / n_users, and the tokens there may be to read.
+// Measured at 64 users x 8 heads x 4096 tokens, caches cold (us):
+//   R                   8    16    32    64   128
+//   in registers      125   128   199   369     -   (histories decoded once per 16 rows)
+//   in tiles          171   171   171   175   181   (once per 128 rows)
+//   decoded first       -     -     -     -   416
+// 102 users, R = 160, 1150 tokens: tiles 175, decoded first 221; 60 users,
+// R = 546, 2048 tokens: 365 and 336; 15 users, R = 2184: 304 and 225.  So up to
+// 16 rows in registers, from 512 on decoded first, between them in tiles,
+// unless the tile kernel's longer start and end (about 12 us) are not made up
+// for: the register kernel gets through 18000 (16-row tile, token, head)s in a
+// microsecond, the tile kernel through 13500 of 128 rows.
+enum QcAttnVariant { QATTN_REGISTERS = 1, QATTN_TILES = 2, QATTN_DECODED = 3 };
+
+QcAttnVariant qattn_variant(int64_t rows, int n_users, int H_kv, int Lkv) {
+  if (rows <= 16 * static_cast<int64_t>(n_users)) return QATTN_REGISTERS;
+  if (rows > 512 * static_cast<int64_t>(n_users)) return QATTN_DECODED;
+  const double tokens = static_cast<double>(Lkv) * H_kv;
+  const double r = static_cast<double>(rows) / n_users;
+  const double registers_us = std::ceil(r / 16) * tokens / 18000;
+  const double tiles_us = 12 + std::ceil(r / 128) * tokens / 13500;
+  return registers_us < tiles_us ? QATTN_REGISTERS : QATTN_TILES;
 }
 
 ikbo_status_t rope_call(ikbo_plan_t p, ikbo_rope_t r, const void* X, const int64_t* xs, void* Y, const int64_t* ys,
@@ -293,7 +322,8 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   if (rows * H_kv > INT32_LIMIT) return IKBO_ERR_UNSUPPORTED;
   const int blocks_log2 = blocks_log2_of(page);
 
-  if (rows > static_cast<int64_t>(QATTN_FEW_ROWS) * n_users) {
+  const QcAttnVariant variant = qattn_variant(rows, n_users, H_kv, Lkv);
+  if (variant == QATTN_DECODED) {
     // decode each history once into padded bf16 rows, then the bf16 kernel
     const int64_t cap = (static_cast<int64_t>(Lkv) + static_cast<int64_t>(ATT_BN) * n_users + ATT_BN - 1) / ATT_BN * ATT_BN;
     if (cap > INT32_LIMIT) return IKBO_ERR_UNSUPPORTED;
@@ -335,9 +365,15 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
     return attn_launch(p, c, stream);
   }
 
-  if (grow_kept(p, &p->d_qa_part, &p->qa_part_elems, qattn_part_elems(p->num_sms), stream) != cudaSuccess ||
-      grow_kept(p, &p->d_qa_tickets, &p->qa_tickets_elems, 2 * static_cast<size_t>(qattn_target(p->num_sms)), stream) !=
-          cudaSuccess)
+  const bool few = variant == QATTN_REGISTERS;
+  if (!few && qattn_tile_smem() > p->max_smem) return IKBO_ERR_UNSUPPORTED;
+  const int ctas = few ? qattn_ctas(p->num_sms) : p->num_sms;
+  const size_t part = few ? qattn_part_elems(p->num_sms) : qattn_tile_part_elems(p->num_sms);
+  const size_t tickets = static_cast<size_t>(QA_MOST_SPLITS) * ctas * (few ? 1 : 8);
+  const int64_t items = few ? 0 : qattn_tile_items(rows, n_users, H_kv, p->num_sms);
+  if (grow_kept(p, &p->d_qa_part, &p->qa_part_elems, part, stream) != cudaSuccess ||
+      grow_kept(p, &p->d_qa_tickets, &p->qa_tickets_elems, tickets, stream) != cudaSuccess ||
+      (!few && grow_kept(p, &p->d_qa_list, &p->qa_list_elems, static_cast<size_t>(items) * 3, stream) != cudaSuccess))
     return IKBO_ERR_CUDA;
   QcAttnParams ap;
   std::memset(&ap, 0, sizeof(ap));
@@ -362,10 +398,13 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   ap.n_pages = n_pages;
   ap.max_blocks = max_blocks;
   ap.blocks_log2 = blocks_log2;
-  ap.target = qattn_target(p->num_sms);
+  ap.ctas = ctas;
+  ap.list = p->d_qa_list;
+  ap.max_items = items;
   ap.scale_log2 = scale * 1.4426950408889634f;
   ap.timeout_ns = p->timeout_ns;
-  if (launch_qattn(ap, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+  if ((few ? launch_qattn(ap, stream) : launch_qattn_tile(ap, stream)) != cudaSuccess)
+    return IKBO_ERR_CUDA;
   p->launches++;
   return IKBO_OK;
 }

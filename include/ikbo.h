@@ -448,11 +448,14 @@ ikbo_status_t ikbo_qcache_load(ikbo_plan_t p, const void* data, int n_pages, int
  * Workspaces are the plan's, grown by the first call that needs more (which
  * allocates; under stream capture that call fails with IKBO_ERR_CUDA and
  * allocates nothing, so make one eager call of the largest size first; a
- * captured call stays valid when later ones grow them).  Two variants, chosen
- * from the sizes: with few query rows per user and head the 4-bit blocks are
- * decoded in registers and nothing else is written; with many, histories are
- * decoded once into the workspace (512 bytes per token, head and the 128 rows
- * a history is padded to) and the kernel of ikbo_attn_forward reads that. */
+ * captured call stays valid when later ones grow them).  Three variants,
+ * chosen from the sizes (Lkv among them): with few query rows per user and K/V
+ * head (16, or a little more over short histories) the 4-bit blocks become
+ * operands in registers; with up to about 512 four-bit tiles are decoded in
+ * shared memory beside the tensor cores' work, once per 128 rows; with more,
+ * histories are decoded once into the workspace (512 bytes per token and head,
+ * each history padded to 128 rows) and the kernel of ikbo_attn_forward reads
+ * that. */
 ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void* data, int n_pages, int page,
                                        int H_kv, const int32_t* d_table, int max_blocks, const int32_t* d_lens,
                                        void* O, float* lse, int Lkv, int d, float scale, cudaStream_t stream);

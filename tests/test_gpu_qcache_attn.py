@@ -14,6 +14,12 @@ pytestmark = pytest.mark.gpu
 
 SCALE = 1.0 / math.sqrt(128)
 
+# The attention's three variants, reached by sizes alone: query rows a user
+# (candidates times Lq) and the bound on the tokens, which may be any.
+VARIANTS = {"registers": dict(c=1, Lq=8, Lkv=None), "tiles": dict(c=12, Lq=24, Lkv=8_000_000),
+            "decoded": dict(c=5, Lq=128, Lkv=2000)}
+each_variant = pytest.mark.parametrize("variant", list(VARIANTS))
+
 
 def queries(seed, n, H, Lq, big=1.0):
     return R.bf16(np.random.default_rng(seed).standard_normal((n, H, Lq, 128)) * big)
@@ -55,62 +61,72 @@ CASES = [
     ([3000, 129], [1, 2], 8, 2, 24, 128),
     ([5000], [1], 4, 1, 8, 1024),
     ([40] * 70, [1] * 70, 2, 2, 8, 16),
-    # many rows a user: decoded first
     ([130, 0, 128], [2, 2, 2], 1, 1, 128, 16),
     ([300, 1, 257], [40, 1, 30], 2, 2, 16, 64),
     ([64, 500], [9, 8], 4, 2, 40, 32),
     ([1, 1, 2], [30, 40, 50], 3, 1, 8, 16),
+    ([2500], [3], 4, 1, 16, 64),
+    ([700, 0, 129, 1], [70, 2, 1, 80], 2, 2, 16, 32),
 ]
 
 
+@pytest.mark.parametrize("bound", ["sum", "large"])
 @pytest.mark.parametrize("lens,cands,H,H_kv,Lq,page", CASES)
-def test_against_the_definition(lens, cands, H, H_kv, Lq, page):
+def test_against_the_definition(lens, cands, H, H_kv, Lq, page, bound):
+    """With the sum of the lengths as Lkv, and with a bound so large that every request of more
+    than 16 rows a user goes through the tile kernel (up to 512)."""
     st = R.Store(sum(lens) + H, lens, H_kv, page)
     m = np.repeat(np.arange(len(lens)), cands)
     m = np.random.default_rng(1).permutation(m).astype(np.int32)
     Q = queries(2, len(m), H, Lq)
+    Lkv = max(1, sum(lens)) if bound == "sum" else 1_000_000
     with B.Plan(len(m), len(lens), H) as p:
         p.plan(i32(m), len(lens), H, Lq)
-        O, lse = attend(p, Q, st)
+        O, lse = attend(p, Q, st, Lkv=Lkv)
         assert p.status() == B.IKBO_OK
         check(O, lse, Q, st.kv, m, H_kv)
-        O2, _ = attend(p, Q, st, lse=False, Lkv=max(1, sum(lens)))
-        assert torch.equal(O, O2)  # bit for bit, with or without the log-sum-exp, whatever the bound
+        O2, _ = attend(p, Q, st, lse=False, Lkv=Lkv)
+        assert torch.equal(O, O2)  # bit for bit, with or without the log-sum-exp
 
 
-@pytest.mark.parametrize("many", [False, True])
-def test_peaked_scores_and_other_scales(many):
+@each_variant
+def test_peaked_scores_and_other_scales(variant):
     """Scores of several hundred: the reference maximum moves; a scale of its own."""
-    lens, cands, Lq = ([600, 100], [1, 2], 8) if not many else ([600, 100], [30, 40], 16)
-    st = R.Store(8, lens, 2, 16, outlier=8.0)
-    m = np.repeat(np.arange(2), cands).astype(np.int32)
+    v = VARIANTS[variant]
+    Lq, Lkv = v["Lq"], v["Lkv"]
+    st = R.Store(8, [600, 100], 2, 16, outlier=8.0)
+    m = np.repeat(np.arange(2), v["c"]).astype(np.int32)
     Q = queries(5, len(m), 2, Lq, big=4.0)
     with B.Plan(len(m), 2, 2) as p:
         p.plan(i32(m), 2, 2, Lq)
         for scale in (SCALE, 0.01, 0.5):
-            O, _ = attend(p, Q, st, lse=False, scale=scale)
+            O, _ = attend(p, Q, st, lse=False, Lkv=Lkv, scale=scale)
             check(O, None, Q, st.kv, m, 2, scale)
 
 
-@pytest.mark.parametrize("many", [False, True])
-def test_candidates_without_a_user_keep_their_rows(many):
-    Lq = 128 if many else 8
+@each_variant
+def test_candidates_without_a_user_keep_their_rows(variant):
+    v = VARIANTS[variant]
+    Lq = v["Lq"]
     st = R.Store(4, [50, 20], 1, 16)
-    m = np.array([1, 7, 0, -1, 1, 0, 1, 1], np.int32)
-    Q = queries(6, 8, 1, Lq)
-    with B.Plan(8, 2, 1) as p:
+    m = np.repeat([1, 7, 0, -1, 1, 0, 1, 1], v["c"]).astype(np.int32)
+    if variant == "registers":
+        m = m[:4]
+    Q = queries(6, len(m), 1, Lq)
+    with B.Plan(len(m), 2, 1) as p:
         p.plan(i32(m), 2, 1, Lq)
-        O, lse = attend(p, Q, st)
+        O, lse = attend(p, Q, st, Lkv=v["Lkv"])
         assert p.status() == B.IKBO_ERR_MAP_OUT_OF_RANGE
         check(O, lse, Q, st.kv, m, 1)
-        assert bool(torch.isnan(O[[1, 3]]).all()) and bool(torch.isnan(lse[[1, 3]]).all())
+        out = torch.from_numpy((m < 0) | (m > 1))
+        assert bool(torch.isnan(O[out]).all()) and bool(torch.isnan(lse[out]).all())
 
 
-@pytest.mark.parametrize("many", [False, True])
-def test_values_that_are_not_finite(many):
+@each_variant
+def test_values_that_are_not_finite(variant):
     """A NaN in one user's values reaches that user's rows and no others; an
     infinite query makes its own row NaN."""
-    Lq, c = (64, 4) if many else (8, 1)
+    Lq, c, Lkv = (VARIANTS[variant][k] for k in ("Lq", "c", "Lkv"))
     st = R.Store(7, [40, 40, 40], 1, 16)
     st.data[st.table[1, 2], 0, 0, 1280 + 1024:1280 + 1040] = 0xFF  # a value's pairs of user 1's token 32
     m = np.repeat(np.arange(3), c).astype(np.int32)
@@ -118,20 +134,20 @@ def test_values_that_are_not_finite(many):
     Q[2 * c, 0, 3, 5] = np.inf
     with B.Plan(3 * c, 3, 1) as p:
         p.plan(i32(m), 3, 1, Lq)
-        O, _ = attend(p, Q, st)
+        O, _ = attend(p, Q, st, Lkv=Lkv)
     nan = torch.isnan(O).cpu().numpy()
     assert nan[c:2 * c].all() and not nan[:c].any()
     rows = nan[2 * c:].any(-1)
     assert rows[0, 0, 3] and rows.sum() == 1
 
 
-@pytest.mark.parametrize("many", [False, True])
-def test_broken_tables_are_reported(many):
-    Lq, c = (128, 3) if many else (8, 1)
+@each_variant
+def test_broken_tables_are_reported(variant):
+    Lq, c, bound = (VARIANTS[variant][k] for k in ("Lq", "c", "Lkv"))
     m = np.repeat(np.arange(2), c).astype(np.int32)
     Q = queries(6, 2 * c, 1, Lq)
 
-    def run(change, Lkv=None):
+    def run(change, Lkv=bound):
         st = R.Store(9, [40, 300], 1, 16)
         kv = list(st.kv)
         change(st)
@@ -156,7 +172,8 @@ def test_broken_tables_are_reported(many):
 
     O, kv = run(length)
     check(O, None, Q, [kv[0], (kv[1][0][:0], kv[1][1][:0])], m, 1)
-    run(lambda st: None, Lkv=339)
+    if variant != "tiles":  # a bound below the sum (the tile kernel takes such short histories with a large one only)
+        run(lambda st: None, Lkv=339)
 
 
 def test_refusals_of_the_planned_request():
@@ -184,28 +201,30 @@ def test_refusals_of_the_planned_request():
             B.IKBO_ERR_INVALID_ARG  # 3 heads over 2
 
 
-@pytest.mark.parametrize("many", [False, True])
-def test_other_stream_and_repeats(many):
-    lens, cands, Lq = ([3000, 2000], [1, 1], 8) if not many else ([300, 200], [20, 20], 16)
-    st = R.Store(11, lens, 4, 64)
-    m = np.repeat(np.arange(2), cands).astype(np.int32)
+@each_variant
+def test_other_stream_and_repeats(variant):
+    v = VARIANTS[variant]
+    Lq = v["Lq"]
+    st = R.Store(11, [3000, 2000] if variant != "decoded" else [700, 300], 4, 64)
+    m = np.repeat(np.arange(2), v["c"]).astype(np.int32)
     Q = queries(3, len(m), 4, Lq)
     with B.Plan(len(m), 2, 4) as p:
         s = torch.cuda.Stream()
         torch.cuda.synchronize()
         p.plan(i32(m), 2, 4, Lq, stream=s)
-        outs = [attend(p, Q, st, stream=s)[0] for _ in range(3)]
+        outs = [attend(p, Q, st, Lkv=v["Lkv"], stream=s)[0] for _ in range(3)]
         assert p.status(s) == B.IKBO_OK
         check(outs[0], None, Q, st.kv, m, 4)
         assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
-@pytest.mark.parametrize("many", [False, True])
-def test_graphs_keep_their_workspace(many):
+@each_variant
+def test_graphs_keep_their_workspace(variant):
     """A captured call replays after a larger eager call has grown the plan's workspaces; a call
     that would have to allocate is refused under capture."""
     small, large = ([200, 90], [400, 3000])
-    c, Lq = (20, 16) if many else (1, 8)
+    c, Lq = VARIANTS[variant]["c"], VARIANTS[variant]["Lq"]
+    low, high = (290, 3400) if variant != "tiles" else (8_000_000, 8_000_000)
     m = np.repeat(np.arange(2), c).astype(np.int32)
     Q = queries(3, len(m), 2, Lq)
     a, b = R.Store(1, small, 2, 16), R.Store(2, large, 2, 64)
@@ -216,14 +235,14 @@ def test_graphs_keep_their_workspace(many):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             with pytest.raises(B.IkboError) as e:
-                p.attn_qcache_forward(q, data, 16, table, ln, O, Lkv=290)
+                p.attn_qcache_forward(q, data, 16, table, ln, O, Lkv=low)
         assert e.value.code == B.IKBO_ERR_CUDA
-        p.attn_qcache_forward(q, data, 16, table, ln, O, Lkv=290)
+        p.attn_qcache_forward(q, data, 16, table, ln, O, Lkv=low)
         first = O.clone()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            p.attn_qcache_forward(q, data, 16, table, ln, O, Lkv=290)
-        big, _ = attend(p, Q, b)
+            p.attn_qcache_forward(q, data, 16, table, ln, O, Lkv=low)
+        big, _ = attend(p, Q, b, Lkv=high)
         check(big, None, Q, b.kv, m, 2)
         O.zero_()
         graph.replay()
@@ -233,7 +252,7 @@ def test_graphs_keep_their_workspace(many):
 
 
 def test_pages_behind_four_gigabytes():
-    """Pages whose byte offsets need more than 32 bits, read by both variants and written."""
+    """Pages whose byte offsets need more than 32 bits, read by every variant and written."""
     page, H = 128, 8
     n_pages = 30000  # 4.9 GB
     assert B.ikbo_qcache_bytes(n_pages, page, H) > 2**32
@@ -245,13 +264,13 @@ def test_pages_behind_four_gigabytes():
     values = [R.values(*R.quantise(x)) for x in (K, V)]
     with B.Plan(40, 1, H) as p:
         p.qcache_append(bf(K), bf(V), i32(slots), data, page)
-        for n, Lq in ((1, 8), (24, 8)):
+        for n, Lq, Lkv in ((1, 8, 300), (24, 8, 1_000_000), (24, 24, 300)):
             m = np.zeros(n, np.int32)
             Q = queries(3, n, H, Lq)
             p.plan(i32(m), 1, H, Lq)
             q = bf(Q)
             O = torch.empty_like(q)
-            p.attn_qcache_forward(q, data, page, i32(table), i32([300]), O, Lkv=300)
+            p.attn_qcache_forward(q, data, page, i32(table), i32([300]), O, Lkv=Lkv)
             assert p.status() == B.IKBO_OK
             check(O, None, Q, [(values[0], values[1])], m, H)
 
