@@ -355,12 +355,24 @@ QCACHE_BLOCK_BYTES = 2560  # 16 tokens of one head
 QCACHE_MAX_USERS = 8192
 
 
-def _here(t: torch.Tensor, dtype, name: str) -> int:
-    """_dev, and the tensor lies on the current device (where the call launches)."""
-    ptr = _dev(t, dtype, name)
-    if t.device.index != torch.cuda.current_device():
+def _current_device(t: torch.Tensor, name: str) -> int:
+    """The current device, for a call whose argument t is on a CUDA device at all."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """_stream for the calls that take single tokens: the current stream without a Python object for it."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _here(t: torch.Tensor, dtype, name: str, dev: int) -> int:
+    """_dev, and the tensor lies on device dev (the current one, where the call launches)."""
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        _dev(t, dtype, name)
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return ptr
+    return t.data_ptr()
 
 
 def ikbo_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -389,33 +401,37 @@ def ikbo_rope_destroy(rope: int) -> None:
     load().ikbo_rope_destroy(rope)
 
 
-def _rope(name: str, plan: int, rope: int, X: torch.Tensor, Y: torch.Tensor, start, broadcast: bool, stream) -> None:
-    for t, what in ((X, "input"), (Y, "output")):
-        if not t.is_cuda:
-            raise ValueError(f"{what} must be a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{what} is on {t.device}, not on the current device")
-    if X.dtype not in ROPE_DTYPES or Y.dtype != X.dtype:
+_I64X3 = ctypes.c_int64 * 3
+
+
+def _rope(fn, name: str, plan: int, rope: int, X: torch.Tensor, Y: torch.Tensor, start, broadcast: bool, stream) -> None:
+    dev = _current_device(X, "input")
+    if X.get_device() != dev or Y.get_device() != dev:
+        raise ValueError(f"input and output are on {X.device} and {Y.device}, not on the current device")
+    shape = X.shape
+    dtype = ROPE_DTYPES.get(X.dtype)
+    if dtype is None or Y.dtype is not X.dtype:
         raise ValueError("input and output must share a dtype: bfloat16, float16 or float32")
-    if X.shape != Y.shape or X.dim() not in (3, 4):
+    if shape != Y.shape or len(shape) not in (3, 4):
         raise ValueError("input and output must share a shape [n, H, L, d] or [rows, H, d]")
-    if X.shape[-1] > 1 and (X.stride(-1) != 1 or Y.stride(-1) != 1):
-        raise ValueError("the last dimension must be contiguous")
-    if X.dim() == 4:
-        n, H, L, d = X.shape
-        xs, ys = X.stride()[:3], Y.stride()[:3]
+    if len(shape) == 4:
+        n, H, L, d = shape
     else:
-        n, H, d = X.shape
-        L, xs, ys = 1, X.stride()[:2] + (0,), Y.stride()[:2] + (0,)
+        n, H, d = shape
+        L = 1
+    cx = cy = None  # NULL: contiguous
+    if not (X.is_contiguous() and Y.is_contiguous()):
+        if d > 1 and (X.stride(-1) != 1 or Y.stride(-1) != 1):
+            raise ValueError("the last dimension must be contiguous")
+        cx, cy = (_I64X3(*(t.stride()[:3] if len(shape) == 4 else t.stride()[:2] + (0,))) for t in (X, Y))
     sptr = None
     if start is not None:
-        sptr = _here(start, torch.int32, "start")
+        sptr = _here(start, torch.int32, "start", dev)
         if start.dim() != 1 or (not broadcast and start.numel() != n):
             raise ValueError("start must be [n], or [n_users] with broadcast")
-    i64x3 = ctypes.c_int64 * 3
-    cx, cy = i64x3(*xs), i64x3(*ys)
-    _check(getattr(load(), name)(plan, rope, X.data_ptr(), ctypes.addressof(cx), Y.data_ptr(), ctypes.addressof(cy),
-                                 sptr, int(broadcast), ROPE_DTYPES[X.dtype], n, H, L, d, _stream(stream)), name)
+    rc = fn(plan, rope, X.data_ptr(), cx, Y.data_ptr(), cy, sptr, broadcast, dtype, n, H, L, d, _raw_stream(stream, dev))
+    if rc != IKBO_OK:
+        raise IkboError(rc, name)
 
 
 def ikbo_rope_forward(plan: int, rope: int, X: torch.Tensor, Y: torch.Tensor, start: Optional[torch.Tensor] = None,
@@ -423,13 +439,13 @@ def ikbo_rope_forward(plan: int, rope: int, X: torch.Tensor, Y: torch.Tensor, st
     """Y = X [n, H, L, d] (or [rows, H, d]: one token each) with its pairs rotated by the
     angles of positions start[i] + l; with broadcast start[map[i]] + l of the planned
     request (start then holds one position per user).  Y may be X."""
-    _rope("ikbo_rope_forward", plan, rope, X, Y, start, broadcast, stream)
+    _rope(load().ikbo_rope_forward, "ikbo_rope_forward", plan, rope, X, Y, start, broadcast, stream)
 
 
 def ikbo_rope_backward(plan: int, rope: int, dY: torch.Tensor, dX: torch.Tensor, start: Optional[torch.Tensor] = None,
                        broadcast: bool = False, stream=None) -> None:
     """Gradient of ikbo_rope_forward: dX from dY."""
-    _rope("ikbo_rope_backward", plan, rope, dY, dX, start, broadcast, stream)
+    _rope(load().ikbo_rope_backward, "ikbo_rope_backward", plan, rope, dY, dX, start, broadcast, stream)
 
 
 def ikbo_qcache_bytes(n_pages: int, page: int, H: int) -> int:
@@ -437,18 +453,20 @@ def ikbo_qcache_bytes(n_pages: int, page: int, H: int) -> int:
     return int(load().ikbo_qcache_bytes(n_pages, page, H))
 
 
-def _qcache(data: torch.Tensor, page: int):
-    ptr = _here(data, torch.uint8, "data")
-    if data.dim() != 4 or page < 16 or data.shape[2] * 16 != page or data.shape[3] != QCACHE_BLOCK_BYTES:
+def _qcache(data: torch.Tensor, page: int, dev: int):
+    ptr = _here(data, torch.uint8, "data", dev)
+    shape = data.shape
+    if len(shape) != 4 or page < 16 or shape[2] * 16 != page or shape[3] != QCACHE_BLOCK_BYTES:
         raise ValueError(f"data must be [n_pages, H, page // 16, {QCACHE_BLOCK_BYTES}]")
-    return ptr, data.shape[0], data.shape[1]
+    return ptr, shape[0], shape[1]
 
 
-def _qtable(table: torch.Tensor, lens: torch.Tensor):
-    tptr, lptr = _here(table, torch.int32, "table"), _here(lens, torch.int32, "lens")
-    if table.dim() != 2 or lens.dim() != 1 or lens.numel() != table.shape[0]:
+def _qtable(table: torch.Tensor, lens: torch.Tensor, dev: int):
+    tptr, lptr = _here(table, torch.int32, "table", dev), _here(lens, torch.int32, "lens", dev)
+    shape = table.shape
+    if len(shape) != 2 or lens.dim() != 1 or lens.numel() != shape[0]:
         raise ValueError("table must be [n_users, max_blocks] and lens [n_users]")
-    return tptr, lptr, table.shape[0], table.shape[1]
+    return tptr, lptr, shape[0], shape[1]
 
 
 def ikbo_qcache_resize(plan: int, lens: torch.Tensor, new_lens: torch.Tensor, table: torch.Tensor, page: int,
@@ -457,40 +475,43 @@ def ikbo_qcache_resize(plan: int, lens: torch.Tensor, new_lens: torch.Tensor, ta
     """Set every user's length: pages are taken from and given back to the free list,
     and each added token gets its slot (and position).  lens, table, free and n_free
     change in place; all or nothing."""
-    tptr, lptr, n_users, max_blocks = _qtable(table, lens)
-    if new_lens.shape != lens.shape or tuple(slot_offsets.shape) != (n_users + 1,) or n_free.numel() != 1 or \
-            free.dim() != 1 or slots.dim() != 1 or (positions is not None and positions.shape != slots.shape):
+    dev, i32 = _current_device(lens, "lens"), torch.int32
+    tptr, lptr, n_users, max_blocks = _qtable(table, lens, dev)
+    if new_lens.shape != lens.shape or slot_offsets.dim() != 1 or slot_offsets.numel() != n_users + 1 or \
+            n_free.numel() != 1 or free.dim() != 1 or slots.dim() != 1 or \
+            (positions is not None and positions.shape != slots.shape):
         raise ValueError("inconsistent cache shapes")
-    i32 = torch.int32
-    _check(load().ikbo_qcache_resize(plan, lptr, _here(new_lens, i32, "new_lens"), n_users, tptr, max_blocks, page,
-                                     _here(free, i32, "free"), _here(n_free, i32, "n_free"), free.numel(),
-                                     _here(slots, i32, "slots"), _here(slot_offsets, i32, "slot_offsets"),
-                                     None if positions is None else _here(positions, i32, "positions"), slots.numel(),
-                                     _stream(stream)), "ikbo_qcache_resize")
+    _check(load().ikbo_qcache_resize(plan, lptr, _here(new_lens, i32, "new_lens", dev), n_users, tptr, max_blocks, page,
+                                     _here(free, i32, "free", dev), _here(n_free, i32, "n_free", dev), free.numel(),
+                                     _here(slots, i32, "slots", dev), _here(slot_offsets, i32, "slot_offsets", dev),
+                                     None if positions is None else _here(positions, i32, "positions", dev),
+                                     slots.numel(), _raw_stream(stream, dev)), "ikbo_qcache_resize")
 
 
 def ikbo_qcache_append(plan: int, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, data: torch.Tensor,
                        page: int, stream=None) -> None:
     """Quantise row r of K and V ([n_rows, H, 128] bf16; rows may be strided, both
     alike) into slot slots[r] of the cache (-1: skipped)."""
-    dptr, n_pages, H = _qcache(data, page)
-    for t, name in ((K, "K"), (V, "V")):
-        if not t.is_cuda or t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be a CUDA tensor of bfloat16")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, not on the current device")
-    if K.dim() != 3 or K.shape != V.shape or K.shape[1] != H or tuple(slots.shape) != (K.shape[0],):
+    dev, bf = _current_device(data, "data"), torch.bfloat16
+    dptr, n_pages, H = _qcache(data, page, dev)
+    shape = K.shape
+    if len(shape) != 3 or shape != V.shape or shape[1] != H or slots.dim() != 1 or slots.numel() != shape[0]:
         raise ValueError("K and V must be [n_rows, H, d] and slots [n_rows]")
-    n, _, d = K.shape
-    strides = {(t.stride(0) if n > 1 else max(t.stride(0), H * d)) for t in (K, V)}
-    for t in (K, V):
-        if n and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
-            raise ValueError("the heads of a row must be contiguous")
-    if n > 1 and len(strides) != 1:
-        raise ValueError("K and V must have the same row stride")
-    stride = max(strides) if n > 1 else (H * d + 7) // 8 * 8
-    _check(load().ikbo_qcache_append(plan, K.data_ptr(), V.data_ptr(), stride, _here(slots, torch.int32, "slots"), n,
-                                     H, d, dptr, n_pages, page, _stream(stream)), "ikbo_qcache_append")
+    n, _, d = shape
+    for t, name in ((K, "K"), (V, "V")):
+        if t.get_device() != dev or t.dtype is not bf:
+            raise ValueError(f"{name} must be a tensor of bfloat16 on the current CUDA device")
+    stride = (H * d + 7) // 8 * 8
+    if not (K.is_contiguous() and V.is_contiguous()):
+        for t in (K, V):
+            if n and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+                raise ValueError("the heads of a row must be contiguous")
+        if n > 1:
+            stride = K.stride(0)
+            if V.stride(0) != stride:
+                raise ValueError("K and V must have the same row stride")
+    _check(load().ikbo_qcache_append(plan, K.data_ptr(), V.data_ptr(), stride, _here(slots, torch.int32, "slots", dev), n,
+                                     H, d, dptr, n_pages, page, _raw_stream(stream, dev)), "ikbo_qcache_append")
 
 
 def ikbo_qcache_load(plan: int, data: torch.Tensor, page: int, table: torch.Tensor, lens: torch.Tensor,
@@ -498,9 +519,10 @@ def ikbo_qcache_load(plan: int, data: torch.Tensor, page: int, table: torch.Tens
                      stream=None) -> None:
     """Read histories back as jagged bf16 rows: token t of user u to row
     kv_offsets[u] + t of K and V [rows, H, 128] (either may be None)."""
-    dptr, n_pages, H = _qcache(data, page)
-    tptr, lptr, n_users, max_blocks = _qtable(table, lens)
-    if tuple(kv_offsets.shape) != (n_users + 1,):
+    dev, bf = _current_device(data, "data"), torch.bfloat16
+    dptr, n_pages, H = _qcache(data, page, dev)
+    tptr, lptr, n_users, max_blocks = _qtable(table, lens, dev)
+    if kv_offsets.dim() != 1 or kv_offsets.numel() != n_users + 1:
         raise ValueError("kv_offsets must be [n_users + 1]")
     some = K if K is not None else V
     if some is None:
@@ -508,11 +530,11 @@ def ikbo_qcache_load(plan: int, data: torch.Tensor, page: int, table: torch.Tens
     for t in (K, V):
         if t is not None and (t.dim() != 3 or t.shape != some.shape or t.shape[1] != H):
             raise ValueError("K and V must be [rows, H, d]")
-    kptr = None if K is None else _here(K, torch.bfloat16, "K")
-    vptr = None if V is None else _here(V, torch.bfloat16, "V")
+    kptr = None if K is None else _here(K, bf, "K", dev)
+    vptr = None if V is None else _here(V, bf, "V", dev)
     _check(load().ikbo_qcache_load(plan, dptr, n_pages, page, H, some.shape[2], tptr, max_blocks, lptr, n_users,
-                                   _here(kv_offsets, torch.int32, "kv_offsets"), kptr, vptr, some.shape[0],
-                                   _stream(stream)), "ikbo_qcache_load")
+                                   _here(kv_offsets, torch.int32, "kv_offsets", dev), kptr, vptr, some.shape[0],
+                                   _raw_stream(stream, dev)), "ikbo_qcache_load")
 
 
 def ikbo_attn_qcache_forward(plan: int, Q: torch.Tensor, data: torch.Tensor, page: int, table: torch.Tensor,
@@ -520,21 +542,22 @@ def ikbo_attn_qcache_forward(plan: int, Q: torch.Tensor, data: torch.Tensor, pag
                              Lkv: Optional[int] = None, scale: Optional[float] = None, stream=None) -> None:
     """ikbo_attn_forward's definition over the cache: user u's keys are the lens[u]
     tokens of its pages.  Lkv: a bound on the sum of the lengths (default: what the
-    table can hold); the call's workspace goes by it."""
-    dptr, n_pages, H_kv = _qcache(data, page)
-    tptr, lptr, n_users, max_blocks = _qtable(table, lens)
-    if Q.dim() != 4 or O.shape != Q.shape or Q.shape[1] % H_kv != 0 or \
-            (lse is not None and tuple(lse.shape) != tuple(Q.shape[:3])):
+    table can hold); the call's workspace and variant go by it."""
+    dev, bf = _current_device(data, "data"), torch.bfloat16
+    dptr, n_pages, H_kv = _qcache(data, page, dev)
+    tptr, lptr, n_users, max_blocks = _qtable(table, lens, dev)
+    shape = Q.shape
+    if len(shape) != 4 or O.shape != shape or shape[1] % H_kv != 0 or (lse is not None and lse.shape != shape[:3]):
         raise ValueError("inconsistent attention shapes")
-    d = Q.shape[-1]
+    d = shape[3]
     if Lkv is None:
         Lkv = min(n_users * max_blocks * page, 2**31 - 1)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    bf = torch.bfloat16
-    _check(load().ikbo_attn_qcache_forward(plan, _here(Q, bf, "Q"), dptr, n_pages, page, H_kv, tptr, max_blocks, lptr,
-                                           _here(O, bf, "O"), None if lse is None else _here(lse, torch.float32, "lse"),
-                                           max(1, int(Lkv)), d, float(scale), _stream(stream)),
+    _check(load().ikbo_attn_qcache_forward(plan, _here(Q, bf, "Q", dev), dptr, n_pages, page, H_kv, tptr, max_blocks,
+                                           lptr, _here(O, bf, "O", dev),
+                                           None if lse is None else _here(lse, torch.float32, "lse", dev),
+                                           max(1, int(Lkv)), d, scale, _raw_stream(stream, dev)),
            "ikbo_attn_qcache_forward")
 
 
@@ -566,7 +589,7 @@ class Plan:
 
     def __init__(self, max_cand: int, max_users: int, max_heads: int = 1):
         self._map = None
-        self._request = None  # (n_cand, n_users, H, Lq) of the last plan()
+        self._request = None  # (n_cand, H, Lq) and n_users of the last plan()
         self.handle = ikbo_plan_create(max_cand, max_users, max_heads)
 
     def __enter__(self):
@@ -592,7 +615,7 @@ class Plan:
         # the plan borrows the map for every later call of this request: hold
         # the tensor so that a temporary passed here stays allocated
         self._map = map_
-        self._request = (map_.numel(), n_users, H, Lq)
+        self._request = ((map_.numel(), H, Lq), n_users)
 
     def lce_forward(self, U, C, Wu, Wc, b, Y, stream=None):
         ikbo_lce_forward(self.handle, U, C, Wu, Wc, b, Y, stream)
@@ -631,8 +654,7 @@ class Plan:
         ikbo_qcache_load(self.handle, data, page, table, lens, kv_offsets, K, V, stream)
 
     def attn_qcache_forward(self, Q, data, page, table, lens, O, lse=None, Lkv=None, scale=None, stream=None):
-        if self._request is not None and (Q.dim() != 4 or (Q.shape[0],) + tuple(Q.shape[1:3]) != self._request[:1] +
-                                          self._request[2:] or lens.numel() != self._request[1]):
+        if self._request is not None and (Q.shape[:3] != self._request[0] or lens.numel() != self._request[1]):
             raise ValueError("Q and lens must have the sizes of the planned request")
         ikbo_attn_qcache_forward(self.handle, Q, data, page, table, lens, O, lse, Lkv, scale, stream)
 

@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(QR_THREADS) qc_resize_kernel(const QcResizePar
   int32_t* take0 = qr_sm;                      // [n_users] pages taken before this user
   int32_t* give0 = qr_sm + p.n_users;          // [n_users] pages given back before
   int32_t* token0 = qr_sm + 2 * p.n_users;     // [n_users] tokens added before
+  int32_t* old = qr_sm + 3 * p.n_users;        // [n_users] lengths, as they were ..
+  int32_t* fresh = qr_sm + 4 * p.n_users;      // .. and as they are to be
   __shared__ int64_t warp_sums[3][33];
   __shared__ int bad_users;
   const int tid = threadIdx.x, n = p.n_users;
@@ -71,14 +73,18 @@ __global__ void __launch_bounds__(QR_THREADS) qc_resize_kernel(const QcResizePar
   const int page = 1 << p.page_log2;
   const int64_t most = static_cast<int64_t>(p.max_blocks) << p.page_log2;
   if (tid == 0) bad_users = 0;
+  bool bad = false;
+  for (int u = tid; u < n; u += QR_THREADS) {
+    old[u] = qc_length(p.lens, u, most, bad);
+    fresh[u] = qc_length(p.new_lens, u, most, bad);
+  }
   __syncthreads();
 
   const int per = (n + QR_THREADS - 1) / QR_THREADS;
   const int lo = min(tid * per, n), hi = min(lo + per, n);
   int64_t v[3] = {0, 0, 0}, total[3];
-  bool bad = false;
   for (int u = lo; u < hi; ++u) {
-    const int before = qc_length(p.lens, u, most, bad), after = qc_length(p.new_lens, u, most, bad);
+    const int before = old[u], after = fresh[u];
     const int have = (before + page - 1) >> p.page_log2, need = (after + page - 1) >> p.page_log2;
     v[0] += max(need - have, 0);
     v[1] += max(have - need, 0);
@@ -86,9 +92,8 @@ __global__ void __launch_bounds__(QR_THREADS) qc_resize_kernel(const QcResizePar
   }
   if (bad) bad_users = 1;
   scan3(v, total, warp_sums);
-  bool ignored = false;
   for (int u = lo; u < hi; ++u) {
-    const int before = qc_length(p.lens, u, most, ignored), after = qc_length(p.new_lens, u, most, ignored);
+    const int before = old[u], after = fresh[u];
     const int have = (before + page - 1) >> p.page_log2, need = (after + page - 1) >> p.page_log2;
     take0[u] = static_cast<int32_t>(v[0]);
     give0[u] = static_cast<int32_t>(v[1]);
@@ -111,25 +116,57 @@ __global__ void __launch_bounds__(QR_THREADS) qc_resize_kernel(const QcResizePar
   bool bad_page = false;
   for (int k = first; k < takes; k += step) {
     const int u = qc_find(take0, n, k);
-    const int have = (p.lens[u] + page - 1) >> p.page_log2;
+    const int have = (old[u] + page - 1) >> p.page_log2;
     const int id = p.free_pages[n_free - 1 - k];
     if (id < 0 || id >= p.n_pages) bad_page = true;
     p.table[static_cast<int64_t>(u) * p.max_blocks + have + (k - take0[u])] = id;
   }
-  for (int i = first; i < p.max_new; i += step) {
-    int slot = -1, pos = 0;
-    if (i < tokens) {
-      const int u = qc_find(token0, n, i);
-      const int before = p.lens[u];
-      pos = before + (i - token0[u]);
-      const int blk = pos >> p.page_log2, have = (before + page - 1) >> p.page_log2;
-      const int id = blk < have ? p.table[static_cast<int64_t>(u) * p.max_blocks + blk]
-                                : p.free_pages[n_free - 1 - (take0[u] + blk - have)];
-      if (id < 0 || id >= p.n_pages) bad_page = true;
-      else slot = (id << p.page_log2) + (pos & (page - 1));
+  // eight tokens in a row per thread: the first one's user is looked for, the
+  // others follow; their page numbers are loaded together
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
+  for (int64_t i0 = static_cast<int64_t>(first) * 8; i0 < p.max_new; i0 += static_cast<int64_t>(step) * 8) {
+    int slot[8], pos[8];
+    const int32_t* from[8];
+    int u = i0 < tokens ? qc_find(token0, n, static_cast<int>(i0)) : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      pos[j] = 0;
+      from[j] = nullptr;
+      const int i = static_cast<int>(i0) + j;
+      if (i0 + j < tokens) {
+        while (u + 1 < n && token0[u + 1] <= i) ++u;
+        const int before = old[u], have = (before + page - 1) >> p.page_log2;
+        pos[j] = before + (i - token0[u]);
+        const int blk = pos[j] >> p.page_log2;
+        from[j] = blk < have ? p.table + static_cast<int64_t>(u) * p.max_blocks + blk
+                             : p.free_pages + (n_free - 1 - (take0[u] + blk - have));
+      }
     }
-    p.slots[i] = slot;
-    if (p.positions) p.positions[i] = pos;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) slot[j] = from[j] ? *from[j] : -1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (slot[j] >= 0 && slot[j] < p.n_pages) {
+        slot[j] = (slot[j] << p.page_log2) + (pos[j] & (page - 1));
+      } else {
+        bad_page = bad_page || from[j] != nullptr;
+        slot[j] = -1;
+      }
+    }
+    if (wide && i0 + 8 <= p.max_new) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        *reinterpret_cast<int4*>(p.slots + i0 + j) = make_int4(slot[j], slot[j + 1], slot[j + 2], slot[j + 3]);
+        if (p.positions) *reinterpret_cast<int4*>(p.positions + i0 + j) = make_int4(pos[j], pos[j + 1], pos[j + 2], pos[j + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + j < p.max_new) {
+          p.slots[i0 + j] = slot[j];
+          if (p.positions) p.positions[i0 + j] = pos[j];
+        }
+    }
   }
   for (int u = first; u <= n; u += step) p.offsets[u] = refused ? 0 : (u == n ? tokens : token0[u]);
 
@@ -137,7 +174,7 @@ __global__ void __launch_bounds__(QR_THREADS) qc_resize_kernel(const QcResizePar
 
   for (int k = first; k < gives; k += step) {
     const int u = qc_find(give0, n, k);
-    const int need = (p.new_lens[u] + page - 1) >> p.page_log2;
+    const int need = (fresh[u] + page - 1) >> p.page_log2;
     int32_t* entry = p.table + static_cast<int64_t>(u) * p.max_blocks + need + (k - give0[u]);
     const int id = *entry;
     if (id < 0 || id >= p.n_pages) bad_page = true;
@@ -145,26 +182,25 @@ __global__ void __launch_bounds__(QR_THREADS) qc_resize_kernel(const QcResizePar
     *entry = -1;
   }
   if (!refused)
-    for (int u = first; u < n; u += step) p.lens[u] = p.new_lens[u];
+    for (int u = first; u < n; u += step) p.lens[u] = fresh[u];
   if (!refused && rank == 0 && tid == 0) *p.n_free = n_free - takes + gives;
   if (bad_page) atomicOr(p.status, DEV_ERR_CACHE);
 }
 
 // ------------------------------------------------------------------ append
-// Sixteen lanes take one head of one row: eight elements of K and eight of V
-// each, four lanes to a group of 32.  Bound: memory (2 bytes read and 0.625
-// written an element); per element about a dozen instructions, so the
-// quotient is not a division: q = (x - z) / s by one step of Markstein's
-// correction from the correctly rounded 1 / s ("Computation of elementary
-// functions on the IBM RISC System/6000 processor", 1990).  The codes are the
-// division's: the corrected quotient can only differ from the rounded one
-// where the true quotient is closer to a midpoint of fp32 than these operands
-// (a difference of bf16 values over a bf16 value) can be without hitting it.
+// Eight lanes take a head of a row, sixteen elements of K and of V each, two
+// lanes to a group of 32; a thread runs over its row's heads, so the slot and
+// the address are worked out once.  Bound: issue, not memory (2 bytes read and
+// 0.625 written an element): about ten instructions an element.  So there is no
+// division: q = (x - z) / s comes from an approximate reciprocal and one step of
+// Markstein's correction ("Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990), and so does the 7.5 below.  The codes are the
+// division's: the corrected quotient is exact where the quotient is an fp32
+// number, ties among them, and nowhere else does the quotient of these operands
+// (a difference of bf16 values over a bf16 value) come close enough to a
+// half-integer for its error of half an ulp to matter.
 constexpr int QA_THREADS = 256;
-
-struct GroupCode {
-  uint32_t codes, pair;
-};
+constexpr int QA_LANES = 8;  // of a head of a row
 
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -178,18 +214,52 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ float low_half(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_half(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
-__device__ __forceinline__ GroupCode quantise8(const uint4 x) {
-  uint32_t mn = min2(min2(x.x, x.y), min2(x.z, x.w)), mx = max2(max2(x.x, x.y), max2(x.z, x.w));
+struct GroupCode {
+  uint2 codes;    // of this lane's sixteen elements
+  uint32_t pair;  // (s, z)
+};
+
+// The codes by division: groups of extreme scales, or without values (0, or NaN).
+__device__ __noinline__ uint2 slow_codes(const uint4 x, const uint4 y, float s, float z) {
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t c[2] = {0, 0};
+  if (s > 0.f) {
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    mn = min2(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = max2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int j = 0; j < 16; ++j) {
+      const float t = ((j & 1) ? high_half(w[j >> 1]) : low_half(w[j >> 1])) - z;
+      const float q = fminf(fmaxf(__fdiv_rn(t, s), 16.f), 31.f);
+      c[j >> 3] |= (__float_as_uint(q + 8388608.f) & 15u) << (4 * (j & 7));
+    }
   }
+  return make_uint2(c[0], c[1]);
+}
+
+// Sixteen of a group's 32 elements; the other lane of the pair has the rest.
+__device__ __forceinline__ GroupCode quantise16(const uint4 x, const uint4 y) {
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t mn = min2(min2(min2(w[0], w[1]), min2(w[2], w[3])), min2(min2(w[4], w[5]), min2(w[6], w[7])));
+  uint32_t mx = max2(max2(max2(w[0], w[1]), max2(w[2], w[3])), max2(max2(w[4], w[5]), max2(w[6], w[7])));
+  mn = min2(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
+  mx = max2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mn = min2(mn, mn >> 16);  // the low half holds the group's, also where it is NaN
   mx = max2(mx, mx >> 16);
   const float lo = low_half(mn), hi = low_half(mx);
-  __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi * 0.5f - lo * 0.5f, 7.5f));
+  const float range = hi * 0.5f - lo * 0.5f;
+  float step;
+  if (range >= 1e-30f) {
+    constexpr float inv = 1.0f / 7.5f;
+    const float q0 = range * inv;
+    step = fmaf(fmaf(-q0, 7.5f, range), inv, q0);
+  } else {
+    step = __fdiv_rn(range, 7.5f);  // remainders would not be normal numbers (or the range is NaN)
+  }
+  __nv_bfloat16 sb = __float2bfloat16_rn(step);
   __nv_bfloat16 zb = __float2bfloat16_rn(lo - 16.f * __bfloat162float(sb));
   float s = __bfloat162float(sb), z = __bfloat162float(zb);
   if (!(fabsf(s) <= 3.4e38f && fabsf(z) <= 3.4e38f)) {
@@ -198,55 +268,79 @@ __device__ __forceinline__ GroupCode quantise8(const uint4 x) {
   }
   GroupCode g;
   g.pair = static_cast<uint32_t>(__bfloat16_as_ushort(sb)) | (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
-  g.codes = 0;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  const bool wide = s >= 1e-30f;  // the reciprocal and the remainder stay normal numbers
-  const float inv = __frcp_rn(s);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float t = ((j & 1) ? high_half(w[j >> 1]) : low_half(w[j >> 1])) - z;
-    float q;
-    if (wide) {
-      const float q0 = t * inv;
-      q = fmaf(fmaf(-q0, s, t), inv, q0);
-    } else {
-      q = s > 0.f ? __fdiv_rn(t, s) : 16.f;
-    }
-    q = fminf(fmaxf(q, 16.f), 31.f);  // 16 for a NaN
-    // adding 2^23 rounds to an integer, whose low four bits are q - 16
-    g.codes |= (__float_as_uint(q + 8388608.f) & 15u) << (4 * j);
+  if (!(s >= 1e-30f && s <= 1e30f)) {  // the reciprocal or the remainders would not be normal numbers
+    g.codes = slow_codes(x, y, s, z);
+    return g;
   }
+  // a quotient q in 16 .. 31 plus 2^23 is rounded to an integer in its low bits:
+  // 0x4B000000 + q.  Sixteen-fold sums of those, less the constants', are the codes
+  const float inv = rcp_approx(s);
+  uint32_t c[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    c[h] = 0;
+#pragma unroll
+    for (int j = 7; j >= 0; --j) {
+      const uint32_t e = w[4 * h + (j >> 1)];
+      const float t = ((j & 1) ? high_half(e) : low_half(e)) - z;
+      const float q0 = t * inv;
+      const float q = fminf(fmaxf(fmaf(fmaf(-q0, s, t), inv, q0), 16.f), 31.f);
+      c[h] = c[h] * 16u + __float_as_uint(q + 8388608.f);
+    }
+    c[h] -= 0x4B000010u * 0x11111111u;
+  }
+  g.codes = make_uint2(c[0], c[1]);
   return g;
 }
 
 __global__ void __launch_bounds__(QA_THREADS) qc_append_kernel(const QcAppendParams p) {
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * QA_THREADS + threadIdx.x;
-  const int64_t unit = e >> 4;  // (row, head)
-  const int lane16 = static_cast<int>(e & 15);
-  const int64_t units = static_cast<int64_t>(p.n_rows) * p.H;
-  const bool there = unit < units;
-  const int64_t row = there ? unit / p.H : 0;
-  const int h = there ? static_cast<int>(unit - row * p.H) : 0;
+  const int row = static_cast<int>(blockIdx.x) * (QA_THREADS / QA_LANES) + (static_cast<int>(threadIdx.x) / QA_LANES);
+  const int lane8 = static_cast<int>(threadIdx.x) % QA_LANES;
+  const int h0 = static_cast<int>(blockIdx.y) * p.heads_per_cta, h1 = min(p.H, h0 + p.heads_per_cta);
+  const bool there = row < p.n_rows;
   const int slot = there ? __ldg(p.slots + row) : -1;
   const bool valid = slot >= 0 && slot < p.n_slots;
-  if (there && slot != -1 && !valid && lane16 == 0 && h == 0) atomicOr(p.status, DEV_ERR_CACHE);
-  uint4 k = make_uint4(0, 0, 0, 0), v = k;
-  if (valid) {
-    const int64_t at = row * p.row_stride + h * QC_D + lane16 * 8;
-    k = __ldg(reinterpret_cast<const uint4*>(p.K + at));
-    v = __ldg(reinterpret_cast<const uint4*>(p.V + at));
-  }
-  const GroupCode gk = quantise8(k), gv = quantise8(v);  // whole warps: lanes without a row code zeros
-  if (!valid) return;
+  if (there && slot != -1 && !valid && lane8 == 0 && h0 == 0) atomicOr(p.status, DEV_ERR_CACHE);
+  const int64_t at = (valid ? row * p.row_stride : 0) + static_cast<int64_t>(h0) * QC_D + lane8 * 16;
+  const uint4* k = reinterpret_cast<const uint4*>(p.K + at);
+  const uint4* v = reinterpret_cast<const uint4*>(p.V + at);
   const int64_t block = slot >> 4;
   const int64_t page = block >> p.blocks_log2, sub = block & ((1 << p.blocks_log2) - 1);
-  uint8_t* base = p.data + (((page * p.H + h) << p.blocks_log2) + sub) * QC_BLOCK_BYTES;
   const int r = slot & 15;
-  *reinterpret_cast<uint32_t*>(base + r * 64 + lane16 * 4) = gk.codes;
-  *reinterpret_cast<uint32_t*>(base + QC_HALF_BYTES + r * 64 + lane16 * 4) = gv.codes;
-  if ((lane16 & 3) == 0) {
-    *reinterpret_cast<uint32_t*>(base + QC_CODE_BYTES + r * 16 + lane16) = gk.pair;
-    *reinterpret_cast<uint32_t*>(base + QC_HALF_BYTES + QC_CODE_BYTES + r * 16 + lane16) = gv.pair;
+  uint8_t* base = p.data + (((page * p.H + h0) << p.blocks_log2) + sub) * QC_BLOCK_BYTES + r * 64 + lane8 * 8;
+  uint8_t* pairs = base - r * 64 - lane8 * 8 + QC_CODE_BYTES + r * 16 + (lane8 >> 1) * 4;
+  const int64_t step = static_cast<int64_t>(QC_BLOCK_BYTES) << p.blocks_log2;  // from a head to the next
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  // whole warps: lanes without a row code zeros; the next head's elements are on their way
+  uint4 k0 = none, k1 = none, v0 = none, v1 = none;
+  if (valid) {
+    k0 = __ldg(k);
+    k1 = __ldg(k + 1);
+    v0 = __ldg(v);
+    v1 = __ldg(v + 1);
+  }
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    const uint4 a0 = k0, a1 = k1, b0 = v0, b1 = v1;
+    k += QC_D / 8;
+    v += QC_D / 8;
+    if (valid && h + 1 < h1) {
+      k0 = __ldg(k);
+      k1 = __ldg(k + 1);
+      v0 = __ldg(v);
+      v1 = __ldg(v + 1);
+    }
+    const GroupCode gk = quantise16(a0, a1), gv = quantise16(b0, b1);
+    if (valid) {
+      *reinterpret_cast<uint2*>(base) = gk.codes;
+      *reinterpret_cast<uint2*>(base + QC_HALF_BYTES) = gv.codes;
+      if ((lane8 & 1) == 0) {
+        *reinterpret_cast<uint32_t*>(pairs) = gk.pair;
+        *reinterpret_cast<uint32_t*>(pairs + QC_HALF_BYTES) = gv.pair;
+      }
+    }
+    base += step;
+    pairs += step;
   }
 }
 
@@ -409,9 +503,9 @@ __global__ void __launch_bounds__(QL_THREADS) qc_load_kernel(const QcLoadParams 
 }  // namespace
 
 cudaError_t launch_qc_resize(const QcResizeParams& p, cudaStream_t s) {
-  const size_t smem = 3 * sizeof(int32_t) * static_cast<size_t>(p.n_users);
+  const size_t smem = 5 * sizeof(int32_t) * static_cast<size_t>(p.n_users);
   cudaError_t e = cudaFuncSetAttribute(qc_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(3 * sizeof(int32_t) * SEG_MAX_USERS));
+                                       static_cast<int>(5 * sizeof(int32_t) * SEG_MAX_USERS));
   if (e != cudaSuccess) return e;
   // a CTA for each 8192 tokens, up to the portable cluster of 8
   int ctas = 1;
@@ -431,11 +525,17 @@ cudaError_t launch_qc_resize(const QcResizeParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, qc_resize_kernel, p);
 }
 
-cudaError_t launch_qc_append(const QcAppendParams& p, cudaStream_t s) {
-  const int64_t threads = static_cast<int64_t>(p.n_rows) * p.H * 16;
-  const int64_t ctas = (threads + QA_THREADS - 1) / QA_THREADS;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  qc_append_kernel<<<static_cast<unsigned>(ctas), QA_THREADS, 0, s>>>(p);
+cudaError_t launch_qc_append(QcAppendParams p, int num_sms, cudaStream_t s) {
+  const int per = QA_THREADS / QA_LANES;
+  const int ctas = (p.n_rows + per - 1) / per;
+  // heads are spread over CTAs only while that gives work to more SMs
+  int parts = 1;
+  while (parts < p.H && static_cast<int64_t>(ctas) * parts < 16 * static_cast<int64_t>(num_sms)) parts *= 2;
+  if (parts > p.H) parts = p.H;
+  p.heads_per_cta = (p.H + parts - 1) / parts;
+  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>((p.H + p.heads_per_cta - 1) / p.heads_per_cta));
+  if (grid.y > 65535) return cudaErrorInvalidValue;
+  qc_append_kernel<<<grid, QA_THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -12,7 +12,7 @@
 namespace ikbo {
 cudaError_t launch_rope(const RopeParams& p, int dtype, int num_sms, cudaStream_t s);
 cudaError_t launch_qc_resize(const QcResizeParams& p, cudaStream_t s);
-cudaError_t launch_qc_append(const QcAppendParams& p, cudaStream_t s);
+cudaError_t launch_qc_append(QcAppendParams p, int num_sms, cudaStream_t s);
 cudaError_t launch_qc_load(const QcLoadParams& p, int num_sms, cudaStream_t s);
 int qattn_ctas(int num_sms);
 size_t qattn_part_elems(int num_sms);
@@ -261,9 +261,10 @@ ikbo_status_t ikbo_qcache_append(ikbo_plan_t p, const void* K, const void* V, in
   ap.row_stride = row_stride;
   ap.n_rows = n_rows;
   ap.H = H;
+  ap.heads_per_cta = H;
   ap.blocks_log2 = blocks_log2_of(page);
   ap.n_slots = static_cast<int64_t>(n_pages) * page;
-  if (launch_qc_append(ap, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+  if (launch_qc_append(ap, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
   p->launches++;
   return IKBO_OK;
 }

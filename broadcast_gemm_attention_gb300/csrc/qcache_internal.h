@@ -59,7 +59,7 @@ struct QcAppendParams {
   uint8_t* data;
   uint32_t* status;
   int64_t row_stride;
-  int n_rows, H;
+  int n_rows, H, heads_per_cta;
   int blocks_log2;      // log2(page / 16)
   int64_t n_slots;
 };
