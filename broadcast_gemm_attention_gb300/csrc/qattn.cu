@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
         for (int nt = 0; nt < 2; ++nt) {
           const uint32_t s2 = __byte_perm(kp[nt], 0, 0x1010), z2 = __byte_perm(kp[nt], 0, 0x3232);
           const uint32_t w4 = w == 0 ? kc[nt].x : (w == 1 ? kc[nt].y : (w == 2 ? kc[nt].z : kc[nt].w));
-          mma16816(sc[nt], q[2 * w], qc_decode<0>(w4, s2, z2), qc_decode<1>(w4, s2, z2));
-          mma16816(sd[nt], q[2 * w + 1], qc_decode<2>(w4, s2, z2), qc_decode<3>(w4, s2, z2));
+          mma16816(sc[nt], q[2 * w], qc_decode<0>(w4, s2, z2, p.sixteen), qc_decode<1>(w4, s2, z2, p.sixteen));
+          mma16816(sd[nt], q[2 * w + 1], qc_decode<2>(w4, s2, z2, p.sixteen), qc_decode<3>(w4, s2, z2, p.sixteen));
         }
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
@@ -276,10 +276,10 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
         const uint32_t sel = (quad & 1) ? 0x7632u : 0x5410u;
         const uint32_t a = quad < 2 ? __byte_perm(vc[0].x, vc[1].x, sel) : __byte_perm(vc[0].y, vc[1].y, sel);
         const uint32_t b = quad < 2 ? __byte_perm(vc[2].x, vc[3].x, sel) : __byte_perm(vc[2].y, vc[3].y, sel);
-        mma16816(o[4 * quad + 0], pr, qc_decode<0>(a, sa, za), qc_decode<0>(b, sb, zb));
-        mma16816(o[4 * quad + 1], pr, qc_decode<1>(a, sa, za), qc_decode<1>(b, sb, zb));
-        mma16816(o[4 * quad + 2], pr, qc_decode<2>(a, sa, za), qc_decode<2>(b, sb, zb));
-        mma16816(o[4 * quad + 3], pr, qc_decode<3>(a, sa, za), qc_decode<3>(b, sb, zb));
+        mma16816(o[4 * quad + 0], pr, qc_decode<0>(a, sa, za, p.sixteen), qc_decode<0>(b, sb, zb, p.sixteen));
+        mma16816(o[4 * quad + 1], pr, qc_decode<1>(a, sa, za, p.sixteen), qc_decode<1>(b, sb, zb, p.sixteen));
+        mma16816(o[4 * quad + 2], pr, qc_decode<2>(a, sa, za, p.sixteen), qc_decode<2>(b, sb, zb, p.sixteen));
+        mma16816(o[4 * quad + 3], pr, qc_decode<3>(a, sa, za, p.sixteen), qc_decode<3>(b, sb, zb, p.sixteen));
       }
       load_v(next);
     }

@@ -12,6 +12,7 @@
 // tiles, and a chain of reference maxima between them.
 //
 // Per CTA (persistent, one per SM, 20 warps):
+//   warp 0       asks for the codes of the tiles ahead in L2
 //   warp 1       S issuer and TMEM owner;  warp 2  P.V issuer
 //   warp 3       Q: 128 gathered rows by 16-byte asynchronous copies
 //   warps 4-11   softmax and epilogue (as in attn.cu)
@@ -43,7 +44,7 @@ constexpr int TL_THREADS = 640;
 constexpr int SOFTMAX_WARP0 = 4, DECODE_WARP0 = 12;
 constexpr int SOFTMAX_THREADS = 256, GROUP_THREADS = 128;
 constexpr int DECODE_WARPS = 4;  // of each kind
-constexpr int CTRL_REGS = 56, SOFTMAX_REGS = 120, DECODE_REGS = 88;
+constexpr int CTRL_REGS = 56, SOFTMAX_REGS = 136, DECODE_REGS = 72;
 constexpr int LAUNCH_REGS = 96;  // 65536 / 640, in eights
 static_assert(128 * CTRL_REGS + SOFTMAX_THREADS * SOFTMAX_REGS + 64 * DECODE_WARPS * DECODE_REGS <= TL_THREADS * LAUNCH_REGS,
               "register split exceeds the launch's registers");
@@ -59,17 +60,18 @@ constexpr int STAGE_BYTES = 1024;  // of O, per softmax warp: 32 rows x 16 eleme
 constexpr uint32_t K_AT = 2 * ATT_Q_TILE_BYTES, V_AT = K_AT + 2 * ATT_KV_STAGE_BYTES;
 constexpr uint32_t OUT_AT = V_AT + 2 * ATT_KV_STAGE_BYTES;
 constexpr uint32_t AUX_AT = OUT_AT + 8 * STAGE_BYTES;
-constexpr int NUM_BARS = 6 + 3 * S_BUFS + 8 + 8;
+constexpr int NUM_BARS = 6 + 3 * S_BUFS + 8 + 2;
 
 constexpr int LIST_NEAR = 64;  // of a CTA's items, kept in shared memory
 
 struct Aux {
   int4 list[3 * LIST_NEAR];
   uint64_t bars[NUM_BARS];
-  float xval[2 * 2 * ATT_BM];
+  float2 fin[2][2][ATT_BM];  // [item parity][group][row]: reference and sum of a finished item
   uint32_t chain[ATT_BM];
   int64_t red[QA_ROUNDS][TL_THREADS / 32];
   uint32_t tmem_slot, abort, n_tiles;
+  uint32_t decoded;  // key tile that the decode is at
 };
 constexpr uint32_t SMEM_USED = AUX_AT + sizeof(Aux);
 constexpr uint32_t SMEM_ALLOC = 227 * 1024;
@@ -79,7 +81,7 @@ static_assert(2 * sizeof(int32_t) * (SEG_MAX_USERS + 1) <= AUX_AT, "the users' p
 struct Smem {
   uint8_t *q, *k, *v, *out;
   uint64_t *q_full, *q_empty, *s_full, *p_full, *pv_done, *o_full, *o_empty, *k_full, *k_empty, *v_full,
-      *v_empty, *xbar;
+      *v_empty, *fin_full;
   Aux* x;
 };
 
@@ -102,7 +104,7 @@ __device__ __forceinline__ Smem carve(uint8_t* base) {
   s.k_empty = s.k_full + 2;
   s.v_full = s.k_empty + 2;
   s.v_empty = s.v_full + 2;
-  s.xbar = s.v_empty + 2;
+  s.fin_full = s.v_empty + 2;
   return s;
 }
 
@@ -120,8 +122,12 @@ __device__ __forceinline__ int4 ld_int4(const int4* p) {  // written by this CTA
   return r;
 }
 
-// This CTA's items: the first ones in shared memory, the others in list entries
-// b, b + grid, .. of CTA b.
+// This CTA's items: the first ones in shared memory, the others in the list.
+// Its place in the grid moves by one from each round of items to the next, so
+// that no CTA gets only the first tiles of pairs, or only the short second ones.
+__device__ __forceinline__ int64_t list_entry(int k) {
+  return static_cast<int64_t>(k) * gridDim.x + (blockIdx.x + static_cast<uint32_t>(k)) % gridDim.x;
+}
 struct List {
   const int4* near;
   const int4* far;
@@ -129,7 +135,7 @@ struct List {
 };
 __device__ __forceinline__ int4 item_part(const List& l, int k, int i) {
   if (k < LIST_NEAR) return l.near[3 * k + i];
-  return ld_int4(l.far + 3 * (static_cast<int64_t>(blockIdx.x) + static_cast<int64_t>(k) * gridDim.x) + i);
+  return ld_int4(l.far + 3 * list_entry(k) + i);
 }
 __device__ __forceinline__ int item_tiles(const List& l, int k) { return item_part(l, k, 1).w; }
 __device__ __forceinline__ Item load_item(const List& l, int k) {
@@ -157,11 +163,12 @@ __device__ int make_list(const QcAttnParams& p, int32_t* sm, Aux& x) {
       p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, item0, part0, x.red);
   if (it.items > p.max_items || it.slots > QA_MOST_SPLITS * static_cast<int64_t>(p.ctas)) return -1;
   bool ignored = false;
-  const int n_items = static_cast<int>(it.items), grid = static_cast<int>(gridDim.x), b = static_cast<int>(blockIdx.x);
-  const int count = n_items > b ? (n_items - b + grid - 1) / grid : 0;
+  const int n_items = static_cast<int>(it.items), grid = static_cast<int>(gridDim.x);
+  const int full = n_items / grid;
+  const int count = full + (list_entry(full) < n_items ? 1 : 0);
   int tiles = 0;
   for (int k = tid; k < count; k += TL_THREADS) {
-    const int i = b + k * grid;
+    const int i = static_cast<int>(list_entry(k));
     const int u = qc_find(item0, n, i);
     const QcUserWork w = user_work(p, u, most, ignored);
     const int ns = qc_splits(w.units, it.chunk);
@@ -225,8 +232,7 @@ struct Raw {
 // Four warps turn the keys' half tiles, four the values', so that one kind's
 // waits lie beside the other's work.  The codes come straight from global
 // memory into registers, a warp reading 512 contiguous bytes, and each chunk's
-// registers are loaded again (for the next tile) as soon as it is decoded; the
-// lines of the tiles after that are asked for in L2.  (Codes that passed
+// registers are loaded again (for the next tile) as soon as it is decoded.  (Codes that passed
 // through shared memory by bulk copies cost a producer warp over a thousand
 // cycles a tile to issue.)  A quarter warp's 16-byte stores (2 tokens x 4
 // groups) hit all banks because the second 64 elements' pieces lie two places
@@ -244,7 +250,7 @@ __device__ void decode_warps(const QcAttnParams& p, const Smem& s, const List& l
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     place[k] = (grp >> 1) * HALF_TILE + (((((grp & 1) * 4 + k) ^ (grp & 2)) ^ tok8) << 4);
-  const uint32_t tiles = s.x->n_tiles;
+  const uint32_t tiles = s.x->n_tiles, sixteen = p.sixteen;
   const int64_t page_bytes = (static_cast<int64_t>(p.H_kv) << p.blocks_log2) * QC_BLOCK_BYTES;
 
   Cursor c = {};
@@ -272,17 +278,6 @@ __device__ void decode_warps(const QcAttnParams& p, const Smem& s, const List& l
       const int page = __shfl_sync(0xffffffffu, c.page, ((c.t & 15) << 1) | b);
       src[b] = c.data + page * page_bytes + ((blk + b) & ((1 << p.blocks_log2) - 1)) * QC_BLOCK_BYTES;
     }
-    // the lines of the warp's blocks two tiles on (of this item)
-    if (c.t + 2 < c.nt) {
-      const int at = ((c.t & 15) + 2) * 2 + (lane >= 10);
-      const int page = __shfl_sync(0xffffffffu, c.page, at & 31);
-      if (lane < 20 && at < 32) {
-        const uint8_t* line = c.data + page * page_bytes +
-                              ((blk + 16 + (lane >= 10)) & ((1 << p.blocks_log2) - 1)) * QC_BLOCK_BYTES +
-                              (lane >= 10 ? lane - 10 : lane) * 128;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
-      }
-    }
     if (++c.t == c.nt) {
       ++c.k;
       cursor_item(p, l, c, half);
@@ -304,6 +299,7 @@ __device__ void decode_warps(const QcAttnParams& p, const Smem& s, const List& l
   for (uint32_t g = 0; g < tiles; ++g) {
     const int valid = left - tok8;  // > 8 i: the lane's token of chunk i exists
     if (g + 1 < tiles) point();
+    if (!values && dw == 0 && lane == 0) *const_cast<volatile uint32_t*>(&s.x->decoded) = g;
     if (!warp_wait(empty + (g & 1u), ((g >> 1) & 1u) ^ 1u, s, p)) return;
     uint8_t* dst = ring + (g & 1u) * ATT_KV_STAGE_BYTES;
 #pragma unroll
@@ -313,8 +309,8 @@ __device__ void decode_warps(const QcAttnParams& p, const Smem& s, const List& l
       const uint32_t w[4] = {raw.c[i].x, raw.c[i].y, raw.c[i].z, raw.c[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint4 o = make_uint4(qc_decode<0>(w[k], s2, z2), qc_decode<1>(w[k], s2, z2), qc_decode<2>(w[k], s2, z2),
-                                   qc_decode<3>(w[k], s2, z2));
+        const uint4 o = make_uint4(qc_decode<0>(w[k], s2, z2, sixteen), qc_decode<1>(w[k], s2, z2, sixteen),
+                                   qc_decode<2>(w[k], s2, z2, sixteen), qc_decode<3>(w[k], s2, z2, sixteen));
         *reinterpret_cast<uint4*>(dst + i * 1024 + place[k]) = o;
       }
       fetch(i);
@@ -322,6 +318,39 @@ __device__ void decode_warps(const QcAttnParams& p, const Smem& s, const List& l
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(full + (g & 1u));
+  }
+}
+
+// Asks for the codes of the tiles ahead in L2, four tiles at a time (a lane per
+// block of keys and values), as soon as they are AHEAD tiles past the one being
+// decoded; across items.
+constexpr uint32_t AHEAD = 3;
+
+__device__ void prefetcher(const QcAttnParams& p, const Smem& s, const List& l) {
+  const int lane = static_cast<int>(lane_id());
+  const int64_t page_bytes = (static_cast<int64_t>(p.H_kv) << p.blocks_log2) * QC_BLOCK_BYTES;
+  uint32_t g = 0;
+  Cursor c = {};
+#pragma unroll 1
+  for (cursor_item(p, l, c, 0); c.k < l.count; ++c.k, cursor_item(p, l, c, 0)) {
+#pragma unroll 1
+    for (int t = 0; t < c.nt; t += 4, g += 4) {
+      const int blk = (c.t0 + t) * 8 + lane;
+      const bool there = t + (lane >> 3) < c.nt && blk * QC_ROWS < c.len;
+      const int page = there ? __ldg(c.table + (blk >> p.blocks_log2)) : -1;
+      const uint64_t t_0 = globaltimer_ns();
+      // bounded like every wait here, though nothing depends on this warp
+      while (!__any_sync(0xffffffffu, g <= *const_cast<volatile uint32_t*>(&s.x->decoded) + AHEAD)) {
+        __nanosleep(200);
+        if (__any_sync(0xffffffffu, *const_cast<volatile uint32_t*>(&s.x->abort) || globaltimer_ns() - t_0 > p.timeout_ns)) return;
+      }
+      if (page >= 0 && page < p.n_pages) {
+        const uint8_t* block = c.data + page * page_bytes + (blk & ((1 << p.blocks_log2) - 1)) * QC_BLOCK_BYTES;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(block), "n"(QC_BLOCK_BYTES) : "memory");
+      }
+      __syncwarp();
+    }
+    g -= (4 - (c.nt & 3)) & 3;  // the last four were fewer
   }
 }
 
@@ -428,19 +457,7 @@ __device__ void pv_issuer(const QcAttnParams& p, const Smem& s, uint32_t tmem, c
 // ---------------------------------------------------- softmax and epilogue
 struct Lane {
   int quarter, half, r;  // half: the warp's group (its key tiles) and its d half of O
-  uint32_t xc;           // exchanges done with the partner warp
 };
-
-__device__ __forceinline__ bool pair_exchange(const QcAttnParams& p, const Smem& s, Lane& ln, float mine, float& theirs) {
-  const uint32_t buf = ln.xc & 1u;
-  s.x->xval[buf * 256 + ln.half * 128 + ln.r] = mine;
-  uint64_t* bar = &s.xbar[ln.quarter * 2 + buf];
-  mbar_arrive(bar);
-  if (!mbar_wait(bar, (ln.xc >> 1) & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
-  theirs = s.x->xval[buf * 256 + (ln.half ^ 1) * 128 + ln.r];
-  ++ln.xc;
-  return true;
-}
 
 // The chain of reference maxima through the tiles of both groups (attn.cu
 // describes it): the high 24 bits of the value, the tile's tag below.
@@ -488,9 +505,8 @@ __device__ __forceinline__ void mask_columns(uint32_t (&v)[32], int n) {
     if (j >= n) v[j] = __float_as_uint(-INFINITY);
 }
 
-// The running maximum of 32 columns' scores, of which n exist.
-__device__ __forceinline__ void row_max(uint32_t (&v)[32], int n, float& mx) {
-  if (n < 32) mask_columns(v, n);
+// The running maximum of 32 columns' scores.
+__device__ __forceinline__ void row_max(const uint32_t (&v)[32], float& mx) {
   float mx0 = mx, mx1 = -INFINITY;
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
@@ -515,39 +531,43 @@ __device__ __forceinline__ void row_exp(const uint32_t (&v)[32], float sl, float
   tmem_st16(to, pk);
 }
 
-struct RowOut {
-  bool pending;    // a finished item whose O has not been read out yet
-  bool rows_here;  // any of the warp's rows exists
-  int64_t row;     // this thread's row of O (in rows), or -1
-  float l, m;      // this group's row sum, its last reference (-inf: no tile)
-  int ns, slot, first, step;
+// A finished item whose O has not been read out yet: its place in the list
+// (-1: none), and what this thread read of it early.
+struct Done {
+  int k;
+  int cand;  // the candidate of this thread's row, if the row exists
 };
 
-// 16 columns (the c-th of four in the warp's 64) of the finished rows, scaled,
-// in element order, to global memory: through 1 KB of shared memory, so that
-// every store fills whole 32-byte sectors.  Column 8k + j holds element
-// 8 (k ^ 2 half) + (j >> 1) + 4 (j & 1) of the warp's half.
-__device__ __forceinline__ void store_columns(const QcAttnParams& p, uint8_t* stage, const Lane& ln, int64_t row, int c,
-                                              const float* o, float inv) {
-  const int lane = static_cast<int>(lane_id());
+// Packs 16 columns of finished rows, scaled, in element order: column 8k + j
+// holds element 8 (k ^ 2 half) + (j >> 1) + 4 (j & 1) of the warp's half.
+__device__ __forceinline__ void pack_columns(const float* o, float inv, uint32_t* w) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const float* e = o + 8 * k;
-    uint4 w;
-    w.x = pack_bf16x2(e[0] * inv, e[2] * inv);
-    w.y = pack_bf16x2(e[4] * inv, e[6] * inv);
-    w.z = pack_bf16x2(e[1] * inv, e[3] * inv);
-    w.w = pack_bf16x2(e[5] * inv, e[7] * inv);
-    *reinterpret_cast<uint4*>(stage + lane * 32 + ((k ^ ((lane >> 2) & 1)) << 4)) = w;
+    w[4 * k + 0] = pack_bf16x2(e[0] * inv, e[2] * inv);
+    w[4 * k + 1] = pack_bf16x2(e[4] * inv, e[6] * inv);
+    w[4 * k + 2] = pack_bf16x2(e[1] * inv, e[3] * inv);
+    w[4 * k + 3] = pack_bf16x2(e[5] * inv, e[7] * inv);
   }
+}
+
+// The c-th 16 packed columns of the warp's 64 to global memory: through 1 KB of
+// shared memory, so that every store fills whole 32-byte sectors.
+__device__ __forceinline__ void store_columns(const QcAttnParams& p, uint8_t* stage, const Lane& ln, int64_t row, int c,
+                                              const uint32_t* w) {
+  const int lane = static_cast<int>(lane_id());
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    *reinterpret_cast<uint4*>(stage + lane * 32 + ((k ^ ((lane >> 2) & 1)) << 4)) =
+        make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
   __syncwarp();
   const int piece = lane & 1;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = 16 * i + (lane >> 1);
     const int64_t at = __shfl_sync(0xffffffffu, row, r);
-    const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 32 + ((piece ^ ((r >> 2) & 1)) << 4));
-    if (at >= 0) reinterpret_cast<uint4*>(p.O + at * ATT_D + ln.half * 64)[(2 * c + piece) ^ (2 * ln.half)] = w;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 32 + ((piece ^ ((r >> 2) & 1)) << 4));
+    if (at >= 0) reinterpret_cast<uint4*>(p.O + at * ATT_D + ln.half * 64)[(2 * c + piece) ^ (2 * ln.half)] = v;
   }
   __syncwarp();
 }
@@ -559,8 +579,8 @@ __device__ __forceinline__ void store_lse(const QcAttnParams& p, int64_t row, fl
 
 // A split's piece of O (this warp's 32 rows x 64 columns) to its slot; the
 // warp that completes the tile's piece adds the splits in order and stores it.
-__device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, const RowOut& ro, const Lane& ln, float mf,
-                                            float l, uint8_t* stage, uint64_t* o_empty) {
+__device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, const Item& ro, int64_t row, const Lane& ln,
+                                            float mf, float l, uint8_t* stage, uint64_t* o_empty) {
   const int lane = static_cast<int>(lane_id());
   // slot: [half][64 columns][128 rows], then [half][m, l][128 rows]
   constexpr int64_t SLOT = TL_PART;
@@ -600,7 +620,7 @@ __device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, 
     L += (m == -INFINITY ? 0.f : ex2(m - M)) * __ldcg(first + k * stride + ml + ATT_BM);
   }
   const float inv = inverse(L);
-  if (p.lse && ro.row >= 0 && ln.half == 0) store_lse(p, ro.row, M, L);
+  if (p.lse && row >= 0 && ln.half == 0) store_lse(p, row, M, L);
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float acc[16];
@@ -617,188 +637,205 @@ __device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, 
 #pragma unroll
       for (int j = 0; j < 16; ++j) acc[j] = fmaf(x[j], f, acc[j]);
     }
-    store_columns(p, stage, ln, ro.row, c, acc, inv);
+    uint32_t w[8];
+    pack_columns(acc, inv, w);
+    store_columns(p, stage, ln, row, c, w);
   }
 }
 
-// An item's epilogue: the groups' row sums joined, O out of TMEM to global
-// memory (or through the partial rows of a split item).
-__device__ __forceinline__ bool epilogue(const QcAttnParams& p, const Smem& s, uint32_t Ot, const RowOut& ro, Lane& ln,
-                                         uint32_t& ou) {
-  if (!ro.rows_here) {  // both warps of the quarter skip
-    if (!mbar_wait(s.o_full, ou & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
-    ++ou;
+// An item's epilogue: the groups' row sums joined (both have posted theirs), O
+// out of TMEM to global memory (or through the partial rows of a split item).
+__device__ __forceinline__ bool epilogue(const QcAttnParams& p, const Smem& s, uint32_t Ot, const List& list, const Done& done,
+                                         const Lane& ln, uint32_t& ou) {
+  const Item x = load_item(list, done.k);
+  if (!mbar_wait(&s.fin_full[ou & 1u], (ou >> 1) & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
+  const float2 f0 = s.x->fin[ou & 1u][0][ln.r], f1 = s.x->fin[ou & 1u][1][ln.r];
+  if (!mbar_wait(s.o_full, ou & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
+  ++ou;
+  if (x.row0 + ln.quarter * 32 >= x.n_rows) {  // none of the warp's rows exists
     mbar_arrive(s.o_empty);
     return true;
   }
-  float mp, lp;
-  if (!pair_exchange(p, s, ln, ro.m, mp)) return false;
-  const float mf = fmaxf(ro.m, mp);
-  const float lm = ro.m == -INFINITY ? ro.l : ro.l * ex2(ro.m - mf);  // without a reference: 0, or NaN
-  if (!pair_exchange(p, s, ln, lm, lp)) return false;
-  const float l = lm + lp;
-  if (!mbar_wait(s.o_full, ou & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
-  ++ou;
+  const float mf = fmaxf(f0.x, f1.x);
+  // a group without a reference (no tile, or no score that is a number) has the sum 0, or NaN
+  const float l = (f0.x == -INFINITY ? f0.y : f0.y * ex2(f0.x - mf)) + (f1.x == -INFINITY ? f1.y : f1.y * ex2(f1.x - mf));
+  const int rows_per_cand = p.group * p.Lq, rr = x.row0 + ln.r;
+  const int64_t row = rr < x.n_rows
+      ? (static_cast<int64_t>(done.cand) * p.H + x.hk * p.group) * p.Lq + rr % rows_per_cand : -1;
   tc_fence_after();
   uint8_t* stage = s.out + (ln.quarter * 2 + ln.half) * STAGE_BYTES;
-  if (ro.ns > 1) {
-    join_splits(p, Ot, ro, ln, mf, l, stage, s.o_empty);
+  if (x.ns > 1) {
+    join_splits(p, Ot, x, row, ln, mf, l, stage, s.o_empty);
     return true;
   }
-  if (p.lse && ro.row >= 0 && ln.half == 0) store_lse(p, ro.row, mf, l);
   const float inv = inverse(l);
-#pragma unroll 1
+  uint32_t w[32];
+#pragma unroll
   for (int c = 0; c < 2; ++c) {
     uint32_t o[32];
     tmem_ld32(Ot + c * 32, o);
     tmem_ld_wait(o);
-    if (c == 1) {
-      tc_fence_before();
-      mbar_arrive(s.o_empty);
-    }
-    store_columns(p, stage, ln, ro.row, 2 * c, reinterpret_cast<const float*>(o), inv);
-    store_columns(p, stage, ln, ro.row, 2 * c + 1, reinterpret_cast<const float*>(o) + 16, inv);
+    pack_columns(reinterpret_cast<const float*>(o), inv, w + 16 * c);
+    pack_columns(reinterpret_cast<const float*>(o) + 16, inv, w + 16 * c + 8);
   }
+  tc_fence_before();
+  mbar_arrive(s.o_empty);
+  if (p.lse && row >= 0 && ln.half == 0) store_lse(p, row, mf, l);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) store_columns(p, stage, ln, row, c, w + 8 * c);
   return true;
 }
 
-__device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tmem, const List& l_) {
+__device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tmem, const List& list) {
   const int warp = threadIdx.x >> 5;
   Lane ln;
   ln.quarter = warp & 3;
   ln.half = (warp - SOFTMAX_WARP0) >> 2;
   ln.r = (ln.quarter << 5) + static_cast<int>(lane_id());
-  ln.xc = 0;
   const int grp = ln.half;
   const uint32_t lane_base = static_cast<uint32_t>(ln.quarter * 32) << 16;
   const uint32_t Oall = tmem + lane_base + TM_O;
   const uint32_t Ot = Oall + grp * 64;
   const float sl = p.scale_log2;
   const int rows_per_cand = p.group * p.Lq;
-  uint32_t g = 0, ou = 0;
-  RowOut prev = {};
+  uint32_t g0 = 0, ic = 0, ou = 0;  // tiles before the item, items finished, items read out
+  Done prev = {-1, 0};
 
-  for (int k = 0; k < l_.count; ++k) {
-    const Item x = load_item(l_, k);
-    const int rr = x.row0 + ln.r;
-    const int64_t row = rr < x.n_rows ? row_index(p, x, rr, rows_per_cand) : -1;
-    const bool rows_here = x.row0 + ln.quarter * 32 < x.n_rows;
-    if (x.nt == 0) {  // no tokens: O = 0, LSE = -inf
-      if (row >= 0) {
-        const uint4 z = make_uint4(0, 0, 0, 0);
+  // One turn more than there are items: the last one's epilogue.  The code of a
+  // tile and of an epilogue stands once each: with the SM's 20 warps at four
+  // kinds of work, what is copied into several places is fetched from behind the
+  // instruction cache again and again.
+  for (int k = 0; k <= list.count; ++k) {
+    int nt = 0, rem = 0, cand = 0;  // rem: tokens from the split's first on
+    bool rows_here = false;
+    if (k < list.count) {
+      const Item x = load_item(list, k);
+      const int rr = x.row0 + ln.r;
+      if (rr < x.n_rows) cand = __ldg(p.perm + x.seg + rr / rows_per_cand);
+      rows_here = x.row0 + ln.quarter * 32 < x.n_rows;
+      nt = x.nt;
+      rem = x.len - x.t0 * ATT_BN;
+      if (nt == 0) {  // no tokens: O = 0, LSE = -inf
+        if (rr < x.n_rows) {
+          const int64_t row = (static_cast<int64_t>(cand) * p.H + x.hk * p.group) * p.Lq + rr % rows_per_cand;
+          const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(p.O + row * ATT_D + grp * 64)[c] = z;
-        if (p.lse && grp == 0) p.lse[row] = -INFINITY;
-      }
-      continue;
-    }
-    bool epi = prev.pending;  // the previous item's epilogue is still to come
-    float mref = -INFINITY, l = 0.f;
-    const uint32_t g0 = g;
-    for (int jt = static_cast<int>((static_cast<uint32_t>(grp) - g0) & 1u); jt < x.nt; jt += 2) {
-      g = g0 + static_cast<uint32_t>(jt);
-      const uint32_t sb = g % S_BUFS;
-      const uint32_t St = tmem + lane_base + TM_S + sb * 128;
-      if (!mbar_wait(&s.s_full[sb], (g / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1)) return;
-      tc_fence_after();
-      if (!rows_here) {  // none of the warp's 32 rows exists: keep the hand-shakes in step, nothing else
-        float ignored;
-        if (!chain_wait(p, s, ln.r, g, ignored)) return;
-        chain_post(s, ln.r, g + 1, 0.f);
-        tc_fence_before();
-        mbar_arrive(&s.p_full[sb]);
-        if (epi && !epilogue(p, s, Ot, prev, ln, ou)) return;
-        epi = false;
+          for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(p.O + row * ATT_D + grp * 64)[c] = z;
+          if (p.lse && grp == 0) p.lse[row] = -INFINITY;
+        }
         continue;
       }
-      // two passes over the row, 32 columns at a time with the next ones on
-      // their way from TMEM (whole rows in registers, unrolled, are too much for
-      // the instruction cache that the SM's 20 warps share); the first pass goes
-      // down so that the second begins with what it ended on
-      const int ncols = min(ATT_BN, x.len - (x.t0 + jt) * ATT_BN);
-      uint32_t va[32], vb[32];
-      float mx = -INFINITY;
-      tmem_ld32p(St + 96, va);
-      tmem_ld_wait();
-      reg_fence32(va);
-      tmem_ld32p(St + 64, vb);
-      row_max(va, ncols - 96, mx);
-      tmem_ld_wait();
-      reg_fence32(vb);
-      tmem_ld32p(St + 32, va);
-      row_max(vb, ncols - 64, mx);
-      tmem_ld_wait();
-      reg_fence32(va);
-      tmem_ld32p(St, vb);
-      row_max(va, ncols - 32, mx);
-      tmem_ld_wait();
-      reg_fence32(vb);
-      row_max(vb, ncols, mx);
-      mx *= sl;
-      const uint32_t cw = chain_load(s, ln.r);
-      float mprev = __uint_as_float(cw & 0xFFFFFF00u);
-      if (!__all_sync(0xffffffffu, (cw & 0xFFu) == (g & 0xFFu)) && !chain_wait(p, s, ln.r, g, mprev)) return;
-      if (jt == 0) mprev = -INFINITY;
-      const bool rescale = __any_sync(0xffffffffu, mx > mprev + RESCALE_THRESHOLD);
-      const float mj = rescale ? chain_value(fmaxf(mprev, mx)) : mprev;
-      chain_post(s, ln.r, g + 1, mj);
-      if (mj != mref) {
-        l *= ex2(mref - mj);
-        mref = mj;
-      }
-      float l0 = 0.f, l1 = 0.f;
-      // P takes the place of the scores already read
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        tmem_ld32p(St + 64 * h + 32, va);
-        row_exp(vb, sl, mj, l0, l1, St + 32 * h);
-        tmem_ld_wait();
-        reg_fence32(va);
-        if (h == 0) tmem_ld32p(St + 64, vb);
-        if (ncols < 64 * h + 64) mask_columns(va, ncols - 64 * h - 32);
-        row_exp(va, sl, mj, l0, l1, St + 32 * h + 16);
-        tmem_ld_wait();
-        reg_fence32(vb);
-        if (ncols < 96) mask_columns(vb, ncols - 64);
-      }
-      l += l0 + l1;
-      if (rescale && jt > 0) {
-        // O must hold only this item's P.V: the previous item's is read out first
-        if (epi && !epilogue(p, s, Ot, prev, ln, ou)) return;
-        epi = false;
-        const uint32_t gp = g - 1;
-        if (!mbar_wait(&s.pv_done[gp % S_BUFS], (gp / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1)) return;
+    }
+    bool epi = prev.k >= 0;  // the previous item's epilogue is still to come
+    float mref = -INFINITY, l = 0.f;
+    int jt = static_cast<int>((static_cast<uint32_t>(grp) - g0) & 1u);
+    do {
+      const uint32_t g = g0 + static_cast<uint32_t>(jt), sb = g % S_BUFS;
+      float mprev = 0.f, mj = 0.f;
+      bool rescale = false;
+      if (jt < nt) {
+        const uint32_t St = tmem + lane_base + TM_S + sb * 128;
+        if (!mbar_wait(&s.s_full[sb], (g / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1)) return;
         tc_fence_after();
-        const float alpha = ex2(mprev - mj);
+        if (!rows_here) {  // none of the warp's 32 rows exists: keep the hand-shakes in step, nothing else
+          if (!chain_wait(p, s, ln.r, g, mprev)) return;
+          chain_post(s, ln.r, g + 1, 0.f);
+        } else {
+          // two passes over the row, 32 columns at a time with the next ones on
+          // their way from TMEM (whole rows in registers, unrolled, are too much for
+          // the instruction cache); the first pass goes down so that the second
+          // begins with what it ended on
+          const int ncols = min(ATT_BN, rem - jt * ATT_BN);
+          uint32_t va[32], vb[32];
+          if (ncols < ATT_BN) {  // a history's last tile: scores behind its end become -inf where they lie
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32(Oall + c * 32, o);
-          tmem_ld_wait(o);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-          tmem_st32(Oall + c * 32, o);
+            for (int c = ncols >> 5; c < 4; ++c) {
+              tmem_ld32p(St + 32 * c, va);
+              tmem_ld_wait();
+              reg_fence32(va);
+              mask_columns(va, ncols - 32 * c);
+              tmem_st32(St + 32 * c, va);
+            }
+            tmem_st_wait();
+          }
+          float mx = -INFINITY;
+          tmem_ld32p(St + 96, va);
+          tmem_ld_wait();
+          reg_fence32(va);
+#pragma unroll 1
+          for (int h = 1; h >= 0; --h) {
+            tmem_ld32p(St + 64 * h, vb);
+            row_max(va, mx);
+            tmem_ld_wait();
+            reg_fence32(vb);
+            tmem_ld32p(St + 32, va);  // (the second time of no use)
+            row_max(vb, mx);
+            tmem_ld_wait();
+            reg_fence32(va);
+          }
+          mx *= sl;
+          const uint32_t cw = chain_load(s, ln.r);
+          mprev = __uint_as_float(cw & 0xFFFFFF00u);
+          if (!__all_sync(0xffffffffu, (cw & 0xFFu) == (g & 0xFFu)) && !chain_wait(p, s, ln.r, g, mprev)) return;
+          if (jt == 0) mprev = -INFINITY;
+          rescale = __any_sync(0xffffffffu, mx > mprev + RESCALE_THRESHOLD);
+          mj = rescale ? chain_value(fmaxf(mprev, mx)) : mprev;
+          chain_post(s, ln.r, g + 1, mj);
+          if (mj != mref) {
+            l *= ex2(mref - mj);
+            mref = mj;
+          }
+          float l0 = 0.f, l1 = 0.f;
+          // P takes the place of the scores already read
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld32p(St + 64 * h + 32, va);
+            row_exp(vb, sl, mj, l0, l1, St + 32 * h);
+            tmem_ld_wait();
+            reg_fence32(va);
+            if (h == 0) tmem_ld32p(St + 64, vb);
+            row_exp(va, sl, mj, l0, l1, St + 32 * h + 16);
+            tmem_ld_wait();
+            reg_fence32(vb);
+          }
+          l += l0 + l1;
         }
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&s.p_full[sb]);
-      if (epi && !epilogue(p, s, Ot, prev, ln, ou)) return;  // after the group's first tile of the next item
+      // Between the group's first tile of this item and that tile's P.V, which
+      // waits for O anyway.
+      if (epi && !epilogue(p, s, Ot, list, prev, ln, ou)) return;
       epi = false;
+      if (jt < nt) {
+        if (rescale && jt > 0) {
+          const uint32_t gp = g - 1;
+          if (!mbar_wait(&s.pv_done[gp % S_BUFS], (gp / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1)) return;
+          tc_fence_after();
+          const float alpha = ex2(mprev - mj);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(Oall + c * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st32(Oall + c * 32, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&s.p_full[sb]);
+      }
+      jt += 2;
+    } while (jt < nt);
+    if (k < list.count) {
+      g0 += static_cast<uint32_t>(nt);
+      prev.k = k;
+      prev.cand = cand;
+      s.x->fin[ic & 1u][grp][ln.r] = make_float2(mref, l);
+      mbar_arrive(&s.fin_full[ic & 1u]);
+      ++ic;
     }
-    g = g0 + static_cast<uint32_t>(x.nt);
-    if (epi && !epilogue(p, s, Ot, prev, ln, ou)) return;
-    prev.pending = true;
-    prev.row = row;
-    prev.rows_here = rows_here;
-    prev.l = l;
-    prev.m = mref;
-    prev.ns = x.ns;
-    prev.slot = x.slot;
-    prev.first = x.first;
-    prev.step = x.step;
   }
-  if (prev.pending) epilogue(p, s, Ot, prev, ln, ou);
 }
 
 __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnParams p) {
@@ -818,6 +855,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
       mbar_init(&s.pv_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.fin_full[i], SOFTMAX_THREADS);
       mbar_init(&s.q_full[i], 1);
       mbar_init(&s.q_empty[i], 1);
       mbar_init(&s.k_full[i], DECODE_WARPS);
@@ -827,10 +865,10 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
     }
     mbar_init(s.o_full, 1);
     mbar_init(s.o_empty, SOFTMAX_THREADS);
-    for (int i = 0; i < 8; ++i) mbar_init(&s.xbar[i], 64);
     for (int r = 0; r < ATT_BM; ++r) s.x->chain[r] = 0;
     s.x->abort = 0;
     s.x->n_tiles = 0;
+    s.x->decoded = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -854,7 +892,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
 
   if (warp < SOFTMAX_WARP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
-    if (warp == 1) s_issuer(p, s, tmem, l);
+    if (warp == 0) prefetcher(p, s, l);
+    else if (warp == 1) s_issuer(p, s, tmem, l);
     else if (warp == 2) pv_issuer(p, s, tmem, l);
     else if (warp == 3) q_loader(p, s, l);
   } else if (warp < DECODE_WARP0) {

@@ -403,6 +403,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   ap.list = p->d_qa_list;
   ap.max_items = items;
   ap.scale_log2 = scale * 1.4426950408889634f;
+  ap.sixteen = QC_SIXTEEN;
   ap.timeout_ns = p->timeout_ns;
   if ((few ? launch_qattn(ap, stream) : launch_qattn_tile(ap, stream)) != cudaSuccess)
     return IKBO_ERR_CUDA;

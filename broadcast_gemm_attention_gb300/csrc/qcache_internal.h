@@ -97,6 +97,7 @@ struct QcAttnParams {
   int n_pages, max_blocks, blocks_log2;
   int ctas;                // of the launch
   float scale_log2;
+  uint32_t sixteen;        // QC_SIXTEEN
   uint64_t timeout_ns;
 };
 
@@ -293,14 +294,18 @@ __device__ __forceinline__ QcItems qc_items(const QcAttnParams& p, const Work& w
 
 // Two bf16 values from nibbles at bits SHIFT .. of each half of w:
 // z + (16 + c) s in one rounding.  The nibble lands in the top four mantissa
-// bits of 16.0, which makes the operand 16 + c exactly.
+// bits of 16.0, which makes the operand 16 + c exactly.  sixteen: QC_SIXTEEN, by
+// way of the launch's parameters: of two constants that it can see the compiler
+// makes two instructions (an AND and an OR take one, with one constant in a
+// register), a quarter of the tile kernel's integer work.
+constexpr uint32_t QC_SIXTEEN = 0x41804180u;
 template <int kNibble>
-__device__ __forceinline__ uint32_t qc_decode(uint32_t w, uint32_t s2, uint32_t z2) {
+__device__ __forceinline__ uint32_t qc_decode(uint32_t w, uint32_t s2, uint32_t z2, uint32_t sixteen = QC_SIXTEEN) {
   constexpr int kShift = 3 - 4 * kNibble;
   uint32_t c;
   if (kShift >= 0) c = w << (kShift >= 0 ? kShift : 0);
   else c = w >> (kShift < 0 ? -kShift : 0);
-  c = (c & 0x00780078u) | 0x41804180u;
+  c = (c & 0x00780078u) | sixteen;
   uint32_t r;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(s2), "r"(z2));
   return r;
