@@ -56,7 +56,7 @@ struct QtShared {
   float m[QT_WARPS][QT_ROWS];
   float l[QT_WARPS][QT_ROWS];
   float le[QT_WARPS][QT_ROWS];
-  int64_t red[QA_ROUNDS][QT_WARPS];
+  QcItemsShared items;
   uint32_t last;
 };
 
@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
   const int64_t most = (static_cast<int64_t>(p.max_blocks) << p.blocks_log2) * QC_ROWS;
 
   const QcItems it = qc_items<QT_THREADS, QT_MIN_BLOCKS, QT_ITEM_BLOCKS, QT_JOIN_BLOCKS>(
-      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, item0, part0, s.red);
-  if (it.items > 0x7fffffff || it.slots > QA_MOST_SPLITS * static_cast<int64_t>(p.ctas)) {  // cannot be: see the host's checks
+      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, item0, part0, s.items);
+  if (it.items > 0x7fffffffu || it.slots > static_cast<uint32_t>(QA_MOST_SPLITS * p.ctas)) {  // cannot be: see the host's checks
     if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, DEV_ERR_BAD_WORK);
     return;
   }

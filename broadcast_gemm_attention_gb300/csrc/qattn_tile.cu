@@ -69,7 +69,7 @@ struct Aux {
   uint64_t bars[NUM_BARS];
   float2 fin[2][2][ATT_BM];  // [item parity][group][row]: reference and sum of a finished item
   uint32_t chain[ATT_BM];
-  int64_t red[QA_ROUNDS][TL_THREADS / 32];
+  QcItemsShared items;
   uint32_t tmem_slot, abort, n_tiles;
   uint32_t decoded;  // key tile that the decode is at
 };
@@ -160,8 +160,8 @@ __device__ int make_list(const QcAttnParams& p, int32_t* sm, Aux& x) {
   int32_t* part0 = sm + n;
   const int64_t most = (static_cast<int64_t>(p.max_blocks) << p.blocks_log2) * QC_ROWS;
   const QcItems it = qc_items<TL_THREADS, TL_MIN_TILES, TL_ITEM_TILES, TL_JOIN_TILES>(
-      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, item0, part0, x.red);
-  if (it.items > p.max_items || it.slots > QA_MOST_SPLITS * static_cast<int64_t>(p.ctas)) return -1;
+      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, item0, part0, x.items);
+  if (it.items > p.max_items || it.slots > static_cast<uint32_t>(QA_MOST_SPLITS * p.ctas)) return -1;
   bool ignored = false;
   const int n_items = static_cast<int>(it.items), grid = static_cast<int>(gridDim.x);
   const int full = n_items / grid;
@@ -172,10 +172,9 @@ __device__ int make_list(const QcAttnParams& p, int32_t* sm, Aux& x) {
     const int u = qc_find(item0, n, i);
     const QcUserWork w = user_work(p, u, most, ignored);
     const int ns = qc_splits(w.units, it.chunk);
-    int local = i - item0[u];
-    const int tile = local % w.tiles;
-    local /= w.tiles;
-    const int split = local % ns, hk = local / ns;
+    const uint32_t local = static_cast<uint32_t>(i - item0[u]), other = local / static_cast<uint32_t>(w.tiles);
+    const int tile = static_cast<int>(local) - static_cast<int>(other) * w.tiles;
+    const int hk = static_cast<int>(other / static_cast<uint32_t>(ns)), split = static_cast<int>(other) - hk * ns;
     const int t0 = qc_split_start(w.units, ns, split);
     const int t1 = qc_split_start(w.units, ns, split + 1);
     const int first = part0[u] + hk * ns * w.tiles + tile;

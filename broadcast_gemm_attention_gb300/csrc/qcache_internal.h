@@ -124,9 +124,13 @@ __device__ __forceinline__ int qc_find(const int32_t* base, int n, int x) {
   return lo;
 }
 
-// Splits of a history of `units` (blocks or key tiles) into at most `chunk` each.
+// Splits of a history of `units` (blocks or key tiles) into about `chunk` each:
+// the quotient rounded up, in fp32 and so that an error of its last bits adds
+// no split (a split may be 1/100000 longer than `chunk`).  The same in every
+// place that asks.
 __device__ __forceinline__ int qc_splits(int units, int chunk) {
-  return units <= chunk ? 1 : (units + chunk - 1) / chunk;
+  const float q = __fmul_rn(__fdividef(static_cast<float>(units), static_cast<float>(chunk)), 0.99999f);
+  return units <= chunk ? 1 : static_cast<int>(ceilf(q));
 }
 
 // First unit of split i of n of `units` (the first units % n are one longer).
@@ -135,161 +139,161 @@ __device__ __forceinline__ int qc_split_start(int units, int n, int i) {
   return q * i + min(i, rest);
 }
 
-// Sums (scan: exclusive prefixes) of N values over the CTA's threads, or with
-// `warp` over each warp's lanes, where every warp holds the same values.
-// red: [N][the CTA's warps].
-template <int N, int kThreads>
-__device__ __forceinline__ void qc_sum(int64_t (&v)[N], int64_t (*red)[kThreads / 32], bool warp) {
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (!warp && (threadIdx.x & 31) == 0) red[k][threadIdx.x >> 5] = v[k];
-  }
-  if (warp) return;
+// Sums over the CTA's threads, or with `warp` over one warp that is alone here;
+// red: a word per warp.
+template <int kThreads>
+__device__ __forceinline__ uint32_t qc_sum(uint32_t v, uint32_t* red, bool warp) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  if (warp) return v;
+  const int lane = threadIdx.x & 31;
+  __syncthreads();  // red has been read
+  if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    v[k] = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) v[k] += red[k][w];
-  }
-  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? red[lane] : 0u);
 }
 
-template <int N, int kThreads>
-__device__ __forceinline__ void qc_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t (*red)[kThreads / 32], bool warp) {
-  const int lane = threadIdx.x & 31, w0 = threadIdx.x >> 5;
-  int64_t incl[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    incl[k] = v[k];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl[k], o);
-      if (lane >= o) incl[k] += y;
-    }
-    if (!warp && lane == 31) red[k][w0] = incl[k];
-    total[k] = __shfl_sync(0xffffffffu, incl[k], 31);
-    v[k] = incl[k] - v[k];
+__device__ __forceinline__ float qc_warp_sum(float v) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Exclusive prefixes of a warp's lanes.
+__device__ __forceinline__ uint32_t qc_warp_scan(uint32_t v) {
+  uint32_t x = v;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (static_cast<int>(threadIdx.x & 31) >= o) x += y;
   }
-  if (warp) return;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    total[k] = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      v[k] += w < w0 ? red[k][w] : 0;
-      total[k] += red[k][w];
-    }
-  }
-  __syncthreads();
+  return x - v;
 }
 
 // The list of items that every CTA of an attention launch works out for
 // itself: item0[u], part0[u] = items and partial slots before user u; an item
 // is (user, K/V head, split, tile) in that order, slots only where a history
 // has several splits.  work(u, bad) gives a user's tiles per head, units
-// (blocks or key tiles) and length.  With up to 32 users every warp does it by
-// itself.  Lengths of a split are compared by the CTAs' largest share: its
+// (blocks or key tiles) and length.  With up to 32 users one warp does it
+// alone.  Lengths of a split are compared by the CTAs' largest share: its
 // items' units, kItem beside each and kJoin for each split of a tile.
+//
+// A CTA runs this once, from instructions that no cache holds yet (a small
+// launch spends more time here than on its products), so it is written for few
+// instructions: loops stay loops, 32-bit and fp32 numbers, no integer division.
+// (All items and tiles fit in 31 bits: checked on the host.)
 struct QcUserWork {
   int tiles, units, len;
 };
 struct QcItems {
-  int64_t items, slots;
+  uint32_t items, slots;
   int chunk;  // units of a split, at most
+};
+struct QcItemsShared {
+  uint32_t red[32];
+  QcItems it;
 };
 
 template <int kThreads, int kMin, int kItem, int kJoin, typename Work>
 __device__ __forceinline__ QcItems qc_items(const QcAttnParams& p, const Work& work, int32_t* item0, int32_t* part0,
-                                            int64_t (*red)[kThreads / 32]) {
+                                            QcItemsShared& sh) {
+  static_assert(kThreads <= 1024, "a word of red per warp");
   const int n = p.n_users;
   const bool few = n <= 32;
-  const int me = few ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
-  const int per = few ? 1 : (n + kThreads - 1) / kThreads;
-  const int lo = min(me * per, n), hi = min(lo + per, n);
-  bool bad = false, ignored = false;
-  QcUserWork one = {};  // this thread's user where it has only one
-  if (per == 1 && lo < n) one = work(lo, bad);
-  const auto get = [&](int u) { return per == 1 ? one : work(u, ignored); };
-  int64_t sums[3] = {0, 0, 0};
-  int longest = 0;
-  for (int u = lo; u < hi; ++u) {
-    const QcUserWork w = per == 1 ? one : work(u, bad);
-    sums[0] += static_cast<int64_t>(w.tiles) * w.units;
-    sums[1] += w.len;
-    sums[2] += w.tiles;
-    if (w.tiles > 0) longest = max(longest, w.units);
-  }
-  qc_sum<3, kThreads>(sums, red, few);
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (!few) {
-    if ((threadIdx.x & 31) == 0) red[0][threadIdx.x >> 5] = longest;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) longest = max(longest, static_cast<int>(red[0][w]));
-    __syncthreads();
-  }
-  if (sums[1] > p.bound) bad = true;
-  if (bad && blockIdx.x == 0) atomicOr(p.status, DEV_ERR_CACHE);
-  // r CTAs' worth of items: a tile's splits are rounded up, hence the tiles
-  // taken off; too few to split anything: one item per tile
-  // (fp32 quotients, rounded up by more than their error: 64-bit divisions are
-  // the slowest part of a small launch)
-  const int64_t work_all = sums[0] * p.H_kv, tiles_all = sums[2] * p.H_kv;
-  int chunks[QA_ROUNDS];
-  int64_t counts[QA_ROUNDS];
-#pragma unroll
-  for (int r = 0; r < QA_ROUNDS; ++r) {
-    const int64_t room = (static_cast<int64_t>(p.ctas) << r) - tiles_all;
-    const float c = static_cast<float>(work_all) / static_cast<float>(room) * 1.00001f + 1.f;
-    chunks[r] = room > 0 ? max(static_cast<int>(fminf(c, 1e8f)), kMin) : max(longest, 1);
-    counts[r] = 0;
-  }
-  for (int u = lo; u < hi; ++u) {
-    const QcUserWork w = get(u);
-#pragma unroll
-    for (int r = 0; r < QA_ROUNDS; ++r) counts[r] += static_cast<int64_t>(w.tiles) * qc_splits(w.units, chunks[r]);
-  }
-  qc_sum<QA_ROUNDS, kThreads>(counts, red, few);
-  QcItems it;
-  it.chunk = chunks[0];
-  float best = 0.f;
-#pragma unroll
-  for (int r = 0; r < QA_ROUNDS; ++r) {
-    const int ns = qc_splits(longest, chunks[r]);
-    const float share = ceilf(static_cast<float>(counts[r] * p.H_kv) / static_cast<float>(p.ctas)) *
-                            static_cast<float>((longest + ns - 1) / ns + kItem) +
-                        (ns > 1 ? static_cast<float>(ns * kJoin) : 0.f);
-    if (r == 0 || share < best) {
-      best = share;
-      it.chunk = chunks[r];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  if (!few || warp == 0) {
+    const int per = few ? 1 : (n + kThreads - 1) / kThreads;
+    const int lo = min(tid * per, n), hi = min(lo + per, n);
+    bool bad = false, ignored = false;
+    QcUserWork one = {};  // this thread's user where it has only one
+    if (per == 1 && lo < n) one = work(lo, bad);
+    const auto get = [&](int u) { return per == 1 ? one : work(u, ignored); };
+    float sum = 0.f;  // of tiles x units: a bound with a margin for its rounding is made of it
+    int64_t lens = 0;
+    uint32_t tiles = 0;
+    int longest = 0;
+    for (int u = lo; u < hi; ++u) {
+      const QcUserWork w = per == 1 ? one : work(u, bad);
+      sum += static_cast<float>(w.tiles) * static_cast<float>(w.units);
+      lens += w.len;
+      tiles += static_cast<uint32_t>(w.tiles);
+      if (w.tiles > 0) longest = max(longest, w.units);
     }
-  }
-  int64_t v[2] = {0, 0}, total[2];
-  for (int u = lo; u < hi; ++u) {
-    const QcUserWork w = get(u);
-    const int ns = qc_splits(w.units, it.chunk);
-    const int64_t items = static_cast<int64_t>(w.tiles) * p.H_kv * ns;
-    v[0] += items;
-    v[1] += ns > 1 ? items : 0;
-  }
-  qc_scan<2, kThreads>(v, total, red, few);
-  for (int u = lo; u < hi; ++u) {
-    const QcUserWork w = get(u);
-    const int ns = qc_splits(w.units, it.chunk);
-    const int64_t items = static_cast<int64_t>(w.tiles) * p.H_kv * ns;
-    item0[u] = static_cast<int32_t>(v[0]);
-    part0[u] = static_cast<int32_t>(v[1]);
-    v[0] += items;
-    v[1] += ns > 1 ? items : 0;
+    sum = qc_warp_sum(sum);
+    longest = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(longest)));
+    if (!few) {
+      if (lane == 0) {
+        sh.red[warp] = __float_as_uint(sum);
+        item0[warp] = longest;  // (there are more users than warps)
+      }
+      __syncthreads();
+      sum = qc_warp_sum(lane < kThreads / 32 ? __uint_as_float(sh.red[lane]) : 0.f);
+      longest = static_cast<int>(__reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? static_cast<unsigned>(item0[lane]) : 0u));
+    }
+    tiles = qc_sum<kThreads>(tiles, sh.red, few);
+    // 24 bits and the rest: neither sum leaves 32 bits
+    const uint32_t l0 = qc_sum<kThreads>(static_cast<uint32_t>(lens & 0xFFFFFF), sh.red, few);
+    const uint32_t l1 = qc_sum<kThreads>(static_cast<uint32_t>(lens >> 24), sh.red, few);
+    if ((static_cast<int64_t>(l1) << 24) + l0 > p.bound) bad = true;
+    if (bad && blockIdx.x == 0) atomicOr(p.status, DEV_ERR_CACHE);
+    // r: 2^r items per CTA aimed at (a tile's splits are rounded up, hence the
+    // tiles taken off); too few to split anything: one item per tile
+    const float work_all = sum * static_cast<float>(p.H_kv) * 1.0001f;
+    const int64_t tiles_all = static_cast<int64_t>(tiles) * p.H_kv;
+    QcItems it = {0, 0, 1};
+    float best = 0.f;
+#pragma unroll 1
+    for (int r = 0; r < QA_ROUNDS; ++r) {
+      const int64_t room = (static_cast<int64_t>(p.ctas) << r) - tiles_all;
+      int chunk = max(longest, 1);
+      if (room > 0) chunk = max(static_cast<int>(fminf(__fdividef(work_all, static_cast<float>(room)) + 1.f, 1e8f)), kMin);
+      uint32_t count = 0;
+      for (int u = lo; u < hi; ++u) {
+        const QcUserWork w = get(u);
+        count += static_cast<uint32_t>(w.tiles * qc_splits(w.units, chunk));
+      }
+      count = qc_sum<kThreads>(count, sh.red, few) * static_cast<uint32_t>(p.H_kv);
+      const int ns = qc_splits(longest, chunk);
+      const float share = ceilf(static_cast<float>(count) / static_cast<float>(p.ctas)) *
+                              (ceilf(__fdividef(static_cast<float>(longest), static_cast<float>(ns))) + kItem) +
+                          (ns > 1 ? static_cast<float>(ns * kJoin) : 0.f);
+      if (r == 0 || share < best) {
+        best = share;
+        it.chunk = chunk;
+      }
+      if (room > 0 && chunk == kMin) break;  // shorter splits there are not
+    }
+    uint32_t items = 0, slots = 0;
+    for (int u = lo; u < hi; ++u) {
+      const QcUserWork w = get(u);
+      const int ns = qc_splits(w.units, it.chunk);
+      const uint32_t k = static_cast<uint32_t>(w.tiles) * static_cast<uint32_t>(p.H_kv * ns);
+      items += k;
+      slots += ns > 1 ? k : 0u;
+    }
+    uint32_t v0 = qc_warp_scan(items), v1 = qc_warp_scan(slots);
+    it.items = qc_sum<kThreads>(items, sh.red, few);
+    if (!few) {  // red holds the warps' sums
+      uint32_t before = qc_warp_scan(lane < kThreads / 32 ? sh.red[lane] : 0u);
+      v0 += __shfl_sync(0xffffffffu, before, warp);
+      it.slots = qc_sum<kThreads>(slots, sh.red, few);
+      before = qc_warp_scan(lane < kThreads / 32 ? sh.red[lane] : 0u);
+      v1 += __shfl_sync(0xffffffffu, before, warp);
+    } else {
+      it.slots = qc_sum<kThreads>(slots, sh.red, few);
+    }
+    for (int u = lo; u < hi; ++u) {
+      const QcUserWork w = get(u);
+      const int ns = qc_splits(w.units, it.chunk);
+      const uint32_t k = static_cast<uint32_t>(w.tiles) * static_cast<uint32_t>(p.H_kv * ns);
+      item0[u] = static_cast<int32_t>(v0);
+      part0[u] = static_cast<int32_t>(v1);
+      v0 += k;
+      v1 += ns > 1 ? k : 0u;
+    }
+    if (tid == 0) sh.it = it;
   }
   __syncthreads();
-  it.items = total[0];
-  it.slots = total[1];
-  return it;
+  return sh.it;
 }
 
 // Two bf16 values from nibbles at bits SHIFT .. of each half of w:

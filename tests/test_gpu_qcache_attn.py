@@ -322,3 +322,32 @@ def test_a_run_of_requests():
             Oj = torch.empty_like(q)
             p.attn_forward(q, Kj, Vj, offs, Oj)
             check(Oj, None, q.float().cpu().numpy(), host, m, H)
+
+
+@pytest.mark.parametrize("variant,users,H,most", [
+    ("registers", 33, 2, 90), ("registers", 150, 1, 90), ("registers", 700, 2, 60), ("registers", 2000, 1, 40),
+    ("tiles", 33, 2, 90), ("tiles", 150, 1, 200), ("tiles", 700, 1, 60), ("tiles", 1300, 8, 20),
+    ("decoded", 33, 1, 300), ("decoded", 400, 1, 40)])
+def test_many_users(variant, users, H, most):
+    """More users than a warp, a CTA's threads or a list in shared memory hold (1300 x 8 heads: over
+    64 items for each CTA), one long history among short and empty ones, users without candidates."""
+    c, Lq = {"registers": (1, 16), "tiles": (2, 24), "decoded": (5, 128)}[variant]
+    rng = np.random.default_rng(users)
+    lens = rng.integers(0, most, users)
+    lens[[1, users - 1]] = 0, 1
+    lens[users // 2] = 3000
+    st = R.Store(users, lens.tolist(), H, 16)
+    m = np.repeat(np.arange(users), c)
+    m[rng.random(m.size) < 0.1] = users // 2  # some users without candidates, one with more
+    m = rng.permutation(m).astype(np.int32)
+    Q = np.tile(queries(4, 50, H, Lq), (-(-m.size // 50), 1, 1, 1))[:m.size]
+    with B.Plan(m.size, users, H) as p:
+        p.plan(i32(m), users, H, Lq)
+        O, lse = attend(p, Q, st, Lkv=8_000_000 if variant == "tiles" else int(lens.sum()))
+        assert p.status() == B.IKBO_OK
+        O2, _ = attend(p, Q, st, lse=False, Lkv=8_000_000 if variant == "tiles" else int(lens.sum()))
+        assert torch.equal(O, O2)
+        assert not bool(torch.isnan(O).any())
+        some = np.flatnonzero((m % max(1, users // 30) == 0) | (m == users - 1) | (m == 1))
+        some = np.concatenate([some, np.flatnonzero(m == users // 2)[:5]])
+        check(O[some], lse[some], Q[some], st.kv, m[some], H)
