@@ -42,8 +42,7 @@ namespace {
 constexpr int QT_WARPS = 4;
 constexpr int QT_THREADS = 32 * QT_WARPS;
 constexpr int QT_MIN_BLOCKS = 4 * QT_WARPS;  // blocks of a split, at least
-constexpr int QT_ITEM_BLOCKS = 48;           // what an item costs beside its blocks, in blocks
-constexpr int QT_JOIN_BLOCKS = 1;            // and each split of a tile
+constexpr int QT_ITEM_BLOCKS = 24;           // what an item costs beside its blocks, in blocks
 constexpr float QT_THRESHOLD = 8.0f;         // log2 units
 constexpr int QT_EXTRA = 3;                  // per row besides O: reference, sum, sum of the log-sum-exp
 
@@ -56,7 +55,7 @@ struct QtShared {
   float m[QT_WARPS][QT_ROWS];
   float l[QT_WARPS][QT_ROWS];
   float le[QT_WARPS][QT_ROWS];
-  QcItemsShared items;
+  QcSharesScratch shares;
   uint32_t last;
 };
 
@@ -91,34 +90,32 @@ __device__ __forceinline__ void add_scaled(float4& a, const float4 x, float f) {
 __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const QcAttnParams p) {
   extern __shared__ __align__(128) uint8_t qt_sm[];
   __shared__ QtShared s;
-  int32_t* item0 = reinterpret_cast<int32_t*>(qt_sm + QT_WARPS * QT_WARP_BYTES);  // [n_users] items before a user
-  int32_t* part0 = item0 + p.n_users;                                                     // [n_users] partial rows before
+  int64_t* cost0 = reinterpret_cast<int64_t*>(qt_sm + QT_WARPS * QT_WARP_BYTES);  // [n_users] cost of the items before a user's
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int64_t most = (static_cast<int64_t>(p.max_blocks) << p.blocks_log2) * QC_ROWS;
 
-  const QcItems it = qc_items<QT_THREADS, QT_MIN_BLOCKS, QT_ITEM_BLOCKS, QT_JOIN_BLOCKS>(
-      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, item0, part0, s.items);
-  if (it.items > 0x7fffffffu || it.slots > static_cast<uint32_t>(QA_MOST_SPLITS * p.ctas)) {  // cannot be: see the host's checks
-    if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, DEV_ERR_BAD_WORK);
-    return;
-  }
-  const int n_items = static_cast<int>(it.items);
+  const QcShares sh = qc_shares<QT_THREADS, QT_MIN_BLOCKS, QT_ITEM_BLOCKS>(
+      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, cost0, nullptr, s.shares);
   bool ignored = false;
   const int rows_per_cand = p.group * p.Lq;
   const int64_t page_bytes = (static_cast<int64_t>(p.H_kv) << p.blocks_log2) * QC_BLOCK_BYTES;
 
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    const int u = qc_find(item0, p.n_users, item);
+  const int cta = static_cast<int>(blockIdx.x);
+  const int64_t end = cta < sh.parts ? sh.start(cta + 1) : 0;
+  for (int64_t at = cta < sh.parts ? sh.start(cta) : 0; at < end;) {
+    const int u = qc_find(cost0, p.n_users, at);
     const QcUserWork uw = user_work(p, u, most, ignored);
     const int len = uw.len;
-    const int ns = qc_splits(uw.units, it.chunk);
-    int local = item - item0[u];
-    const int tile = local % uw.tiles;
-    local /= uw.tiles;
-    const int split = local % ns, hk = local / ns;
-    const int b0 = qc_split_start(uw.units, ns, split) + warp;
-    const int b1 = qc_split_start(uw.units, ns, split + 1);
+    const int cost = sh.item_cost(uw.units);
+    const int local = static_cast<int>(qc_div(at - cost0[u], cost));
+    const int64_t pos = cost0[u] + static_cast<int64_t>(local) * cost;
+    at = pos + cost;  // the next item
+    const int hk = local / uw.tiles, tile = local - hk * uw.tiles;
+    const QcPart part = qc_part<QT_MIN_BLOCKS>(sh, uw, pos);
+    if (uw.units > 0 && part.nt == 0) continue;
+    const int ns = part.ns;
+    const int b0 = part.t0 + warp, b1 = part.t0 + part.nt;
     const int nb = b1 > b0 ? (b1 - b0 + QT_WARPS - 1) / QT_WARPS : 0;  // this warp's blocks
     const int seg = __ldg(p.offsets + u), count = __ldg(p.offsets + u + 1) - seg;
     const int n_rows = count * rows_per_cand;
@@ -324,13 +321,13 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
     }
     bool write = ns == 1;
     if (!write) {
-      // partial rows [r][128], then reference and sums; the tile's splits lie uw.tiles slots apart
-      const int first = part0[u] + hk * ns * uw.tiles + tile;
-      float* part = p.part + static_cast<int64_t>(first + split * uw.tiles) * QT_PART;
+      // partial rows [r][128], then reference and sums
+      const int first = part.first;
+      float* mine = p.part + static_cast<int64_t>(part.slot) * QT_PART;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) __stcg(reinterpret_cast<float4*>(part) + r * 32 + 8 * k + cc, acc[k]);
+      for (int k = 0; k < 4; ++k) __stcg(reinterpret_cast<float4*>(mine) + r * 32 + 8 * k + cc, acc[k]);
       if (cc == 0) {
-        float* ex = part + QT_ROWS * QC_D + r;
+        float* ex = mine + QT_ROWS * QC_D + r;
         __stcg(ex, mm);
         __stcg(ex + QT_ROWS, ll);
         __stcg(ex + 2 * QT_ROWS, ee);
@@ -346,24 +343,23 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
       write = s.last != 0;
       if (write) {
         __threadfence();
-        const float* p0 = p.part + static_cast<int64_t>(first) * QT_PART;
-        const int64_t step = static_cast<int64_t>(uw.tiles) * QT_PART;
-        const float* ex = p0 + QT_ROWS * QC_D + r;
+        const auto rows = [&](int k) { return p.part + static_cast<int64_t>(qc_slot(first, k)) * QT_PART; };
+        const auto ex = [&](int k) { return rows(k) + QT_ROWS * QC_D + r; };
         mm = -INFINITY;
 #pragma unroll 4
-        for (int k = 0; k < ns; ++k) mm = fmaxf(mm, __ldcg(ex + k * step));
+        for (int k = 0; k < ns; ++k) mm = fmaxf(mm, __ldcg(ex(k)));
         ll = ee = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int sp = 0; sp < ns; ++sp) {
-          const float mw = __ldcg(ex + sp * step);
+          const float mw = __ldcg(ex(sp));
           const float f = mw == -INFINITY ? 0.f : ex2(mw - mm);
-          ll += __ldcg(ex + sp * step + QT_ROWS) * f;
-          ee += __ldcg(ex + sp * step + 2 * QT_ROWS) * f;
+          ll += __ldcg(ex(sp) + QT_ROWS) * f;
+          ee += __ldcg(ex(sp) + 2 * QT_ROWS) * f;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            add_scaled(acc[k], __ldcg(reinterpret_cast<const float4*>(p0 + sp * step) + r * 32 + 8 * k + cc), f);
+            add_scaled(acc[k], __ldcg(reinterpret_cast<const float4*>(rows(sp)) + r * 32 + 8 * k + cc), f);
         }
       }
     }
@@ -387,13 +383,13 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
 }  // namespace
 
 int qattn_ctas(int num_sms) { return num_sms * QT_CTAS_PER_SM; }
-size_t qattn_part_elems(int num_sms) { return static_cast<size_t>(QA_MOST_SPLITS) * qattn_ctas(num_sms) * QT_PART; }
+size_t qattn_part_elems(int num_sms) { return static_cast<size_t>(QA_SLOTS) * qattn_ctas(num_sms) * QT_PART; }
 
 cudaError_t launch_qattn(const QcAttnParams& p, cudaStream_t s) {
   constexpr size_t rows = QT_WARPS * QT_WARP_BYTES;
-  const size_t smem = rows + 2 * sizeof(int32_t) * static_cast<size_t>(p.n_users);
+  const size_t smem = rows + sizeof(int64_t) * static_cast<size_t>(p.n_users);
   cudaError_t e = cudaFuncSetAttribute(qattn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(rows + 2 * sizeof(int32_t) * SEG_MAX_USERS));
+                                       static_cast<int>(rows + sizeof(int64_t) * SEG_MAX_USERS));
   if (e != cudaSuccess) return e;
   qattn_kernel<<<p.ctas, QT_THREADS, smem, s>>>(p);
   return cudaGetLastError();

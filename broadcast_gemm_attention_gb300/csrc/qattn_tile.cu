@@ -22,9 +22,9 @@
 //                once per tile (an inner product does not care), and V's
 //                columns are, which the epilogue undoes by its choice of names.
 //
-// Work: items (user, K/V head, split, tile) are listed by every CTA for itself
-// (a scan over the users); histories are split over CTAs where tiles alone do
-// not fill the GPU.  A split leaves its unnormalised O, [column][row], with
+// Work: each CTA takes an equal share of all tiles' histories, in a row, and
+// lists it for itself (a scan over the users); a history is split where one
+// CTA's share ends and the next one's begins.  A split leaves its unnormalised O, [column][row], with
 // each row's reference and sum; the last warp to finish a 32-row, 64-column
 // piece of a tile adds that piece's splits in order, so results repeat bit for
 // bit whichever CTA that is.
@@ -49,8 +49,7 @@ constexpr int LAUNCH_REGS = 96;  // 65536 / 640, in eights
 static_assert(128 * CTRL_REGS + SOFTMAX_THREADS * SOFTMAX_REGS + 64 * DECODE_WARPS * DECODE_REGS <= TL_THREADS * LAUNCH_REGS,
               "register split exceeds the launch's registers");
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
-constexpr int TL_ITEM_TILES = 14;           // what an item costs beside its key tiles, in key tiles
-constexpr int TL_JOIN_TILES = 1;           // and each split of a tile
+constexpr int TL_ITEM_TILES = 3;           // what an item costs beside its key tiles, in key tiles
 constexpr int TL_MIN_TILES = 4;            // key tiles of a split, at least
 constexpr int TL_PART = ATT_BM * ATT_D + 4 * ATT_BM;  // floats of a split's partial rows: O, and m and l per half
 constexpr int S_BUFS = 3;
@@ -69,14 +68,15 @@ struct Aux {
   uint64_t bars[NUM_BARS];
   float2 fin[2][2][ATT_BM];  // [item parity][group][row]: reference and sum of a finished item
   uint32_t chain[ATT_BM];
-  QcItemsShared items;
+  QcSharesScratch shares;
   uint32_t tmem_slot, abort, n_tiles;
+  int n_items;
   uint32_t decoded;  // key tile that the decode is at
 };
 constexpr uint32_t SMEM_USED = AUX_AT + sizeof(Aux);
 constexpr uint32_t SMEM_ALLOC = 227 * 1024;
 static_assert(SMEM_USED <= SMEM_ALLOC, "tiles do not fit in shared memory");
-static_assert(2 * sizeof(int32_t) * (SEG_MAX_USERS + 1) <= AUX_AT, "the users' prefixes do not fit");
+static_assert((sizeof(int64_t) + sizeof(int32_t)) * SEG_MAX_USERS <= AUX_AT, "the users' prefixes do not fit");
 
 struct Smem {
   uint8_t *q, *k, *v, *out;
@@ -113,7 +113,7 @@ __device__ __forceinline__ Smem carve(uint8_t* base) {
 struct Item {
   int u, hk, seg, n_rows;     // user, K/V head, the user's first place in perm, rows that read this history
   int row0, len, t0, nt;      // the tile's first row; tokens of the history; the split's key tiles t0 .. t0 + nt - 1
-  int ns, slot, first, step;  // splits of the tile; this split's slot for partial rows, the first split's, the step between them
+  int ns, slot, first, pad;  // splits of the tile; this split's slot for partial rows, the first split's
 };
 
 __device__ __forceinline__ int4 ld_int4(const int4* p) {  // written by this CTA in this launch: not the read-only path
@@ -122,20 +122,15 @@ __device__ __forceinline__ int4 ld_int4(const int4* p) {  // written by this CTA
   return r;
 }
 
-// This CTA's items: the first ones in shared memory, the others in the list.
-// Its place in the grid moves by one from each round of items to the next, so
-// that no CTA gets only the first tiles of pairs, or only the short second ones.
-__device__ __forceinline__ int64_t list_entry(int k) {
-  return static_cast<int64_t>(k) * gridDim.x + (blockIdx.x + static_cast<uint32_t>(k)) % gridDim.x;
-}
+// This CTA's items: the first ones in shared memory, the others in its part of
+// the list.
 struct List {
   const int4* near;
   const int4* far;
   int count;
 };
 __device__ __forceinline__ int4 item_part(const List& l, int k, int i) {
-  if (k < LIST_NEAR) return l.near[3 * k + i];
-  return ld_int4(l.far + 3 * list_entry(k) + i);
+  return k < LIST_NEAR ? l.near[3 * k + i] : ld_int4(l.far + 3 * static_cast<int64_t>(k) + i);
 }
 __device__ __forceinline__ int item_tiles(const List& l, int k) { return item_part(l, k, 1).w; }
 __device__ __forceinline__ Item load_item(const List& l, int k) {
@@ -152,42 +147,54 @@ __device__ __forceinline__ QcUserWork user_work(const QcAttnParams& p, int u, in
   return w;
 }
 
-// Writes this CTA's entries of the list; sm: [2 * n_users] ints of scratch.
-// Returns how many (-1: the sizes do not add up).
-__device__ int make_list(const QcAttnParams& p, int32_t* sm, Aux& x) {
+// Lists this CTA's items; sm: 12 bytes of scratch per user.
+__device__ List make_list(const QcAttnParams& p, uint8_t* sm, Aux& x) {
   const int tid = threadIdx.x, n = p.n_users;
-  int32_t* item0 = sm;
-  int32_t* part0 = sm + n;
+  int64_t* cost0 = reinterpret_cast<int64_t*>(sm);
+  int32_t* item0 = reinterpret_cast<int32_t*>(cost0 + n);
   const int64_t most = (static_cast<int64_t>(p.max_blocks) << p.blocks_log2) * QC_ROWS;
-  const QcItems it = qc_items<TL_THREADS, TL_MIN_TILES, TL_ITEM_TILES, TL_JOIN_TILES>(
-      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, item0, part0, x.items);
-  if (it.items > p.max_items || it.slots > static_cast<uint32_t>(QA_MOST_SPLITS * p.ctas)) return -1;
+  const QcShares sh = qc_shares<TL_THREADS, TL_MIN_TILES, TL_ITEM_TILES>(
+      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, cost0, item0, x.shares);
+  List l = {x.list, p.list, 0};
   bool ignored = false;
-  const int n_items = static_cast<int>(it.items), grid = static_cast<int>(gridDim.x);
-  const int full = n_items / grid;
-  const int count = full + (list_entry(full) < n_items ? 1 : 0);
-  int tiles = 0;
-  for (int k = tid; k < count; k += TL_THREADS) {
-    const int i = static_cast<int>(list_entry(k));
-    const int u = qc_find(item0, n, i);
-    const QcUserWork w = user_work(p, u, most, ignored);
-    const int ns = qc_splits(w.units, it.chunk);
-    const uint32_t local = static_cast<uint32_t>(i - item0[u]), other = local / static_cast<uint32_t>(w.tiles);
-    const int tile = static_cast<int>(local) - static_cast<int>(other) * w.tiles;
-    const int hk = static_cast<int>(other / static_cast<uint32_t>(ns)), split = static_cast<int>(other) - hk * ns;
-    const int t0 = qc_split_start(w.units, ns, split);
-    const int t1 = qc_split_start(w.units, ns, split + 1);
-    const int first = part0[u] + hk * ns * w.tiles + tile;
-    int4* e = k < LIST_NEAR ? x.list + 3 * k : p.list + 3 * static_cast<int64_t>(i);
-    const int seg = __ldg(p.offsets + u);
-    e[0] = make_int4(u, hk, seg, (__ldg(p.offsets + u + 1) - seg) * p.group * p.Lq);
-    e[1] = make_int4(tile * ATT_BM, w.len, t0, t1 - t0);
-    e[2] = make_int4(ns, first + split * w.tiles, first, w.tiles);
-    tiles += t1 - t0;
+  const int cta = static_cast<int>(blockIdx.x);
+  const int64_t end = cta < sh.parts ? sh.start(cta + 1) : 0;
+  if (cta < sh.parts && sh.start(cta) < end) {
+    int u = qc_find(cost0, n, sh.start(cta));
+    QcUserWork w = user_work(p, u, most, ignored);
+    const int i0 = item0[u] + static_cast<int>(qc_div(sh.start(cta) - cost0[u], sh.item_cost(w.units)));
+    l.far += 3 * (static_cast<int64_t>(i0) + cta);  // a CTA's first item may be the last of the one before
+    int tiles = 0, k = tid;
+    for (;; k += TL_THREADS) {
+      if (k > 0) {
+        u = qc_find(item0, n, i0 + k);
+        w = user_work(p, u, most, ignored);
+      }
+      const int local = i0 + k - item0[u];
+      const int64_t pos = cost0[u] + static_cast<int64_t>(local) * sh.item_cost(w.units);
+      if (pos >= end) break;
+      if (static_cast<int64_t>(i0) + cta + k >= p.max_items) {  // cannot be: the host counts them the same way
+        atomicOr(p.status, DEV_ERR_BAD_WORK);
+        break;
+      }
+      const QcPart part = qc_part<TL_MIN_TILES>(sh, w, pos);
+      const int hk = static_cast<int>(static_cast<uint32_t>(local) / static_cast<uint32_t>(w.tiles));
+      const int seg = __ldg(p.offsets + u);
+      int rows = (__ldg(p.offsets + u + 1) - seg) * p.group * p.Lq;
+      if (w.units > 0 && part.nt == 0) rows = 0;  // an empty part of an item
+      int4* e = k < LIST_NEAR ? x.list + 3 * k : const_cast<int4*>(l.far) + 3 * static_cast<int64_t>(k);
+      e[0] = make_int4(u, hk, seg, rows);
+      e[1] = make_int4((local - hk * w.tiles) * ATT_BM, w.len, part.t0, part.nt);
+      e[2] = make_int4(part.ns, part.slot, part.first, 0);
+      tiles += part.nt;
+    }
+    // the threads' first places behind the end: the least is the number of items
+    if (tiles) atomicAdd(&x.n_tiles, static_cast<uint32_t>(tiles));
+    atomicMin(&x.n_items, k);
   }
-  if (tiles) atomicAdd(&x.n_tiles, static_cast<uint32_t>(tiles));
   __syncthreads();  // the entries are visible to the CTA, the scratch is free
-  return count;
+  l.count = x.n_items == 0x7fffffff ? 0 : x.n_items;
+  return l;
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Smem& s, const QcAttnParams& p) {
@@ -609,14 +616,13 @@ __device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, 
   last = __shfl_sync(0xffffffffu, last, 0);
   if (!last) return;
   __threadfence();
-  const float* first = p.part + ro.first * SLOT;
-  const int64_t stride = ro.step * SLOT;
+  const auto part = [&](int k) { return p.part + qc_slot(ro.first, k) * SLOT; };
   float M = -INFINITY;
-  for (int k = 0; k < ro.ns; ++k) M = fmaxf(M, __ldcg(first + k * stride + ml));
+  for (int k = 0; k < ro.ns; ++k) M = fmaxf(M, __ldcg(part(k) + ml));
   float L = 0.f;
   for (int k = 0; k < ro.ns; ++k) {
-    const float m = __ldcg(first + k * stride + ml);
-    L += (m == -INFINITY ? 0.f : ex2(m - M)) * __ldcg(first + k * stride + ml + ATT_BM);
+    const float m = __ldcg(part(k) + ml);
+    L += (m == -INFINITY ? 0.f : ex2(m - M)) * __ldcg(part(k) + ml + ATT_BM);
   }
   const float inv = inverse(L);
   if (p.lse && row >= 0 && ln.half == 0) store_lse(p, row, M, L);
@@ -627,7 +633,7 @@ __device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, 
     for (int j = 0; j < 16; ++j) acc[j] = 0.f;
 #pragma unroll 2
     for (int k = 0; k < ro.ns; ++k) {
-      const float* sp = first + k * stride;
+      const float* sp = part(k);
       const float m = __ldcg(sp + ml);
       const float f = m == -INFINITY ? 0.f : ex2(m - M);
       float x[16];
@@ -867,6 +873,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
     for (int r = 0; r < ATT_BM; ++r) s.x->chain[r] = 0;
     s.x->abort = 0;
     s.x->n_tiles = 0;
+    s.x->n_items = 0x7fffffff;
     s.x->decoded = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -875,14 +882,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
     tmem_alloc(&s.x->tmem_slot, 512);
     tmem_relinquish();
   }
-  List l;
-  l.near = s.x->list;
-  l.far = p.list;
-  l.count = make_list(p, reinterpret_cast<int32_t*>(smem_raw + pad), *s.x);
-  if (l.count < 0) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(p.status, DEV_ERR_BAD_WORK);
-    l.count = 0;
-  }
+  const List l = make_list(p, smem_raw + pad, *s.x);
   fence_proxy_async_smem();  // the scratch of the list lay where bulk copies go
   tc_fence_before();
   __syncthreads();
@@ -915,10 +915,10 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
 }  // namespace
 
 size_t qattn_tile_smem() { return SMEM_ALLOC; }
-size_t qattn_tile_part_elems(int num_sms) { return static_cast<size_t>(QA_MOST_SPLITS) * num_sms * TL_PART; }
-// Items of a request: one per tile, and at most QA_MOST_SPLITS splits per CTA.
+size_t qattn_tile_part_elems(int num_sms) { return static_cast<size_t>(QA_SLOTS) * num_sms * TL_PART; }
+// Entries of the list: one per tile, and one per CTA for a tile it shares.
 int64_t qattn_tile_items(int64_t rows, int n_users, int H_kv, int num_sms) {
-  return (rows / ATT_BM + n_users) * H_kv + QA_MOST_SPLITS * static_cast<int64_t>(num_sms);
+  return (rows / ATT_BM + n_users) * H_kv + num_sms;
 }
 
 cudaError_t launch_qattn_tile(const QcAttnParams& p, cudaStream_t s) {

@@ -370,7 +370,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   if (!few && qattn_tile_smem() > p->max_smem) return IKBO_ERR_UNSUPPORTED;
   const int ctas = few ? qattn_ctas(p->num_sms) : p->num_sms;
   const size_t part = few ? qattn_part_elems(p->num_sms) : qattn_tile_part_elems(p->num_sms);
-  const size_t tickets = static_cast<size_t>(QA_MOST_SPLITS) * ctas * (few ? 1 : 8);
+  const size_t tickets = static_cast<size_t>(QA_SLOTS) * ctas * (few ? 1 : 8);
   const int64_t items = few ? 0 : qattn_tile_items(rows, n_users, H_kv, p->num_sms);
   if (grow_kept(p, &p->d_qa_part, &p->qa_part_elems, part, stream) != cudaSuccess ||
       grow_kept(p, &p->d_qa_tickets, &p->qa_tickets_elems, tickets, stream) != cudaSuccess ||

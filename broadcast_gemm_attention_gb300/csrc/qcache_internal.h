@@ -33,11 +33,9 @@ constexpr int QC_HALF_BYTES = 1280;    // keys' or values' codes and pairs
 constexpr int QC_CODE_BYTES = 1024;    // 16 x 64 bytes of codes, then 16 x 4 pairs (s, z) of two bf16
 constexpr int QC_MAX_PAGE = 1024;
 
-// Histories are split so that the longest CTA's share is short: QA_ROUNDS
-// lengths of a split are compared, aiming at 1, 2, 4 .. items per CTA; the
-// splits of a launch are at most QA_MOST_SPLITS per CTA.
-constexpr int QA_ROUNDS = 4;
-constexpr int QA_MOST_SPLITS = 1 << (QA_ROUNDS - 1);
+// Slots for partial rows per CTA of an attention launch: its share of the work
+// begins and ends within an item.
+constexpr int QA_SLOTS = 2;
 
 struct QcResizeParams {
   int32_t* lens;
@@ -87,7 +85,7 @@ struct QcAttnParams {
   const int32_t* lens;
   const int32_t* offsets;  // the plan's segments
   const int32_t* perm;
-  float* part;             // [QA_MOST_SPLITS * ctas] splits' partial rows: unnormalised O, reference and sums
+  float* part;             // [QA_SLOTS * ctas] splits' partial rows: unnormalised O, reference and sums
   uint32_t* tickets;       // one per slot of part (tiles of 128 rows: 8 each)
   int4* list;              // tiles of 128 rows: the work list, three per item
   int64_t max_items;
@@ -114,7 +112,8 @@ __device__ __forceinline__ int qc_length(const int32_t* lens, int u, int64_t mos
 
 // The last u in [0, n) with base[u] <= x (base ascending, base[0] <= x): the
 // user whose range of a flattened index holds x (empty ranges are skipped).
-__device__ __forceinline__ int qc_find(const int32_t* base, int n, int x) {
+template <typename T>
+__device__ __forceinline__ int qc_find(const T* base, int n, T x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -124,78 +123,95 @@ __device__ __forceinline__ int qc_find(const int32_t* base, int n, int x) {
   return lo;
 }
 
-// Splits of a history of `units` (blocks or key tiles) into about `chunk` each:
-// the quotient rounded up, in fp32 and so that an error of its last bits adds
-// no split (a split may be 1/100000 longer than `chunk`).  The same in every
-// place that asks.
-__device__ __forceinline__ int qc_splits(int units, int chunk) {
-  const float q = __fmul_rn(__fdividef(static_cast<float>(units), static_cast<float>(chunk)), 0.99999f);
-  return units <= chunk ? 1 : static_cast<int>(ceilf(q));
+// The sum of a warp's lanes (none below 0), 24 bits at a time.
+__device__ __forceinline__ int64_t qc_warp_sum(int64_t v) {
+  const int64_t x = v;
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x) & 0xFFFFFFu);
+  const uint32_t mid = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x >> 24) & 0xFFFFFFu);
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(x >> 48));
+  return (static_cast<int64_t>(hi) << 48) + (static_cast<int64_t>(mid) << 24) + lo;
 }
 
-// First unit of split i of n of `units` (the first units % n are one longer).
-__device__ __forceinline__ int qc_split_start(int units, int n, int i) {
-  const int q = units / n, rest = units - q * n;
-  return q * i + min(i, rest);
-}
-
-// Sums over the CTA's threads, or with `warp` over one warp that is alone here;
-// red: a word per warp.
-template <int kThreads>
-__device__ __forceinline__ uint32_t qc_sum(uint32_t v, uint32_t* red, bool warp) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  if (warp) return v;
-  const int lane = threadIdx.x & 31;
-  __syncthreads();  // red has been read
-  if (lane == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? red[lane] : 0u);
-}
-
-__device__ __forceinline__ float qc_warp_sum(float v) {
+// x / c for 0 <= x, 1 <= c: an estimate, put right.
+__device__ __forceinline__ int64_t qc_div(int64_t x, int c) {
+  int64_t q = static_cast<int64_t>(__fdividef(static_cast<float>(x), static_cast<float>(c)));
 #pragma unroll 1
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  while (q * c > x) --q;
+#pragma unroll 1
+  while ((q + 1) * c <= x) ++q;
+  return q;
 }
 
-// Exclusive prefixes of a warp's lanes.
-__device__ __forceinline__ uint32_t qc_warp_scan(uint32_t v) {
-  uint32_t x = v;
+// Inclusive prefixes of a warp's lanes.
+template <typename T>
+__device__ __forceinline__ T qc_warp_scan(T x) {
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (static_cast<int>(threadIdx.x & 31) >= o) x += y;
   }
-  return x - v;
+  return x;
 }
 
-// The list of items that every CTA of an attention launch works out for
-// itself: item0[u], part0[u] = items and partial slots before user u; an item
-// is (user, K/V head, split, tile) in that order, slots only where a history
-// has several splits.  work(u, bad) gives a user's tiles per head, units
-// (blocks or key tiles) and length.  With up to 32 users one warp does it
-// alone.  Lengths of a split are compared by the CTAs' largest share: its
-// items' units, kItem beside each and kJoin for each split of a tile.
+// ---- how the CTAs of an attention launch share the work
+// An item is (user, K/V head, tile of query rows), in that order; its length is
+// the history's units (blocks or key tiles), and its cost that and `overhead`
+// units more (1 where there are no tokens).  All items' costs in a row are cut
+// into as many equal shares as there are CTAs, so a CTA has a run of items, of
+// which the first and the last may be parts: every CTA works for the same time
+// (to the rows that a tile lacks), there are no more parts than items and CTAs,
+// and parts of one item always lie in consecutive CTAs.  (Whole items dealt out
+// in turn, with histories cut to one length that fills the CTAs best, took 10%
+// to 25% longer where histories differ.)
 //
-// A CTA runs this once, from instructions that no cache holds yet (a small
-// launch spends more time here than on its products), so it is written for few
-// instructions: loops stay loops, 32-bit and fp32 numbers, no integer division.
-// (All items and tiles fit in 31 bits: checked on the host.)
+// A request too small for shares of an item's overhead and kMin units is cut
+// evenly instead, each item into parts of about `chunk` units, one for a CTA: an
+// item's cost is then its parts, and a share 1.
 struct QcUserWork {
   int tiles, units, len;
 };
-struct QcItems {
-  uint32_t items, slots;
-  int chunk;  // units of a split, at most
+struct QcShares {
+  int64_t base;         // start(b) = b base + b rest / parts
+  int parts, rest;      // shares (at most the launch's CTAs), items' costs beside base parts
+  int overhead, chunk;  // chunk > 0: even parts
+  // The quotient is of numbers below 2^18 by one below 2^9: with a half added it
+  // is further from a whole number than an fp32 quotient's error.
+  __device__ __forceinline__ int64_t start(int b) const {
+    return b * base + static_cast<int>(__fdividef(static_cast<float>(b * rest) + 0.5f, static_cast<float>(parts)));
+  }
+  __device__ __forceinline__ int item_cost(int units) const;
 };
-struct QcItemsShared {
-  uint32_t red[32];
-  QcItems it;
+struct QcSharesScratch {
+  int64_t red[3][32];
+  QcShares shares;
 };
+// A CTA's part of an item.
+struct QcPart {
+  int t0, nt;       // units t0 .. t0 + nt - 1
+  int ns;           // parts of the item that are not empty; if above 1:
+  int slot, first;  // this part's slot for partial rows, the first part's
+};
+__device__ __forceinline__ int QcShares::item_cost(int units) const {
+  if (units == 0) return 1;
+  // parts of at most `chunk`, but for the quotient's last bits
+  return chunk > 0 ? static_cast<int>(ceilf(__fmul_rn(__fdividef(static_cast<float>(units), static_cast<float>(chunk)), 0.99999f)))
+                   : units + overhead;
+}
+// The k-th part's slot (the first part ends its CTA's share, the others begin one).
+__device__ __forceinline__ int qc_slot(int first, int k) { return k == 0 ? first : (first & ~1) + 2 * k; }
 
-template <int kThreads, int kMin, int kItem, int kJoin, typename Work>
-__device__ __forceinline__ QcItems qc_items(const QcAttnParams& p, const Work& work, int32_t* item0, int32_t* part0,
-                                            QcItemsShared& sh) {
+// Works out the shares, and where each user's items begin: cost0[u] in costs,
+// item0[u] (if not null) counted.  work(u, bad) gives a user's tiles per head,
+// units and length.  With up to 32 users one warp does it alone.
+//
+// A CTA runs this once, from instructions that no cache holds yet (a small
+// launch spends more time here than on its products), so it is written for few
+// instructions: loops stay loops, and no integer division.  (All items fit in 31
+// bits: checked on the host.)
+template <int kThreads, int kMin, int kOverhead, typename Work>
+__device__ __forceinline__ QcShares qc_shares(const QcAttnParams& p, const Work& work, int64_t* cost0, int32_t* item0,
+                                              QcSharesScratch& sh) {
+  constexpr int kWarps = kThreads / 32;
   static_assert(kThreads <= 1024, "a word of red per warp");
   const int n = p.n_users;
   const bool few = n <= 32;
@@ -207,93 +223,120 @@ __device__ __forceinline__ QcItems qc_items(const QcAttnParams& p, const Work& w
     QcUserWork one = {};  // this thread's user where it has only one
     if (per == 1 && lo < n) one = work(lo, bad);
     const auto get = [&](int u) { return per == 1 ? one : work(u, ignored); };
-    float sum = 0.f;  // of tiles x units: a bound with a margin for its rounding is made of it
-    int64_t lens = 0;
-    uint32_t tiles = 0;
-    int longest = 0;
+    // three sums: the units of all items, tokens, and items with units (low half) and without
+    int64_t v[3] = {0, 0, 0};
     for (int u = lo; u < hi; ++u) {
       const QcUserWork w = per == 1 ? one : work(u, bad);
-      sum += static_cast<float>(w.tiles) * static_cast<float>(w.units);
-      lens += w.len;
-      tiles += static_cast<uint32_t>(w.tiles);
-      if (w.tiles > 0) longest = max(longest, w.units);
+      const int64_t items = static_cast<int64_t>(w.tiles) * p.H_kv;
+      v[0] += items * w.units;
+      v[1] += w.len;
+      v[2] += w.units > 0 ? items : items << 32;
     }
-    sum = qc_warp_sum(sum);
-    longest = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(longest)));
+#pragma unroll 1
+    for (int k = 0; k < 3; ++k) {
+      const int64_t x = qc_warp_sum(v[0]);
+      v[0] = v[1], v[1] = v[2], v[2] = x;
+      if (!few && lane == 0) sh.red[k][warp] = x;
+    }
     if (!few) {
-      if (lane == 0) {
-        sh.red[warp] = __float_as_uint(sum);
-        item0[warp] = longest;  // (there are more users than warps)
+      __syncthreads();
+#pragma unroll 1
+      for (int k = 0; k < 3; ++k) {
+        const int64_t x = qc_warp_sum(lane < kWarps ? sh.red[k][lane] : int64_t{0});
+        v[0] = v[1], v[1] = v[2], v[2] = x;
+      }
+      __syncthreads();  // red has been read
+    }
+    if (v[1] > p.bound) bad = true;
+    if (bad && blockIdx.x == 0) atomicOr(p.status, DEV_ERR_CACHE);
+    const int64_t with = v[2] & 0xFFFFFFFF, without = v[2] >> 32, items_all = with + without;
+    int64_t total = v[0] + with * kOverhead + without;
+    QcShares r = {0, p.ctas, 0, kOverhead, 0};
+    if (total < static_cast<int64_t>(kMin + kOverhead) * p.ctas) {
+      if (items_all < p.ctas)  // (each item's parts are rounded up, hence the items taken off)
+        r.chunk = max(kMin, static_cast<int>(__fdividef(static_cast<float>(v[0]), static_cast<float>(p.ctas - items_all)) * 1.0001f) + 1);
+      else
+        r.parts = max(1, static_cast<int>(total) / (kMin + kOverhead));
+    }
+    int64_t cost = 0;
+    uint32_t items = 0;
+    const auto add = [&](const QcUserWork& w) {
+      const int64_t k = static_cast<int64_t>(w.tiles) * p.H_kv;
+      cost += k * r.item_cost(w.units);
+      items += static_cast<uint32_t>(k);
+    };
+    for (int u = lo; u < hi; ++u) add(get(u));
+    const int64_t mine = cost;
+    const uint32_t mine_items = items;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, cost, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, items, o);
+      if (lane >= o) cost += x, items += y;
+    }
+    if (!few) {  // and the warps before
+      if (lane == 31) {
+        sh.red[0][warp] = cost;
+        sh.red[1][warp] = items;
       }
       __syncthreads();
-      sum = qc_warp_sum(lane < kThreads / 32 ? __uint_as_float(sh.red[lane]) : 0.f);
-      longest = static_cast<int>(__reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? static_cast<unsigned>(item0[lane]) : 0u));
+      cost += qc_warp_sum(lane < warp ? sh.red[0][lane] : int64_t{0});
+      items += __reduce_add_sync(0xffffffffu, lane < warp ? static_cast<uint32_t>(sh.red[1][lane]) : 0u);
     }
-    tiles = qc_sum<kThreads>(tiles, sh.red, few);
-    // 24 bits and the rest: neither sum leaves 32 bits
-    const uint32_t l0 = qc_sum<kThreads>(static_cast<uint32_t>(lens & 0xFFFFFF), sh.red, few);
-    const uint32_t l1 = qc_sum<kThreads>(static_cast<uint32_t>(lens >> 24), sh.red, few);
-    if ((static_cast<int64_t>(l1) << 24) + l0 > p.bound) bad = true;
-    if (bad && blockIdx.x == 0) atomicOr(p.status, DEV_ERR_CACHE);
-    // r: 2^r items per CTA aimed at (a tile's splits are rounded up, hence the
-    // tiles taken off); too few to split anything: one item per tile
-    const float work_all = sum * static_cast<float>(p.H_kv) * 1.0001f;
-    const int64_t tiles_all = static_cast<int64_t>(tiles) * p.H_kv;
-    QcItems it = {0, 0, 1};
-    float best = 0.f;
-#pragma unroll 1
-    for (int r = 0; r < QA_ROUNDS; ++r) {
-      const int64_t room = (static_cast<int64_t>(p.ctas) << r) - tiles_all;
-      int chunk = max(longest, 1);
-      if (room > 0) chunk = max(static_cast<int>(fminf(__fdividef(work_all, static_cast<float>(room)) + 1.f, 1e8f)), kMin);
-      uint32_t count = 0;
-      for (int u = lo; u < hi; ++u) {
-        const QcUserWork w = get(u);
-        count += static_cast<uint32_t>(w.tiles * qc_splits(w.units, chunk));
+    if (tid == (few ? 31 : kThreads - 1)) {  // has all costs
+      if (r.chunk > 0) {
+        total = cost;
+        r.parts = max(1, static_cast<int>(cost));
       }
-      count = qc_sum<kThreads>(count, sh.red, few) * static_cast<uint32_t>(p.H_kv);
-      const int ns = qc_splits(longest, chunk);
-      const float share = ceilf(static_cast<float>(count) / static_cast<float>(p.ctas)) *
-                              (ceilf(__fdividef(static_cast<float>(longest), static_cast<float>(ns))) + kItem) +
-                          (ns > 1 ? static_cast<float>(ns * kJoin) : 0.f);
-      if (r == 0 || share < best) {
-        best = share;
-        it.chunk = chunk;
-      }
-      if (room > 0 && chunk == kMin) break;  // shorter splits there are not
+      r.base = qc_div(total, r.parts);
+      r.rest = static_cast<int>(total - r.base * r.parts);
+      sh.shares = r;
     }
-    uint32_t items = 0, slots = 0;
+    cost -= mine;
+    items -= mine_items;
     for (int u = lo; u < hi; ++u) {
-      const QcUserWork w = get(u);
-      const int ns = qc_splits(w.units, it.chunk);
-      const uint32_t k = static_cast<uint32_t>(w.tiles) * static_cast<uint32_t>(p.H_kv * ns);
-      items += k;
-      slots += ns > 1 ? k : 0u;
+      cost0[u] = cost;
+      if (item0) item0[u] = static_cast<int32_t>(items);
+      add(get(u));
     }
-    uint32_t v0 = qc_warp_scan(items), v1 = qc_warp_scan(slots);
-    it.items = qc_sum<kThreads>(items, sh.red, few);
-    if (!few) {  // red holds the warps' sums
-      uint32_t before = qc_warp_scan(lane < kThreads / 32 ? sh.red[lane] : 0u);
-      v0 += __shfl_sync(0xffffffffu, before, warp);
-      it.slots = qc_sum<kThreads>(slots, sh.red, few);
-      before = qc_warp_scan(lane < kThreads / 32 ? sh.red[lane] : 0u);
-      v1 += __shfl_sync(0xffffffffu, before, warp);
-    } else {
-      it.slots = qc_sum<kThreads>(slots, sh.red, few);
-    }
-    for (int u = lo; u < hi; ++u) {
-      const QcUserWork w = get(u);
-      const int ns = qc_splits(w.units, it.chunk);
-      const uint32_t k = static_cast<uint32_t>(w.tiles) * static_cast<uint32_t>(p.H_kv * ns);
-      item0[u] = static_cast<int32_t>(v0);
-      part0[u] = static_cast<int32_t>(v1);
-      v0 += k;
-      v1 += ns > 1 ? k : 0u;
-    }
-    if (tid == 0) sh.it = it;
   }
   __syncthreads();
-  return sh.it;
+  return sh.shares;
+}
+
+// The part of the item at `pos` (of a user's work w) that belongs to this CTA,
+// whose share overlaps it.  Cuts that would leave a part of fewer than kMin
+// units move to the item's end, the same way for the CTAs on both sides.
+template <int kMin>
+__device__ __forceinline__ QcPart qc_part(const QcShares& sh, const QcUserWork& w, int64_t pos) {
+  QcPart r = {0, w.units, 1, 0, 0};
+  const int cta = static_cast<int>(blockIdx.x), cost = sh.item_cost(w.units);
+  const int64_t start = sh.start(cta), end = sh.start(cta + 1);
+  if (w.units == 0 || (pos >= start && pos + cost <= end)) return r;
+  const auto cut = [&](int64_t at) {  // a cut at cost `at`, in units
+    const int x = static_cast<int>(at - pos);
+    if (sh.chunk > 0) return static_cast<int>(static_cast<uint32_t>(x) * static_cast<uint32_t>(w.units) / static_cast<uint32_t>(cost));
+    const int t = x - sh.overhead;
+    return t < kMin ? 0 : (t > w.units - kMin ? w.units : t);
+  };
+  // the CTAs whose shares the item lies in: at least so many, then the others
+  const uint32_t most = static_cast<uint32_t>(min(sh.base + (sh.rest > 0), int64_t{0x7fffffff}));  // of a share
+  int first = cta, last = cta;
+  if (pos < start) first -= static_cast<int>(static_cast<uint32_t>(start - pos) / most);
+  if (pos + cost > end) last += static_cast<int>(static_cast<uint32_t>(pos + cost - end) / most);
+#pragma unroll 1
+  while (sh.start(first) > pos) --first;
+#pragma unroll 1
+  while (sh.start(last + 1) < pos + cost) ++last;
+  r.t0 = first < cta ? cut(start) : 0;
+  r.nt = (cta < last ? cut(end) : w.units) - r.t0;
+  // a share is at least kMin and the overhead, so only the first and the last part can be empty
+  const int headless = cut(sh.start(first + 1)) == 0;
+  const int tailless = cut(sh.start(last)) == w.units;
+  r.ns = last - first + 1 - headless - tailless;
+  r.first = 2 * (first + headless) + (headless ? 0 : 1);
+  r.slot = 2 * cta + (first < cta ? 0 : 1);
+  return r;
 }
 
 // Two bf16 values from nibbles at bits SHIFT .. of each half of w:
