@@ -7,7 +7,7 @@
 // queries of the heads that share g: R = count[u] * (H / H_kv) * Lq.  With few
 // of them the operator is bound by the cache's bytes (160 a token and head),
 // and the work that counts besides is turning 4-bit codes into operands.
-// Here that happens once per tile of 16 rows, in registers: the operand
+// Here that happens once per tile of 8 or 16 rows, in registers: the operand
 // layout of the 16x8x16 warp-level matrix instruction lets a lane read its
 // share of a block as whole 16- or 8-byte pieces of codes (the order of
 // elements along a product's inner dimension is free, so Q is permuted to
@@ -15,10 +15,16 @@
 // product would have to write them to shared memory first and would use 8 to
 // 16 of its 128 rows.
 //
-// Work: a tile is 16 rows of one (u, g); its history is cut into splits
-// of whole blocks (16 tokens, 2560 contiguous bytes), sized on the device so
-// that the splits of all tiles fill the GPU.  A CTA takes one (tile, split); its
-// four warps take every fourth block, loading the next block's codes into the
+// The products are S^T = K Q^T (16 tokens x 8 rows) and O^T = V^T P^T (16
+// elements x 8 rows): the few rows are the instruction's short side, so that 8
+// of them take half the products and registers of 16, and 16 warps fit on an SM
+// instead of 12.  P^T comes out of the first product as the second one needs it
+// but for a transposition of 8 x 8 pairs within the warp.
+//
+// Work: a tile is 8 or 16 rows of one (u, g); its history is cut into parts of
+// whole blocks (16 tokens, 2560 contiguous bytes) where the CTAs' equal shares
+// end.  A CTA works through its share, item by item; its four warps take every
+// fourth block, loading the next block's codes into the
 // registers of the one just decoded (no barrier in the loop; the lines of the
 // block after that are asked for in L2), and keep their own running maximum,
 // sum and O in registers.  The warps are joined through shared memory; splits of
@@ -46,15 +52,16 @@ constexpr int QT_ITEM_BLOCKS = 24;           // what an item costs beside its bl
 constexpr float QT_THRESHOLD = 8.0f;         // log2 units
 constexpr int QT_EXTRA = 3;                  // per row besides O: reference, sum, sum of the log-sum-exp
 
-constexpr int QT_ROWS = 16;
-constexpr int QT_CTAS_PER_SM = 3;
-constexpr int QT_PART = QT_ROWS * (QC_D + QT_EXTRA);  // floats of a split's partial rows
-constexpr int QT_WARP_BYTES = QT_ROWS * QC_D * 4;     // a warp's O on its way to the others
+// By rows of a tile (8 kRows8): CTAs resident on an SM, floats of a part's
+// partial rows, bytes of a warp's O on its way to the others.
+__host__ __device__ constexpr int qt_ctas_per_sm(int rows8) { return rows8 == 1 ? 3 : 2; }
+__host__ __device__ constexpr int qt_part(int rows8) { return 8 * rows8 * (QC_D + QT_EXTRA); }
+__host__ __device__ constexpr int qt_warp_bytes(int rows8) { return 8 * rows8 * QC_D * 4; }
 
 struct QtShared {
-  float m[QT_WARPS][QT_ROWS];
-  float l[QT_WARPS][QT_ROWS];
-  float le[QT_WARPS][QT_ROWS];
+  float m[QT_WARPS][16];
+  float l[QT_WARPS][16];
+  float le[QT_WARPS][16];
   QcSharesScratch shares;
   uint32_t last;
 };
@@ -66,19 +73,35 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// c += the columns' sums of the bf16 matrix b (16 x 8): a product with ones, of
+// which one row is kept.
+__device__ __forceinline__ void mma_sums(float (&c)[2], uint32_t b0, uint32_t b1) {
+  float d2, d3;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%4,%4,%4}, {%5,%6}, {%0,%1,%7,%7};"
+      : "+f"(c[0]), "+f"(c[1]), "=f"(d2), "=f"(d3)
+      : "r"(0x3F803F80u), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The 8 x 8 matrix of 16-bit elements that a warp holds, two of a row per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int kRows>
 __device__ __forceinline__ QcUserWork user_work(const QcAttnParams& p, int u, int64_t most, bool& bad) {
   QcUserWork w;
   const int count = __ldg(p.offsets + u + 1) - __ldg(p.offsets + u);
   w.len = qc_length(p.lens, u, most, bad);
-  w.tiles = static_cast<int>((static_cast<int64_t>(count) * p.group * p.Lq + QT_ROWS - 1) / QT_ROWS);
+  w.tiles = static_cast<int>((static_cast<int64_t>(count) * p.group * p.Lq + kRows - 1) / kRows);
   w.units = (w.len + QC_ROWS - 1) / QC_ROWS;
   return w;
 }
 
 // Place of 16-byte piece c (of 32) of a row of a warp's staged O: pieces are
-// permuted so that the lanes' stores (rows g, quarters t) and the readers'
-// loads spread over the banks.
-__device__ __forceinline__ int o_piece(int row, int c) { return (c & ~7) | ((c & 7) ^ ((c >> 3) | ((row & 1) << 2))); }
+// permuted so that the lanes' stores (rows 2t, pieces 4g) spread over the banks.
+__device__ __forceinline__ int o_piece(int row, int c) { return c ^ ((row >> 1) & 3); }
 
 __device__ __forceinline__ void add_scaled(float4& a, const float4 x, float f) {
   a.x = fmaf(x.x, f, a.x);
@@ -87,17 +110,20 @@ __device__ __forceinline__ void add_scaled(float4& a, const float4 x, float f) {
   a.w = fmaf(x.w, f, a.w);
 }
 
-__global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const QcAttnParams p) {
+template <int kRows8>
+__global__ void __launch_bounds__(QT_THREADS, qt_ctas_per_sm(kRows8)) qattn_kernel(const QcAttnParams p) {
+  constexpr int kRows = 8 * kRows8, kPart = qt_part(kRows8), kWarpBytes = qt_warp_bytes(kRows8);
   extern __shared__ __align__(128) uint8_t qt_sm[];
   __shared__ QtShared s;
-  int64_t* cost0 = reinterpret_cast<int64_t*>(qt_sm + QT_WARPS * QT_WARP_BYTES);  // [n_users] cost of the items before a user's
+  int64_t* cost0 = reinterpret_cast<int64_t*>(qt_sm + QT_WARPS * kWarpBytes);  // [n_users] cost of the items before a user's
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int64_t most = (static_cast<int64_t>(p.max_blocks) << p.blocks_log2) * QC_ROWS;
 
   const QcShares sh = qc_shares<QT_THREADS, QT_MIN_BLOCKS, QT_ITEM_BLOCKS>(
-      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, cost0, nullptr, s.shares);
+      p, [&](int u, bool& bad) { return user_work<kRows>(p, u, most, bad); }, cost0, nullptr, s.shares);
   bool ignored = false;
+  const uint32_t sixteen = p.sixteen;
   const int rows_per_cand = p.group * p.Lq;
   const int64_t page_bytes = (static_cast<int64_t>(p.H_kv) << p.blocks_log2) * QC_BLOCK_BYTES;
 
@@ -105,7 +131,7 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
   const int64_t end = cta < sh.parts ? sh.start(cta + 1) : 0;
   for (int64_t at = cta < sh.parts ? sh.start(cta) : 0; at < end;) {
     const int u = qc_find(cost0, p.n_users, at);
-    const QcUserWork uw = user_work(p, u, most, ignored);
+    const QcUserWork uw = user_work<kRows>(p, u, most, ignored);
     const int len = uw.len;
     const int cost = sh.item_cost(uw.units);
     const int local = static_cast<int>(qc_div(at - cost0[u], cost));
@@ -137,9 +163,10 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
     const auto block_at = [&](int j) {
       return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine), j & 31));
     };
-    // a block in registers: for column g lane (g, t) reads token
-    // (g >> 1) + 4 (g & 1) + 8 nt of the keys, so that its own scores are of
-    // tokens t, t + 4, t + 8, t + 12, whose values it reads
+    // a block in registers: for row g of the first product (and g + 8) lane
+    // (g, t) reads token (g >> 1) + 4 (g & 1) (and 8 more), so that the inner
+    // elements 2t, 2t + 1, 2t + 8, 2t + 9 of the second are tokens t, t + 4,
+    // t + 8, t + 12, of which it reads elements 16g .. 16g + 15
     uint4 kc[2];
     uint32_t kp[2], vp[4];
     uint2 vc[4];
@@ -165,12 +192,12 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
       load_v(cur);
     }
 
-    // Q: rows g and g + 8; lane t holds elements 32t .. 32t+31, in the order in
-    // which a block's codes unpack (element e of a word of eight with e + 4)
-    uint32_t q[8][4];
+    // Q: row g of each eight; lane t holds elements 32t .. 32t+31, in the order
+    // in which a block's codes unpack (element e of a word of eight with e + 4)
+    uint32_t q[kRows8][8][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = tile * QT_ROWS + g + 8 * half;
+    for (int n = 0; n < kRows8; ++n) {
+      const int r = tile * kRows + g + 8 * n;
       uint4 x[4] = {};
       if (r < n_rows) {
         const int slot = r / rows_per_cand, rest = r - slot * rows_per_cand;
@@ -182,16 +209,23 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
       }
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        q[2 * w][half] = __byte_perm(x[w].x, x[w].z, 0x5410);
-        q[2 * w][2 + half] = __byte_perm(x[w].x, x[w].z, 0x7632);
-        q[2 * w + 1][half] = __byte_perm(x[w].y, x[w].w, 0x5410);
-        q[2 * w + 1][2 + half] = __byte_perm(x[w].y, x[w].w, 0x7632);
+        q[n][2 * w][0] = __byte_perm(x[w].x, x[w].z, 0x5410);
+        q[n][2 * w][1] = __byte_perm(x[w].x, x[w].z, 0x7632);
+        q[n][2 * w + 1][0] = __byte_perm(x[w].y, x[w].w, 0x5410);
+        q[n][2 * w + 1][1] = __byte_perm(x[w].y, x[w].w, 0x7632);
       }
     }
 
-    float o[16][4] = {}, sum[4] = {};                // sum: the column of ones
-    float m0 = -INFINITY, m1 = -INFINITY;            // reference of rows g, g + 8
-    float u0 = 0.f, u1 = 0.f, le0 = 0.f, le1 = 0.f;  // the one subtracted (0 while it is -inf), log-sum-exp's sums
+    // per eight rows, of which the lane has 2t and 2t + 1
+    float o[kRows8][8][4] = {}, sum[kRows8][2] = {};  // sum: a row of ones beside V^T
+    float m[kRows8][2], le[kRows8][2];  // reference, log-sum-exp's sums
+#pragma unroll
+    for (int n = 0; n < kRows8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[n][e] = -INFINITY;
+        le[n][e] = 0.f;
+      }
 
 #pragma unroll 1
     for (int j = 0; j < nb; ++j) {
@@ -202,70 +236,80 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
         const uint8_t* ahead = block_at(j + 2);
         if (lane < 20 && ((j + 2) & 31) >= 2 && j + 2 < nb) asm volatile("prefetch.global.L2 [%0];" ::"l"(ahead + lane * 128));
       }
-      // four chains of products, two per eight tokens
-      float sc[2][4] = {}, sd[2][4] = {};
+      float sc[2][4] = {};  // two chains of products: of the two eights of rows, or one's even and odd steps
+      {
+        const uint32_t s0 = __byte_perm(kp[0], 0, 0x1010), z0 = __byte_perm(kp[0], 0, 0x3232);
+        const uint32_t s1 = __byte_perm(kp[1], 0, 0x1010), z1 = __byte_perm(kp[1], 0, 0x3232);
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t w0 = w == 0 ? kc[0].x : (w == 1 ? kc[0].y : (w == 2 ? kc[0].z : kc[0].w));
+          const uint32_t w1 = w == 0 ? kc[1].x : (w == 1 ? kc[1].y : (w == 2 ? kc[1].z : kc[1].w));
+          const uint32_t a[4] = {qc_decode<0>(w0, s0, z0, sixteen), qc_decode<0>(w1, s1, z1, sixteen),
+                                 qc_decode<1>(w0, s0, z0, sixteen), qc_decode<1>(w1, s1, z1, sixteen)};
+          const uint32_t b[4] = {qc_decode<2>(w0, s0, z0, sixteen), qc_decode<2>(w1, s1, z1, sixteen),
+                                 qc_decode<3>(w0, s0, z0, sixteen), qc_decode<3>(w1, s1, z1, sixteen)};
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const uint32_t s2 = __byte_perm(kp[nt], 0, 0x1010), z2 = __byte_perm(kp[nt], 0, 0x3232);
-          const uint32_t w4 = w == 0 ? kc[nt].x : (w == 1 ? kc[nt].y : (w == 2 ? kc[nt].z : kc[nt].w));
-          mma16816(sc[nt], q[2 * w], qc_decode<0>(w4, s2, z2, p.sixteen), qc_decode<1>(w4, s2, z2, p.sixteen));
-          mma16816(sd[nt], q[2 * w + 1], qc_decode<2>(w4, s2, z2, p.sixteen), qc_decode<3>(w4, s2, z2, p.sixteen));
+          for (int n = 0; n < kRows8; ++n) {
+            mma16816(sc[n], a, q[n][2 * w][0], q[n][2 * w][1]);
+            mma16816(sc[kRows8 == 1 ? 1 : n], b, q[n][2 * w + 1][0], q[n][2 * w + 1][1]);
+          }
         }
+      }
+      if (kRows8 == 1) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[nt][k] += sd[nt][k];
-      load_k(next);
+        for (int k = 0; k < 4; ++k) sc[0][k] += sc[1][k];
+      }
       if (left < QC_ROWS) {  // tokens behind the end: no score, and value 0 whatever the page holds there
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (t + 4 * i >= left) {
-            sc[i >> 1][i & 1] = sc[i >> 1][2 + (i & 1)] = -INFINITY;
-            vp[i] = 0;
+        for (int i = 0; i < 4; ++i) {
+          if (t + 4 * i >= left) vp[i] = 0;
+          if (ktok + 8 * (i >> 1) >= left) {
+#pragma unroll
+            for (int n = 0; n < kRows8; ++n) sc[n][i] = -INFINITY;
+          }
+        }
+      }
+      bool above = false;
+#pragma unroll
+      for (int n = 0; n < kRows8; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) above |= fmaxf(sc[n][e], sc[n][2 + e]) * p.scale_log2 > m[n][e] + QT_THRESHOLD;
+      }
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int n = 0; n < kRows8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(fmaxf(sc[n][e], sc[n][2 + e]) * p.scale_log2, m[n][e]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            const float f = m[n][e] == -INFINITY ? 0.f : ex2(m[n][e] - x);
+            le[n][e] *= f;
+            sum[n][e] *= f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[n][i][e] *= f;
+              o[n][i][2 + e] *= f;
+            }
+            m[n][e] = x;
           }
       }
-      const float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])) * p.scale_log2;
-      const float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])) * p.scale_log2;
-      if (__any_sync(0xffffffffu, x0 > m0 + QT_THRESHOLD || x1 > m1 + QT_THRESHOLD)) {
-        float n0 = fmaxf(x0, m0), n1 = fmaxf(x1, m1);
+      uint32_t pr[kRows8][2];  // P^T: rows of tokens, then of query rows
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-          n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
-          n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, d));
+      for (int n = 0; n < kRows8; ++n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // (no reference yet: 0)
+          sc[n][k] = ex2(fmaf(sc[n][k], p.scale_log2, m[n][k & 1] == -INFINITY ? 0.f : -m[n][k & 1]));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) pr[n][h] = transpose8x8(pack_bf16x2(sc[n][2 * h], sc[n][2 * h + 1]));
+        if (p.lse) {
+          le[n][0] += sc[n][0] + sc[n][2];
+          le[n][1] += sc[n][1] + sc[n][3];
         }
-        const float a0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), a1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
-        le0 *= a0;
-        le1 *= a1;
-        sum[0] *= a0;
-        sum[2] *= a1;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          o[i][0] *= a0;
-          o[i][1] *= a0;
-          o[i][2] *= a1;
-          o[i][3] *= a1;
-        }
-        m0 = n0;
-        m1 = n1;
-        u0 = m0 == -INFINITY ? 0.f : m0;
-        u1 = m1 == -INFINITY ? 0.f : m1;
+        mma_sums(sum[n], pr[n][0], pr[n][1]);
       }
-      uint32_t pr[4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[nt][k] = ex2(fmaf(sc[nt][k], p.scale_log2, k < 2 ? -u0 : -u1));
-        pr[2 * nt] = pack_bf16x2(sc[nt][0], sc[nt][1]);
-        pr[2 * nt + 1] = pack_bf16x2(sc[nt][2], sc[nt][3]);
-      }
-      if (p.lse) {
-        le0 += (sc[0][0] + sc[0][1]) + (sc[1][0] + sc[1][1]);
-        le1 += (sc[0][2] + sc[0][3]) + (sc[1][2] + sc[1][3]);
-      }
-      mma16816(sum, pr, 0x3F803F80u, 0x3F803F80u);
-      // O += P V: column g of product n is element 16 g + n
+      if (kRows8 == 1) load_k(next);  // (later with 16 rows: they have no registers to spare)
+      // O^T += V^T P^T: rows g and g + 8 of product 2 quad + c are elements 16g + 4 quad + 2c and the next
       const uint32_t sa = __byte_perm(vp[0], vp[1], 0x5410), za = __byte_perm(vp[0], vp[1], 0x7632);
       const uint32_t sb = __byte_perm(vp[2], vp[3], 0x5410), zb = __byte_perm(vp[2], vp[3], 0x7632);
 #pragma unroll
@@ -273,64 +317,74 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
         const uint32_t sel = (quad & 1) ? 0x7632u : 0x5410u;
         const uint32_t a = quad < 2 ? __byte_perm(vc[0].x, vc[1].x, sel) : __byte_perm(vc[0].y, vc[1].y, sel);
         const uint32_t b = quad < 2 ? __byte_perm(vc[2].x, vc[3].x, sel) : __byte_perm(vc[2].y, vc[3].y, sel);
-        mma16816(o[4 * quad + 0], pr, qc_decode<0>(a, sa, za, p.sixteen), qc_decode<0>(b, sb, zb, p.sixteen));
-        mma16816(o[4 * quad + 1], pr, qc_decode<1>(a, sa, za, p.sixteen), qc_decode<1>(b, sb, zb, p.sixteen));
-        mma16816(o[4 * quad + 2], pr, qc_decode<2>(a, sa, za, p.sixteen), qc_decode<2>(b, sb, zb, p.sixteen));
-        mma16816(o[4 * quad + 3], pr, qc_decode<3>(a, sa, za, p.sixteen), qc_decode<3>(b, sb, zb, p.sixteen));
+        const uint32_t x[4] = {qc_decode<0>(a, sa, za, sixteen), qc_decode<1>(a, sa, za, sixteen),
+                               qc_decode<0>(b, sb, zb, sixteen), qc_decode<1>(b, sb, zb, sixteen)};
+        const uint32_t y[4] = {qc_decode<2>(a, sa, za, sixteen), qc_decode<3>(a, sa, za, sixteen),
+                               qc_decode<2>(b, sb, zb, sixteen), qc_decode<3>(b, sb, zb, sixteen)};
+#pragma unroll
+        for (int n = 0; n < kRows8; ++n) {
+          mma16816(o[n][2 * quad], x, pr[n][0], pr[n][1]);
+          mma16816(o[n][2 * quad + 1], y, pr[n][0], pr[n][1]);
+        }
       }
+      if (kRows8 == 2) load_k(next);
       load_v(next);
     }
 
     // ---- join the warps: rows' sums, references and O through shared memory
-    le0 += __shfl_xor_sync(0xffffffffu, le0, 1);
-    le1 += __shfl_xor_sync(0xffffffffu, le1, 1);
-    le0 += __shfl_xor_sync(0xffffffffu, le0, 2);
-    le1 += __shfl_xor_sync(0xffffffffu, le1, 2);
-    if (t == 0) {
-      s.m[warp][g] = m0;
-      s.m[warp][g + 8] = m1;
-      s.l[warp][g] = sum[0];
-      s.l[warp][g + 8] = sum[2];
-      s.le[warp][g] = le0;
-      s.le[warp][g + 8] = le1;
-    }
-    float4* ow = reinterpret_cast<float4*>(qt_sm + warp * QT_WARP_BYTES);
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int n = 0; n < kRows8; ++n)
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {  // elements 32 t + 4 c ..: products 4 (c % 4) .., column 2t (c < 4) or 2t + 1
-        const int r = g + 8 * half, k = 2 * half + (c >> 2), i = 4 * (c & 3);
-        ow[r * 32 + o_piece(r, t * 8 + c)] = make_float4(o[i][k], o[i + 1][k], o[i + 2][k], o[i + 3][k]);
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) le[n][e] += __shfl_xor_sync(0xffffffffu, le[n][e], d);
+        if (g == 0) {
+          s.m[warp][8 * n + 2 * t + e] = m[n][e];
+          s.l[warp][8 * n + 2 * t + e] = sum[n][e];
+          s.le[warp][8 * n + 2 * t + e] = le[n][e];
+        }
       }
+    float4* ow = reinterpret_cast<float4*>(qt_sm + warp * kWarpBytes);
+#pragma unroll
+    for (int n = 0; n < kRows8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int quad = 0; quad < 4; ++quad) {
+          const int r = 8 * n + 2 * t + e;
+          ow[r * 32 + o_piece(r, 4 * g + quad)] =
+              make_float4(o[n][2 * quad][e], o[n][2 * quad][2 + e], o[n][2 * quad + 1][e], o[n][2 * quad + 1][2 + e]);
+        }
     __syncthreads();
-    // a thread joins 4 x 4 elements of row tid / 8
-    const int r = tid >> 3, cc = tid & 7;
+    // a thread joins kPieces x 4 elements of a row
+    constexpr int kPieces = 2 * kRows8, kPer = 32 / kPieces;
+    const int r = tid / kPer, cc = tid % kPer;
     float mm = -INFINITY, ll = 0.f, ee = 0.f;
 #pragma unroll
     for (int w = 0; w < QT_WARPS; ++w) mm = fmaxf(mm, s.m[w][r]);
-    float4 acc[4] = {};
+    float4 acc[kPieces] = {};
 #pragma unroll
     for (int w = 0; w < QT_WARPS; ++w) {
       const float mw = s.m[w][r];
       const float f = mw == -INFINITY ? 0.f : ex2(mw - mm);
       ll += s.l[w][r] * f;
       ee += s.le[w][r] * f;
-      const float4* src = reinterpret_cast<const float4*>(qt_sm + w * QT_WARP_BYTES);
+      const float4* src = reinterpret_cast<const float4*>(qt_sm + w * kWarpBytes);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) add_scaled(acc[k], src[r * 32 + o_piece(r, 8 * k + cc)], f);
+      for (int k = 0; k < kPieces; ++k) add_scaled(acc[k], src[r * 32 + o_piece(r, kPer * k + cc)], f);
     }
     bool write = ns == 1;
     if (!write) {
       // partial rows [r][128], then reference and sums
       const int first = part.first;
-      float* mine = p.part + static_cast<int64_t>(part.slot) * QT_PART;
+      float* mine = p.part + static_cast<int64_t>(part.slot) * kPart;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) __stcg(reinterpret_cast<float4*>(mine) + r * 32 + 8 * k + cc, acc[k]);
+      for (int k = 0; k < kPieces; ++k) __stcg(reinterpret_cast<float4*>(mine) + r * 32 + kPer * k + cc, acc[k]);
       if (cc == 0) {
-        float* ex = mine + QT_ROWS * QC_D + r;
+        float* ex = mine + kRows * QC_D + r;
         __stcg(ex, mm);
-        __stcg(ex + QT_ROWS, ll);
-        __stcg(ex + 2 * QT_ROWS, ee);
+        __stcg(ex + kRows, ll);
+        __stcg(ex + 2 * kRows, ee);
       }
       __threadfence();
       __syncthreads();
@@ -343,28 +397,28 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
       write = s.last != 0;
       if (write) {
         __threadfence();
-        const auto rows = [&](int k) { return p.part + static_cast<int64_t>(qc_slot(first, k)) * QT_PART; };
-        const auto ex = [&](int k) { return rows(k) + QT_ROWS * QC_D + r; };
+        const auto rows = [&](int k) { return p.part + static_cast<int64_t>(qc_slot(first, k)) * kPart; };
+        const auto ex = [&](int k) { return rows(k) + kRows * QC_D + r; };
         mm = -INFINITY;
 #pragma unroll 4
         for (int k = 0; k < ns; ++k) mm = fmaxf(mm, __ldcg(ex(k)));
         ll = ee = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < kPieces; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int sp = 0; sp < ns; ++sp) {
           const float mw = __ldcg(ex(sp));
           const float f = mw == -INFINITY ? 0.f : ex2(mw - mm);
-          ll += __ldcg(ex(sp) + QT_ROWS) * f;
-          ee += __ldcg(ex(sp) + 2 * QT_ROWS) * f;
+          ll += __ldcg(ex(sp) + kRows) * f;
+          ee += __ldcg(ex(sp) + 2 * kRows) * f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            add_scaled(acc[k], __ldcg(reinterpret_cast<const float4*>(rows(sp)) + r * 32 + 8 * k + cc), f);
+          for (int k = 0; k < kPieces; ++k)
+            add_scaled(acc[k], __ldcg(reinterpret_cast<const float4*>(rows(sp)) + r * 32 + kPer * k + cc), f);
         }
       }
     }
     // the row, normalised, to O, and its log-sum-exp.  No tokens: 0 and -inf; NaN stays NaN
-    const int rr = tile * QT_ROWS + r;
+    const int rr = tile * kRows + r;
     if (write && rr < n_rows) {
       const int slot = rr / rows_per_cand;
       const int64_t at =
@@ -372,8 +426,8 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
       const float inv = ll > 0.f ? 1.0f / ll : (ll == 0.f ? 0.f : ll);
       uint2* dst = reinterpret_cast<uint2*>(p.O + at * QC_D);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        dst[8 * k + cc] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+      for (int k = 0; k < kPieces; ++k)
+        dst[kPer * k + cc] = make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
       if (p.lse && cc == 0) p.lse[at] = ee > 0.f ? (mm + __log2f(ee)) * 0.69314718055994531f : (ee == 0.f ? -INFINITY : ee);
     }
     __syncthreads();  // the next item writes the shared rows
@@ -382,17 +436,26 @@ __global__ void __launch_bounds__(QT_THREADS, QT_CTAS_PER_SM) qattn_kernel(const
 
 }  // namespace
 
-int qattn_ctas(int num_sms) { return num_sms * QT_CTAS_PER_SM; }
-size_t qattn_part_elems(int num_sms) { return static_cast<size_t>(QA_SLOTS) * qattn_ctas(num_sms) * QT_PART; }
+// Rows per tile: 8 where no user has more on average.
+int qattn_ctas(int num_sms, bool eight) { return num_sms * qt_ctas_per_sm(eight ? 1 : 2); }
+size_t qattn_part_elems(int num_sms) {
+  return static_cast<size_t>(QA_SLOTS) * num_sms *
+         (qt_ctas_per_sm(1) * qt_part(1) > qt_ctas_per_sm(2) * qt_part(2) ? qt_ctas_per_sm(1) * qt_part(1)
+                                                                          : qt_ctas_per_sm(2) * qt_part(2));
+}
 
-cudaError_t launch_qattn(const QcAttnParams& p, cudaStream_t s) {
-  constexpr size_t rows = QT_WARPS * QT_WARP_BYTES;
-  const size_t smem = rows + sizeof(int64_t) * static_cast<size_t>(p.n_users);
-  cudaError_t e = cudaFuncSetAttribute(qattn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int kRows8>
+static cudaError_t launch(const QcAttnParams& p, cudaStream_t s) {
+  constexpr size_t rows = QT_WARPS * qt_warp_bytes(kRows8);
+  cudaError_t e = cudaFuncSetAttribute(qattn_kernel<kRows8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(rows + sizeof(int64_t) * SEG_MAX_USERS));
   if (e != cudaSuccess) return e;
-  qattn_kernel<<<p.ctas, QT_THREADS, smem, s>>>(p);
+  qattn_kernel<kRows8><<<p.ctas, QT_THREADS, rows + sizeof(int64_t) * static_cast<size_t>(p.n_users), s>>>(p);
   return cudaGetLastError();
+}
+
+cudaError_t launch_qattn(const QcAttnParams& p, bool eight, cudaStream_t s) {
+  return eight ? launch<1>(p, s) : launch<2>(p, s);
 }
 
 }  // namespace ikbo

@@ -14,9 +14,9 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, int num_sms, cudaStream_
 cudaError_t launch_qc_resize(const QcResizeParams& p, cudaStream_t s);
 cudaError_t launch_qc_append(QcAppendParams p, int num_sms, cudaStream_t s);
 cudaError_t launch_qc_load(const QcLoadParams& p, int num_sms, cudaStream_t s);
-int qattn_ctas(int num_sms);
+int qattn_ctas(int num_sms, bool eight);
 size_t qattn_part_elems(int num_sms);
-cudaError_t launch_qattn(const QcAttnParams& p, cudaStream_t s);
+cudaError_t launch_qattn(const QcAttnParams& p, bool eight, cudaStream_t s);
 size_t qattn_tile_smem();
 size_t qattn_tile_part_elems(int num_sms);
 int64_t qattn_tile_items(int64_t rows, int n_users, int H_kv, int num_sms);
@@ -63,24 +63,27 @@ ikbo_status_t check_table(const int32_t* table, const int32_t* lens, int max_blo
 // history's K/V head, R = rows / n_users, and the tokens there may be to read.
 // Measured at 64 users x 8 heads x 4096 tokens, caches cold (us):
 //   R                   8    16    32    64   128
-//   in registers      125   128   199   369     -   (histories decoded once per 16 rows)
-//   in tiles          171   171   171   175   181   (once per 128 rows)
-//   decoded first       -     -     -     -   416
-// 102 users, R = 160, 1150 tokens: tiles 175, decoded first 221; 60 users,
-// R = 546, 2048 tokens: 365 and 336; 15 users, R = 2184: 304 and 225.  So up to
-// 16 rows in registers, from 512 on decoded first, between them in tiles,
-// unless the tile kernel's longer start and end (about 12 us) are not made up
-// for: the register kernel gets through 18000 (16-row tile, token, head)s in a
-// microsecond, the tile kernel through 13500 of 128 rows.
+//   in registers       85   105   190   358   695  (histories decoded once per 8 or 16 rows)
+//   in tiles          126   126   126   130   135  (once per 128 rows)
+// 1024 candidates of 32 queries x 8 heads over 2048 tokens each:
+//   R                 546  1092  2184  4369
+//   in tiles          287   262   255   478 (2048 candidates)
+//   decoded first     338   262   226   396
+// So up to 16 rows in registers, from 1024 on decoded first, between them in
+// tiles, unless the tile kernel's longer start and end (about 12 us) are not
+// made up for: the register kernel gets through 21000 (16-row tile, token,
+// head)s in a microsecond, the tile kernel through 20500 of 128 rows (4
+// candidates of one history of 32000 tokens, 32 rows: 40 and 49 us; 8 of the
+// same with four heads sharing, 256 rows: 169 and 56).
 enum QcAttnVariant { QATTN_REGISTERS = 1, QATTN_TILES = 2, QATTN_DECODED = 3 };
 
 QcAttnVariant qattn_variant(int64_t rows, int n_users, int H_kv, int Lkv) {
   if (rows <= 16 * static_cast<int64_t>(n_users)) return QATTN_REGISTERS;
-  if (rows > 512 * static_cast<int64_t>(n_users)) return QATTN_DECODED;
+  if (rows > 1024 * static_cast<int64_t>(n_users)) return QATTN_DECODED;
   const double tokens = static_cast<double>(Lkv) * H_kv;
   const double r = static_cast<double>(rows) / n_users;
-  const double registers_us = std::ceil(r / 16) * tokens / 18000;
-  const double tiles_us = 12 + std::ceil(r / 128) * tokens / 13500;
+  const double registers_us = std::ceil(r / 16) * tokens / 21000;
+  const double tiles_us = 12 + std::ceil(r / 128) * tokens / 20500;
   return registers_us < tiles_us ? QATTN_REGISTERS : QATTN_TILES;
 }
 
@@ -368,9 +371,10 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
 
   const bool few = variant == QATTN_REGISTERS;
   if (!few && qattn_tile_smem() > p->max_smem) return IKBO_ERR_UNSUPPORTED;
-  const int ctas = few ? qattn_ctas(p->num_sms) : p->num_sms;
+  const bool eight = rows <= 8 * static_cast<int64_t>(n_users);  // rows of a register kernel's tile, or 16
+  const int ctas = few ? qattn_ctas(p->num_sms, eight) : p->num_sms;
   const size_t part = few ? qattn_part_elems(p->num_sms) : qattn_tile_part_elems(p->num_sms);
-  const size_t tickets = static_cast<size_t>(QA_SLOTS) * ctas * (few ? 1 : 8);
+  const size_t tickets = static_cast<size_t>(QA_SLOTS) * p->num_sms * 8;
   const int64_t items = few ? 0 : qattn_tile_items(rows, n_users, H_kv, p->num_sms);
   if (grow_kept(p, &p->d_qa_part, &p->qa_part_elems, part, stream) != cudaSuccess ||
       grow_kept(p, &p->d_qa_tickets, &p->qa_tickets_elems, tickets, stream) != cudaSuccess ||
@@ -405,7 +409,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   ap.scale_log2 = scale * 1.4426950408889634f;
   ap.sixteen = QC_SIXTEEN;
   ap.timeout_ns = p->timeout_ns;
-  if ((few ? launch_qattn(ap, stream) : launch_qattn_tile(ap, stream)) != cudaSuccess)
+  if ((few ? launch_qattn(ap, eight, stream) : launch_qattn_tile(ap, stream)) != cudaSuccess)
     return IKBO_ERR_CUDA;
   p->launches++;
   return IKBO_OK;

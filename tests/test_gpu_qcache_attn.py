@@ -17,7 +17,7 @@ SCALE = 1.0 / math.sqrt(128)
 # The attention's three variants, reached by sizes alone: query rows a user
 # (candidates times Lq) and the bound on the tokens, which may be any.
 VARIANTS = {"registers": dict(c=1, Lq=8, Lkv=None), "tiles": dict(c=12, Lq=24, Lkv=8_000_000),
-            "decoded": dict(c=5, Lq=128, Lkv=2000)}
+            "decoded": dict(c=9, Lq=128, Lkv=2000)}
 each_variant = pytest.mark.parametrize("variant", list(VARIANTS))
 
 
@@ -262,9 +262,9 @@ def test_pages_behind_four_gigabytes():
     table = np.array([[n_pages - 1, n_pages - 7, n_pages - 3]], np.int32)
     slots = table[0][np.arange(300) // page] * page + np.arange(300) % page
     values = [R.values(*R.quantise(x)) for x in (K, V)]
-    with B.Plan(40, 1, H) as p:
+    with B.Plan(48, 1, H) as p:
         p.qcache_append(bf(K), bf(V), i32(slots), data, page)
-        for n, Lq, Lkv in ((1, 8, 300), (24, 8, 1_000_000), (24, 24, 300)):
+        for n, Lq, Lkv in ((1, 8, 300), (24, 8, 1_000_000), (48, 24, 300)):
             m = np.zeros(n, np.int32)
             Q = queries(3, n, H, Lq)
             p.plan(i32(m), 1, H, Lq)
@@ -331,7 +331,7 @@ def test_a_run_of_requests():
 def test_many_users(variant, users, H, most):
     """More users than a warp, a CTA's threads or a list in shared memory hold (1300 x 8 heads: over
     64 items for each CTA), one long history among short and empty ones, users without candidates."""
-    c, Lq = {"registers": (1, 16), "tiles": (2, 24), "decoded": (5, 128)}[variant]
+    c, Lq = {"registers": (1, 16), "tiles": (2, 24), "decoded": (9, 128)}[variant]
     rng = np.random.default_rng(users)
     lens = rng.integers(0, most, users)
     lens[[1, users - 1]] = 0, 1
