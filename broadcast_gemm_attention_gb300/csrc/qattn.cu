@@ -95,7 +95,7 @@ __device__ __forceinline__ QcUserWork user_work(const QcAttnParams& p, int u, in
   const int count = __ldg(p.offsets + u + 1) - __ldg(p.offsets + u);
   w.len = qc_length(p.lens, u, most, bad);
   w.tiles = static_cast<int>((static_cast<int64_t>(count) * p.group * p.Lq + kRows - 1) / kRows);
-  w.units = (w.len + QC_ROWS - 1) / QC_ROWS;
+  w.units = static_cast<int>((static_cast<uint32_t>(w.len) + QC_ROWS - 1) / QC_ROWS);
   return w;
 }
 

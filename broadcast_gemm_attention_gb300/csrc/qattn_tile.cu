@@ -59,7 +59,7 @@ constexpr int STAGE_BYTES = 1024;  // of O, per softmax warp: 32 rows x 16 eleme
 constexpr uint32_t K_AT = 2 * ATT_Q_TILE_BYTES, V_AT = K_AT + 2 * ATT_KV_STAGE_BYTES;
 constexpr uint32_t OUT_AT = V_AT + 2 * ATT_KV_STAGE_BYTES;
 constexpr uint32_t AUX_AT = OUT_AT + 8 * STAGE_BYTES;
-constexpr int NUM_BARS = 6 + 3 * S_BUFS + 8 + 2;
+constexpr int NUM_BARS = 6 + 3 * S_BUFS + 8 + 2 + 2;
 
 constexpr int LIST_NEAR = 64;  // of a CTA's items, kept in shared memory
 
@@ -81,7 +81,7 @@ static_assert((sizeof(int64_t) + sizeof(int32_t)) * SEG_MAX_USERS <= AUX_AT, "th
 struct Smem {
   uint8_t *q, *k, *v, *out;
   uint64_t *q_full, *q_empty, *s_full, *p_full, *pv_done, *o_full, *o_empty, *k_full, *k_empty, *v_full,
-      *v_empty, *fin_full;
+      *v_empty, *fin_full, *drain;
   Aux* x;
 };
 
@@ -105,6 +105,7 @@ __device__ __forceinline__ Smem carve(uint8_t* base) {
   s.v_full = s.k_empty + 2;
   s.v_empty = s.v_full + 2;
   s.fin_full = s.v_empty + 2;
+  s.drain = s.fin_full + 2;
   return s;
 }
 
@@ -143,7 +144,7 @@ __device__ __forceinline__ QcUserWork user_work(const QcAttnParams& p, int u, in
   const int count = __ldg(p.offsets + u + 1) - __ldg(p.offsets + u);
   w.len = qc_length(p.lens, u, most, bad);
   w.tiles = static_cast<int>((static_cast<int64_t>(count) * p.group * p.Lq + ATT_BM - 1) / ATT_BM);
-  w.units = (w.len + ATT_BN - 1) / ATT_BN;
+  w.units = static_cast<int>((static_cast<uint32_t>(w.len) + ATT_BN - 1) / ATT_BN);
   return w;
 }
 
@@ -458,6 +459,16 @@ __device__ void pv_issuer(const QcAttnParams& p, const Smem& s, uint32_t tmem, c
       if (jt + 1 == nt) ++ou;
     }
   }
+}
+
+// After a wait that ran out: an issuer's products in flight end (they need
+// nothing more), or a million looks are over, before the CTA frees their memory.
+__device__ void drain(uint64_t* bar) {
+  __syncwarp();
+  if (elect_one()) mma_commit(bar);
+  __syncwarp();
+  for (int i = 0; i < 1000000 && !mbar_try_wait(bar, 0); ++i) {}
+  __syncwarp();
 }
 
 // ---------------------------------------------------- softmax and epilogue
@@ -861,6 +872,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.fin_full[i], SOFTMAX_THREADS);
+      mbar_init(&s.drain[i], 1);
       mbar_init(&s.q_full[i], 1);
       mbar_init(&s.q_empty[i], 1);
       mbar_init(&s.k_full[i], DECODE_WARPS);
@@ -895,6 +907,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
     else if (warp == 1) s_issuer(p, s, tmem, l);
     else if (warp == 2) pv_issuer(p, s, tmem, l);
     else if (warp == 3) q_loader(p, s, l);
+    if ((warp == 1 || warp == 2) && *const_cast<volatile uint32_t*>(&s.x->abort)) drain(&s.drain[warp - 1]);
   } else if (warp < DECODE_WARP0) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
     softmax_warps(p, s, tmem, l);

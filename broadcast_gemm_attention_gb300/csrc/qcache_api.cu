@@ -75,11 +75,21 @@ ikbo_status_t check_table(const int32_t* table, const int32_t* lens, int max_blo
 // head)s in a microsecond, the tile kernel through 20500 of 128 rows (4
 // candidates of one history of 32000 tokens, 32 rows: 40 and 49 us; 8 of the
 // same with four heads sharing, 256 rows: 169 and 56).
+// (And in tiles where the bound on the tokens is so large, or so loose, that
+// decoded histories would take more than QA_MOST_DECODED bytes.)
 enum QcAttnVariant { QATTN_REGISTERS = 1, QATTN_TILES = 2, QATTN_DECODED = 3 };
+
+constexpr int64_t QA_MOST_DECODED = int64_t{8} << 30;
+
+// Rows of decoded histories, each padded to the attention kernel's key tile.
+int64_t decoded_rows(int n_users, int Lkv) {
+  return (static_cast<int64_t>(Lkv) + static_cast<int64_t>(ATT_BN) * n_users + ATT_BN - 1) / ATT_BN * ATT_BN;
+}
+int64_t decoded_bytes(int n_users, int H_kv, int Lkv) { return decoded_rows(n_users, Lkv) * H_kv * QC_D * 4; }
 
 QcAttnVariant qattn_variant(int64_t rows, int n_users, int H_kv, int Lkv) {
   if (rows <= 16 * static_cast<int64_t>(n_users)) return QATTN_REGISTERS;
-  if (rows > 1024 * static_cast<int64_t>(n_users)) return QATTN_DECODED;
+  if (rows > 1024 * static_cast<int64_t>(n_users) && decoded_bytes(n_users, H_kv, Lkv) <= QA_MOST_DECODED) return QATTN_DECODED;
   const double tokens = static_cast<double>(Lkv) * H_kv;
   const double r = static_cast<double>(rows) / n_users;
   const double registers_us = std::ceil(r / 16) * tokens / 21000;
@@ -329,8 +339,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   const QcAttnVariant variant = qattn_variant(rows, n_users, H_kv, Lkv);
   if (variant == QATTN_DECODED) {
     // decode each history once into padded bf16 rows, then the bf16 kernel
-    const int64_t cap = (static_cast<int64_t>(Lkv) + static_cast<int64_t>(ATT_BN) * n_users + ATT_BN - 1) / ATT_BN * ATT_BN;
-    if (cap > INT32_LIMIT) return IKBO_ERR_UNSUPPORTED;
+    const int64_t cap = decoded_rows(n_users, Lkv);  // (below 2^31: QA_MOST_DECODED)
     const size_t half = static_cast<size_t>(cap) * H_kv * QC_D;
     if (grow_kept(p, &p->d_qa_kv, &p->qa_kv_elems, 2 * half, stream) != cudaSuccess ||
         grow_kept(p, &p->d_qa_ranges, &p->qa_ranges_elems, 2 * static_cast<size_t>(n_users), stream) != cudaSuccess)

@@ -442,20 +442,21 @@ ikbo_status_t ikbo_qcache_load(ikbo_plan_t p, const void* data, int n_pages, int
  *         A larger sum is reported as IKBO_ERR_CACHE; O is then not defined.
  * Rows of a user with no tokens get O = 0, lse = -inf; a candidate whose map
  * value is out of range keeps its rows; rows of a user with a page out of
- * range are not defined (the page is not touched).  What lies in a page behind a history's end is never
- * used.  fp32 scores and softmax, P rounded to bf16 for P.V, fp32
+ * range are not defined (the page is not touched).  What lies in a page behind
+ * a history's end is never used.  fp32 scores and softmax, P rounded to bf16 for P.V, fp32
  * accumulation.  Results repeat bit for bit.
  * Workspaces are the plan's, grown by the first call that needs more (which
  * allocates; under stream capture that call fails with IKBO_ERR_CUDA and
  * allocates nothing, so make one eager call of the largest size first; a
- * captured call stays valid when later ones grow them).  Three variants,
+ * captured call stays valid when later ones grow them).  Calls and replayed
+ * graphs of one plan share them and must not overlap on the GPU.  Three variants,
  * chosen from the sizes (Lkv among them): with few query rows per user and K/V
  * head (16, or a little more over short histories) the 4-bit blocks become
- * operands in registers; with up to about 512 four-bit tiles are decoded in
- * shared memory beside the tensor cores' work, once per 128 rows; with more,
- * histories are decoded once into the workspace (512 bytes per token and head,
- * each history padded to 128 rows) and the kernel of ikbo_attn_forward reads
- * that. */
+ * operands in registers; with up to 1024 they are decoded in shared memory
+ * beside the tensor cores' work, once per 128 rows; with more, and a bound Lkv
+ * that makes it no more than 8 GiB, histories are decoded once into the
+ * workspace (512 bytes per token and head, each history padded to 128 rows) and
+ * the kernel of ikbo_attn_forward reads that. */
 ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void* data, int n_pages, int page,
                                        int H_kv, const int32_t* d_table, int max_blocks, const int32_t* d_lens,
                                        void* O, float* lse, int Lkv, int d, float scale, cudaStream_t stream);

@@ -351,3 +351,17 @@ def test_many_users(variant, users, H, most):
         some = np.flatnonzero((m % max(1, users // 30) == 0) | (m == users - 1) | (m == 1))
         some = np.concatenate([some, np.flatnonzero(m == users // 2)[:5]])
         check(O[some], lse[some], Q[some], st.kv, m[some], H)
+
+
+def test_a_loose_bound_costs_no_workspace():
+    """Many rows a user, and the largest bound there is: no workspace of its size, the same rows."""
+    st = R.Store(13, [300, 7], 2, 16)
+    m = np.repeat(np.arange(2), 9).astype(np.int32)
+    Q = queries(8, m.size, 2, 128)
+    with B.Plan(m.size, 2, 2) as p:
+        p.plan(i32(m), 2, 2, 128)
+        before = torch.cuda.mem_get_info()[0]
+        O, lse = attend(p, Q, st, Lkv=2**31 - 1)
+        assert p.status() == B.IKBO_OK
+        assert before - torch.cuda.mem_get_info()[0] < 2**30
+        check(O, lse, Q, st.kv, m, 2)
