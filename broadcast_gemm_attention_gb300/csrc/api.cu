@@ -243,7 +243,8 @@ ikbo_status_t attn_launch(ikbo_plan_s* p, const AttnCall& c, cudaStream_t stream
   ap.n_units = p->d_n_units;
   ap.kv_offsets = d_kv_offsets;
   ap.kv_lens = c.kv_lens;
-  ap.kv_group = p->H / c.H_kv;
+  const uint32_t group = static_cast<uint32_t>(p->H / c.H_kv);
+  ap.kv_inverse = group == 1 ? 0 : 0xFFFFFFFFu / group + 1;  // exact for heads below 2^32 / group
   ap.O = static_cast<uint16_t*>(O);
   ap.lse = lse;
   ap.status = p->d_status;

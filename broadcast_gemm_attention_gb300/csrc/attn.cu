@@ -227,7 +227,7 @@ __device__ __forceinline__ void load_slots(const AttnParams& p, const Unit& x, Q
 __device__ __forceinline__ void load_kv_tile(const AttnParams& p, const CUtensorMap* tm, uint8_t* dst, uint64_t* bar,
                                              const Unit& x, int jt) {
   if (p.kv_offsets) {
-    const int hk = p.kv_group == 1 ? x.h : x.h / p.kv_group;
+    const int hk = p.kv_inverse ? static_cast<int>(__umulhi(static_cast<uint32_t>(x.h), p.kv_inverse)) : x.h;
     tma_load_3d(dst, tm, bar, 0, hk, x.kv0 + jt * ATT_BN);
     tma_load_3d(dst + HALF_TILE, tm, bar, 64, hk, x.kv0 + jt * ATT_BN);
   } else {
@@ -650,10 +650,8 @@ __device__ void att_softmax(const AttnParams& p, const AttSmem& s, uint32_t tmem
         if (!__all_sync(0xffffffffu, (cw & 0xFFu) == (g & 0xFFu)) && !chain_wait(p, s, ln.r, g, mprev)) return;
         if (jt == 0) mprev = -INFINITY;
         // tcgen05.ld/st are warp-collective: the rescale decision must be
-        // uniform across the warp, so any row that needs it moves all 32.  Rows
-        // behind the tile's last candidate (Lq does not divide 128) hold whatever
-        // shared memory held: they have no vote, or results would not repeat
-        const bool rescale = __any_sync(0xffffffffu, row_in_tile && mx > mprev + RESCALE_THRESHOLD);
+        // uniform across the warp, so any row that needs it moves all 32
+        const bool rescale = __any_sync(0xffffffffu, mx > mprev + RESCALE_THRESHOLD);
         const float mj = rescale ? chain_value(fmaxf(mprev, mx)) : mprev;
         chain_post(s, ln.r, g + 1, mj);
         if (mj != mref) {  // this group's sum follows the reference (l = 0 on its first tile)
@@ -790,6 +788,17 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
     for (int r = 0; r < ATT_BM; ++r) s.chain[r] = 0;  // tag 0: no tile has posted (tags start at 1)
     *s.abort = 0;
     fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  // Rows behind the tile's last candidate (Lq does not divide 128) are never
+  // loaded.  They have a vote in moving their warp's reference, so they hold
+  // zeros, not what the launch before left, or results would not repeat.
+  const int used = p.cands_per_tile * p.Lq;
+  if (used < ATT_BM) {
+    for (int i = threadIdx.x; i < (ATT_BM - used) * 32; i += ATT_THREADS) {
+      const int r = used + (i >> 5), half = (i >> 4) & 1, buf = (i >> 3) & 1;
+      *reinterpret_cast<uint4*>(s.q + buf * ATT_Q_TILE_BYTES + half * HALF_TILE + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
     fence_proxy_async_smem();
   }
   if (warp == 0 && lane_id() == 0) {

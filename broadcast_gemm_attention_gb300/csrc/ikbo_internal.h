@@ -157,7 +157,7 @@ struct AttnParams {
   uint32_t* status;
   int n_cand, n_users, H, Lq, Lkv;  // Lkv: dense length (ignored when jagged)
   int cands_per_tile;        // floor(128 / Lq)
-  int kv_group;              // query heads that share a K/V head
+  uint32_t kv_inverse;       // of the query heads that share a K/V head, in 1 / 2^32, rounded up; 0: none shared (a division here took 3% of the kernel)
   float scale_log2;          // scale * log2(e)
   uint64_t timeout_ns;
   // self units (users' own queries against the same K/V), after the work
