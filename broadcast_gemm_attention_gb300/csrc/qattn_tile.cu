@@ -29,9 +29,18 @@
 // piece of a tile adds that piece's splits in order, so results repeat bit for
 // bit whichever CTA that is.
 //
-// What bounds it: the softmax warps and the decode share the four issue slots
-// (about 640 and 500 cycles of each per key tile; the products take 1024
-// cycles of the tensor pipe).
+// What bounds it: not the products (1024 cycles of the tensor pipe per key
+// tile, 46% busy) and hardly the decode (without three quarters of its
+// arithmetic, on wrong results, 7% less time), but each softmax group's chain
+// through its tile, which two groups share: about 1850 cycles per key tile, the
+// pace of attn.cu.  152 tiles of 128 rows over 64 key tiles each (19 histories of
+// 8192, 8 heads): 78.5 us, 520 TFLOP/s; with 4 key tiles each 21 us, of which the
+// work list, the cold instructions and the first loads are about 15.
+// Measured slower: one pass that makes P with the last reference and corrects it
+// where the chain says otherwise, with P beside S in TMEM (89 us: P.V has to be
+// through before the group's next P); codes through shared memory by bulk copies
+// (over a thousand cycles of a producer warp a tile); the epilogue's code copied
+// into five places (ten candidates for 102 users: 207 us against 176).
 #include <cuda_bf16.h>
 
 #include "attn_common.cuh"
