@@ -43,8 +43,9 @@
 // and the 12 warps' own latencies.  One candidate for each of 64 histories of
 // 4096 tokens, 8 heads of 8 queries: 84.6 us, 3.99 TB/s of the cache (0.59 of the
 // measured rate); 16 rows each 105.  Measured slower: 4 CTAs an SM 88.7 us (128
-// registers), 5 CTAs 98.9; 16 rows with the rows as the products' long side was
-// 102, and with 3 CTAs an SM in 168 registers, which spill, 107.
+// registers), 5 CTAs 98.9; the rows as the products' long side 99.9.  For 16
+// rows (histories of 1200 to 4096 tokens) that layout was the faster, 72.3 us
+// against 75.1, and 77.2 with 3 CTAs an SM in 168 registers, which spill.
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"

@@ -34,7 +34,7 @@
 // arithmetic, on wrong results, 7% less time), but each softmax group's chain
 // through its tile, which two groups share: about 1850 cycles per key tile, the
 // pace of attn.cu.  152 tiles of 128 rows over 64 key tiles each (19 histories of
-// 8192, 8 heads): 78.5 us, 520 TFLOP/s; with 4 key tiles each 21 us, of which the
+// 8192, 8 heads): 78.5 us, 1040 TFLOP/s; with 4 key tiles each 21 us, of which the
 // work list, the cold instructions and the first loads are about 15.
 // Measured slower: one pass that makes P with the last reference and corrects it
 // where the chain says otherwise, with P beside S in TMEM (89 us: P.V has to be
