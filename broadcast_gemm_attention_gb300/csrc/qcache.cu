@@ -18,7 +18,7 @@ namespace {
 // that reads the old state (pages taken, slots), then what replaces it.
 // Bound: latency (a launch, one scan, two dependent loads): 15 users growing
 // by 12 tokens each 5.8 us, one user 3.9; with many tokens the slots'
-// bisections: 2048 users, 307200 new tokens, 30 us.
+// bisections: 2048 users with 150 new tokens each, 30 us.
 constexpr int QR_THREADS = 1024;
 
 __device__ __forceinline__ void cluster_sync() {
