@@ -365,3 +365,34 @@ def test_a_loose_bound_costs_no_workspace():
         assert p.status() == B.IKBO_OK
         assert before - torch.cuda.mem_get_info()[0] < 2**30
         check(O, lse, Q, st.kv, m, 2)
+
+
+@pytest.mark.parametrize("variant", ["registers", "tiles"])
+def test_one_long_history(variant):
+    """A history cut into a part for each of a hundred or more CTAs (registers: even parts)."""
+    c, Lq = VARIANTS[variant]["c"], VARIANTS[variant]["Lq"]
+    n = 40_000 if variant == "registers" else 60_000
+    st = R.Store(17, [n], 1, 128)
+    m = np.zeros(c, np.int32)
+    Q = queries(9, c, 1, Lq, big=2.0)
+    with B.Plan(c, 1, 1) as p:
+        p.plan(i32(m), 1, 1, Lq)
+        O, lse = attend(p, Q, st, Lkv=8_000_000)
+        assert p.status() == B.IKBO_OK
+        check(O, lse, Q, st.kv, m, 1)
+        for _ in range(3):
+            assert torch.equal(O, attend(p, Q, st, Lkv=8_000_000)[0])
+
+
+def test_candidates_of_few_users():
+    """Most users have none: the variant goes by the average, so a user's 2000 rows are many tiles of 16."""
+    lens = [20] * 150 + [700] + [5] * 20
+    st = R.Store(18, lens, 2, 16)
+    m = np.concatenate([np.full(125, 150), np.arange(100, 140)]).astype(np.int32)
+    m = np.random.default_rng(2).permutation(m)
+    Q = queries(10, m.size, 2, 16)
+    with B.Plan(m.size, len(lens), 2) as p:
+        p.plan(i32(m), len(lens), 2, 16)
+        O, lse = attend(p, Q, st, Lkv=sum(lens))
+        assert p.status() == B.IKBO_OK
+        check(O, lse, Q, st.kv, m, 2)
