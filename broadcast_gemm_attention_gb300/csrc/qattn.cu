@@ -24,12 +24,13 @@
 // Work: a tile is 8 or 16 rows of one (u, g); its history is cut into parts of
 // whole blocks (16 tokens, 2560 contiguous bytes) where the CTAs' equal shares
 // end.  A CTA works through its share, item by item; its four warps take every
-// fourth block, loading the next block's codes into the
+// fourth block (with an item or more for every warp each has a share of its own
+// instead, which needs no joining of warps), loading the next block's codes into the
 // registers of the one just decoded (no barrier in the loop; the lines of the
 // block after that are asked for in L2), and keep their own running maximum,
-// sum and O in registers.  The warps are joined through shared memory; splits of
-// a tile leave unnormalised partial rows, which the last split's CTA to finish
-// adds in split order (so results repeat bit for bit).
+// sum and O in registers.  The warps are joined through shared memory; parts of
+// a tile leave unnormalised rows, which the last one to finish adds in order (so
+// results repeat bit for bit).
 //
 // Softmax in fp32 in the log2 domain.  The reference maximum moves only when
 // a score exceeds it by more than 2^8 (one vote per block instead of four
@@ -58,6 +59,7 @@ constexpr int QT_WARPS = 4;
 constexpr int QT_THREADS = 32 * QT_WARPS;
 constexpr int QT_MIN_BLOCKS = 4 * QT_WARPS;  // blocks of a split, at least
 constexpr int QT_ITEM_BLOCKS = 24;           // what an item costs beside its blocks, in blocks
+constexpr int QT_SOLO_MIN_BLOCKS = 8, QT_SOLO_ITEM_BLOCKS = 4;  // the same where warps work alone
 constexpr float QT_THRESHOLD = 8.0f;         // log2 units
 constexpr int QT_EXTRA = 3;                  // per row besides O: reference, sum, sum of the log-sum-exp
 
@@ -119,24 +121,126 @@ __device__ __forceinline__ void add_scaled(float4& a, const float4 x, float f) {
   a.w = fmaf(x.w, f, a.w);
 }
 
+// A warp that works alone: its rows (lane (g, t): elements 16g .. 16g + 15 of
+// rows 2t and 2t + 1 of each eight) to O, or as a part's rows to its slot, where
+// the last of the parts adds them in order.
 template <int kRows8>
+__device__ __forceinline__ void solo_rows(const QcAttnParams& p, const QcPart& part,
+                                          float (&o)[kRows8][8][4], float (&m)[kRows8][2], float (&sum)[kRows8][2],
+                                          float (&le)[kRows8][2], int tile, int hk, int seg, int n_rows, int rows_per_cand) {
+  constexpr int kRows = 8 * kRows8, kPart = qt_part(kRows8);
+  const int lane = static_cast<int>(threadIdx.x) & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < kRows8; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) le[n][e] += __shfl_xor_sync(0xffffffffu, le[n][e], d);
+  if (part.ns > 1) {
+    float* mine = p.part + static_cast<int64_t>(part.slot) * kPart;
+#pragma unroll
+    for (int n = 0; n < kRows8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
+#pragma unroll
+        for (int quad = 0; quad < 4; ++quad)
+          __stcg(reinterpret_cast<float4*>(mine) + r * 32 + 4 * g + quad,
+                 make_float4(o[n][2 * quad][e], o[n][2 * quad][2 + e], o[n][2 * quad + 1][e], o[n][2 * quad + 1][2 + e]));
+        if (g == 0) {
+          float* ex = mine + kRows * QC_D + r;
+          __stcg(ex, m[n][e]);
+          __stcg(ex + kRows, sum[n][e]);
+          __stcg(ex + 2 * kRows, le[n][e]);
+        }
+      }
+    __threadfence();
+    __syncwarp();
+    uint32_t last = 0;
+    if (lane == 0) {
+      last = atomicAdd(p.tickets + part.first, 1u) + 1 == static_cast<uint32_t>(part.ns);
+      if (last) p.tickets[part.first] = 0;  // zero again for the next call
+    }
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __threadfence();
+    const auto rows = [&](int k) { return p.part + static_cast<int64_t>(qc_slot(part.first, k)) * kPart; };
+#pragma unroll
+    for (int n = 0; n < kRows8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
+        float mm = -INFINITY;
+#pragma unroll 4
+        for (int k = 0; k < part.ns; ++k) mm = fmaxf(mm, __ldcg(rows(k) + kRows * QC_D + r));
+        float ll = 0.f, ee = 0.f;
+        float4 acc[4] = {};
+#pragma unroll 2
+        for (int k = 0; k < part.ns; ++k) {
+          const float* ex = rows(k) + kRows * QC_D + r;
+          const float mw = __ldcg(ex);
+          const float f = mw == -INFINITY ? 0.f : ex2(mw - mm);
+          ll += __ldcg(ex + kRows) * f;
+          ee += __ldcg(ex + 2 * kRows) * f;
+#pragma unroll
+          for (int quad = 0; quad < 4; ++quad)
+            add_scaled(acc[quad], __ldcg(reinterpret_cast<const float4*>(rows(k)) + r * 32 + 4 * g + quad), f);
+        }
+        m[n][e] = mm;
+        sum[n][e] = ll;
+        le[n][e] = ee;
+#pragma unroll
+        for (int quad = 0; quad < 4; ++quad) {
+          o[n][2 * quad][e] = acc[quad].x;
+          o[n][2 * quad][2 + e] = acc[quad].y;
+          o[n][2 * quad + 1][e] = acc[quad].z;
+          o[n][2 * quad + 1][2 + e] = acc[quad].w;
+        }
+      }
+  }
+  // normalised, to O, and the log-sum-exp.  No tokens: 0 and -inf; NaN stays NaN
+#pragma unroll
+  for (int n = 0; n < kRows8; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr = tile * kRows + 8 * n + 2 * t + e;
+      if (rr >= n_rows) continue;
+      const int slot = rr / rows_per_cand;
+      const int64_t at =
+          (static_cast<int64_t>(__ldg(p.perm + seg + slot)) * p.H + hk * p.group) * p.Lq + (rr - slot * rows_per_cand);
+      const float l = sum[n][e], inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+      uint4* dst = reinterpret_cast<uint4*>(p.O + at * QC_D + 16 * g);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        dst[h] = make_uint4(pack_bf16x2(o[n][4 * h][e] * inv, o[n][4 * h][2 + e] * inv),
+                            pack_bf16x2(o[n][4 * h + 1][e] * inv, o[n][4 * h + 1][2 + e] * inv),
+                            pack_bf16x2(o[n][4 * h + 2][e] * inv, o[n][4 * h + 2][2 + e] * inv),
+                            pack_bf16x2(o[n][4 * h + 3][e] * inv, o[n][4 * h + 3][2 + e] * inv));
+      if (p.lse && g == 0)
+        p.lse[at] = le[n][e] > 0.f ? (m[n][e] + __log2f(le[n][e])) * 0.69314718055994531f
+                                   : (le[n][e] == 0.f ? -INFINITY : le[n][e]);
+    }
+}
+
+template <int kRows8, bool kSolo>
 __global__ void __launch_bounds__(QT_THREADS, qt_ctas_per_sm(kRows8)) qattn_kernel(const QcAttnParams p) {
+  constexpr int kWarps = kSolo ? 1 : QT_WARPS;  // that share an item
   constexpr int kRows = 8 * kRows8, kPart = qt_part(kRows8), kWarpBytes = qt_warp_bytes(kRows8);
   extern __shared__ __align__(128) uint8_t qt_sm[];
   __shared__ QtShared s;
-  int64_t* cost0 = reinterpret_cast<int64_t*>(qt_sm + QT_WARPS * kWarpBytes);  // [n_users] cost of the items before a user's
+  int64_t* cost0 = reinterpret_cast<int64_t*>(qt_sm + (kSolo ? 0 : QT_WARPS * kWarpBytes));  // [n_users] cost of the items before a user's
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int64_t most = (static_cast<int64_t>(p.max_blocks) << p.blocks_log2) * QC_ROWS;
 
-  const QcShares sh = qc_shares<QT_THREADS, QT_MIN_BLOCKS, QT_ITEM_BLOCKS>(
-      p, [&](int u, bool& bad) { return user_work<kRows>(p, u, most, bad); }, cost0, nullptr, s.shares);
+  constexpr int kMin = kSolo ? QT_SOLO_MIN_BLOCKS : QT_MIN_BLOCKS;
+  const QcShares sh = qc_shares<QT_THREADS, kMin, kSolo ? QT_SOLO_ITEM_BLOCKS : QT_ITEM_BLOCKS>(
+      p, p.ctas * (QT_WARPS / kWarps), [&](int u, bool& bad) { return user_work<kRows>(p, u, most, bad); }, cost0, nullptr, s.shares);
   bool ignored = false;
   const uint32_t sixteen = p.sixteen;
   const int rows_per_cand = p.group * p.Lq;
   const int64_t page_bytes = (static_cast<int64_t>(p.H_kv) << p.blocks_log2) * QC_BLOCK_BYTES;
 
-  const int cta = static_cast<int>(blockIdx.x);
+  const int cta = kSolo ? static_cast<int>(blockIdx.x) * QT_WARPS + warp : static_cast<int>(blockIdx.x);
   const int64_t end = cta < sh.parts ? sh.start(cta + 1) : 0;
   for (int64_t at = cta < sh.parts ? sh.start(cta) : 0; at < end;) {
     const int u = qc_find(cost0, p.n_users, at);
@@ -147,11 +251,11 @@ __global__ void __launch_bounds__(QT_THREADS, qt_ctas_per_sm(kRows8)) qattn_kern
     const int64_t pos = cost0[u] + static_cast<int64_t>(local) * cost;
     at = pos + cost;  // the next item
     const int hk = local / uw.tiles, tile = local - hk * uw.tiles;
-    const QcPart part = qc_part<QT_MIN_BLOCKS>(sh, uw, pos);
+    const QcPart part = qc_part<kMin>(sh, cta, uw, pos);
     if (uw.units > 0 && part.nt == 0) continue;
     const int ns = part.ns;
-    const int b0 = part.t0 + warp, b1 = part.t0 + part.nt;
-    const int nb = b1 > b0 ? (b1 - b0 + QT_WARPS - 1) / QT_WARPS : 0;  // this warp's blocks
+    const int b0 = part.t0 + (kSolo ? 0 : warp), b1 = part.t0 + part.nt;
+    const int nb = b1 > b0 ? (b1 - b0 + kWarps - 1) / kWarps : 0;  // this warp's blocks
     const int seg = __ldg(p.offsets + u), count = __ldg(p.offsets + u + 1) - seg;
     const int n_rows = count * rows_per_cand;
 
@@ -163,7 +267,7 @@ __global__ void __launch_bounds__(QT_THREADS, qt_ctas_per_sm(kRows8)) qattn_kern
     const auto place = [&](int j) {
       mine = head;
       if (j < nb) {
-        const int b = b0 + j * QT_WARPS;
+        const int b = b0 + j * kWarps;
         const int id = __ldg(table + (b >> p.blocks_log2));
         if (id >= 0 && id < p.n_pages) mine = head + id * page_bytes + (b & ((1 << p.blocks_log2) - 1)) * QC_BLOCK_BYTES;
         else atomicOr(p.status, DEV_ERR_CACHE);
@@ -238,7 +342,7 @@ __global__ void __launch_bounds__(QT_THREADS, qt_ctas_per_sm(kRows8)) qattn_kern
 
 #pragma unroll 1
     for (int j = 0; j < nb; ++j) {
-      const int left = len - (b0 + j * QT_WARPS) * QC_ROWS;  // tokens of the block that exist, if below 16
+      const int left = len - (b0 + j * kWarps) * QC_ROWS;  // tokens of the block that exist, if below 16
       if (((j + 1) & 31) == 0) place(j + 1 + lane);
       const uint8_t* next = block_at(j + 1);
       {  // the lines of the block after the next (of those whose address is at hand)
@@ -340,6 +444,10 @@ __global__ void __launch_bounds__(QT_THREADS, qt_ctas_per_sm(kRows8)) qattn_kern
       load_v(next);
     }
 
+    if (kSolo) {
+      solo_rows<kRows8>(p, part, o, m, sum, le, tile, hk, seg, n_rows, rows_per_cand);
+      continue;
+    }
     // ---- join the warps: rows' sums, references and O through shared memory
 #pragma unroll
     for (int n = 0; n < kRows8; ++n)
@@ -448,23 +556,24 @@ __global__ void __launch_bounds__(QT_THREADS, qt_ctas_per_sm(kRows8)) qattn_kern
 // Rows per tile: 8 where no user has more on average.
 int qattn_ctas(int num_sms, bool eight) { return num_sms * qt_ctas_per_sm(eight ? 1 : 2); }
 size_t qattn_part_elems(int num_sms) {
-  return static_cast<size_t>(QA_SLOTS) * num_sms *
-         (qt_ctas_per_sm(1) * qt_part(1) > qt_ctas_per_sm(2) * qt_part(2) ? qt_ctas_per_sm(1) * qt_part(1)
-                                                                          : qt_ctas_per_sm(2) * qt_part(2));
+  constexpr int a = qt_ctas_per_sm(1) * qt_part(1), b = qt_ctas_per_sm(2) * qt_part(2);
+  return static_cast<size_t>(QA_SLOTS) * num_sms * QT_WARPS * (a > b ? a : b);
 }
+size_t qattn_tickets(int num_sms) { return static_cast<size_t>(QA_SLOTS) * num_sms * QT_WARPS * qt_ctas_per_sm(1); }
 
-template <int kRows8>
+template <int kRows8, bool kSolo>
 static cudaError_t launch(const QcAttnParams& p, cudaStream_t s) {
-  constexpr size_t rows = QT_WARPS * qt_warp_bytes(kRows8);
-  cudaError_t e = cudaFuncSetAttribute(qattn_kernel<kRows8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  constexpr size_t rows = kSolo ? 0 : QT_WARPS * qt_warp_bytes(kRows8);
+  cudaError_t e = cudaFuncSetAttribute(qattn_kernel<kRows8, kSolo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(rows + sizeof(int64_t) * SEG_MAX_USERS));
   if (e != cudaSuccess) return e;
-  qattn_kernel<kRows8><<<p.ctas, QT_THREADS, rows + sizeof(int64_t) * static_cast<size_t>(p.n_users), s>>>(p);
+  qattn_kernel<kRows8, kSolo><<<p.ctas, QT_THREADS, rows + sizeof(int64_t) * static_cast<size_t>(p.n_users), s>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_qattn(const QcAttnParams& p, bool eight, cudaStream_t s) {
-  return eight ? launch<1>(p, s) : launch<2>(p, s);
+cudaError_t launch_qattn(const QcAttnParams& p, bool eight, bool solo, cudaStream_t s) {
+  if (solo) return eight ? launch<1, true>(p, s) : launch<2, true>(p, s);
+  return eight ? launch<1, false>(p, s) : launch<2, false>(p, s);
 }
 
 }  // namespace ikbo

@@ -164,7 +164,7 @@ __device__ List make_list(const QcAttnParams& p, uint8_t* sm, Aux& x) {
   int32_t* item0 = reinterpret_cast<int32_t*>(cost0 + n);
   const int64_t most = (static_cast<int64_t>(p.max_blocks) << p.blocks_log2) * QC_ROWS;
   const QcShares sh = qc_shares<TL_THREADS, TL_MIN_TILES, TL_ITEM_TILES>(
-      p, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, cost0, item0, x.shares);
+      p, p.ctas, [&](int u, bool& bad) { return user_work(p, u, most, bad); }, cost0, item0, x.shares);
   List l = {x.list, p.list, 0};
   bool ignored = false;
   const int cta = static_cast<int>(blockIdx.x);
@@ -187,7 +187,7 @@ __device__ List make_list(const QcAttnParams& p, uint8_t* sm, Aux& x) {
         atomicOr(p.status, DEV_ERR_BAD_WORK);
         break;
       }
-      const QcPart part = qc_part<TL_MIN_TILES>(sh, w, pos);
+      const QcPart part = qc_part<TL_MIN_TILES>(sh, cta, w, pos);
       const int hk = static_cast<int>(static_cast<uint32_t>(local) / static_cast<uint32_t>(w.tiles));
       const int seg = __ldg(p.offsets + u);
       int rows = (__ldg(p.offsets + u + 1) - seg) * p.group * p.Lq;

@@ -2,6 +2,7 @@
 // attention that reads it (declared in ikbo.h): argument checks, workspaces
 // and launches.  No computation of the method happens on the host but a
 // rotation's table of frequencies, formed once.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -16,7 +17,8 @@ cudaError_t launch_qc_append(QcAppendParams p, int num_sms, cudaStream_t s);
 cudaError_t launch_qc_load(const QcLoadParams& p, int num_sms, cudaStream_t s);
 int qattn_ctas(int num_sms, bool eight);
 size_t qattn_part_elems(int num_sms);
-cudaError_t launch_qattn(const QcAttnParams& p, bool eight, cudaStream_t s);
+size_t qattn_tickets(int num_sms);
+cudaError_t launch_qattn(const QcAttnParams& p, bool eight, bool solo, cudaStream_t s);
 size_t qattn_tile_smem();
 size_t qattn_tile_part_elems(int num_sms);
 int64_t qattn_tile_items(int64_t rows, int n_users, int H_kv, int num_sms);
@@ -383,7 +385,13 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   const bool eight = rows <= 8 * static_cast<int64_t>(n_users);  // rows of a register kernel's tile, or 16
   const int ctas = few ? qattn_ctas(p->num_sms, eight) : p->num_sms;
   const size_t part = few ? qattn_part_elems(p->num_sms) : qattn_tile_part_elems(p->num_sms);
-  const size_t tickets = static_cast<size_t>(QA_SLOTS) * p->num_sms * 8;
+  // In registers, warps work alone where there is an item for each; with fewer,
+  // a CTA's four share one and join in shared memory.  Measured, four together
+  // and alone: 1000 users of 30 to 100 tokens, 8 heads 91 and 52 us, 300 of 150 to
+  // 500 56 and 52, 1024 of 600 to 2048 396 and 357; 64 of 1200 to 4096 62 and 64,
+  // one of 1000 15 and 23.
+  const bool solo = rows * H_kv >= static_cast<int64_t>(eight ? 8 : 16) * 4 * ctas;
+  const size_t tickets = std::max(static_cast<size_t>(QA_SLOTS) * p->num_sms * 8, qattn_tickets(p->num_sms));
   const int64_t items = few ? 0 : qattn_tile_items(rows, n_users, H_kv, p->num_sms);
   if (grow_kept(p, &p->d_qa_part, &p->qa_part_elems, part, stream) != cudaSuccess ||
       grow_kept(p, &p->d_qa_tickets, &p->qa_tickets_elems, tickets, stream) != cudaSuccess ||
@@ -418,7 +426,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   ap.scale_log2 = scale * 1.4426950408889634f;
   ap.sixteen = QC_SIXTEEN;
   ap.timeout_ns = p->timeout_ns;
-  if ((few ? launch_qattn(ap, eight, stream) : launch_qattn_tile(ap, stream)) != cudaSuccess)
+  if ((few ? launch_qattn(ap, eight, solo, stream) : launch_qattn_tile(ap, stream)) != cudaSuccess)
     return IKBO_ERR_CUDA;
   p->launches++;
   return IKBO_OK;

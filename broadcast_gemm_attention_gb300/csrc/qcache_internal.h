@@ -33,8 +33,8 @@ constexpr int QC_HALF_BYTES = 1280;    // keys' or values' codes and pairs
 constexpr int QC_CODE_BYTES = 1024;    // 16 x 64 bytes of codes, then 16 x 4 pairs (s, z) of two bf16
 constexpr int QC_MAX_PAGE = 1024;
 
-// Slots for partial rows per CTA of an attention launch: its share of the work
-// begins and ends within an item.
+// Slots for partial rows per worker (CTA or warp) of an attention launch: its
+// share of the work begins and ends within an item.
 constexpr int QA_SLOTS = 2;
 
 struct QcResizeParams {
@@ -85,7 +85,7 @@ struct QcAttnParams {
   const int32_t* lens;
   const int32_t* offsets;  // the plan's segments
   const int32_t* perm;
-  float* part;             // [QA_SLOTS * ctas] splits' partial rows: unnormalised O, reference and sums
+  float* part;             // [QA_SLOTS * workers] parts' rows: unnormalised O, reference and sums
   uint32_t* tickets;       // one per slot of part (tiles of 128 rows: 8 each)
   int4* list;              // tiles of 128 rows: the work list, three per item
   int64_t max_items;
@@ -157,10 +157,10 @@ __device__ __forceinline__ T qc_warp_scan(T x) {
 // An item is (user, K/V head, tile of query rows), in that order; its length is
 // the history's units (blocks or key tiles), and its cost that and `overhead`
 // units more (1 where there are no tokens).  All items' costs in a row are cut
-// into as many equal shares as there are CTAs, so a CTA has a run of items, of
-// which the first and the last may be parts: every CTA works for the same time
-// (to the rows that a tile lacks), there are no more parts than items and CTAs,
-// and parts of one item always lie in consecutive CTAs.  (Whole items dealt out
+// into as many equal shares as there are workers (CTAs, or single warps), so each has a run of items,
+// of which the first and the last may be parts: every worker has the same to do
+// (to the rows that a tile lacks), there are no more parts than items and
+// workers, and parts of one item always lie with consecutive workers.  (Whole items dealt out
 // in turn, with histories cut to one length that fills the CTAs best, took 10%
 // to 25% longer where histories differ.)
 //
@@ -172,12 +172,13 @@ struct QcUserWork {
 };
 struct QcShares {
   int64_t base;         // start(b) = b base + b rest / parts
-  int parts, rest;      // shares (at most the launch's CTAs), items' costs beside base parts
+  int parts, rest;      // shares (at most the launch's workers), items' costs beside base parts
   int overhead, chunk;  // chunk > 0: even parts
-  // The quotient is of numbers below 2^18 by one below 2^9: with a half added it
-  // is further from a whole number than an fp32 quotient's error.
   __device__ __forceinline__ int64_t start(int b) const {
-    return b * base + static_cast<int>(__fdividef(static_cast<float>(b * rest) + 0.5f, static_cast<float>(parts)));
+    const int x = b * rest;  // (both below parts, of which there are at most a few thousand)
+    int q = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(parts)));
+    q += (q + 1) * parts <= x ? 1 : (q * parts > x ? -1 : 0);
+    return b * base + q;
   }
   __device__ __forceinline__ int item_cost(int units) const;
 };
@@ -209,8 +210,8 @@ __device__ __forceinline__ int qc_slot(int first, int k) { return k == 0 ? first
 // instructions: loops stay loops, and no integer division.  (All items fit in 31
 // bits: checked on the host.)
 template <int kThreads, int kMin, int kOverhead, typename Work>
-__device__ __forceinline__ QcShares qc_shares(const QcAttnParams& p, const Work& work, int64_t* cost0, int32_t* item0,
-                                              QcSharesScratch& sh) {
+__device__ __forceinline__ QcShares qc_shares(const QcAttnParams& p, int workers, const Work& work, int64_t* cost0,
+                                              int32_t* item0, QcSharesScratch& sh) {
   constexpr int kWarps = kThreads / 32;
   static_assert(kThreads <= 1024, "a word of red per warp");
   const int n = p.n_users;
@@ -251,10 +252,10 @@ __device__ __forceinline__ QcShares qc_shares(const QcAttnParams& p, const Work&
     if (bad && blockIdx.x == 0) atomicOr(p.status, DEV_ERR_CACHE);
     const int64_t with = v[2] & 0xFFFFFFFF, without = v[2] >> 32, items_all = with + without;
     int64_t total = v[0] + with * kOverhead + without;
-    QcShares r = {0, p.ctas, 0, kOverhead, 0};
-    if (total < static_cast<int64_t>(kMin + kOverhead) * p.ctas) {
-      if (items_all < p.ctas)  // (each item's parts are rounded up, hence the items taken off)
-        r.chunk = max(kMin, static_cast<int>(__fdividef(static_cast<float>(v[0]), static_cast<float>(p.ctas - items_all)) * 1.0001f) + 1);
+    QcShares r = {0, workers, 0, kOverhead, 0};
+    if (total < static_cast<int64_t>(kMin + kOverhead) * workers) {
+      if (items_all < workers)  // (each item's parts are rounded up, hence the items taken off)
+        r.chunk = max(kMin, static_cast<int>(__fdividef(static_cast<float>(v[0]), static_cast<float>(workers - items_all)) * 1.0001f) + 1);
       else
         r.parts = max(1, static_cast<int>(total) / (kMin + kOverhead));
     }
@@ -304,13 +305,13 @@ __device__ __forceinline__ QcShares qc_shares(const QcAttnParams& p, const Work&
   return sh.shares;
 }
 
-// The part of the item at `pos` (of a user's work w) that belongs to this CTA,
+// The part of the item at `pos` (of a user's work w) that belongs to worker cta,
 // whose share overlaps it.  Cuts that would leave a part of fewer than kMin
 // units move to the item's end, the same way for the CTAs on both sides.
 template <int kMin>
-__device__ __forceinline__ QcPart qc_part(const QcShares& sh, const QcUserWork& w, int64_t pos) {
+__device__ __forceinline__ QcPart qc_part(const QcShares& sh, int cta, const QcUserWork& w, int64_t pos) {
   QcPart r = {0, w.units, 1, 0, 0};
-  const int cta = static_cast<int>(blockIdx.x), cost = sh.item_cost(w.units);
+  const int cost = sh.item_cost(w.units);
   const int64_t start = sh.start(cta), end = sh.start(cta + 1);
   if (w.units == 0 || (pos >= start && pos + cost <= end)) return r;
   const auto cut = [&](int64_t at) {  // a cut at cost `at`, in units
