@@ -454,11 +454,16 @@ __global__ void __launch_bounds__(QL_THREADS) qc_load_kernel(const QcLoadParams 
   const int per = (n + QL_THREADS - 1) / QL_THREADS;
   const int lo = min(tid * per, n), hi = min(lo + per, n);
   // blocks of a user: its tokens' blocks, or when packed all of its padded rows'
+  // (unsigned: a length may be 16 short of 2^31)
+  const auto user_blocks = [](int len) {
+    const uint32_t x = static_cast<uint32_t>(len);
+    return static_cast<int>(kPacked ? (x + ATT_BN - 1) / ATT_BN * (ATT_BN / QC_ROWS) : (x + QC_ROWS - 1) / QC_ROWS);
+  };
   int64_t mine = 0;
   bool bad = false;
   for (int u = lo; u < hi; ++u) {
     const int len = qc_length(p.lens, u, most, bad);
-    mine += kPacked ? ((len + ATT_BN - 1) / ATT_BN) * (ATT_BN / QC_ROWS) : (len + QC_ROWS - 1) / QC_ROWS;
+    mine += user_blocks(len);
   }
   int64_t total;
   int64_t before = block_scan(mine, warp_sums, &total);
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(QL_THREADS) qc_load_kernel(const QcLoadParams 
   for (int u = lo; u < hi; ++u) {
     block0[u] = static_cast<int32_t>(before);
     const int len = qc_length(p.lens, u, most, ignored);
-    const int b = kPacked ? ((len + ATT_BN - 1) / ATT_BN) * (ATT_BN / QC_ROWS) : (len + QC_ROWS - 1) / QC_ROWS;
+    const int b = user_blocks(len);
     if (kPacked && blockIdx.x == 0) {
       const int64_t first = before * QC_ROWS;
       const bool fits = !too_many && first + static_cast<int64_t>(b) * QC_ROWS <= p.n_rows;
