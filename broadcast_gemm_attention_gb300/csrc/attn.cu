@@ -611,6 +611,14 @@ __device__ void att_softmax(const AttnParams& p, const AttSmem& s, uint32_t tmem
       // runs over g % 2 == group (visiting every tile to skip half of them
       // cost the group ~3 % of the kernel's time in loop control)
       const uint32_t g0 = g;
+      // Is this row one that the unit's Q load writes?  The others (behind the
+      // tile's last candidate where Lq does not divide 128, behind the rows of a
+      // self tile) hold what was in shared memory, of an earlier unit or launch:
+      // they have no vote in moving the reference, or a row's rounding would
+      // depend on that (no score is above infinity, nor above the NaN that the
+      // sum with a reference of -infinity is).
+      const bool loaded = kSelf && x.self ? ln.r < p.self_rows : row_in_tile;
+      const float margin = loaded ? RESCALE_THRESHOLD : INFINITY;
       for (int jt = static_cast<int>((static_cast<uint32_t>(grp) - g0) & 1u); jt < x.ntiles; jt += 2) {
         g = g0 + static_cast<uint32_t>(jt);
         if (!mbar_wait(&s.s_full[grp], (g >> 1) & 1u, s.abort, p.timeout_ns, 1)) return;
@@ -651,7 +659,7 @@ __device__ void att_softmax(const AttnParams& p, const AttSmem& s, uint32_t tmem
         if (jt == 0) mprev = -INFINITY;
         // tcgen05.ld/st are warp-collective: the rescale decision must be
         // uniform across the warp, so any row that needs it moves all 32
-        const bool rescale = __any_sync(0xffffffffu, mx > mprev + RESCALE_THRESHOLD);
+        const bool rescale = __any_sync(0xffffffffu, mx > mprev + margin);
         const float mj = rescale ? chain_value(fmaxf(mprev, mx)) : mprev;
         chain_post(s, ln.r, g + 1, mj);
         if (mj != mref) {  // this group's sum follows the reference (l = 0 on its first tile)
@@ -788,17 +796,6 @@ __global__ void __launch_bounds__(ATT_THREADS, 1)
     for (int r = 0; r < ATT_BM; ++r) s.chain[r] = 0;  // tag 0: no tile has posted (tags start at 1)
     *s.abort = 0;
     fence_barrier_init();
-    fence_proxy_async_smem();
-  }
-  // Rows behind the tile's last candidate (Lq does not divide 128) are never
-  // loaded.  They have a vote in moving their warp's reference, so they hold
-  // zeros, not what the launch before left, or results would not repeat.
-  const int used = p.cands_per_tile * p.Lq;
-  if (used < ATT_BM) {
-    for (int i = threadIdx.x; i < (ATT_BM - used) * 32; i += ATT_THREADS) {
-      const int r = used + (i >> 5), half = (i >> 4) & 1, buf = (i >> 3) & 1;
-      *reinterpret_cast<uint4*>(s.q + buf * ATT_Q_TILE_BYTES + half * HALF_TILE + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-    }
     fence_proxy_async_smem();
   }
   if (warp == 0 && lane_id() == 0) {
