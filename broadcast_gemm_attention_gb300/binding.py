@@ -33,6 +33,7 @@ IKBO_ERR_OUT_OF_PAGES = 8
 IKBO_ERR_CACHE = 9
 DEBUG_WITHHOLD_USER_PARTIAL = 1
 DEBUG_NO_COOPERATIVE = 2
+DEBUG_WITHHOLD_KEYS = 4
 
 # every function the header declares: name -> (restype, argtypes)
 _vp, _i, _u64, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_double

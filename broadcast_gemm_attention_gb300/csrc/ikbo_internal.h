@@ -26,6 +26,7 @@ enum : uint32_t {
 enum : uint32_t {
   DEBUG_WITHHOLD_USER_PARTIAL = 1u << 0,  // LCE: never publish user partials
   DEBUG_NO_COOPERATIVE = 1u << 1,         // LCE backward: the candidate pass and its finish as two launches
+  DEBUG_WITHHOLD_KEYS = 1u << 2,          // cache attention in tiles: some CTAs' keys are never handed over
 };
 
 // ------------------------------------------------------------ segments

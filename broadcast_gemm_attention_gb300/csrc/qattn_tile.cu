@@ -207,6 +207,9 @@ __device__ List make_list(const QcAttnParams& p, uint8_t* sm, Aux& x) {
   return l;
 }
 
+// A wait taken by a whole warp: the lanes agree on its outcome, so that a limit
+// that expires while the barrier completes never splits the warp before its next
+// warp-wide instruction.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Smem& s, const QcAttnParams& p) {
   const bool ok = mbar_wait(bar, parity, &s.x->abort, p.timeout_ns, 1);
   return __all_sync(0xffffffffu, ok);
@@ -470,8 +473,11 @@ __device__ void pv_issuer(const QcAttnParams& p, const Smem& s, uint32_t tmem, c
   }
 }
 
-// After a wait that ran out: an issuer's products in flight end (they need
-// nothing more), or a million looks are over, before the CTA frees their memory.
+// An issuer leaves when its products in flight have ended (they need nothing
+// more), or a million looks are over: whichever warp's wait ran out, the CTA does
+// not free their memory before.  (Only where a wait ran out does anything remain in
+// flight here.  Asked for by a flag behind the roles' last barrier instead, the
+// drain cost 2% of the kernel.)
 __device__ void drain(uint64_t* bar) {
   __syncwarp();
   if (elect_one()) mma_commit(bar);
@@ -497,8 +503,14 @@ __device__ __forceinline__ uint32_t chain_load(const Smem& s, int r) {
   asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(w) : "r"(smem_u32(s.x->chain + r)) : "memory");
   return w;
 }
+// The softmax warps' waits for barriers are taken lane by lane, without a vote
+// (which cost up to 4% of the kernel), and a lane whose wait ran out does not
+// leave: it goes on with whatever it finds, as the abort flag has made the call's
+// results worthless, until the warp leaves as one at the chain, where it votes in any
+// case: the tag that such a lane wants there is one that no word has (those hold g
+// or g - 1), so that it looks at the flag.
+__device__ __forceinline__ uint32_t tag_wanted(uint32_t g, bool there) { return (g + (there ? 0u : 0x80u)) & 0xFFu; }
 __device__ __forceinline__ bool chain_wait(const QcAttnParams& p, const Smem& s, int r, uint32_t tag, float& m) {
-  tag &= 0xFFu;
   uint32_t w = chain_load(s, r);
   bool ok = true;
   if ((w & 0xFFu) != tag) {
@@ -670,16 +682,16 @@ __device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, 
 
 // An item's epilogue: the groups' row sums joined (both have posted theirs), O
 // out of TMEM to global memory (or through the partial rows of a split item).
-__device__ __forceinline__ bool epilogue(const QcAttnParams& p, const Smem& s, uint32_t Ot, const List& list, const Done& done,
+__device__ __forceinline__ void epilogue(const QcAttnParams& p, const Smem& s, uint32_t Ot, const List& list, const Done& done,
                                          const Lane& ln, uint32_t& ou) {
   const Item x = load_item(list, done.k);
-  if (!mbar_wait(&s.fin_full[ou & 1u], (ou >> 1) & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
+  mbar_wait(&s.fin_full[ou & 1u], (ou >> 1) & 1u, &s.x->abort, p.timeout_ns, 1);
   const float2 f0 = s.x->fin[ou & 1u][0][ln.r], f1 = s.x->fin[ou & 1u][1][ln.r];
-  if (!mbar_wait(s.o_full, ou & 1u, &s.x->abort, p.timeout_ns, 1)) return false;
+  mbar_wait(s.o_full, ou & 1u, &s.x->abort, p.timeout_ns, 1);
   ++ou;
   if (x.row0 + ln.quarter * 32 >= x.n_rows) {  // none of the warp's rows exists
     mbar_arrive(s.o_empty);
-    return true;
+    return;
   }
   const float mf = fmaxf(f0.x, f1.x);
   // a group without a reference (no tile, or no score that is a number) has the sum 0, or NaN
@@ -691,7 +703,7 @@ __device__ __forceinline__ bool epilogue(const QcAttnParams& p, const Smem& s, u
   uint8_t* stage = s.out + (ln.quarter * 2 + ln.half) * STAGE_BYTES;
   if (x.ns > 1) {
     join_splits(p, Ot, x, row, ln, mf, l, stage, s.o_empty);
-    return true;
+    return;
   }
   const float inv = inverse(l);
   uint32_t w[32];
@@ -708,7 +720,6 @@ __device__ __forceinline__ bool epilogue(const QcAttnParams& p, const Smem& s, u
   if (p.lse && row >= 0 && ln.half == 0) store_lse(p, row, mf, l);
 #pragma unroll
   for (int c = 0; c < 4; ++c) store_columns(p, stage, ln, row, c, w + 8 * c);
-  return true;
 }
 
 __device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tmem, const List& list) {
@@ -760,10 +771,10 @@ __device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tme
       bool rescale = false;
       if (jt < nt) {
         const uint32_t St = tmem + lane_base + TM_S + sb * 128;
-        if (!mbar_wait(&s.s_full[sb], (g / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1)) return;
+        const uint32_t want = tag_wanted(g, mbar_wait(&s.s_full[sb], (g / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1));
         tc_fence_after();
         if (!rows_here) {  // none of the warp's 32 rows exists: keep the hand-shakes in step, nothing else
-          if (!chain_wait(p, s, ln.r, g, mprev)) return;
+          if (!chain_wait(p, s, ln.r, want, mprev)) return;
           chain_post(s, ln.r, g + 1, 0.f);
         } else {
           // two passes over the row, 32 columns at a time with the next ones on
@@ -801,7 +812,7 @@ __device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tme
           mx *= sl;
           const uint32_t cw = chain_load(s, ln.r);
           mprev = __uint_as_float(cw & 0xFFFFFF00u);
-          if (!__all_sync(0xffffffffu, (cw & 0xFFu) == (g & 0xFFu)) && !chain_wait(p, s, ln.r, g, mprev)) return;
+          if (!__all_sync(0xffffffffu, (cw & 0xFFu) == want) && !chain_wait(p, s, ln.r, want, mprev)) return;
           if (jt == 0) mprev = -INFINITY;
           rescale = __any_sync(0xffffffffu, mx > mprev + RESCALE_THRESHOLD);
           mj = rescale ? chain_value(fmaxf(mprev, mx)) : mprev;
@@ -828,12 +839,12 @@ __device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tme
       }
       // Between the group's first tile of this item and that tile's P.V, which
       // waits for O anyway.
-      if (epi && !epilogue(p, s, Ot, list, prev, ln, ou)) return;
+      if (epi) epilogue(p, s, Ot, list, prev, ln, ou);
       epi = false;
       if (jt < nt) {
         if (rescale && jt > 0) {
           const uint32_t gp = g - 1;
-          if (!mbar_wait(&s.pv_done[gp % S_BUFS], (gp / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1)) return;
+          mbar_wait(&s.pv_done[gp % S_BUFS], (gp / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1);
           tc_fence_after();
           const float alpha = ex2(mprev - mj);
 #pragma unroll 1
@@ -884,7 +895,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
       mbar_init(&s.drain[i], 1);
       mbar_init(&s.q_full[i], 1);
       mbar_init(&s.q_empty[i], 1);
-      mbar_init(&s.k_full[i], DECODE_WARPS);
+      mbar_init(&s.k_full[i], DECODE_WARPS + ((p.debug & DEBUG_WITHHOLD_KEYS) && (blockIdx.x & 3u) == 1u ? 1 : 0));
       mbar_init(&s.k_empty[i], 1);
       mbar_init(&s.v_full[i], DECODE_WARPS);
       mbar_init(&s.v_empty[i], 1);
@@ -916,7 +927,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
     else if (warp == 1) s_issuer(p, s, tmem, l);
     else if (warp == 2) pv_issuer(p, s, tmem, l);
     else if (warp == 3) q_loader(p, s, l);
-    if ((warp == 1 || warp == 2) && *const_cast<volatile uint32_t*>(&s.x->abort)) drain(&s.drain[warp - 1]);
+    if (warp == 1 || warp == 2) drain(&s.drain[warp - 1]);
   } else if (warp < DECODE_WARP0) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
     softmax_warps(p, s, tmem, l);

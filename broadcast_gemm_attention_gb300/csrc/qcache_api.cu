@@ -425,6 +425,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   ap.max_items = items;
   ap.scale_log2 = scale * 1.4426950408889634f;
   ap.sixteen = QC_SIXTEEN;
+  ap.debug = p->debug;
   ap.timeout_ns = p->timeout_ns;
   if ((few ? launch_qattn(ap, eight, solo, stream) : launch_qattn_tile(ap, stream)) != cudaSuccess)
     return IKBO_ERR_CUDA;

@@ -96,6 +96,7 @@ struct QcAttnParams {
   int ctas;                // of the launch
   float scale_log2;
   uint32_t sixteen;        // QC_SIXTEEN
+  uint32_t debug;          // the plan's switches
   uint64_t timeout_ns;
 };
 

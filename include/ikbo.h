@@ -473,7 +473,10 @@ ikbo_status_t ikbo_plan_get_status(ikbo_plan_t p, cudaStream_t stream);
  * correct Y, and the call reports IKBO_ERR_TIMEOUT); bit 1 = the LCE
  * backward's candidate pass does not end with its finish in the same
  * (cooperative) launch but is followed by a finish kernel, the path taken
- * where a cooperative launch is refused.  The timeout bounds every wait
+ * where a cooperative launch is refused; bit 2 = in the cache attention's
+ * launches in tiles every fourth CTA never hands its keys to the products (which
+ * wait for them, and the call ends with IKBO_ERR_TIMEOUT and an O that is not
+ * defined).  The timeout bounds every wait
  * inside the kernels (default 2 s). */
 ikbo_status_t ikbo_plan_set_debug(ikbo_plan_t p, unsigned flags);
 ikbo_status_t ikbo_plan_set_timeout_ns(ikbo_plan_t p, uint64_t timeout_ns);
