@@ -534,10 +534,6 @@ ikbo_status_t ikbo_plan_get_status(ikbo_plan_t p, cudaStream_t stream) {
   uint32_t word = 0;
   if (cudaMemcpy(&word, p->d_status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return IKBO_ERR_CUDA;
   if (word && cudaMemset(p->d_status, 0, sizeof(uint32_t)) != cudaSuccess) return IKBO_ERR_CUDA;
-  // a cache attention that gave up may have left parts of an item unjoined
-  if ((word & DEV_ERR_PIPE_TIMEOUT) && p->d_qa_tickets &&
-      cudaMemset(p->d_qa_tickets, 0, p->qa_tickets_elems * sizeof(uint32_t)) != cudaSuccess)
-    return IKBO_ERR_CUDA;
   if (word & DEV_ERR_MAP_RANGE) return IKBO_ERR_MAP_OUT_OF_RANGE;
   if (word & (DEV_ERR_FLAG_TIMEOUT | DEV_ERR_PIPE_TIMEOUT)) return IKBO_ERR_TIMEOUT;
   if (word & DEV_ERR_OUT_OF_PAGES) return IKBO_ERR_OUT_OF_PAGES;

@@ -615,6 +615,11 @@ __device__ __forceinline__ void store_lse(const QcAttnParams& p, int64_t row, fl
   p.lse[row] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
 }
 
+// How many splits of an item's tile have a piece's rows in their slots.
+__device__ __forceinline__ uint32_t* ticket(const QcAttnParams& p, const Item& x, int quarter, int half) {
+  return p.tickets + static_cast<int64_t>(x.first) * 8 + quarter * 2 + half;
+}
+
 // A split's piece of O (this warp's 32 rows x 64 columns) to its slot; the
 // warp that completes the tile's piece adds the splits in order and stores it.
 __device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, const Item& ro, int64_t row, const Lane& ln,
@@ -641,7 +646,7 @@ __device__ __forceinline__ void join_splits(const QcAttnParams& p, uint32_t Ot, 
   __syncwarp();
   uint32_t last = 0;
   if (lane == 0) {
-    uint32_t* t = p.tickets + static_cast<int64_t>(ro.first) * 8 + ln.quarter * 2 + ln.half;
+    uint32_t* t = ticket(p, ro, ln.quarter, ln.half);
     last = atomicAdd(t, 1u) + 1 == static_cast<uint32_t>(ro.ns);
     if (last) *t = 0;  // zero again for the next call
   }
@@ -722,7 +727,9 @@ __device__ __forceinline__ void epilogue(const QcAttnParams& p, const Smem& s, u
   for (int c = 0; c < 4; ++c) store_columns(p, stage, ln, row, c, w + 8 * c);
 }
 
-__device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tmem, const List& list) {
+// Returns the first item whose epilogue has not run (the list's end, unless a wait
+// ran out).
+__device__ int softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tmem, const List& list) {
   const int warp = threadIdx.x >> 5;
   Lane ln;
   ln.quarter = warp & 3;
@@ -774,7 +781,7 @@ __device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tme
         const uint32_t want = tag_wanted(g, mbar_wait(&s.s_full[sb], (g / S_BUFS) & 1u, &s.x->abort, p.timeout_ns, 1));
         tc_fence_after();
         if (!rows_here) {  // none of the warp's 32 rows exists: keep the hand-shakes in step, nothing else
-          if (!chain_wait(p, s, ln.r, want, mprev)) return;
+          if (!chain_wait(p, s, ln.r, want, mprev)) return epi ? prev.k : k;
           chain_post(s, ln.r, g + 1, 0.f);
         } else {
           // two passes over the row, 32 columns at a time with the next ones on
@@ -812,7 +819,7 @@ __device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tme
           mx *= sl;
           const uint32_t cw = chain_load(s, ln.r);
           mprev = __uint_as_float(cw & 0xFFFFFF00u);
-          if (!__all_sync(0xffffffffu, (cw & 0xFFu) == want) && !chain_wait(p, s, ln.r, want, mprev)) return;
+          if (!__all_sync(0xffffffffu, (cw & 0xFFu) == want) && !chain_wait(p, s, ln.r, want, mprev)) return epi ? prev.k : k;
           if (jt == 0) mprev = -INFINITY;
           rescale = __any_sync(0xffffffffu, mx > mprev + RESCALE_THRESHOLD);
           mj = rescale ? chain_value(fmaxf(mprev, mx)) : mprev;
@@ -872,6 +879,21 @@ __device__ void softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tme
       ++ic;
     }
   }
+  return list.count;
+}
+
+// A softmax warp that gave up: its tickets of the items from k on, so that every
+// piece of a split tile has all of its tickets in the end, whoever gave up, and its
+// count is zero again for the next call.  (What the last to finish then joins is of
+// no worth.)
+__device__ void abandon(const QcAttnParams& p, const List& list, int k) {
+  const int warp = static_cast<int>(threadIdx.x >> 5), quarter = warp & 3, half = (warp - SOFTMAX_WARP0) >> 2;
+  for (; k < list.count; ++k) {
+    const Item x = load_item(list, k);
+    if (x.nt == 0 || x.ns == 1 || x.row0 + quarter * 32 >= x.n_rows || lane_id() != 0) continue;
+    uint32_t* t = ticket(p, x, quarter, half);
+    if (atomicAdd(t, 1u) + 1 == static_cast<uint32_t>(x.ns)) *t = 0;
+  }
 }
 
 __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnParams p) {
@@ -930,7 +952,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1) qattn_tile_kernel(const QcAttnP
     if (warp == 1 || warp == 2) drain(&s.drain[warp - 1]);
   } else if (warp < DECODE_WARP0) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
-    softmax_warps(p, s, tmem, l);
+    const int k = softmax_warps(p, s, tmem, l);
+    if (k < l.count) abandon(p, l, k);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(DECODE_REGS));
     decode_warps(p, s, l);

@@ -444,7 +444,9 @@ ikbo_status_t ikbo_qcache_load(ikbo_plan_t p, const void* data, int n_pages, int
  * value is out of range keeps its rows; rows of a user with a page out of
  * range are not defined (the page is not touched).  What lies in a page behind
  * a history's end is never used.  fp32 scores and softmax, P rounded to bf16 for P.V, fp32
- * accumulation.  Results repeat bit for bit.
+ * accumulation.  Results repeat bit for bit.  Of a call in which a bounded wait ran
+ * out (IKBO_ERR_TIMEOUT) O and lse are not defined; the calls after it are not
+ * touched by that, whether the status has been read or not.
  * Workspaces are the plan's, grown by the first call that needs more (which
  * allocates; under stream capture that call fails with IKBO_ERR_CUDA and
  * allocates nothing, so make one eager call of the largest size first; a

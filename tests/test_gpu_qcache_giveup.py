@@ -23,21 +23,22 @@ class Request:
     def __init__(self):
         self.st = R.Store(1, [2500, 1900, 3300], 2, 64)
         self.m = np.repeat(np.arange(3), [16, 3, 40]).astype(np.int32)
-        self.Q = queries(3, self.m.size, 2, 8)
-        self.q, self.cache = bf(self.Q), self.st.cuda()
+        self.Q = [queries(3 + k, self.m.size, 2, 8) for k in range(2)]
+        self.q, self.cache = [bf(x) for x in self.Q], self.st.cuda()
 
     def plan(self, stream=None):
         p = B.Plan(self.m.size, 3, 2)
         p.plan(i32(self.m), 3, 2, 8, stream=stream)
         return p
 
-    def attend(self, p, stream=None):
+    def attend(self, p, stream=None, k=0):
+        """With the k-th queries."""
         data, table, lens = self.cache
-        O = torch.zeros_like(self.q)
+        O = torch.zeros_like(self.q[k])
         if stream is not None:
             torch.cuda.synchronize()
         # so large a bound that this is not a few short histories: the tile kernel
-        p.attn_qcache_forward(self.q, data, 64, table, lens, O, Lkv=8_000_000, stream=stream)
+        p.attn_qcache_forward(self.q[k], data, 64, table, lens, O, Lkv=8_000_000, stream=stream)
         return O
 
 
@@ -55,9 +56,30 @@ def test_a_wait_that_ran_out_is_reported_and_over():
     with r.plan() as p:
         before = r.attend(p)
         assert p.status() == B.IKBO_OK
-        check(before, None, r.Q, r.st.kv, r.m, 2)
+        check(before, None, r.Q[0], r.st.kv, r.m, 2)
         for _ in range(3):
             give_up(p, r)
             assert p.status() == B.IKBO_ERR_TIMEOUT
             assert torch.equal(r.attend(p), before)
             assert p.status() == B.IKBO_OK
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_the_next_call_needs_no_status_read(side):
+    """Every split's pieces are counted also where their CTA gave up: the calls after are
+    right, on whichever stream, although nobody has read the status in between."""
+    r = Request()
+    stream = torch.cuda.Stream() if side else None
+    with r.plan(stream) as p:
+        before = [r.attend(p, stream, k) for k in range(2)]
+        assert p.status(stream) == B.IKBO_OK
+        for k in range(2):
+            check(before[k], None, r.Q[k], r.st.kv, r.m, 2)
+        for _ in range(3):
+            give_up(p, r, stream)
+            after = [r.attend(p, stream, k) for k in (1, 0, 1)]  # other rows than the ones that lie in the slots
+            assert p.status(stream) == B.IKBO_ERR_TIMEOUT
+            assert torch.equal(after[0], before[1]) and torch.equal(after[1], before[0]) and torch.equal(after[2], before[1])
+        last = r.attend(p, stream)
+        assert p.status(stream) == B.IKBO_OK
+        assert torch.equal(last, before[0])
