@@ -530,10 +530,16 @@ ikbo_status_t ikbo_plan_worklist(ikbo_plan_t p, const int32_t** d_work, const in
 
 ikbo_status_t ikbo_plan_get_status(ikbo_plan_t p, cudaStream_t stream) {
   if (!p) return IKBO_ERR_INVALID_ARG;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return IKBO_ERR_CUDA;
   uint32_t word = 0;
-  if (cudaMemcpy(&word, p->d_status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return IKBO_ERR_CUDA;
-  if (word && cudaMemset(p->d_status, 0, sizeof(uint32_t)) != cudaSuccess) return IKBO_ERR_CUDA;
+  // read and cleared in the stream's order: the default stream's would not be that
+  // of a stream made without waiting for it, and a clear that comes after the next
+  // call's error would lose it
+  if (cudaMemcpyAsync(&word, p->d_status, sizeof(word), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return IKBO_ERR_CUDA;
+  if (word && (cudaMemsetAsync(p->d_status, 0, sizeof(uint32_t), stream) != cudaSuccess ||
+               cudaStreamSynchronize(stream) != cudaSuccess))
+    return IKBO_ERR_CUDA;
   if (word & DEV_ERR_MAP_RANGE) return IKBO_ERR_MAP_OUT_OF_RANGE;
   if (word & (DEV_ERR_FLAG_TIMEOUT | DEV_ERR_PIPE_TIMEOUT)) return IKBO_ERR_TIMEOUT;
   if (word & DEV_ERR_OUT_OF_PAGES) return IKBO_ERR_OUT_OF_PAGES;
