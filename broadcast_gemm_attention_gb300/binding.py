@@ -639,10 +639,16 @@ class Plan:
     def attn_self_target_forward(self, Q, Q_user, K, V, kv_offsets, O, O_user, scale=None, stream=None):
         ikbo_attn_self_target_forward(self.handle, Q, Q_user, K, V, kv_offsets, O, O_user, scale, stream)
 
+    def _check_start(self, start, broadcast):
+        if broadcast and start is not None and self._request is not None and start.numel() != self._request[1]:
+            raise ValueError(f"with broadcast, start must hold a position for each of the plan's {self._request[1]} users")
+
     def rope_forward(self, rope, X, Y, start=None, broadcast=False, stream=None):
+        self._check_start(start, broadcast)
         ikbo_rope_forward(self.handle, rope.handle, X, Y, start, broadcast, stream)
 
     def rope_backward(self, rope, dY, dX, start=None, broadcast=False, stream=None):
+        self._check_start(start, broadcast)
         ikbo_rope_backward(self.handle, rope.handle, dY, dX, start, broadcast, stream)
 
     def qcache_resize(self, lens, new_lens, table, page, free, n_free, slots, slot_offsets, positions=None, stream=None):
