@@ -128,12 +128,13 @@ void free_plan(ikbo_plan_t p) {
   cudaFree(p->d_abwd_lse);
   cudaFree(p->d_abwd_drow);
   cudaFree(p->d_abwd_blk);
-  cudaFree(p->d_qa_part);
-  cudaFree(p->d_qa_tickets);
-  cudaFree(p->d_qa_kv);
-  cudaFree(p->d_qa_list);
-  cudaFree(p->d_qa_ranges);
+  cudaFree(p->qa_part.ptr);
+  cudaFree(p->qa_tickets.ptr);
+  cudaFree(p->qa_kv.ptr);
+  cudaFree(p->qa_list.ptr);
+  cudaFree(p->qa_ranges.ptr);
   for (int i = 0; i < p->n_retired; ++i) cudaFree(p->retired[i]);
+  std::free(p->retired);
   delete p;
 }
 

@@ -7,13 +7,20 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
 
 #include "ikbo.h"
 #include "ikbo_internal.h"
 
 namespace ikbo {
-constexpr int PLAN_RETIRED_MAX = 96;
-}
+// A workspace of the plan that captured graphs may hold (see grow_kept).
+template <typename T>
+struct KeptBuffer {
+  T* ptr = nullptr;
+  size_t elems = 0;
+  bool captured = false;  // a call under stream capture has used it
+};
+}  // namespace ikbo
 
 struct ikbo_plan_s {
   int device = 0;
@@ -62,19 +69,13 @@ struct ikbo_plan_s {
   size_t abwd_drow_elems = 0;
   int32_t* d_abwd_blk = nullptr;
   size_t abwd_blk_elems = 0;
-  // 4-bit cache attention (grown on first use; replaced buffers stay allocated
-  // until the plan is destroyed, because a captured graph may hold them)
-  float* d_qa_part = nullptr;  // partial rows of histories split over several CTAs
-  size_t qa_part_elems = 0;
-  uint32_t* d_qa_tickets = nullptr;  // splits of a tile that have finished (zero between calls)
-  size_t qa_tickets_elems = 0;
-  int4* d_qa_list = nullptr;  // work items
-  size_t qa_list_elems = 0;
-  uint16_t* d_qa_kv = nullptr;  // decoded K rows, then V rows
-  size_t qa_kv_elems = 0;
-  int32_t* d_qa_ranges = nullptr;  // each user's first decoded row, then each user's length
-  size_t qa_ranges_elems = 0;
-  void* retired[ikbo::PLAN_RETIRED_MAX] = {};
+  // 4-bit cache attention (grown on first use)
+  ikbo::KeptBuffer<float> qa_part;        // partial rows of histories split over several CTAs
+  ikbo::KeptBuffer<uint32_t> qa_tickets;  // splits of a tile that have finished (zero between calls)
+  ikbo::KeptBuffer<int4> qa_list;         // work items
+  ikbo::KeptBuffer<uint16_t> qa_kv;       // decoded K rows, then V rows
+  ikbo::KeptBuffer<int32_t> qa_ranges;    // each user's first decoded row, then each user's length
+  void** retired = nullptr;               // replaced buffers that captured graphs may hold, freed with the plan
   int n_retired = 0;
   bool lce_flags_dirty = false;  // an LCE launch failed: its flags may still be set
   uint32_t debug = 0;
@@ -94,34 +95,65 @@ inline bool plan_device_current(const ikbo_plan_s* p) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == p->device;
 }
 
-// Grows a workspace that captured graphs may hold: the old buffer is kept
-// until the plan is destroyed, sizes grow by a quarter at least (so that a
-// plan meets few of them), and a stream that is being captured is refused
-// before any allocation is tried on it.  New memory is zeroed on `stream`.
-template <typename T>
-cudaError_t grow_kept(ikbo_plan_s* p, T** ptr, size_t* have, size_t need, cudaStream_t stream) {
-  if (*have >= need && *ptr) return cudaSuccess;
+inline cudaError_t is_capturing(cudaStream_t stream, bool* yes) {
   cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(stream, &st);
+  const cudaError_t e = cudaStreamIsCapturing(stream, &st);
+  *yes = st != cudaStreamCaptureStatusNone;
+  return e;
+}
+
+// Makes a workspace hold `need` elements.  Sizes grow by a quarter at least (so
+// that a plan meets few of them), up to `most` where that holds `need`, unless the
+// memory for that is not there.  A buffer that a captured call has used is kept
+// until the plan is destroyed, as its graph may be replayed at any time; others are
+// freed before the new one is allocated.  A call under capture that would have to
+// allocate is refused before anything is tried.  kZeroed: new memory is zeroed on
+// `stream`.
+template <bool kZeroed, typename T>
+cudaError_t grow_kept(ikbo_plan_s* p, KeptBuffer<T>* b, size_t need, size_t most, bool capturing, cudaStream_t stream) {
+  if (b->ptr && b->elems >= need) {
+    b->captured = b->captured || capturing;
+    return cudaSuccess;
+  }
+  // (asked again: for the default stream it is an error that another one is captured,
+  // whose capture an allocation would end)
+  cudaError_t e = is_capturing(stream, &capturing);
   if (e != cudaSuccess) return e;
-  if (st != cudaStreamCaptureStatusNone) return cudaErrorStreamCaptureUnsupported;
-  if (*ptr && p->n_retired == PLAN_RETIRED_MAX) return cudaErrorMemoryAllocation;
-  const size_t least = *have + *have / 4;
-  if (need < least) need = least;
-  T* fresh = nullptr;
-  e = cudaMalloc(reinterpret_cast<void**>(&fresh), need * sizeof(T));
+  if (capturing) return cudaErrorStreamCaptureUnsupported;
+  size_t size = b->elems + b->elems / 4;
+  if (size > most) size = most;
+  if (size < need) size = need;
+  if (b->ptr && b->captured) {
+    void** list = static_cast<void**>(std::realloc(p->retired, sizeof(void*) * (static_cast<size_t>(p->n_retired) + 1)));
+    if (!list) return cudaErrorMemoryAllocation;
+    p->retired = list;
+    p->retired[p->n_retired++] = b->ptr;
+  } else if (b->ptr) {  // (whichever stream the last call that used it ran on)
+    e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return e;
+    cudaFree(b->ptr);
+  }
+  *b = KeptBuffer<T>();
+  e = cudaMalloc(reinterpret_cast<void**>(&b->ptr), size * sizeof(T));
+  if (e != cudaSuccess && size > need) {
+    cudaGetLastError();
+    size = need;
+    e = cudaMalloc(reinterpret_cast<void**>(&b->ptr), size * sizeof(T));
+  }
   if (e != cudaSuccess) {
     cudaGetLastError();
+    b->ptr = nullptr;
     return e;
   }
-  e = cudaMemsetAsync(fresh, 0, need * sizeof(T), stream);
-  if (e != cudaSuccess) {
-    cudaFree(fresh);
-    return e;
+  if (kZeroed) {
+    e = cudaMemsetAsync(b->ptr, 0, size * sizeof(T), stream);
+    if (e != cudaSuccess) {
+      cudaFree(b->ptr);
+      b->ptr = nullptr;
+      return e;
+    }
   }
-  if (*ptr) p->retired[p->n_retired++] = *ptr;
-  *ptr = fresh;
-  *have = need;
+  b->elems = size;
   return cudaSuccess;
 }
 

@@ -338,22 +338,27 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   if (rows * H_kv > INT32_LIMIT) return IKBO_ERR_UNSUPPORTED;
   const int blocks_log2 = blocks_log2_of(page);
 
+  // (the default stream cannot be captured, and asking took half a microsecond)
+  bool capturing = false;
+  if (stream && is_capturing(stream, &capturing) != cudaSuccess) return IKBO_ERR_CUDA;
+  constexpr size_t ANY = ~size_t{0};
+
   const QcAttnVariant variant = qattn_variant(rows, n_users, H_kv, Lkv);
   if (variant == QATTN_DECODED) {
     // decode each history once into padded bf16 rows, then the bf16 kernel
     const int64_t cap = decoded_rows(n_users, Lkv);  // (below 2^31: QA_MOST_DECODED)
     const size_t half = static_cast<size_t>(cap) * H_kv * QC_D;
-    if (grow_kept(p, &p->d_qa_kv, &p->qa_kv_elems, 2 * half, stream) != cudaSuccess ||
-        grow_kept(p, &p->d_qa_ranges, &p->qa_ranges_elems, 2 * static_cast<size_t>(n_users), stream) != cudaSuccess)
+    if (grow_kept<false>(p, &p->qa_kv, 2 * half, QA_MOST_DECODED / sizeof(uint16_t), capturing, stream) != cudaSuccess ||
+        grow_kept<false>(p, &p->qa_ranges, 2 * static_cast<size_t>(n_users), ANY, capturing, stream) != cudaSuccess)
       return IKBO_ERR_CUDA;
     QcLoadParams lp;
     std::memset(&lp, 0, sizeof(lp));
     lp.data = static_cast<const uint8_t*>(data);
     lp.table = d_table;
     lp.lens = d_lens;
-    lp.ranges = p->d_qa_ranges;
-    lp.K = p->d_qa_kv;
-    lp.V = p->d_qa_kv + half;
+    lp.ranges = p->qa_ranges.ptr;
+    lp.K = p->qa_kv.ptr;
+    lp.V = p->qa_kv.ptr + half;
     lp.status = p->d_status;
     lp.n_rows = cap;
     lp.bound = Lkv;
@@ -369,8 +374,8 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
     c.Q = Q;
     c.K = lp.K;
     c.V = lp.V;
-    c.kv_offsets = p->d_qa_ranges;
-    c.kv_lens = p->d_qa_ranges + n_users;
+    c.kv_offsets = p->qa_ranges.ptr;
+    c.kv_lens = p->qa_ranges.ptr + n_users;
     c.O = O;
     c.lse = lse;
     c.Lkv = static_cast<int>(cap);
@@ -393,9 +398,9 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   const bool solo = rows * H_kv >= static_cast<int64_t>(eight ? 8 : 16) * 4 * ctas;
   const size_t tickets = std::max(static_cast<size_t>(QA_SLOTS) * p->num_sms * 8, qattn_tickets(p->num_sms));
   const int64_t items = few ? 0 : qattn_tile_items(rows, n_users, H_kv, p->num_sms);
-  if (grow_kept(p, &p->d_qa_part, &p->qa_part_elems, part, stream) != cudaSuccess ||
-      grow_kept(p, &p->d_qa_tickets, &p->qa_tickets_elems, tickets, stream) != cudaSuccess ||
-      (!few && grow_kept(p, &p->d_qa_list, &p->qa_list_elems, static_cast<size_t>(items) * 3, stream) != cudaSuccess))
+  if (grow_kept<false>(p, &p->qa_part, part, ANY, capturing, stream) != cudaSuccess ||
+      grow_kept<true>(p, &p->qa_tickets, tickets, ANY, capturing, stream) != cudaSuccess ||
+      (!few && grow_kept<false>(p, &p->qa_list, static_cast<size_t>(items) * 3, ANY, capturing, stream) != cudaSuccess))
     return IKBO_ERR_CUDA;
   QcAttnParams ap;
   std::memset(&ap, 0, sizeof(ap));
@@ -407,8 +412,8 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   ap.lens = d_lens;
   ap.offsets = p->d_offsets;
   ap.perm = p->d_perm;
-  ap.part = p->d_qa_part;
-  ap.tickets = p->d_qa_tickets;
+  ap.part = p->qa_part.ptr;
+  ap.tickets = p->qa_tickets.ptr;
   ap.status = p->d_status;
   ap.bound = Lkv;
   ap.n_cand = p->n_cand;
@@ -421,7 +426,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   ap.max_blocks = max_blocks;
   ap.blocks_log2 = blocks_log2;
   ap.ctas = ctas;
-  ap.list = p->d_qa_list;
+  ap.list = p->qa_list.ptr;
   ap.max_items = items;
   ap.scale_log2 = scale * 1.4426950408889634f;
   ap.sixteen = QC_SIXTEEN;

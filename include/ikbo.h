@@ -448,9 +448,11 @@ ikbo_status_t ikbo_qcache_load(ikbo_plan_t p, const void* data, int n_pages, int
  * out (IKBO_ERR_TIMEOUT) O and lse are not defined; the calls after it are not
  * touched by that, whether the status has been read or not.
  * Workspaces are the plan's, grown by the first call that needs more (which
- * allocates; under stream capture that call fails with IKBO_ERR_CUDA and
- * allocates nothing, so make one eager call of the largest size first; a
- * captured call stays valid when later ones grow them).  Calls and replayed
+ * allocates, and synchronises the device where it replaces one; under stream
+ * capture that call fails with IKBO_ERR_CUDA and allocates nothing, so make one
+ * eager call of the largest size first).  A plan holds what its largest calls need
+ * and up to a quarter more; a workspace that a captured call used is kept when a
+ * later call grows it, until the plan is destroyed, so the captured call stays valid.  Calls and replayed
  * graphs of one plan share them and must not overlap on the GPU.  Three variants,
  * chosen from the sizes (Lkv among them): with few query rows per user and K/V
  * head (16, or a little more over short histories) the 4-bit blocks become
