@@ -36,7 +36,26 @@ struct ikbo_rope_s {
 namespace {
 
 constexpr double TWO_PI = 6.283185307179586476925286766559;
+constexpr double TWO_PI_REST = 2.4492935982947064e-16;  // 2 pi - TWO_PI
 constexpr int64_t INT32_LIMIT = 0x7fffffff;
+
+// x modulo 1 in units of 2^-64, to the nearest.
+uint64_t fixed_fraction(double x) {
+  const double a = std::fabs(x), part = a - std::floor(a);  // both exact
+  const uint64_t v = static_cast<uint64_t>(std::nearbyint(std::ldexp(part, 64)));  // below 2^64: part is at most 1 - 2^-53
+  return x < 0 ? 0 - v : v;
+}
+
+// The turns of f radians, modulo 1, in units of 2^-64 turn: the quotient to 53 bits,
+// and the same for what it leaves of f.  (The first alone is off by 2^-56 of a turn
+// at f = 1, and in proportion to f; a position of 31 bits makes that 2^-25.)  Each
+// is rounded to a unit, and the second's own rounding, 2^-106 f, is below one for f
+// up to 2^40.
+uint64_t fixed_turns(double f) {
+  const double q = f / TWO_PI;
+  const double left = std::fma(-q, TWO_PI, f) - q * TWO_PI_REST;
+  return fixed_fraction(q) + fixed_fraction(left / TWO_PI);
+}
 
 // log2(page / 16), or -1 for a page that is not 16, 32, .., 1024
 int blocks_log2_of(int page) {
@@ -189,13 +208,7 @@ ikbo_status_t ikbo_rope_create(ikbo_rope_t* out, int rot_dim, const double* freq
   r->rot = rot_dim;
   r->interleaved = interleaved ? 1 : 0;
   r->magnitude = magnitude;
-  for (int j = 0; j < rot_dim / 2; ++j) {
-    // turns per position modulo 1, in units of 2^-64 turn (53 bits of it are
-    // the frequency's; the rest of the fraction is zeros)
-    double turns = freqs[j] / TWO_PI;
-    turns -= std::floor(turns);
-    r->turn[j] = turns >= 1.0 ? 0 : static_cast<uint64_t>(std::ldexp(turns, 64));
-  }
+  for (int j = 0; j < rot_dim / 2; ++j) r->turn[j] = fixed_turns(freqs[j]);
   *out = r;
   return IKBO_OK;
 }

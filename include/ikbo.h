@@ -341,9 +341,12 @@ void ikbo_rope_destroy(ikbo_rope_t r);
  *         strides with rot_dim a multiple of 16 and d of 8 runs faster.
  *   Y may be X itself with the same strides (in place); other overlaps of X
  *   and Y, and strides that make rows of Y overlap, are not allowed.
- * Angles are exact to 2^-32 of a turn at any position (a position times a
- * frequency is formed in 64-bit fixed point, where whole turns drop out);
- * fp32 arithmetic, one rounding to dtype.  A candidate whose map value is out
+ * A position times a frequency is formed in 64-bit fixed point, where whole turns
+ * drop out: it is within 2^-32 of a turn of the product of the double and the
+ * integer at any position, for frequencies up to 2^40.  As an fp32 number, which
+ * the sine and cosine take, the angle is within 2^-26 of a turn; those are within 2
+ * units of their last place for fp32, and the hardware's approximations (2^-20.5
+ * absolute) for the 16-bit types.  fp32 arithmetic, one rounding to dtype.  A candidate whose map value is out
  * of range keeps its rows of Y and is reported by the plan's status.
  * The plan need not be planned unless broadcast is set.  n = 0 launches
  * nothing (X and Y may then be NULL). */
