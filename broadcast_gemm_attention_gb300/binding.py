@@ -552,13 +552,13 @@ def ikbo_attn_qcache_forward(plan: int, Q: torch.Tensor, data: torch.Tensor, pag
         raise ValueError("inconsistent attention shapes")
     d = shape[3]
     if Lkv is None:
-        Lkv = min(n_users * max_blocks * page, 2**31 - 1)
+        Lkv = n_users * max_blocks * page
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     _check(load().ikbo_attn_qcache_forward(plan, _here(Q, bf, "Q", dev), dptr, n_pages, page, H_kv, tptr, max_blocks,
                                            lptr, _here(O, bf, "O", dev),
                                            None if lse is None else _here(lse, torch.float32, "lse", dev),
-                                           max(1, int(Lkv)), d, scale, _raw_stream(stream, dev)),
+                                           min(max(1, int(Lkv)), 2**31 - 1), d, scale, _raw_stream(stream, dev)),
            "ikbo_attn_qcache_forward")
 
 
