@@ -17,8 +17,8 @@
 //
 // The products are S^T = K Q^T (16 tokens x 8 rows) and O^T = V^T P^T (16
 // elements x 8 rows): the few rows are the instruction's short side, so that 8
-// of them take half the products and registers of 16, and 16 warps fit on an SM
-// instead of 12.  P^T comes out of the first product as the second one needs it
+// of them take half the products and registers of 16, and 12 warps fit on an SM
+// instead of 8.  P^T comes out of the first product as the second one needs it
 // but for a transposition of 8 x 8 pairs within the warp.
 //
 // Work: a tile is 8 or 16 rows of one (u, g); its history is cut into parts of
@@ -39,9 +39,11 @@
 // beside V, so that a common rounding of P cancels.  The log-sum-exp has a sum
 // of its own, of the unrounded values.
 //
-// What bounds it: 374 instructions a block and warp, half of them on the integer
-// pipe at two cycles each (shifts and AND-ORs of the codes, 58% of its time),
-// and the 12 warps' own latencies.  One candidate for each of 64 histories of
+// What bounds it: each warp's chain through a block, 360 instructions from the
+// codes over two products and the vote between them to the next block, with 12
+// warps on an SM to fill its gaps.  No unit is full (memory 55%, issue 55%, the
+// integer pipe 54% with the codes' shifts and AND-ORs), and the instructions'
+// fixed latencies are the largest stall (1.1 warps an issue, memory 0.6).  One candidate for each of 64 histories of
 // 4096 tokens, 8 heads of 8 queries: 84.6 us, 3.99 TB/s of the cache (0.59 of the
 // measured rate); 16 rows each 105.  Measured slower: 4 CTAs an SM 88.7 us (128
 // registers), 5 CTAs 98.9; the rows as the products' long side 99.9.  For 16

@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(QR_THREADS) qc_resize_kernel(const QcResizePar
 // Eight lanes take a head of a row, sixteen elements of K and of V each, two
 // lanes to a group of 32; a thread runs over its row's heads, so the slot and
 // the address are worked out once.  Bound: issue, not memory (2 bytes read and
-// 0.625 written an element): about seven instructions an element, with two
-// elements to most of them, and the integer pipe 69% busy.  So there is no
+// 0.625 written an element): twelve instructions an element, although the
+// arithmetic takes two elements in one; 77% of the issue slots and 71% of the
+// integer pipe are busy, DRAM 63%.  So there is no
 // division: q = (x - z) / s comes from an approximate reciprocal and one step of
 // Markstein's correction ("Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990), and so does the 7.5 below.  The codes are the
