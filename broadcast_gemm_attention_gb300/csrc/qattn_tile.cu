@@ -474,15 +474,16 @@ __device__ void pv_issuer(const QcAttnParams& p, const Smem& s, uint32_t tmem, c
 }
 
 // An issuer leaves when its products in flight have ended (they need nothing
-// more), or a million looks are over: whichever warp's wait ran out, the CTA does
-// not free their memory before.  (Only where a wait ran out does anything remain in
+// more), or a second is over: whichever warp's wait ran out, the CTA does not free
+// their memory before.  (Only where a wait ran out does anything remain in
 // flight here.  Asked for by a flag behind the roles' last barrier instead, the
 // drain cost 2% of the kernel.)
 __device__ void drain(uint64_t* bar) {
   __syncwarp();
   if (elect_one()) mma_commit(bar);
   __syncwarp();
-  for (int i = 0; i < 1000000 && !mbar_try_wait(bar, 0); ++i) {}
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, 0) && globaltimer_ns() - t0 < 1000000000ull) {}
   __syncwarp();
 }
 
@@ -506,9 +507,11 @@ __device__ __forceinline__ uint32_t chain_load(const Smem& s, int r) {
 // The softmax warps' waits for barriers are taken lane by lane, without a vote
 // (which cost up to 4% of the kernel), and a lane whose wait ran out does not
 // leave: it goes on with whatever it finds, as the abort flag has made the call's
-// results worthless, until the warp leaves as one at the chain, where it votes in any
-// case: the tag that such a lane wants there is one that no word has (those hold g
-// or g - 1), so that it looks at the flag.
+// results worthless (no address comes from that, the tensor memory stays allocated
+// until the products have ended, and barriers still count whole warps), until the
+// warp leaves as one at the chain, where it votes in any case: the tag that such a
+// lane wants there is one that no word has (those hold g or g - 1), so that it looks
+// at the flag.
 __device__ __forceinline__ uint32_t tag_wanted(uint32_t g, bool there) { return (g + (there ? 0u : 0x80u)) & 0xFFu; }
 __device__ __forceinline__ bool chain_wait(const QcAttnParams& p, const Smem& s, int r, uint32_t tag, float& m) {
   uint32_t w = chain_load(s, r);
