@@ -493,10 +493,14 @@ struct Lane {
 };
 
 // The chain of reference maxima through the tiles of both groups (attn.cu
-// describes it): the high 24 bits of the value, the tile's tag below.
-__device__ __forceinline__ float chain_value(float m) { return __uint_as_float(__float_as_uint(m) & 0xFFFFFF00u); }
+// describes it): the high 30 bits of the value, the tile's tag below (a reader finds
+// the word it waits for or the one before).  A score may lie above its reference by
+// what the cut bits are worth, 2^-21 of it, and P then by two to that power: in range
+// for scores up to 2^27 in magnitude.
+constexpr uint32_t CHAIN_TAG = 3u;
+__device__ __forceinline__ float chain_value(float m) { return __uint_as_float(__float_as_uint(m) & ~CHAIN_TAG); }
 __device__ __forceinline__ void chain_post(const Smem& s, int r, uint32_t tag, float m) {
-  const uint32_t w = (__float_as_uint(m) & 0xFFFFFF00u) | (tag & 0xFFu);
+  const uint32_t w = (__float_as_uint(m) & ~CHAIN_TAG) | (tag & CHAIN_TAG);
   asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(smem_u32(s.x->chain + r)), "r"(w) : "memory");
 }
 __device__ __forceinline__ uint32_t chain_load(const Smem& s, int r) {
@@ -512,15 +516,15 @@ __device__ __forceinline__ uint32_t chain_load(const Smem& s, int r) {
 // warp leaves as one at the chain, where it votes in any case: the tag that such a
 // lane wants there is one that no word has (those hold g or g - 1), so that it looks
 // at the flag.
-__device__ __forceinline__ uint32_t tag_wanted(uint32_t g, bool there) { return (g + (there ? 0u : 0x80u)) & 0xFFu; }
+__device__ __forceinline__ uint32_t tag_wanted(uint32_t g, bool there) { return (g + (there ? 0u : 2u)) & CHAIN_TAG; }
 __device__ __forceinline__ bool chain_wait(const QcAttnParams& p, const Smem& s, int r, uint32_t tag, float& m) {
   uint32_t w = chain_load(s, r);
   bool ok = true;
-  if ((w & 0xFFu) != tag) {
+  if ((w & CHAIN_TAG) != tag) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
       w = chain_load(s, r);
-      if ((w & 0xFFu) == tag) break;
+      if ((w & CHAIN_TAG) == tag) break;
       if ((it & 63u) == 0) {
         volatile uint32_t* abort = &s.x->abort;
         if (*abort) {
@@ -535,7 +539,7 @@ __device__ __forceinline__ bool chain_wait(const QcAttnParams& p, const Smem& s,
       }
     }
   }
-  m = __uint_as_float(w & 0xFFFFFF00u);
+  m = __uint_as_float(w & ~CHAIN_TAG);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -821,8 +825,8 @@ __device__ int softmax_warps(const QcAttnParams& p, const Smem& s, uint32_t tmem
           }
           mx *= sl;
           const uint32_t cw = chain_load(s, ln.r);
-          mprev = __uint_as_float(cw & 0xFFFFFF00u);
-          if (!__all_sync(0xffffffffu, (cw & 0xFFu) == want) && !chain_wait(p, s, ln.r, want, mprev)) return epi ? prev.k : k;
+          mprev = __uint_as_float(cw & ~CHAIN_TAG);
+          if (!__all_sync(0xffffffffu, (cw & CHAIN_TAG) == want) && !chain_wait(p, s, ln.r, want, mprev)) return epi ? prev.k : k;
           if (jt == 0) mprev = -INFINITY;
           rescale = __any_sync(0xffffffffu, mx > mprev + RESCALE_THRESHOLD);
           mj = rescale ? chain_value(fmaxf(mprev, mx)) : mprev;

@@ -226,7 +226,8 @@ ikbo_status_t ikbo_lce_backward(ikbo_plan_t p, const void* U, const void* C, con
  *   scale  > 0 (usually 1/sqrt(d)).  No mask.
  * Each user's K/V tile is read once per work unit and shared by up to
  * floor(128/Lq) candidates.  fp32 scores and softmax, P rounded to bf16
- * for P.V, fp32 accumulation, bf16 output.  Limits: d == 128. */
+ * for P.V, fp32 accumulation, bf16 output.  Limits: d == 128; scores (scale Q.K)
+ * of up to 2^21 in magnitude. */
 ikbo_status_t ikbo_attn_forward(ikbo_plan_t p, const void* Q, const void* K, const void* V,
                                 const int32_t* d_kv_offsets, void* O, int Lkv, int d, float scale,
                                 cudaStream_t stream);
@@ -447,7 +448,9 @@ ikbo_status_t ikbo_qcache_load(ikbo_plan_t p, const void* data, int n_pages, int
  * value is out of range keeps its rows; rows of a user with a page out of
  * range are not defined (the page is not touched).  What lies in a page behind
  * a history's end is never used.  fp32 scores and softmax, P rounded to bf16 for P.V, fp32
- * accumulation.  Results repeat bit for bit.  Of a call in which a bounded wait ran
+ * accumulation (the sum that divides O is of the rounded P in the first variant
+ * below, of the unrounded one in the others).  Scores (scale Q.K) of up to 2^26 in
+ * magnitude, 2^21 in the third variant.  Results repeat bit for bit.  Of a call in which a bounded wait ran
  * out (IKBO_ERR_TIMEOUT) O and lse are not defined; the calls after it are not
  * touched by that, whether the status has been read or not.
  * Workspaces are the plan's, grown by the first call that needs more (which
