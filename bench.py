@@ -78,8 +78,8 @@ def source_hash(files):
 
 
 KERNEL_SOURCES = {
-    "attn": ["broadcast_gemm_attention_gb300/csrc/attn.cu", "broadcast_gemm_attention_gb300/csrc/ptx.cuh",
-             "broadcast_gemm_attention_gb300/csrc/ikbo_internal.h"],
+    "attn": ["broadcast_gemm_attention_gb300/csrc/attn.cu", "broadcast_gemm_attention_gb300/csrc/attn_common.cuh",
+             "broadcast_gemm_attention_gb300/csrc/ptx.cuh", "broadcast_gemm_attention_gb300/csrc/ikbo_internal.h"],
     "lce": ["broadcast_gemm_attention_gb300/csrc/lce.cu", "broadcast_gemm_attention_gb300/csrc/ptx.cuh",
             "broadcast_gemm_attention_gb300/csrc/ikbo_internal.h"],
 }

@@ -461,7 +461,8 @@ ikbo_status_t ikbo_qcache_load(ikbo_plan_t p, const void* data, int n_pages, int
  * later call grows it, until the plan is destroyed, so the captured call stays valid.  Calls and replayed
  * graphs of one plan share them and must not overlap on the GPU.  Three variants,
  * chosen from the sizes (Lkv among them): with few query rows per user and K/V
- * head (16, or a little more over short histories) the 4-bit blocks become
+ * head, on average over the request's n_users, whether they have candidates or not
+ * (16, or a little more over short histories), the 4-bit blocks become
  * operands in registers; with up to 1024 they are decoded in shared memory
  * beside the tensor cores' work, once per 128 rows; with more, and a bound Lkv
  * that makes it no more than 8 GiB, histories are decoded once into the
