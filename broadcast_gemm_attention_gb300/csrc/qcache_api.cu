@@ -87,9 +87,9 @@ ikbo_status_t check_table(const int32_t* table, const int32_t* lens, int max_blo
 //   in registers       85   105   190   358   695  (histories decoded once per 8 or 16 rows)
 //   in tiles          126   126   126   130   135  (once per 128 rows)
 // 1024 candidates of 32 queries x 8 heads over 2048 tokens each:
-//   R                 546  1092  2184  4369
-//   in tiles          287   262   255   478 (2048 candidates)
-//   decoded first     338   262   226   396
+//   R                 546  1092  2184  4369 (2048 candidates)
+//   in tiles          281   258   253   497
+//   decoded first     338   248   208   375 (the first with an earlier attention forward, 3% slower)
 // So up to 16 rows in registers, from 1024 on decoded first, between them in
 // tiles, unless the tile kernel's longer start and end (about 12 us) are not
 // made up for: the register kernel gets through 21000 (16-row tile, token,
