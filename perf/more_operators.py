@@ -466,11 +466,11 @@ def _own(s):
     if c["backward"]:
         dQ, dK, dV = rows(), rows(), rows()
         p.linattn_backward(s["Q"], s["K"], s["V"], s["dO"], s["decay"], dQ, dK, dV, state_in=s["S"], d_state_out=s["dS"],
-                           d_state_in=last, offsets=s["offsets"])
+                           d_state_in=last, offsets=s["offsets"], max_len=c["len"])
         return [dQ, dK, dV, last]
     O = rows() if c["queries"] else None
     p.linattn_forward(s["Q"] if c["queries"] else None, s["K"], s["V"], s["decay"], O, state_in=s["S"], state_out=last,
-                      offsets=s["offsets"])
+                      offsets=s["offsets"], max_len=c["len"])
     return [last] if O is None else [O, last]
 
 
