@@ -436,7 +436,7 @@ def _plan(s):
         s["plan"] = _Held(plan)
         if c["op"] == "axes":
             freqs = binding.ikbo_rope_frequencies(c["rot"], base=10000.0)
-            s["rope"] = binding.Rope(c["rot"], freqs, interleaved=c["interleaved"], axes=s["axis"])
+            s["rope"] = binding.Rope(c["rot"], freqs, interleaved=c["interleaved"], axes=s["axis"], n_axes=c["axes"])
     return s["plan"].plan
 
 
