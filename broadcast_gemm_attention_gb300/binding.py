@@ -63,6 +63,16 @@ SIGNATURES = {
     "ikbo_qcache_load": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp]),
     "ikbo_attn_qcache_forward": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _i, ctypes.c_float,
                                       _vp]),
+    "ikbo_rope_create_axes": (_i, [ctypes.POINTER(_vp), _i, _vp, _i, _vp, _i, ctypes.c_float]),
+    "ikbo_rope_axes_forward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, _i, _i, _i, _i, _i, _i, _vp]),
+    "ikbo_rope_axes_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, _i, _i, _i, _i, _i, _i, _vp]),
+    "ikbo_attn_qcache_tree_forward": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp,
+                                           _i, _i, ctypes.c_float, _vp]),
+    "ikbo_linattn_forward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, ctypes.c_float, _vp]),
+    "ikbo_linattn_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   ctypes.c_float, _vp]),
+    "ikbo_linattn_read_forward": (_i, [_vp, _vp, _vp, _vp, _i, ctypes.c_float, _vp]),
+    "ikbo_linattn_read_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, ctypes.c_float, _vp]),
     "ikbo_plan_get_status": (_i, [_vp, _vp]),
     "ikbo_plan_set_debug": (_i, [_vp, ctypes.c_uint]),
     "ikbo_plan_set_timeout_ns": (_i, [_vp, _u64]),
@@ -398,6 +408,23 @@ def ikbo_rope_create(rot_dim: int, freqs, interleaved: bool = False, magnitude: 
     return h.value
 
 
+def ikbo_rope_create_axes(rot_dim: int, freqs, axes, interleaved: bool = False, magnitude: float = 1.0,
+                          n_axes: Optional[int] = None) -> int:
+    """A rotation with several axes: axes[j] is the axis of pair j, of n_axes (default: as many
+    as the pairs name)."""
+    if len(freqs) != rot_dim // 2 or len(axes) != rot_dim // 2:
+        raise ValueError(f"freqs and axes must hold rot_dim / 2 = {rot_dim // 2} values")
+    if any(a < 0 or a > 255 for a in axes):
+        raise ValueError("an axis is out of range")
+    table = (ctypes.c_double * max(1, len(freqs)))(*freqs)
+    of = (ctypes.c_uint8 * max(1, len(axes)))(*axes)
+    h = ctypes.c_void_p()
+    _check(load().ikbo_rope_create_axes(ctypes.byref(h), rot_dim, ctypes.addressof(table),
+                                        max(axes, default=0) + 1 if n_axes is None else n_axes,
+                                        ctypes.addressof(of), int(interleaved), magnitude), "ikbo_rope_create_axes")
+    return h.value
+
+
 def ikbo_rope_destroy(rope: int) -> None:
     load().ikbo_rope_destroy(rope)
 
@@ -405,7 +432,8 @@ def ikbo_rope_destroy(rope: int) -> None:
 _I64X3 = ctypes.c_int64 * 3
 
 
-def _rope(fn, name: str, plan: int, rope: int, X: torch.Tensor, Y: torch.Tensor, start, broadcast: bool, stream) -> None:
+def _rope(fn, name: str, plan: int, rope: int, X: torch.Tensor, Y: torch.Tensor, start, broadcast: bool, stream,
+          axes: int = 0, positions: Optional[torch.Tensor] = None) -> None:
     dev = _current_device(X, "input")
     if X.get_device() != dev or Y.get_device() != dev:
         raise ValueError(f"input and output are on {X.device} and {Y.device}, not on the current device")
@@ -428,9 +456,24 @@ def _rope(fn, name: str, plan: int, rope: int, X: torch.Tensor, Y: torch.Tensor,
     sptr = None
     if start is not None:
         sptr = _here(start, torch.int32, "start", dev)
-        if start.dim() != 1 or (not broadcast and start.numel() != n):
+        if axes:
+            if start.dim() != 2 or start.shape[1] != axes or (not broadcast and start.shape[0] != n):
+                raise ValueError(f"start must be [n, {axes}], or [n_users, {axes}] with broadcast")
+        elif start.dim() != 1 or (not broadcast and start.numel() != n):
             raise ValueError("start must be [n], or [n_users] with broadcast")
-    rc = fn(plan, rope, X.data_ptr(), cx, Y.data_ptr(), cy, sptr, broadcast, dtype, n, H, L, d, _raw_stream(stream, dev))
+    if not axes:
+        rc = fn(plan, rope, X.data_ptr(), cx, Y.data_ptr(), cy, sptr, broadcast, dtype, n, H, L, d, _raw_stream(stream, dev))
+    else:
+        pptr, step = None, 0
+        if positions is not None:
+            pptr = _here(positions, torch.int32, "positions", dev)
+            each = tuple(positions.shape)
+            if each == (n, L, axes) or (L == 1 and each == (n, axes)):
+                step = L * axes
+            elif each != (L, axes):
+                raise ValueError(f"positions must be [n, L, {axes}], or [L, {axes}] for all items")
+        rc = fn(plan, rope, X.data_ptr(), cx, Y.data_ptr(), cy, sptr, pptr, step, broadcast, dtype, n, H, L, d,
+                _raw_stream(stream, dev))
     if rc != IKBO_OK:
         raise IkboError(rc, name)
 
@@ -447,6 +490,22 @@ def ikbo_rope_backward(plan: int, rope: int, dY: torch.Tensor, dX: torch.Tensor,
                        broadcast: bool = False, stream=None) -> None:
     """Gradient of ikbo_rope_forward: dX from dY."""
     _rope(load().ikbo_rope_backward, "ikbo_rope_backward", plan, rope, dY, dX, start, broadcast, stream)
+
+
+def ikbo_rope_axes_forward(plan: int, rope: int, axes: int, X: torch.Tensor, Y: torch.Tensor,
+                           positions: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
+                           broadcast: bool = False, stream=None) -> None:
+    """Y = X with pair j of row (i, h, l) turned by (start[i, a] + positions[i, l, a]) f_j,
+    a the pair's axis; positions [n, L, axes], or [L, axes] for all items (with L = 1 and
+    n rows also [n, axes]); start [n, axes], or [n_users, axes] with broadcast."""
+    _rope(load().ikbo_rope_axes_forward, "ikbo_rope_axes_forward", plan, rope, X, Y, start, broadcast, stream, axes, positions)
+
+
+def ikbo_rope_axes_backward(plan: int, rope: int, axes: int, dY: torch.Tensor, dX: torch.Tensor,
+                            positions: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None,
+                            broadcast: bool = False, stream=None) -> None:
+    """Gradient of ikbo_rope_axes_forward: dX from dY."""
+    _rope(load().ikbo_rope_axes_backward, "ikbo_rope_axes_backward", plan, rope, dY, dX, start, broadcast, stream, axes, positions)
 
 
 def ikbo_qcache_bytes(n_pages: int, page: int, H: int) -> int:
@@ -562,6 +621,170 @@ def ikbo_attn_qcache_forward(plan: int, Q: torch.Tensor, data: torch.Tensor, pag
            "ikbo_attn_qcache_forward")
 
 
+def ikbo_attn_qcache_tree_forward(plan: int, Q: torch.Tensor, data: torch.Tensor, page: int, table: torch.Tensor,
+                                  lens: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
+                                  parents: Optional[torch.Tensor], O: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                                  Lkv: Optional[int] = None, scale: Optional[float] = None, stream=None) -> None:
+    """ikbo_attn_qcache_forward for drafts: candidate i's Lq rows also read their ancestors in
+    the draft and themselves, K_new and V_new [n_cand, Lq, H_kv, 128] (rows may be strided,
+    both alike).  parents int32 [n_cand, Lq]: the row above, -1: none, below: the row is
+    not there; None: chains."""
+    dev, bf = _current_device(data, "data"), torch.bfloat16
+    dptr, n_pages, H_kv = _qcache(data, page, dev)
+    tptr, lptr, n_users, max_blocks = _qtable(table, lens, dev)
+    shape = Q.shape
+    if len(shape) != 4 or O.shape != shape or shape[1] % H_kv != 0 or (lse is not None and lse.shape != shape[:3]):
+        raise ValueError("inconsistent attention shapes")
+    n, _, Lq, d = shape
+    if tuple(K_new.shape) != (n, Lq, H_kv, d) or V_new.shape != K_new.shape:
+        raise ValueError("K_new and V_new must be [n_cand, Lq, H_kv, d]")
+    stride = H_kv * d
+    for t, name in ((K_new, "K_new"), (V_new, "V_new")):
+        if t.get_device() != dev or t.dtype is not bf:
+            raise ValueError(f"{name} must be a tensor of bfloat16 on the current CUDA device")
+    if not (K_new.is_contiguous() and V_new.is_contiguous()):
+        stride = K_new.stride(1) if Lq > 1 else K_new.stride(0)
+        for t in (K_new, V_new):
+            if t.stride(3) != 1 or (H_kv > 1 and t.stride(2) != d) or (Lq > 1 and t.stride(1) != stride) or \
+                    (n > 1 and t.stride(0) != Lq * stride):
+                raise ValueError("K_new and V_new must have contiguous heads and one row stride, both alike")
+    if parents is not None and tuple(parents.shape) != (n, Lq):
+        raise ValueError("parents must be [n_cand, Lq]")
+    if Lkv is None:
+        Lkv = n_users * max_blocks * page
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    _check(load().ikbo_attn_qcache_tree_forward(plan, _here(Q, bf, "Q", dev), dptr, n_pages, page, H_kv, tptr, max_blocks, lptr,
+                                                K_new.data_ptr(), V_new.data_ptr(), stride,
+                                                None if parents is None else _here(parents, torch.int32, "parents", dev),
+                                                _here(O, bf, "O", dev),
+                                                None if lse is None else _here(lse, torch.float32, "lse", dev),
+                                                min(max(1, int(Lkv)), 2**31 - 1), d, scale, _raw_stream(stream, dev)),
+           "ikbo_attn_qcache_tree_forward")
+
+
+def _lin_rows(tensors, names, dev: int, shape):
+    """Pointers and row strides of [rows, H, d] tensors whose rows may be strided (None: NULL)."""
+    ptrs, strides = [], []
+    H, d = shape[1], shape[2]
+    for t, name in zip(tensors, names):
+        if t is None:
+            ptrs.append(None)
+            strides.append(H * d)
+            continue
+        if t.get_device() != dev or t.dtype is not torch.bfloat16:
+            raise ValueError(f"{name} must be a tensor of bfloat16 on the current CUDA device")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be [rows, H, d], alike for all")
+        if t.is_contiguous():
+            strides.append(H * d)
+        else:
+            if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+                raise ValueError(f"the heads of a row of {name} must be contiguous")
+            strides.append(t.stride(0) if shape[0] > 1 else H * d)
+        ptrs.append(t.data_ptr())
+    return ptrs, (ctypes.c_int64 * len(strides))(*strides)
+
+
+def _lin_states(states, names, decay: torch.Tensor, offsets: Optional[torch.Tensor], n_users: Optional[int], dev: int, H: int,
+                d: int):
+    """The number of users, and pointers of the states given, the decay and the offsets."""
+    f32 = torch.float32
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 2 or (n_users is not None and offsets.numel() != n_users + 1):
+            raise ValueError("offsets must be [n_users + 1]")
+        n_users = offsets.numel() - 1
+    for t, name in zip(states, names):
+        if t is not None:
+            if n_users is None:
+                n_users = t.shape[0]
+            if tuple(t.shape) != (n_users, H, d, d):
+                raise ValueError(f"{name} must be [n_users, H, d, d]")
+    if n_users is None:
+        raise ValueError("the number of users must follow from offsets, a state or n_users")
+    if tuple(decay.shape) != (H,):
+        raise ValueError("decay must be [H]")
+    ptrs = [None if t is None else _here(t, f32, name, dev) for t, name in zip(states, names)]
+    return n_users, ptrs, _here(decay, f32, "decay", dev), None if offsets is None else _here(offsets, torch.int32, "offsets", dev)
+
+
+def ikbo_linattn_forward(plan: int, Q: Optional[torch.Tensor], K: torch.Tensor, V: torch.Tensor, decay: torch.Tensor,
+                         O: Optional[torch.Tensor], state_in: Optional[torch.Tensor] = None,
+                         state_out: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
+                         n_users: Optional[int] = None, max_len: int = 0, scale: Optional[float] = None, stream=None) -> None:
+    """Linear attention with a decay for each head, S_t = decay S_{t-1} + k_t v_t^T and
+    O_t = scale q_t S_t, over each user's rows of Q, K, V, O [rows, H, 128] (rows may be strided)
+    from state_in to state_out [n_users, H, 128, 128] (fp32; either may be None, or the same).
+    offsets [n_users + 1]: the users' rows; None: equally many each.  Q and O None: the states alone.
+    max_len: a bound on a user's rows (0: all)."""
+    dev = _current_device(K, "K")
+    shape = K.shape
+    if len(shape) != 3:
+        raise ValueError("K must be [rows, H, d]")
+    (q, k, v, o), strides = _lin_rows((Q, K, V, O), ("Q", "K", "V", "O"), dev, shape)
+    n_users, (si, so), dptr, optr = _lin_states((state_in, state_out), ("state_in", "state_out"), decay, offsets, n_users, dev,
+                                                shape[1], shape[2])
+    if scale is None:
+        scale = 1.0 / math.sqrt(shape[2])
+    _check(load().ikbo_linattn_forward(plan, q, k, v, strides, optr, n_users, shape[0], int(max_len), shape[1], shape[2], dptr, si,
+                                       so, o, scale, _raw_stream(stream, dev)), "ikbo_linattn_forward")
+
+
+def ikbo_linattn_backward(plan: int, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, dO: torch.Tensor, decay: torch.Tensor,
+                          dQ: Optional[torch.Tensor] = None, dK: Optional[torch.Tensor] = None,
+                          dV: Optional[torch.Tensor] = None, state_in: Optional[torch.Tensor] = None,
+                          d_state_out: Optional[torch.Tensor] = None, d_state_in: Optional[torch.Tensor] = None,
+                          offsets: Optional[torch.Tensor] = None, n_users: Optional[int] = None, max_len: int = 0,
+                          scale: Optional[float] = None, stream=None) -> None:
+    """Gradients of ikbo_linattn_forward for upstream dO and d_state_out (None: zero): any of
+    dQ, dK, dV (bf16, like Q) and d_state_in (fp32); overwritten."""
+    dev = _current_device(K, "K")
+    shape = K.shape
+    if len(shape) != 3:
+        raise ValueError("K must be [rows, H, d]")
+    ptrs, strides = _lin_rows((Q, K, V, dO, dQ, dK, dV), ("Q", "K", "V", "dO", "dQ", "dK", "dV"), dev, shape)
+    n_users, (si, dso, dsi), dptr, optr = _lin_states((state_in, d_state_out, d_state_in),
+                                                      ("state_in", "d_state_out", "d_state_in"), decay, offsets, n_users, dev,
+                                                      shape[1], shape[2])
+    if scale is None:
+        scale = 1.0 / math.sqrt(shape[2])
+    _check(load().ikbo_linattn_backward(plan, *ptrs[:4], strides, optr, n_users, shape[0], int(max_len), shape[1], shape[2], dptr,
+                                        si, dso, *ptrs[4:], dsi, scale, _raw_stream(stream, dev)), "ikbo_linattn_backward")
+
+
+def ikbo_linattn_read_forward(plan: int, Q: torch.Tensor, state: torch.Tensor, O: torch.Tensor,
+                              scale: Optional[float] = None, stream=None) -> None:
+    """O[i,h] = scale Q[i,h] S[map[i],h] for the planned request: Q, O [n_cand, H, Lq, 128],
+    state fp32 [n_users, H, 128, 128].  O may be Q."""
+    dev, bf = _current_device(Q, "Q"), torch.bfloat16
+    d = Q.shape[-1]
+    if Q.dim() != 4 or O.shape != Q.shape or state.dim() != 4 or tuple(state.shape[1:]) != (Q.shape[1], d, d):
+        raise ValueError("inconsistent shapes")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    _check(load().ikbo_linattn_read_forward(plan, _here(Q, bf, "Q", dev), _here(state, torch.float32, "state", dev),
+                                            _here(O, bf, "O", dev), d, scale, _raw_stream(stream, dev)),
+           "ikbo_linattn_read_forward")
+
+
+def ikbo_linattn_read_backward(plan: int, Q: Optional[torch.Tensor], state: Optional[torch.Tensor], dO: torch.Tensor,
+                               dQ: Optional[torch.Tensor] = None, d_state: Optional[torch.Tensor] = None,
+                               scale: Optional[float] = None, stream=None) -> None:
+    """Gradients of ikbo_linattn_read_forward: dQ (bf16) and d_state (fp32, summed over each
+    user's candidates), either or both."""
+    dev, bf, f32 = _current_device(dO, "dO"), torch.bfloat16, torch.float32
+    d = dO.shape[-1]
+    if dO.dim() != 4 or any(t is not None and t.shape != dO.shape for t in (Q, dQ)) or \
+            any(t is not None and (t.dim() != 4 or tuple(t.shape[1:]) != (dO.shape[1], d, d)) for t in (state, d_state)):
+        raise ValueError("inconsistent shapes")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    opt = lambda t, dtype, name: None if t is None else _here(t, dtype, name, dev)  # noqa: E731
+    _check(load().ikbo_linattn_read_backward(plan, opt(Q, bf, "Q"), opt(state, f32, "state"), _here(dO, bf, "dO", dev),
+                                             opt(dQ, bf, "dQ"), opt(d_state, f32, "d_state"), d, scale,
+                                             _raw_stream(stream, dev)), "ikbo_linattn_read_backward")
+
+
 def ikbo_plan_get_status(plan: int, stream=None) -> int:
     """Synchronises the stream; returns the device-detected status code (and clears it)."""
     return int(load().ikbo_plan_get_status(plan, _stream(stream)))
@@ -665,6 +888,48 @@ class Plan:
             raise ValueError("Q and lens must have the sizes of the planned request")
         ikbo_attn_qcache_forward(self.handle, Q, data, page, table, lens, O, lse, Lkv, scale, stream)
 
+    def _check_start_axes(self, rope, start, broadcast):
+        if not rope.axes:
+            raise ValueError("the rotation has no axes")
+        if broadcast and start is not None and self._request is not None and start.shape[0] != self._request[1]:
+            raise ValueError(f"with broadcast, start must hold positions for each of the plan's {self._request[1]} users")
+
+    def rope_axes_forward(self, rope, X, Y, positions=None, start=None, broadcast=False, stream=None):
+        self._check_start_axes(rope, start, broadcast)
+        ikbo_rope_axes_forward(self.handle, rope.handle, rope.axes, X, Y, positions, start, broadcast, stream)
+
+    def rope_axes_backward(self, rope, dY, dX, positions=None, start=None, broadcast=False, stream=None):
+        self._check_start_axes(rope, start, broadcast)
+        ikbo_rope_axes_backward(self.handle, rope.handle, rope.axes, dY, dX, positions, start, broadcast, stream)
+
+    def attn_qcache_tree_forward(self, Q, data, page, table, lens, K_new, V_new, parents, O, lse=None, Lkv=None, scale=None,
+                                 stream=None):
+        if self._request is not None and (Q.shape[:3] != self._request[0] or lens.numel() != self._request[1]):
+            raise ValueError("Q and lens must have the sizes of the planned request")
+        ikbo_attn_qcache_tree_forward(self.handle, Q, data, page, table, lens, K_new, V_new, parents, O, lse, Lkv, scale, stream)
+
+    def linattn_forward(self, Q, K, V, decay, O, state_in=None, state_out=None, offsets=None, n_users=None, max_len=0,
+                        scale=None, stream=None):
+        ikbo_linattn_forward(self.handle, Q, K, V, decay, O, state_in, state_out, offsets, n_users, max_len, scale, stream)
+
+    def linattn_backward(self, Q, K, V, dO, decay, dQ=None, dK=None, dV=None, state_in=None, d_state_out=None,
+                         d_state_in=None, offsets=None, n_users=None, max_len=0, scale=None, stream=None):
+        ikbo_linattn_backward(self.handle, Q, K, V, dO, decay, dQ, dK, dV, state_in, d_state_out, d_state_in, offsets, n_users,
+                              max_len, scale, stream)
+
+    def _check_read(self, like, *states):
+        if self._request is not None and (like.shape[:3] != self._request[0] or
+                                          any(t is not None and t.shape[0] != self._request[1] for t in states)):
+            raise ValueError("queries and states must have the sizes of the planned request")
+
+    def linattn_read_forward(self, Q, state, O, scale=None, stream=None):
+        self._check_read(Q, state)
+        ikbo_linattn_read_forward(self.handle, Q, state, O, scale, stream)
+
+    def linattn_read_backward(self, Q, state, dO, dQ=None, d_state=None, scale=None, stream=None):
+        self._check_read(dO, state, d_state)
+        ikbo_linattn_read_backward(self.handle, Q, state, dO, dQ, d_state, scale, stream)
+
     def status(self, stream=None) -> int:
         return ikbo_plan_get_status(self.handle, stream)
 
@@ -688,12 +953,19 @@ class Plan:
 
 class Rope:
     """Owns one ikbo_rope_t: the first rot_dim elements of a head, rotated by freqs
-    (radians per position; ikbo_rope_frequencies makes the usual ones)."""
+    (radians per position; ikbo_rope_frequencies makes the usual ones).  axes: the axis of
+    each pair (of n_axes), for rope_axes_forward and rope_axes_backward."""
 
-    def __init__(self, rot_dim: int, freqs=None, interleaved: bool = False, magnitude: float = 1.0):
+    def __init__(self, rot_dim: int, freqs=None, interleaved: bool = False, magnitude: float = 1.0, axes=None,
+                 n_axes: Optional[int] = None):
         self.handle = None
-        self.handle = ikbo_rope_create(rot_dim, ikbo_rope_frequencies(rot_dim) if freqs is None else freqs, interleaved,
-                                       magnitude)
+        self.axes = 0 if axes is None else max(axes, default=0) + 1 if n_axes is None else n_axes
+        if freqs is None:
+            freqs = ikbo_rope_frequencies(rot_dim)
+        if axes is None:
+            self.handle = ikbo_rope_create(rot_dim, freqs, interleaved, magnitude)
+        else:
+            self.handle = ikbo_rope_create_axes(rot_dim, freqs, axes, interleaved, magnitude, n_axes)
 
     def __del__(self):
         try:

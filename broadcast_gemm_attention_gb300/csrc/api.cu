@@ -133,6 +133,9 @@ void free_plan(ikbo_plan_t p) {
   cudaFree(p->qa_kv.ptr);
   cudaFree(p->qa_list.ptr);
   cudaFree(p->qa_ranges.ptr);
+  cudaFree(p->qa_lse.ptr);
+  cudaFree(p->lin_states.ptr);
+  cudaFree(p->lin_part.ptr);
   for (int i = 0; i < p->n_retired; ++i) cudaFree(p->retired[i]);
   std::free(p->retired);
   delete p;

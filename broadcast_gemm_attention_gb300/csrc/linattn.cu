@@ -1,0 +1,390 @@
+// linattn.cu -- linear attention with a decay for each head: whole histories
+// in chunks, single tokens, and the gradient.
+//
+//   S_t = decay S_{t-1} + k_t v_t^T,   o_t = scale q_t S_t
+//
+// In chunks of C rows (S the state before the chunk, i and j counted in it):
+//   o_i = scale ( sum_{j <= i} decay^(i-j) (q_i.k_j) v_j + decay^(i+1) q_i S )
+//   S  <- decay^n S + sum_j decay^(n-1-j) k_j v_j^T        (n rows in the chunk)
+//
+// The gradient is three scans of the same kind.  With
+//   R_t = sum_{i >= t} decay^(i-t) scale q_i do_i^T + decay^(T-t) dS_T,
+//   dq_t = scale S_t do_t     a scan with queries do, keys v, values k,
+//   dk_t = R_t v_t            from the last row on: queries v, keys do, values q,
+//   dv_t = R_t^T k_t          from the last row on: queries k, keys q, values do,
+// and the gradient of the first state is decay R_1, the last one's end.  So one
+// kernel does all of it, three jobs a launch; nothing but the inputs is kept
+// from the forward pass.
+#include <cuda_bf16.h>
+
+#include "linattn_internal.h"
+#include "mma_common.cuh"
+
+namespace ikbo {
+namespace {
+
+constexpr int LIN_CHUNK = 64;
+constexpr int LIN_THREADS = 256;
+constexpr int LIN_TILE = LIN_CHUNK * LIN_D * 2;  // bytes of a chunk of x, y or z
+constexpr int LIN_STAGES = 2;
+
+// decay^n, n >= 0 (decay^0 = 1 for any decay).
+__device__ __forceinline__ float lin_power(float log2_decay, int n) {
+  return n == 0 ? 1.f : exp2f(static_cast<float>(n) * log2_decay);
+}
+
+// The rows of user u; none, and a report, where the offsets are out of range.
+__device__ __forceinline__ int lin_rows(const LinParams& p, int u, int& first) {
+  if (!p.offsets) {
+    const int each = p.n_rows / p.n_users;
+    first = u * each;
+    return each;
+  }
+  const int a = __ldg(p.offsets + u), b = __ldg(p.offsets + u + 1);
+  if (a < 0 || b < a || b > p.n_rows || b - a > p.max_len) {
+    if (threadIdx.x == 0) atomicOr(p.status, DEV_ERR_CACHE);
+    first = 0;
+    return 0;
+  }
+  first = a;
+  return b - a;
+}
+
+// Place of 16-byte piece c of row r in a tile of 256-byte rows: eight rows' same
+// pieces lie in different banks.
+__device__ __forceinline__ uint32_t tile_at(int r, int c) { return static_cast<uint32_t>(r * 256 + ((c ^ (r & 7)) << 4)); }
+
+struct LinShared {
+  float power[LIN_CHUNK + 1];  // decay^n
+};
+
+// kOutputs: with queries; else the states alone.  kLocal: a segment's own part
+// of its end state, from zero, to the workspace.
+template <bool kOutputs, bool kLocal>
+__global__ void __launch_bounds__(LIN_THREADS, 1) lin_chunk_kernel(const __grid_constant__ LinParams p) {
+  extern __shared__ __align__(128) uint8_t lin_sm[];
+  __shared__ LinShared sh;
+  constexpr int kTiles = kOutputs ? 3 : 2;  // y, z, x
+  constexpr int kStage = kTiles * LIN_TILE;
+  const uint32_t base = smem_u32(lin_sm), probs = base + LIN_STAGES * kStage;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int item = static_cast<int>(blockIdx.x) / p.segs, seg = static_cast<int>(blockIdx.x) - item * p.segs;
+  const int u = item / p.H, h = item - u * p.H;
+  const LinJob& job = p.job[blockIdx.y];
+
+  int first_row;
+  const int len = lin_rows(p, u, first_row);
+  const int segs = p.segs > 1 ? max(1, (len + p.seg_len - 1) / p.seg_len) : 1;
+  if (seg >= segs || (kLocal && seg + 1 >= segs)) return;
+  const int r0 = seg * (p.segs > 1 ? p.seg_len : 0);                    // of the scan's order
+  const int n = segs > 1 ? min(p.seg_len, len - r0) : len;
+  const float log2_decay = log2f(__ldg(p.decay + h));
+  if (tid <= LIN_CHUNK) sh.power[tid] = lin_power(log2_decay, tid);
+
+  // rows r0 .. r0 + n - 1 of the scan's order, as rows of the tensors
+  const int64_t dir = job.reverse ? -1 : 1;
+  const int64_t row_at = static_cast<int64_t>(first_row) + (job.reverse ? len - 1 - r0 : r0);
+  const auto load_tile = [&](const uint16_t* src, int64_t stride, uint32_t dst, int c0) {
+#pragma unroll
+    for (int k = 0; k < LIN_TILE / 16 / LIN_THREADS; ++k) {
+      const int i = k * LIN_THREADS + tid, r = i >> 4, c = i & 15;
+      const bool there = c0 + r < n;
+      copy16(dst + tile_at(r, c), there ? src + (row_at + dir * (c0 + r)) * stride + h * LIN_D + c * 8 : src, there);
+    }
+  };
+  const auto load_stage = [&](int stage, int c0) {
+    const uint32_t at = base + stage * kStage;
+    load_tile(job.y, job.ys, at, c0);
+    load_tile(job.z, job.zs, at + LIN_TILE, c0);
+    if (kOutputs) load_tile(job.x, job.xs, at + 2 * LIN_TILE, c0);
+  };
+  const int chunks = (n + LIN_CHUNK - 1) / LIN_CHUNK;
+  if (chunks > 0) load_stage(0, 0);
+  copies_commit();
+
+  // the state, turned: row m of s[i] is z's element 16 warp + m, columns y's 8 i ..
+  float s[16][4];
+  const int64_t state = (static_cast<int64_t>(u) * p.H + h) * LIN_STATE;
+  const int64_t ws = ((static_cast<int64_t>(blockIdx.y) * p.n_users + u) * p.H + h) * p.segs;
+  const float* from = nullptr;
+  if (!kLocal) {  // of several segments the first one's start is in the workspace too, as s_out may be s_in
+    if (segs > 1) from = p.ws + (ws + (seg > 0 ? seg - 1 : segs - 1)) * LIN_STATE;
+    else if (job.s_in) from = job.s_in + state;
+  }
+  const float factor = segs > 1 ? 1.f : job.s_in_factor;
+  const int e0 = 16 * warp + g;
+  if (from && (segs > 1 || !job.s_in_turned)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[i][k] = __ldcg(from + (8 * i + 2 * t + (k & 1)) * LIN_D + e0 + 8 * (k >> 1)) * factor;
+  } else if (from) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(from + (e0 + 8 * k) * LIN_D + 8 * i + 2 * t));
+        s[i][2 * k] = v.x * factor;
+        s[i][2 * k + 1] = v.y * factor;
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
+  }
+  // a reverse scan's start is taken as it is by its first row
+  int early = !kLocal && seg == 0 && job.reverse ? 1 : 0;
+
+#pragma unroll 1
+  for (int ch = 0; ch < chunks; ++ch) {
+    const int c0 = ch * LIN_CHUNK, rows = min(LIN_CHUNK, n - c0);
+    if (ch + 1 < chunks) load_stage((ch + 1) & 1, c0 + LIN_CHUNK);
+    copies_commit();
+    copies_wait<1>();
+    __syncthreads();
+    const uint32_t y_at = base + (ch & 1) * kStage, z_at = y_at + LIN_TILE, x_at = y_at + 2 * LIN_TILE;
+    if (kOutputs) {
+      // A = x y^T with decay^(i-j), rows 16 (warp / 2) .., columns 32 (warp % 2) .., to shared memory
+      const int rb = 16 * (warp >> 1), cb = 32 * (warp & 1);
+      if (cb <= rb + 15) {
+        float a[4][4] = {};
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          uint32_t xf[4];
+          ldsm4(xf, x_at + tile_at(rb + (lane & 15), 2 * kk + (lane >> 4)));
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t yf[4];
+            ldsm4(yf, y_at + tile_at(cb + 16 * half + (lane & 7) + 8 * (lane >> 4), 2 * kk + ((lane >> 3) & 1)));
+            mma_16816(a[2 * half], xf, yf[0], yf[1]);
+            mma_16816(a[2 * half + 1], xf, yf[2], yf[3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int row = rb + g + 8 * k, gap = row - (cb + 8 * i + 2 * t);
+            const float w0 = gap >= 0 ? a[i][2 * k] * sh.power[gap] : 0.f;
+            const float w1 = gap >= 1 ? a[i][2 * k + 1] * sh.power[gap - 1] : 0.f;
+            const int piece = (cb >> 3) + i;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(probs + row * 128 + ((piece ^ (row & 7)) << 4) + 4 * t), "r"(pack_bf16x2(w0, w1))
+                         : "memory");
+          }
+      }
+      __syncthreads();
+    }
+    // z's columns 16 warp .. of 16 rows each: A of the state's product, B of the outputs'
+    uint32_t zf[4][4];
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb)  // matrices: (columns 0-7, rows 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+      ldsm4_t(zf[kb], z_at + tile_at(16 * kb + (lane & 7) + 8 * (lane >> 4), 2 * warp + ((lane >> 3) & 1)));
+    if (kOutputs) {
+      uint32_t sb[16][2];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        sb[i][0] = pack_bf16x2(s[i][0], s[i][1]);
+        sb[i][1] = pack_bf16x2(s[i][2], s[i][3]);
+      }
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        float o[2][4] = {};
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          uint32_t xf[4];
+          ldsm4(xf, x_at + tile_at(16 * mt + (lane & 15), 2 * kk + (lane >> 4)));
+          mma_16816(o[0], xf, sb[2 * kk][0], sb[2 * kk + 1][0]);
+          mma_16816(o[1], xf, sb[2 * kk][1], sb[2 * kk + 1][1]);
+        }
+        const int row = 16 * mt + g;
+        const float w0 = sh.power[row + 1 - early], w1 = sh.power[row + 9 - early];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          o[e][0] *= w0;
+          o[e][1] *= w0;
+          o[e][2] *= w1;
+          o[e][3] *= w1;
+        }
+#pragma unroll
+        for (int kb = 0; kb <= mt; ++kb) {
+          uint32_t pf[4];
+          const int r = 16 * mt + (lane & 15);
+          ldsm4(pf, probs + r * 128 + (((2 * kb + (lane >> 4)) ^ (r & 7)) << 4));
+          mma_16816(o[0], pf, zf[kb][0], zf[kb][2]);
+          mma_16816(o[1], pf, zf[kb][1], zf[kb][3]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = row + 8 * k;
+          if (r >= rows || !job.out) continue;
+          uint16_t* dst = job.out + (row_at + dir * (c0 + r)) * job.os + h * LIN_D + 16 * warp + 2 * t;
+          *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0][2 * k] * p.scale, o[0][2 * k + 1] * p.scale);
+          *reinterpret_cast<uint32_t*>(dst + 8) = pack_bf16x2(o[1][2 * k] * p.scale, o[1][2 * k + 1] * p.scale);
+        }
+      }
+    }
+    // the state: decayed, and z^T y with each row's decay on z, to 16 bits of mantissa
+    const float down = sh.power[rows - early];
+    early = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[i][k] *= down;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      if (16 * kb >= rows) break;
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = rows - 1 - (16 * kb + 2 * t + 8 * (k >> 1));
+        split_bf16x2(bf16_lo(zf[kb][k]) * sh.power[max(j, 0)], bf16_hi(zf[kb][k]) * sh.power[max(j - 1, 0)], hi[k], lo[k]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t yf[4];
+        ldsm4_t(yf, y_at + tile_at(16 * kb + (lane & 15), 2 * i + (lane >> 4)));
+        mma_16816(s[2 * i], hi, yf[0], yf[1]);
+        mma_16816(s[2 * i + 1], hi, yf[2], yf[3]);
+        mma_16816(s[2 * i], lo, yf[0], yf[1]);
+        mma_16816(s[2 * i + 1], lo, yf[2], yf[3]);
+      }
+    }
+    __syncthreads();  // the stage is loaded again
+  }
+
+  float* to = kLocal ? p.ws + (ws + seg) * LIN_STATE : (seg + 1 == segs && job.s_out ? job.s_out + state : nullptr);
+  if (!to) return;
+  float up = 1.f;
+  if (!kLocal) up = len > 0 && job.reverse ? job.s_out_factor * sh.power[1] : job.s_out_factor;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) to[(8 * i + 2 * t + (k & 1)) * LIN_D + e0 + 8 * (k >> 1)] = s[i][k] * up;
+}
+
+// The states at the segments' ends, from the segments' own parts (in the last
+// one's place, which has no part, the start).
+__global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ LinParams p) {
+  constexpr int kParts = LIN_STATE / 256;
+  const int item = static_cast<int>(blockIdx.x) / kParts;
+  const int u = item / p.H, h = item - u * p.H;
+  const LinJob& job = p.job[blockIdx.y];
+  int first;
+  const int len = lin_rows(p, u, first);
+  const int segs = max(1, (len + p.seg_len - 1) / p.seg_len);
+  if (segs == 1) return;
+  const int e = (static_cast<int>(blockIdx.x) - item * kParts) * 256 + threadIdx.x;
+  const int64_t state = (static_cast<int64_t>(u) * p.H + h) * LIN_STATE;
+  float* ws = p.ws + ((static_cast<int64_t>(blockIdx.y) * p.n_users + u) * p.H + h) * p.segs * LIN_STATE + e;
+  float s = 0.f;
+  if (job.s_in) s = job.s_in[state + (job.s_in_turned ? (e % LIN_D) * LIN_D + e / LIN_D : e)] * job.s_in_factor;
+  ws[static_cast<int64_t>(segs - 1) * LIN_STATE] = s;
+  const float log2_decay = log2f(__ldg(p.decay + h));
+  const float down = lin_power(log2_decay, p.seg_len);
+  s *= job.reverse ? lin_power(log2_decay, p.seg_len - 1) : down;
+#pragma unroll 4
+  for (int k = 0; k + 1 < segs; ++k) {
+    s += ws[static_cast<int64_t>(k) * LIN_STATE];
+    ws[static_cast<int64_t>(k) * LIN_STATE] = s;
+    s *= down;
+  }
+}
+
+// Few rows a user: the state through registers once, a row at a time.  A warp
+// has 16 of the state's rows (y's elements), a lane 4 of its columns.
+template <bool kOutputs>
+__global__ void __launch_bounds__(LIN_THREADS) lin_step_kernel(const __grid_constant__ LinParams p) {
+  __shared__ float part[2][8][LIN_D];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int u = static_cast<int>(blockIdx.x) / p.H, h = static_cast<int>(blockIdx.x) - u * p.H;
+  const LinJob& job = p.job[0];
+  int row;
+  const int len = lin_rows(p, u, row);
+  const int64_t state = (static_cast<int64_t>(u) * p.H + h) * LIN_STATE;
+  float* to = job.s_out ? job.s_out + state : nullptr;
+  const float* from = job.s_in ? job.s_in + state : nullptr;
+  if (len == 0 && (!to || to == from)) return;
+  float4 s[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    s[k] = from ? reinterpret_cast<const float4*>(from)[(16 * warp + k) * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float decay = __ldg(p.decay + h);
+#pragma unroll 1
+  for (int r = 0; r < len; ++r) {
+    const int64_t at = static_cast<int64_t>(row + r);
+    const uint2 zv = *reinterpret_cast<const uint2*>(job.z + at * job.zs + h * LIN_D + 4 * lane);
+    const uint32_t yv = reinterpret_cast<const uint16_t*>(job.y + at * job.ys + h * LIN_D + 16 * warp)[lane & 15];
+    const uint32_t xv = kOutputs ? reinterpret_cast<const uint16_t*>(job.x + at * job.xs + h * LIN_D + 16 * warp)[lane & 15] : 0u;
+    const float z0 = bf16_lo(zv.x), z1 = bf16_hi(zv.x), z2 = bf16_lo(zv.y), z3 = bf16_hi(zv.y);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float y = bf16_lo(__shfl_sync(0xffffffffu, yv, k));
+      s[k].x = fmaf(y, z0, s[k].x * decay);
+      s[k].y = fmaf(y, z1, s[k].y * decay);
+      s[k].z = fmaf(y, z2, s[k].z * decay);
+      s[k].w = fmaf(y, z3, s[k].w * decay);
+      if (kOutputs) {
+        const float x = bf16_lo(__shfl_sync(0xffffffffu, xv, k));
+        o.x = fmaf(x, s[k].x, o.x);
+        o.y = fmaf(x, s[k].y, o.y);
+        o.z = fmaf(x, s[k].z, o.z);
+        o.w = fmaf(x, s[k].w, o.w);
+      }
+    }
+    if (kOutputs) {
+      reinterpret_cast<float4*>(part[r & 1][warp])[lane] = o;
+      __syncthreads();  // (the other half is written next)
+      if (tid < LIN_D) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) sum += part[r & 1][w][tid];
+        reinterpret_cast<__nv_bfloat16*>(job.out)[at * job.os + h * LIN_D + tid] = __float2bfloat16_rn(sum * p.scale);
+      }
+    }
+  }
+  if (!to) return;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) reinterpret_cast<float4*>(to)[(16 * warp + k) * 32 + lane] = s[k];
+}
+
+template <bool kOutputs, bool kLocal>
+cudaError_t launch_chunks(const LinParams& p, cudaStream_t s) {
+  constexpr int smem = LIN_STAGES * (kOutputs ? 3 : 2) * LIN_TILE + (kOutputs ? LIN_CHUNK * LIN_CHUNK * 2 : 0);
+  const cudaError_t e = cudaFuncSetAttribute(lin_chunk_kernel<kOutputs, kLocal>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(p.segs * p.n_users * p.H), static_cast<unsigned>(p.n_jobs));
+  lin_chunk_kernel<kOutputs, kLocal><<<grid, LIN_THREADS, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Launches: one, or three where histories are cut into segments.
+cudaError_t launch_linattn(const LinParams& p, cudaStream_t s, int* launches) {
+  *launches = 0;
+  const bool outputs = p.job[0].x != nullptr;
+  cudaError_t e;
+  if (p.steps) {
+    const unsigned grid = static_cast<unsigned>(p.n_users * p.H);
+    if (outputs) lin_step_kernel<true><<<grid, LIN_THREADS, 0, s>>>(p);
+    else lin_step_kernel<false><<<grid, LIN_THREADS, 0, s>>>(p);
+    *launches = 1;
+    return cudaGetLastError();
+  }
+  if (p.segs > 1) {
+    e = launch_chunks<false, true>(p, s);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(LIN_STATE / 256 * p.n_users * p.H), static_cast<unsigned>(p.n_jobs));
+    lin_join_kernel<<<grid, 256, 0, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    *launches += 2;
+  }
+  e = outputs ? launch_chunks<true, false>(p, s) : launch_chunks<false, false>(p, s);
+  *launches += e == cudaSuccess;
+  return e;
+}
+
+}  // namespace ikbo

@@ -1,0 +1,246 @@
+// linattn_api.cu -- host side of linear attention with a decay and of the
+// candidates' reads of its states (declared in ikbo.h): argument checks,
+// workspaces and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "linattn_internal.h"
+#include "plan_internal.h"
+
+namespace ikbo {
+cudaError_t launch_linattn(const LinParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_lin_read(const LinReadParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_lin_read_state(const LinReadParams& p, int num_sms, cudaStream_t s);
+int lin_read_ctas(int num_sms);
+}  // namespace ikbo
+
+using namespace ikbo;
+
+namespace {
+
+constexpr size_t ANY = ~size_t{0};
+constexpr int64_t INT32_LIMIT = 0x7fffffff;
+
+// A row stride of H heads of 128 elements, 16-byte pieces.
+ikbo_status_t check_stride(int64_t stride, int H) {
+  if (stride < static_cast<int64_t>(H) * LIN_D) return IKBO_ERR_INVALID_ARG;
+  return stride % 8 != 0 ? IKBO_ERR_UNSUPPORTED : IKBO_OK;
+}
+
+// What forward and backward check alike, and the parameters that they share.
+ikbo_status_t lin_params(ikbo_plan_t p, const int32_t* d_offsets, int n_users, int n_rows, int max_len, int H, int d,
+                         const float* decay, float scale, LinParams* lp) {
+  if (n_users < 1 || n_rows < 0 || max_len < 0 || H < 1 || !decay || !aligned4(decay) || !aligned4(d_offsets) || !(scale > 0.f) ||
+      !std::isfinite(scale) || !std::isfinite(1.f / scale))
+    return IKBO_ERR_INVALID_ARG;
+  if (d != LIN_D || n_users > SEG_MAX_USERS || H > 1024) return IKBO_ERR_UNSUPPORTED;
+  if (!d_offsets && n_rows % n_users != 0) return IKBO_ERR_INVALID_ARG;
+  if (!p || !plan_device_current(p)) return IKBO_ERR_INVALID_ARG;
+  std::memset(lp, 0, sizeof(*lp));
+  lp->offsets = d_offsets;
+  lp->decay = decay;
+  lp->status = p->d_status;
+  lp->n_users = n_users;
+  lp->n_rows = n_rows;
+  lp->H = H;
+  lp->max_len = d_offsets ? (max_len > 0 ? std::min(max_len, n_rows) : n_rows) : n_rows / n_users;
+  lp->scale = scale;
+  lp->segs = 1;
+  return IKBO_OK;
+}
+
+// Whether, and into what, long histories are cut.  A scan is one CTA's, so a few
+// long ones leave SMs idle; cut into segments each one's keys and values are read
+// (and multiplied) once more, for the states between them.  With fewer scans than
+// half the SMs, segments are as long as makes one for each SM; else only rows far
+// above a CTA's share are cut, as where one user's history is much longer than the
+// others'.  At most LIN_MOST_STATES states lie between segments.
+constexpr int64_t LIN_MOST_STATES = 16384;  // 1 GiB
+constexpr int LIN_LEAST_SEGMENT = 256;
+
+void cut_segments(LinParams* lp, int num_sms) {
+  const int64_t items = static_cast<int64_t>(lp->n_users) * lp->H * lp->n_jobs;
+  const int64_t share = static_cast<int64_t>(lp->n_rows) * lp->H * lp->n_jobs / num_sms;  // rows of a CTA
+  int64_t seg = std::max<int64_t>(items * 2 <= num_sms ? share : 4 * share, LIN_LEAST_SEGMENT);
+  const int64_t most = LIN_MOST_STATES / items;  // segments of a user
+  if (most < 2) return;
+  seg = std::max(seg, (lp->max_len + most - 1) / most);
+  seg = (seg + 63) / 64 * 64;
+  if (lp->max_len <= seg + seg / 2) return;
+  lp->seg_len = static_cast<int>(seg);
+  lp->segs = static_cast<int>((lp->max_len + seg - 1) / seg);
+}
+
+ikbo_status_t lin_run(ikbo_plan_t p, LinParams* lp, cudaStream_t stream) {
+  if (static_cast<int64_t>(lp->n_users) * lp->H > INT32_LIMIT / 256) return IKBO_ERR_UNSUPPORTED;
+  if (!lp->steps) cut_segments(lp, p->num_sms);
+  if (lp->segs > 1) {
+    bool capturing = false;
+    if (stream && is_capturing(stream, &capturing) != cudaSuccess) return IKBO_ERR_CUDA;
+    const size_t need = static_cast<size_t>(lp->n_jobs) * lp->n_users * lp->H * lp->segs * LIN_STATE;
+    if (grow_kept<false>(p, &p->lin_states, need, ANY, capturing, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+    lp->ws = p->lin_states.ptr;
+  }
+  int launches = 0;
+  const cudaError_t e = launch_linattn(*lp, stream, &launches);
+  p->launches += launches;
+  return e == cudaSuccess ? IKBO_OK : IKBO_ERR_CUDA;
+}
+
+ikbo_status_t read_call(ikbo_plan_t p, const void* x, const float* state, int d, float scale, LinReadParams* rp) {
+  if (!x || !aligned16(x) || !aligned16(state) || !(scale > 0.f) || !std::isfinite(scale)) return IKBO_ERR_INVALID_ARG;
+  if (d != LIN_D) return IKBO_ERR_UNSUPPORTED;
+  if (!p) return IKBO_ERR_INVALID_ARG;
+  if (!p->planned) return IKBO_ERR_NOT_PLANNED;
+  if (!plan_device_current(p)) return IKBO_ERR_INVALID_ARG;
+  std::memset(rp, 0, sizeof(*rp));
+  rp->x = static_cast<const uint16_t*>(x);
+  rp->state = state;
+  rp->offsets = p->d_offsets;
+  rp->perm = p->d_perm;
+  rp->work = p->d_work;
+  rp->n_units = p->d_n_units;
+  rp->status = p->d_status;
+  rp->max_units = p->max_units;
+  rp->n_cand = p->n_cand;
+  rp->n_users = p->n_users;
+  rp->H = p->H;
+  rp->Lq = p->Lq;
+  rp->scale = scale;
+  return IKBO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ikbo_status_t ikbo_linattn_forward(ikbo_plan_t p, const void* Q, const void* K, const void* V, const int64_t* row_strides,
+                                   const int32_t* d_offsets, int n_users, int n_rows, int max_len, int H, int d,
+                                   const float* decay, const float* state_in, float* state_out, void* O, float scale,
+                                   cudaStream_t stream) {
+  if ((Q == nullptr) != (O == nullptr) || (n_rows > 0 && (!K || !V)) || (!O && !state_out)) return IKBO_ERR_INVALID_ARG;
+  const void* ptrs[] = {Q, K, V, O, state_in, state_out};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return IKBO_ERR_INVALID_ARG;
+  if (O && (O == K || O == V || O == Q)) return IKBO_ERR_INVALID_ARG;
+  int64_t strides[4] = {0, 0, 0, 0};
+  for (int k = 0; k < 4; ++k) {
+    strides[k] = row_strides ? row_strides[k] : static_cast<int64_t>(H) * LIN_D;
+    if ((k == 0 || k == 3) && !Q) continue;
+    const ikbo_status_t st = check_stride(strides[k], H);
+    if (st != IKBO_OK) return st;
+  }
+  LinParams lp;
+  ikbo_status_t st = lin_params(p, d_offsets, n_users, n_rows, max_len, H, d, decay, scale, &lp);
+  if (st != IKBO_OK) return st;
+  LinJob& j = lp.job[0];
+  j.x = static_cast<const uint16_t*>(Q);
+  j.y = static_cast<const uint16_t*>(K);
+  j.z = static_cast<const uint16_t*>(V);
+  j.out = static_cast<uint16_t*>(O);
+  j.xs = strides[0];
+  j.ys = strides[1];
+  j.zs = strides[2];
+  j.os = strides[3];
+  j.s_in = state_in;
+  j.s_out = state_out;
+  j.s_in_factor = j.s_out_factor = 1.f;
+  lp.n_jobs = 1;
+  lp.steps = lp.max_len <= LIN_STEP_MOST;
+  return lin_run(p, &lp, stream);
+}
+
+ikbo_status_t ikbo_linattn_backward(ikbo_plan_t p, const void* Q, const void* K, const void* V, const void* dO,
+                                    const int64_t* row_strides, const int32_t* d_offsets, int n_users, int n_rows,
+                                    int max_len, int H, int d, const float* decay, const float* state_in,
+                                    const float* d_state_out, void* dQ, void* dK, void* dV, float* d_state_in, float scale,
+                                    cudaStream_t stream) {
+  const void* in[] = {Q, K, V, dO, state_in, d_state_out};
+  const void* out[] = {dQ, dK, dV, d_state_in};
+  for (int k = 0; k < 4; ++k)
+    if (n_rows > 0 && !in[k]) return IKBO_ERR_INVALID_ARG;
+  if (!dQ && !dK && !dV && !d_state_in) return IKBO_ERR_INVALID_ARG;
+  for (const void* q : in)
+    if (!aligned16(q)) return IKBO_ERR_INVALID_ARG;
+  for (const void* q : out) {
+    if (!aligned16(q)) return IKBO_ERR_INVALID_ARG;
+    for (const void* r : in)
+      if (q && q == r) return IKBO_ERR_INVALID_ARG;
+  }
+  int64_t strides[7];
+  for (int k = 0; k < 7; ++k) {
+    strides[k] = row_strides ? row_strides[k] : static_cast<int64_t>(H) * LIN_D;
+    if (k >= 4 && !out[k - 4]) continue;
+    const ikbo_status_t st = check_stride(strides[k], H);
+    if (st != IKBO_OK) return st;
+  }
+  LinParams lp;
+  ikbo_status_t st = lin_params(p, d_offsets, n_users, n_rows, max_len, H, d, decay, scale, &lp);
+  if (st != IKBO_OK) return st;
+  const auto add = [&](int x, int y, int z, void* o, int os, const float* s_in, bool turned, float* s_out, bool reverse) {
+    LinJob& j = lp.job[lp.n_jobs++];
+    j.x = static_cast<const uint16_t*>(in[x]);
+    j.y = static_cast<const uint16_t*>(in[y]);
+    j.z = static_cast<const uint16_t*>(in[z]);
+    j.out = static_cast<uint16_t*>(o);
+    j.xs = strides[x];
+    j.ys = strides[y];
+    j.zs = strides[z];
+    j.os = strides[os];
+    j.s_in = s_in;
+    j.s_out = s_out;
+    j.s_in_turned = turned;
+    j.reverse = reverse;
+    j.s_in_factor = reverse ? 1.f / scale : 1.f;
+    j.s_out_factor = reverse ? scale : 1.f;
+  };
+  if (dQ) add(3, 2, 1, dQ, 4, state_in, true, nullptr, false);
+  if (dK) add(2, 3, 0, dK, 5, d_state_out, true, nullptr, true);
+  if (dV || d_state_in) add(1, 0, 3, dV, 6, d_state_out, false, d_state_in, true);
+  return lin_run(p, &lp, stream);
+}
+
+ikbo_status_t ikbo_linattn_read_forward(ikbo_plan_t p, const void* Q, const float* state, void* O, int d, float scale,
+                                        cudaStream_t stream) {
+  if (!O || !aligned16(O) || !state) return IKBO_ERR_INVALID_ARG;
+  LinReadParams rp;
+  const ikbo_status_t st = read_call(p, Q, state, d, scale, &rp);
+  if (st != IKBO_OK) return st;
+  rp.out = static_cast<uint16_t*>(O);
+  if (launch_lin_read(rp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+  p->launches++;
+  return IKBO_OK;
+}
+
+ikbo_status_t ikbo_linattn_read_backward(ikbo_plan_t p, const void* Q, const float* state, const void* dO, void* dQ,
+                                         float* d_state, int d, float scale, cudaStream_t stream) {
+  if ((!dQ && !d_state) || !aligned16(dQ) || !aligned16(d_state) || !aligned16(Q) || (dQ && !state) || (d_state && !Q) ||
+      (dQ && d_state && (dQ == Q || dQ == dO)) || (d_state && d_state == state))
+    return IKBO_ERR_INVALID_ARG;
+  LinReadParams rp;
+  const ikbo_status_t st = read_call(p, dO, state, d, scale, &rp);
+  if (st != IKBO_OK) return st;
+  rp.q = static_cast<const uint16_t*>(Q);
+  if (d_state) {
+    bool capturing = false;
+    if (stream && is_capturing(stream, &capturing) != cudaSuccess) return IKBO_ERR_CUDA;
+    const size_t need = 2 * static_cast<size_t>(lin_read_ctas(p->num_sms)) * LIN_STATE;
+    if (grow_kept<false>(p, &p->lin_part, need, ANY, capturing, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+    rp.part = p->lin_part.ptr;
+    rp.d_state = d_state;
+  }
+  if (dQ) {
+    rp.out = static_cast<uint16_t*>(dQ);
+    rp.turned = 1;
+    if (launch_lin_read(rp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+    p->launches++;
+  }
+  if (d_state) {
+    if (launch_lin_read_state(rp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+    p->launches += 2;
+  }
+  return IKBO_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,61 @@
+// linattn_internal.h -- parameter blocks of linear attention with a decay
+// (linattn.cu) and of the candidates' reads of its states (linread.cu).  Not
+// part of the public ABI.
+#pragma once
+#include "ikbo_internal.h"
+
+namespace ikbo {
+
+constexpr int LIN_D = 128;                    // head dimension of queries, keys and values
+constexpr int LIN_STATE = LIN_D * LIN_D;      // floats of a state
+constexpr int LIN_MAX_JOBS = 3;
+constexpr int LIN_STEP_MOST = 4;              // rows of a user up to which single steps are taken
+
+// One scan: with queries x, keys y and values z,
+//   S <- decay S + y_t z_t^T,   out_t = scale x_t S
+// from the first row of a user to the last, or (reverse) from the last to the
+// first.  A reverse scan's start has been decayed already: its first step
+// takes it as it is, and its end is decayed once more.
+struct LinJob {
+  const uint16_t *x, *y, *z;  // x null: no outputs
+  uint16_t* out;
+  int64_t xs, ys, zs, os;     // row strides in elements
+  const float* s_in;          // [n_users][H][128][128], rows of y's elements; null: zero
+  float* s_out;               // the same, or null; may be s_in
+  float s_in_factor;          // of the start
+  float s_out_factor;         // of the end
+  int s_in_turned;            // s_in has rows of z's elements
+  int reverse;
+};
+
+struct LinParams {
+  LinJob job[LIN_MAX_JOBS];
+  const int32_t* offsets;  // [n_users + 1], or null: n_rows / n_users rows each
+  const float* decay;      // [H]
+  uint32_t* status;
+  float* ws;               // states between segments [job][u][h][segs], at a segment's end
+  int n_jobs, n_users, n_rows, H, max_len;
+  int seg_len, segs;       // rows of a segment (a multiple of the chunk), segments of the longest user; 1: no segments
+  int steps;               // rows one by one (a forward scan alone)
+  float scale;
+};
+
+struct LinReadParams {
+  const uint16_t* x;        // rows [n_cand][H][Lq][128]
+  const float* state;       // [n_users][H][128][128]
+  uint16_t* out;            // like x
+  const uint16_t* q;        // backward: the queries (x is dO), for d_state
+  float* d_state;
+  float* part;              // two states a CTA: of the first and the last run of units that it shares
+  const int32_t* offsets;   // the plan's segments
+  const int32_t* perm;
+  const int32_t* work;      // units {u, h, first place, run}
+  const int32_t* n_units;
+  uint32_t* status;
+  int64_t max_units;
+  int n_cand, n_users, H, Lq;
+  int turned;               // out = x S^T
+  float scale;
+};
+
+}  // namespace ikbo

@@ -75,6 +75,10 @@ struct ikbo_plan_s {
   ikbo::KeptBuffer<int4> qa_list;         // work items
   ikbo::KeptBuffer<uint16_t> qa_kv;       // decoded K rows, then V rows
   ikbo::KeptBuffer<int32_t> qa_ranges;    // each user's first decoded row, then each user's length
+  ikbo::KeptBuffer<float> qa_lse;         // drafted trees: the history's log-sum-exp, where the caller wants none
+  // linear attention (grown on first use)
+  ikbo::KeptBuffer<float> lin_states;     // states between the segments of long histories
+  ikbo::KeptBuffer<float> lin_part;       // gradients of states: what CTAs that share a state have of it
   void** retired = nullptr;               // replaced buffers that captured graphs may hold, freed with the plan
   int n_retired = 0;
   bool lce_flags_dirty = false;  // an LCE launch failed: its flags may still be set

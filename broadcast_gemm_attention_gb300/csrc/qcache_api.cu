@@ -23,6 +23,7 @@ size_t qattn_tile_smem();
 size_t qattn_tile_part_elems(int num_sms);
 int64_t qattn_tile_items(int64_t rows, int n_users, int H_kv, int num_sms);
 cudaError_t launch_qattn_tile(const QcAttnParams& p, cudaStream_t s);
+cudaError_t launch_qtree(const QcTreeParams& p, int num_sms, cudaStream_t s);
 }  // namespace ikbo
 
 using namespace ikbo;
@@ -30,7 +31,9 @@ using namespace ikbo;
 struct ikbo_rope_s {
   int rot, interleaved;
   float magnitude;
+  int axes;  // 0: made for one axis
   uint64_t turn[ROPE_MAX_DIM / 2];
+  uint8_t axis[ROPE_MAX_DIM / 2];
 };
 
 namespace {
@@ -118,9 +121,12 @@ QcAttnVariant qattn_variant(int64_t rows, int n_users, int H_kv, int Lkv) {
   return registers_us < tiles_us ? QATTN_REGISTERS : QATTN_TILES;
 }
 
+// axes: a call with positions on the rotation's axes, d_pos and the stride from one
+// item's to the next's among them.
 ikbo_status_t rope_call(ikbo_plan_t p, ikbo_rope_t r, const void* X, const int64_t* xs, void* Y, const int64_t* ys,
                         const int32_t* d_start, int broadcast, int dtype, int n, int H, int L, int d, bool backward,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, bool axes = false, const int32_t* d_pos = nullptr, int64_t pos_item = 0) {
+  if (r && (axes ? r->axes < 1 || !aligned4(d_pos) || pos_item < 0 : r->axes > 0)) return IKBO_ERR_INVALID_ARG;
   if (!r || n < 0 || (n > 0 && (!X || !Y)) || H < 1 || L < 1 || d < 1) return IKBO_ERR_INVALID_ARG;
   if (dtype < IKBO_BF16 || dtype > IKBO_FP32) return IKBO_ERR_INVALID_ARG;
   const uintptr_t elt = dtype == IKBO_FP32 ? 4 : 2;
@@ -161,6 +167,12 @@ ikbo_status_t rope_call(ikbo_plan_t p, ikbo_rope_t r, const void* X, const int64
   rp.backward = backward ? 1 : 0;
   rp.copy_rest = (!same && r->rot < d) ? 1 : 0;
   rp.magnitude = r->magnitude;
+  if (axes) {
+    rp.axes = r->axes;
+    rp.pos = d_pos;
+    rp.pos_item = pos_item;
+    std::memcpy(rp.axis, r->axis, sizeof(uint8_t) * (r->rot / 2));
+  }
   std::memcpy(rp.turn, r->turn, sizeof(uint64_t) * (r->rot / 2));
   if (launch_rope(rp, dtype, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
   p->launches++;
@@ -213,6 +225,27 @@ ikbo_status_t ikbo_rope_create(ikbo_rope_t* out, int rot_dim, const double* freq
   return IKBO_OK;
 }
 
+ikbo_status_t ikbo_rope_create_axes(ikbo_rope_t* out, int rot_dim, const double* freqs, int n_axes,
+                                    const uint8_t* axis_of_pair, int interleaved, float magnitude) {
+  if (!out) return IKBO_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (n_axes < 1 || !axis_of_pair) return IKBO_ERR_INVALID_ARG;
+  if (n_axes > ROPE_MAX_AXES) return IKBO_ERR_UNSUPPORTED;
+  ikbo_rope_t r = nullptr;
+  const ikbo_status_t st = ikbo_rope_create(&r, rot_dim, freqs, interleaved, magnitude);
+  if (st != IKBO_OK) return st;
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    if (axis_of_pair[j] >= n_axes) {
+      delete r;
+      return IKBO_ERR_INVALID_ARG;
+    }
+    r->axis[j] = axis_of_pair[j];
+  }
+  r->axes = n_axes;
+  *out = r;
+  return IKBO_OK;
+}
+
 void ikbo_rope_destroy(ikbo_rope_t r) { delete r; }
 
 ikbo_status_t ikbo_rope_forward(ikbo_plan_t p, ikbo_rope_t r, const void* X, const int64_t* x_strides, void* Y,
@@ -225,6 +258,22 @@ ikbo_status_t ikbo_rope_backward(ikbo_plan_t p, ikbo_rope_t r, const void* dY, c
                                  const int64_t* dx_strides, const int32_t* d_start, int broadcast, int dtype, int n,
                                  int H, int L, int d, cudaStream_t stream) {
   return rope_call(p, r, dY, dy_strides, dX, dx_strides, d_start, broadcast, dtype, n, H, L, d, true, stream);
+}
+
+ikbo_status_t ikbo_rope_axes_forward(ikbo_plan_t p, ikbo_rope_t r, const void* X, const int64_t* x_strides, void* Y,
+                                     const int64_t* y_strides, const int32_t* d_start, const int32_t* d_positions,
+                                     int64_t positions_stride, int broadcast, int dtype, int n, int H, int L, int d,
+                                     cudaStream_t stream) {
+  return rope_call(p, r, X, x_strides, Y, y_strides, d_start, broadcast, dtype, n, H, L, d, false, stream, true, d_positions,
+                   positions_stride);
+}
+
+ikbo_status_t ikbo_rope_axes_backward(ikbo_plan_t p, ikbo_rope_t r, const void* dY, const int64_t* dy_strides, void* dX,
+                                      const int64_t* dx_strides, const int32_t* d_start, const int32_t* d_positions,
+                                      int64_t positions_stride, int broadcast, int dtype, int n, int H, int L, int d,
+                                      cudaStream_t stream) {
+  return rope_call(p, r, dY, dy_strides, dX, dx_strides, d_start, broadcast, dtype, n, H, L, d, true, stream, true, d_positions,
+                   positions_stride);
 }
 
 // ------------------------------------------------------------------- cache
@@ -447,6 +496,52 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   ap.timeout_ns = p->timeout_ns;
   if ((few ? launch_qattn(ap, eight, solo, stream) : launch_qattn_tile(ap, stream)) != cudaSuccess)
     return IKBO_ERR_CUDA;
+  p->launches++;
+  return IKBO_OK;
+}
+
+ikbo_status_t ikbo_attn_qcache_tree_forward(ikbo_plan_t p, const void* Q, const void* data, int n_pages, int page,
+                                            int H_kv, const int32_t* d_table, int max_blocks, const int32_t* d_lens,
+                                            const void* K_new, const void* V_new, int64_t row_stride,
+                                            const int32_t* d_parents, void* O, float* lse, int Lkv, int d, float scale,
+                                            cudaStream_t stream) {
+  if (!K_new || !V_new || !aligned16(K_new) || !aligned16(V_new) || !aligned4(d_parents) || !Q || Q == O)
+    return IKBO_ERR_INVALID_ARG;
+  if (H_kv < 1 || row_stride < static_cast<int64_t>(H_kv) * QC_D) return IKBO_ERR_INVALID_ARG;
+  if (row_stride % 8 != 0) return IKBO_ERR_UNSUPPORTED;
+  float* hist = lse;
+  if (p && p->planned && !lse) {  // the history's log-sum-exp has to be somewhere
+    bool capturing = false;
+    if (stream && is_capturing(stream, &capturing) != cudaSuccess) return IKBO_ERR_CUDA;
+    if (!plan_device_current(p)) return IKBO_ERR_INVALID_ARG;
+    const size_t need = static_cast<size_t>(p->n_cand) * p->H * p->Lq;
+    if (grow_kept<false>(p, &p->qa_lse, need, ~size_t{0}, capturing, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+    hist = p->qa_lse.ptr;
+  }
+  const ikbo_status_t st = ikbo_attn_qcache_forward(p, Q, data, n_pages, page, H_kv, d_table, max_blocks, d_lens, O, hist, Lkv, d,
+                                                    scale, stream);
+  if (st != IKBO_OK) return st;
+  QcTreeParams tp;
+  std::memset(&tp, 0, sizeof(tp));
+  tp.Q = static_cast<const uint16_t*>(Q);
+  tp.K = static_cast<const uint16_t*>(K_new);
+  tp.V = static_cast<const uint16_t*>(V_new);
+  tp.O = static_cast<uint16_t*>(O);
+  tp.hist_lse = hist;
+  tp.lse = lse;
+  tp.parents = d_parents;
+  tp.map = p->d_map;
+  tp.status = p->d_status;
+  tp.row_stride = row_stride;
+  tp.cand_stride = row_stride * p->Lq;
+  tp.n_cand = p->n_cand;
+  tp.n_users = p->n_users;
+  tp.H = p->H;
+  tp.H_kv = H_kv;
+  tp.group = p->H / H_kv;
+  tp.Lq = p->Lq;
+  tp.scale_log2 = scale * 1.4426950408889634f;
+  if (launch_qtree(tp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
   p->launches++;
   return IKBO_OK;
 }

@@ -10,6 +10,7 @@ namespace ikbo {
 
 // --------------------------------------------------------------- rotation
 constexpr int ROPE_MAX_DIM = 512;
+constexpr int ROPE_MAX_AXES = 4;
 
 struct RopeParams {
   const void* X;
@@ -18,11 +19,15 @@ struct RopeParams {
   const int32_t* map;    // null: item i reads start[i]
   uint32_t* status;
   int64_t xs[3], ys[3];  // element strides of item, head, token
+  const int32_t* pos;    // several axes: [n or 1][L][axes] beside the start's [..][axes]; null: 0
+  int64_t pos_item;      // elements from one item's to the next's (0: all items share them)
   int n, n_users, H, L, d;
   int heads_per_cta;
+  int axes;              // 0: one axis, position start + l
   int rot, interleaved, backward, copy_rest;  // copy_rest: elements from rot on are written (not in place)
   float magnitude;
   uint64_t turn[ROPE_MAX_DIM / 2];  // turns per position, 2^64 = one turn
+  uint8_t axis[ROPE_MAX_DIM / 2];   // of each pair
 };
 
 // ------------------------------------------------------------ 4-bit cache
@@ -98,6 +103,22 @@ struct QcAttnParams {
   uint32_t sixteen;        // QC_SIXTEEN
   uint32_t debug;          // the plan's switches
   uint64_t timeout_ns;
+};
+
+// The drafted rows' part of attention over a tree (qtree.cu).
+struct QcTreeParams {
+  const uint16_t* Q;
+  const uint16_t* K;        // [n_cand][Lq] rows of [H_kv][128], row_stride apart
+  const uint16_t* V;
+  uint16_t* O;              // in: the history's part
+  const float* hist_lse;    // [n_cand][H][Lq], of the history's part
+  float* lse;               // may be hist_lse, or null
+  const int32_t* parents;   // [n_cand][Lq], or null: a chain
+  const int32_t* map;
+  uint32_t* status;
+  int64_t row_stride, cand_stride;
+  int n_cand, n_users, H, H_kv, group, Lq;
+  float scale_log2;
 };
 
 #ifdef __CUDACC__

@@ -6,6 +6,10 @@
 // start of a candidate's queries is its user's, read through the map, so
 // positions stay at the user batch like the rest of the request.
 //
+// With several axes (time, height and width of an item; a drafted token's depth)
+// each pair belongs to one of them and pos = start[axis] + the row's own place
+// there: a token's places (four at most) are read once and a pair takes its own.
+//
 // The angle.  A float product pos * f_j loses pos * 2^-24 radians (0.06 at a
 // position of a million).  Here f_j is held as turns per position in 64-bit
 // fixed point (2^64 = one turn): pos * turn[j] modulo 2^64 drops whole turns
@@ -50,8 +54,19 @@ struct Num<float> {
   static __device__ __forceinline__ float down(float x) { return x; }
 };
 
-// Position of token l of item i; false for a candidate whose user is out of range.
-__device__ __forceinline__ bool position(const RopeParams& p, int i, int l, int64_t* pos) {
+// Position of token l of item i on each axis; false for a candidate whose user is out of range.
+template <bool kAxes>
+struct Place {
+  int64_t at[kAxes ? ROPE_MAX_AXES : 1];
+  __device__ __forceinline__ int64_t of(const RopeParams& p, int j) const {
+    if (!kAxes) return at[0];
+    const int a = p.axis[j];  // (selected, so that the places stay in registers)
+    return a == 0 ? at[0] : (a == 1 ? at[kAxes ? 1 : 0] : (a == 2 ? at[kAxes ? 2 : 0] : at[kAxes ? 3 : 0]));
+  }
+};
+
+template <bool kAxes>
+__device__ __forceinline__ bool position(const RopeParams& p, int i, int l, Place<kAxes>* pos) {
   int src = i;
   if (p.map) {
     src = __ldg(p.map + i);
@@ -60,7 +75,17 @@ __device__ __forceinline__ bool position(const RopeParams& p, int i, int l, int6
       return false;
     }
   }
-  *pos = (p.start ? static_cast<int64_t>(__ldg(p.start + src)) : 0) + l;
+  if constexpr (!kAxes) {
+    pos->at[0] = (p.start ? static_cast<int64_t>(__ldg(p.start + src)) : 0) + l;
+  } else {
+#pragma unroll
+    for (int a = 0; a < ROPE_MAX_AXES; ++a) {
+      pos->at[a] = 0;
+      if (a >= p.axes) continue;
+      if (p.start) pos->at[a] = __ldg(p.start + static_cast<int64_t>(src) * p.axes + a);
+      if (p.pos) pos->at[a] += __ldg(p.pos + i * p.pos_item + static_cast<int64_t>(l) * p.axes + a);
+    }
+  }
   return true;
 }
 
@@ -110,7 +135,7 @@ __device__ __forceinline__ void store8(T* p, const Vec8<T>& r) {
 // rot % 16 == 0, d % 8 == 0, pointers and strides multiples of 8 elements and
 // 16 bytes.
 // kAhead: heads whose loads are in flight together.
-template <typename T, bool kInterleaved, int kAhead>
+template <typename T, bool kInterleaved, int kAhead, bool kAxes>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_constant__ RopeParams p) {
   const int turning = p.rot >> 4;
   const int pieces = turning + (p.copy_rest ? (p.d - p.rot + 15) >> 4 : 0);
@@ -121,7 +146,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_con
   if (r >= rows_per_cta || row64 >= static_cast<int64_t>(p.n) * p.L) return;
   const int row = static_cast<int>(row64);  // n * L is below 2^31
   const int i = row / p.L, l = row - i * p.L;
-  int64_t pos;
+  Place<kAxes> pos;
   if (!position(p, i, l, &pos)) return;
   const int h0 = static_cast<int>(blockIdx.y) * p.heads_per_cta;
   const int h1 = min(p.H, h0 + p.heads_per_cta);
@@ -151,7 +176,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_con
   float cs[8], sn[8];
   if (turn) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) turn_of<T>(p, pos, piece * 8 + j, &cs[j], &sn[j]);
+    for (int j = 0; j < 8; ++j) turn_of<T>(p, pos.of(p, piece * 8 + j), piece * 8 + j, &cs[j], &sn[j]);
   }
   for (int h = h0; h < h1; h += kAhead) {
     if (h > h0) fetch(h);
@@ -188,7 +213,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_con
 
 // Any sizes and strides: a thread per pair (or element behind the rotated
 // ones) of a token, over its heads.
-template <typename T>
+template <typename T, bool kAxes>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_constant__ RopeParams p) {
   const int half = p.rot >> 1;
   const int pieces = half + (p.copy_rest ? p.d - p.rot : 0);
@@ -198,7 +223,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_con
     const int64_t row = e / pieces;
     const int piece = static_cast<int>(e - row * pieces);
     const int i = static_cast<int>(row / p.L), l = static_cast<int>(row - static_cast<int64_t>(i) * p.L);
-    int64_t pos;
+    Place<kAxes> pos;
     if (!position(p, i, l, &pos)) continue;
     const T* x = static_cast<const T*>(p.X) + i * p.xs[0] + l * p.xs[2];
     T* y = static_cast<T*>(p.Y) + i * p.ys[0] + l * p.ys[2];
@@ -210,7 +235,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_con
       continue;
     }
     float cs, sn;
-    turn_of<T>(p, pos, piece, &cs, &sn);
+    turn_of<T>(p, pos.of(p, piece), piece, &cs, &sn);
     const int a = p.interleaved ? 2 * piece : piece, b = p.interleaved ? a + 1 : a + half;
     for (int h = h0; h < h1; ++h) {
       const float x0 = Num<T>::up(x[h * p.xs[1] + a]), y0 = Num<T>::up(x[h * p.xs[1] + b]);
@@ -224,14 +249,14 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_con
 // thread has only one (200000 rows of one bf16 head: 32 us, against 49 with the
 // registers of four), else as many as their registers pay for (the 70:1 queries:
 // 22.3 us with four, 22.8 with two, 26.2 with eight).
-template <typename T, bool kInterleaved>
+template <typename T, bool kInterleaved, bool kAxes>
 void launch_vec(const RopeParams& p, dim3 grid, cudaStream_t s) {
   constexpr int kMost = sizeof(T) == 4 ? 2 : 4;
-  if (p.heads_per_cta == 1) rope_vec_kernel<T, kInterleaved, 1><<<grid, ROPE_THREADS, 0, s>>>(p);
-  else rope_vec_kernel<T, kInterleaved, kMost><<<grid, ROPE_THREADS, 0, s>>>(p);
+  if (p.heads_per_cta == 1) rope_vec_kernel<T, kInterleaved, 1, kAxes><<<grid, ROPE_THREADS, 0, s>>>(p);
+  else rope_vec_kernel<T, kInterleaved, kMost, kAxes><<<grid, ROPE_THREADS, 0, s>>>(p);
 }
 
-template <typename T>
+template <typename T, bool kAxes>
 cudaError_t launch(RopeParams p, bool vec, int num_sms, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.n) * p.L;
   int64_t ctas;
@@ -252,9 +277,9 @@ cudaError_t launch(RopeParams p, bool vec, int num_sms, cudaStream_t s) {
   if (parts > p.H) parts = p.H;
   p.heads_per_cta = (p.H + parts - 1) / parts;
   const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>((p.H + p.heads_per_cta - 1) / p.heads_per_cta));
-  if (!vec) rope_any_kernel<T><<<grid, ROPE_THREADS, 0, s>>>(p);
-  else if (p.interleaved) launch_vec<T, true>(p, grid, s);
-  else launch_vec<T, false>(p, grid, s);
+  if (!vec) rope_any_kernel<T, kAxes><<<grid, ROPE_THREADS, 0, s>>>(p);
+  else if (p.interleaved) launch_vec<T, true, kAxes>(p, grid, s);
+  else launch_vec<T, false, kAxes>(p, grid, s);
   return cudaGetLastError();
 }
 
@@ -265,9 +290,10 @@ cudaError_t launch_rope(const RopeParams& p, int dtype, int num_sms, cudaStream_
   bool vec = p.rot % 16 == 0 && p.d % 8 == 0;
   for (int k = 0; k < 3; ++k) vec = vec && p.xs[k] * elt % 16 == 0 && p.ys[k] * elt % 16 == 0;
   vec = vec && reinterpret_cast<uintptr_t>(p.X) % 16 == 0 && reinterpret_cast<uintptr_t>(p.Y) % 16 == 0;
-  if (dtype == 0) return launch<__nv_bfloat16>(p, vec, num_sms, s);
-  if (dtype == 1) return launch<__half>(p, vec, num_sms, s);
-  return launch<float>(p, vec, num_sms, s);
+  const bool axes = p.axes > 0;
+  if (dtype == 0) return axes ? launch<__nv_bfloat16, true>(p, vec, num_sms, s) : launch<__nv_bfloat16, false>(p, vec, num_sms, s);
+  if (dtype == 1) return axes ? launch<__half, true>(p, vec, num_sms, s) : launch<__half, false>(p, vec, num_sms, s);
+  return axes ? launch<float, true>(p, vec, num_sms, s) : launch<float, false>(p, vec, num_sms, s);
 }
 
 }  // namespace ikbo

@@ -17,7 +17,10 @@
  * and, for users whose histories are kept between requests, what broadcast
  * attention needs around it: rotary positions of queries and keys
  * (ikbo_rope_*), a paged cache of 4-bit keys and values (ikbo_qcache_*) and
- * the attention that reads it (ikbo_attn_qcache_forward).  The write-ups have
+ * the attention that reads it (ikbo_attn_qcache_forward), also for trees of
+ * drafted tokens (ikbo_attn_qcache_tree_forward); or, in place of keys and
+ * values, a state of fixed size per user and head: linear attention with a
+ * decay (ikbo_linattn_*) and the candidates' reads of it.  The write-ups have
  * no counterpart to these.
  *
  * Conventions for every entry point:
@@ -361,6 +364,34 @@ ikbo_status_t ikbo_rope_backward(ikbo_plan_t p, ikbo_rope_t r, const void* dY, c
                                  const int64_t* dx_strides, const int32_t* d_start, int broadcast, int dtype, int n,
                                  int H, int L, int d, cudaStream_t stream);
 
+/* A rotation with several axes, as items with a time and a place, the patches
+ * of an image or a video, or drafted tokens (whose position is their depth)
+ * need: pair j turns by its position on axis axis_of_pair[j], in [0, n_axes),
+ * n_axes 1..4 (host memory, rot_dim / 2 values).  Else as ikbo_rope_create.
+ * Such a rotation is for the two calls below alone, one of ikbo_rope_create for
+ * the two above alone (IKBO_ERR_INVALID_ARG otherwise). */
+ikbo_status_t ikbo_rope_create_axes(ikbo_rope_t* out, int rot_dim, const double* freqs, int n_axes,
+                                    const uint8_t* axis_of_pair, int interleaved, float magnitude);
+
+/* ikbo_rope_forward with a position on each axis: pair j of row (i, h, l) turns
+ * by (start[a] + positions[l][a]) f_j, a its axis, where
+ *   start      = d_start[i], or d_start[map[i]] with broadcast: int32
+ *                [n or n_users][n_axes]; NULL: 0
+ *   positions  = d_positions[i]: int32 [L][n_axes], items positions_stride
+ *                elements apart, 0: all items share one (the patches' grid);
+ *                NULL: 0
+ * The sum is exact (64 bits).  Both arrays are 4-byte aligned. */
+ikbo_status_t ikbo_rope_axes_forward(ikbo_plan_t p, ikbo_rope_t r, const void* X, const int64_t* x_strides, void* Y,
+                                     const int64_t* y_strides, const int32_t* d_start, const int32_t* d_positions,
+                                     int64_t positions_stride, int broadcast, int dtype, int n, int H, int L, int d,
+                                     cudaStream_t stream);
+
+/* Its gradient, as ikbo_rope_backward is ikbo_rope_forward's. */
+ikbo_status_t ikbo_rope_axes_backward(ikbo_plan_t p, ikbo_rope_t r, const void* dY, const int64_t* dy_strides, void* dX,
+                                      const int64_t* dx_strides, const int32_t* d_start, const int32_t* d_positions,
+                                      int64_t positions_stride, int broadcast, int dtype, int n, int H, int L, int d,
+                                      cudaStream_t stream);
+
 /* A paged cache of users' keys and values in 4 bits.  All of its memory is
  * the caller's:
  *   data   uint8 [n_pages][H][page / 16][2560]: a page holds `page` tokens
@@ -471,6 +502,96 @@ ikbo_status_t ikbo_qcache_load(ikbo_plan_t p, const void* data, int n_pages, int
 ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void* data, int n_pages, int page,
                                        int H_kv, const int32_t* d_table, int max_blocks, const int32_t* d_lens,
                                        void* O, float* lse, int Lkv, int d, float scale, cudaStream_t stream);
+
+/* Attention for trees of drafted tokens over the cache.  The Lq rows of a
+ * candidate are the tokens of one draft; row l reads its user's history as in
+ * ikbo_attn_qcache_forward, and of the draft its ancestors and itself:
+ *   O[i,h,l,:] = sum_j softmax_j(scale Q[i,h,l,:].k_j) v_j   over the lens[u]
+ *   tokens of user u = map[i] and the rows j of the draft that l reads,
+ *   k_j = K_new[i][j][g], v_j = V_new[i][j][g]
+ *   K_new, V_new  bf16 [n_cand][Lq] rows of [H_kv][128], heads contiguous, all
+ *                 rows row_stride elements apart (>= H_kv * 128, a multiple of 8):
+ *                 rows as ikbo_qcache_append takes them, which stores the
+ *                 accepted ones once their slots are known
+ *   d_parents     int32 [n_cand][Lq]: the row above row l, in [0, l); -1: none
+ *                 (a child of the history); below -1: row l is not there, so a
+ *                 draft may have fewer rows than Lq.  NULL: chains, row l below
+ *                 row l - 1.  A parent of l or more, or one that is not there, is
+ *                 reported (IKBO_ERR_CACHE), and the row is not there.
+ * Rows that are not there get O = 0, lse = -inf and are read by none; what K_new
+ * and V_new hold there, infinities and NaN too, reaches no other row, nor does any
+ * row's reach rows that do not read it.  O must not be Q, and not overlap other
+ * inputs.  Else as ikbo_attn_qcache_forward: its launches and one more, which takes
+ * the history's O (rounded to bf16) and log-sum-exp as where its softmax begins.
+ * With lse NULL the plan keeps the history's, a workspace as described there. */
+ikbo_status_t ikbo_attn_qcache_tree_forward(ikbo_plan_t p, const void* Q, const void* data, int n_pages, int page,
+                                            int H_kv, const int32_t* d_table, int max_blocks, const int32_t* d_lens,
+                                            const void* K_new, const void* V_new, int64_t row_stride,
+                                            const int32_t* d_parents, void* O, float* lse, int Lkv, int d, float scale,
+                                            cudaStream_t stream);
+
+/* Linear attention with a decay for each head, causal over each user's rows:
+ *   S_t = decay[h] S_{t-1} + k_t v_t^T,   O_t = scale q_t S_t
+ * A user's state S, 64 KB a head whatever the history's length, is what a
+ * server keeps of the user; new events are taken in from where it stands, and
+ * candidates read it (ikbo_linattn_read_forward).
+ *   Q, K, V, O  bf16, n_rows rows of [H][128], heads contiguous, rows
+ *               row_strides[k] elements apart (host, 4 values in that order, each
+ *               >= H * 128 and a multiple of 8; NULL: contiguous), so all may be
+ *               slices of one projection.  Q and O both NULL: the states alone.
+ *   d_offsets   int32 [n_users + 1]: user u's rows are d_offsets[u] ..
+ *               d_offsets[u + 1] - 1, ascending, within [0, n_rows]; rows that
+ *               belong to no user are left alone.  NULL: n_rows / n_users each.
+ *   max_len     a bound on a user's rows (0: n_rows); the variant and the
+ *               workspace go by it.  A user with more rows, or with offsets out
+ *               of range, is taken for one without rows and reported
+ *               (IKBO_ERR_CACHE).
+ *   decay       fp32 [H], each in [0, 1]
+ *   state_in    fp32 [n_users][H][128][128] (k's elements by v's), or NULL: zero
+ *   state_out   the same, or NULL (then O is given); may be state_in
+ * n_users <= 8192, H <= 1024, d == 128; scale > 0, and so that 1 / scale is
+ * finite; no plan() is needed.  States are held in fp32.  With up to 4 rows a
+ * user (max_len) they are taken one by one, in fp32.  Else in chunks of 64 on the
+ * tensor cores: decayed values in two bf16 parts (2^-17) for the state, the
+ * products q_i.k_j with their decays and, for O, the state rounded to bf16 (2^-9
+ * each), fp32 sums.  A row that holds an infinity or NaN makes its user's O of
+ * that head undefined from 63 rows before it.  O must not overlap inputs.  Histories far longer than a CTA's share
+ * are cut into segments (two launches more, and a workspace of the plan's, as
+ * described at ikbo_attn_qcache_forward).  Results repeat bit for bit. */
+ikbo_status_t ikbo_linattn_forward(ikbo_plan_t p, const void* Q, const void* K, const void* V, const int64_t* row_strides,
+                                   const int32_t* d_offsets, int n_users, int n_rows, int max_len, int H, int d,
+                                   const float* decay, const float* state_in, float* state_out, void* O, float scale,
+                                   cudaStream_t stream);
+
+/* Its gradients, for upstream dO and (or NULL: zero) d_state_out:
+ *   dQ_t = scale dO_t S_t^T,   dK_t = V_t R_t^T,   dV_t = K_t R_t,
+ *   R_t = sum_{s >= t} decay^(s-t) scale q_s dO_s^T + decay^(T-t) d_state_out,
+ *   d_state_in = decay R_1 (d_state_out for a user without rows)
+ * Only inputs are read: the states are formed again from state_in.  dQ, dK, dV
+ * bf16, d_state_in fp32, overwritten; any may be NULL, and none may overlap an
+ * input.  row_strides: 7 values, of Q, K, V, dO, dQ, dK, dV.  The decays are
+ * constants.  Else as above. */
+ikbo_status_t ikbo_linattn_backward(ikbo_plan_t p, const void* Q, const void* K, const void* V, const void* dO,
+                                    const int64_t* row_strides, const int32_t* d_offsets, int n_users, int n_rows,
+                                    int max_len, int H, int d, const float* decay, const float* state_in,
+                                    const float* d_state_out, void* dQ, void* dK, void* dV, float* d_state_in, float scale,
+                                    cudaStream_t stream);
+
+/* Candidates read their user's state: O[i,h,l,:] = scale Q[i,h,l,:] S[map[i],h],
+ * for the request of the last ikbo_plan.
+ *   Q, O   bf16 [n_cand][H][Lq][128];  state fp32 [n_users][H][128][128]
+ * The state is rounded to bf16 for the products, fp32 sums; O may be Q.  A
+ * candidate whose map value is out of range keeps its rows.  One launch. */
+ikbo_status_t ikbo_linattn_read_forward(ikbo_plan_t p, const void* Q, const float* state, void* O, int d, float scale,
+                                        cudaStream_t stream);
+
+/* Its gradients: dQ[i,h] = scale dO[i,h] S[map[i],h]^T (bf16; may be NULL or dO
+ * where d_state is NULL; not Q) and d_state[u,h] = scale sum_{map[i]=u} Q[i,h]^T dO[i,h] (fp32, 0
+ * for a user without candidates; may be NULL), overwritten.  Q may be NULL
+ * without d_state, state without dQ.  One launch for dQ, two for d_state;
+ * results repeat bit for bit. */
+ikbo_status_t ikbo_linattn_read_backward(ikbo_plan_t p, const void* Q, const float* state, const void* dO, void* dQ,
+                                         float* d_state, int d, float scale, cudaStream_t stream);
 
 /* Synchronise `stream`, then return (and clear) the first device-detected
  * error recorded since the last call: IKBO_ERR_MAP_OUT_OF_RANGE,
