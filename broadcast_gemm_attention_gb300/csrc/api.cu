@@ -68,6 +68,9 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
+namespace ikbo {
 // bf16 tensor map with 128-byte swizzle; out-of-bounds elements read as zero.
 bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
                  const uint32_t* box) {
@@ -86,6 +89,9 @@ bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+}  // namespace ikbo
+
+namespace {
 
 // Grows a plan workspace to `need` elements.  New memory is zeroed on
 // `stream`, the stream of the call that will use it, so the clear is ordered

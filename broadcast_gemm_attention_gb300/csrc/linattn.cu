@@ -361,8 +361,10 @@ cudaError_t launch_chunks(const LinParams& p, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t launch_lin_tiles(const LinParams& p, bool local, int num_sms, cudaStream_t s);
+
 // Launches: one, or three where histories are cut into segments.
-cudaError_t launch_linattn(const LinParams& p, cudaStream_t s, int* launches) {
+cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int* launches) {
   *launches = 0;
   const bool outputs = p.job[0].x != nullptr;
   cudaError_t e;
@@ -374,7 +376,7 @@ cudaError_t launch_linattn(const LinParams& p, cudaStream_t s, int* launches) {
     return cudaGetLastError();
   }
   if (p.segs > 1) {
-    e = launch_chunks<false, true>(p, s);
+    e = p.tiles ? launch_lin_tiles(p, true, num_sms, s) : launch_chunks<false, true>(p, s);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(LIN_STATE / 256 * p.n_users * p.H), static_cast<unsigned>(p.n_jobs));
     lin_join_kernel<<<grid, 256, 0, s>>>(p);
@@ -382,7 +384,8 @@ cudaError_t launch_linattn(const LinParams& p, cudaStream_t s, int* launches) {
     if (e != cudaSuccess) return e;
     *launches += 2;
   }
-  e = outputs ? launch_chunks<true, false>(p, s) : launch_chunks<false, false>(p, s);
+  if (p.tiles) e = launch_lin_tiles(p, false, num_sms, s);
+  else e = outputs ? launch_chunks<true, false>(p, s) : launch_chunks<false, false>(p, s);
   *launches += e == cudaSuccess;
   return e;
 }

@@ -9,7 +9,8 @@
 #include "plan_internal.h"
 
 namespace ikbo {
-cudaError_t launch_linattn(const LinParams& p, cudaStream_t s, int* launches);
+cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int* launches);
+size_t lin_tile_smem();
 cudaError_t launch_lin_read(const LinReadParams& p, int num_sms, cudaStream_t s);
 cudaError_t launch_lin_read_state(const LinReadParams& p, int num_sms, cudaStream_t s);
 int lin_read_ctas(int num_sms);
@@ -47,6 +48,7 @@ ikbo_status_t lin_params(ikbo_plan_t p, const int32_t* d_offsets, int n_users, i
   lp->max_len = d_offsets ? (max_len > 0 ? std::min(max_len, n_rows) : n_rows) : n_rows / n_users;
   lp->scale = scale;
   lp->segs = 1;
+  lp->timeout_ns = p->timeout_ns;
   return IKBO_OK;
 }
 
@@ -58,15 +60,17 @@ ikbo_status_t lin_params(ikbo_plan_t p, const int32_t* d_offsets, int n_users, i
 // others'.  At most LIN_MOST_STATES states lie between segments.
 constexpr int64_t LIN_MOST_STATES = 16384;  // 1 GiB
 constexpr int LIN_LEAST_SEGMENT = 256;
+constexpr int LIN_LEAST_TILES = 128;
 
 void cut_segments(LinParams* lp, int num_sms) {
   const int64_t items = static_cast<int64_t>(lp->n_users) * lp->H * lp->n_jobs;
-  const int64_t share = static_cast<int64_t>(lp->n_rows) * lp->H * lp->n_jobs / num_sms;  // rows of a CTA
-  int64_t seg = std::max<int64_t>(items * 2 <= num_sms ? share : 4 * share, LIN_LEAST_SEGMENT);
+  const int64_t rows = static_cast<int64_t>(lp->n_rows) * lp->H * lp->n_jobs;
+  // (each scan's last segment is a part of one: as many SMs are left out of the division)
+  int64_t seg = std::max<int64_t>(items * 2 <= num_sms ? (rows + num_sms - items - 1) / (num_sms - items) : 4 * (rows / num_sms), LIN_LEAST_SEGMENT);
   const int64_t most = LIN_MOST_STATES / items;  // segments of a user
   if (most < 2) return;
   seg = std::max(seg, (lp->max_len + most - 1) / most);
-  seg = (seg + 63) / 64 * 64;
+  seg = (seg + 127) / 128 * 128;
   if (lp->max_len <= seg + seg / 2) return;
   lp->seg_len = static_cast<int>(seg);
   lp->segs = static_cast<int>((lp->max_len + seg - 1) / seg);
@@ -74,7 +78,10 @@ void cut_segments(LinParams* lp, int num_sms) {
 
 ikbo_status_t lin_run(ikbo_plan_t p, LinParams* lp, cudaStream_t stream) {
   if (static_cast<int64_t>(lp->n_users) * lp->H > INT32_LIMIT / 256) return IKBO_ERR_UNSUPPORTED;
-  if (!lp->steps) cut_segments(lp, p->num_sms);
+  if (!lp->steps) {
+    cut_segments(lp, p->num_sms);
+    lp->tiles = lp->max_len > LIN_LEAST_TILES && lin_tile_smem() <= p->max_smem;
+  }
   if (lp->segs > 1) {
     bool capturing = false;
     if (stream && is_capturing(stream, &capturing) != cudaSuccess) return IKBO_ERR_CUDA;
@@ -83,7 +90,7 @@ ikbo_status_t lin_run(ikbo_plan_t p, LinParams* lp, cudaStream_t stream) {
     lp->ws = p->lin_states.ptr;
   }
   int launches = 0;
-  const cudaError_t e = launch_linattn(*lp, stream, &launches);
+  const cudaError_t e = launch_linattn(*lp, p->num_sms, stream, &launches);
   p->launches += launches;
   return e == cudaSuccess ? IKBO_OK : IKBO_ERR_CUDA;
 }

@@ -37,6 +37,8 @@ struct LinParams {
   int n_jobs, n_users, n_rows, H, max_len;
   int seg_len, segs;       // rows of a segment (a multiple of the chunk), segments of the longest user; 1: no segments
   int steps;               // rows one by one (a forward scan alone)
+  int tiles;               // the chunks' products on the 5th-gen tensor cores
+  uint64_t timeout_ns;
   float scale;
 };
 

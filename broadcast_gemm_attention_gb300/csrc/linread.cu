@@ -32,6 +32,14 @@ __device__ __forceinline__ int64_t row_of(const LinReadParams& p, const int4& w,
   return (static_cast<int64_t>(__ldg(p.perm + w.z + slot)) * p.H + w.y) * p.Lq + (r - slot * p.Lq);
 }
 
+// 16 bytes that nobody reads again (and that may be overwritten by whoever read
+// them: not the read-only path).
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
 // This CTA's units: an equal run of the list.
 __device__ __forceinline__ void unit_range(const LinReadParams& p, int cta, int& a, int& b) {
   const int n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
@@ -44,32 +52,40 @@ __device__ __forceinline__ void unit_range(const LinReadParams& p, int cta, int&
 // ones of a row: column 32 m + 8 t + 2 i + e at 32 m + 8 i + 2 t + e.  A lane loads
 // its rows in 16-byte pieces, which the inner order of the products follows: slot k
 // of step 2 j + f is element 32 j + 8 ((k & 7) >> 1) + 4 f + 2 (k >> 3) + (k & 1).
-__global__ void __launch_bounds__(RD_THREADS) lin_read_kernel(const __grid_constant__ LinReadParams p) {
+struct ReadRows {
+  uint4 x[2][4];  // rows g and g + 8 of the warp's 16, element 32 j + 8 t of piece j
+  int64_t at[2];  // their places, -1: not there
+};
+
+__global__ void __launch_bounds__(RD_THREADS, 2) lin_read_kernel(const __grid_constant__ LinReadParams p) {
   __shared__ __align__(128) uint8_t st[LIN_STATE * 2];
   const uint32_t base = smem_u32(st);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   int a, b;
   unit_range(p, static_cast<int>(blockIdx.x), a, b);
   int held = -1;  // (user, head) of the state in shared memory
-  uint32_t row_addr[2];  // inner rows of this lane for a step's B: of f = 0 and 1, without 32 j
+  const int slot = lane & 15;
+  const uint32_t inner = static_cast<uint32_t>(8 * ((slot & 7) >> 1) + 2 * (slot >> 3) + (slot & 1));  // of f = 0, without 32 j
+  int4 w = make_int4(0, 0, 0, 0);
+  ReadRows now;
+  const auto fetch = [&](int i, int4& w, ReadRows& r) {
+    if (!read_unit(p, i, w)) w.w = 0;
 #pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    const int k = lane & 15;
-    row_addr[f] = static_cast<uint32_t>(8 * ((k & 7) >> 1) + 4 * f + 2 * (k >> 3) + (k & 1));
-  }
+    for (int e = 0; e < 2; ++e) {
+      const int row = 16 * warp + g + 8 * e;
+      r.at[e] = row < w.w * p.Lq ? row_of(p, w, row) : -1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        r.x[e][j] = r.at[e] >= 0 ? ld_once(reinterpret_cast<const uint4*>(p.x + r.at[e] * LIN_D + 32 * j + 8 * t)) : uint4{};
+    }
+  };
+  if (a < b) fetch(a, w, now);
 #pragma unroll 1
   for (int i = a; i < b; ++i) {
-    int4 w;
-    if (!read_unit(p, i, w)) continue;
-    const int rows = w.w * p.Lq, r = 16 * warp + g;
-    const int64_t at0 = r < rows ? row_of(p, w, r) : -1, at1 = r + 8 < rows ? row_of(p, w, r + 8) : -1;
-    uint4 x0[4] = {}, x1[4] = {};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (at0 >= 0) x0[j] = __ldg(reinterpret_cast<const uint4*>(p.x + at0 * LIN_D + 32 * j + 8 * t));
-      if (at1 >= 0) x1[j] = __ldg(reinterpret_cast<const uint4*>(p.x + at1 * LIN_D + 32 * j + 8 * t));
-    }
-    if (w.x * p.H + w.y != held) {
+    int4 w_next = make_int4(0, 0, 0, 0);
+    ReadRows next;
+    if (i + 1 < b) fetch(i + 1, w_next, next);  // on its way meanwhile
+    if (w.w > 0 && w.x * p.H + w.y != held) {
       __syncthreads();
       held = w.x * p.H + w.y;
       const float* s = p.state + static_cast<int64_t>(held) * LIN_STATE;
@@ -82,7 +98,7 @@ __global__ void __launch_bounds__(RD_THREADS) lin_read_kernel(const __grid_const
           *reinterpret_cast<uint32_t*>(st + row * 256 + (((at >> 3) ^ (row & 7)) << 4) + (at & 7) * 2) = pack_bf16x2(v.x, v.y);
         }
       } else {  // rows of the state are the columns: two of them, four inner elements
-#pragma unroll 4
+#pragma unroll 2
         for (int k = 0; k < LIN_STATE / 8 / RD_THREADS; ++k) {
           const int e = k * RD_THREADS + tid, c = (e >> 5) * 2, row = (e & 31) * 4;
           const float4 v = __ldg(reinterpret_cast<const float4*>(s + c * LIN_D + row));
@@ -96,33 +112,39 @@ __global__ void __launch_bounds__(RD_THREADS) lin_read_kernel(const __grid_const
       }
       __syncthreads();
     }
-    if (16 * warp >= rows) continue;
-    float o[16][4] = {};
+    if (16 * warp < w.w * p.Lq) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int half = 0; half < 2; ++half) {  // of the columns
+        float o[8][4] = {};
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const uint32_t af[4] = {f ? x0[j].z : x0[j].x, f ? x1[j].z : x1[j].x, f ? x0[j].w : x0[j].y, f ? x1[j].w : x1[j].y};
-        const uint32_t row = 32 * j + row_addr[f];
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          uint32_t bf[4];
-          ldsm4_t(bf, base + row * 256 + (((2 * n + (lane >> 4)) ^ (row & 7)) << 4));
-          mma_16816(o[2 * n], af, bf[0], bf[1]);
-          mma_16816(o[2 * n + 1], af, bf[2], bf[3]);
-        }
+          for (int f = 0; f < 2; ++f) {
+            const uint32_t af[4] = {f ? now.x[0][j].z : now.x[0][j].x, f ? now.x[1][j].z : now.x[1][j].x, f ? now.x[0][j].w : now.x[0][j].y,
+                                    f ? now.x[1][j].w : now.x[1][j].y};
+            const uint32_t row = 32 * j + 4 * f + inner;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              uint32_t bf[4];
+              ldsm4_t(bf, base + row * 256 + (((8 * half + 2 * n + (lane >> 4)) ^ (row & 7)) << 4));
+              mma_16816(o[2 * n], af, bf[0], bf[1]);
+              mma_16816(o[2 * n + 1], af, bf[2], bf[3]);
+            }
+          }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (now.at[k] < 0) continue;
+            uint32_t v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = pack_bf16x2(o[4 * m + q][2 * k] * p.scale, o[4 * m + q][2 * k + 1] * p.scale);
+            *reinterpret_cast<uint4*>(p.out + now.at[k] * LIN_D + 64 * half + 32 * m + 8 * t) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
       }
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int64_t at = k ? at1 : at0;
-        if (at < 0) continue;
-        uint32_t v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = pack_bf16x2(o[4 * m + q][2 * k] * p.scale, o[4 * m + q][2 * k + 1] * p.scale);
-        *reinterpret_cast<uint4*>(p.out + at * LIN_D + 32 * m + 8 * t) = make_uint4(v[0], v[1], v[2], v[3]);
-      }
+    }
+    w = w_next;
+    now = next;
   }
 }
 
@@ -256,7 +278,7 @@ __global__ void __launch_bounds__(RD_THREADS) lin_read_join_kernel(const __grid_
 int lin_read_ctas(int num_sms) { return num_sms; }
 
 cudaError_t launch_lin_read(const LinReadParams& p, int num_sms, cudaStream_t s) {
-  const int64_t ctas = p.max_units < 4 * static_cast<int64_t>(num_sms) ? p.max_units : 4 * static_cast<int64_t>(num_sms);
+  const int64_t ctas = p.max_units < 2 * static_cast<int64_t>(num_sms) ? p.max_units : 2 * static_cast<int64_t>(num_sms);
   lin_read_kernel<<<static_cast<unsigned>(ctas), RD_THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }

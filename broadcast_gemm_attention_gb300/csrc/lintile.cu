@@ -1,0 +1,782 @@
+// lintile.cu -- linear attention with a decay on the 5th-gen tensor cores, for
+// histories of more than a few chunks (linattn.cu has the mathematics).
+//
+// In chunks of 128 rows, every product a 128 x 128 x 128 one with its result in
+// tensor memory (x queries, y keys, z values, S the state before the chunk):
+//   A  = x y^T            to registers, decayed and masked, back as bf16
+//   O1 = x S              S's bf16 image in shared memory
+//   O2 = A z
+//   S  = decay^n S + (w y)^T z
+//                         S stays in tensor memory in fp32; w y, each row with its
+//                         decay to the chunk's end, as two bf16 parts in shared
+//                         memory (2^-16), so two products
+//   out = scale (O2 + decay^(i+1) O1)
+//
+// Per CTA (persistent, one per SM, 32 warps):
+//   warp 0       loads x, y, z by TMA; warp 1 issues A, O1, O2; warp 2 issues S
+//   warps 4-11   A's decays
+//   warps 12-19  the outputs
+//   warps 20-27  S: its image, and its decay before a chunk is added
+//   warps 28-31  the two parts of w y
+// The groups' work is bound by latencies (loads of tensor memory, barriers, a few
+// dozen dependent instructions), so each has warps of its own.
+// Each tile has one buffer: y is free once w y and A are formed, x after O1, z after
+// O2 and M, so that a chunk's loads lie beside the products of the one before.
+// A reverse scan keeps the rows' order in its tiles and turns masks and decays around
+// instead (row j reaches i <= j, and the chunk's first row is its end).
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "attn_common.cuh"
+#include "linattn_internal.h"
+#include "mma_common.cuh"
+
+namespace ikbo {
+namespace {
+
+constexpr int LT_CHUNK = 128;
+constexpr int LT_THREADS = 1024;
+constexpr int DECAY_WARP0 = 4, OUT_WARP0 = 12, STATE_WARP0 = 20, PARTS_WARP0 = 28;
+constexpr int GROUP_WARPS = 8, PARTS_WARPS = 4;
+constexpr uint32_t TM_A = 0, TM_O1 = 128, TM_O2 = 256, TM_S = 384;
+
+constexpr uint32_t TILE = 2 * HALF_TILE;  // 32 KB
+constexpr uint32_t X_AT = 0, Y_AT = TILE, Z_AT = 2 * TILE, HI_AT = 3 * TILE, LO_AT = 4 * TILE, S_AT = 5 * TILE, OUT_AT = 6 * TILE;
+constexpr uint32_t OUT_BYTES = 32 * 128;  // of the outputs, per warp
+constexpr uint32_t AUX_AT = OUT_AT + GROUP_WARPS * OUT_BYTES;
+
+struct Aux {
+  uint64_t x_full, y_full, z_full, x_empty, y_empty, z_empty;
+  uint64_t a_full, p_full, o_full, o_empty, s_full, s_empty, w_full, m_full, m_begun, drain[2], group[2];
+  float4 near[4];             // a 16-column block's decays to its nearest column
+  float power[LT_CHUNK + 4];  // decay^n of the current item
+  uint2 parts[LT_CHUNK];      // decay^n as a bf16 pair of the same, and what that lacks
+  uint32_t tmem_slot, abort;
+};
+constexpr uint32_t LT_SMEM_USED = AUX_AT + sizeof(Aux);
+constexpr uint32_t LT_SMEM = LT_SMEM_USED + 1024;
+static_assert(LT_SMEM <= 227 * 1024, "tiles do not fit in shared memory");
+
+struct LtMaps {
+  CUtensorMap x[LIN_MAX_JOBS], y[LIN_MAX_JOBS], z[LIN_MAX_JOBS];
+};
+
+// One scan or segment of one.
+struct Item {
+  int job, u, h, seg, segs;
+  int base, n;      // its rows: base .. base + n - 1 of the tensors
+  bool reverse, whole_user_empty;
+  int early;        // its first row takes the start as it is
+  int chunks;
+  // chunk c's rows, first and count
+  __device__ __forceinline__ int rows(int c) const { return min(LT_CHUNK, n - c * LT_CHUNK); }
+  __device__ __forceinline__ int first(int c) const { return base + (reverse ? n - c * LT_CHUNK - rows(c) : c * LT_CHUNK); }
+};
+
+// The rows of user u; none where the offsets are out of range.
+__device__ __forceinline__ int user_rows(const LinParams& p, int u, int& first, bool report) {
+  if (!p.offsets) {
+    const int each = p.n_rows / p.n_users;
+    first = u * each;
+    return each;
+  }
+  const int a = __ldg(p.offsets + u), b = __ldg(p.offsets + u + 1);
+  first = a;
+  if (a >= 0 && b >= a && b <= p.n_rows && b - a <= p.max_len) return b - a;
+  if (report) atomicOr(p.status, DEV_ERR_CACHE);
+  first = 0;
+  return 0;
+}
+
+// Of user u's scans, items a launch has of each: all segments, or (local) all but the last.
+template <bool kLocal>
+__device__ __forceinline__ int user_segs(const LinParams& p, int u) {
+  if (u >= p.n_users) return 0;
+  int first;
+  const int len = user_rows(p, u, first, false);
+  return max(1, (len + p.seg_len - 1) / p.seg_len) - (kLocal ? 1 : 0);
+}
+
+// Items of one job.  (By whole warps, like get_item.)
+template <bool kLocal>
+__device__ __forceinline__ int job_items(const LinParams& p) {
+  if (p.segs == 1) return p.n_users * p.H;
+  int sum = 0;
+#pragma unroll 1
+  for (int u = 0; u < p.n_users; u += 32) sum += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(user_segs<kLocal>(p, u + static_cast<int>(lane_id())))));
+  return sum * p.H;
+}
+
+// Item i of the launch, of per_job = job_items().
+template <bool kLocal>
+__device__ __forceinline__ void get_item(const LinParams& p, int i, int per_job, Item& x, bool report) {
+  x.job = i / per_job;
+  const int r = i - x.job * per_job;
+  x.seg = 0;
+  if (p.segs == 1) {
+    x.u = r / p.H;
+    x.h = r - x.u * p.H;
+  } else {  // users one after the other, each with its own number of segments for each head
+    int before = 0, u0 = 0, mine, upto;
+#pragma unroll 1
+    for (;; u0 += 32) {
+      mine = user_segs<kLocal>(p, u0 + static_cast<int>(lane_id()));
+      upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (static_cast<int>(lane_id()) >= o) upto += y;
+      }
+      const int all = __shfl_sync(0xffffffffu, upto, 31);
+      if (r < (before + all) * p.H || u0 + 32 >= p.n_users) break;
+      before += all;
+    }
+    const int l = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, r < (before + upto) * p.H))) - 1;
+    mine = __shfl_sync(0xffffffffu, mine, l);
+    const int in = r - (before + __shfl_sync(0xffffffffu, upto, l) - mine) * p.H;
+    x.u = u0 + l;
+    x.h = in / mine;
+    x.seg = in - x.h * mine;
+  }
+  int first;
+  const int len = user_rows(p, x.u, first, report);
+  x.reverse = p.job[x.job].reverse != 0;
+  x.segs = p.segs > 1 ? max(1, (len + p.seg_len - 1) / p.seg_len) : 1;
+  const int r0 = x.segs > 1 ? x.seg * p.seg_len : 0;
+  x.n = x.segs > 1 ? min(p.seg_len, len - r0) : len;
+  x.base = first + (x.reverse ? len - r0 - x.n : r0);
+  x.whole_user_empty = len == 0;
+  x.early = !kLocal && x.seg == 0 && x.reverse ? 1 : 0;
+  x.chunks = (x.n + LT_CHUNK - 1) / LT_CHUNK;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Aux& x, const LinParams& p) {
+  const bool ok = mbar_wait(bar, parity, &x.abort, p.timeout_ns, 1);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(bar);
+}
+
+// A group's warps meet.  (Not a hardware barrier: a warp that gave up does not come.)
+__device__ __forceinline__ bool group_sync(uint64_t* bar, uint32_t& phase, Aux& x, const LinParams& p) {
+  warp_arrive(bar);
+  return warp_wait(bar, phase++ & 1u, x, p);
+}
+
+// Ends when `bar` completes its phase, or a second is over.
+__device__ __forceinline__ void wait_a_second(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 1000000000ull) {}
+}
+
+// 32 lanes x 16 columns from, or 8 columns to, tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Waits for loads, and keeps uses of r behind that.
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// (r0, r1) = (a0, a1) * (b0, b1)
+__device__ __forceinline__ void mul2(float& r0, float& r1, float a0, float a1, float b0, float b1) {
+  asm("{.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\t"
+      "mov.b64 {%0, %1}, w;}"
+      : "=f"(r0), "=f"(r1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// (r0, r1) = (a0, a1) * b + (c0, c1)
+__device__ __forceinline__ void fma2v(float& r0, float& r1, float a0, float a1, float b, float c0, float c1) {
+  asm("{.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %4};\n\t"
+      "mov.b64 z, {%5, %6};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, w;}"
+      : "=f"(r0), "=f"(r1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+// bf16 pairs: a b, and a b + c, in one rounding each.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// v (w.x + w.y) in two parts: the first is v w.x, rounded; what it lacks of that
+// product has few enough bits to be exact, and v w.y is added to it.
+__device__ __forceinline__ void decayed(uint32_t v, uint2 w, uint32_t& hi, uint32_t& lo) {
+  hi = mul_bf16x2(v, w.x);
+  lo = fma_bf16x2(v, w.y, fma_bf16x2(v, w.x, hi ^ 0x80008000u));
+}
+
+// ------------------------------------------------------------------ loader
+// Asks for a tile in L2.
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+template <bool kOutputs, bool kLocal>
+__device__ void loader(const LinParams& p, const LtMaps& maps, uint8_t* sm, Aux& x) {
+  uint32_t g = 0;  // chunks loaded
+  const auto load = [&](uint32_t at, const CUtensorMap* map, uint64_t* full, int h, int row) {
+    if (elect_one()) {
+      mbar_arrive_expect_tx(full, TILE);
+      tma_load_3d(sm + at, map, full, 0, h, row);
+      tma_load_3d(sm + at + HALF_TILE, map, full, 64, h, row);
+    }
+    __syncwarp();
+  };
+  uint32_t ny = 0, nx = 0, nz = 0;
+  bool ok = true;
+  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
+  for (int i = static_cast<int>(blockIdx.x); i < items && ok; i += static_cast<int>(gridDim.x)) {
+    Item it;
+    get_item<kLocal>(p, i, per_job, it, false);
+    for (int c = 0; c < it.chunks && ok; ++c, ++g) {
+      const uint32_t free = (g & 1u) ^ 1u;
+      const int row = it.first(c);
+      ok = warp_wait(&x.y_empty, free, x, p);
+      if (!ok) break;
+      load(Y_AT, &maps.y[it.job], &x.y_full, it.h, row);
+      ++ny;
+      if (kOutputs) {
+        ok = warp_wait(&x.x_empty, free, x, p);
+        if (!ok) break;
+        load(X_AT, &maps.x[it.job], &x.x_full, it.h, row);
+        ++nx;
+      }
+      ok = warp_wait(&x.z_empty, free, x, p);
+      if (!ok) break;
+      load(Z_AT, &maps.z[it.job], &x.z_full, it.h, row);
+      ++nz;
+      if (c + 1 < it.chunks && elect_one()) {  // the next chunk's tiles, ahead of their buffers
+        const int next = it.first(c + 1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          prefetch_3d(&maps.y[it.job], 64 * half, it.h, next);
+          prefetch_3d(&maps.z[it.job], 64 * half, it.h, next);
+          if (kOutputs) prefetch_3d(&maps.x[it.job], 64 * half, it.h, next);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  // the copies in flight end before the CTA does (where all went well, their readers have seen to it)
+  if (!ok) {
+    if (ny) wait_a_second(&x.y_full, (ny - 1) & 1u);
+    if (nx) wait_a_second(&x.x_full, (nx - 1) & 1u);
+    if (nz) wait_a_second(&x.z_full, (nz - 1) & 1u);
+  }
+  __syncwarp();
+}
+
+// ----------------------------------------------------------------- issuers
+// O1 = x S: A K-major, B (rows of S's y elements) MN-major.
+__device__ __forceinline__ void issue_xs(uint32_t o_tmem, uint32_t x_base, uint32_t s_base) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, true);
+  const uint64_t xd = sdesc_sw128(x_base, 16, 1024), sd = sdesc_sw128(s_base, HALF_TILE, 1024);
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks)
+    mma_bf16_ss(o_tmem, xd + (((ks >> 2) * HALF_TILE + (ks & 3) * 32) >> 4), sd + ((ks * 2048u) >> 4), idesc, ks > 0 ? 1u : 0u);
+}
+
+// O2 = A z over the chunk's first 16 `steps` rows.  A's columns 64 .. lie behind
+// 32 unused ones (each half of the output warps writes where it has read).
+__device__ __forceinline__ void issue_az(uint32_t o_tmem, uint32_t a_tmem, uint32_t z_base, int steps) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, true);
+  const uint64_t zd = sdesc_sw128(z_base, HALF_TILE, 1024);
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    if (ks >= steps) break;
+    mma_bf16_ts(o_tmem, a_tmem + ks * 8 + (ks & 4) * 8, zd + ((ks * 2048u) >> 4), idesc, ks > 0 ? 1u : 0u);
+  }
+}
+
+// S += (w y)^T z: both MN-major.
+__device__ __forceinline__ void issue_wyz(uint32_t m_tmem, uint32_t hi_base, uint32_t lo_base, uint32_t z_base, int steps) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, true, true);
+  const uint64_t hd = sdesc_sw128(hi_base, HALF_TILE, 1024), ld = sdesc_sw128(lo_base, HALF_TILE, 1024),
+                 zd = sdesc_sw128(z_base, HALF_TILE, 1024);
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    if (ks >= steps) break;
+    const uint32_t off = (ks * 2048u) >> 4;
+    mma_bf16_ss(m_tmem, hd + off, zd + off, idesc, 1u);
+    mma_bf16_ss(m_tmem, ld + off, zd + off, idesc, 1u);
+  }
+}
+
+template <bool kLocal>
+__device__ void output_issuer(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
+  uint32_t g = 0;
+  const uint32_t xb = smem_u32(sm + X_AT), yb = smem_u32(sm + Y_AT), zb = smem_u32(sm + Z_AT), sb = smem_u32(sm + S_AT);
+  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
+  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
+    Item it;
+    get_item<kLocal>(p, i, per_job, it, false);
+    for (int c = 0; c < it.chunks; ++c, ++g) {
+      const uint32_t ph = g & 1u;
+      if (!warp_wait(&x.y_full, ph, x, p) || !warp_wait(&x.x_full, ph, x, p)) return;
+      // (A's place is free: O2 of the chunk before has ended)
+      if (g > 0 && !warp_wait(&x.o_full, ph ^ 1u, x, p)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_qk_ss(tmem + TM_A, xb, yb);
+        mma_commit(&x.a_full);
+        mma_commit(&x.y_empty);
+      }
+      __syncwarp();
+      // (behind the state's products, which the next chunk's image waits for)
+      if (!warp_wait(&x.m_begun, ph, x, p) || !warp_wait(&x.s_full, ph, x, p) || !warp_wait(&x.o_empty, ph ^ 1u, x, p)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_xs(tmem + TM_O1, xb, sb);
+        mma_commit(&x.x_empty);
+        mma_commit(&x.s_empty);
+      }
+      __syncwarp();
+      // (of a part of a chunk, z's rows behind it are zeros: w y was there before the state's products began.
+      // No wait for it here, only sometimes: a waiter has to see every phase.)
+      if (!warp_wait(&x.z_full, ph, x, p) || !warp_wait(&x.p_full, ph, x, p)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_az(tmem + TM_O2, tmem + TM_A, zb, (it.rows(c) + 15) >> 4);
+        mma_commit(&x.o_full);
+        mma_commit(&x.z_empty);
+      }
+      __syncwarp();
+    }
+  }
+}
+
+template <bool kLocal>
+__device__ void state_issuer(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
+  uint32_t g = 0;
+  const uint32_t zb = smem_u32(sm + Z_AT), hb = smem_u32(sm + HI_AT), lb = smem_u32(sm + LO_AT);
+  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
+  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
+    Item it;
+    get_item<kLocal>(p, i, per_job, it, false);
+    for (int c = 0; c < it.chunks; ++c, ++g) {
+      const uint32_t ph = g & 1u;
+      if (!warp_wait(&x.z_full, ph, x, p) || !warp_wait(&x.w_full, ph, x, p) || !warp_wait(&x.s_full, ph, x, p)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_wyz(tmem + TM_S, hb, lb, zb, (it.rows(c) + 15) >> 4);
+        mma_commit(&x.m_full);
+        mma_commit(&x.z_empty);
+      }
+      warp_arrive(&x.m_begun);
+    }
+  }
+}
+
+// An issuer leaves when its products in flight have ended, or a second is over.
+__device__ void drain(uint64_t* bar) {
+  __syncwarp();
+  if (elect_one()) mma_commit(bar);
+  __syncwarp();
+  wait_a_second(bar, 0);
+  __syncwarp();
+}
+
+__device__ __forceinline__ float decay_power(float log2_decay, int n) {
+  return n == 0 ? 1.f : exp2f(static_cast<float>(n) * log2_decay);
+}
+
+// ---------------------------------------------------------------- A's decays
+// Loops stay loops: code in straight lines is fetched at about 12 cycles an
+// instruction (64 columns unrolled took 6200 cycles a chunk).
+template <bool kLocal>
+__device__ void decay_warps(const LinParams& p, Aux& x, uint32_t tmem) {
+  const int tid = static_cast<int>(threadIdx.x) - 32 * DECAY_WARP0;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
+  const int quarter = warp & 3, half = (warp - DECAY_WARP0) >> 2, i_row = quarter * 32 + lane;
+  const uint32_t At = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM_A + half * 64;
+  uint32_t g = 0, meet = 0;
+  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
+  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
+    Item it;
+    get_item<kLocal>(p, i, per_job, it, false);
+    if (it.chunks == 0) continue;
+    const float log2_decay = log2f(__ldg(p.decay + it.h));
+    if (!group_sync(&x.group[0], meet, x, p)) return;
+    if (tid < LT_CHUNK) x.power[tid] = decay_power(log2_decay, tid) * p.scale;
+    if (tid < 16) reinterpret_cast<float*>(x.near)[tid] = decay_power(log2_decay, it.reverse ? tid : 15 - tid);
+    if (!group_sync(&x.group[0], meet, x, p)) return;
+    for (int c = 0; c < it.chunks; ++c, ++g) {
+      const int rows = it.rows(c);
+      if (!warp_wait(&x.a_full, g & 1u, x, p)) return;
+      tc_fence_after();
+      // columns 64 half .. of row i_row, sixteen at a time, to where they came from
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        uint32_t a[16];
+        tmem_ld16(At + 16 * b, a);
+        const int j0 = 64 * half + 16 * b;
+        const int gap = it.reverse ? j0 - i_row : i_row - (j0 + 15);  // to the block's nearest column
+        uint32_t pk[8] = {};
+        if (__all_sync(0xffffffffu, gap >= 0) && (!it.reverse || j0 + 16 <= rows)) {  // every row reaches all columns
+          const float w = x.power[gap];
+          tmem_ld16_wait(a);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 n = x.near[k];
+            float c0, c1, c2, c3;
+            mul2(c0, c1, __uint_as_float(a[4 * k]), __uint_as_float(a[4 * k + 1]), n.x, n.y);
+            mul2(c2, c3, __uint_as_float(a[4 * k + 2]), __uint_as_float(a[4 * k + 3]), n.z, n.w);
+            mul2(c0, c1, c0, c1, w, w);
+            mul2(c2, c3, c2, c3, w, w);
+            pk[2 * k] = pack_bf16x2(c0, c1);
+            pk[2 * k + 1] = pack_bf16x2(c2, c3);
+          }
+        } else {
+          tmem_ld16_wait(a);
+          if (__any_sync(0xffffffffu, gap >= -15)) {
+            // row by column; columns from `rows` on are another user's, or none's
+            const int most = it.reverse ? rows - 1 - i_row : LT_CHUNK;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int e = it.reverse ? j0 + 2 * k - i_row : i_row - j0 - 2 * k, d = it.reverse ? e + 1 : e - 1;
+              const float w0 = e >= 0 && e <= most ? __uint_as_float(a[2 * k]) * x.power[max(e, 0)] : 0.f;
+              const float w1 = d >= 0 && d <= most ? __uint_as_float(a[2 * k + 1]) * x.power[max(d, 0)] : 0.f;
+              pk[k] = pack_bf16x2(w0, w1);
+            }
+          }
+        }
+        tmem_st8(At + 8 * b, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&x.p_full);
+    }
+  }
+}
+
+// ----------------------------------------------------------------- outputs
+template <bool kLocal>
+__device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
+  const int quarter = warp & 3, half = (warp - OUT_WARP0) >> 2, i_row = quarter * 32 + lane;
+  const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t O1 = tmem + lane_base + TM_O1 + half * 64, O2 = tmem + lane_base + TM_O2 + half * 64;
+  uint8_t* stage = sm + OUT_AT + (warp - OUT_WARP0) * OUT_BYTES;
+  uint32_t g = 0;
+  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
+  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
+    Item it;
+    get_item<kLocal>(p, i, per_job, it, false);
+    const LinJob& job = p.job[it.job];
+    const float log2_decay = log2f(__ldg(p.decay + it.h));
+    for (int c = 0; c < it.chunks; ++c, ++g) {
+      const int rows = it.rows(c);
+      const float w1 = decay_power(log2_decay, max(it.reverse ? rows - i_row - (c == 0 ? it.early : 0) : i_row + 1, 0)) * p.scale;
+      const bool stores = quarter * 32 < rows && job.out;
+      if (!warp_wait(&x.o_full, g & 1u, x, p)) return;
+      tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; b < 4 && stores; ++b) {
+        uint32_t a[16], o[16], out[8];
+        tmem_ld16(O1 + 16 * b, a);
+        tmem_ld16(O2 + 16 * b, o);
+        tmem_ld16_wait(a);
+        tmem_ld16_wait(o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float u, v;
+          fma2v(u, v, __uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]), w1, __uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+          out[j] = pack_bf16x2(u, v);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * b + q) ^ (lane & 7)) << 4)) =
+              make_uint4(out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]);
+      }
+      tc_fence_before();
+      warp_arrive(&x.o_empty);
+      if (!stores) continue;
+      // through shared memory, so that a store fills whole lines: stores of a sector in each of 32 lines took the
+      // unit that shared memory goes through for 57 cycles each
+      uint16_t* dst = job.out + static_cast<int64_t>(it.first(c) + quarter * 32) * job.os + it.h * LIN_D + half * 64 + 8 * (lane & 7);
+#pragma unroll 4
+      for (int q = 0; q < 8; ++q) {
+        const int r = 4 * q + (lane >> 3);
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+        if (quarter * 32 + r < rows) *reinterpret_cast<uint4*>(dst + r * job.os) = v;
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// ------------------------------------------------------------------- state
+template <bool kOutputs, bool kLocal>
+__device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
+  const int quarter = warp & 3, half = (warp - STATE_WARP0) >> 2, e_row = quarter * 32 + lane;  // a row of the state, 64 half .. of its columns
+  const uint32_t St = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM_S + half * 64;
+  uint8_t* image = sm + S_AT + half * HALF_TILE + e_row * 128;
+  uint32_t g = 0;
+  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
+  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
+    Item it;
+    get_item<kLocal>(p, i, per_job, it, threadIdx.x == 32 * STATE_WARP0);
+    const LinJob& job = p.job[it.job];
+    const float log2_decay = log2f(__ldg(p.decay + it.h));
+    const int64_t state = (static_cast<int64_t>(it.u) * p.H + it.h) * LIN_STATE;
+    const int64_t ws = ((static_cast<int64_t>(it.job) * p.n_users + it.u) * p.H + it.h) * p.segs;
+    const float* from = nullptr;
+    if (!kLocal) {  // of several segments the first one's start is in the workspace too, as s_out may be s_in
+      if (it.segs > 1) from = p.ws + (ws + (it.seg > 0 ? it.seg - 1 : it.segs - 1)) * LIN_STATE;
+      else if (job.s_in) from = job.s_in + state;
+    }
+    const float factor = it.segs > 1 ? 1.f : job.s_in_factor;
+    const bool turned = it.segs == 1 && job.s_in_turned;
+    float* to = kLocal ? p.ws + (ws + it.seg) * LIN_STATE : (it.seg + 1 == it.segs && job.s_out ? job.s_out + state : nullptr);
+    const float up = kLocal ? 1.f : (it.reverse && !it.whole_user_empty ? job.s_out_factor * decay_power(log2_decay, 1) : job.s_out_factor);
+    // chunk by chunk: the image of the state before it, and the decay over it; then
+    // the products add the chunk.  One turn more gives the end away.
+    for (int c = 0; c <= it.chunks; ++c) {
+      const bool last = c == it.chunks;
+      if (c > 0 && !warp_wait(&x.m_full, (g - 1) & 1u, x, p)) return;
+      if (last && !to) break;
+      if (kOutputs && !last && !warp_wait(&x.s_empty, (g & 1u) ^ 1u, x, p)) return;
+      tc_fence_after();
+      const float down = last ? up : decay_power(log2_decay, it.rows(c) - (c == 0 ? it.early : 0));
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {
+        uint32_t v[32];
+        if (c > 0) {
+          tmem_ld32(St + 32 * b, v);
+          tmem_ld_wait(v);
+        } else if (!from) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = 0;
+        } else if (!turned) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(from + e_row * LIN_D + 64 * half + 32 * b) + k);
+            v[4 * k] = __float_as_uint(f.x * factor);
+            v[4 * k + 1] = __float_as_uint(f.y * factor);
+            v[4 * k + 2] = __float_as_uint(f.z * factor);
+            v[4 * k + 3] = __float_as_uint(f.w * factor);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__ldcg(from + (64 * half + 32 * b + k) * LIN_D + e_row) * factor);
+        }
+        if (kOutputs && !last) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = pack_bf16x2(__uint_as_float(v[8 * k + 2 * q]), __uint_as_float(v[8 * k + 2 * q + 1]));
+            *reinterpret_cast<uint4*>(image + (((4 * b + k) ^ (e_row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float f0, f1;
+          mul2(f0, f1, __uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]), down, down);
+          v[2 * k] = __float_as_uint(f0);
+          v[2 * k + 1] = __float_as_uint(f1);
+        }
+        if (last) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<uint4*>(to + e_row * LIN_D + 64 * half + 32 * b)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        } else {
+          tmem_st32(St + 32 * b, v);
+        }
+      }
+      if (last) break;
+      tmem_st_wait();
+      tc_fence_before();
+      fence_proxy_async_smem();
+      warp_arrive(&x.s_full);
+      ++g;
+    }
+  }
+}
+
+// -------------------------------------------------------------- w y's parts
+template <bool kLocal>
+__device__ void parts_warps(const LinParams& p, uint8_t* sm, Aux& x) {
+  constexpr int kThreads = 32 * PARTS_WARPS;
+  const int tid = static_cast<int>(threadIdx.x) - 32 * PARTS_WARP0;
+  uint32_t g = 0, meet = 0;
+  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
+  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
+    Item it;
+    get_item<kLocal>(p, i, per_job, it, false);
+    if (it.chunks == 0) continue;
+    if (!group_sync(&x.group[1], meet, x, p)) return;
+    {
+      static_assert(kThreads == LT_CHUNK, "a decay a thread");
+      const float w = decay_power(log2f(__ldg(p.decay + it.h)), tid);
+      const uint32_t hi = pack_bf16x2(w, w);
+      const float rest = w - bf16_lo(hi);
+      x.parts[tid] = make_uint2(hi, pack_bf16x2(rest, rest));
+    }
+    if (!group_sync(&x.group[1], meet, x, p)) return;
+    for (int c = 0; c < it.chunks; ++c, ++g) {
+      const uint32_t ph = g & 1u;
+      const int rows = it.rows(c);
+      // (element-wise: any order of the tile's 16-byte pieces)
+      if (!warp_wait(&x.y_full, ph, x, p) || (g > 0 && !warp_wait(&x.m_full, ph ^ 1u, x, p))) return;
+#pragma unroll 1
+      for (int k0 = 0; k0 < 16; k0 += 4) {
+        uint4 v[4];
+        uint2 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = (k0 + k) * kThreads + tid, j = (e >> 3) & (LT_CHUNK - 1);
+          v[k] = *reinterpret_cast<const uint4*>(sm + Y_AT + e * 16);
+          w[k] = x.parts[it.reverse ? j : max(rows - 1 - j, 0)];
+          if (j >= rows) v[k] = uint4{};
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = (k0 + k) * kThreads + tid;
+          uint4 hi, lo;
+          decayed(v[k].x, w[k], hi.x, lo.x);
+          decayed(v[k].y, w[k], hi.y, lo.y);
+          decayed(v[k].z, w[k], hi.z, lo.z);
+          decayed(v[k].w, w[k], hi.w, lo.w);
+          *reinterpret_cast<uint4*>(sm + HI_AT + e * 16) = hi;
+          *reinterpret_cast<uint4*>(sm + LO_AT + e * 16) = lo;
+        }
+      }
+      if (rows < LT_CHUNK) {  // rows that are another user's, or none's: no value, whatever they hold
+        if (!warp_wait(&x.z_full, ph, x, p)) return;
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) {
+          const int e = k * kThreads + tid, j = (e >> 3) & (LT_CHUNK - 1);
+          if (j >= rows) *reinterpret_cast<uint4*>(sm + Z_AT + e * 16) = uint4{};
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane_id() == 0) {
+        mbar_arrive(&x.w_full);
+        mbar_arrive(&x.y_empty);
+      }
+    }
+  }
+}
+
+template <bool kOutputs, bool kLocal>
+__global__ void __launch_bounds__(LT_THREADS, 1) lin_tile_kernel(const __grid_constant__ LinParams p, const __grid_constant__ LtMaps maps) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  Aux& x = *reinterpret_cast<Aux*>(sm + AUX_AT);
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  if (threadIdx.x == 0) {
+    uint64_t* once[] = {&x.x_full, &x.y_full, &x.z_full, &x.x_empty, &x.a_full, &x.o_full, &x.s_empty, &x.m_full, &x.m_begun, &x.drain[0], &x.drain[1]};
+    for (uint64_t* b : once) mbar_init(b, 1);
+    mbar_init(&x.y_empty, PARTS_WARPS + (kOutputs ? 1 : 0));
+    mbar_init(&x.z_empty, kOutputs ? 2 : 1);
+    uint64_t* warps[] = {&x.p_full, &x.o_empty, &x.s_full, &x.group[0]};
+    for (uint64_t* b : warps) mbar_init(b, GROUP_WARPS);
+    mbar_init(&x.w_full, PARTS_WARPS);
+    mbar_init(&x.group[1], PARTS_WARPS);
+    x.abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 3) {
+    tmem_alloc(&x.tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = x.tmem_slot;
+
+  if (warp < DECAY_WARP0) {
+    if (warp == 0) loader<kOutputs, kLocal>(p, maps, sm, x);
+    if (warp == 1 && kOutputs) output_issuer<kLocal>(p, sm, x, tmem);
+    if (warp == 2) state_issuer<kLocal>(p, sm, x, tmem);
+    if (warp == 1 || warp == 2) drain(&x.drain[warp - 1]);
+  } else if (warp < OUT_WARP0) {
+    if (kOutputs) decay_warps<kLocal>(p, x, tmem);
+  } else if (warp < STATE_WARP0) {
+    if (kOutputs) output_warps<kLocal>(p, sm, x, tmem);
+  } else if (warp < PARTS_WARP0) {
+    state_warps<kOutputs, kLocal>(p, sm, x, tmem);
+  } else {
+    parts_warps<kLocal>(p, sm, x);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (x.abort && threadIdx.x == 0) atomicOr(p.status, DEV_ERR_PIPE_TIMEOUT);
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool kOutputs, bool kLocal>
+cudaError_t launch(const LinParams& p, const LtMaps& maps, int num_sms, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(lin_tile_kernel<kOutputs, kLocal>, cudaFuncAttributeMaxDynamicSharedMemorySize, LT_SMEM);
+  if (e != cudaSuccess) return e;
+  // (segments of all users: no more than their rows hold, and one each)
+  const int64_t segs = p.segs > 1 ? p.n_rows / p.seg_len + static_cast<int64_t>(p.n_users) : p.n_users;
+  const int64_t items = segs * p.H * p.n_jobs;
+  lin_tile_kernel<kOutputs, kLocal><<<static_cast<unsigned>(items < num_sms ? items : num_sms), LT_THREADS, LT_SMEM, s>>>(p, maps);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box);
+
+size_t lin_tile_smem() { return LT_SMEM; }
+
+// The scans, or (local) the segments' own parts.
+cudaError_t launch_lin_tiles(const LinParams& p, bool local, int num_sms, cudaStream_t s) {
+  LtMaps maps;
+  const auto encode = [&](CUtensorMap* m, const uint16_t* t, int64_t stride) {
+    const uint64_t dims[3] = {LIN_D, static_cast<uint64_t>(p.H), static_cast<uint64_t>(p.n_rows)};
+    const uint64_t strides[2] = {LIN_D * 2, static_cast<uint64_t>(stride) * 2};
+    const uint32_t box[3] = {64, 1, LT_CHUNK};
+    return encode_bf16(m, t, 3, dims, strides, box);
+  };
+  const bool outputs = p.job[0].x != nullptr && !local;
+  for (int k = 0; k < p.n_jobs; ++k) {
+    const LinJob& j = p.job[k];
+    if (!encode(&maps.y[k], j.y, j.ys) || !encode(&maps.z[k], j.z, j.zs) || (outputs && !encode(&maps.x[k], j.x, j.xs)))
+      return cudaErrorInvalidValue;
+  }
+  for (int k = p.n_jobs; k < LIN_MAX_JOBS; ++k) maps.y[k] = maps.z[k] = maps.y[0];
+  for (int k = outputs ? p.n_jobs : 0; k < LIN_MAX_JOBS; ++k) maps.x[k] = maps.y[0];
+  if (local) return launch<false, true>(p, maps, num_sms, s);
+  return outputs ? launch<true, false>(p, maps, num_sms, s) : launch<false, false>(p, maps, num_sms, s);
+}
+
+}  // namespace ikbo

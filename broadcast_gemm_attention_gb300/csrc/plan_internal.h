@@ -161,6 +161,10 @@ cudaError_t grow_kept(ikbo_plan_s* p, KeptBuffer<T>* b, size_t need, size_t most
   return cudaSuccess;
 }
 
+// A bf16 tensor map with the 128-byte swizzle (api.cu).
+bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                 const uint32_t* box);
+
 // Broadcast attention over bf16 K/V (api.cu), every entry point's launch:
 // target units of the plan's work list, plus self units when Q_user is given.
 // kv_lens (with jagged kv_offsets): user u's keys are rows kv_offsets[u] ..

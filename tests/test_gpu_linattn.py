@@ -222,7 +222,7 @@ def test_slices_of_a_projection_and_dense_rows():
     with plan() as p:
         p.linattn_forward(Q, K, V, decay, wide[:, 1], n_users=U)
         plain = torch.empty((U * L, H, D), dtype=torch.bfloat16, device="cuda")
-        p.linattn_forward(Q.contiguous(), K.contiguous(), V.contiguous(), decay, plain, offsets=i32(offsets_of([L] * U)))
+        p.linattn_forward(Q.contiguous(), K.contiguous(), V.contiguous(), decay, plain, offsets=i32(offsets_of([L] * U)), max_len=L)  # (the variant goes by it)
         assert torch.equal(wide[:, 1], plain) and not wide[:, 0].any()
         g, dq = torch.zeros_like(qkv), bf(rng.standard_normal((U * L, H, D)))
         p.linattn_backward(Q, K, V, dq, decay, g[:, 0], g[:, 1], g[:, 2], n_users=U)
@@ -296,6 +296,29 @@ def test_many_users_of_a_few_rows():
         O, S = run_forward(p, d, max_len=9)
         near(O, ref)
         near_state(S, last, R.weights(d.K, d.V, d.decay, d.off, d.S))
+
+
+def test_more_histories_than_sms():
+    """Each CTA of the tile kernel goes through several, most ending in a part of a chunk."""
+    rng = np.random.default_rng(2)
+    lens = rng.integers(0, 400, 90)
+    lens[[3, 40]] = 0, 256
+    d = Data(16, lens, 4, decay=[0.99, 1.0, 0.7, 0.0])
+    ref, last = R.forward(d.Q, d.K, d.V, d.decay, d.off, d.S, SCALE)
+    g64 = R.backward(d.Q, d.K, d.V, d.dO, d.decay, d.off, d.S, d.dS, SCALE)
+    gmass = R.backward(*(np.abs(x) for x in (d.Q, d.K, d.V, d.dO)), d.decay, d.off, np.abs(d.S), np.abs(d.dS), SCALE)[3]
+    with plan() as p:
+        O, S = run_forward(p, d, max_len=400)
+        near(O, ref)
+        near_state(S, last, R.weights(d.K, d.V, d.decay, d.off, d.S))
+        Q, K, V, decay, off = d.cuda()
+        outs, dS = [torch.empty_like(Q) for _ in range(3)], torch.empty_like(S)
+        p.linattn_backward(Q, K, V, bf(d.dO), decay, *outs, state_in=f32(d.S), d_state_out=f32(d.dS), d_state_in=dS, offsets=off,
+                           max_len=400)
+        for got, want, name in zip(outs, g64, ("dQ", "dK", "dV")):
+            near(got, want, name)
+        near_state(dS, g64[3], gmass)
+        assert p.status() == B.IKBO_OK
 
 
 # ------------------------------------------------------------------- reads
