@@ -61,7 +61,7 @@ struct LinShared {
 // kOutputs: with queries; else the states alone.  kLocal: a segment's own part
 // of its end state, from zero, to the workspace.
 template <bool kOutputs, bool kLocal>
-__global__ void __launch_bounds__(LIN_THREADS, 1) lin_chunk_kernel(const __grid_constant__ LinParams p) {
+__global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kernel(const __grid_constant__ LinParams p) {
   extern __shared__ __align__(128) uint8_t lin_sm[];
   __shared__ LinShared sh;
   constexpr int kTiles = kOutputs ? 3 : 2;  // y, z, x
@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(LIN_THREADS, 1) lin_chunk_kernel(const __grid_
       }
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
+        if (16 * mt >= rows) break;
         float o[2][4] = {};
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
@@ -292,15 +293,19 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ L
 }
 
 // Few rows a user: the state through registers once, a row at a time.  A warp
-// has 16 of the state's rows (y's elements), a lane 4 of its columns.
+// has 16 of the state's rows (y's elements), a lane 4 of its columns; x, y and z
+// come as fp32 through shared memory, 16 rows of them at a time.
+constexpr int STEP_ROWS = 16;
+
 template <bool kOutputs>
 __global__ void __launch_bounds__(LIN_THREADS) lin_step_kernel(const __grid_constant__ LinParams p) {
+  __shared__ float4 rows[kOutputs ? 3 : 2][STEP_ROWS][LIN_D / 4];  // y, z, x
   __shared__ float part[2][8][LIN_D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int u = static_cast<int>(blockIdx.x) / p.H, h = static_cast<int>(blockIdx.x) - u * p.H;
   const LinJob& job = p.job[0];
-  int row;
-  const int len = lin_rows(p, u, row);
+  int first;
+  const int len = lin_rows(p, u, first);
   const int64_t state = (static_cast<int64_t>(u) * p.H + h) * LIN_STATE;
   float* to = job.s_out ? job.s_out + state : nullptr;
   const float* from = job.s_in ? job.s_in + state : nullptr;
@@ -308,39 +313,55 @@ __global__ void __launch_bounds__(LIN_THREADS) lin_step_kernel(const __grid_cons
   float4 s[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k)
-    s[k] = from ? reinterpret_cast<const float4*>(from)[(16 * warp + k) * 32 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    s[k] = from ? __ldcg(reinterpret_cast<const float4*>(from) + (16 * warp + k) * 32 + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
   const float decay = __ldg(p.decay + h);
 #pragma unroll 1
-  for (int r = 0; r < len; ++r) {
-    const int64_t at = static_cast<int64_t>(row + r);
-    const uint2 zv = *reinterpret_cast<const uint2*>(job.z + at * job.zs + h * LIN_D + 4 * lane);
-    const uint32_t yv = reinterpret_cast<const uint16_t*>(job.y + at * job.ys + h * LIN_D + 16 * warp)[lane & 15];
-    const uint32_t xv = kOutputs ? reinterpret_cast<const uint16_t*>(job.x + at * job.xs + h * LIN_D + 16 * warp)[lane & 15] : 0u;
-    const float z0 = bf16_lo(zv.x), z1 = bf16_hi(zv.x), z2 = bf16_lo(zv.y), z3 = bf16_hi(zv.y);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float y = bf16_lo(__shfl_sync(0xffffffffu, yv, k));
-      s[k].x = fmaf(y, z0, s[k].x * decay);
-      s[k].y = fmaf(y, z1, s[k].y * decay);
-      s[k].z = fmaf(y, z2, s[k].z * decay);
-      s[k].w = fmaf(y, z3, s[k].w * decay);
-      if (kOutputs) {
-        const float x = bf16_lo(__shfl_sync(0xffffffffu, xv, k));
-        o.x = fmaf(x, s[k].x, o.x);
-        o.y = fmaf(x, s[k].y, o.y);
-        o.z = fmaf(x, s[k].z, o.z);
-        o.w = fmaf(x, s[k].w, o.w);
-      }
+  for (int r0 = 0; r0 < len; r0 += STEP_ROWS) {
+    const int n = min(STEP_ROWS, len - r0);
+    if (r0 > 0) __syncthreads();
+    for (int i = tid; i < n * 16 * (kOutputs ? 3 : 2); i += LIN_THREADS) {  // 16-byte pieces
+      const int t = i / (16 * n), r = (i - t * 16 * n) >> 4, c = i & 15;
+      const uint16_t* src = t == 0 ? job.y : (t == 1 ? job.z : job.x);
+      const int64_t stride = t == 0 ? job.ys : (t == 1 ? job.zs : job.xs);
+      const uint4 v = *reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(first) + r0 + r) * stride + h * LIN_D + 8 * c);
+      rows[t][r][2 * c] = make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+      rows[t][r][2 * c + 1] = make_float4(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w));
     }
-    if (kOutputs) {
-      reinterpret_cast<float4*>(part[r & 1][warp])[lane] = o;
-      __syncthreads();  // (the other half is written next)
-      if (tid < LIN_D) {
-        float sum = 0.f;
+    __syncthreads();
+#pragma unroll 1
+    for (int r = 0; r < n; ++r) {
+      const float4 z = rows[1][r][lane];
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < 8; ++w) sum += part[r & 1][w][tid];
-        reinterpret_cast<__nv_bfloat16*>(job.out)[at * job.os + h * LIN_D + tid] = __float2bfloat16_rn(sum * p.scale);
+      for (int q = 0; q < 4; ++q) {
+        const float4 yv = rows[0][r][4 * warp + q], xv = kOutputs ? rows[kOutputs ? 2 : 0][r][4 * warp + q] : yv;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = e == 0 ? yv.x : (e == 1 ? yv.y : (e == 2 ? yv.z : yv.w));
+          float4& v = s[4 * q + e];
+          v.x = fmaf(y, z.x, v.x * decay);
+          v.y = fmaf(y, z.y, v.y * decay);
+          v.z = fmaf(y, z.z, v.z * decay);
+          v.w = fmaf(y, z.w, v.w * decay);
+          if (kOutputs) {
+            const float x = e == 0 ? xv.x : (e == 1 ? xv.y : (e == 2 ? xv.z : xv.w));
+            o.x = fmaf(x, v.x, o.x);
+            o.y = fmaf(x, v.y, o.y);
+            o.z = fmaf(x, v.z, o.z);
+            o.w = fmaf(x, v.w, o.w);
+          }
+        }
+      }
+      if (kOutputs) {
+        reinterpret_cast<float4*>(part[r & 1][warp])[lane] = o;
+        __syncthreads();  // (the other half is written next)
+        if (tid < LIN_D) {
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < 8; ++w) sum += part[r & 1][w][tid];
+          reinterpret_cast<__nv_bfloat16*>(job.out)[(static_cast<int64_t>(first) + r0 + r) * job.os + h * LIN_D + tid] =
+              __float2bfloat16_rn(sum * p.scale);
+        }
       }
     }
   }

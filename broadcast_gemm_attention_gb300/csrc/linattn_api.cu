@@ -12,7 +12,8 @@ namespace ikbo {
 cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int* launches);
 size_t lin_tile_smem();
 cudaError_t launch_lin_read(const LinReadParams& p, int num_sms, cudaStream_t s);
-cudaError_t launch_lin_read_state(const LinReadParams& p, int num_sms, cudaStream_t s);
+cudaError_t launch_lin_read_join(const LinReadParams& p, int num_sms, cudaStream_t s);
+size_t lin_read_smem();
 int lin_read_ctas(int num_sms);
 }  // namespace ikbo
 
@@ -60,11 +61,19 @@ ikbo_status_t lin_params(ikbo_plan_t p, const int32_t* d_offsets, int n_users, i
 // others'.  At most LIN_MOST_STATES states lie between segments.
 constexpr int64_t LIN_MOST_STATES = 16384;  // 1 GiB
 constexpr int LIN_LEAST_SEGMENT = 256;
-constexpr int LIN_LEAST_TILES = 128;
+
+// The variant, from the bound on a user's rows.  Measured, 8 heads (us):
+//   forward              15 users of 4     8    16    64   128   192   256 rows   100 users of 8   128   256
+//   row by row                     4.6   6.2   9.1  27.6                                       32.8
+//   chunks, warps' registers             6.9   6.9   9.2  13.5  17.8  22.2                     41.3  83.7 135.5
+//   chunks, tensor memory               13.6  13.6  14.1  14.1  16.8  17.0                     75.5  90.2 113.9
+//   the states alone: row by row 3.8 4.5 6.0 15.2, registers 5.4 (8 rows) .. 8.3 (128) 12.0 (256) 18.7 (512),
+//   tensor memory 10.8 .. 10.9 12.5 15.6; the gradient, 64 and 128 rows: registers 22.1 and 35.1, tensor memory 24.3 and 24.7
+constexpr int LIN_TILES_FROM[3] = {129, 257, 65};  // forward, states alone, gradient
 
 void cut_segments(LinParams* lp, int num_sms) {
-  const int64_t items = static_cast<int64_t>(lp->n_users) * lp->H * lp->n_jobs;
-  const int64_t rows = static_cast<int64_t>(lp->n_rows) * lp->H * lp->n_jobs;
+  const int64_t items = static_cast<int64_t>(lp->n_users) * lp->H * (lp->backward ? LIN_MAX_JOBS : 1);
+  const int64_t rows = static_cast<int64_t>(lp->n_rows) * lp->H * (lp->backward ? LIN_MAX_JOBS : 1);
   // (each scan's last segment is a part of one: as many SMs are left out of the division)
   int64_t seg = std::max<int64_t>(items * 2 <= num_sms ? (rows + num_sms - items - 1) / (num_sms - items) : 4 * (rows / num_sms), LIN_LEAST_SEGMENT);
   const int64_t most = LIN_MOST_STATES / items;  // segments of a user
@@ -80,7 +89,7 @@ ikbo_status_t lin_run(ikbo_plan_t p, LinParams* lp, cudaStream_t stream) {
   if (static_cast<int64_t>(lp->n_users) * lp->H > INT32_LIMIT / 256) return IKBO_ERR_UNSUPPORTED;
   if (!lp->steps) {
     cut_segments(lp, p->num_sms);
-    lp->tiles = lp->max_len > LIN_LEAST_TILES && lin_tile_smem() <= p->max_smem;
+    lp->tiles = lp->max_len >= LIN_TILES_FROM[lp->backward ? 2 : (lp->job[0].x ? 0 : 1)] && lin_tile_smem() <= p->max_smem;
   }
   if (lp->segs > 1) {
     bool capturing = false;
@@ -101,6 +110,7 @@ ikbo_status_t read_call(ikbo_plan_t p, const void* x, const float* state, int d,
   if (!p) return IKBO_ERR_INVALID_ARG;
   if (!p->planned) return IKBO_ERR_NOT_PLANNED;
   if (!plan_device_current(p)) return IKBO_ERR_INVALID_ARG;
+  if (lin_read_smem() > p->max_smem) return IKBO_ERR_UNSUPPORTED;
   std::memset(rp, 0, sizeof(*rp));
   rp->x = static_cast<const uint16_t*>(x);
   rp->state = state;
@@ -115,6 +125,7 @@ ikbo_status_t read_call(ikbo_plan_t p, const void* x, const float* state, int d,
   rp->H = p->H;
   rp->Lq = p->Lq;
   rp->scale = scale;
+  rp->timeout_ns = p->timeout_ns;
   return IKBO_OK;
 }
 
@@ -185,6 +196,7 @@ ikbo_status_t ikbo_linattn_backward(ikbo_plan_t p, const void* Q, const void* K,
   LinParams lp;
   ikbo_status_t st = lin_params(p, d_offsets, n_users, n_rows, max_len, H, d, decay, scale, &lp);
   if (st != IKBO_OK) return st;
+  lp.backward = 1;
   const auto add = [&](int x, int y, int z, void* o, int os, const float* s_in, bool turned, float* s_out, bool reverse) {
     LinJob& j = lp.job[lp.n_jobs++];
     j.x = static_cast<const uint16_t*>(in[x]);
@@ -237,15 +249,13 @@ ikbo_status_t ikbo_linattn_read_backward(ikbo_plan_t p, const void* Q, const flo
     rp.part = p->lin_part.ptr;
     rp.d_state = d_state;
   }
-  if (dQ) {
-    rp.out = static_cast<uint16_t*>(dQ);
-    rp.turned = 1;
-    if (launch_lin_read(rp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
-    p->launches++;
-  }
+  rp.out = static_cast<uint16_t*>(dQ);
+  rp.turned = 1;
+  if (launch_lin_read(rp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+  p->launches++;
   if (d_state) {
-    if (launch_lin_read_state(rp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
-    p->launches += 2;
+    if (launch_lin_read_join(rp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+    p->launches++;
   }
   return IKBO_OK;
 }

@@ -36,6 +36,7 @@ struct LinParams {
   float* ws;               // states between segments [job][u][h][segs], at a segment's end
   int n_jobs, n_users, n_rows, H, max_len;
   int seg_len, segs;       // rows of a segment (a multiple of the chunk), segments of the longest user; 1: no segments
+  int backward;            // the jobs are a gradient's (variants do not go by which of them are asked for)
   int steps;               // rows one by one (a forward scan alone)
   int tiles;               // the chunks' products on the 5th-gen tensor cores
   uint64_t timeout_ns;
@@ -58,6 +59,7 @@ struct LinReadParams {
   int n_cand, n_users, H, Lq;
   int turned;               // out = x S^T
   float scale;
+  uint64_t timeout_ns;
 };
 
 }  // namespace ikbo

@@ -1,240 +1,367 @@
-// linread.cu -- candidates' queries of their user's state of linear attention,
+// linread.cu -- candidates' queries of their users' states of linear attention,
 // read through the map, and the gradient.
 //
 //   O[i,h] = scale Q[i,h] S[map[i],h]
 //   dQ[i,h] = scale dO[i,h] S[map[i],h]^T,   dS[u,h] = scale sum_{map[i]=u} Q[i,h]^T dO[i,h]
 //
 // The broadcast's linear form: a user's 64 KB state serves all of its
-// candidates, grouped by the plan's work list as the attention's are, and the
-// gradient of the state is the sum over them.
+// candidates, and the gradient of the state is the sum over them.
+//
+// A unit of the plan's work list is up to 128 rows (the queries of a few candidates)
+// of one user and head.  Its tile is gathered by TMA, a box for each candidate, and
+//   O = x S       with S's bf16 image as B (MN-major),
+//   dQ = dO S^T   with the same image as a K-major B,
+//   dS += Q^T dO  (backward) into tensor memory over all of a run of units of one
+//                 (user, head), both operands MN-major: rows are the inner dimension.
+// One pass over the rows serves both gradients.  Bound: memory.
+//
+// Per CTA (persistent, one per SM, an equal run of the list, 20 warps):
+//   warp 0       loads; warp 1 issues
+//   warps 4-11   outputs, and at a run's end the state's gradient
+//   warps 12-19  images of the states, one run ahead; zeros for users without candidates
+// Runs cut by a CTA's share leave their gradients as parts, which
+// lin_read_join_kernel adds in order.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "linattn_internal.h"
 #include "mma_common.cuh"
+#include "tile_common.cuh"
 
 namespace ikbo {
+int lin_read_ctas(int num_sms);
 namespace {
 
-constexpr int RD_THREADS = 256;
-constexpr int RD_ROWS = 128;  // of a unit, at most (16 a warp)
-constexpr int RD_TILE = RD_ROWS * LIN_D * 2;
+constexpr int RT_THREADS = 640, JOIN_THREADS = 256;
+constexpr int OUT_WARP0 = 4, IMAGE_WARP0 = 12, GROUP_WARPS = 8;
+constexpr uint32_t TILE = 2 * HALF_TILE;  // 32 KB
+constexpr int RING_TILES = 4;             // a stage is a tile (forward) or two
+constexpr uint32_t IMAGE_AT = RING_TILES * TILE, OUT_AT = IMAGE_AT + 2 * TILE;
+constexpr uint32_t OUT_BYTES = 32 * 128;  // of the outputs, per warp
+constexpr uint32_t AUX_AT = OUT_AT + GROUP_WARPS * OUT_BYTES;
+constexpr uint32_t TM_O = 0, TM_DS = 256;
 
-// Whether unit i exists and is sound (n is the list's length).
-__device__ __forceinline__ bool read_unit(const LinReadParams& p, int i, int4& w) {
-  w = __ldg(reinterpret_cast<const int4*>(p.work) + i);
-  if (w.x >= 0 && w.x < p.n_users && w.y >= 0 && w.y < p.H && w.z >= 0 && w.w > 0 && w.z + w.w <= p.n_cand && w.w * p.Lq <= RD_ROWS) return true;
-  if (threadIdx.x == 0) atomicOr(p.status, DEV_ERR_BAD_WORK);
-  return false;
-}
+struct Aux {
+  uint64_t full[RING_TILES], empty[RING_TILES];
+  uint64_t o_full[2], o_empty[2], image_full[2], image_empty[2], ds_full[2], ds_empty[2], drain;
+  uint32_t tmem_slot, abort;
+};
+constexpr uint32_t RT_SMEM = AUX_AT + sizeof(Aux) + 1024;
+static_assert(RT_SMEM <= 227 * 1024, "tiles do not fit in shared memory");
 
-__device__ __forceinline__ int64_t row_of(const LinReadParams& p, const int4& w, int r) {
-  const int slot = r / p.Lq;
-  return (static_cast<int64_t>(__ldg(p.perm + w.z + slot)) * p.H + w.y) * p.Lq + (r - slot * p.Lq);
-}
-
-// 16 bytes that nobody reads again (and that may be overwritten by whoever read
-// them: not the read-only path).
-__device__ __forceinline__ uint4 ld_once(const uint4* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
-  return r;
-}
-
-// This CTA's units: an equal run of the list.
-__device__ __forceinline__ void unit_range(const LinReadParams& p, int cta, int& a, int& b) {
-  const int n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
-  a = static_cast<int>(static_cast<int64_t>(cta) * n / gridDim.x);
-  b = static_cast<int>(static_cast<int64_t>(cta + 1) * n / gridDim.x);
-}
-
-// out = scale x S (or x S^T).  The state's bf16 image lies in shared memory, [inner
-// element][column], columns in the order that leaves each lane eight consecutive
-// ones of a row: column 32 m + 8 t + 2 i + e at 32 m + 8 i + 2 t + e.  A lane loads
-// its rows in 16-byte pieces, which the inner order of the products follows: slot k
-// of step 2 j + f is element 32 j + 8 ((k & 7) >> 1) + 4 f + 2 (k >> 3) + (k & 1).
-struct ReadRows {
-  uint4 x[2][4];  // rows g and g + 8 of the warp's 16, element 32 j + 8 t of piece j
-  int64_t at[2];  // their places, -1: not there
+// This CTA's units a .. b - 1, and a walk over them with the runs of one (user, head).
+struct Walk {
+  int a, b;
+  uint32_t runs;   // begun so far
+  int u, h;        // of the run
+  bool begins, ends;
+  int4 w;
+  __device__ __forceinline__ Walk(const LinReadParams& p) : runs(0), u(-1), h(-1) {
+    const int64_t n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
+    a = static_cast<int>(blockIdx.x * n / gridDim.x);
+    b = static_cast<int>((blockIdx.x + 1) * n / gridDim.x);
+  }
+  __device__ __forceinline__ static int4 unit(const LinReadParams& p, int i) { return __ldg(reinterpret_cast<const int4*>(p.work) + i); }
+  // Unit i; false (to every role alike) where the list is not sound, which ends the share.
+  __device__ __forceinline__ bool at(const LinReadParams& p, int i) {
+    w = unit(p, i);
+    if (w.x < 0 || w.x >= p.n_users || w.y < 0 || w.y >= p.H || w.z < 0 || w.w <= 0 || w.z + w.w > p.n_cand || w.w * p.Lq > 128) {
+      if (threadIdx.x == 0) atomicOr(p.status, DEV_ERR_BAD_WORK);
+      return false;
+    }
+    begins = w.x != u || w.y != h;
+    runs += begins;
+    u = w.x;
+    h = w.y;
+    ends = true;
+    if (i + 1 < b) {
+      const int4 n = unit(p, i + 1);
+      ends = n.x != u || n.y != h;
+    }
+    return true;
+  }
 };
 
-__global__ void __launch_bounds__(RD_THREADS, 2) lin_read_kernel(const __grid_constant__ LinReadParams p) {
-  __shared__ __align__(128) uint8_t st[LIN_STATE * 2];
-  const uint32_t base = smem_u32(st);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  int a, b;
-  unit_range(p, static_cast<int>(blockIdx.x), a, b);
-  int held = -1;  // (user, head) of the state in shared memory
-  const int slot = lane & 15;
-  const uint32_t inner = static_cast<uint32_t>(8 * ((slot & 7) >> 1) + 2 * (slot >> 3) + (slot & 1));  // of f = 0, without 32 j
-  int4 w = make_int4(0, 0, 0, 0);
-  ReadRows now;
-  const auto fetch = [&](int i, int4& w, ReadRows& r) {
-    if (!read_unit(p, i, w)) w.w = 0;
+// ------------------------------------------------------------------ loader
+template <bool kBack>
+__device__ void loader(const LinReadParams& p, const CUtensorMap* mx, const CUtensorMap* mq, uint8_t* sm, Aux& x) {
+  constexpr int kStages = kBack ? RING_TILES / 2 : RING_TILES;
+  constexpr uint32_t kStage = (kBack ? 2 : 1) * TILE;
+  const int lane = static_cast<int>(lane_id());
+  Walk k(p);
+  uint32_t g = 0;
+  bool ok = true;
+  for (int i = k.a; i < k.b && ok && k.at(p, i); ++i, ++g) {
+    const uint32_t st = g % kStages;
+    ok = warp_wait(&x.empty[st], ((g / kStages) & 1u) ^ 1u, x, p);
+    if (!ok) break;
+    uint8_t* at = sm + st * kStage;
+    const int rows = k.w.w * p.Lq;
+    if (kBack && (rows & 15)) {  // eight rows more are multiplied: zeros
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int row = 16 * warp + g + 8 * e;
-      r.at[e] = row < w.w * p.Lq ? row_of(p, w, row) : -1;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        r.x[e][j] = r.at[e] >= 0 ? ld_once(reinterpret_cast<const uint4*>(p.x + r.at[e] * LIN_D + 32 * j + 8 * t)) : uint4{};
-    }
-  };
-  if (a < b) fetch(a, w, now);
-#pragma unroll 1
-  for (int i = a; i < b; ++i) {
-    int4 w_next = make_int4(0, 0, 0, 0);
-    ReadRows next;
-    if (i + 1 < b) fetch(i + 1, w_next, next);  // on its way meanwhile
-    if (w.w > 0 && w.x * p.H + w.y != held) {
-      __syncthreads();
-      held = w.x * p.H + w.y;
-      const float* s = p.state + static_cast<int64_t>(held) * LIN_STATE;
-      if (!p.turned) {  // rows of the state are the inner elements; a thread takes two columns
-#pragma unroll 8
-        for (int k = 0; k < LIN_STATE / 2 / RD_THREADS; ++k) {
-          const int e = k * RD_THREADS + tid, row = e >> 6, c = (e & 63) * 2;
-          const float2 v = __ldg(reinterpret_cast<const float2*>(s) + e);
-          const int at = (c & 96) + 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3);
-          *reinterpret_cast<uint32_t*>(st + row * 256 + (((at >> 3) ^ (row & 7)) << 4) + (at & 7) * 2) = pack_bf16x2(v.x, v.y);
-        }
-      } else {  // rows of the state are the columns: two of them, four inner elements
-#pragma unroll 2
-        for (int k = 0; k < LIN_STATE / 8 / RD_THREADS; ++k) {
-          const int e = k * RD_THREADS + tid, c = (e >> 5) * 2, row = (e & 31) * 4;
-          const float4 v = __ldg(reinterpret_cast<const float4*>(s + c * LIN_D + row));
-          const float4 n = __ldg(reinterpret_cast<const float4*>(s + (c + 1) * LIN_D + row));
-          const int at = (c & 96) + 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3);
-          const float lo[4] = {v.x, v.y, v.z, v.w}, hi[4] = {n.x, n.y, n.z, n.w};
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-            *reinterpret_cast<uint32_t*>(st + (row + d) * 256 + (((at >> 3) ^ ((row + d) & 7)) << 4) + (at & 7) * 2) = pack_bf16x2(lo[d], hi[d]);
-        }
+      for (int q = 0; q < 4; ++q) {
+        uint4* z = reinterpret_cast<uint4*>(at + q * HALF_TILE + rows * 128);
+        z[lane] = uint4{};
+        z[lane + 32] = uint4{};
       }
-      __syncthreads();
+      fence_proxy_async_smem();
     }
-    if (16 * warp < w.w * p.Lq) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {  // of the columns
-        float o[8][4] = {};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const uint32_t af[4] = {f ? now.x[0][j].z : now.x[0][j].x, f ? now.x[1][j].z : now.x[1][j].x, f ? now.x[0][j].w : now.x[0][j].y,
-                                    f ? now.x[1][j].w : now.x[1][j].y};
-            const uint32_t row = 32 * j + 4 * f + inner;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              uint32_t bf[4];
-              ldsm4_t(bf, base + row * 256 + (((8 * half + 2 * n + (lane >> 4)) ^ (row & 7)) << 4));
-              mma_16816(o[2 * n], af, bf[0], bf[1]);
-              mma_16816(o[2 * n + 1], af, bf[2], bf[3]);
-            }
-          }
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (now.at[k] < 0) continue;
-            uint32_t v[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = pack_bf16x2(o[4 * m + q][2 * k] * p.scale, o[4 * m + q][2 * k + 1] * p.scale);
-            *reinterpret_cast<uint4*>(p.out + now.at[k] * LIN_D + 64 * half + 32 * m + 8 * t) = make_uint4(v[0], v[1], v[2], v[3]);
-          }
+    __syncwarp();
+    if (lane == 0) mbar_arrive_expect_tx(&x.full[st], static_cast<uint32_t>(rows) * 256u * (kBack ? 2 : 1));
+    __syncwarp();
+    if (lane < k.w.w) {
+      const int cand = __ldg(p.perm + k.w.z + lane);
+      uint8_t* to = at + lane * p.Lq * 128;
+      tma_load_4d(to, mx, &x.full[st], 0, 0, k.h, cand);
+      tma_load_4d(to + HALF_TILE, mx, &x.full[st], 64, 0, k.h, cand);
+      if (kBack) {
+        tma_load_4d(to + TILE, mq, &x.full[st], 0, 0, k.h, cand);
+        tma_load_4d(to + TILE + HALF_TILE, mq, &x.full[st], 64, 0, k.h, cand);
       }
     }
-    w = w_next;
-    now = next;
+    __syncwarp();
+  }
+  if (!ok)  // the copies in flight end before the CTA does
+    for (uint32_t s = g > static_cast<uint32_t>(kStages) ? g - kStages : 0; s < g; ++s) wait_a_second(&x.full[s % kStages], (s / kStages) & 1u);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ issuer
+// x S: A K-major, B the image, its rows the inner dimension; x S^T: its rows the columns.
+__device__ __forceinline__ void issue_read(uint32_t o_tmem, uint32_t x_base, uint32_t image, bool turned) {
+  const uint32_t idesc = turned ? idesc_bf16_f32(128, 128, false, false) : idesc_bf16_f32(128, 128, false, true);
+  const uint64_t xd = sdesc_sw128(x_base, 16, 1024), sd = turned ? sdesc_sw128(image, 16, 1024) : sdesc_sw128(image, HALF_TILE, 1024);
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    const uint32_t a = ((ks >> 2) * HALF_TILE + (ks & 3) * 32) >> 4;
+    mma_bf16_ss(o_tmem, xd + a, sd + (turned ? a : (ks * 2048u) >> 4), idesc, ks > 0 ? 1u : 0u);
   }
 }
 
-// dS, unit by unit: a warp has 16 of the state's rows, all columns, in registers
-// over the units of a (user, head).  A CTA's first and last (user, head) may have
-// units of other CTAs too: those sums go to the CTA's two places of the workspace.
-__global__ void __launch_bounds__(RD_THREADS, 1) lin_read_state_kernel(const __grid_constant__ LinReadParams p) {
-  extern __shared__ __align__(128) uint8_t rd_sm[];
-  const uint32_t base = smem_u32(rd_sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  int a, b;
-  unit_range(p, static_cast<int>(blockIdx.x), a, b);
-  const int n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
-  // users without candidates: zero
-  for (int64_t uh = blockIdx.x; uh < static_cast<int64_t>(p.n_users) * p.H; uh += gridDim.x) {
-    const int u = static_cast<int>(uh / p.H);
-    if (__ldg(p.offsets + u + 1) > __ldg(p.offsets + u)) continue;
-    for (int e = tid; e < LIN_STATE / 4; e += RD_THREADS)
-      reinterpret_cast<float4*>(p.d_state + uh * LIN_STATE)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  const auto load = [&](int i, int stage) {
-    int4 w;
-    if (!read_unit(p, i, w)) w = make_int4(0, 0, 0, 0);
-    const int rows = w.w * p.Lq;
+// Q^T dO: both MN-major.
+__device__ __forceinline__ void issue_state(uint32_t s_tmem, uint32_t q_base, uint32_t o_base, int steps, bool more) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, true, true);
+  const uint64_t qd = sdesc_sw128(q_base, HALF_TILE, 1024), od = sdesc_sw128(o_base, HALF_TILE, 1024);
 #pragma unroll
-    for (int k = 0; k < RD_TILE / 16 / RD_THREADS; ++k) {
-      const int r = k * (RD_THREADS / 16) + (tid >> 4), c = tid & 15;
-      const int64_t at = r < rows ? row_of(p, w, r) * LIN_D + 8 * c : -1;
-      const uint32_t dst = base + stage * 2 * RD_TILE + r * 256 + ((c ^ (r & 7)) << 4);
-      copy16(dst, p.q + max(at, int64_t{0}), at >= 0);
-      copy16(dst + RD_TILE, p.x + max(at, int64_t{0}), at >= 0);
+  for (int ks = 0; ks < 8; ++ks) {
+    if (ks >= steps) break;
+    mma_bf16_ss(s_tmem, qd + ((ks * 2048u) >> 4), od + ((ks * 2048u) >> 4), idesc, more || ks > 0 ? 1u : 0u);
+  }
+}
+
+template <bool kBack>
+__device__ void issuer(const LinReadParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
+  constexpr int kStages = kBack ? RING_TILES / 2 : RING_TILES;
+  constexpr uint32_t kStage = (kBack ? 2 : 1) * TILE;
+  const uint32_t ring = smem_u32(sm), images = smem_u32(sm + IMAGE_AT);
+  const bool out = p.out != nullptr;
+  Walk k(p);
+  uint32_t g = 0;
+  for (int i = k.a; i < k.b && k.at(p, i); ++i, ++g) {
+    const uint32_t st = g % kStages, r = k.runs - 1, rb = r & 1u, rp = (r >> 1) & 1u, ob = g & 1u;
+    if (!warp_wait(&x.full[st], (g / kStages) & 1u, x, p)) return;
+    if (out && k.begins && !warp_wait(&x.image_full[rb], rp, x, p)) return;
+    if (out && !warp_wait(&x.o_empty[ob], ((g >> 1) & 1u) ^ 1u, x, p)) return;
+    if (kBack && k.begins && !warp_wait(&x.ds_empty[rb], rp ^ 1u, x, p)) return;
+    tc_fence_after();
+    if (elect_one()) {
+      const uint32_t at = ring + st * kStage;
+      if (out) {
+        issue_read(tmem + TM_O + 128 * ob, at, images + rb * TILE, p.turned != 0);
+        mma_commit(&x.o_full[ob]);
+        if (k.ends) mma_commit(&x.image_empty[rb]);
+      }
+      if (kBack) {
+        issue_state(tmem + TM_DS + 128 * rb, at + TILE, at, (k.w.w * p.Lq + 15) >> 4, !k.begins);
+        if (k.ends) mma_commit(&x.ds_full[rb]);
+      }
+      mma_commit(&x.empty[st]);
     }
-  };
-  if (a < b) load(a, 0);
-  copies_commit();
-  float s[16][4] = {};
-#pragma unroll 1
-  for (int i = a; i < b; ++i) {
-    if (i + 1 < b) load(i + 1, (i + 1 - a) & 1);
-    copies_commit();
-    copies_wait<1>();
-    __syncthreads();
-    const uint32_t q_at = base + ((i - a) & 1) * 2 * RD_TILE, o_at = q_at + RD_TILE;
-    int4 w;
-    if (!read_unit(p, i, w)) {
-      __syncthreads();
-      continue;
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------ images
+template <bool kBack>
+__device__ void image_warps(const LinReadParams& p, uint8_t* sm, Aux& x) {
+  const int tid = static_cast<int>(threadIdx.x) - 32 * IMAGE_WARP0, warp = tid >> 5, lane = tid & 31;
+  if (kBack) {  // users without candidates
+    for (int64_t uh = blockIdx.x; uh < static_cast<int64_t>(p.n_users) * p.H; uh += gridDim.x) {
+      const int u = static_cast<int>(uh / p.H);
+      if (__ldg(p.offsets + u + 1) > __ldg(p.offsets + u)) continue;
+#pragma unroll 4
+      for (int e = tid; e < LIN_STATE / 4; e += 32 * GROUP_WARPS) reinterpret_cast<float4*>(p.d_state + uh * LIN_STATE)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const int steps = (w.w * p.Lq + 15) >> 4;
+  }
+  if (!p.out) return;
+  Walk k(p);
+  for (int i = k.a; i < k.b && k.at(p, i); ++i) {
+    if (!k.begins) continue;
+    const uint32_t r = k.runs - 1, rb = r & 1u;
+    const float4* s = reinterpret_cast<const float4*>(p.state + (static_cast<int64_t>(k.u) * p.H + k.h) * LIN_STATE) + lane;
+    if (!warp_wait(&x.image_empty[rb], ((r >> 1) & 1u) ^ 1u, x, p)) return;
+    // row by row: four elements a lane
+    uint8_t* to = sm + IMAGE_AT + rb * TILE + (lane >> 4) * HALF_TILE + (lane & 1) * 8;
 #pragma unroll 1
-    for (int kb = 0; kb < steps; ++kb) {
-      uint32_t af[4];
-      int r = 16 * kb + (lane & 7) + 8 * (lane >> 4);
-      ldsm4_t(af, q_at + r * 256 + (((2 * warp + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
-      r = 16 * kb + (lane & 15);
+    for (int q = 0; q < 16; q += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = __ldg(s + (8 * (q + c) + warp) * 32);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        uint32_t bf[4];
-        ldsm4_t(bf, o_at + r * 256 + (((2 * c + (lane >> 4)) ^ (r & 7)) << 4));
-        mma_16816(s[2 * c], af, bf[0], bf[1]);
-        mma_16816(s[2 * c + 1], af, bf[2], bf[3]);
+        const int row = 8 * (q + c) + warp;
+        *reinterpret_cast<uint2*>(to + row * 128 + ((((lane & 15) >> 1) ^ (row & 7)) << 4)) = make_uint2(pack_bf16x2(v[c].x, v[c].y), pack_bf16x2(v[c].z, v[c].w));
       }
     }
-    __syncthreads();
-    // the (user, head) ends here, or the CTA's units do
-    const int4 next = i + 1 < n ? __ldg(reinterpret_cast<const int4*>(p.work) + i + 1) : make_int4(-1, -1, 0, 0);
-    const bool ends = next.x != w.x || next.y != w.y;
-    if (!ends && i + 1 < b) continue;
-    bool begun = true;  // within this CTA
-    if (a > 0) {
-      const int4 before = __ldg(reinterpret_cast<const int4*>(p.work) + a - 1);
-      begun = before.x != w.x || before.y != w.y;
-    }
-    const bool whole = begun && ends;
-    float* to = whole ? p.d_state + (static_cast<int64_t>(w.x) * p.H + w.y) * LIN_STATE
-                      : p.part + (2 * static_cast<int64_t>(blockIdx.x) + (begun ? 1 : 0)) * LIN_STATE;
-    const float f = whole ? p.scale : 1.f;
+    fence_proxy_async_smem();
+    warp_arrive(&x.image_full[rb]);
+  }
+}
+
+// ----------------------------------------------------------------- outputs
+template <bool kBack>
+__device__ void output_warps(const LinReadParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
+  const int quarter = warp & 3, half = (warp - OUT_WARP0) >> 2, row = quarter * 32 + lane;
+  const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+  uint8_t* stage = sm + OUT_AT + (warp - OUT_WARP0) * OUT_BYTES;
+  const int piece = lane & 7;
+  Walk k(p);
+  uint32_t g = 0;
+  for (int i = k.a; i < k.b && k.at(p, i); ++i, ++g) {
+    const uint32_t r = k.runs - 1, rb = r & 1u, rp = (r >> 1) & 1u, ob = g & 1u;
+    if (p.out) {
+      const int slot = row / p.Lq;
+      const int64_t mine = row < k.w.w * p.Lq
+          ? ((static_cast<int64_t>(__ldg(p.perm + k.w.z + slot)) * p.H + k.h) * p.Lq + (row - slot * p.Lq)) * LIN_D : -1;
+      if (!warp_wait(&x.o_full[ob], (g >> 1) & 1u, x, p)) return;
+      tc_fence_after();
+      const uint32_t Ot = tmem + lane_base + TM_O + 128 * ob + 64 * half;
+      const bool any = quarter * 32 < k.w.w * p.Lq;
+#pragma unroll 1
+      for (int b = 0; b < 2 && any; ++b) {
+        uint32_t v[32];
+        tmem_ld32(Ot + 32 * b, v);
+        tmem_ld_wait(v);
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        *reinterpret_cast<float2*>(to + (16 * warp + g + 8 * k) * LIN_D + 8 * c + 2 * t) = make_float2(s[c][2 * k] * f, s[c][2 * k + 1] * f);
-        s[c][2 * k] = s[c][2 * k + 1] = 0.f;
+          for (int e = 0; e < 4; ++e) {
+            float f0, f1;
+            mul2(f0, f1, __uint_as_float(v[8 * c + 2 * e]), __uint_as_float(v[8 * c + 2 * e + 1]), p.scale, p.scale);
+            o[e] = pack_bf16x2(f0, f1);
+          }
+          *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * b + c) ^ piece) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
+      tc_fence_before();
+      warp_arrive(&x.o_empty[ob]);
+      // whole lines: eight lanes to a row's half
+      if (any) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int rr = 4 * q + (lane >> 3);
+          const int64_t at = __shfl_sync(0xffffffffu, mine, rr);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
+          if (at >= 0) *reinterpret_cast<uint4*>(p.out + at + 64 * half + 8 * piece) = v;
+        }
+        __syncwarp();
+      }
+    }
+    if (kBack && k.ends) {  // the run's gradient: whole, or a part
+      const auto same = [&](int j) {
+        const int4 n = Walk::unit(p, j);
+        return n.x == k.u && n.y == k.h;
+      };
+      const int64_t n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
+      const bool begun = r > 0 || k.a == 0 || !same(k.a - 1), whole = begun && (i + 1 < k.b || i + 1 >= n || !same(i + 1));
+      float* to = whole ? p.d_state + (static_cast<int64_t>(k.u) * p.H + k.h) * LIN_STATE
+                        : p.part + (2 * static_cast<int64_t>(blockIdx.x) + (begun ? 1 : 0)) * LIN_STATE;
+      const float f = whole ? p.scale : 1.f;
+      if (!warp_wait(&x.ds_full[rb], rp, x, p)) return;
+      tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {
+        uint32_t v[32];
+        tmem_ld32(tmem + lane_base + TM_DS + 128 * rb + 64 * half + 32 * b, v);
+        tmem_ld_wait(v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<float4*>(stage + lane * 128 + ((c ^ piece) << 4)) =
+              make_float4(__uint_as_float(v[4 * c]) * f, __uint_as_float(v[4 * c + 1]) * f, __uint_as_float(v[4 * c + 2]) * f, __uint_as_float(v[4 * c + 3]) * f);
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int rr = 4 * q + (lane >> 3);
+          *reinterpret_cast<float4*>(to + (quarter * 32 + rr) * LIN_D + 64 * half + 32 * b + 4 * piece) =
+              *reinterpret_cast<const float4*>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      warp_arrive(&x.ds_empty[rb]);
+    }
+  }
+}
+
+template <bool kBack>
+__global__ void __launch_bounds__(RT_THREADS, 1)
+    lin_read_kernel(const __grid_constant__ LinReadParams p, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mq) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  Aux& x = *reinterpret_cast<Aux*>(sm + AUX_AT);
+  const int warp = static_cast<int>(threadIdx.x >> 5);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < RING_TILES; ++i) {
+      mbar_init(&x.full[i], 1);
+      mbar_init(&x.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&x.o_full[i], 1);
+      mbar_init(&x.image_empty[i], 1);
+      mbar_init(&x.ds_full[i], 1);
+      mbar_init(&x.o_empty[i], GROUP_WARPS);
+      mbar_init(&x.image_full[i], GROUP_WARPS);
+      mbar_init(&x.ds_empty[i], GROUP_WARPS);
+    }
+    mbar_init(&x.drain, 1);
+    x.abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 3) {
+    tmem_alloc(&x.tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = x.tmem_slot;
+  if (warp < OUT_WARP0) {
+    if (warp == 0) loader<kBack>(p, &mx, &mq, sm, x);
+    if (warp == 1) {
+      issuer<kBack>(p, sm, x, tmem);
+      drain(&x.drain);
+    }
+  } else if (warp < IMAGE_WARP0) {
+    output_warps<kBack>(p, sm, x, tmem);
+  } else {
+    image_warps<kBack>(p, sm, x);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (x.abort && threadIdx.x == 0) atomicOr(p.status, DEV_ERR_PIPE_TIMEOUT);
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
 // Adds the parts of each (user, head) whose units several CTAs had, in order:
 // block c those of the one that begins in CTA c and goes on in the next.
-__global__ void __launch_bounds__(RD_THREADS) lin_read_join_kernel(const __grid_constant__ LinReadParams p) {
+__global__ void __launch_bounds__(JOIN_THREADS) lin_read_join_kernel(const __grid_constant__ LinReadParams p) {
   const int c = static_cast<int>(blockIdx.x);
   const int n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
   const int4* work = reinterpret_cast<const int4*>(p.work);
@@ -242,26 +369,30 @@ __global__ void __launch_bounds__(RD_THREADS) lin_read_join_kernel(const __grid_
     const int4 x = __ldg(work + i), y = __ldg(work + j);
     return x.x == y.x && x.y == y.y;
   };
+  const auto unit_range = [&](int cta, int& a, int& b) {
+    a = static_cast<int>(static_cast<int64_t>(cta) * n / gridDim.x);
+    b = static_cast<int>(static_cast<int64_t>(cta + 1) * n / gridDim.x);
+  };
   int a, b;
-  unit_range(p, c, a, b);
+  unit_range(c, a, b);
   if (a >= b || b >= n || !same(b - 1, b)) return;  // nothing, or its last one ends here
   if (a > 0 && same(a - 1, a) && same(a, b - 1)) return;  // begins in a CTA before
   const int4 w = __ldg(work + b - 1);
   int last = c;  // the CTA where it ends
   for (int end = b; end < n && same(b - 1, end);) {
     int x, y;
-    unit_range(p, ++last, x, y);
+    unit_range(++last, x, y);
     end = y;
     if (y > x && !same(b - 1, y - 1)) break;
   }
   float* to = p.d_state + (static_cast<int64_t>(w.x) * p.H + w.y) * LIN_STATE;
   const int per = LIN_STATE / 4 / gridDim.y, e0 = static_cast<int>(blockIdx.y) * per;
-  for (int e = e0 + threadIdx.x; e < e0 + per; e += RD_THREADS) {
+  for (int e = e0 + threadIdx.x; e < e0 + per; e += JOIN_THREADS) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = c; k <= last; ++k) {
       int x, y;
-      unit_range(p, k, x, y);
+      unit_range(k, x, y);
       if (x >= y) continue;  // a CTA without units has left nothing
       const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + (2 * static_cast<int64_t>(k) + (k == c ? 1 : 0)) * LIN_STATE) + e);
       s.x += v.x;
@@ -273,26 +404,36 @@ __global__ void __launch_bounds__(RD_THREADS) lin_read_join_kernel(const __grid_
   }
 }
 
-}  // namespace
-
-int lin_read_ctas(int num_sms) { return num_sms; }
-
-cudaError_t launch_lin_read(const LinReadParams& p, int num_sms, cudaStream_t s) {
-  const int64_t ctas = p.max_units < 2 * static_cast<int64_t>(num_sms) ? p.max_units : 2 * static_cast<int64_t>(num_sms);
-  lin_read_kernel<<<static_cast<unsigned>(ctas), RD_THREADS, 0, s>>>(p);
+template <bool kBack>
+cudaError_t launch(const LinReadParams& p, const CUtensorMap& mx, const CUtensorMap& mq, int num_sms, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(lin_read_kernel<kBack>, cudaFuncAttributeMaxDynamicSharedMemorySize, RT_SMEM);
+  if (e != cudaSuccess) return e;
+  lin_read_kernel<kBack><<<static_cast<unsigned>(lin_read_ctas(num_sms)), RT_THREADS, RT_SMEM, s>>>(p, mx, mq);
   return cudaGetLastError();
 }
 
-cudaError_t launch_lin_read_state(const LinReadParams& p, int num_sms, cudaStream_t s) {
-  constexpr int smem = 4 * RD_TILE;
-  cudaError_t e = cudaFuncSetAttribute(lin_read_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const unsigned ctas = static_cast<unsigned>(lin_read_ctas(num_sms));
-  lin_read_state_kernel<<<ctas, RD_THREADS, smem, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  lin_read_join_kernel<<<dim3(ctas, 8), RD_THREADS, 0, s>>>(p);
+}  // namespace
+
+bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box);
+
+size_t lin_read_smem() { return RT_SMEM; }
+int lin_read_ctas(int num_sms) { return num_sms; }
+
+cudaError_t launch_lin_read_join(const LinReadParams& p, int num_sms, cudaStream_t s) {
+  lin_read_join_kernel<<<dim3(static_cast<unsigned>(lin_read_ctas(num_sms)), 8), JOIN_THREADS, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+cudaError_t launch_lin_read(const LinReadParams& p, int num_sms, cudaStream_t s) {
+  CUtensorMap mx, mq;
+  const uint64_t H = static_cast<uint64_t>(p.H), Lq = static_cast<uint64_t>(p.Lq);
+  const uint64_t dims[4] = {LIN_D, Lq, H, static_cast<uint64_t>(p.n_cand)};
+  const uint64_t strides[3] = {LIN_D * 2, Lq * LIN_D * 2, H * Lq * LIN_D * 2};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(p.Lq), 1, 1};
+  if (!encode_bf16(&mx, p.x, 4, dims, strides, box)) return cudaErrorInvalidValue;
+  mq = mx;
+  if (p.d_state && !encode_bf16(&mq, p.q, 4, dims, strides, box)) return cudaErrorInvalidValue;
+  return p.d_state ? launch<true>(p, mx, mq, num_sms, s) : launch<false>(p, mx, mq, num_sms, s);
 }
 
 }  // namespace ikbo

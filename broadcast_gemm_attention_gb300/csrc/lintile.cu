@@ -27,9 +27,9 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include "attn_common.cuh"
 #include "linattn_internal.h"
 #include "mma_common.cuh"
+#include "tile_common.cuh"
 
 namespace ikbo {
 namespace {
@@ -150,71 +150,12 @@ __device__ __forceinline__ void get_item(const LinParams& p, int i, int per_job,
   x.chunks = (x.n + LT_CHUNK - 1) / LT_CHUNK;
 }
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Aux& x, const LinParams& p) {
-  const bool ok = mbar_wait(bar, parity, &x.abort, p.timeout_ns, 1);
-  return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
-  __syncwarp();
-  if (lane_id() == 0) mbar_arrive(bar);
-}
-
 // A group's warps meet.  (Not a hardware barrier: a warp that gave up does not come.)
 __device__ __forceinline__ bool group_sync(uint64_t* bar, uint32_t& phase, Aux& x, const LinParams& p) {
   warp_arrive(bar);
   return warp_wait(bar, phase++ & 1u, x, p);
 }
 
-// Ends when `bar` completes its phase, or a second is over.
-__device__ __forceinline__ void wait_a_second(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 1000000000ull) {}
-}
-
-// 32 lanes x 16 columns from, or 8 columns to, tensor memory.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
-        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-// Waits for loads, and keeps uses of r behind that.
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
-                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-// (r0, r1) = (a0, a1) * (b0, b1)
-__device__ __forceinline__ void mul2(float& r0, float& r1, float a0, float a1, float b0, float b1) {
-  asm("{.reg .b64 x, y, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 w, x, y;\n\t"
-      "mov.b64 {%0, %1}, w;}"
-      : "=f"(r0), "=f"(r1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
-// (r0, r1) = (a0, a1) * b + (c0, c1)
-__device__ __forceinline__ void fma2v(float& r0, float& r1, float a0, float a1, float b, float c0, float c1) {
-  asm("{.reg .b64 x, y, z, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 y, {%4, %4};\n\t"
-      "mov.b64 z, {%5, %6};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\t"
-      "mov.b64 {%0, %1}, w;}"
-      : "=f"(r0), "=f"(r1)
-      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
-}
 // bf16 pairs: a b, and a b + c, in one rounding each.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -393,15 +334,6 @@ __device__ void state_issuer(const LinParams& p, uint8_t* sm, Aux& x, uint32_t t
       warp_arrive(&x.m_begun);
     }
   }
-}
-
-// An issuer leaves when its products in flight have ended, or a second is over.
-__device__ void drain(uint64_t* bar) {
-  __syncwarp();
-  if (elect_one()) mma_commit(bar);
-  __syncwarp();
-  wait_a_second(bar, 0);
-  __syncwarp();
 }
 
 __device__ __forceinline__ float decay_power(float log2_decay, int n) {
