@@ -636,76 +636,69 @@ def ikbo_attn_qcache_tree_forward(plan: int, Q: torch.Tensor, data: torch.Tensor
     if len(shape) != 4 or O.shape != shape or shape[1] % H_kv != 0 or (lse is not None and lse.shape != shape[:3]):
         raise ValueError("inconsistent attention shapes")
     n, _, Lq, d = shape
-    if tuple(K_new.shape) != (n, Lq, H_kv, d) or V_new.shape != K_new.shape:
+    if K_new.shape != (n, Lq, H_kv, d) or V_new.shape != K_new.shape:
         raise ValueError("K_new and V_new must be [n_cand, Lq, H_kv, d]")
     stride = H_kv * d
-    for t, name in ((K_new, "K_new"), (V_new, "V_new")):
-        if t.get_device() != dev or t.dtype is not bf:
-            raise ValueError(f"{name} must be a tensor of bfloat16 on the current CUDA device")
+    if K_new.get_device() != dev or V_new.get_device() != dev or K_new.dtype is not bf or V_new.dtype is not bf:
+        raise ValueError("K_new and V_new must be tensors of bfloat16 on the current CUDA device")
     if not (K_new.is_contiguous() and V_new.is_contiguous()):
         stride = K_new.stride(1) if Lq > 1 else K_new.stride(0)
         for t in (K_new, V_new):
             if t.stride(3) != 1 or (H_kv > 1 and t.stride(2) != d) or (Lq > 1 and t.stride(1) != stride) or \
                     (n > 1 and t.stride(0) != Lq * stride):
                 raise ValueError("K_new and V_new must have contiguous heads and one row stride, both alike")
-    if parents is not None and tuple(parents.shape) != (n, Lq):
+    if parents is not None and parents.shape != (n, Lq):
         raise ValueError("parents must be [n_cand, Lq]")
     if Lkv is None:
         Lkv = n_users * max_blocks * page
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    _check(load().ikbo_attn_qcache_tree_forward(plan, _here(Q, bf, "Q", dev), dptr, n_pages, page, H_kv, tptr, max_blocks, lptr,
-                                                K_new.data_ptr(), V_new.data_ptr(), stride,
-                                                None if parents is None else _here(parents, torch.int32, "parents", dev),
-                                                _here(O, bf, "O", dev),
-                                                None if lse is None else _here(lse, torch.float32, "lse", dev),
-                                                min(max(1, int(Lkv)), 2**31 - 1), d, scale, _raw_stream(stream, dev)),
-           "ikbo_attn_qcache_tree_forward")
+    rc = load().ikbo_attn_qcache_tree_forward(plan, _here(Q, bf, "Q", dev), dptr, n_pages, page, H_kv, tptr, max_blocks, lptr,
+                                              K_new.data_ptr(), V_new.data_ptr(), stride,
+                                              None if parents is None else _here(parents, torch.int32, "parents", dev),
+                                              _here(O, bf, "O", dev),
+                                              None if lse is None else _here(lse, torch.float32, "lse", dev),
+                                              min(max(1, int(Lkv)), 2**31 - 1), d, scale, _raw_stream(stream, dev))
+    if rc != IKBO_OK:
+        raise IkboError(rc, "ikbo_attn_qcache_tree_forward")
 
 
-def _lin_rows(tensors, names, dev: int, shape):
-    """Pointers and row strides of [rows, H, d] tensors whose rows may be strided (None: NULL)."""
-    ptrs, strides = [], []
+def _lin_stride(t: torch.Tensor, name: str, dev: int, shape) -> int:
+    """The row stride of t, which must be [rows, H, d] with contiguous heads."""
     H, d = shape[1], shape[2]
-    for t, name in zip(tensors, names):
-        if t is None:
-            ptrs.append(None)
-            strides.append(H * d)
-            continue
-        if t.get_device() != dev or t.dtype is not torch.bfloat16:
-            raise ValueError(f"{name} must be a tensor of bfloat16 on the current CUDA device")
-        if t.shape != shape:
-            raise ValueError(f"{name} must be [rows, H, d], alike for all")
-        if t.is_contiguous():
-            strides.append(H * d)
-        else:
-            if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
-                raise ValueError(f"the heads of a row of {name} must be contiguous")
-            strides.append(t.stride(0) if shape[0] > 1 else H * d)
-        ptrs.append(t.data_ptr())
-    return ptrs, (ctypes.c_int64 * len(strides))(*strides)
+    if t.get_device() != dev or t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be a tensor of bfloat16 on the current CUDA device")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [rows, H, d], alike for all")
+    if t.is_contiguous():
+        return H * d
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return t.stride(0) if shape[0] > 1 else H * d
 
 
-def _lin_states(states, names, decay: torch.Tensor, offsets: Optional[torch.Tensor], n_users: Optional[int], dev: int, H: int,
-                d: int):
-    """The number of users, and pointers of the states given, the decay and the offsets."""
-    f32 = torch.float32
+_I64X4, _I64X7 = ctypes.c_int64 * 4, ctypes.c_int64 * 7
+
+
+def _lin_users(offsets: Optional[torch.Tensor], n_users: Optional[int], states) -> int:
     if offsets is not None:
         if offsets.dim() != 1 or offsets.numel() < 2 or (n_users is not None and offsets.numel() != n_users + 1):
             raise ValueError("offsets must be [n_users + 1]")
-        n_users = offsets.numel() - 1
-    for t, name in zip(states, names):
-        if t is not None:
-            if n_users is None:
-                n_users = t.shape[0]
-            if tuple(t.shape) != (n_users, H, d, d):
-                raise ValueError(f"{name} must be [n_users, H, d, d]")
+        return offsets.numel() - 1
     if n_users is None:
+        for t in states:
+            if t is not None:
+                return t.shape[0]
         raise ValueError("the number of users must follow from offsets, a state or n_users")
-    if tuple(decay.shape) != (H,):
-        raise ValueError("decay must be [H]")
-    ptrs = [None if t is None else _here(t, f32, name, dev) for t, name in zip(states, names)]
-    return n_users, ptrs, _here(decay, f32, "decay", dev), None if offsets is None else _here(offsets, torch.int32, "offsets", dev)
+    return n_users
+
+
+def _lin_state(t: Optional[torch.Tensor], name: str, dev: int, shape):
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [n_users, H, d, d]")
+    return _here(t, torch.float32, name, dev)
 
 
 def ikbo_linattn_forward(plan: int, Q: Optional[torch.Tensor], K: torch.Tensor, V: torch.Tensor, decay: torch.Tensor,
@@ -717,17 +710,30 @@ def ikbo_linattn_forward(plan: int, Q: Optional[torch.Tensor], K: torch.Tensor, 
     from state_in to state_out [n_users, H, 128, 128] (fp32; either may be None, or the same).
     offsets [n_users + 1]: the users' rows; None: equally many each.  Q and O None: the states alone.
     max_len: a bound on a user's rows (0: all)."""
-    dev = _current_device(K, "K")
-    shape = K.shape
+    dev, shape = _current_device(K, "K"), K.shape
     if len(shape) != 3:
         raise ValueError("K must be [rows, H, d]")
-    (q, k, v, o), strides = _lin_rows((Q, K, V, O), ("Q", "K", "V", "O"), dev, shape)
-    n_users, (si, so), dptr, optr = _lin_states((state_in, state_out), ("state_in", "state_out"), decay, offsets, n_users, dev,
-                                                shape[1], shape[2])
+    rows, H, d = shape
+    ks, vs = _lin_stride(K, "K", dev, shape), _lin_stride(V, "V", dev, shape)
+    qs = os_ = H * d
+    q = o = None
+    if Q is not None:
+        qs, q = _lin_stride(Q, "Q", dev, shape), Q.data_ptr()
+    if O is not None:
+        os_, o = _lin_stride(O, "O", dev, shape), O.data_ptr()
+    strides = None if ks == vs == qs == os_ == H * d else _I64X4(qs, ks, vs, os_)
+    users = _lin_users(offsets, n_users, (state_in, state_out))
+    square = (users, H, d, d)
+    if decay.shape != (H,):
+        raise ValueError("decay must be [H]")
     if scale is None:
-        scale = 1.0 / math.sqrt(shape[2])
-    _check(load().ikbo_linattn_forward(plan, q, k, v, strides, optr, n_users, shape[0], int(max_len), shape[1], shape[2], dptr, si,
-                                       so, o, scale, _raw_stream(stream, dev)), "ikbo_linattn_forward")
+        scale = 1.0 / math.sqrt(d)
+    rc = load().ikbo_linattn_forward(plan, q, K.data_ptr(), V.data_ptr(), strides,
+                                     None if offsets is None else _here(offsets, torch.int32, "offsets", dev), users, rows, max_len, H,
+                                     d, _here(decay, torch.float32, "decay", dev), _lin_state(state_in, "state_in", dev, square),
+                                     _lin_state(state_out, "state_out", dev, square), o, scale, _raw_stream(stream, dev))
+    if rc != IKBO_OK:
+        raise IkboError(rc, "ikbo_linattn_forward")
 
 
 def ikbo_linattn_backward(plan: int, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, dO: torch.Tensor, decay: torch.Tensor,
@@ -738,18 +744,27 @@ def ikbo_linattn_backward(plan: int, Q: torch.Tensor, K: torch.Tensor, V: torch.
                           scale: Optional[float] = None, stream=None) -> None:
     """Gradients of ikbo_linattn_forward for upstream dO and d_state_out (None: zero): any of
     dQ, dK, dV (bf16, like Q) and d_state_in (fp32); overwritten."""
-    dev = _current_device(K, "K")
-    shape = K.shape
+    dev, shape = _current_device(K, "K"), K.shape
     if len(shape) != 3:
         raise ValueError("K must be [rows, H, d]")
-    ptrs, strides = _lin_rows((Q, K, V, dO, dQ, dK, dV), ("Q", "K", "V", "dO", "dQ", "dK", "dV"), dev, shape)
-    n_users, (si, dso, dsi), dptr, optr = _lin_states((state_in, d_state_out, d_state_in),
-                                                      ("state_in", "d_state_out", "d_state_in"), decay, offsets, n_users, dev,
-                                                      shape[1], shape[2])
+    rows, H, d = shape
+    ptrs, strides = [], []
+    for t, name in ((Q, "Q"), (K, "K"), (V, "V"), (dO, "dO"), (dQ, "dQ"), (dK, "dK"), (dV, "dV")):
+        strides.append(H * d if t is None else _lin_stride(t, name, dev, shape))
+        ptrs.append(None if t is None else t.data_ptr())
+    users = _lin_users(offsets, n_users, (state_in, d_state_out, d_state_in))
+    square = (users, H, d, d)
+    if decay.shape != (H,):
+        raise ValueError("decay must be [H]")
     if scale is None:
-        scale = 1.0 / math.sqrt(shape[2])
-    _check(load().ikbo_linattn_backward(plan, *ptrs[:4], strides, optr, n_users, shape[0], int(max_len), shape[1], shape[2], dptr,
-                                        si, dso, *ptrs[4:], dsi, scale, _raw_stream(stream, dev)), "ikbo_linattn_backward")
+        scale = 1.0 / math.sqrt(d)
+    rc = load().ikbo_linattn_backward(plan, *ptrs[:4], _I64X7(*strides),
+                                      None if offsets is None else _here(offsets, torch.int32, "offsets", dev), users, rows, max_len, H,
+                                      d, _here(decay, torch.float32, "decay", dev), _lin_state(state_in, "state_in", dev, square),
+                                      _lin_state(d_state_out, "d_state_out", dev, square), *ptrs[4:],
+                                      _lin_state(d_state_in, "d_state_in", dev, square), scale, _raw_stream(stream, dev))
+    if rc != IKBO_OK:
+        raise IkboError(rc, "ikbo_linattn_backward")
 
 
 def ikbo_linattn_read_forward(plan: int, Q: torch.Tensor, state: torch.Tensor, O: torch.Tensor,

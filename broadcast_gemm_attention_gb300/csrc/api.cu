@@ -142,6 +142,7 @@ void free_plan(ikbo_plan_t p) {
   cudaFree(p->qa_lse.ptr);
   cudaFree(p->lin_states.ptr);
   cudaFree(p->lin_part.ptr);
+  cudaFree(p->lin_tickets.ptr);
   for (int i = 0; i < p->n_retired; ++i) cudaFree(p->retired[i]);
   std::free(p->retired);
   delete p;

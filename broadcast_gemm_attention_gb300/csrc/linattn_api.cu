@@ -12,7 +12,6 @@ namespace ikbo {
 cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int* launches);
 size_t lin_tile_smem();
 cudaError_t launch_lin_read(const LinReadParams& p, int num_sms, cudaStream_t s);
-cudaError_t launch_lin_read_join(const LinReadParams& p, int num_sms, cudaStream_t s);
 size_t lin_read_smem();
 int lin_read_ctas(int num_sms);
 }  // namespace ikbo
@@ -245,18 +244,17 @@ ikbo_status_t ikbo_linattn_read_backward(ikbo_plan_t p, const void* Q, const flo
     bool capturing = false;
     if (stream && is_capturing(stream, &capturing) != cudaSuccess) return IKBO_ERR_CUDA;
     const size_t need = 2 * static_cast<size_t>(lin_read_ctas(p->num_sms)) * LIN_STATE;
-    if (grow_kept<false>(p, &p->lin_part, need, ANY, capturing, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+    if (grow_kept<false>(p, &p->lin_part, need, ANY, capturing, stream) != cudaSuccess ||
+        grow_kept<true>(p, &p->lin_tickets, static_cast<size_t>(lin_read_ctas(p->num_sms)), ANY, capturing, stream) != cudaSuccess)
+      return IKBO_ERR_CUDA;
     rp.part = p->lin_part.ptr;
+    rp.tickets = p->lin_tickets.ptr;
     rp.d_state = d_state;
   }
   rp.out = static_cast<uint16_t*>(dQ);
   rp.turned = 1;
   if (launch_lin_read(rp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
   p->launches++;
-  if (d_state) {
-    if (launch_lin_read_join(rp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
-    p->launches++;
-  }
   return IKBO_OK;
 }
 

@@ -50,6 +50,7 @@ struct LinReadParams {
   const uint16_t* q;        // backward: the queries (x is dO), for d_state
   float* d_state;
   float* part;              // two states a CTA: of the first and the last run of units that it shares
+  uint32_t* tickets;        // a count a CTA, zero between calls: parts of the run that begins there
   const int32_t* offsets;   // the plan's segments
   const int32_t* perm;
   const int32_t* work;      // units {u, h, first place, run}

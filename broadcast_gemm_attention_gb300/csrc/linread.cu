@@ -19,8 +19,8 @@
 //   warp 0       loads; warp 1 issues
 //   warps 4-11   outputs, and at a run's end the state's gradient
 //   warps 12-19  images of the states, one run ahead; zeros for users without candidates
-// Runs cut by a CTA's share leave their gradients as parts, which
-// lin_read_join_kernel adds in order.
+// Runs cut by a CTA's share leave their gradients as parts, which the last CTA to end
+// adds in order (so results repeat bit for bit).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -32,7 +32,7 @@ namespace ikbo {
 int lin_read_ctas(int num_sms);
 namespace {
 
-constexpr int RT_THREADS = 640, JOIN_THREADS = 256;
+constexpr int RT_THREADS = 640;
 constexpr int OUT_WARP0 = 4, IMAGE_WARP0 = 12, GROUP_WARPS = 8;
 constexpr uint32_t TILE = 2 * HALF_TILE;  // 32 KB
 constexpr int RING_TILES = 4;             // a stage is a tile (forward) or two
@@ -44,41 +44,44 @@ constexpr uint32_t TM_O = 0, TM_DS = 256;
 struct Aux {
   uint64_t full[RING_TILES], empty[RING_TILES];
   uint64_t o_full[2], o_empty[2], image_full[2], image_empty[2], ds_full[2], ds_empty[2], drain;
-  uint32_t tmem_slot, abort;
+  uint32_t tmem_slot, abort, last;
 };
 constexpr uint32_t RT_SMEM = AUX_AT + sizeof(Aux) + 1024;
 static_assert(RT_SMEM <= 227 * 1024, "tiles do not fit in shared memory");
 
 // This CTA's units a .. b - 1, and a walk over them with the runs of one (user, head).
+// The unit after the current one is at hand already.
 struct Walk {
   int a, b;
   uint32_t runs;   // begun so far
   int u, h;        // of the run
   bool begins, ends;
-  int4 w;
+  int4 w, next;
   __device__ __forceinline__ Walk(const LinReadParams& p) : runs(0), u(-1), h(-1) {
     const int64_t n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
     a = static_cast<int>(blockIdx.x * n / gridDim.x);
     b = static_cast<int>((blockIdx.x + 1) * n / gridDim.x);
+    next = a < b ? unit(p, a) : make_int4(-1, -1, 0, 0);
   }
   __device__ __forceinline__ static int4 unit(const LinReadParams& p, int i) { return __ldg(reinterpret_cast<const int4*>(p.work) + i); }
-  // Unit i; false (to every role alike) where the list is not sound, which ends the share.
+  // To unit i; false (to every role alike) where the list is not sound, which ends the share.
   __device__ __forceinline__ bool at(const LinReadParams& p, int i) {
-    w = unit(p, i);
+    w = next;
     if (w.x < 0 || w.x >= p.n_users || w.y < 0 || w.y >= p.H || w.z < 0 || w.w <= 0 || w.z + w.w > p.n_cand || w.w * p.Lq > 128) {
       if (threadIdx.x == 0) atomicOr(p.status, DEV_ERR_BAD_WORK);
       return false;
     }
+    next = i + 1 < b ? unit(p, i + 1) : make_int4(-1, -1, 0, 0);
     begins = w.x != u || w.y != h;
     runs += begins;
     u = w.x;
     h = w.y;
-    ends = true;
-    if (i + 1 < b) {
-      const int4 n = unit(p, i + 1);
-      ends = n.x != u || n.y != h;
-    }
+    ends = next.x != u || next.y != h;
     return true;
+  }
+  // The candidate of place k of unit w (0 for none).
+  __device__ __forceinline__ static int cand(const LinReadParams& p, const int4& w, int k) {
+    return k < w.w && w.z >= 0 && w.z + k < p.n_cand ? __ldg(p.perm + w.z + k) : 0;
   }
 };
 
@@ -91,8 +94,11 @@ __device__ void loader(const LinReadParams& p, const CUtensorMap* mx, const CUte
   Walk k(p);
   uint32_t g = 0;
   bool ok = true;
+  int cand_next = Walk::cand(p, k.next, lane);
   for (int i = k.a; i < k.b && ok && k.at(p, i); ++i, ++g) {
     const uint32_t st = g % kStages;
+    const int cand = cand_next;
+    cand_next = Walk::cand(p, k.next, lane);
     ok = warp_wait(&x.empty[st], ((g / kStages) & 1u) ^ 1u, x, p);
     if (!ok) break;
     uint8_t* at = sm + st * kStage;
@@ -110,7 +116,6 @@ __device__ void loader(const LinReadParams& p, const CUtensorMap* mx, const CUte
     if (lane == 0) mbar_arrive_expect_tx(&x.full[st], static_cast<uint32_t>(rows) * 256u * (kBack ? 2 : 1));
     __syncwarp();
     if (lane < k.w.w) {
-      const int cand = __ldg(p.perm + k.w.z + lane);
       uint8_t* to = at + lane * p.Lq * 128;
       tma_load_4d(to, mx, &x.full[st], 0, 0, k.h, cand);
       tma_load_4d(to + HALF_TILE, mx, &x.full[st], 64, 0, k.h, cand);
@@ -199,19 +204,16 @@ __device__ void image_warps(const LinReadParams& p, uint8_t* sm, Aux& x) {
     if (!k.begins) continue;
     const uint32_t r = k.runs - 1, rb = r & 1u;
     const float4* s = reinterpret_cast<const float4*>(p.state + (static_cast<int64_t>(k.u) * p.H + k.h) * LIN_STATE) + lane;
-    if (!warp_wait(&x.image_empty[rb], ((r >> 1) & 1u) ^ 1u, x, p)) return;
-    // row by row: four elements a lane
+    // row by row: four elements a lane (all on their way before the place is free)
     uint8_t* to = sm + IMAGE_AT + rb * TILE + (lane >> 4) * HALF_TILE + (lane & 1) * 8;
-#pragma unroll 1
-    for (int q = 0; q < 16; q += 8) {
-      float4 v[8];
+    float4 v[16];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = __ldg(s + (8 * (q + c) + warp) * 32);
+    for (int c = 0; c < 16; ++c) v[c] = __ldg(s + (8 * c + warp) * 32);
+    if (!warp_wait(&x.image_empty[rb], ((r >> 1) & 1u) ^ 1u, x, p)) return;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int row = 8 * (q + c) + warp;
-        *reinterpret_cast<uint2*>(to + row * 128 + ((((lane & 15) >> 1) ^ (row & 7)) << 4)) = make_uint2(pack_bf16x2(v[c].x, v[c].y), pack_bf16x2(v[c].z, v[c].w));
-      }
+    for (int c = 0; c < 16; ++c) {
+      const int row = 8 * c + warp;
+      *reinterpret_cast<uint2*>(to + row * 128 + ((((lane & 15) >> 1) ^ (row & 7)) << 4)) = make_uint2(pack_bf16x2(v[c].x, v[c].y), pack_bf16x2(v[c].z, v[c].w));
     }
     fence_proxy_async_smem();
     warp_arrive(&x.image_full[rb]);
@@ -225,15 +227,16 @@ __device__ void output_warps(const LinReadParams& p, uint8_t* sm, Aux& x, uint32
   const int quarter = warp & 3, half = (warp - OUT_WARP0) >> 2, row = quarter * 32 + lane;
   const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
   uint8_t* stage = sm + OUT_AT + (warp - OUT_WARP0) * OUT_BYTES;
-  const int piece = lane & 7;
+  const int piece = lane & 7, slot = row / p.Lq;
   Walk k(p);
   uint32_t g = 0;
+  int cand_next = Walk::cand(p, k.next, slot);
   for (int i = k.a; i < k.b && k.at(p, i); ++i, ++g) {
     const uint32_t r = k.runs - 1, rb = r & 1u, rp = (r >> 1) & 1u, ob = g & 1u;
+    const int cand = cand_next;
+    cand_next = Walk::cand(p, k.next, slot);
     if (p.out) {
-      const int slot = row / p.Lq;
-      const int64_t mine = row < k.w.w * p.Lq
-          ? ((static_cast<int64_t>(__ldg(p.perm + k.w.z + slot)) * p.H + k.h) * p.Lq + (row - slot * p.Lq)) * LIN_D : -1;
+      const int64_t mine = row < k.w.w * p.Lq ? ((static_cast<int64_t>(cand) * p.H + k.h) * p.Lq + (row - slot * p.Lq)) * LIN_D : -1;
       if (!warp_wait(&x.o_full[ob], (g >> 1) & 1u, x, p)) return;
       tc_fence_after();
       const uint32_t Ot = tmem + lane_base + TM_O + 128 * ob + 64 * half;
@@ -305,6 +308,67 @@ __device__ void output_warps(const LinReadParams& p, uint8_t* sm, Aux& x, uint32
   }
 }
 
+// The run that unit i belongs to: its first unit and the one behind its last.
+__device__ __forceinline__ void run_of(const LinReadParams& p, int i, int& lo, int& hi) {
+  const int4 w = Walk::unit(p, i);
+  const int cands = 128 / p.Lq, first = __ldg(p.offsets + w.x);
+  lo = i - (w.z - first) / cands;
+  hi = lo + (__ldg(p.offsets + w.x + 1) - first + cands - 1) / cands;
+}
+
+// The parts of the runs that this CTA shares (its first and its last, at most), where it
+// is the last of their CTAs.  Counted whatever happened before, so that counts are zero
+// again for the next call.
+__device__ void join_runs(const LinReadParams& p, uint32_t* last) {
+  const int64_t n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units), ctas = gridDim.x;
+  const auto begin = [&](int64_t c) { return static_cast<int>(c * n / ctas); };
+  const int a = begin(blockIdx.x), b = begin(static_cast<int64_t>(blockIdx.x) + 1);
+  if (a >= b) return;
+  int done = -1;
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    int lo, hi;
+    run_of(p, k == 0 ? a : b - 1, lo, hi);
+    if ((lo >= a && hi <= b) || lo == done || lo < 0 || hi > n) continue;  // its own, or the same again
+    done = lo;
+    const int c0 = static_cast<int>(((lo + 1) * ctas - 1) / n), c1 = static_cast<int>((hi * ctas - 1) / n);
+    const uint32_t parts = n >= ctas ? c1 - c0 + 1 : hi - lo;  // (with fewer units than CTAs each has one at most)
+    if (threadIdx.x == 0) {
+      __threadfence();
+      *last = atomicAdd(p.tickets + c0, 1u) + 1 == parts;
+      if (*last) p.tickets[c0] = 0;
+    }
+    __syncthreads();
+    if (*last) {
+      __threadfence();
+      const int4 w = Walk::unit(p, lo);
+      float4* to = reinterpret_cast<float4*>(p.d_state + (static_cast<int64_t>(w.x) * p.H + w.y) * LIN_STATE);
+      constexpr int kMine = (LIN_STATE / 4 + RT_THREADS - 1) / RT_THREADS;
+      float4 sum[kMine] = {};
+#pragma unroll 2
+      for (int c = c0; c <= c1; ++c) {
+        if (begin(c) >= begin(c + 1)) continue;
+        const float4* part = reinterpret_cast<const float4*>(p.part + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * LIN_STATE);
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) {
+          const int e = q * RT_THREADS + static_cast<int>(threadIdx.x);
+          const float4 v = e < LIN_STATE / 4 ? __ldcg(part + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+          sum[q].x += v.x;
+          sum[q].y += v.y;
+          sum[q].z += v.z;
+          sum[q].w += v.w;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kMine; ++q) {
+        const int e = q * RT_THREADS + static_cast<int>(threadIdx.x);
+        if (e < LIN_STATE / 4) to[e] = make_float4(sum[q].x * p.scale, sum[q].y * p.scale, sum[q].z * p.scale, sum[q].w * p.scale);
+      }
+    }
+    __syncthreads();
+  }
+}
+
 template <bool kBack>
 __global__ void __launch_bounds__(RT_THREADS, 1)
     lin_read_kernel(const __grid_constant__ LinReadParams p, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mq) {
@@ -357,51 +421,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-}
-
-// Adds the parts of each (user, head) whose units several CTAs had, in order:
-// block c those of the one that begins in CTA c and goes on in the next.
-__global__ void __launch_bounds__(JOIN_THREADS) lin_read_join_kernel(const __grid_constant__ LinReadParams p) {
-  const int c = static_cast<int>(blockIdx.x);
-  const int n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
-  const int4* work = reinterpret_cast<const int4*>(p.work);
-  const auto same = [&](int i, int j) {
-    const int4 x = __ldg(work + i), y = __ldg(work + j);
-    return x.x == y.x && x.y == y.y;
-  };
-  const auto unit_range = [&](int cta, int& a, int& b) {
-    a = static_cast<int>(static_cast<int64_t>(cta) * n / gridDim.x);
-    b = static_cast<int>(static_cast<int64_t>(cta + 1) * n / gridDim.x);
-  };
-  int a, b;
-  unit_range(c, a, b);
-  if (a >= b || b >= n || !same(b - 1, b)) return;  // nothing, or its last one ends here
-  if (a > 0 && same(a - 1, a) && same(a, b - 1)) return;  // begins in a CTA before
-  const int4 w = __ldg(work + b - 1);
-  int last = c;  // the CTA where it ends
-  for (int end = b; end < n && same(b - 1, end);) {
-    int x, y;
-    unit_range(++last, x, y);
-    end = y;
-    if (y > x && !same(b - 1, y - 1)) break;
-  }
-  float* to = p.d_state + (static_cast<int64_t>(w.x) * p.H + w.y) * LIN_STATE;
-  const int per = LIN_STATE / 4 / gridDim.y, e0 = static_cast<int>(blockIdx.y) * per;
-  for (int e = e0 + threadIdx.x; e < e0 + per; e += JOIN_THREADS) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = c; k <= last; ++k) {
-      int x, y;
-      unit_range(k, x, y);
-      if (x >= y) continue;  // a CTA without units has left nothing
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + (2 * static_cast<int64_t>(k) + (k == c ? 1 : 0)) * LIN_STATE) + e);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-    reinterpret_cast<float4*>(to)[e] = make_float4(s.x * p.scale, s.y * p.scale, s.z * p.scale, s.w * p.scale);
-  }
+  if (kBack) join_runs(p, &x.last);
 }
 
 template <bool kBack>
@@ -418,11 +438,6 @@ bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
 
 size_t lin_read_smem() { return RT_SMEM; }
 int lin_read_ctas(int num_sms) { return num_sms; }
-
-cudaError_t launch_lin_read_join(const LinReadParams& p, int num_sms, cudaStream_t s) {
-  lin_read_join_kernel<<<dim3(static_cast<unsigned>(lin_read_ctas(num_sms)), 8), JOIN_THREADS, 0, s>>>(p);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_lin_read(const LinReadParams& p, int num_sms, cudaStream_t s) {
   CUtensorMap mx, mq;

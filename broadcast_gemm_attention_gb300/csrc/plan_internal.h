@@ -79,6 +79,7 @@ struct ikbo_plan_s {
   // linear attention (grown on first use)
   ikbo::KeptBuffer<float> lin_states;     // states between the segments of long histories
   ikbo::KeptBuffer<float> lin_part;       // gradients of states: what CTAs that share a state have of it
+  ikbo::KeptBuffer<uint32_t> lin_tickets; // how many of them have ended (zero between calls)
   void** retired = nullptr;               // replaced buffers that captured graphs may hold, freed with the plan
   int n_retired = 0;
   bool lce_flags_dirty = false;  // an LCE launch failed: its flags may still be set

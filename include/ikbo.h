@@ -588,7 +588,7 @@ ikbo_status_t ikbo_linattn_read_forward(ikbo_plan_t p, const void* Q, const floa
 /* Its gradients: dQ[i,h] = scale dO[i,h] S[map[i],h]^T (bf16; may be NULL or dO
  * where d_state is NULL; not Q) and d_state[u,h] = scale sum_{map[i]=u} Q[i,h]^T dO[i,h] (fp32, 0
  * for a user without candidates; may be NULL), overwritten.  Q may be NULL
- * without d_state, state without dQ.  One launch for dQ, two for d_state;
+ * without d_state, state without dQ.  One launch;
  * results repeat bit for bit. */
 ikbo_status_t ikbo_linattn_read_backward(ikbo_plan_t p, const void* Q, const float* state, const void* dO, void* dQ,
                                          float* d_state, int d, float scale, cudaStream_t stream);
