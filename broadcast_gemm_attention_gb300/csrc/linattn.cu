@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ L
   const float log2_decay = log2f(__ldg(p.decay + h));
   const float down = lin_power(log2_decay, p.seg_len);
   s *= job.reverse ? lin_power(log2_decay, p.seg_len - 1) : down;
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 0; k + 1 < segs; ++k) {
     s += ws[static_cast<int64_t>(k) * LIN_STATE];
     ws[static_cast<int64_t>(k) * LIN_STATE] = s;

@@ -97,57 +97,118 @@ __device__ __forceinline__ int user_segs(const LinParams& p, int u) {
   return max(1, (len + p.seg_len - 1) / p.seg_len) - (kLocal ? 1 : 0);
 }
 
-// Items of one job.  (By whole warps, like get_item.)
+// A CTA's items, one after the other, by whole warps.
+//
+// Scans are dealt out longest first, back and forth over the CTAs (so that a CTA's long
+// one meets a short one: the gradient of 15 users' 524 to 1024 rows 83 -> 76 us), where there
+// are no segments, more than one a CTA, and a lane for each user; else in order.
 template <bool kLocal>
-__device__ __forceinline__ int job_items(const LinParams& p) {
-  if (p.segs == 1) return p.n_users * p.H;
-  int sum = 0;
-#pragma unroll 1
-  for (int u = 0; u < p.n_users; u += 32) sum += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(user_segs<kLocal>(p, u + static_cast<int>(lane_id())))));
-  return sum * p.H;
-}
+struct Items {
+  int per_job;    // items of one job
+  int items, k;   // of the launch; turns taken
+  bool sorted;
+  int rank;       // of the lane's user, by rows
 
-// Item i of the launch, of per_job = job_items().
-template <bool kLocal>
-__device__ __forceinline__ void get_item(const LinParams& p, int i, int per_job, Item& x, bool report) {
-  x.job = i / per_job;
-  const int r = i - x.job * per_job;
-  x.seg = 0;
-  if (p.segs == 1) {
-    x.u = r / p.H;
-    x.h = r - x.u * p.H;
-  } else {  // users one after the other, each with its own number of segments for each head
-    int before = 0, u0 = 0, mine, upto;
+  __device__ __forceinline__ Items(const LinParams& p) : k(0) {
+    const int lane = static_cast<int>(lane_id());
+    sorted = p.segs == 1 && p.n_users <= 32 && p.n_users * p.H * p.n_jobs > static_cast<int>(gridDim.x);
+    rank = lane;
+    if (p.segs == 1) {
+      per_job = p.n_users * p.H;
+      if (sorted) {
+        int first;
+        const int len = lane < p.n_users ? user_rows(p, lane, first, false) : -1;
+        rank = 0;
 #pragma unroll 1
-    for (;; u0 += 32) {
-      mine = user_segs<kLocal>(p, u0 + static_cast<int>(lane_id()));
-      upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (static_cast<int>(lane_id()) >= o) upto += y;
+        for (int v = 0; v < 32; ++v) {
+          const int other = __shfl_sync(0xffffffffu, len, v);
+          rank += other > len || (other == len && v < lane);
+        }
       }
-      const int all = __shfl_sync(0xffffffffu, upto, 31);
-      if (r < (before + all) * p.H || u0 + 32 >= p.n_users) break;
-      before += all;
+    } else {
+      int sum = 0;
+#pragma unroll 1
+      for (int u = 0; u < p.n_users; u += 32) sum += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(user_segs<kLocal>(p, u + lane))));
+      per_job = sum * p.H;
     }
-    const int l = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, r < (before + upto) * p.H))) - 1;
-    mine = __shfl_sync(0xffffffffu, mine, l);
-    const int in = r - (before + __shfl_sync(0xffffffffu, upto, l) - mine) * p.H;
-    x.u = u0 + l;
-    x.h = in / mine;
-    x.seg = in - x.h * mine;
+    items = per_job * p.n_jobs;
   }
-  int first;
-  const int len = user_rows(p, x.u, first, report);
-  x.reverse = p.job[x.job].reverse != 0;
-  x.segs = p.segs > 1 ? max(1, (len + p.seg_len - 1) / p.seg_len) : 1;
-  const int r0 = x.segs > 1 ? x.seg * p.seg_len : 0;
-  x.n = x.segs > 1 ? min(p.seg_len, len - r0) : len;
-  x.base = first + (x.reverse ? len - r0 - x.n : r0);
-  x.whole_user_empty = len == 0;
-  x.early = !kLocal && x.seg == 0 && x.reverse ? 1 : 0;
-  x.chunks = (x.n + LT_CHUNK - 1) / LT_CHUNK;
+
+  // The CTA's next item; false: none is left.
+  __device__ __forceinline__ bool next(const LinParams& p, Item& x, bool report) {
+    const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+#pragma unroll 1
+    for (; k * ctas < items; ++k) {
+      const int i = k & 1 ? (k + 1) * ctas - 1 - cta : k * ctas + cta;
+      if (i >= items) continue;
+      ++k;
+      get(p, i, x, report);
+      return true;
+    }
+    return false;
+  }
+
+  __device__ __forceinline__ void get(const LinParams& p, int i, Item& x, bool report) const {
+    const int lane = static_cast<int>(lane_id());
+    x.seg = 0;
+    if (sorted) {
+      const int each = p.n_jobs * p.H, which = i / each, r = i - which * each;
+      x.u = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, rank == which))) - 1;
+      x.job = r / p.H;
+      x.h = r - x.job * p.H;
+    } else {
+      x.job = i / per_job;
+      const int r = i - x.job * per_job;
+      if (p.segs == 1) {
+        x.u = r / p.H;
+        x.h = r - x.u * p.H;
+      } else {  // users one after the other, each with its own number of segments for each head
+        int before = 0, u0 = 0, mine, upto;
+#pragma unroll 1
+        for (;; u0 += 32) {
+          mine = user_segs<kLocal>(p, u0 + lane);
+          upto = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+          }
+          const int all = __shfl_sync(0xffffffffu, upto, 31);
+          if (r < (before + all) * p.H || u0 + 32 >= p.n_users) break;
+          before += all;
+        }
+        const int l = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, r < (before + upto) * p.H))) - 1;
+        mine = __shfl_sync(0xffffffffu, mine, l);
+        const int in = r - (before + __shfl_sync(0xffffffffu, upto, l) - mine) * p.H;
+        x.u = u0 + l;
+        x.h = in / mine;
+        x.seg = in - x.h * mine;
+      }
+    }
+    int first;
+    const int len = user_rows(p, x.u, first, report);
+    x.reverse = p.job[x.job].reverse != 0;
+    x.segs = p.segs > 1 ? max(1, (len + p.seg_len - 1) / p.seg_len) : 1;
+    const int r0 = x.segs > 1 ? x.seg * p.seg_len : 0;
+    x.n = x.segs > 1 ? min(p.seg_len, len - r0) : len;
+    x.base = first + (x.reverse ? len - r0 - x.n : r0);
+    x.whole_user_empty = len == 0;
+    x.early = !kLocal && x.seg == 0 && x.reverse ? 1 : 0;
+    x.chunks = (x.n + LT_CHUNK - 1) / LT_CHUNK;
+  }
+};
+
+// Where an item's state comes from (null: zero), and whether rows there are z's elements.
+template <bool kLocal>
+__device__ __forceinline__ const float* state_from(const LinParams& p, const Item& it, bool& turned) {
+  turned = false;
+  if (kLocal) return nullptr;
+  const int64_t uh = static_cast<int64_t>(it.u) * p.H + it.h;
+  // of several segments the first one's start is in the workspace too, as s_out may be s_in
+  if (it.segs > 1)
+    return p.ws + ((static_cast<int64_t>(it.job) * p.n_users * p.H + uh) * p.segs + (it.seg > 0 ? it.seg - 1 : it.segs - 1)) * LIN_STATE;
+  turned = p.job[it.job].s_in_turned != 0;
+  return p.job[it.job].s_in ? p.job[it.job].s_in + uh * LIN_STATE : nullptr;
 }
 
 // A group's warps meet.  (Not a hardware barrier: a warp that gave up does not come.)
@@ -193,10 +254,9 @@ __device__ void loader(const LinParams& p, const LtMaps& maps, uint8_t* sm, Aux&
   };
   uint32_t ny = 0, nx = 0, nz = 0;
   bool ok = true;
-  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
-  for (int i = static_cast<int>(blockIdx.x); i < items && ok; i += static_cast<int>(gridDim.x)) {
-    Item it;
-    get_item<kLocal>(p, i, per_job, it, false);
+  Items<kLocal> items(p);
+  Item it;
+  for (bool more = items.next(p, it, false); more && ok;) {
     for (int c = 0; c < it.chunks && ok; ++c, ++g) {
       const uint32_t free = (g & 1u) ^ 1u;
       const int row = it.first(c);
@@ -225,6 +285,11 @@ __device__ void loader(const LinParams& p, const LtMaps& maps, uint8_t* sm, Aux&
       }
       __syncwarp();
     }
+    more = ok && items.next(p, it, false);
+    bool turned;
+    const float* state = more ? state_from<kLocal>(p, it, turned) : nullptr;
+    if (state && elect_one()) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(state), "n"(LIN_STATE * 4) : "memory");
+    __syncwarp();
   }
   // the copies in flight end before the CTA does (where all went well, their readers have seen to it)
   if (!ok) {
@@ -275,10 +340,8 @@ template <bool kLocal>
 __device__ void output_issuer(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
   uint32_t g = 0;
   const uint32_t xb = smem_u32(sm + X_AT), yb = smem_u32(sm + Y_AT), zb = smem_u32(sm + Z_AT), sb = smem_u32(sm + S_AT);
-  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
-  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
-    Item it;
-    get_item<kLocal>(p, i, per_job, it, false);
+  Items<kLocal> items(p);
+  for (Item it; items.next(p, it, false);) {
     for (int c = 0; c < it.chunks; ++c, ++g) {
       const uint32_t ph = g & 1u;
       if (!warp_wait(&x.y_full, ph, x, p) || !warp_wait(&x.x_full, ph, x, p)) return;
@@ -318,10 +381,8 @@ template <bool kLocal>
 __device__ void state_issuer(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
   uint32_t g = 0;
   const uint32_t zb = smem_u32(sm + Z_AT), hb = smem_u32(sm + HI_AT), lb = smem_u32(sm + LO_AT);
-  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
-  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
-    Item it;
-    get_item<kLocal>(p, i, per_job, it, false);
+  Items<kLocal> items(p);
+  for (Item it; items.next(p, it, false);) {
     for (int c = 0; c < it.chunks; ++c, ++g) {
       const uint32_t ph = g & 1u;
       if (!warp_wait(&x.z_full, ph, x, p) || !warp_wait(&x.w_full, ph, x, p) || !warp_wait(&x.s_full, ph, x, p)) return;
@@ -350,10 +411,8 @@ __device__ void decay_warps(const LinParams& p, Aux& x, uint32_t tmem) {
   const int quarter = warp & 3, half = (warp - DECAY_WARP0) >> 2, i_row = quarter * 32 + lane;
   const uint32_t At = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM_A + half * 64;
   uint32_t g = 0, meet = 0;
-  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
-  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
-    Item it;
-    get_item<kLocal>(p, i, per_job, it, false);
+  Items<kLocal> items(p);
+  for (Item it; items.next(p, it, false);) {
     if (it.chunks == 0) continue;
     const float log2_decay = log2f(__ldg(p.decay + it.h));
     if (!group_sync(&x.group[0], meet, x, p)) return;
@@ -418,10 +477,8 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t t
   const uint32_t O1 = tmem + lane_base + TM_O1 + half * 64, O2 = tmem + lane_base + TM_O2 + half * 64;
   uint8_t* stage = sm + OUT_AT + (warp - OUT_WARP0) * OUT_BYTES;
   uint32_t g = 0;
-  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
-  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
-    Item it;
-    get_item<kLocal>(p, i, per_job, it, false);
+  Items<kLocal> items(p);
+  for (Item it; items.next(p, it, false);) {
     const LinJob& job = p.job[it.job];
     const float log2_decay = log2f(__ldg(p.decay + it.h));
     for (int c = 0; c < it.chunks; ++c, ++g) {
@@ -471,56 +528,64 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tm
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
   const int quarter = warp & 3, half = (warp - STATE_WARP0) >> 2, e_row = quarter * 32 + lane;  // a row of the state, 64 half .. of its columns
   const uint32_t St = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM_S + half * 64;
-  uint8_t* image = sm + S_AT + half * HALF_TILE + e_row * 128;
+  uint8_t* stage = sm + S_AT + half * HALF_TILE + quarter * 32 * 128;  // the warp's rows of the image
+  uint8_t* image = stage + lane * 128;
   uint32_t g = 0;
-  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
-  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
-    Item it;
-    get_item<kLocal>(p, i, per_job, it, threadIdx.x == 32 * STATE_WARP0);
+  Items<kLocal> items(p);
+  for (Item it; items.next(p, it, threadIdx.x == 32 * STATE_WARP0);) {
     const LinJob& job = p.job[it.job];
     const float log2_decay = log2f(__ldg(p.decay + it.h));
     const int64_t state = (static_cast<int64_t>(it.u) * p.H + it.h) * LIN_STATE;
     const int64_t ws = ((static_cast<int64_t>(it.job) * p.n_users + it.u) * p.H + it.h) * p.segs;
-    const float* from = nullptr;
-    if (!kLocal) {  // of several segments the first one's start is in the workspace too, as s_out may be s_in
-      if (it.segs > 1) from = p.ws + (ws + (it.seg > 0 ? it.seg - 1 : it.segs - 1)) * LIN_STATE;
-      else if (job.s_in) from = job.s_in + state;
-    }
+    bool turned;
+    const float* from = state_from<kLocal>(p, it, turned);
     const float factor = it.segs > 1 ? 1.f : job.s_in_factor;
-    const bool turned = it.segs == 1 && job.s_in_turned;
     float* to = kLocal ? p.ws + (ws + it.seg) * LIN_STATE : (it.seg + 1 == it.segs && job.s_out ? job.s_out + state : nullptr);
     const float up = kLocal ? 1.f : (it.reverse && !it.whole_user_empty ? job.s_out_factor * decay_power(log2_decay, 1) : job.s_out_factor);
+    // The start to tensor memory.  Rows of a state are 512 bytes apart, a lane's place is a row: eight lanes load a row's
+    // 128 bytes, by way of the warp's place in the image (a load of 16 bytes of each of 32 rows took 18000 cycles in all).
+    if (kOutputs && !warp_wait(&x.s_empty, (g & 1u) ^ 1u, x, p)) return;
+    const int sub = lane >> 3, piece = lane & 7;
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+      uint32_t v[32];
+      if (from && !turned) {
+        float4 f[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] = __ldcg(reinterpret_cast<const float4*>(from + (quarter * 32 + 4 * q + sub) * LIN_D + 64 * half + 32 * b) + piece);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) *reinterpret_cast<float4*>(stage + (4 * q + sub) * 128 + ((piece ^ ((4 * q + sub) & 7)) << 4)) = f[q];
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 r = *reinterpret_cast<const float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4));
+          v[4 * k] = __float_as_uint(r.x * factor);
+          v[4 * k + 1] = __float_as_uint(r.y * factor);
+          v[4 * k + 2] = __float_as_uint(r.z * factor);
+          v[4 * k + 3] = __float_as_uint(r.w * factor);
+        }
+        __syncwarp();
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(from ? __ldcg(from + (64 * half + 32 * b + k) * LIN_D + e_row) * factor : 0.f);
+      }
+      tmem_st32(St + 32 * b, v);
+    }
+    tmem_st_wait();
     // chunk by chunk: the image of the state before it, and the decay over it; then
     // the products add the chunk.  One turn more gives the end away.
     for (int c = 0; c <= it.chunks; ++c) {
       const bool last = c == it.chunks;
       if (c > 0 && !warp_wait(&x.m_full, (g - 1) & 1u, x, p)) return;
       if (last && !to) break;
-      if (kOutputs && !last && !warp_wait(&x.s_empty, (g & 1u) ^ 1u, x, p)) return;
+      if (kOutputs && !warp_wait(&x.s_empty, (g & 1u) ^ 1u, x, p)) return;
       tc_fence_after();
       const float down = last ? up : decay_power(log2_decay, it.rows(c) - (c == 0 ? it.early : 0));
 #pragma unroll 1
       for (int b = 0; b < 2; ++b) {
         uint32_t v[32];
-        if (c > 0) {
-          tmem_ld32(St + 32 * b, v);
-          tmem_ld_wait(v);
-        } else if (!from) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = 0;
-        } else if (!turned) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(from + e_row * LIN_D + 64 * half + 32 * b) + k);
-            v[4 * k] = __float_as_uint(f.x * factor);
-            v[4 * k + 1] = __float_as_uint(f.y * factor);
-            v[4 * k + 2] = __float_as_uint(f.z * factor);
-            v[4 * k + 3] = __float_as_uint(f.w * factor);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__ldcg(from + (64 * half + 32 * b + k) * LIN_D + e_row) * factor);
-        }
+        tmem_ld32(St + 32 * b, v);
+        tmem_ld_wait(v);
         if (kOutputs && !last) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -537,13 +602,19 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tm
           v[2 * k] = __float_as_uint(f0);
           v[2 * k + 1] = __float_as_uint(f1);
         }
-        if (last) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            reinterpret_cast<uint4*>(to + e_row * LIN_D + 64 * half + 32 * b)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        } else {
+        if (!last) {
           tmem_st32(St + 32 * b, v);
+          continue;
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          reinterpret_cast<uint4*>(to + (quarter * 32 + 4 * q + sub) * LIN_D + 64 * half + 32 * b)[piece] =
+              *reinterpret_cast<const uint4*>(stage + (4 * q + sub) * 128 + ((piece ^ ((4 * q + sub) & 7)) << 4));
+        __syncwarp();
       }
       if (last) break;
       tmem_st_wait();
@@ -561,10 +632,8 @@ __device__ void parts_warps(const LinParams& p, uint8_t* sm, Aux& x) {
   constexpr int kThreads = 32 * PARTS_WARPS;
   const int tid = static_cast<int>(threadIdx.x) - 32 * PARTS_WARP0;
   uint32_t g = 0, meet = 0;
-  const int per_job = job_items<kLocal>(p), items = per_job * p.n_jobs;
-  for (int i = static_cast<int>(blockIdx.x); i < items; i += static_cast<int>(gridDim.x)) {
-    Item it;
-    get_item<kLocal>(p, i, per_job, it, false);
+  Items<kLocal> items(p);
+  for (Item it; items.next(p, it, false);) {
     if (it.chunks == 0) continue;
     if (!group_sync(&x.group[1], meet, x, p)) return;
     {

@@ -49,15 +49,36 @@ struct Tree {
   int up[2][TR_MOST];   // the row above, -1: none, -2: the row is not there
 };
 
-// Which rows of the draft each row reads, by doubling the way up.
-__device__ void build_tree(const QcTreeParams& p, int cand, Tree& tr) {
+__device__ __forceinline__ int parent(const QcTreeParams& p, int cand, int l) {
+  const int up = p.parents ? __ldg(p.parents + static_cast<int64_t>(cand) * p.Lq + l) : l - 1;
+  if (up >= l) atomicOr(p.status, DEV_ERR_CACHE);
+  return up >= l || up < -1 ? -2 : up;
+}
+
+// Which rows of a draft of up to 32 each row reads, by doubling the way up: every warp
+// for itself, a lane a row.
+__device__ __forceinline__ uint32_t small_tree(const QcTreeParams& p, int up, int lane) {
+  uint32_t m = 1u << lane;
+#pragma unroll 1
+  for (int reach = 1; reach < p.Lq; reach <<= 1) {
+    const int at = up >= 0 ? up : lane;
+    const uint32_t more = __shfl_sync(0xffffffffu, m, at);
+    const int next = __shfl_sync(0xffffffffu, up, at);
+    if (up < 0) continue;
+    if (next == -2) atomicOr(p.status, DEV_ERR_CACHE);  // below a row that is not there
+    up = next;
+    m |= more;
+  }
+  return up == -2 ? 0u : m;
+}
+
+// The same for up to 128, by the whole CTA.
+__device__ void large_tree(const QcTreeParams& p, int cand, Tree& tr) {
   const int l = threadIdx.x, L = p.Lq;  // TR_THREADS >= Lq
   uint32_t m[4] = {};
   int up = -1;
   if (l < L) {
-    up = p.parents ? __ldg(p.parents + static_cast<int64_t>(cand) * L + l) : l - 1;
-    if (up >= l) atomicOr(p.status, DEV_ERR_CACHE);
-    if (up >= l || up < -1) up = -2;
+    up = parent(p, cand, l);
 #pragma unroll
     for (int w = 0; w < 4; ++w) m[w] = (l >> 5) == w ? 1u << (l & 31) : 0u;
     tr.sees[l] = make_uint4(m[0], m[1], m[2], m[3]);
@@ -90,13 +111,16 @@ __device__ void build_tree(const QcTreeParams& p, int cand, Tree& tr) {
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(TR_THREADS) qtree_kernel(const QcTreeParams p) {
+__global__ void __launch_bounds__(TR_THREADS, 2) qtree_kernel(const QcTreeParams p) {
   __shared__ Tree tr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int cand = static_cast<int>(blockIdx.x);
   const int u = __ldg(p.map + cand);
   if (u < 0 || u >= p.n_users) return;  // (reported by the plan)
   const int rows = p.group * p.Lq, tiles = (rows + 15) >> 4, items = tiles * p.H_kv;
+  const bool small = p.Lq <= 32;
+  const int up = small && lane < p.Lq ? parent(p, cand, lane) : -1;
+  uint32_t line = 0;
   bool built = false;
 #pragma unroll 1
   for (int first = static_cast<int>(blockIdx.y) * 4; first < items; first += static_cast<int>(gridDim.y) * 4) {
@@ -128,25 +152,40 @@ __global__ void __launch_bounds__(TR_THREADS) qtree_kernel(const QcTreeParams p)
       m[e] = lse * 1.4426950408889634f;
       l[e] = lse == -INFINITY ? 0.f : 1.f;
     }
-    if (!built) build_tree(p, cand, tr);
+    const uint16_t* kp = p.K + static_cast<int64_t>(cand) * p.cand_stride + hk * QC_D + 8 * t;
+    const uint16_t* vp = p.V + static_cast<int64_t>(cand) * p.cand_stride + hk * QC_D + 8 * t;
+    uint4 k[2][4], v[2][4];
+    const auto fetch = [&](const uint16_t* from, int k0, uint4 (&to)[2][4]) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          to[n][j] = k0 + 8 * n + g < p.Lq ? __ldg(reinterpret_cast<const uint4*>(from + (k0 + 8 * n + g) * p.row_stride + 32 * j)) : uint4{};
+    };
+    fetch(kp, 0, k);
+    fetch(vp, 0, v);
+    if (!built) {
+      if (small) line = small_tree(p, up, lane);
+      else large_tree(p, cand, tr);
+    }
     built = true;
     const int l0 = r0 % p.Lq, l1 = (r0 + 8) % p.Lq;
-    uint4 sees[2] = {here[0] ? tr.sees[l0] : uint4{}, here[1] ? tr.sees[l1] : uint4{}};
+    uint4 sees[2] = {};
+    if (small) {
+      const uint32_t s0 = __shfl_sync(0xffffffffu, line, l0), s1 = __shfl_sync(0xffffffffu, line, l1);
+      sees[0].x = here[0] ? s0 : 0u;
+      sees[1].x = here[1] ? s1 : 0u;
+    } else {
+      if (here[0]) sees[0] = tr.sees[l0];
+      if (here[1]) sees[1] = tr.sees[l1];
+    }
     const int n_keys = min(p.Lq, 16 * tile % p.Lq + 16);  // up to the tile's last row (all, where it goes on in the next head)
 #pragma unroll 1
     for (int k0 = 0; k0 < n_keys; k0 += 16) {
-      const uint16_t* kp = p.K + static_cast<int64_t>(cand) * p.cand_stride + hk * QC_D + 8 * t;
-      const uint16_t* vp = p.V + static_cast<int64_t>(cand) * p.cand_stride + hk * QC_D + 8 * t;
-      uint4 k[2][4] = {}, v[2][4] = {};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-        if (k0 + 8 * n + g < p.Lq) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            k[n][j] = __ldg(reinterpret_cast<const uint4*>(kp + (k0 + 8 * n + g) * p.row_stride + 32 * j));
-            v[n][j] = __ldg(reinterpret_cast<const uint4*>(vp + (k0 + 8 * n + g) * p.row_stride + 32 * j));
-          }
-        }
+      if (k0 > 0) {
+        fetch(kp, k0, k);
+        fetch(vp, k0, v);
+      }
       float s[2][4] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -263,7 +302,7 @@ cudaError_t launch_qtree(const QcTreeParams& p, int num_sms, cudaStream_t s) {
   const int items = ((p.group * p.Lq + 15) / 16) * p.H_kv;
   // a CTA takes four items of a candidate, more where there are CTAs enough
   int parts = (items + 3) / 4;
-  while (parts > 1 && static_cast<int64_t>(parts / 2) * p.n_cand >= 16 * static_cast<int64_t>(num_sms)) parts = (parts + 1) / 2;
+  while (parts > 1 && static_cast<int64_t>(parts / 2) * p.n_cand >= 4 * static_cast<int64_t>(num_sms)) parts = (parts + 1) / 2;
   qtree_kernel<<<dim3(static_cast<unsigned>(p.n_cand), static_cast<unsigned>(parts)), TR_THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
