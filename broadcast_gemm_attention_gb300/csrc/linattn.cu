@@ -19,6 +19,7 @@
 
 #include "linattn_internal.h"
 #include "mma_common.cuh"
+#include "tile_common.cuh"
 
 namespace ikbo {
 namespace {
@@ -339,16 +340,14 @@ __global__ void __launch_bounds__(LIN_THREADS) lin_step_kernel(const __grid_cons
         for (int e = 0; e < 4; ++e) {
           const float y = e == 0 ? yv.x : (e == 1 ? yv.y : (e == 2 ? yv.z : yv.w));
           float4& v = s[4 * q + e];
-          v.x = fmaf(y, z.x, v.x * decay);
-          v.y = fmaf(y, z.y, v.y * decay);
-          v.z = fmaf(y, z.z, v.z * decay);
-          v.w = fmaf(y, z.w, v.w * decay);
+          mul2(v.x, v.y, v.x, v.y, decay, decay);
+          mul2(v.z, v.w, v.z, v.w, decay, decay);
+          fma2v(v.x, v.y, z.x, z.y, y, v.x, v.y);
+          fma2v(v.z, v.w, z.z, z.w, y, v.z, v.w);
           if (kOutputs) {
             const float x = e == 0 ? xv.x : (e == 1 ? xv.y : (e == 2 ? xv.z : xv.w));
-            o.x = fmaf(x, v.x, o.x);
-            o.y = fmaf(x, v.y, o.y);
-            o.z = fmaf(x, v.z, o.z);
-            o.w = fmaf(x, v.w, o.w);
+            fma2v(o.x, o.y, v.x, v.y, x, o.x, o.y);
+            fma2v(o.z, o.w, v.z, v.w, x, o.z, o.w);
           }
         }
       }

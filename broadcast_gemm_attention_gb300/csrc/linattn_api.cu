@@ -48,6 +48,7 @@ ikbo_status_t lin_params(ikbo_plan_t p, const int32_t* d_offsets, int n_users, i
   lp->max_len = d_offsets ? (max_len > 0 ? std::min(max_len, n_rows) : n_rows) : n_rows / n_users;
   lp->scale = scale;
   lp->segs = 1;
+  lp->debug = p->debug;
   lp->timeout_ns = p->timeout_ns;
   return IKBO_OK;
 }
@@ -62,12 +63,12 @@ constexpr int64_t LIN_MOST_STATES = 16384;  // 1 GiB
 constexpr int LIN_LEAST_SEGMENT = 256;
 
 // The variant, from the bound on a user's rows.  Measured, 8 heads (us):
-//   forward              15 users of 4     8    16    64   128   192   256 rows   100 users of 8   128   256
-//   row by row                     4.6   6.2   9.1  27.6                                       32.8
-//   chunks, warps' registers             6.9   6.9   9.2  13.5  17.8  22.2                     41.3  83.7 135.5
-//   chunks, tensor memory               13.6  13.6  14.1  14.1  16.8  17.0                     75.5  90.2 113.9
-//   the states alone: row by row 3.8 4.5 6.0 15.2, registers 5.4 (8 rows) .. 8.3 (128) 12.0 (256) 18.7 (512),
-//   tensor memory 10.8 .. 10.9 12.5 15.6; the gradient, 64 and 128 rows: registers 22.1 and 35.1, tensor memory 24.3 and 24.7
+//   forward, rows           15 users:  4     8    16    32    64   128   192   256   100 users: 8    16   128   256
+//   row by row                       4.4   5.8   8.3  13.7                                   29.0  40.6
+//   chunks, in registers                   6.9   7.0   7.7   9.2  13.5  17.8  22.2           41.7  42.7  83.8 135.5
+//   chunks, tensor memory                 13.6  13.6  13.9  14.1  14.1  14.1  14.0           75.5  81.6  90.2  79.6
+//   the states alone:  row by row 3.9 4.4 5.8 8.6, in registers 5.3 (8 rows) .. 8.3 (128) 12.0 (256) 18.7 (512), tensor
+//   memory 10.8 (8) .. 10.9 (128) 12.5 (256) 15.6 (512); the gradient of 64 and 128 rows: 22.1 and 35.1, and 24.3 and 25.6
 constexpr int LIN_TILES_FROM[3] = {129, 257, 65};  // forward, states alone, gradient
 
 void cut_segments(LinParams* lp, int num_sms) {
@@ -124,6 +125,7 @@ ikbo_status_t read_call(ikbo_plan_t p, const void* x, const float* state, int d,
   rp->H = p->H;
   rp->Lq = p->Lq;
   rp->scale = scale;
+  rp->debug = p->debug;
   rp->timeout_ns = p->timeout_ns;
   return IKBO_OK;
 }

@@ -9,7 +9,7 @@ namespace ikbo {
 constexpr int LIN_D = 128;                    // head dimension of queries, keys and values
 constexpr int LIN_STATE = LIN_D * LIN_D;      // floats of a state
 constexpr int LIN_MAX_JOBS = 3;
-constexpr int LIN_STEP_MOST = 4;              // rows of a user up to which single steps are taken
+constexpr int LIN_STEP_MOST = 8;              // rows of a user up to which single steps are taken
 
 // One scan: with queries x, keys y and values z,
 //   S <- decay S + y_t z_t^T,   out_t = scale x_t S
@@ -39,6 +39,7 @@ struct LinParams {
   int backward;            // the jobs are a gradient's (variants do not go by which of them are asked for)
   int steps;               // rows one by one (a forward scan alone)
   int tiles;               // the chunks' products on the 5th-gen tensor cores
+  uint32_t debug;          // the plan's switches
   uint64_t timeout_ns;
   float scale;
 };
@@ -60,6 +61,7 @@ struct LinReadParams {
   int n_cand, n_users, H, Lq;
   int turned;               // out = x S^T
   float scale;
+  uint32_t debug;           // the plan's switches
   uint64_t timeout_ns;
 };
 

@@ -126,8 +126,8 @@ __device__ void loader(const LinReadParams& p, const CUtensorMap* mx, const CUte
     }
     __syncwarp();
   }
-  if (!ok)  // the copies in flight end before the CTA does
-    for (uint32_t s = g > static_cast<uint32_t>(kStages) ? g - kStages : 0; s < g; ++s) wait_a_second(&x.full[s % kStages], (s / kStages) & 1u);
+  // the copies in flight end before the CTA does, whichever warp's wait ran out
+  for (uint32_t s = g > static_cast<uint32_t>(kStages) ? g - kStages : 0; s < g; ++s) wait_a_second(&x.full[s % kStages], (s / kStages) & 1u);
   __syncwarp();
 }
 
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       mbar_init(&x.image_empty[i], 1);
       mbar_init(&x.ds_full[i], 1);
       mbar_init(&x.o_empty[i], GROUP_WARPS);
-      mbar_init(&x.image_full[i], GROUP_WARPS);
+      mbar_init(&x.image_full[i], GROUP_WARPS + ((p.debug & DEBUG_WITHHOLD_STATES) && (blockIdx.x & 3u) == 1u ? 1 : 0));
       mbar_init(&x.ds_empty[i], GROUP_WARPS);
     }
     mbar_init(&x.drain, 1);

@@ -47,7 +47,7 @@ constexpr uint32_t AUX_AT = OUT_AT + GROUP_WARPS * OUT_BYTES;
 
 struct Aux {
   uint64_t x_full, y_full, z_full, x_empty, y_empty, z_empty;
-  uint64_t a_full, p_full, o_full, o_empty, s_full, s_empty, w_full, m_full, m_begun, drain[2], group[2];
+  uint64_t a_full, p_full, o_full, o_empty, s_full, s_empty, w_full[2], m_full, m_begun, w_empty[2], drain[2], group[2];
   float4 near[4];             // a 16-column block's decays to its nearest column
   float power[LT_CHUNK + 4];  // decay^n of the current item
   uint2 parts[LT_CHUNK];      // decay^n as a bf16 pair of the same, and what that lacks
@@ -291,12 +291,10 @@ __device__ void loader(const LinParams& p, const LtMaps& maps, uint8_t* sm, Aux&
     if (state && elect_one()) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(state), "n"(LIN_STATE * 4) : "memory");
     __syncwarp();
   }
-  // the copies in flight end before the CTA does (where all went well, their readers have seen to it)
-  if (!ok) {
-    if (ny) wait_a_second(&x.y_full, (ny - 1) & 1u);
-    if (nx) wait_a_second(&x.x_full, (nx - 1) & 1u);
-    if (nz) wait_a_second(&x.z_full, (nz - 1) & 1u);
-  }
+  // the copies in flight end before the CTA does, whichever warp's wait ran out
+  if (ny) wait_a_second(&x.y_full, (ny - 1) & 1u);
+  if (nx) wait_a_second(&x.x_full, (nx - 1) & 1u);
+  if (nz) wait_a_second(&x.z_full, (nz - 1) & 1u);
   __syncwarp();
 }
 
@@ -377,19 +375,32 @@ __device__ void output_issuer(const LinParams& p, uint8_t* sm, Aux& x, uint32_t 
   }
 }
 
-template <bool kLocal>
+// w y's parts have one place, or without outputs two by turns (x's tile and the image are
+// not needed there); each place's barriers have a phase a turn.
+template <bool kOutputs>
+__device__ __forceinline__ uint32_t place(uint32_t g) {
+  return kOutputs ? 0u : g & 1u;
+}
+template <bool kOutputs>
+__device__ __forceinline__ uint32_t turn(uint32_t g) {
+  return (kOutputs ? g : g >> 1) & 1u;
+}
+
+template <bool kOutputs, bool kLocal>
 __device__ void state_issuer(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
   uint32_t g = 0;
-  const uint32_t zb = smem_u32(sm + Z_AT), hb = smem_u32(sm + HI_AT), lb = smem_u32(sm + LO_AT);
+  const uint32_t zb = smem_u32(sm + Z_AT);
   Items<kLocal> items(p);
   for (Item it; items.next(p, it, false);) {
     for (int c = 0; c < it.chunks; ++c, ++g) {
       const uint32_t ph = g & 1u;
-      if (!warp_wait(&x.z_full, ph, x, p) || !warp_wait(&x.w_full, ph, x, p) || !warp_wait(&x.s_full, ph, x, p)) return;
+      const uint32_t wb = place<kOutputs>(g);
+      if (!warp_wait(&x.z_full, ph, x, p) || !warp_wait(&x.w_full[wb], turn<kOutputs>(g), x, p) || !warp_wait(&x.s_full, ph, x, p)) return;
       tc_fence_after();
       if (elect_one()) {
-        issue_wyz(tmem + TM_S, hb, lb, zb, (it.rows(c) + 15) >> 4);
+        issue_wyz(tmem + TM_S, smem_u32(sm + (wb ? X_AT : HI_AT)), smem_u32(sm + (wb ? S_AT : LO_AT)), zb, (it.rows(c) + 15) >> 4);
         mma_commit(&x.m_full);
+        mma_commit(&x.w_empty[wb]);
         mma_commit(&x.z_empty);
       }
       warp_arrive(&x.m_begun);
@@ -528,7 +539,8 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tm
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
   const int quarter = warp & 3, half = (warp - STATE_WARP0) >> 2, e_row = quarter * 32 + lane;  // a row of the state, 64 half .. of its columns
   const uint32_t St = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM_S + half * 64;
-  uint8_t* stage = sm + S_AT + half * HALF_TILE + quarter * 32 * 128;  // the warp's rows of the image
+  // the warp's rows of the image; without outputs a place of its own
+  uint8_t* stage = sm + (kOutputs ? S_AT + half * HALF_TILE + quarter * 32 * 128 : OUT_AT + (warp - STATE_WARP0) * OUT_BYTES);
   uint8_t* image = stage + lane * 128;
   uint32_t g = 0;
   Items<kLocal> items(p);
@@ -573,14 +585,20 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tm
     }
     tmem_st_wait();
     // chunk by chunk: the image of the state before it, and the decay over it; then
-    // the products add the chunk.  One turn more gives the end away.
+    // the products add the chunk.  One turn more gives the end away.  (Without outputs
+    // all decays reach to the end: the start's at once, a chunk's with w y.)
     for (int c = 0; c <= it.chunks; ++c) {
       const bool last = c == it.chunks;
       if (c > 0 && !warp_wait(&x.m_full, (g - 1) & 1u, x, p)) return;
       if (last && !to) break;
       if (kOutputs && !warp_wait(&x.s_empty, (g & 1u) ^ 1u, x, p)) return;
       tc_fence_after();
-      const float down = last ? up : decay_power(log2_decay, it.rows(c) - (c == 0 ? it.early : 0));
+      if (!kOutputs && c > 0 && !last) {
+        warp_arrive(&x.s_full);
+        ++g;
+        continue;
+      }
+      const float down = last ? up : decay_power(log2_decay, (kOutputs ? it.rows(c) : it.n) - (c == 0 ? it.early : 0));
 #pragma unroll 1
       for (int b = 0; b < 2; ++b) {
         uint32_t v[32];
@@ -627,7 +645,7 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tm
 }
 
 // -------------------------------------------------------------- w y's parts
-template <bool kLocal>
+template <bool kOutputs, bool kLocal>
 __device__ void parts_warps(const LinParams& p, uint8_t* sm, Aux& x) {
   constexpr int kThreads = 32 * PARTS_WARPS;
   const int tid = static_cast<int>(threadIdx.x) - 32 * PARTS_WARP0;
@@ -635,20 +653,23 @@ __device__ void parts_warps(const LinParams& p, uint8_t* sm, Aux& x) {
   Items<kLocal> items(p);
   for (Item it; items.next(p, it, false);) {
     if (it.chunks == 0) continue;
-    if (!group_sync(&x.group[1], meet, x, p)) return;
-    {
-      static_assert(kThreads == LT_CHUNK, "a decay a thread");
-      const float w = decay_power(log2f(__ldg(p.decay + it.h)), tid);
-      const uint32_t hi = pack_bf16x2(w, w);
-      const float rest = w - bf16_lo(hi);
-      x.parts[tid] = make_uint2(hi, pack_bf16x2(rest, rest));
-    }
-    if (!group_sync(&x.group[1], meet, x, p)) return;
+    static_assert(kThreads == LT_CHUNK, "a decay a thread");
+    const float log2_decay = log2f(__ldg(p.decay + it.h));
     for (int c = 0; c < it.chunks; ++c, ++g) {
       const uint32_t ph = g & 1u;
       const int rows = it.rows(c);
+      if (c == 0 || !kOutputs) {  // the decays: to the chunk's end, or to the scan's
+        if (!group_sync(&x.group[1], meet, x, p)) return;
+        const float w = decay_power(log2_decay, tid + (kOutputs ? 0 : it.n - c * LT_CHUNK - rows));
+        const uint32_t hi = pack_bf16x2(w, w);
+        const float rest = w - bf16_lo(hi);
+        x.parts[tid] = make_uint2(hi, pack_bf16x2(rest, rest));
+        if (!group_sync(&x.group[1], meet, x, p)) return;
+      }
       // (element-wise: any order of the tile's 16-byte pieces)
-      if (!warp_wait(&x.y_full, ph, x, p) || (g > 0 && !warp_wait(&x.m_full, ph ^ 1u, x, p))) return;
+      const uint32_t wb = place<kOutputs>(g);
+      if (!warp_wait(&x.y_full, ph, x, p) || !warp_wait(&x.w_empty[wb], turn<kOutputs>(g) ^ 1u, x, p)) return;
+      uint8_t *hi_to = sm + (wb ? X_AT : HI_AT), *lo_to = sm + (wb ? S_AT : LO_AT);
 #pragma unroll 1
       for (int k0 = 0; k0 < 16; k0 += 4) {
         uint4 v[4];
@@ -668,11 +689,13 @@ __device__ void parts_warps(const LinParams& p, uint8_t* sm, Aux& x) {
           decayed(v[k].y, w[k], hi.y, lo.y);
           decayed(v[k].z, w[k], hi.z, lo.z);
           decayed(v[k].w, w[k], hi.w, lo.w);
-          *reinterpret_cast<uint4*>(sm + HI_AT + e * 16) = hi;
-          *reinterpret_cast<uint4*>(sm + LO_AT + e * 16) = lo;
+          *reinterpret_cast<uint4*>(hi_to + e * 16) = hi;
+          *reinterpret_cast<uint4*>(lo_to + e * 16) = lo;
         }
       }
       if (rows < LT_CHUNK) {  // rows that are another user's, or none's: no value, whatever they hold
+        // (after the products of the chunk before, so that z_full is not a phase behind)
+        if (!kOutputs && g > 0 && !warp_wait(&x.w_empty[place<kOutputs>(g - 1)], turn<kOutputs>(g - 1), x, p)) return;
         if (!warp_wait(&x.z_full, ph, x, p)) return;
 #pragma unroll 1
         for (int k = 0; k < 16; ++k) {
@@ -683,7 +706,7 @@ __device__ void parts_warps(const LinParams& p, uint8_t* sm, Aux& x) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane_id() == 0) {
-        mbar_arrive(&x.w_full);
+        mbar_arrive(&x.w_full[wb]);
         mbar_arrive(&x.y_empty);
       }
     }
@@ -698,13 +721,15 @@ __global__ void __launch_bounds__(LT_THREADS, 1) lin_tile_kernel(const __grid_co
   Aux& x = *reinterpret_cast<Aux*>(sm + AUX_AT);
   const int warp = static_cast<int>(threadIdx.x >> 5);
   if (threadIdx.x == 0) {
-    uint64_t* once[] = {&x.x_full, &x.y_full, &x.z_full, &x.x_empty, &x.a_full, &x.o_full, &x.s_empty, &x.m_full, &x.m_begun, &x.drain[0], &x.drain[1]};
+    uint64_t* once[] = {&x.x_full, &x.y_full, &x.z_full, &x.x_empty, &x.a_full, &x.o_full, &x.s_empty, &x.m_full, &x.m_begun, &x.w_empty[0], &x.w_empty[1], &x.drain[0], &x.drain[1]};
     for (uint64_t* b : once) mbar_init(b, 1);
     mbar_init(&x.y_empty, PARTS_WARPS + (kOutputs ? 1 : 0));
     mbar_init(&x.z_empty, kOutputs ? 2 : 1);
     uint64_t* warps[] = {&x.p_full, &x.o_empty, &x.s_full, &x.group[0]};
     for (uint64_t* b : warps) mbar_init(b, GROUP_WARPS);
-    mbar_init(&x.w_full, PARTS_WARPS);
+    const int withheld = (p.debug & DEBUG_WITHHOLD_STATES) && (blockIdx.x & 3u) == 1u ? 1 : 0;
+    mbar_init(&x.w_full[0], PARTS_WARPS + withheld);
+    mbar_init(&x.w_full[1], PARTS_WARPS + withheld);
     mbar_init(&x.group[1], PARTS_WARPS);
     x.abort = 0;
     fence_barrier_init();
@@ -722,7 +747,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) lin_tile_kernel(const __grid_co
   if (warp < DECAY_WARP0) {
     if (warp == 0) loader<kOutputs, kLocal>(p, maps, sm, x);
     if (warp == 1 && kOutputs) output_issuer<kLocal>(p, sm, x, tmem);
-    if (warp == 2) state_issuer<kLocal>(p, sm, x, tmem);
+    if (warp == 2) state_issuer<kOutputs, kLocal>(p, sm, x, tmem);
     if (warp == 1 || warp == 2) drain(&x.drain[warp - 1]);
   } else if (warp < OUT_WARP0) {
     if (kOutputs) decay_warps<kLocal>(p, x, tmem);
@@ -731,7 +756,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) lin_tile_kernel(const __grid_co
   } else if (warp < PARTS_WARP0) {
     state_warps<kOutputs, kLocal>(p, sm, x, tmem);
   } else {
-    parts_warps<kLocal>(p, sm, x);
+    parts_warps<kOutputs, kLocal>(p, sm, x);
   }
   tc_fence_before();
   __syncthreads();

@@ -608,8 +608,9 @@ ikbo_status_t ikbo_plan_get_status(ikbo_plan_t p, cudaStream_t stream);
  * where a cooperative launch is refused; bit 2 = in the cache attention's
  * launches in tiles every fourth CTA never hands its keys to the products (which
  * wait for them, and the call ends with IKBO_ERR_TIMEOUT and an O that is not
- * defined).  The timeout bounds every wait
- * inside the kernels (default 2 s). */
+ * defined); bit 3 = the same in linear attention's launches in tiles and the
+ * candidates' reads, with what states are made of and their images.  The timeout
+ * bounds every wait inside the kernels (default 2 s). */
 ikbo_status_t ikbo_plan_set_debug(ikbo_plan_t p, unsigned flags);
 ikbo_status_t ikbo_plan_set_timeout_ns(ikbo_plan_t p, uint64_t timeout_ns);
 

@@ -193,6 +193,29 @@ def test_histories_in_segments(lens, H):
         assert p.status() == B.IKBO_OK
 
 
+def test_again_and_again():
+    """The tile kernel's warps hand over to each other differently every time; results and status do not."""
+    d = Data(17, [3000, 130, 700], 2, decay=[0.995, 0.9])
+    with plan() as p:
+        O, S = run_forward(p, d)
+        Q, K, V, decay, off = d.cuda()
+        dO, s_in, ds_out = bf(d.dO), f32(d.S), f32(d.dS)
+        O2, S2, S3 = torch.empty_like(O), torch.empty_like(S), torch.empty_like(S)
+        g = [torch.empty_like(Q) for _ in range(3)]
+        p.linattn_backward(Q, K, V, dO, decay, *g, state_in=s_in, d_state_out=ds_out, d_state_in=S3, offsets=off)
+        first = [t.clone() for t in (*g, S3)]
+        _, alone = run_forward(p, d, queries=False)
+        wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+        for _ in range(300):
+            p.linattn_forward(Q, K, V, decay, O2, state_in=s_in, state_out=S2, offsets=off)
+            p.linattn_forward(None, K, V, decay, None, state_in=s_in, state_out=S3, offsets=off)
+            wrong += (O2 != O).sum() + (S2 != S).sum() + (S3 != alone).sum()
+            p.linattn_backward(Q, K, V, dO, decay, *g, state_in=s_in, d_state_out=ds_out, d_state_in=S3, offsets=off)
+            for a, b in zip((*g, S3), first):
+                wrong += (a != b).sum()
+        assert p.status() == B.IKBO_OK and int(wrong) == 0
+
+
 def test_events_one_by_one_are_the_whole():
     """A history taken in at once, in pieces, and token by token ends in the same state."""
     d = Data(5, [150], 3)
@@ -286,6 +309,36 @@ def test_captured_and_on_another_stream():
                 p.linattn_forward(Q, K, V, decay, O2, state_in=s_in, state_out=S2, offsets=off)
 
 
+def test_a_wait_that_runs_out_is_reported_and_passes():
+    """Every fourth CTA of the tile kernels waits for what never comes: the calls end, say so, and leave nothing behind."""
+    d = Data(18, [700, 150, 30], 3, decay=[0.99, 0.9, 1.0])
+    rng = np.random.default_rng(18)
+    m = np.sort(rng.integers(0, 3, 200)).astype(np.int32)
+    X, dO = bf16(rng.standard_normal((200, 3, 16, D))), bf16(rng.standard_normal((200, 3, 16, D)))
+    with plan() as p:
+        mm = i32(m)
+        p.plan(mm, 3, 3, 16)
+        O, S = run_forward(p, d)
+        dX, dS, dS2 = torch.empty_like(bf(X)), torch.empty_like(S), torch.empty_like(S)
+        p.linattn_read_backward(bf(X), S, bf(dO), dX, dS)
+        assert p.status() == B.IKBO_OK
+        for _ in range(3):
+            B.ikbo_plan_set_timeout_ns(p.handle, 20_000_000)
+            B.ikbo_plan_set_debug(p.handle, B.DEBUG_WITHHOLD_STATES)
+            run_forward(p, d)
+            assert p.status() == B.IKBO_ERR_TIMEOUT
+            run_forward(p, d, queries=False)
+            assert p.status() == B.IKBO_ERR_TIMEOUT
+            p.linattn_read_backward(bf(X), S, bf(dO), dX, dS2)
+            assert p.status() == B.IKBO_ERR_TIMEOUT
+            B.ikbo_plan_set_timeout_ns(p.handle, 2_000_000_000)
+            B.ikbo_plan_set_debug(p.handle, 0)
+            O2, S2 = run_forward(p, d)
+            p.linattn_read_backward(bf(X), S, bf(dO), dX, dS2)
+            assert p.status() == B.IKBO_OK
+            assert torch.equal(O2, O) and torch.equal(S2, S) and torch.equal(dS2, dS)
+
+
 def test_many_users_of_a_few_rows():
     rng = np.random.default_rng(1)
     lens = rng.integers(0, 4, 400)
@@ -311,6 +364,8 @@ def test_more_histories_than_sms():
         O, S = run_forward(p, d, max_len=400)
         near(O, ref)
         near_state(S, last, R.weights(d.K, d.V, d.decay, d.off, d.S))
+        _, S2 = run_forward(p, d, queries=False, max_len=400)
+        near_state(S2, last, R.weights(d.K, d.V, d.decay, d.off, d.S))
         Q, K, V, decay, off = d.cuda()
         outs, dS = [torch.empty_like(Q) for _ in range(3)], torch.empty_like(S)
         p.linattn_backward(Q, K, V, bf(d.dO), decay, *outs, state_in=f32(d.S), d_state_out=f32(d.dS), d_state_in=dS, offsets=off,
