@@ -710,7 +710,7 @@ def ikbo_linattn_forward(plan: int, Q: Optional[torch.Tensor], K: torch.Tensor, 
     O_t = scale q_t S_t, over each user's rows of Q, K, V, O [rows, H, 128] (rows may be strided)
     from state_in to state_out [n_users, H, 128, 128] (fp32; either may be None, or the same).
     offsets [n_users + 1]: the users' rows; None: equally many each.  Q and O None: the states alone.
-    max_len: a bound on a user's rows (0: all)."""
+    max_len: a bound on a user's rows (0: none known; the variant then goes by four times the average)."""
     dev, shape = _current_device(K, "K"), K.shape
     if len(shape) != 3:
         raise ValueError("K must be [rows, H, d]")

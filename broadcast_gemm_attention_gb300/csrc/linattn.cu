@@ -59,9 +59,8 @@ struct LinShared {
   float power[LIN_CHUNK + 1];  // decay^n
 };
 
-// kOutputs: with queries; else the states alone.  kLocal: a segment's own part
-// of its end state, from zero, to the workspace.
-template <bool kOutputs, bool kLocal>
+// kOutputs: with queries; else the states alone.
+template <bool kOutputs>
 __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kernel(const __grid_constant__ LinParams p) {
   extern __shared__ __align__(128) uint8_t lin_sm[];
   __shared__ LinShared sh;
@@ -69,22 +68,17 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
   constexpr int kStage = kTiles * LIN_TILE;
   const uint32_t base = smem_u32(lin_sm), probs = base + LIN_STAGES * kStage;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int item = static_cast<int>(blockIdx.x) / p.segs, seg = static_cast<int>(blockIdx.x) - item * p.segs;
-  const int u = item / p.H, h = item - u * p.H;
+  const int u = static_cast<int>(blockIdx.x) / p.H, h = static_cast<int>(blockIdx.x) - u * p.H;
   const LinJob& job = p.job[blockIdx.y];
 
   int first_row;
-  const int len = lin_rows(p, u, first_row);
-  const int segs = p.segs > 1 ? max(1, (len + p.seg_len - 1) / p.seg_len) : 1;
-  if (seg >= segs || (kLocal && seg + 1 >= segs)) return;
-  const int r0 = seg * (p.segs > 1 ? p.seg_len : 0);                    // of the scan's order
-  const int n = segs > 1 ? min(p.seg_len, len - r0) : len;
+  const int n = lin_rows(p, u, first_row);
   const float log2_decay = log2f(__ldg(p.decay + h));
   if (tid <= LIN_CHUNK) sh.power[tid] = lin_power(log2_decay, tid);
 
-  // rows r0 .. r0 + n - 1 of the scan's order, as rows of the tensors
+  // the scan's order as rows of the tensors
   const int64_t dir = job.reverse ? -1 : 1;
-  const int64_t row_at = static_cast<int64_t>(first_row) + (job.reverse ? len - 1 - r0 : r0);
+  const int64_t row_at = static_cast<int64_t>(first_row) + (job.reverse ? n - 1 : 0);
   const auto load_tile = [&](const uint16_t* src, int64_t stride, uint32_t dst, int c0) {
 #pragma unroll
     for (int k = 0; k < LIN_TILE / 16 / LIN_THREADS; ++k) {
@@ -106,15 +100,10 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
   // the state, turned: row m of s[i] is z's element 16 warp + m, columns y's 8 i ..
   float s[16][4];
   const int64_t state = (static_cast<int64_t>(u) * p.H + h) * LIN_STATE;
-  const int64_t ws = ((static_cast<int64_t>(blockIdx.y) * p.n_users + u) * p.H + h) * p.segs;
-  const float* from = nullptr;
-  if (!kLocal) {  // of several segments the first one's start is in the workspace too, as s_out may be s_in
-    if (segs > 1) from = p.ws + (ws + (seg > 0 ? seg - 1 : segs - 1)) * LIN_STATE;
-    else if (job.s_in) from = job.s_in + state;
-  }
-  const float factor = segs > 1 ? 1.f : job.s_in_factor;
+  const float* from = job.s_in ? job.s_in + state : nullptr;
+  const float factor = job.s_in_factor;
   const int e0 = 16 * warp + g;
-  if (from && (segs > 1 || !job.s_in_turned)) {
+  if (from && !job.s_in_turned) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -135,7 +124,7 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
       for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
   }
   // a reverse scan's start is taken as it is by its first row
-  int early = !kLocal && seg == 0 && job.reverse ? 1 : 0;
+  int early = job.reverse ? 1 : 0;
 
 #pragma unroll 1
   for (int ch = 0; ch < chunks; ++ch) {
@@ -255,10 +244,9 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
     __syncthreads();  // the stage is loaded again
   }
 
-  float* to = kLocal ? p.ws + (ws + seg) * LIN_STATE : (seg + 1 == segs && job.s_out ? job.s_out + state : nullptr);
+  float* to = job.s_out ? job.s_out + state : nullptr;
   if (!to) return;
-  float up = 1.f;
-  if (!kLocal) up = len > 0 && job.reverse ? job.s_out_factor * sh.power[1] : job.s_out_factor;
+  const float up = n > 0 && job.reverse ? job.s_out_factor * sh.power[1] : job.s_out_factor;
 #pragma unroll
   for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -369,13 +357,14 @@ __global__ void __launch_bounds__(LIN_THREADS) lin_step_kernel(const __grid_cons
   for (int k = 0; k < 16; ++k) reinterpret_cast<float4*>(to)[(16 * warp + k) * 32 + lane] = s[k];
 }
 
-template <bool kOutputs, bool kLocal>
+template <bool kOutputs>
 cudaError_t launch_chunks(const LinParams& p, cudaStream_t s) {
   constexpr int smem = LIN_STAGES * (kOutputs ? 3 : 2) * LIN_TILE + (kOutputs ? LIN_CHUNK * LIN_CHUNK * 2 : 0);
-  const cudaError_t e = cudaFuncSetAttribute(lin_chunk_kernel<kOutputs, kLocal>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(lin_chunk_kernel<kOutputs>, smem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(p.segs * p.n_users * p.H), static_cast<unsigned>(p.n_jobs));
-  lin_chunk_kernel<kOutputs, kLocal><<<grid, LIN_THREADS, smem, s>>>(p);
+  const dim3 grid(static_cast<unsigned>(p.n_users * p.H), static_cast<unsigned>(p.n_jobs));
+  lin_chunk_kernel<kOutputs><<<grid, LIN_THREADS, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -396,7 +385,7 @@ cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int*
     return cudaGetLastError();
   }
   if (p.segs > 1) {
-    e = p.tiles ? launch_lin_tiles(p, true, num_sms, s) : launch_chunks<false, true>(p, s);
+    e = launch_lin_tiles(p, true, num_sms, s);
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>(LIN_STATE / 256 * p.n_users * p.H), static_cast<unsigned>(p.n_jobs));
     lin_join_kernel<<<grid, 256, 0, s>>>(p);
@@ -405,7 +394,7 @@ cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int*
     *launches += 2;
   }
   if (p.tiles) e = launch_lin_tiles(p, false, num_sms, s);
-  else e = outputs ? launch_chunks<true, false>(p, s) : launch_chunks<false, false>(p, s);
+  else e = outputs ? launch_chunks<true>(p, s) : launch_chunks<false>(p, s);
   *launches += e == cudaSuccess;
   return e;
 }

@@ -46,6 +46,8 @@ ikbo_status_t lin_params(ikbo_plan_t p, const int32_t* d_offsets, int n_users, i
   lp->n_rows = n_rows;
   lp->H = H;
   lp->max_len = d_offsets ? (max_len > 0 ? std::min(max_len, n_rows) : n_rows) : n_rows / n_users;
+  const int64_t each = (static_cast<int64_t>(n_rows) + n_users - 1) / n_users;
+  lp->likely_len = !d_offsets || max_len > 0 ? lp->max_len : static_cast<int>(std::min<int64_t>(lp->max_len, 4 * each));
   lp->scale = scale;
   lp->segs = 1;
   lp->debug = p->debug;
@@ -58,11 +60,13 @@ ikbo_status_t lin_params(ikbo_plan_t p, const int32_t* d_offsets, int n_users, i
 // (and multiplied) once more, for the states between them.  With fewer scans than
 // half the SMs, segments are as long as makes one for each SM; else only rows far
 // above a CTA's share are cut, as where one user's history is much longer than the
-// others'.  At most LIN_MOST_STATES states lie between segments.
+// others'.  At most LIN_MOST_STATES states lie between segments, and with more than
+// LIN_MOST_CUT users none is cut (each item looks for its place among all users').
 constexpr int64_t LIN_MOST_STATES = 16384;  // 1 GiB
 constexpr int LIN_LEAST_SEGMENT = 256;
+constexpr int LIN_MOST_CUT = 256;
 
-// The variant, from the bound on a user's rows.  Measured, 8 heads (us):
+// The variant, from the bound on a user's rows (every variant takes any length).  Measured, 8 heads (us):
 //   forward, rows           15 users:  4     8    16    32    64   128   192   256   100 users: 8    16   128   256
 //   row by row                       4.4   5.8   8.3  13.7                                   29.0  40.6
 //   chunks, in registers                   6.9   7.0   7.7   9.2  13.5  17.8  22.2           41.7  42.7  83.8 135.5
@@ -77,19 +81,19 @@ void cut_segments(LinParams* lp, int num_sms) {
   // (each scan's last segment is a part of one: as many SMs are left out of the division)
   int64_t seg = std::max<int64_t>(items * 2 <= num_sms ? (rows + num_sms - items - 1) / (num_sms - items) : 4 * (rows / num_sms), LIN_LEAST_SEGMENT);
   const int64_t most = LIN_MOST_STATES / items;  // segments of a user
-  if (most < 2) return;
+  if (most < 2 || lp->n_users > LIN_MOST_CUT) return;
   seg = std::max(seg, (lp->max_len + most - 1) / most);
   seg = (seg + 127) / 128 * 128;
-  if (lp->max_len <= seg + seg / 2) return;
+  if (lp->likely_len <= seg + seg / 2) return;
   lp->seg_len = static_cast<int>(seg);
   lp->segs = static_cast<int>((lp->max_len + seg - 1) / seg);
 }
 
 ikbo_status_t lin_run(ikbo_plan_t p, LinParams* lp, cudaStream_t stream) {
-  if (static_cast<int64_t>(lp->n_users) * lp->H > INT32_LIMIT / 256) return IKBO_ERR_UNSUPPORTED;
+  if (lin_tile_smem() > p->max_smem) return IKBO_ERR_UNSUPPORTED;
   if (!lp->steps) {
-    cut_segments(lp, p->num_sms);
-    lp->tiles = lp->max_len >= LIN_TILES_FROM[lp->backward ? 2 : (lp->job[0].x ? 0 : 1)] && lin_tile_smem() <= p->max_smem;
+    lp->tiles = lp->likely_len >= LIN_TILES_FROM[lp->backward ? 2 : (lp->job[0].x ? 0 : 1)];
+    if (lp->tiles) cut_segments(lp, p->num_sms);
   }
   if (lp->segs > 1) {
     bool capturing = false;
@@ -166,7 +170,7 @@ ikbo_status_t ikbo_linattn_forward(ikbo_plan_t p, const void* Q, const void* K, 
   j.s_out = state_out;
   j.s_in_factor = j.s_out_factor = 1.f;
   lp.n_jobs = 1;
-  lp.steps = lp.max_len <= LIN_STEP_MOST;
+  lp.steps = lp.likely_len <= LIN_STEP_MOST;
   return lin_run(p, &lp, stream);
 }
 

@@ -2,6 +2,10 @@
 // (linattn.cu) and of the candidates' reads of its states (linread.cu).  Not
 // part of the public ABI.
 #pragma once
+#include <cuda_runtime.h>
+
+#include <atomic>
+
 #include "ikbo_internal.h"
 
 namespace ikbo {
@@ -35,6 +39,7 @@ struct LinParams {
   uint32_t* status;
   float* ws;               // states between segments [job][u][h][segs], at a segment's end
   int n_jobs, n_users, n_rows, H, max_len;
+  int likely_len;          // what variants are chosen by: max_len, or without a bound four times the average
   int seg_len, segs;       // rows of a segment (a multiple of the chunk), segments of the longest user; 1: no segments
   int backward;            // the jobs are a gradient's (variants do not go by which of them are asked for)
   int steps;               // rows one by one (a forward scan alone)
@@ -43,6 +48,20 @@ struct LinParams {
   uint64_t timeout_ns;
   float scale;
 };
+
+// Lets a kernel use `bytes` of dynamic shared memory, once on each device (asking each
+// time took half a microsecond of a call).  `done` is the kernel's own.
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 struct LinReadParams {
   const uint16_t* x;        // rows [n_cand][H][Lq][128]

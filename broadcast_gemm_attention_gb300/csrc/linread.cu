@@ -426,7 +426,8 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
 
 template <bool kBack>
 cudaError_t launch(const LinReadParams& p, const CUtensorMap& mx, const CUtensorMap& mq, int num_sms, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(lin_read_kernel<kBack>, cudaFuncAttributeMaxDynamicSharedMemorySize, RT_SMEM);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(lin_read_kernel<kBack>, RT_SMEM, done);
   if (e != cudaSuccess) return e;
   lin_read_kernel<kBack><<<static_cast<unsigned>(lin_read_ctas(num_sms)), RT_THREADS, RT_SMEM, s>>>(p, mx, mq);
   return cudaGetLastError();

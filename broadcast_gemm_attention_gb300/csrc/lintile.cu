@@ -769,7 +769,8 @@ __global__ void __launch_bounds__(LT_THREADS, 1) lin_tile_kernel(const __grid_co
 
 template <bool kOutputs, bool kLocal>
 cudaError_t launch(const LinParams& p, const LtMaps& maps, int num_sms, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(lin_tile_kernel<kOutputs, kLocal>, cudaFuncAttributeMaxDynamicSharedMemorySize, LT_SMEM);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(lin_tile_kernel<kOutputs, kLocal>, LT_SMEM, done);
   if (e != cudaSuccess) return e;
   // (segments of all users: no more than their rows hold, and one each)
   const int64_t segs = p.segs > 1 ? p.n_rows / p.seg_len + static_cast<int64_t>(p.n_users) : p.n_users;

@@ -542,22 +542,25 @@ ikbo_status_t ikbo_attn_qcache_tree_forward(ikbo_plan_t p, const void* Q, const 
  *   d_offsets   int32 [n_users + 1]: user u's rows are d_offsets[u] ..
  *               d_offsets[u + 1] - 1, ascending, within [0, n_rows]; rows that
  *               belong to no user are left alone.  NULL: n_rows / n_users each.
- *   max_len     a bound on a user's rows (0: n_rows); the variant and the
- *               workspace go by it.  A user with more rows, or with offsets out
- *               of range, is taken for one without rows and reported
- *               (IKBO_ERR_CACHE).
+ *   max_len     a bound on a user's rows; the variant and the workspace go by it.
+ *               0: no bound is known (then they go by four times the average).  A
+ *               user with more rows, or with offsets out of range, is taken for one
+ *               without rows and reported (IKBO_ERR_CACHE).
  *   decay       fp32 [H], each in [0, 1]
  *   state_in    fp32 [n_users][H][128][128] (k's elements by v's), or NULL: zero
  *   state_out   the same, or NULL (then O is given); may be state_in
  * n_users <= 8192, H <= 1024, d == 128; scale > 0, and so that 1 / scale is
- * finite; no plan() is needed.  States are held in fp32.  With up to 4 rows a
- * user (max_len) they are taken one by one, in fp32.  Else in chunks of 64 on the
- * tensor cores: decayed values in two bf16 parts (2^-17) for the state, the
- * products q_i.k_j with their decays and, for O, the state rounded to bf16 (2^-9
- * each), fp32 sums.  A row that holds an infinity or NaN makes its user's O of
- * that head undefined from 63 rows before it.  O must not overlap inputs.  Histories far longer than a CTA's share
- * are cut into segments (two launches more, and a workspace of the plan's, as
- * described at ikbo_attn_qcache_forward).  Results repeat bit for bit. */
+ * finite; no ikbo_plan is needed.  States are held in fp32.  Any variant takes any
+ * length; up to 8 rows a user they are taken one by one, in fp32, else in chunks of
+ * 64 or (from 129 rows, the states alone from 257) 128 on the tensor cores: decayed
+ * keys or values in two bf16 parts (2^-16) for the state, the products q_i.k_j with
+ * their decays and, for O, the state rounded to bf16 (2^-8 each), fp32 sums.  A row
+ * that holds an infinity or NaN makes its user's O of that head undefined from 127 rows
+ * before it on; other users' are not touched.  O must not overlap inputs.  Histories far
+ * longer than a CTA's share are cut into segments (two launches more, and a workspace of
+ * the plan's of up to 1 GiB, as described at ikbo_attn_qcache_forward).  Results repeat
+ * bit for bit.  Of a call in which a bounded wait ran out (IKBO_ERR_TIMEOUT) the outputs
+ * are not defined; the calls after it are not touched by that. */
 ikbo_status_t ikbo_linattn_forward(ikbo_plan_t p, const void* Q, const void* K, const void* V, const int64_t* row_strides,
                                    const int32_t* d_offsets, int n_users, int n_rows, int max_len, int H, int d,
                                    const float* decay, const float* state_in, float* state_out, void* O, float scale,
@@ -570,7 +573,8 @@ ikbo_status_t ikbo_linattn_forward(ikbo_plan_t p, const void* Q, const void* K, 
  * Only inputs are read: the states are formed again from state_in.  dQ, dK, dV
  * bf16, d_state_in fp32, overwritten; any may be NULL, and none may overlap an
  * input.  row_strides: 7 values, of Q, K, V, dO, dQ, dK, dV.  The decays are
- * constants.  Else as above. */
+ * constants.  Chunks of 128 from 65 rows; a gradient does not depend on which others
+ * are asked for.  Else as above. */
 ikbo_status_t ikbo_linattn_backward(ikbo_plan_t p, const void* Q, const void* K, const void* V, const void* dO,
                                     const int64_t* row_strides, const int32_t* d_offsets, int n_users, int n_rows,
                                     int max_len, int H, int d, const float* decay, const float* state_in,

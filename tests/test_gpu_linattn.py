@@ -257,6 +257,50 @@ def test_slices_of_a_projection_and_dense_rows():
             p.linattn_forward(Q, K, V, decay, plain, n_users=4)  # 210 rows are not four times as many
 
 
+def test_no_rows_at_all():
+    """Empty tensors: the states pass through, and nothing is asked of the rows' addresses."""
+    S = torch.randn((3, 2, D, D), device="cuda")
+    none = torch.empty((0, 2, D), dtype=torch.bfloat16, device="cuda")
+    decay = f32([0.9, 1.0])
+    with plan() as p:
+        for off in (i32([0, 0, 0, 0]), None):
+            out = torch.full_like(S, float("nan"))
+            p.linattn_forward(none, none, none, decay, none, state_in=S, state_out=out, offsets=off)
+            assert torch.equal(out, S)
+            out.fill_(float("nan"))
+            p.linattn_forward(None, none, none, decay, None, state_out=out, offsets=off, n_users=3)
+            assert not out.any()
+            out.fill_(float("nan"))
+            p.linattn_backward(none, none, none, none, decay, none, none, none, state_in=S, d_state_out=S, d_state_in=out, offsets=off)
+            near_state(out, host(S), np.abs(host(S)))
+        assert p.status() == B.IKBO_OK
+
+
+@pytest.mark.parametrize("max_len", [0, 300])
+def test_another_user_s_infinities_stay_there(max_len):
+    """Rows beside a user's own, behind its last in the same tile, hold infinities and NaN."""
+    lens = [100, 40, 131, 60]
+    d = Data(19, lens, 2, spare=40)
+    own = np.r_[0:100, 140:271]                  # the first and the third user's rows
+    ref = {}
+    with plan() as p:
+        for bad in (False, True):
+            if bad:
+                for x in (d.Q, d.K, d.V, d.dO):
+                    x[100:140:3] = np.inf
+                    x[101:140:3] = np.nan
+                    x[271:] = np.nan
+            O, S = run_forward(p, d, max_len=max_len)
+            Q, K, V, decay, off = d.cuda()
+            outs, dS = [torch.empty_like(Q) for _ in range(3)], torch.empty_like(S)
+            p.linattn_backward(Q, K, V, bf(d.dO), decay, *outs, state_in=f32(d.S), d_state_out=f32(d.dS), d_state_in=dS, offsets=off,
+                               max_len=max_len)
+            got = [t[own].clone() for t in (O, *outs)] + [S[[0, 2]], dS[[0, 2]]]
+            if bad:
+                assert all(torch.equal(a, b) for a, b in zip(ref["is"], got))
+            ref["is"] = got
+
+
 def test_bad_offsets_are_reported_and_skipped():
     d = Data(9, [10, 10, 10], 2)
     ref, last = R.forward(d.Q, d.K, d.V, d.decay, d.off, d.S, SCALE)
