@@ -27,7 +27,6 @@ enum : uint32_t {
   DEBUG_WITHHOLD_USER_PARTIAL = 1u << 0,  // LCE: never publish user partials
   DEBUG_NO_COOPERATIVE = 1u << 1,         // LCE backward: the candidate pass and its finish as two launches
   DEBUG_WITHHOLD_KEYS = 1u << 2,          // cache attention in tiles: some CTAs' keys are never handed over
-  DEBUG_WITHHOLD_STATES = 1u << 3,        // linear attention in tiles: the same with what states are made of, or read by
 };
 
 // ------------------------------------------------------------ segments

@@ -10,6 +10,10 @@
 
 namespace ikbo {
 
+// A debug switch (ikbo_plan_set_debug), beside those of ikbo_internal.h: some CTAs of the
+// tile kernels never hand over what states are made of, or read by.
+constexpr uint32_t DEBUG_WITHHOLD_STATES = 1u << 3;
+
 constexpr int LIN_D = 128;                    // head dimension of queries, keys and values
 constexpr int LIN_STATE = LIN_D * LIN_D;      // floats of a state
 constexpr int LIN_MAX_JOBS = 3;
