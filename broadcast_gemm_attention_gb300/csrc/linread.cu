@@ -13,7 +13,10 @@
 //   dQ = dO S^T   with the same image as a K-major B,
 //   dS += Q^T dO  (backward) into tensor memory over all of a run of units of one
 //                 (user, head), both operands MN-major: rows are the inner dimension.
-// One pass over the rows serves both gradients.  Bound: memory.
+// One pass over the rows serves both gradients.  Bound: memory, and each CTA's start.
+// 1024 candidates of 15 users, 8 heads x 32 rows: 27.5 us, 5.1 TB/s, 5 us of it start
+// (16x8x16 products in registers: 82); the gradient of 1024 candidates of 64 users
+// unevenly, 8 heads x 16 rows: 46.5 us, 3.6 TB/s (138), 6 of it the parts' adding.
 //
 // Per CTA (persistent, one per SM, an equal run of the list, 20 warps):
 //   warp 0       loads; warp 1 issues

@@ -20,8 +20,17 @@
 //   warps 28-31  the two parts of w y
 // The groups' work is bound by latencies (loads of tensor memory, barriers, a few
 // dozen dependent instructions), so each has warps of its own.
-// Each tile has one buffer: y is free once w y and A are formed, x after O1, z after
-// O2 and M, so that a chunk's loads lie beside the products of the one before.
+// y and z have one buffer each, free once w y and A are formed, and after O2 and S's
+// products, so that a chunk's loads lie beside the products of the one before.  x has two:
+// the outputs leave by way of the one whose products have ended (54.2 us with a place of
+// their own, 53.7 so; two buffers for z instead of x 55.0).
+//
+// Bound: shared memory, 576 KB a chunk, 4500 of the 4950 cycles that a chunk takes
+// (products 288, parts 96, image 32, outputs 64, loads 96).  15 histories of 1200 to
+// 2048 rows, 8 heads, bf16: 53.7 us, 14 of them start and end, 3.7 TB/s of the tensors'
+// bytes, 0.36 of the tensor pipe's cycles; with 16x8x16 products in registers
+// (linattn.cu) 142 us.  Their gradient at 524 to 1024 rows: 75.7 us (178).
+//
 // A reverse scan keeps the rows' order in its tiles and turns masks and decays around
 // instead (row j reaches i <= j, and the chunk's first row is its end).
 #include <cuda.h>
@@ -41,12 +50,13 @@ constexpr int GROUP_WARPS = 8, PARTS_WARPS = 4;
 constexpr uint32_t TM_A = 0, TM_O1 = 128, TM_O2 = 256, TM_S = 384;
 
 constexpr uint32_t TILE = 2 * HALF_TILE;  // 32 KB
-constexpr uint32_t X_AT = 0, Y_AT = TILE, Z_AT = 2 * TILE, HI_AT = 3 * TILE, LO_AT = 4 * TILE, S_AT = 5 * TILE, OUT_AT = 6 * TILE;
-constexpr uint32_t OUT_BYTES = 32 * 128;  // of the outputs, per warp
-constexpr uint32_t AUX_AT = OUT_AT + GROUP_WARPS * OUT_BYTES;
+constexpr uint32_t X_AT = 0, Y_AT = TILE, Z_AT = 2 * TILE, HI_AT = 3 * TILE, LO_AT = 4 * TILE, S_AT = 5 * TILE, X1_AT = 6 * TILE;
+constexpr uint32_t OUT_BYTES = 32 * 128;  // of a tile, per warp of a group
+static_assert(GROUP_WARPS * OUT_BYTES == TILE, "the outputs take x's place");
+constexpr uint32_t AUX_AT = 7 * TILE;
 
 struct Aux {
-  uint64_t x_full, y_full, z_full, x_empty, y_empty, z_empty;
+  uint64_t x_full[2], y_full, z_full, x_empty[2], y_empty, z_empty;
   uint64_t a_full, p_full, o_full, o_empty, s_full, s_empty, w_full[2], m_full, m_begun, w_empty[2], drain[2], group[2];
   float4 near[4];             // a 16-column block's decays to its nearest column
   float power[LT_CHUNK + 4];  // decay^n of the current item
@@ -265,9 +275,9 @@ __device__ void loader(const LinParams& p, const LtMaps& maps, uint8_t* sm, Aux&
       load(Y_AT, &maps.y[it.job], &x.y_full, it.h, row);
       ++ny;
       if (kOutputs) {
-        ok = warp_wait(&x.x_empty, free, x, p);
+        ok = warp_wait(&x.x_empty[g & 1u], ((g >> 1) & 1u) ^ 1u, x, p);
         if (!ok) break;
-        load(X_AT, &maps.x[it.job], &x.x_full, it.h, row);
+        load(g & 1u ? X1_AT : X_AT, &maps.x[it.job], &x.x_full[g & 1u], it.h, row);
         ++nx;
       }
       ok = warp_wait(&x.z_empty, free, x, p);
@@ -293,7 +303,7 @@ __device__ void loader(const LinParams& p, const LtMaps& maps, uint8_t* sm, Aux&
   }
   // the copies in flight end before the CTA does, whichever warp's wait ran out
   if (ny) wait_a_second(&x.y_full, (ny - 1) & 1u);
-  if (nx) wait_a_second(&x.x_full, (nx - 1) & 1u);
+  for (uint32_t k = nx > 2 ? nx - 2 : 0; k < nx; ++k) wait_a_second(&x.x_full[k & 1u], (k >> 1) & 1u);
   if (nz) wait_a_second(&x.z_full, (nz - 1) & 1u);
   __syncwarp();
 }
@@ -337,12 +347,13 @@ __device__ __forceinline__ void issue_wyz(uint32_t m_tmem, uint32_t hi_base, uin
 template <bool kLocal>
 __device__ void output_issuer(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
   uint32_t g = 0;
-  const uint32_t xb = smem_u32(sm + X_AT), yb = smem_u32(sm + Y_AT), zb = smem_u32(sm + Z_AT), sb = smem_u32(sm + S_AT);
+  const uint32_t xbs[2] = {smem_u32(sm + X_AT), smem_u32(sm + X1_AT)}, yb = smem_u32(sm + Y_AT), zb = smem_u32(sm + Z_AT), sb = smem_u32(sm + S_AT);
   Items<kLocal> items(p);
   for (Item it; items.next(p, it, false);) {
     for (int c = 0; c < it.chunks; ++c, ++g) {
       const uint32_t ph = g & 1u;
-      if (!warp_wait(&x.y_full, ph, x, p) || !warp_wait(&x.x_full, ph, x, p)) return;
+      const uint32_t xb = g & 1u ? xbs[1] : xbs[0];
+      if (!warp_wait(&x.y_full, ph, x, p) || !warp_wait(&x.x_full[g & 1u], (g >> 1) & 1u, x, p)) return;
       // (A's place is free: O2 of the chunk before has ended)
       if (g > 0 && !warp_wait(&x.o_full, ph ^ 1u, x, p)) return;
       tc_fence_after();
@@ -357,7 +368,6 @@ __device__ void output_issuer(const LinParams& p, uint8_t* sm, Aux& x, uint32_t 
       tc_fence_after();
       if (elect_one()) {
         issue_xs(tmem + TM_O1, xb, sb);
-        mma_commit(&x.x_empty);
         mma_commit(&x.s_empty);
       }
       __syncwarp();
@@ -486,7 +496,6 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t t
   const int quarter = warp & 3, half = (warp - OUT_WARP0) >> 2, i_row = quarter * 32 + lane;
   const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
   const uint32_t O1 = tmem + lane_base + TM_O1 + half * 64, O2 = tmem + lane_base + TM_O2 + half * 64;
-  uint8_t* stage = sm + OUT_AT + (warp - OUT_WARP0) * OUT_BYTES;
   uint32_t g = 0;
   Items<kLocal> items(p);
   for (Item it; items.next(p, it, false);) {
@@ -496,6 +505,7 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t t
       const int rows = it.rows(c);
       const float w1 = decay_power(log2_decay, max(it.reverse ? rows - i_row - (c == 0 ? it.early : 0) : i_row + 1, 0)) * p.scale;
       const bool stores = quarter * 32 < rows && job.out;
+      uint8_t* stage = sm + (g & 1u ? X1_AT : X_AT) + (warp - OUT_WARP0) * OUT_BYTES;  // x's place: its products have ended
       if (!warp_wait(&x.o_full, g & 1u, x, p)) return;
       tc_fence_after();
 #pragma unroll 1
@@ -518,17 +528,20 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t t
       }
       tc_fence_before();
       warp_arrive(&x.o_empty);
-      if (!stores) continue;
       // through shared memory, so that a store fills whole lines: stores of a sector in each of 32 lines took the
       // unit that shared memory goes through for 57 cycles each
-      uint16_t* dst = job.out + static_cast<int64_t>(it.first(c) + quarter * 32) * job.os + it.h * LIN_D + half * 64 + 8 * (lane & 7);
+      if (stores) {
+        uint16_t* dst = job.out + static_cast<int64_t>(it.first(c) + quarter * 32) * job.os + it.h * LIN_D + half * 64 + 8 * (lane & 7);
 #pragma unroll 4
-      for (int q = 0; q < 8; ++q) {
-        const int r = 4 * q + (lane >> 3);
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-        if (quarter * 32 + r < rows) *reinterpret_cast<uint4*>(dst + r * job.os) = v;
+        for (int q = 0; q < 8; ++q) {
+          const int r = 4 * q + (lane >> 3);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (quarter * 32 + r < rows) *reinterpret_cast<uint4*>(dst + r * job.os) = v;
+        }
+        __syncwarp();
+        fence_proxy_async_smem();  // (before x's next tile)
       }
-      __syncwarp();
+      warp_arrive(&x.x_empty[g & 1u]);
     }
   }
 }
@@ -540,7 +553,7 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tm
   const int quarter = warp & 3, half = (warp - STATE_WARP0) >> 2, e_row = quarter * 32 + lane;  // a row of the state, 64 half .. of its columns
   const uint32_t St = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + TM_S + half * 64;
   // the warp's rows of the image; without outputs a place of its own
-  uint8_t* stage = sm + (kOutputs ? S_AT + half * HALF_TILE + quarter * 32 * 128 : OUT_AT + (warp - STATE_WARP0) * OUT_BYTES);
+  uint8_t* stage = sm + (kOutputs ? S_AT + half * HALF_TILE + quarter * 32 * 128 : X1_AT + (warp - STATE_WARP0) * OUT_BYTES);
   uint8_t* image = stage + lane * 128;
   uint32_t g = 0;
   Items<kLocal> items(p);
@@ -721,11 +734,11 @@ __global__ void __launch_bounds__(LT_THREADS, 1) lin_tile_kernel(const __grid_co
   Aux& x = *reinterpret_cast<Aux*>(sm + AUX_AT);
   const int warp = static_cast<int>(threadIdx.x >> 5);
   if (threadIdx.x == 0) {
-    uint64_t* once[] = {&x.x_full, &x.y_full, &x.z_full, &x.x_empty, &x.a_full, &x.o_full, &x.s_empty, &x.m_full, &x.m_begun, &x.w_empty[0], &x.w_empty[1], &x.drain[0], &x.drain[1]};
+    uint64_t* once[] = {&x.x_full[0], &x.x_full[1], &x.y_full, &x.z_full, &x.a_full, &x.o_full, &x.s_empty, &x.m_full, &x.m_begun, &x.w_empty[0], &x.w_empty[1], &x.drain[0], &x.drain[1]};
     for (uint64_t* b : once) mbar_init(b, 1);
     mbar_init(&x.y_empty, PARTS_WARPS + (kOutputs ? 1 : 0));
     mbar_init(&x.z_empty, kOutputs ? 2 : 1);
-    uint64_t* warps[] = {&x.p_full, &x.o_empty, &x.s_full, &x.group[0]};
+    uint64_t* warps[] = {&x.p_full, &x.o_empty, &x.s_full, &x.x_empty[0], &x.x_empty[1], &x.group[0]};
     for (uint64_t* b : warps) mbar_init(b, GROUP_WARPS);
     const int withheld = (p.debug & DEBUG_WITHHOLD_STATES) && (blockIdx.x & 3u) == 1u ? 1 : 0;
     mbar_init(&x.w_full[0], PARTS_WARPS + withheld);

