@@ -756,6 +756,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) lin_tile_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = x.tmem_slot;
+  wait_for_launch_before();
 
   if (warp < DECAY_WARP0) {
     if (warp == 0) loader<kOutputs, kLocal>(p, maps, sm, x);
@@ -788,7 +789,9 @@ cudaError_t launch(const LinParams& p, const LtMaps& maps, int num_sms, cudaStre
   // (segments of all users: no more than their rows hold, and one each)
   const int64_t segs = p.segs > 1 ? p.n_rows / p.seg_len + static_cast<int64_t>(p.n_users) : p.n_users;
   const int64_t items = segs * p.H * p.n_jobs;
-  lin_tile_kernel<kOutputs, kLocal><<<static_cast<unsigned>(items < num_sms ? items : num_sms), LT_THREADS, LT_SMEM, s>>>(p, maps);
+  const unsigned grid = static_cast<unsigned>(items < num_sms ? items : num_sms);
+  if (!kLocal && p.segs > 1) return launch_behind(lin_tile_kernel<kOutputs, kLocal>, dim3(grid), LT_THREADS, LT_SMEM, s, p, maps);
+  lin_tile_kernel<kOutputs, kLocal><<<grid, LT_THREADS, LT_SMEM, s>>>(p, maps);
   return cudaGetLastError();
 }
 

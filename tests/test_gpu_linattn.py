@@ -216,6 +216,42 @@ def test_again_and_again():
         assert p.status() == B.IKBO_OK and int(wrong) == 0
 
 
+def test_inputs_that_change_right_before_and_after_a_call():
+    """A cut history's launches may be set up while the one before ends: not before what is ahead of the call, nor past what is behind it."""
+    lens = [4000, 900]
+    both = [Data(seed, lens, 2, decay=[0.995, 0.9]) for seed in (31, 32)]
+    with plan() as p:
+        want = [run_forward(p, d) for d in both]
+        ins = [(*d.cuda()[:3], f32(d.S)) for d in both]
+        decay, off = both[0].cuda()[3:]
+        Q, K, V, S = (torch.zeros_like(t) for t in ins[0])
+        O = torch.zeros_like(Q)
+        wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+
+        def once(i):
+            for to, x in zip((Q, K, V, S), ins[i]):
+                to.copy_(x)
+            before = p.launches()
+            p.linattn_forward(Q, K, V, decay, O, state_in=S, state_out=S, offsets=off)  # (the state in its place)
+            assert p.launches() == before + 3
+            for to in (Q, K, V):
+                to.fill_(7.0)
+            wrong.add_((O != want[i][0]).sum() + (S != want[i][1]).sum())
+            O.zero_()
+
+        for i in range(100):
+            once(i % 2)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            once(0)
+            once(1)
+        for _ in range(20):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert p.status() == B.IKBO_OK and int(wrong) == 0
+
+
 def test_events_one_by_one_are_the_whole():
     """A history taken in at once, in pieces, and token by token ends in the same state."""
     d = Data(5, [150], 3)

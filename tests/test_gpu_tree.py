@@ -235,3 +235,38 @@ def test_strided_rows_repeat_captured_and_on_another_stream():
         with pytest.raises(ValueError):
             p.attn_qcache_tree_forward(q, data, c.st.page, table, ln, K, V, par[:, :8], O4)
         assert p.status() == B.IKBO_OK
+
+
+def test_inputs_that_change_right_before_and_after_a_call():
+    """The drafts' part may be set up while the history's ends: not before what is ahead of the call, nor past what is behind it."""
+    c, other = Case(14, [300, 90], [0, 1, 0, 1, 1], 4, 2, 16, 16), Case(15, [300, 90], [0, 1, 0, 1, 1], 4, 2, 16, 16)
+    with plan() as p:
+        other.st, other.Q = c.st, c.Q
+        want = [(k, *k.run(p)) for k in (c, other)]
+        data, table, ln = c.st.cuda()
+        ins = [(bf(k.K), bf(k.V), i32(k.parents)) for k, _, _ in want]
+        q, K, V, par = bf(c.Q), *(torch.zeros_like(t) for t in ins[0])
+        O, lse = torch.zeros_like(q), torch.zeros_like(want[0][2])
+        wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+
+        def once(i):
+            for to, x in zip((K, V, par), ins[i]):
+                to.copy_(x)
+            p.attn_qcache_tree_forward(q, data, c.st.page, table, ln, K, V, par, O, lse=lse)
+            for to in (K, V, par):
+                to.fill_(-1)
+            wrong.add_((O != want[i][1]).sum() + (lse != want[i][2]).sum())
+            O.zero_()
+            lse.zero_()
+
+        for i in range(100):
+            once(i % 2)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            once(0)
+            once(1)
+        for _ in range(20):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert p.status() == B.IKBO_OK and int(wrong) == 0
