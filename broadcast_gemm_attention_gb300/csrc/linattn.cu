@@ -17,6 +17,7 @@
 // from the forward pass.
 #include <cuda_bf16.h>
 
+#include "launch.cuh"
 #include "linattn_internal.h"
 #include "mma_common.cuh"
 #include "tile_common.cuh"
@@ -64,11 +65,12 @@ struct LinShared {
 // Bound: those products (603 TFLOP/s at most on this part, 117 kFLOP a row and head with
 // queries) and each chunk's chain; no state to set up in tensor memory, so the shorter
 // histories are its own.  Measured: the states of 15 users' 0 to 24 new rows, 8 heads,
-// 5.5 us; 15 histories of 1200 to 2048 rows 142 us (lintile.cu: 53.7).
+// 5.5 us; 15 histories of 1200 to 2048 rows 142 us (lintile.cu: 51.4).
 //
 // kOutputs: with queries; else the states alone.
 template <bool kOutputs>
 __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kernel(const __grid_constant__ LinParams p) {
+  wait_for_launch_before();
   extern __shared__ __align__(128) uint8_t lin_sm[];
   __shared__ LinShared sh;
   constexpr int kTiles = kOutputs ? 3 : 2;  // y, z, x
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
 
 // The states at the segments' ends, from the segments' own parts (in the last
 // one's place, which has no part, the start).  Bound: latency, a chain of loads over
-// the segments; 8 of the 86 us of two users' 20000 and 30001 rows, 4 heads.
+// the segments; 8 of the 85 us of two users' 20000 and 30001 rows, 4 heads.
 __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ LinParams p) {
   wait_for_launch_before();
   constexpr int kParts = LIN_STATE / 256;
@@ -294,11 +296,12 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ L
 // has 16 of the state's rows (y's elements), a lane 4 of its columns; x, y and z
 // come as fp32 through shared memory, 16 rows of them at a time.
 // Bound: memory, the state read and written.  One row for each of 256 users, 8 heads:
-// 44.6 us, 6.1 TB/s, 0.92 of a plain copy's rate.
+// 41.9 us, 6.4 TB/s, 0.97 of a plain copy's rate.
 constexpr int STEP_ROWS = 16;
 
 template <bool kOutputs>
 __global__ void __launch_bounds__(LIN_THREADS) lin_step_kernel(const __grid_constant__ LinParams p) {
+  wait_for_launch_before();
   __shared__ float4 rows[kOutputs ? 3 : 2][STEP_ROWS][LIN_D / 4];  // y, z, x
   __shared__ float part[2][8][LIN_D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -375,26 +378,24 @@ cudaError_t launch_chunks(const LinParams& p, cudaStream_t s) {
   const cudaError_t e = allow_smem(lin_chunk_kernel<kOutputs>, smem, done);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(p.n_users * p.H), static_cast<unsigned>(p.n_jobs));
-  lin_chunk_kernel<kOutputs><<<grid, LIN_THREADS, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind(lin_chunk_kernel<kOutputs>, grid, LIN_THREADS, smem, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_lin_tiles(const LinParams& p, bool local, int num_sms, cudaStream_t s);
 
-// Launches: one, or three where histories are cut into segments (each set up while the one
-// before ends: two users' 20000 and 30001 rows 92.4 -> 86.3 us).
+// Launches: one, or three where histories are cut into segments (two users' 20000
+// and 30001 rows 84.5 us).
 cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int* launches) {
   *launches = 0;
   const bool outputs = p.job[0].x != nullptr;
   cudaError_t e;
   if (p.steps) {
     const unsigned grid = static_cast<unsigned>(p.n_users * p.H);
-    if (outputs) lin_step_kernel<true><<<grid, LIN_THREADS, 0, s>>>(p);
-    else lin_step_kernel<false><<<grid, LIN_THREADS, 0, s>>>(p);
     *launches = 1;
-    return cudaGetLastError();
+    return outputs ? launch_behind(lin_step_kernel<true>, dim3(grid), LIN_THREADS, 0, s, p)
+                   : launch_behind(lin_step_kernel<false>, dim3(grid), LIN_THREADS, 0, s, p);
   }
   if (p.segs > 1) {
     e = launch_lin_tiles(p, true, num_sms, s);

@@ -27,6 +27,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "launch.cuh"
 #include "linattn_internal.h"
 #include "mma_common.cuh"
 #include "tile_common.cuh"
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     fence_barrier_init();
     fence_proxy_async_smem();
   }
+  wait_for_launch_before();
   if (warp == 3) {
     tmem_alloc(&x.tmem_slot, 512);
     tmem_relinquish();
@@ -432,8 +434,7 @@ cudaError_t launch(const LinReadParams& p, const CUtensorMap& mx, const CUtensor
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(lin_read_kernel<kBack>, RT_SMEM, done);
   if (e != cudaSuccess) return e;
-  lin_read_kernel<kBack><<<static_cast<unsigned>(lin_read_ctas(num_sms)), RT_THREADS, RT_SMEM, s>>>(p, mx, mq);
-  return cudaGetLastError();
+  return launch_behind(lin_read_kernel<kBack>, dim3(static_cast<unsigned>(lin_read_ctas(num_sms))), RT_THREADS, RT_SMEM, s, p, mx, mq);
 }
 
 }  // namespace

@@ -27,15 +27,16 @@
 //
 // Bound: shared memory, 576 KB a chunk, 4500 of the 4950 cycles that a chunk takes
 // (products 288, parts 96, image 32, outputs 64, loads 96).  15 histories of 1200 to
-// 2048 rows, 8 heads, bf16: 53.7 us, 14 of them start and end, 3.7 TB/s of the tensors'
+// 2048 rows, 8 heads, bf16: 51.4 us, 12 of them start and end, 3.9 TB/s of the tensors'
 // bytes, 0.36 of the tensor pipe's cycles; with 16x8x16 products in registers
-// (linattn.cu) 142 us.  Their gradient at 524 to 1024 rows: 75.7 us (178).
+// (linattn.cu) 142 us.  Their gradient at 524 to 1024 rows: 72.8 us (178).
 //
 // A reverse scan keeps the rows' order in its tiles and turns masks and decays around
 // instead (row j reaches i <= j, and the chunk's first row is its end).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "launch.cuh"
 #include "linattn_internal.h"
 #include "mma_common.cuh"
 #include "tile_common.cuh"
@@ -748,6 +749,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) lin_tile_kernel(const __grid_co
     fence_barrier_init();
     fence_proxy_async_smem();
   }
+  wait_for_launch_before();
   if (warp == 3) {
     tmem_alloc(&x.tmem_slot, 512);
     tmem_relinquish();
@@ -756,7 +758,6 @@ __global__ void __launch_bounds__(LT_THREADS, 1) lin_tile_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = x.tmem_slot;
-  wait_for_launch_before();
 
   if (warp < DECAY_WARP0) {
     if (warp == 0) loader<kOutputs, kLocal>(p, maps, sm, x);
@@ -790,9 +791,7 @@ cudaError_t launch(const LinParams& p, const LtMaps& maps, int num_sms, cudaStre
   const int64_t segs = p.segs > 1 ? p.n_rows / p.seg_len + static_cast<int64_t>(p.n_users) : p.n_users;
   const int64_t items = segs * p.H * p.n_jobs;
   const unsigned grid = static_cast<unsigned>(items < num_sms ? items : num_sms);
-  if (!kLocal && p.segs > 1) return launch_behind(lin_tile_kernel<kOutputs, kLocal>, dim3(grid), LT_THREADS, LT_SMEM, s, p, maps);
-  lin_tile_kernel<kOutputs, kLocal><<<grid, LT_THREADS, LT_SMEM, s>>>(p, maps);
-  return cudaGetLastError();
+  return launch_behind(lin_tile_kernel<kOutputs, kLocal>, dim3(grid), LT_THREADS, LT_SMEM, s, p, maps);
 }
 
 }  // namespace

@@ -23,6 +23,7 @@
 // lane ends up with whole 16-byte pieces of O.
 #include <cuda_bf16.h>
 
+#include "launch.cuh"
 #include "mma_common.cuh"
 #include "qcache_internal.h"
 

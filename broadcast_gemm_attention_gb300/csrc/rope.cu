@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "launch.cuh"
 #include "qcache_internal.h"
 
 namespace ikbo {
@@ -139,6 +140,7 @@ __device__ __forceinline__ void store8(T* p, const Vec8<T>& r) {
 // kAhead: heads whose loads are in flight together.
 template <typename T, bool kInterleaved, int kAhead, bool kAxes>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_constant__ RopeParams p) {
+  if (kAxes) wait_for_launch_before();
   const int turning = p.rot >> 4;
   const int pieces = turning + (p.copy_rest ? (p.d - p.rot + 15) >> 4 : 0);
   const int rows_per_cta = ROPE_THREADS / pieces;
@@ -217,6 +219,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_con
 // ones) of a token, over its heads.
 template <typename T, bool kAxes>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_constant__ RopeParams p) {
+  if (kAxes) wait_for_launch_before();
   const int half = p.rot >> 1;
   const int pieces = half + (p.copy_rest ? p.d - p.rot : 0);
   const int64_t total = static_cast<int64_t>(p.n) * p.L * pieces;
@@ -252,10 +255,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_con
 // registers of four), else as many as their registers pay for (the 70:1 queries:
 // 22.3 us with four, 22.8 with two, 26.2 with eight).
 template <typename T, bool kInterleaved, bool kAxes>
-void launch_vec(const RopeParams& p, dim3 grid, cudaStream_t s) {
+auto vec_kernel(const RopeParams& p) {
   constexpr int kMost = sizeof(T) == 4 ? 2 : 4;
-  if (p.heads_per_cta == 1) rope_vec_kernel<T, kInterleaved, 1, kAxes><<<grid, ROPE_THREADS, 0, s>>>(p);
-  else rope_vec_kernel<T, kInterleaved, kMost, kAxes><<<grid, ROPE_THREADS, 0, s>>>(p);
+  return p.heads_per_cta == 1 ? rope_vec_kernel<T, kInterleaved, 1, kAxes> : rope_vec_kernel<T, kInterleaved, kMost, kAxes>;
 }
 
 template <typename T, bool kAxes>
@@ -279,9 +281,9 @@ cudaError_t launch(RopeParams p, bool vec, int num_sms, cudaStream_t s) {
   if (parts > p.H) parts = p.H;
   p.heads_per_cta = (p.H + parts - 1) / parts;
   const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>((p.H + p.heads_per_cta - 1) / p.heads_per_cta));
-  if (!vec) rope_any_kernel<T, kAxes><<<grid, ROPE_THREADS, 0, s>>>(p);
-  else if (p.interleaved) launch_vec<T, true, kAxes>(p, grid, s);
-  else launch_vec<T, false, kAxes>(p, grid, s);
+  const auto kernel = !vec ? rope_any_kernel<T, kAxes> : (p.interleaved ? vec_kernel<T, true, kAxes>(p) : vec_kernel<T, false, kAxes>(p));
+  if (kAxes) return launch_behind(kernel, grid, ROPE_THREADS, 0, s, p);
+  kernel<<<grid, ROPE_THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
 
