@@ -14,14 +14,18 @@
 //   dS += Q^T dO  (backward) into tensor memory over all of a run of units of one
 //                 (user, head), both operands MN-major: rows are the inner dimension.
 // One pass over the rows serves both gradients.  Bound: memory, and each CTA's start.
-// 1024 candidates of 15 users, 8 heads x 32 rows: 27.5 us, 5.1 TB/s, 5 us of it start
-// (16x8x16 products in registers: 82); the gradient of 1024 candidates of 64 users
-// unevenly, 8 heads x 16 rows: 46.5 us, 3.6 TB/s (138), 6 of it the parts' adding.
+// 1024 candidates of 15 users, 8 heads x 32 rows: 29.4 us with the plan's launch, 4.8 TB/s
+// (16x8x16 products in registers: 107); the gradient of 1024 candidates of 64 users
+// unevenly, 8 heads x 16 rows: 45.8 us, 3.7 TB/s (138), 6 of it the parts' adding.
 //
 // Per CTA (persistent, one per SM, an equal run of the list, 20 warps):
 //   warp 0       loads; warp 1 issues
 //   warps 4-11   outputs, and at a run's end the state's gradient
 //   warps 12-19  images of the states, one run ahead; zeros for users without candidates
+// A run costs about as many bytes as a unit (its state, and that one's gradient), so
+// shares are equal in units and runs together (in units alone the gradient of 1024
+// candidates of 64 users, unevenly, had 63 tiles' bytes in its largest share, of 41 on
+// average; so 45).
 // Runs cut by a CTA's share leave their gradients as parts, which the last CTA to end
 // adds in order (so results repeat bit for bit).
 #include <cuda.h>
@@ -48,7 +52,12 @@ constexpr uint32_t TM_O = 0, TM_DS = 256;
 struct Aux {
   uint64_t full[RING_TILES], empty[RING_TILES];
   uint64_t o_full[2], o_empty[2], image_full[2], image_empty[2], ds_full[2], ds_empty[2], drain;
-  uint32_t tmem_slot, abort, last;
+  uint32_t tmem_slot, abort;
+  int begin, end;               // the CTA's share of the list
+  uint32_t total;               // of all units' and runs' costs; 0: shares are equal in units
+  uint2 sums[RT_THREADS / 32];  // units and runs of a warp's users
+  int4 shared[2];               // runs shared with other CTAs: its user and head, its first and last CTA (-1: none)
+  uint32_t parts[2], last[2];   // how many CTAs that are, whether this was the last of them
 };
 constexpr uint32_t RT_SMEM = AUX_AT + sizeof(Aux) + 1024;
 static_assert(RT_SMEM <= 227 * 1024, "tiles do not fit in shared memory");
@@ -61,10 +70,9 @@ struct Walk {
   int u, h;        // of the run
   bool begins, ends;
   int4 w, next;
-  __device__ __forceinline__ Walk(const LinReadParams& p) : runs(0), u(-1), h(-1) {
-    const int64_t n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
-    a = static_cast<int>(blockIdx.x * n / gridDim.x);
-    b = static_cast<int>((blockIdx.x + 1) * n / gridDim.x);
+  __device__ __forceinline__ Walk(const LinReadParams& p, const Aux& x) : runs(0), u(-1), h(-1) {
+    a = x.begin;
+    b = x.end;
     next = a < b ? unit(p, a) : make_int4(-1, -1, 0, 0);
   }
   __device__ __forceinline__ static int4 unit(const LinReadParams& p, int i) { return __ldg(reinterpret_cast<const int4*>(p.work) + i); }
@@ -89,13 +97,108 @@ struct Walk {
   }
 };
 
+// ------------------------------------------------------------------ shares
+// Where a share of the list begins.  A unit costs 1 and its run's beginning 1 more; counted
+// along the list (P before a run, that run's units at P, P + 2, P + 3, ..), unit i at cost(i)
+// is CTA cost(i) * CTAs / total's.  Units alone count (total: how many) where there are fewer
+// runs than CTAs (15 users' 8 heads: 1.6 us without finding the shares), and where shares
+// are not two wide at least, so that what lies between a run's first CTA and its last has
+// units of it.
+__device__ __forceinline__ uint32_t share_begin(uint32_t c, uint32_t total) {
+  if (total <= 0xffffffffu / 1024) return (c * total + gridDim.x - 1) / gridDim.x;
+  return static_cast<uint32_t>((static_cast<uint64_t>(c) * total + gridDim.x - 1) / gridDim.x);
+}
+__device__ __forceinline__ int share_of(uint32_t cost, uint32_t total) {
+  return static_cast<int>(static_cast<uint64_t>(cost) * gridDim.x / total);
+}
+
+__device__ __forceinline__ uint32_t listed_units(const LinReadParams& p) {
+  return static_cast<uint32_t>(max(0, min(__ldg(p.n_units), static_cast<int>(p.max_units))));
+}
+
+// Units of user u for each head.
+__device__ __forceinline__ uint32_t units_of(const LinReadParams& p, int u, uint32_t cands) {
+  const int count = __ldg(p.offsets + u + 1) - __ldg(p.offsets + u);
+  return count > 0 ? (static_cast<uint32_t>(count) + cands - 1) / cands : 0u;
+}
+
+// By the whole CTA, each thread some users.
+__device__ __forceinline__ void find_share(const LinReadParams& p, Aux& x) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const uint32_t c = blockIdx.x, n = listed_units(p);
+  uint32_t units = 0, runs = 0, before = 0, cost = 0, all = 0, total = 0;
+  const bool weigh = static_cast<int64_t>(p.n_users) * p.H > gridDim.x;
+  const int per = (p.n_users + RT_THREADS - 1) / RT_THREADS, u0 = min(tid * per, p.n_users), u1 = min(u0 + per, p.n_users);
+  const uint32_t cands = 128u / p.Lq;
+  if (weigh) {
+#pragma unroll 4
+    for (int u = u0; u < u1; ++u) {
+      const uint32_t k = units_of(p, u, cands);
+      units += k * p.H;
+      runs += k > 0 ? p.H : 0;
+    }
+    before = units;
+    cost = runs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(0xffffffffu, before, o), b = __shfl_up_sync(0xffffffffu, cost, o);
+      if (lane >= o) {
+        before += a;
+        cost += b;
+      }
+    }
+    if (lane == 31) x.sums[warp] = make_uint2(before, cost);
+    __syncthreads();
+    before -= units;
+    cost += before - runs;  // of the thread's first user
+#pragma unroll 4
+    for (int w = 0; w < RT_THREADS / 32; ++w) {
+      const uint2 v = x.sums[w];
+      all += v.x;
+      total += v.x + v.y;
+      if (w >= warp) continue;
+      before += v.x;
+      cost += v.x + v.y;
+    }
+  }
+  if (!weigh || all != n || total < 2 * gridDim.x) {
+    if (tid == 0) {
+      x.begin = static_cast<int>(share_begin(c, n));
+      x.end = static_cast<int>(share_begin(c + 1, n));
+      x.total = 0;
+    }
+    return;
+  }
+  if (tid == 0) x.total = total;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t ask = share_begin(c + e, total);
+    int* to = e == 0 ? &x.begin : &x.end;
+    if (tid == 0 && ask == total) *to = static_cast<int>(n);
+    if (ask < cost || ask - cost >= units + runs) continue;
+    uint32_t t = ask - cost, at = before;
+    for (int u = u0; u < u1; ++u) {
+      const uint32_t k = units_of(p, u, cands);
+      if (k == 0) continue;
+      if (t >= (k + 1) * p.H) {
+        t -= (k + 1) * p.H;
+        at += k * p.H;
+        continue;
+      }
+      const uint32_t run = t / (k + 1), in = t - run * (k + 1);
+      *to = static_cast<int>(at + run * k + (in == 0 ? 0u : max(in - 1, 1u)));
+      break;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ loader
 template <bool kBack>
 __device__ void loader(const LinReadParams& p, const CUtensorMap* mx, const CUtensorMap* mq, uint8_t* sm, Aux& x) {
   constexpr int kStages = kBack ? RING_TILES / 2 : RING_TILES;
   constexpr uint32_t kStage = (kBack ? 2 : 1) * TILE;
   const int lane = static_cast<int>(lane_id());
-  Walk k(p);
+  Walk k(p, x);
   uint32_t g = 0;
   bool ok = true;
   int cand_next = Walk::cand(p, k.next, lane);
@@ -164,7 +267,7 @@ __device__ void issuer(const LinReadParams& p, uint8_t* sm, Aux& x, uint32_t tme
   constexpr uint32_t kStage = (kBack ? 2 : 1) * TILE;
   const uint32_t ring = smem_u32(sm), images = smem_u32(sm + IMAGE_AT);
   const bool out = p.out != nullptr;
-  Walk k(p);
+  Walk k(p, x);
   uint32_t g = 0;
   for (int i = k.a; i < k.b && k.at(p, i); ++i, ++g) {
     const uint32_t st = g % kStages, r = k.runs - 1, rb = r & 1u, rp = (r >> 1) & 1u, ob = g & 1u;
@@ -203,7 +306,8 @@ __device__ void image_warps(const LinReadParams& p, uint8_t* sm, Aux& x) {
     }
   }
   if (!p.out) return;
-  Walk k(p);
+  Walk k(p, x), ahead(p, x);
+  int j = ahead.a;
   for (int i = k.a; i < k.b && k.at(p, i); ++i) {
     if (!k.begins) continue;
     const uint32_t r = k.runs - 1, rb = r & 1u;
@@ -213,6 +317,12 @@ __device__ void image_warps(const LinReadParams& p, uint8_t* sm, Aux& x) {
     float4 v[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) v[c] = __ldg(s + (8 * c + warp) * 32);
+    if (warp == 0) {  // the next run's state is on its way to L2 meanwhile (47.1 -> 45.8 us)
+      while (j < ahead.b && ahead.runs <= k.runs && ahead.at(p, j)) ++j;
+      if (ahead.runs > k.runs && elect_one())
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.state + (static_cast<int64_t>(ahead.u) * p.H + ahead.h) * LIN_STATE), "n"(LIN_STATE * 4) : "memory");
+      __syncwarp();
+    }
     if (!warp_wait(&x.image_empty[rb], ((r >> 1) & 1u) ^ 1u, x, p)) return;
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
@@ -224,6 +334,50 @@ __device__ void image_warps(const LinReadParams& p, uint8_t* sm, Aux& x) {
   }
 }
 
+// ------------------------------------------------------------ shared runs
+// Which runs this CTA shares, by one warp: its first and its last unit's.
+__device__ void find_shared(const LinReadParams& p, Aux& x) {
+  const int n = static_cast<int>(listed_units(p)), a = x.begin, b = x.end, cands = 128 / p.Lq;
+  int done = -1;
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    int4 run = make_int4(-1, -1, -1, -1);
+    uint32_t parts = 0;
+    const int i = k == 0 ? a : b - 1;
+    const int4 w = a < b ? Walk::unit(p, i) : make_int4(-1, -1, 0, 0);
+    if (w.x >= 0 && w.x < p.n_users) {
+      const int first = __ldg(p.offsets + w.x);
+      const int lo = i - (w.z - first) / cands, hi = lo + (__ldg(p.offsets + w.x + 1) - first + cands - 1) / cands;  // its units
+      if ((lo < a || hi > b) && lo != done && lo >= 0 && hi <= n) {
+        done = lo;
+        uint32_t cost = static_cast<uint32_t>(lo), total = static_cast<uint32_t>(n);
+        if (x.total > 0) {
+          int users = 0;  // with candidates, before the run's
+#pragma unroll 4
+          for (int v = 0; v < w.x; v += 32) {
+            const int u = min(v + static_cast<int>(lane_id()), w.x);
+            users += __popc(__ballot_sync(0xffffffffu, u < w.x && __ldg(p.offsets + u + 1) > __ldg(p.offsets + u)));
+          }
+          cost += static_cast<uint32_t>(users * p.H + w.y);
+          total = x.total;
+        }
+        const int c0 = share_of(cost, total);
+        const int c1 = share_of(cost + static_cast<uint32_t>(hi - lo - 1) + (x.total > 0 && hi - lo > 1 ? 1u : 0u), total);
+        const bool gaps = x.total == 0 && n < static_cast<int>(gridDim.x);  // fewer units than CTAs: each has one at most
+        if (c0 <= c1 && c1 < static_cast<int>(gridDim.x)) {  // (always, in a sound list)
+          run = make_int4(w.x, w.y, c0, c1);
+          parts = static_cast<uint32_t>(gaps ? hi - lo : c1 - c0 + 1);
+        }
+      }
+    }
+    if (lane_id() == 0) {
+      x.shared[k] = run;
+      x.parts[k] = parts;
+    }
+  }
+  __syncwarp();
+}
+
 // ----------------------------------------------------------------- outputs
 template <bool kBack>
 __device__ void output_warps(const LinReadParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
@@ -232,7 +386,7 @@ __device__ void output_warps(const LinReadParams& p, uint8_t* sm, Aux& x, uint32
   const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
   uint8_t* stage = sm + OUT_AT + (warp - OUT_WARP0) * OUT_BYTES;
   const int piece = lane & 7, slot = row / p.Lq;
-  Walk k(p);
+  Walk k(p, x);
   uint32_t g = 0;
   int cand_next = Walk::cand(p, k.next, slot);
   for (int i = k.a; i < k.b && k.at(p, i); ++i, ++g) {
@@ -312,64 +466,52 @@ __device__ void output_warps(const LinReadParams& p, uint8_t* sm, Aux& x, uint32
   }
 }
 
-// The run that unit i belongs to: its first unit and the one behind its last.
-__device__ __forceinline__ void run_of(const LinReadParams& p, int i, int& lo, int& hi) {
-  const int4 w = Walk::unit(p, i);
-  const int cands = 128 / p.Lq, first = __ldg(p.offsets + w.x);
-  lo = i - (w.z - first) / cands;
-  hi = lo + (__ldg(p.offsets + w.x + 1) - first + cands - 1) / cands;
-}
-
 // The parts of the runs that this CTA shares (its first and its last, at most), where it
 // is the last of their CTAs.  Counted whatever happened before, so that counts are zero
 // again for the next call.
-__device__ void join_runs(const LinReadParams& p, uint32_t* last) {
-  const int64_t n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units), ctas = gridDim.x;
-  const auto begin = [&](int64_t c) { return static_cast<int>(c * n / ctas); };
-  const int a = begin(blockIdx.x), b = begin(static_cast<int64_t>(blockIdx.x) + 1);
-  if (a >= b) return;
-  int done = -1;
+__device__ void join_runs(const LinReadParams& p, Aux& x) {
+  if (threadIdx.x == 0) {
+    __threadfence();
+    uint32_t had[2] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (x.parts[k]) had[k] = atomicAdd(p.tickets + x.shared[k].z, 1u);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      x.last[k] = x.parts[k] && had[k] + 1 == x.parts[k];
+      if (x.last[k]) p.tickets[x.shared[k].z] = 0;
+    }
+  }
+  __syncthreads();
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
-    int lo, hi;
-    run_of(p, k == 0 ? a : b - 1, lo, hi);
-    if ((lo >= a && hi <= b) || lo == done || lo < 0 || hi > n) continue;  // its own, or the same again
-    done = lo;
-    const int c0 = static_cast<int>(((lo + 1) * ctas - 1) / n), c1 = static_cast<int>((hi * ctas - 1) / n);
-    const uint32_t parts = n >= ctas ? c1 - c0 + 1 : hi - lo;  // (with fewer units than CTAs each has one at most)
-    if (threadIdx.x == 0) {
-      __threadfence();
-      *last = atomicAdd(p.tickets + c0, 1u) + 1 == parts;
-      if (*last) p.tickets[c0] = 0;
-    }
-    __syncthreads();
-    if (*last) {
-      __threadfence();
-      const int4 w = Walk::unit(p, lo);
-      float4* to = reinterpret_cast<float4*>(p.d_state + (static_cast<int64_t>(w.x) * p.H + w.y) * LIN_STATE);
-      constexpr int kMine = (LIN_STATE / 4 + RT_THREADS - 1) / RT_THREADS;
-      float4 sum[kMine] = {};
+    if (!x.last[k]) continue;
+    __threadfence();
+    const int4 run = x.shared[k];
+    const uint32_t n = listed_units(p);
+    const bool gaps = static_cast<int>(x.parts[k]) != run.w - run.z + 1;
+    float4* to = reinterpret_cast<float4*>(p.d_state + (static_cast<int64_t>(run.x) * p.H + run.y) * LIN_STATE);
+    constexpr int kMine = (LIN_STATE / 4 + RT_THREADS - 1) / RT_THREADS;
+    float4 sum[kMine] = {};
 #pragma unroll 2
-      for (int c = c0; c <= c1; ++c) {
-        if (begin(c) >= begin(c + 1)) continue;
-        const float4* part = reinterpret_cast<const float4*>(p.part + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * LIN_STATE);
-#pragma unroll
-        for (int q = 0; q < kMine; ++q) {
-          const int e = q * RT_THREADS + static_cast<int>(threadIdx.x);
-          const float4 v = e < LIN_STATE / 4 ? __ldcg(part + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-          sum[q].x += v.x;
-          sum[q].y += v.y;
-          sum[q].z += v.z;
-          sum[q].w += v.w;
-        }
-      }
+    for (int c = run.z; c <= run.w; ++c) {
+      if (gaps && share_begin(c, n) >= share_begin(c + 1, n)) continue;
+      const float4* part = reinterpret_cast<const float4*>(p.part + (2 * static_cast<int64_t>(c) + (c == run.z ? 1 : 0)) * LIN_STATE);
 #pragma unroll
       for (int q = 0; q < kMine; ++q) {
         const int e = q * RT_THREADS + static_cast<int>(threadIdx.x);
-        if (e < LIN_STATE / 4) to[e] = make_float4(sum[q].x * p.scale, sum[q].y * p.scale, sum[q].z * p.scale, sum[q].w * p.scale);
+        const float4 v = e < LIN_STATE / 4 ? __ldcg(part + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        sum[q].x += v.x;
+        sum[q].y += v.y;
+        sum[q].z += v.z;
+        sum[q].w += v.w;
       }
     }
-    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const int e = q * RT_THREADS + static_cast<int>(threadIdx.x);
+      if (e < LIN_STATE / 4) to[e] = make_float4(sum[q].x * p.scale, sum[q].y * p.scale, sum[q].z * p.scale, sum[q].w * p.scale);
+    }
   }
 }
 
@@ -404,6 +546,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     tmem_alloc(&x.tmem_slot, 512);
     tmem_relinquish();
   }
+  find_share(p, x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -414,6 +557,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       issuer<kBack>(p, sm, x, tmem);
       drain(&x.drain);
     }
+    if (warp == 2 && kBack) find_shared(p, x);
   } else if (warp < IMAGE_WARP0) {
     output_warps<kBack>(p, sm, x, tmem);
   } else {
@@ -426,7 +570,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (kBack) join_runs(p, &x.last);
+  if (kBack) join_runs(p, x);
 }
 
 template <bool kBack>

@@ -516,6 +516,35 @@ def test_reads_of_whole_numbers_are_exact():
         assert not dS[U - 1].any()
 
 
+@pytest.mark.parametrize("counts,H,Lq", [
+    ([1000] + [1] * 40, 2, 16),            # one user's run over most CTAs, then runs of one
+    ([0, 3] * 30 + [300, 0, 0, 90], 3, 8),  # users without candidates between
+    ([1] * 152, 1, 128), ([1] * 76, 2, 64), ([2] * 151, 1, 128), ([151], 1, 128), ([9, 143], 1, 128),  # a unit or two for each SM
+    ([k % 4 for k in range(700)], 1, 32), ([1] * 1400, 2, 8), ([0] * 1300 + [5, 200], 3, 24)], ids=lambda x: f"{len(x)}u" if isinstance(x, list) else str(x))
+def test_shares_of_uneven_users_are_exact(counts, H, Lq):
+    """Runs of units shared between CTAs, in every way; twice, as counts go back to zero."""
+    g = torch.Generator().manual_seed(len(counts))
+    n, U = sum(counts), len(counts)
+    m = torch.repeat_interleave(torch.arange(U), torch.tensor(counts))[torch.randperm(n, generator=g)].int().cuda()
+    X, dO = (torch.randint(-2, 3, (n, H, Lq, D), generator=g).float().cuda() for _ in range(2))
+    S = torch.randint(-9, 10, (U, H, D, D), generator=g).float().cuda()
+    want = torch.zeros(S.shape, dtype=torch.float64, device="cuda")
+    O64, dX64 = torch.empty(X.shape, dtype=torch.float64, device="cuda"), torch.empty(X.shape, dtype=torch.float64, device="cuda")
+    for i in range(0, n, 64):
+        x, do, u = X[i:i + 64].double(), dO[i:i + 64].double(), m[i:i + 64].long()
+        want.index_add_(0, u, 0.5 * x.transpose(2, 3) @ do)
+        O64[i:i + 64], dX64[i:i + 64] = 0.5 * x @ S[u].double(), 0.5 * do @ S[u].double().transpose(2, 3)
+    with B.Plan(2048, 2048, 4) as p:
+        p.plan(m, U, H, Lq)
+        for _ in range(2):
+            O, dX, dS = torch.full_like(X, 9.0).bfloat16(), torch.full_like(X, 9.0).bfloat16(), torch.full_like(S, float("nan"))
+            p.linattn_read_forward(X.bfloat16(), S, O, scale=0.5)
+            p.linattn_read_backward(X.bfloat16(), S, dO.bfloat16(), dX, dS, scale=0.5)
+            assert torch.equal(dS.double(), want)
+            assert torch.equal(O, O64.bfloat16()) and torch.equal(dX, dX64.bfloat16())
+        assert p.status() == B.IKBO_OK
+
+
 def test_a_candidate_out_of_range_keeps_its_rows():
     rng = np.random.default_rng(2)
     m = np.array([0, 7, 1, -1, 1], np.int32)
