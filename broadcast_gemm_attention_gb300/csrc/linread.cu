@@ -18,7 +18,7 @@
 // (16x8x16 products in registers: 107); the gradient of 1024 candidates of 64 users
 // unevenly, 8 heads x 16 rows: 45.8 us, 3.7 TB/s (138), 6 of it the parts' adding.
 //
-// Per CTA (persistent, one per SM, an equal run of the list, 20 warps):
+// Per CTA (persistent, one per SM, a share of the list, 20 warps):
 //   warp 0       loads; warp 1 issues
 //   warps 4-11   outputs, and at a run's end the state's gradient
 //   warps 12-19  images of the states, one run ahead; zeros for users without candidates
