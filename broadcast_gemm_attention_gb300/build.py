@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libikbo.so")
 SOURCES = ["seg.cu", "lce.cu", "lce_noalloc.cu", "lce_bwd.cu", "attn.cu", "attn_bwd.cu", "rope.cu",
-           "qcache.cu", "qattn.cu", "qattn_tile.cu", "qtree.cu", "linattn.cu", "lintile.cu", "linread.cu", "api.cu",
+           "qcache.cu", "qattn.cu", "qattn_tile.cu", "qtree.cu", "linattn.cu", "linback.cu", "lintile.cu", "linread.cu", "api.cu",
            "qcache_api.cu", "linattn_api.cu"]
 HEADERS = ["ptx.cuh", "ikbo_internal.h", "bwd_internal.h", "plan_internal.h", "qcache_internal.h",
            "attn_common.cuh", "mma_common.cuh", "tile_common.cuh", "linattn_internal.h", "launch.cuh"]

@@ -7,14 +7,14 @@
 //   o_i = scale ( sum_{j <= i} decay^(i-j) (q_i.k_j) v_j + decay^(i+1) q_i S )
 //   S  <- decay^n S + sum_j decay^(n-1-j) k_j v_j^T        (n rows in the chunk)
 //
-// The gradient is three scans of the same kind.  With
+// The gradient of more than a few rows (of those: linback.cu) is three scans of the same kind.  With
 //   R_t = sum_{i >= t} decay^(i-t) scale q_i do_i^T + decay^(T-t) dS_T,
 //   dq_t = scale S_t do_t     a scan with queries do, keys v, values k,
 //   dk_t = R_t v_t            from the last row on: queries v, keys do, values q,
 //   dv_t = R_t^T k_t          from the last row on: queries k, keys q, values do,
-// and the gradient of the first state is decay R_1, the last one's end.  So one
-// kernel does all of it, three jobs a launch; nothing but the inputs is kept
-// from the forward pass.
+// and the gradient of the first state is decay R_1, the last one's end.  So the
+// kernel of lintile.cu does all of it, three jobs a launch; nothing but the inputs
+// is kept from the forward pass.
 #include <cuda_bf16.h>
 
 #include "launch.cuh"
@@ -78,22 +78,20 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
   const uint32_t base = smem_u32(lin_sm), probs = base + LIN_STAGES * kStage;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int u = static_cast<int>(blockIdx.x) / p.H, h = static_cast<int>(blockIdx.x) - u * p.H;
-  const LinJob& job = p.job[blockIdx.y];
+  const LinJob& job = p.job[0];
 
   int first_row;
   const int n = lin_rows(p, u, first_row);
   const float log2_decay = log2f(__ldg(p.decay + h));
   if (tid <= LIN_CHUNK) sh.power[tid] = lin_power(log2_decay, tid);
 
-  // the scan's order as rows of the tensors
-  const int64_t dir = job.reverse ? -1 : 1;
-  const int64_t row_at = static_cast<int64_t>(first_row) + (job.reverse ? n - 1 : 0);
+  const int64_t row_at = first_row;
   const auto load_tile = [&](const uint16_t* src, int64_t stride, uint32_t dst, int c0) {
 #pragma unroll
     for (int k = 0; k < LIN_TILE / 16 / LIN_THREADS; ++k) {
       const int i = k * LIN_THREADS + tid, r = i >> 4, c = i & 15;
       const bool there = c0 + r < n;
-      copy16(dst + tile_at(r, c), there ? src + (row_at + dir * (c0 + r)) * stride + h * LIN_D + c * 8 : src, there);
+      copy16(dst + tile_at(r, c), there ? src + (row_at + c0 + r) * stride + h * LIN_D + c * 8 : src, there);
     }
   };
   const auto load_stage = [&](int stage, int c0) {
@@ -110,30 +108,11 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
   float s[16][4];
   const int64_t state = (static_cast<int64_t>(u) * p.H + h) * LIN_STATE;
   const float* from = job.s_in ? job.s_in + state : nullptr;
-  const float factor = job.s_in_factor;
   const int e0 = 16 * warp + g;
-  if (from && !job.s_in_turned) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < 16; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[i][k] = __ldcg(from + (8 * i + 2 * t + (k & 1)) * LIN_D + e0 + 8 * (k >> 1)) * factor;
-  } else if (from) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(from + (e0 + 8 * k) * LIN_D + 8 * i + 2 * t));
-        s[i][2 * k] = v.x * factor;
-        s[i][2 * k + 1] = v.y * factor;
-      }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
-  }
-  // a reverse scan's start is taken as it is by its first row
-  int early = job.reverse ? 1 : 0;
+    for (int k = 0; k < 4; ++k) s[i][k] = from ? __ldcg(from + (8 * i + 2 * t + (k & 1)) * LIN_D + e0 + 8 * (k >> 1)) : 0.f;
 
 #pragma unroll 1
   for (int ch = 0; ch < chunks; ++ch) {
@@ -198,7 +177,7 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
           mma_16816(o[1], xf, sb[2 * kk][1], sb[2 * kk + 1][1]);
         }
         const int row = 16 * mt + g;
-        const float w0 = sh.power[row + 1 - early], w1 = sh.power[row + 9 - early];
+        const float w0 = sh.power[row + 1], w1 = sh.power[row + 9];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           o[e][0] *= w0;
@@ -217,16 +196,15 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int r = row + 8 * k;
-          if (r >= rows || !job.out) continue;
-          uint16_t* dst = job.out + (row_at + dir * (c0 + r)) * job.os + h * LIN_D + 16 * warp + 2 * t;
+          if (r >= rows) continue;
+          uint16_t* dst = job.out + (row_at + c0 + r) * job.os + h * LIN_D + 16 * warp + 2 * t;
           *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0][2 * k] * p.scale, o[0][2 * k + 1] * p.scale);
           *reinterpret_cast<uint32_t*>(dst + 8) = pack_bf16x2(o[1][2 * k] * p.scale, o[1][2 * k + 1] * p.scale);
         }
       }
     }
     // the state: decayed, and z^T y with each row's decay on z, to 16 bits of mantissa
-    const float down = sh.power[rows - early];
-    early = 0;
+    const float down = sh.power[rows];
 #pragma unroll
     for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -255,11 +233,10 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
 
   float* to = job.s_out ? job.s_out + state : nullptr;
   if (!to) return;
-  const float up = n > 0 && job.reverse ? job.s_out_factor * sh.power[1] : job.s_out_factor;
 #pragma unroll
   for (int i = 0; i < 16; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) to[(8 * i + 2 * t + (k & 1)) * LIN_D + e0 + 8 * (k >> 1)] = s[i][k] * up;
+    for (int k = 0; k < 4; ++k) to[(8 * i + 2 * t + (k & 1)) * LIN_D + e0 + 8 * (k >> 1)] = s[i][k];
 }
 
 // The states at the segments' ends, from the segments' own parts (in the last
@@ -377,8 +354,7 @@ cudaError_t launch_chunks(const LinParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(lin_chunk_kernel<kOutputs>, smem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(p.n_users * p.H), static_cast<unsigned>(p.n_jobs));
-  return launch_behind(lin_chunk_kernel<kOutputs>, grid, LIN_THREADS, smem, s, p);
+  return launch_behind(lin_chunk_kernel<kOutputs>, dim3(static_cast<unsigned>(p.n_users * p.H)), LIN_THREADS, smem, s, p);
 }
 
 }  // namespace

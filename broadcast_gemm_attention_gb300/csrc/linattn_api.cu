@@ -10,6 +10,7 @@
 
 namespace ikbo {
 cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int* launches);
+cudaError_t launch_linattn_back(LinBackParams p, int num_sms, cudaStream_t s);
 size_t lin_tile_smem();
 cudaError_t launch_lin_read(const LinReadParams& p, int num_sms, cudaStream_t s);
 size_t lin_read_smem();
@@ -21,7 +22,6 @@ using namespace ikbo;
 namespace {
 
 constexpr size_t ANY = ~size_t{0};
-constexpr int64_t INT32_LIMIT = 0x7fffffff;
 
 // A row stride of H heads of 128 elements, 16-byte pieces.
 ikbo_status_t check_stride(int64_t stride, int H) {
@@ -72,8 +72,12 @@ constexpr int LIN_MOST_CUT = 256;
 //   chunks, in registers                   6.9   7.0   7.7   9.2  13.5  17.8  22.2           41.7  42.7  83.8 135.5
 //   chunks, tensor memory                 13.6  13.6  13.9  14.1  14.1  14.1  14.0           75.5  81.6  90.2  79.6
 //   the states alone:  row by row 3.9 4.4 5.8 8.6, in registers 5.3 (8 rows) .. 8.3 (128) 12.0 (256) 18.7 (512), tensor
-//   memory 10.8 (8) .. 10.9 (128) 12.5 (256) 15.6 (512); the gradient of 64 and 128 rows: 22.1 and 35.1, and 24.3 and 25.6
-constexpr int LIN_TILES_FROM[3] = {129, 257, 65};  // forward, states alone, gradient
+//   memory 10.8 (8) .. 10.9 (128) 12.5 (256) 15.6 (512)
+constexpr int LIN_TILES_FROM[2] = {129, 257};  // forward, states alone
+//   gradient, rows             15 users: 1    16    32    48    64    96   400 users: 1    16    32    48    64    96
+//   in one pass                        8.0   8.3  14.0  19.0  24.0  34.1          128.7 146.1 257.5 336.5 425.5 608.5
+//   chunks, tensor memory                         24.8  24.9  25.1  25.4                       432  433.3 438.2 448.1
+constexpr int LIN_BACK_MOST = 64;
 
 void cut_segments(LinParams* lp, int num_sms) {
   const int64_t items = static_cast<int64_t>(lp->n_users) * lp->H * (lp->backward ? LIN_MAX_JOBS : 1);
@@ -92,7 +96,7 @@ void cut_segments(LinParams* lp, int num_sms) {
 ikbo_status_t lin_run(ikbo_plan_t p, LinParams* lp, cudaStream_t stream) {
   if (lin_tile_smem() > p->max_smem) return IKBO_ERR_UNSUPPORTED;
   if (!lp->steps) {
-    lp->tiles = lp->likely_len >= LIN_TILES_FROM[lp->backward ? 2 : (lp->job[0].x ? 0 : 1)];
+    lp->tiles = lp->backward || lp->likely_len >= LIN_TILES_FROM[lp->job[0].x ? 0 : 1];
     if (lp->tiles) cut_segments(lp, p->num_sms);
   }
   if (lp->segs > 1) {
@@ -201,6 +205,38 @@ ikbo_status_t ikbo_linattn_backward(ikbo_plan_t p, const void* Q, const void* K,
   LinParams lp;
   ikbo_status_t st = lin_params(p, d_offsets, n_users, n_rows, max_len, H, d, decay, scale, &lp);
   if (st != IKBO_OK) return st;
+  if (lp.likely_len <= LIN_BACK_MOST) {
+    LinBackParams bp;
+    std::memset(&bp, 0, sizeof(bp));
+    bp.q = static_cast<const uint16_t*>(Q);
+    bp.k = static_cast<const uint16_t*>(K);
+    bp.v = static_cast<const uint16_t*>(V);
+    bp.d_o = static_cast<const uint16_t*>(dO);
+    bp.qs = strides[0];
+    bp.ks = strides[1];
+    bp.vs = strides[2];
+    bp.d_os = strides[3];
+    bp.dq = static_cast<uint16_t*>(dQ);
+    bp.dk = static_cast<uint16_t*>(dK);
+    bp.dv = static_cast<uint16_t*>(dV);
+    bp.dqs = strides[4];
+    bp.dks = strides[5];
+    bp.dvs = strides[6];
+    bp.s_in = state_in;
+    bp.ds_out = d_state_out;
+    bp.ds_in = d_state_in;
+    bp.offsets = d_offsets;
+    bp.decay = decay;
+    bp.status = lp.status;
+    bp.n_users = n_users;
+    bp.n_rows = n_rows;
+    bp.H = H;
+    bp.max_len = lp.max_len;
+    bp.scale = scale;
+    if (launch_linattn_back(bp, p->num_sms, stream) != cudaSuccess) return IKBO_ERR_CUDA;
+    p->launches++;
+    return IKBO_OK;
+  }
   lp.backward = 1;
   const auto add = [&](int x, int y, int z, void* o, int os, const float* s_in, bool turned, float* s_out, bool reverse) {
     LinJob& j = lp.job[lp.n_jobs++];

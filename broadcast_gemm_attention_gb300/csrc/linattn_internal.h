@@ -19,6 +19,7 @@ constexpr int LIN_STATE = LIN_D * LIN_D;      // floats of a state
 constexpr int LIN_MAX_JOBS = 3;
 constexpr int LIN_STEP_MOST = 8;              // rows of a user up to which single steps are taken
 
+
 // One scan: with queries x, keys y and values z,
 //   S <- decay S + y_t z_t^T,   out_t = scale x_t S
 // from the first row of a user to the last, or (reverse) from the last to the
@@ -50,6 +51,22 @@ struct LinParams {
   int tiles;               // the chunks' products on the 5th-gen tensor cores
   uint32_t debug;          // the plan's switches
   uint64_t timeout_ns;
+  float scale;
+};
+
+// The gradient of a few rows a user, at once.
+struct LinBackParams {
+  const uint16_t *q, *k, *v, *d_o;
+  int64_t qs, ks, vs, d_os;        // row strides in elements
+  uint16_t *dq, *dk, *dv;          // null: not wanted
+  int64_t dqs, dks, dvs;
+  const float *s_in, *ds_out;      // null: zero
+  float* ds_in;                    // null: not wanted
+  const int32_t* offsets;
+  const float* decay;
+  uint32_t* status;
+  int n_users, n_rows, H, max_len;
+  int ahead;                       // CTAs that run at a time
   float scale;
 };
 

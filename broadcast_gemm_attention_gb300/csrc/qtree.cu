@@ -33,12 +33,6 @@ namespace {
 constexpr int TR_THREADS = 128;
 constexpr int TR_MOST = 128;  // rows of a draft
 
-__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
-  uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint32_t word(const uint4& x, int i) { return i == 0 ? x.x : (i == 1 ? x.y : (i == 2 ? x.z : x.w)); }
 
 // Bits 15 and 31: whether the halves of x are infinite or NaN (the exponent's

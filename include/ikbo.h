@@ -573,8 +573,9 @@ ikbo_status_t ikbo_linattn_forward(ikbo_plan_t p, const void* Q, const void* K, 
  * Only inputs are read: the states are formed again from state_in.  dQ, dK, dV
  * bf16, d_state_in fp32, overwritten; any may be NULL, and none may overlap an
  * input.  row_strides: 7 values, of Q, K, V, dO, dQ, dK, dV.  The decays are
- * constants.  Chunks of 128 from 65 rows; a gradient does not depend on which others
- * are asked for.  Else as above. */
+ * constants.  Up to 64 rows a user one pass over both states, in blocks of 16 rows (the
+ * same roundings, and 2^-17 for the states' parts), else three scans in chunks of 128; a
+ * gradient does not depend on which others are asked for.  Else as above. */
 ikbo_status_t ikbo_linattn_backward(ikbo_plan_t p, const void* Q, const void* K, const void* V, const void* dO,
                                     const int64_t* row_strides, const int32_t* d_offsets, int n_users, int n_rows,
                                     int max_len, int H, int d, const float* decay, const float* state_in,

@@ -164,6 +164,42 @@ def test_backward(lens, start):
         assert p.status() == B.IKBO_OK
 
 
+@pytest.mark.parametrize("lens,H", [([3, 0, 8, 1, 16, 17, 7, 9, 15], 2), ([64, 33, 48, 31], 3), ([300] + [1, 0, 5, 2] * 12, 1), ([2] * 90, 4)],
+                         ids=["few", "blocks", "one_long", "many"])
+def test_gradient_of_few_rows(lens, H):
+    """In one pass: every set of gradients is the same, and that of the definition."""
+    d = Data(50 + len(lens), lens, H, spare=3)
+    g64 = R.backward(d.Q, d.K, d.V, d.dO, d.decay, d.off, d.S, d.dS, SCALE)
+    mass = R.backward(*(np.abs(x) for x in (d.Q, d.K, d.V, d.dO)), d.decay, d.off, np.abs(d.S), np.abs(d.dS), SCALE)[3]
+    with plan() as p:
+        Q, K, V, decay, off = d.cuda()
+        dO, s_in, ds_out = bf(d.dO), f32(d.S), f32(d.dS)
+        full = None
+        for want in ((1, 1, 1, 1), (1, 0, 0, 0), (0, 1, 0, 0), (0, 0, 1, 0), (0, 0, 0, 1), (1, 1, 1, 0)):
+            outs = [torch.full_like(Q, 5.0) if w else None for w in want[:3]] + [torch.full_like(s_in, float("nan")) if want[3] else None]
+            before = p.launches()
+            p.linattn_backward(Q, K, V, dO, decay, *outs[:3], state_in=s_in, d_state_out=ds_out, d_state_in=outs[3], offsets=off)
+            assert p.launches() == before + 1
+            if full is None:
+                full = outs
+                n = int(d.off[-1])
+                for got, ref, name in zip(outs, g64, ("dQ", "dK", "dV")):
+                    near(got[:n], ref[:n], name)
+                    assert torch.all(got[n:] == 5.0)
+                near_state(outs[3], g64[3], mass)
+            for got, same in zip(outs, full):
+                assert got is None or torch.equal(got, same)
+        # without states
+        outs, dS = [torch.empty_like(Q) for _ in range(3)], torch.full_like(s_in, float("nan"))
+        p.linattn_backward(Q, K, V, dO, decay, *outs, d_state_in=dS, offsets=off)
+        zero = np.zeros_like(d.S)
+        ref = R.backward(d.Q, d.K, d.V, d.dO, d.decay, d.off, zero, zero, SCALE)
+        for got, want, name in zip(outs, ref, ("dQ", "dK", "dV")):
+            near(got[:n], want[:n], name)
+        near_state(dS, ref[3], mass)
+        assert p.status() == B.IKBO_OK
+
+
 @pytest.mark.parametrize("lens,H", [([2000], 1), ([900, 0, 2500], 2)], ids=str)
 def test_histories_in_segments(lens, H):
     """Few long histories are cut; the start comes in and the end goes out in place."""
