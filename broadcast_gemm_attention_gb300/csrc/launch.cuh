@@ -1,5 +1,5 @@
 // launch.cuh -- launches that are set up while the kernel before them in the stream
-// ends (programmatic stream serialisation).
+// ends (programmatic stream serialisation), and kernels' shared memory.
 //
 // Such a kernel's CTAs start as the last ones of the kernel before leave, instead of
 // after all it wrote has been made visible: 2.5 us a call between other kernels on one
@@ -10,6 +10,9 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cstdint>
+
 namespace ikbo {
 
 // Every thread of a kernel launched by launch_behind calls this before it touches global
@@ -18,6 +21,20 @@ namespace ikbo {
 // at most barriers and shared memory are set up (and what no kernel just before may
 // write is read); tensor memory is not taken, which a kernel that still runs may be waiting for.
 __device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets a kernel use `bytes` of dynamic shared memory, once on each device (asking each
+// time took half a microsecond of a call).  `done` is the kernel's own.
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 template <typename... Params, typename... Args>
 inline cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args&... args) {

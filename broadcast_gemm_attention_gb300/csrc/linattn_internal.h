@@ -4,8 +4,6 @@
 #pragma once
 #include <cuda_runtime.h>
 
-#include <atomic>
-
 #include "ikbo_internal.h"
 
 namespace ikbo {
@@ -69,20 +67,6 @@ struct LinBackParams {
   int ahead;                       // CTAs that run at a time
   float scale;
 };
-
-// Lets a kernel use `bytes` of dynamic shared memory, once on each device (asking each
-// time took half a microsecond of a call).  `done` is the kernel's own.
-template <typename F>
-cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
 
 struct LinReadParams {
   const uint16_t* x;        // rows [n_cand][H][Lq][128]

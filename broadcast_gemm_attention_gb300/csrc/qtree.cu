@@ -11,12 +11,12 @@
 // rounded to bf16 (2^-9 of it, once more than O): an fp32 image of it would be
 // a quarter of this kernel's bytes at a request's sizes.
 //
-// The draft's K and V are a few rows of bf16, read once per 16 query rows, and
+// The draft's K and V are a few rows of bf16, read once per 16 query rows (or, above 16, once a CTA), and
 // the products are small: bound by memory and latency.  Measured: 1024 drafts of 16
 // rows, 8 heads, 31 us, 5.4 TB/s (three CTAs an SM, whose registers spill: 7 us more);
 // 64 of 32 rows 12 us; one of 8 rows 5.8 us.
 //
-// A warp takes 16 rows of one K/V head by itself and nothing goes through shared memory but the tree:
+// A warp takes 16 rows of one K/V head by itself:
 // the inner order of Q K^T is free, so queries and keys are loaded as 16-byte
 // pieces (element 32 j + 8 t + 4 f + .. for lane t), and so is the order of V's
 // columns, so that V is loaded the same way, turned by 8x8 transposes, and every
@@ -32,6 +32,7 @@ namespace {
 
 constexpr int TR_THREADS = 128;
 constexpr int TR_MOST = 128;  // rows of a draft
+constexpr int TR_SHARED_CTAS = 3;  // an SM
 
 __device__ __forceinline__ uint32_t word(const uint4& x, int i) { return i == 0 ? x.x : (i == 1 ? x.y : (i == 2 ? x.z : x.w)); }
 
@@ -109,8 +110,18 @@ __device__ void large_tree(const QcTreeParams& p, int cand, Tree& tr) {
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(TR_THREADS, 2) qtree_kernel(const QcTreeParams p) {
+// Place of 16-byte piece c of row r of a draft's keys or values in shared memory: a quarter
+// warp reads four pieces of two rows, which lie in different halves of the banks.
+__device__ __forceinline__ uint32_t piece_at(int r, int c) { return static_cast<uint32_t>(r * 256 + ((c ^ ((r & 1) << 2)) << 4)); }
+
+// kShared: a CTA has one K/V head of a draft, whose keys and values are in shared memory, for drafts
+// of more than 16 rows (whose warps wait for one block of 16 after the other else: 60 drafts of 128 rows,
+// 32 heads over 8, 156 us with the history for 193, 335 of 64 rows 92 for 106, 216 of 24 65 for 70).  By
+// turned 8x8 loads of words laid out for them, and 2, 4 CTAs an SM, no faster.
+template <bool kShared>
+__global__ void __launch_bounds__(TR_THREADS, kShared ? TR_SHARED_CTAS : 2) qtree_kernel(const QcTreeParams p) {
   __shared__ Tree tr;
+  extern __shared__ __align__(128) uint8_t kv[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int cand = static_cast<int>(blockIdx.x);
   const int u = __ldg(p.map + cand);
@@ -118,15 +129,26 @@ __global__ void __launch_bounds__(TR_THREADS, 2) qtree_kernel(const QcTreeParams
     wait_for_launch_before();
     return;
   }
-  const int rows = p.group * p.Lq, tiles = (rows + 15) >> 4, items = tiles * p.H_kv;
+  const int rows = p.group * p.Lq, tiles = (rows + 15) >> 4, items = kShared ? tiles : tiles * p.H_kv;
+  const int parts = kShared ? static_cast<int>(gridDim.y) / p.H_kv : static_cast<int>(gridDim.y);
+  const int head = kShared ? static_cast<int>(blockIdx.y) / parts : 0, part = static_cast<int>(blockIdx.y) - head * parts;
+  const int padded = (p.Lq + 15) & ~15;
+  if (kShared) {
+    for (int i = threadIdx.x; i < padded * 32; i += TR_THREADS) {
+      const int of = i >= padded * 16 ? 1 : 0, e = i - of * padded * 16, row = e >> 4, c = e & 15;
+      const uint16_t* from = (of ? p.V : p.K) + static_cast<int64_t>(cand) * p.cand_stride + head * QC_D + 8 * c;
+      copy16(smem_u32(kv) + of * padded * 256 + piece_at(row, c), row < p.Lq ? from + row * p.row_stride : from, row < p.Lq);
+    }
+    copies_commit();
+  }
   const bool small = p.Lq <= 32;
   const int up = small && lane < p.Lq ? parent(p, cand, lane) : -1;
   uint32_t line = 0;
   bool built = false;
 #pragma unroll 1
-  for (int first = static_cast<int>(blockIdx.y) * 4; first < items; first += static_cast<int>(gridDim.y) * 4) {
+  for (int first = part * 4; first < items; first += parts * 4) {
     const int item = min(first + warp, items - 1);  // (the last item's warps again: they store nothing)
-    const int hk = item / tiles, tile = item - hk * tiles;
+    const int hk = kShared ? head : item / tiles, tile = kShared ? item : item - hk * tiles;
     const int64_t row0 = (static_cast<int64_t>(cand) * p.H + hk * p.group) * p.Lq + 16 * tile;
     const int r0 = 16 * tile + g;
     const bool here[2] = {r0 < rows, r0 + 8 < rows};
@@ -134,14 +156,20 @@ __global__ void __launch_bounds__(TR_THREADS, 2) qtree_kernel(const QcTreeParams
     const uint16_t* vp = p.V + static_cast<int64_t>(cand) * p.cand_stride + hk * QC_D + 8 * t;
     uint4 k[2][4], v[2][4];
     const auto fetch = [&](const uint16_t* from, int k0, uint4 (&to)[2][4]) {
+      const uint8_t* at = kv + (from == vp ? padded * 256 : 0);
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          to[n][j] = k0 + 8 * n + g < p.Lq ? __ldg(reinterpret_cast<const uint4*>(from + (k0 + 8 * n + g) * p.row_stride + 32 * j)) : uint4{};
+        for (int j = 0; j < 4; ++j) {
+          const int row = k0 + 8 * n + g;
+          if (kShared) to[n][j] = *reinterpret_cast<const uint4*>(at + piece_at(row, 4 * j + t));
+          else to[n][j] = row < p.Lq ? __ldg(reinterpret_cast<const uint4*>(from + row * p.row_stride + 32 * j)) : uint4{};
+        }
     };
-    fetch(kp, 0, k);
-    fetch(vp, 0, v);
+    if (!kShared) {
+      fetch(kp, 0, k);
+      fetch(vp, 0, v);
+    }
     uint4 q[2][4] = {};
 #pragma unroll
     for (int e = 0; e < 2; ++e)
@@ -172,6 +200,10 @@ __global__ void __launch_bounds__(TR_THREADS, 2) qtree_kernel(const QcTreeParams
       if (small) line = small_tree(p, up, lane);
       else large_tree(p, cand, tr);
     }
+    if (kShared && !built) {
+      copies_wait<0>();
+      __syncthreads();
+    }
     built = true;
     const int l0 = r0 % p.Lq, l1 = (r0 + 8) % p.Lq;
     uint4 sees[2] = {};
@@ -186,9 +218,9 @@ __global__ void __launch_bounds__(TR_THREADS, 2) qtree_kernel(const QcTreeParams
     const int n_keys = min(p.Lq, 16 * tile % p.Lq + 16);  // up to the tile's last row (all, where it goes on in the next head)
 #pragma unroll 1
     for (int k0 = 0; k0 < n_keys; k0 += 16) {
-      if (k0 > 0) {
+      if (kShared || k0 > 0) {
         fetch(kp, k0, k);
-        fetch(vp, k0, v);
+        if (!kShared) fetch(vp, k0, v);
       }
       float s[2][4] = {};
 #pragma unroll
@@ -236,6 +268,7 @@ __global__ void __launch_bounds__(TR_THREADS, 2) qtree_kernel(const QcTreeParams
           o[i][2 * e + 1] *= keep;
         }
       }
+      if (kShared) fetch(vp, k0, v);
       // rows of V with an infinity or NaN stay out of the product, where they would
       // reach rows that do not read them (0 times infinity), and are added after it
       uint32_t odd[2];
@@ -303,12 +336,20 @@ __global__ void __launch_bounds__(TR_THREADS, 2) qtree_kernel(const QcTreeParams
 }  // namespace
 
 cudaError_t launch_qtree(const QcTreeParams& p, int num_sms, cudaStream_t s) {
-  const int items = ((p.group * p.Lq + 15) / 16) * p.H_kv;
-  // a CTA takes four items of a candidate, more where there are CTAs enough (1024 drafts of 8 items 177.6 us, with the
-  // history, for 179.7: the tree is found once); set up while the history's last CTAs end (85.9 -> 83.9, 177.1 -> 174.5)
+  const bool shared = p.Lq > 16;
+  const int heads = shared ? p.H_kv : 1, items = ((p.group * p.Lq + 15) / 16) * (shared ? 1 : p.H_kv);
+  // a CTA takes four items of a candidate (of one K/V head), more where there are CTAs enough (1024 drafts of 8 items
+  // 177.6 us, with the history, for 179.7: the tree is found once); set up while the history's last CTAs end (85.9 -> 83.9,
+  // 177.1 -> 174.5)
   int parts = (items + 3) / 4;
-  while (parts > 1 && static_cast<int64_t>(parts / 2) * p.n_cand >= 4 * static_cast<int64_t>(num_sms)) parts = (parts + 1) / 2;
-  return launch_behind(qtree_kernel, dim3(static_cast<unsigned>(p.n_cand), static_cast<unsigned>(parts)), TR_THREADS, 0, s, p);
+  while (parts > 1 && static_cast<int64_t>(parts / 2) * heads * p.n_cand >= 4 * static_cast<int64_t>(num_sms)) parts = (parts + 1) / 2;
+  const dim3 grid(static_cast<unsigned>(p.n_cand), static_cast<unsigned>(parts * heads));
+  if (!shared) return launch_behind(qtree_kernel<false>, grid, TR_THREADS, 0, s, p);
+  static std::atomic<uint64_t> done{0};
+  const int bytes = 2 * ((p.Lq + 15) / 16 * 16) * QC_D * 2;
+  const cudaError_t e = allow_smem(qtree_kernel<true>, 2 * TR_MOST * QC_D * 2, done);
+  if (e != cudaSuccess) return e;
+  return launch_behind(qtree_kernel<true>, grid, TR_THREADS, bytes, s, p);
 }
 
 }  // namespace ikbo

@@ -270,3 +270,18 @@ def test_inputs_that_change_right_before_and_after_a_call():
             graph.replay()
         torch.cuda.synchronize()
         assert p.status() == B.IKBO_OK and int(wrong) == 0
+
+
+@pytest.mark.parametrize("Lq,H,H_kv", [(24, 4, 4), (40, 8, 4), (56, 6, 1), (104, 4, 2)])
+def test_long_drafts_whose_keys_are_shared(Lq, H, H_kv):
+    """More CTAs than fit, rows that are slices of one projection, sizes that are no multiples of a block (Lq is a multiple of 8)."""
+    rng = np.random.default_rng(Lq)
+    m = rng.integers(0, 3, 90).astype(np.int32)
+    c = Case(60 + Lq, [120, 0, 37], m, H, H_kv, Lq, 16, branch=5)
+    with plan() as p:
+        O, lse = c.run(p)
+        c.check(O, lse)
+        kv = torch.stack([bf(c.K), bf(c.V)], dim=2).contiguous()
+        O2, lse2 = c.run(p, K=kv[:, :, 0], V=kv[:, :, 1])
+        assert torch.equal(O, O2) and torch.equal(lse, lse2)
+        assert p.status() == B.IKBO_OK
