@@ -14,7 +14,7 @@
 //   dS += Q^T dO  (backward) into tensor memory over all of a run of units of one
 //                 (user, head), both operands MN-major: rows are the inner dimension.
 // One pass over the rows serves both gradients.  Bound: memory, and each CTA's start.
-// 1024 candidates of 15 users, 8 heads x 32 rows: 29.4 us with the plan's launch, 4.8 TB/s
+// 1024 candidates of 15 users, 8 heads x 32 rows: 29.4 us among other calls, 4.8 TB/s
 // (16x8x16 products in registers: 107); the gradient of 1024 candidates of 64 users
 // unevenly, 8 heads x 16 rows: 45.8 us, 3.7 TB/s (138), 6 of it the parts' adding.
 //
