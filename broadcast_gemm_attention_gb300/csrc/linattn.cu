@@ -239,9 +239,11 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
     for (int k = 0; k < 4; ++k) to[(8 * i + 2 * t + (k & 1)) * LIN_D + e0 + 8 * (k >> 1)] = s[i][k];
 }
 
+constexpr int JOIN_AHEAD = 32;  // parts on their way at a time
+
 // The states at the segments' ends, from the segments' own parts (in the last
-// one's place, which has no part, the start).  Bound: latency, a chain of loads over
-// the segments; 8 of the 85 us of two users' 20000 and 30001 rows, 4 heads.
+// one's place, which has no part, the start).  Bound: latency; a user's parts are
+// on their way together (by eights two users' 20000 and 30001 rows, 4 heads, 83.9 us, so 82.9).
 __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ LinParams p) {
   wait_for_launch_before();
   constexpr int kParts = LIN_STATE / 256;
@@ -261,11 +263,18 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ L
   const float log2_decay = log2f(__ldg(p.decay + h));
   const float down = lin_power(log2_decay, p.seg_len);
   s *= job.reverse ? lin_power(log2_decay, p.seg_len - 1) : down;
-#pragma unroll 8
-  for (int k = 0; k + 1 < segs; ++k) {
-    s += ws[static_cast<int64_t>(k) * LIN_STATE];
-    ws[static_cast<int64_t>(k) * LIN_STATE] = s;
-    s *= down;
+#pragma unroll 1
+  for (int k0 = 0; k0 + 1 < segs; k0 += JOIN_AHEAD) {
+    float part[JOIN_AHEAD];
+#pragma unroll
+    for (int k = 0; k < JOIN_AHEAD; ++k) part[k] = k0 + k + 1 < segs ? __ldcg(ws + static_cast<int64_t>(k0 + k) * LIN_STATE) : 0.f;
+#pragma unroll
+    for (int k = 0; k < JOIN_AHEAD; ++k) {
+      if (k0 + k + 1 >= segs) break;
+      s += part[k];
+      ws[static_cast<int64_t>(k0 + k) * LIN_STATE] = s;
+      s *= down;
+    }
   }
 }
 
@@ -362,7 +371,7 @@ cudaError_t launch_chunks(const LinParams& p, cudaStream_t s) {
 cudaError_t launch_lin_tiles(const LinParams& p, bool local, int num_sms, cudaStream_t s);
 
 // Launches: one, or three where histories are cut into segments (two users' 20000
-// and 30001 rows 84.5 us).
+// and 30001 rows 82.9 us).
 cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int* launches) {
   *launches = 0;
   const bool outputs = p.job[0].x != nullptr;
