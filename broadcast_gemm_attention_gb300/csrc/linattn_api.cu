@@ -60,7 +60,10 @@ ikbo_status_t lin_params(ikbo_plan_t p, const int32_t* d_offsets, int n_users, i
 // (and multiplied) once more, for the states between them.  With fewer scans than
 // half the SMs, segments are as long as makes one for each SM; else only rows far
 // above a CTA's share are cut, as where one user's history is much longer than the
-// others'.  At most LIN_MOST_STATES states lie between segments, and with more than
+// others'.  In us, of a scan of L rows 6 + 0.0195 L whole, 13 + 0.041 seg + 0.07 (states between
+// segments) cut; the states alone 5 + 0.012 L and 10.8 + 0.0265 seg + 0.072 states (measured from 400 to
+// 6000 rows and 4 to 76 scans: 16 scans of 1152 rows 29 and 29, of 4096 86 and 43; 40 of 2048 48 and 56, of
+// 6000 126 and 104; 60 of 4096 89 and 122).  At most LIN_MOST_STATES states lie between segments, and with more than
 // LIN_MOST_CUT users none is cut (each item looks for its place among all users').
 constexpr int64_t LIN_MOST_STATES = 16384;  // 1 GiB
 constexpr int LIN_LEAST_SEGMENT = 256;
@@ -88,7 +91,8 @@ void cut_segments(LinParams* lp, int num_sms) {
   if (most < 2 || lp->n_users > LIN_MOST_CUT) return;
   seg = std::max(seg, (lp->max_len + most - 1) / most);
   seg = (seg + 127) / 128 * 128;
-  if (lp->likely_len <= seg + seg / 2) return;
+  const int64_t states = items * ((lp->likely_len + seg - 1) / seg);
+  if (lp->likely_len <= (lp->job[0].x ? 360 + 21 * seg / 10 + 36 * states / 10 : 480 + 22 * seg / 10 + 6 * states)) return;
   lp->seg_len = static_cast<int>(seg);
   lp->segs = static_cast<int>((lp->max_len + seg - 1) / seg);
 }
