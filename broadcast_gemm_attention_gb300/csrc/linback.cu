@@ -36,6 +36,7 @@ namespace {
 constexpr int LB_THREADS = 256;
 constexpr int LB_ROWS = 16;                       // of a block
 constexpr int LB_TILE = LB_ROWS * LIN_D * 2;      // bytes of a block of q, k, v or do
+constexpr int LB_ASK = 128;                       // rows asked for at once
 constexpr int LB_SUM = LIN_D + 8;                 // (rows of sums eight banks apart)
 enum { LB_Q, LB_K, LB_V, LB_DO };
 
@@ -179,6 +180,13 @@ __global__ void __launch_bounds__(LB_THREADS, 2) lin_back_kernel(const __grid_co
   const int64_t later = static_cast<int64_t>(blockIdx.x) + p.ahead;
   const float* start = p.dq ? p.s_in : p.ds_out;
   if (start && later < static_cast<int64_t>(p.n_users) * p.H && tid == 32) ask(start + later * LIN_STATE);
+  // later blocks' rows too, a 128-byte line a thread (400 users' 24 rows 246 -> 229 us, 64 rows 428 -> 417)
+  for (int i = LB_ROWS * 8 + tid; i < min(len, LB_ASK) * 8; i += LB_THREADS) {
+    const int of = (i >> 1) & 3;
+    const uint16_t* src = of == LB_Q ? p.q : (of == LB_K ? p.k : (of == LB_V ? p.v : p.d_o));
+    const int64_t stride = of == LB_Q ? p.qs : (of == LB_K ? p.ks : (of == LB_V ? p.vs : p.d_os));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (static_cast<int64_t>(first) + (i >> 3)) * stride + h * LIN_D + 64 * (i & 1)) : "memory");
+  }
   const float log2_decay = log2f(__ldg(p.decay + h));
   if (tid <= LB_ROWS) sh.power[tid] = tid == 0 ? 1.f : exp2f(static_cast<float>(tid) * log2_decay);
   const auto power = [&](int n) { return n >= 0 ? sh.power[n] : 0.f; };
