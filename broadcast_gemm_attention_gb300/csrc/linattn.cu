@@ -108,6 +108,10 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
   float s[16][4];
   const int64_t state = (static_cast<int64_t>(u) * p.H + h) * LIN_STATE;
   const float* from = job.s_in ? job.s_in + state : nullptr;
+  // the start of a scan that begins when this one ends, to L2 (400 users of 24 rows 150 -> 130 us, of 64 191 -> 165)
+  const int64_t later = static_cast<int64_t>(blockIdx.x) + p.ahead;
+  if (job.s_in && tid == 0 && later < static_cast<int64_t>(p.n_users) * p.H)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(job.s_in + later * LIN_STATE), "n"(LIN_STATE * 4) : "memory");
   const int e0 = 16 * warp + g;
 #pragma unroll
   for (int i = 0; i < 16; ++i)

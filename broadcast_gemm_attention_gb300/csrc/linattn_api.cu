@@ -110,6 +110,7 @@ ikbo_status_t lin_run(ikbo_plan_t p, LinParams* lp, cudaStream_t stream) {
     if (grow_kept<false>(p, &p->lin_states, need, ANY, capturing, stream) != cudaSuccess) return IKBO_ERR_CUDA;
     lp->ws = p->lin_states.ptr;
   }
+  lp->ahead = p->num_sms;
   int launches = 0;
   const cudaError_t e = launch_linattn(*lp, p->num_sms, stream, &launches);
   p->launches += launches;

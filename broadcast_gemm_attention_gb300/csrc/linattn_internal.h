@@ -47,6 +47,7 @@ struct LinParams {
   int backward;            // the jobs are a gradient's (variants do not go by which of them are asked for)
   int steps;               // rows one by one (a forward scan alone)
   int tiles;               // the chunks' products on the 5th-gen tensor cores
+  int ahead;               // in registers: the scan whose state is asked for in L2 meanwhile is this many later
   uint32_t debug;          // the plan's switches
   uint64_t timeout_ns;
   float scale;
