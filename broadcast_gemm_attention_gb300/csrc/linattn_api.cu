@@ -70,10 +70,10 @@ constexpr int LIN_LEAST_SEGMENT = 256;
 constexpr int LIN_MOST_CUT = 256;
 
 // The variant, from the bound on a user's rows (every variant takes any length).  Measured, 8 heads (us):
-//   forward, rows           15 users:  4     8    16    32    64   128   192   256   100 users: 8    16   128   256
-//   row by row                       4.4   5.8   8.3  13.7                                   29.0  40.6
-//   chunks, in registers                   6.9   7.0   7.7   9.2  13.5  17.8  22.2           41.7  42.7  83.8 135.5
-//   chunks, tensor memory                 13.6  13.6  13.9  14.1  14.1  14.1  14.0           75.5  81.6  90.2  79.6
+//   forward, rows           15 users:  4     8    16    32    64   128   160   256   100 users: 8    16   128   160   256
+//   row by row                       4.3   5.7   8.3  13.7                                   28.4  40.6
+//   chunks, in registers                   6.0   6.1   6.9   8.2  12.1  14.7  20.3           31.9  32.9  70.3  85.9 118.3
+//   chunks, tensor memory                 13.6  13.6  13.9  14.1  14.1  14.0  14.6           75.5  81.6  90.2  75.8  80.9
 //   the states alone:  row by row 3.9 4.4 5.8 8.6, in registers 5.3 (8 rows) .. 8.3 (128) 12.0 (256) 18.7 (512), tensor
 //   memory 10.8 (8) .. 10.9 (128) 12.5 (256) 15.6 (512)
 constexpr int LIN_TILES_FROM[2] = {129, 257};  // forward, states alone
@@ -91,7 +91,7 @@ void cut_segments(LinParams* lp, int num_sms) {
   if (most < 2 || lp->n_users > LIN_MOST_CUT) return;
   seg = std::max(seg, (lp->max_len + most - 1) / most);
   seg = (seg + 127) / 128 * 128;
-  const int64_t states = items * ((lp->likely_len + seg - 1) / seg);
+  const int64_t states = std::min(items * ((lp->likely_len + seg - 1) / seg), rows / seg + items);
   if (lp->likely_len <= (lp->job[0].x ? 360 + 21 * seg / 10 + 36 * states / 10 : 480 + 22 * seg / 10 + 6 * states)) return;
   lp->seg_len = static_cast<int>(seg);
   lp->segs = static_cast<int>((lp->max_len + seg - 1) / seg);
