@@ -54,7 +54,7 @@ __device__ __forceinline__ int user_rows(const LinBackParams& p, int u, int& fir
     first = u * each;
     return each;
   }
-  const int a = __ldg(p.offsets + u), b = __ldg(p.offsets + u + 1);
+  const int a = __ldcg(p.offsets + u), b = __ldcg(p.offsets + u + 1);
   first = a;
   if (a >= 0 && b >= a && b <= p.n_rows && b - a <= p.max_len) return b - a;
   if (threadIdx.x == 0) atomicOr(p.status, DEV_ERR_CACHE);
@@ -73,8 +73,8 @@ __device__ __forceinline__ void load_rows(const LinBackParams& p, BackShared& sh
     uint4 a = {}, b = {};
     if (r < n) {
       const uint4* from = reinterpret_cast<const uint4*>(src + (first + r) * stride + h * LIN_D) + 2 * c;
-      a = __ldg(from);
-      b = __ldg(from + 1);
+      a = __ldcg(from);
+      b = __ldcg(from + 1);
     }
     const bool mixed = t >= LB_V;
     *reinterpret_cast<uint4*>(sh.rows[t] + place(r, 2 * c)) = mixed ? make_uint4(a.x, a.z, b.x, b.z) : a;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(LB_THREADS, 2) lin_back_kernel(const __grid_co
     const int64_t stride = of == LB_Q ? p.qs : (of == LB_K ? p.ks : (of == LB_V ? p.vs : p.d_os));
     asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (static_cast<int64_t>(first) + (i >> 3)) * stride + h * LIN_D + 64 * (i & 1)) : "memory");
   }
-  const float log2_decay = log2f(__ldg(p.decay + h));
+  const float log2_decay = log2f(__ldcg(p.decay + h));
   if (tid <= LB_ROWS) sh.power[tid] = tid == 0 ? 1.f : exp2f(static_cast<float>(tid) * log2_decay);
   const auto power = [&](int n) { return n >= 0 ? sh.power[n] : 0.f; };
 #pragma unroll 1

@@ -75,7 +75,7 @@ struct Walk {
     b = x.end;
     next = a < b ? unit(p, a) : make_int4(-1, -1, 0, 0);
   }
-  __device__ __forceinline__ static int4 unit(const LinReadParams& p, int i) { return __ldg(reinterpret_cast<const int4*>(p.work) + i); }
+  __device__ __forceinline__ static int4 unit(const LinReadParams& p, int i) { return fresh(reinterpret_cast<const int4*>(p.work) + i); }
   // To unit i; false (to every role alike) where the list is not sound, which ends the share.
   __device__ __forceinline__ bool at(const LinReadParams& p, int i) {
     w = next;
@@ -93,7 +93,7 @@ struct Walk {
   }
   // The candidate of place k of unit w (0 for none).
   __device__ __forceinline__ static int cand(const LinReadParams& p, const int4& w, int k) {
-    return k < w.w && w.z >= 0 && w.z + k < p.n_cand ? __ldg(p.perm + w.z + k) : 0;
+    return k < w.w && w.z >= 0 && w.z + k < p.n_cand ? fresh(p.perm + w.z + k) : 0;
   }
 };
 
@@ -113,12 +113,12 @@ __device__ __forceinline__ int share_of(uint32_t cost, uint32_t total) {
 }
 
 __device__ __forceinline__ uint32_t listed_units(const LinReadParams& p) {
-  return static_cast<uint32_t>(max(0, min(__ldg(p.n_units), static_cast<int>(p.max_units))));
+  return static_cast<uint32_t>(max(0, min(fresh(p.n_units), static_cast<int>(p.max_units))));
 }
 
 // Units of user u for each head.
 __device__ __forceinline__ uint32_t units_of(const LinReadParams& p, int u, uint32_t cands) {
-  const int count = __ldg(p.offsets + u + 1) - __ldg(p.offsets + u);
+  const int count = fresh(p.offsets + u + 1) - fresh(p.offsets + u);
   return count > 0 ? (static_cast<uint32_t>(count) + cands - 1) / cands : 0u;
 }
 
@@ -300,7 +300,7 @@ __device__ void image_warps(const LinReadParams& p, uint8_t* sm, Aux& x) {
   if (kBack) {  // users without candidates
     for (int64_t uh = blockIdx.x; uh < static_cast<int64_t>(p.n_users) * p.H; uh += gridDim.x) {
       const int u = static_cast<int>(uh / p.H);
-      if (__ldg(p.offsets + u + 1) > __ldg(p.offsets + u)) continue;
+      if (fresh(p.offsets + u + 1) > fresh(p.offsets + u)) continue;
 #pragma unroll 4
       for (int e = tid; e < LIN_STATE / 4; e += 32 * GROUP_WARPS) reinterpret_cast<float4*>(p.d_state + uh * LIN_STATE)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -316,7 +316,7 @@ __device__ void image_warps(const LinReadParams& p, uint8_t* sm, Aux& x) {
     uint8_t* to = sm + IMAGE_AT + rb * TILE + (lane >> 4) * HALF_TILE + (lane & 1) * 8;
     float4 v[16];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) v[c] = __ldg(s + (8 * c + warp) * 32);
+    for (int c = 0; c < 16; ++c) v[c] = fresh(s + (8 * c + warp) * 32);
     if (warp == 0) {  // the next run's state is on its way to L2 meanwhile (47.1 -> 45.8 us)
       while (j < ahead.b && ahead.runs <= k.runs && ahead.at(p, j)) ++j;
       if (ahead.runs > k.runs && elect_one())
@@ -346,8 +346,8 @@ __device__ void find_shared(const LinReadParams& p, Aux& x) {
     const int i = k == 0 ? a : b - 1;
     const int4 w = a < b ? Walk::unit(p, i) : make_int4(-1, -1, 0, 0);
     if (w.x >= 0 && w.x < p.n_users) {
-      const int first = __ldg(p.offsets + w.x);
-      const int lo = i - (w.z - first) / cands, hi = lo + (__ldg(p.offsets + w.x + 1) - first + cands - 1) / cands;  // its units
+      const int first = fresh(p.offsets + w.x);
+      const int lo = i - (w.z - first) / cands, hi = lo + (fresh(p.offsets + w.x + 1) - first + cands - 1) / cands;  // its units
       if ((lo < a || hi > b) && lo != done && lo >= 0 && hi <= n) {
         done = lo;
         uint32_t cost = static_cast<uint32_t>(lo), total = static_cast<uint32_t>(n);
@@ -356,7 +356,7 @@ __device__ void find_shared(const LinReadParams& p, Aux& x) {
 #pragma unroll 4
           for (int v = 0; v < w.x; v += 32) {
             const int u = min(v + static_cast<int>(lane_id()), w.x);
-            users += __popc(__ballot_sync(0xffffffffu, u < w.x && __ldg(p.offsets + u + 1) > __ldg(p.offsets + u)));
+            users += __popc(__ballot_sync(0xffffffffu, u < w.x && fresh(p.offsets + u + 1) > fresh(p.offsets + u)));
           }
           cost += static_cast<uint32_t>(users * p.H + w.y);
           total = x.total;
@@ -435,7 +435,7 @@ __device__ void output_warps(const LinReadParams& p, uint8_t* sm, Aux& x, uint32
         const int4 n = Walk::unit(p, j);
         return n.x == k.u && n.y == k.h;
       };
-      const int64_t n = min(static_cast<int64_t>(__ldg(p.n_units)), p.max_units);
+      const int64_t n = min(static_cast<int64_t>(fresh(p.n_units)), p.max_units);
       const bool begun = r > 0 || k.a == 0 || !same(k.a - 1), whole = begun && (i + 1 < k.b || i + 1 >= n || !same(i + 1));
       float* to = whole ? p.d_state + (static_cast<int64_t>(k.u) * p.H + k.h) * LIN_STATE
                         : p.part + (2 * static_cast<int64_t>(blockIdx.x) + (begun ? 1 : 0)) * LIN_STATE;

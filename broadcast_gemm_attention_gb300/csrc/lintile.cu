@@ -91,7 +91,7 @@ __device__ __forceinline__ int user_rows(const LinParams& p, int u, int& first, 
     first = u * each;
     return each;
   }
-  const int a = __ldg(p.offsets + u), b = __ldg(p.offsets + u + 1);
+  const int a = __ldcg(p.offsets + u), b = __ldcg(p.offsets + u + 1);
   first = a;
   if (a >= 0 && b >= a && b <= p.n_rows && b - a <= p.max_len) return b - a;
   if (report) atomicOr(p.status, DEV_ERR_CACHE);
@@ -436,7 +436,7 @@ __device__ void decay_warps(const LinParams& p, Aux& x, uint32_t tmem) {
   Items<kLocal> items(p);
   for (Item it; items.next(p, it, false);) {
     if (it.chunks == 0) continue;
-    const float log2_decay = log2f(__ldg(p.decay + it.h));
+    const float log2_decay = log2f(__ldcg(p.decay + it.h));
     if (!group_sync(&x.group[0], meet, x, p)) return;
     if (tid < LT_CHUNK) x.power[tid] = decay_power(log2_decay, tid) * p.scale;
     if (tid < 16) reinterpret_cast<float*>(x.near)[tid] = decay_power(log2_decay, it.reverse ? tid : 15 - tid);
@@ -501,7 +501,7 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t t
   Items<kLocal> items(p);
   for (Item it; items.next(p, it, false);) {
     const LinJob& job = p.job[it.job];
-    const float log2_decay = log2f(__ldg(p.decay + it.h));
+    const float log2_decay = log2f(__ldcg(p.decay + it.h));
     for (int c = 0; c < it.chunks; ++c, ++g) {
       const int rows = it.rows(c);
       const float w1 = decay_power(log2_decay, max(it.reverse ? rows - i_row - (c == 0 ? it.early : 0) : i_row + 1, 0)) * p.scale;
@@ -560,7 +560,7 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tm
   Items<kLocal> items(p);
   for (Item it; items.next(p, it, threadIdx.x == 32 * STATE_WARP0);) {
     const LinJob& job = p.job[it.job];
-    const float log2_decay = log2f(__ldg(p.decay + it.h));
+    const float log2_decay = log2f(__ldcg(p.decay + it.h));
     const int64_t state = (static_cast<int64_t>(it.u) * p.H + it.h) * LIN_STATE;
     const int64_t ws = ((static_cast<int64_t>(it.job) * p.n_users + it.u) * p.H + it.h) * p.segs;
     bool turned;
@@ -668,7 +668,7 @@ __device__ void parts_warps(const LinParams& p, uint8_t* sm, Aux& x) {
   for (Item it; items.next(p, it, false);) {
     if (it.chunks == 0) continue;
     static_assert(kThreads == LT_CHUNK, "a decay a thread");
-    const float log2_decay = log2f(__ldg(p.decay + it.h));
+    const float log2_decay = log2f(__ldcg(p.decay + it.h));
     for (int c = 0; c < it.chunks; ++c, ++g) {
       const uint32_t ph = g & 1u;
       const int rows = it.rows(c);

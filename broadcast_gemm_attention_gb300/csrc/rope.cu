@@ -72,7 +72,7 @@ template <bool kAxes>
 __device__ __forceinline__ bool position(const RopeParams& p, int i, int l, Place<kAxes>* pos) {
   int src = i;
   if (p.map) {
-    src = __ldg(p.map + i);
+    src = kAxes ? p.map[i] : __ldg(p.map + i);
     if (src < 0 || src >= p.n_users) {
       atomicOr(p.status, DEV_ERR_MAP_RANGE);
       return false;
@@ -85,8 +85,8 @@ __device__ __forceinline__ bool position(const RopeParams& p, int i, int l, Plac
     for (int a = 0; a < ROPE_MAX_AXES; ++a) {
       pos->at[a] = 0;
       if (a >= p.axes) continue;
-      if (p.start) pos->at[a] = __ldg(p.start + static_cast<int64_t>(src) * p.axes + a);
-      if (p.pos) pos->at[a] += __ldg(p.pos + i * p.pos_item + static_cast<int64_t>(l) * p.axes + a);
+      if (p.start) pos->at[a] = p.start[static_cast<int64_t>(src) * p.axes + a];
+      if (p.pos) pos->at[a] += p.pos[i * p.pos_item + static_cast<int64_t>(l) * p.axes + a];
     }
   }
   return true;
