@@ -23,6 +23,7 @@ struct RopeParams {
   int64_t pos_item;      // elements from one item's to the next's (0: all items share them)
   int n, n_users, H, L, d;
   int heads_per_cta;
+  int lanes_log2, row_step;  // sizes off the 16-byte path: threads that share a row, rows of the launch at a time
   int axes;              // 0: one axis, position start + l
   int rot, interleaved, backward, copy_rest;  // copy_rest: elements from rot on are written (not in place)
   float magnitude;

@@ -215,16 +215,23 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_vec_kernel(const __grid_con
   }
 }
 
-// Lanes that share a row of `pieces` pairs and elements.
-__host__ __device__ constexpr int lanes_of(int pieces) {
-  int lanes = 32;
-  while (lanes / 2 >= pieces) lanes /= 2;
-  return lanes;
+// log2 of the threads that share a row of `pieces` pairs and elements: a warp's (fewer for few pieces), and
+// more, one for each piece at most, where that made fewer than ROPE_FILL CTAs an SM: a lane's pieces, one after
+// the other, are the whole time of few rows.  Always a warp's, and so (us): one row of 8 heads x 512 5.7
+// and 1.9, 500 rows of 500 elements 5.4 and 2.6, 2000 of them 5.7 and 4.3; with 1, 2, 8, 16 CTAs an SM
+// 5.7, 5.7, 4.8, 4.8 (4096 rows of 8 heads x 128 7.6, 7.6, 8.1, 10.4; with 4 7.7).
+constexpr int ROPE_FILL = 4;
+
+int lanes_log2_of(int pieces, int64_t rows, int num_sms) {
+  int log2 = 0;
+  while (log2 < 5 && (1 << log2) < pieces) ++log2;
+  while ((1 << log2) < pieces && rows << log2 < int64_t{ROPE_FILL} * num_sms * ROPE_THREADS) ++log2;
+  return log2;
 }
 
 // Any sizes and strides: a pair (or element behind the rotated ones) of a token after
-// the other, over its heads, the lanes of a warp side by side, so that a token's place is read
-// once and nothing divided for each of them (81720 rows of 80 elements in bf16, 24 turned, three
+// the other, over its heads, the threads that share a row side by side, so that a token's place is
+// read once and nothing divided for each of them (81720 rows of 80 elements in bf16, 24 turned, three
 // axes, 52 -> 35 us; 82262 of two heads, 40 turned, 60 -> 46; without axes 40 -> 29).  Two 16-bit
 // elements at a time: 35, but 53 for the 46.
 // kAhead: heads whose loads are in flight together.
@@ -233,11 +240,12 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_any_kernel(const __grid_con
   if (kAxes) wait_for_launch_before();
   const int half = p.rot >> 1;
   const int pieces = half + (p.copy_rest ? p.d - p.rot : 0);
-  const int rows = p.n * p.L, lanes = lanes_of(pieces);  // (n L is below 2^31)
-  const int step = static_cast<int>(gridDim.x) * (ROPE_THREADS / lanes), first = static_cast<int>(threadIdx.x) & (lanes - 1);
+  const int rows = p.n * p.L, lanes = 1 << p.lanes_log2;  // (n L is below 2^31)
+  const int64_t thread = static_cast<int64_t>(blockIdx.x) * ROPE_THREADS + threadIdx.x;
+  const int first = static_cast<int>(thread) & (lanes - 1);
   const int h0 = static_cast<int>(blockIdx.y) * p.heads_per_cta;
   const int h1 = min(p.H, h0 + p.heads_per_cta);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (ROPE_THREADS / lanes) + static_cast<int>(threadIdx.x) / lanes; row < rows; row += step) {
+  for (int64_t row = thread >> p.lanes_log2; row < rows; row += p.row_step) {
     const int i = static_cast<int>(row) / p.L, l = static_cast<int>(row) - i * p.L;
     Place<kAxes> pos;
     if (!position(p, i, l, &pos)) continue;
@@ -301,8 +309,8 @@ cudaError_t launch(RopeParams p, bool vec, int num_sms, cudaStream_t s) {
     ctas = (rows + per - 1) / per;
   } else {
     const int pieces = (p.rot >> 1) + (p.copy_rest ? p.d - p.rot : 0);
-    const int per = ROPE_THREADS / lanes_of(pieces);
-    ctas = (rows + per - 1) / per;
+    p.lanes_log2 = lanes_log2_of(pieces, rows, num_sms);
+    ctas = ((rows << p.lanes_log2) + ROPE_THREADS - 1) / ROPE_THREADS;
     if (ctas > 32 * static_cast<int64_t>(num_sms)) ctas = 32 * static_cast<int64_t>(num_sms);
   }
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
@@ -312,6 +320,7 @@ cudaError_t launch(RopeParams p, bool vec, int num_sms, cudaStream_t s) {
   while (parts < p.H && parts < 32 && ctas * parts < 4 * static_cast<int64_t>(num_sms)) parts *= 2;
   if (parts > p.H) parts = p.H;
   p.heads_per_cta = (p.H + parts - 1) / parts;
+  p.row_step = static_cast<int>((ctas * ROPE_THREADS) >> p.lanes_log2);
   const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>((p.H + p.heads_per_cta - 1) / p.heads_per_cta));
   const auto any = p.heads_per_cta == 1 ? rope_any_kernel<T, 1, kAxes> : rope_any_kernel<T, 4, kAxes>;
   const auto kernel = !vec ? any : (p.interleaved ? vec_kernel<T, true, kAxes>(p) : vec_kernel<T, false, kAxes>(p));
