@@ -121,6 +121,23 @@ QcAttnVariant qattn_variant(int64_t rows, int n_users, int H_kv, int Lkv) {
   return registers_us < tiles_us ? QATTN_REGISTERS : QATTN_TILES;
 }
 
+// What attention over the cache asks of its arguments (before anything is allocated or launched).
+ikbo_status_t check_attn(ikbo_plan_t p, const void* Q, const void* data, int n_pages, int page, int H_kv, const int32_t* d_table,
+                         int max_blocks, const int32_t* d_lens, const void* O, const float* lse, int Lkv, int d, float scale) {
+  if (!Q || !O || !data || !aligned16(Q) || !aligned16(O) || !aligned16(data) || !aligned4(lse))
+    return IKBO_ERR_INVALID_ARG;
+  if (Lkv < 1 || !(scale > 0.f) || !std::isfinite(scale)) return IKBO_ERR_INVALID_ARG;
+  if (d != QC_D) return IKBO_ERR_UNSUPPORTED;
+  ikbo_status_t st = check_cache(n_pages, page, H_kv);
+  if (st != IKBO_OK) return st;
+  st = check_table(d_table, d_lens, max_blocks, p ? (p->planned ? p->n_users : 1) : 1, page);
+  if (st != IKBO_OK) return st;
+  if (!p) return IKBO_ERR_INVALID_ARG;
+  if (!p->planned) return IKBO_ERR_NOT_PLANNED;
+  if (p->H % H_kv != 0 || !plan_device_current(p)) return IKBO_ERR_INVALID_ARG;
+  return static_cast<int64_t>(p->n_cand) * p->H * p->Lq > INT32_LIMIT ? IKBO_ERR_UNSUPPORTED : IKBO_OK;
+}
+
 // axes: a call with positions on the rotation's axes, d_pos and the stride from one
 // item's to the next's among them.
 ikbo_status_t rope_call(ikbo_plan_t p, ikbo_rope_t r, const void* X, const int64_t* xs, void* Y, const int64_t* ys,
@@ -383,21 +400,11 @@ ikbo_status_t ikbo_qcache_load(ikbo_plan_t p, const void* data, int n_pages, int
 ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void* data, int n_pages, int page,
                                        int H_kv, const int32_t* d_table, int max_blocks, const int32_t* d_lens,
                                        void* O, float* lse, int Lkv, int d, float scale, cudaStream_t stream) {
-  if (!Q || !O || !data || !aligned16(Q) || !aligned16(O) || !aligned16(data) || !aligned4(lse))
-    return IKBO_ERR_INVALID_ARG;
-  if (Lkv < 1 || !(scale > 0.f) || !std::isfinite(scale)) return IKBO_ERR_INVALID_ARG;
-  if (d != QC_D) return IKBO_ERR_UNSUPPORTED;
-  ikbo_status_t st = check_cache(n_pages, page, H_kv);
+  const ikbo_status_t st = check_attn(p, Q, data, n_pages, page, H_kv, d_table, max_blocks, d_lens, O, lse, Lkv, d, scale);
   if (st != IKBO_OK) return st;
-  st = check_table(d_table, d_lens, max_blocks, p ? (p->planned ? p->n_users : 1) : 1, page);
-  if (st != IKBO_OK) return st;
-  if (!p) return IKBO_ERR_INVALID_ARG;
-  if (!p->planned) return IKBO_ERR_NOT_PLANNED;
-  if (p->H % H_kv != 0 || !plan_device_current(p)) return IKBO_ERR_INVALID_ARG;
 
   const int n_users = p->n_users, group = p->H / H_kv;
   const int64_t rows = static_cast<int64_t>(p->n_cand) * group * p->Lq;  // that read one K/V head, over all users
-  if (rows * H_kv > INT32_LIMIT) return IKBO_ERR_UNSUPPORTED;
   const int blocks_log2 = blocks_log2_of(page);
 
   // (the default stream cannot be captured, and asking took half a microsecond)
@@ -509,17 +516,17 @@ ikbo_status_t ikbo_attn_qcache_tree_forward(ikbo_plan_t p, const void* Q, const 
     return IKBO_ERR_INVALID_ARG;
   if (H_kv < 1 || row_stride < static_cast<int64_t>(H_kv) * QC_D) return IKBO_ERR_INVALID_ARG;
   if (row_stride % 8 != 0) return IKBO_ERR_UNSUPPORTED;
+  ikbo_status_t st = check_attn(p, Q, data, n_pages, page, H_kv, d_table, max_blocks, d_lens, O, lse, Lkv, d, scale);
+  if (st != IKBO_OK) return st;
   float* hist = lse;
-  if (p && p->planned && !lse) {  // the history's log-sum-exp has to be somewhere
+  if (!lse) {  // the history's log-sum-exp has to be somewhere
     bool capturing = false;
     if (stream && is_capturing(stream, &capturing) != cudaSuccess) return IKBO_ERR_CUDA;
-    if (!plan_device_current(p)) return IKBO_ERR_INVALID_ARG;
     const size_t need = static_cast<size_t>(p->n_cand) * p->H * p->Lq;
     if (grow_kept<false>(p, &p->qa_lse, need, ~size_t{0}, capturing, stream) != cudaSuccess) return IKBO_ERR_CUDA;
     hist = p->qa_lse.ptr;
   }
-  const ikbo_status_t st = ikbo_attn_qcache_forward(p, Q, data, n_pages, page, H_kv, d_table, max_blocks, d_lens, O, hist, Lkv, d,
-                                                    scale, stream);
+  st = ikbo_attn_qcache_forward(p, Q, data, n_pages, page, H_kv, d_table, max_blocks, d_lens, O, hist, Lkv, d, scale, stream);
   if (st != IKBO_OK) return st;
   QcTreeParams tp;
   std::memset(&tp, 0, sizeof(tp));
