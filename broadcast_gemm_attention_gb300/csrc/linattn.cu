@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(256) lin_join_kernel(const __grid_constant__ L
   const int64_t state = (static_cast<int64_t>(u) * p.H + h) * LIN_STATE;
   float* ws = p.ws + ((static_cast<int64_t>(blockIdx.y) * p.n_users + u) * p.H + h) * p.segs * LIN_STATE + e;
   float s = 0.f;
-  if (job.s_in) s = job.s_in[state + (job.s_in_turned ? (e % LIN_D) * LIN_D + e / LIN_D : e)] * job.s_in_factor;
+  if (job.s_in) s = job.s_in[state + (job.s_in_turned ? (e % LIN_D) * LIN_D + e / LIN_D : e)];
   ws[static_cast<int64_t>(segs - 1) * LIN_STATE] = s;
   const float log2_decay = log2f(__ldcg(p.decay + h));
   const float down = lin_power(log2_decay, p.seg_len);

@@ -177,7 +177,8 @@ ikbo_status_t ikbo_linattn_forward(ikbo_plan_t p, const void* Q, const void* K, 
   j.os = strides[3];
   j.s_in = state_in;
   j.s_out = state_out;
-  j.s_in_factor = j.s_out_factor = 1.f;
+  j.add = 1.f;
+  j.read = scale;
   lp.n_jobs = 1;
   lp.steps = lp.likely_len <= LIN_STEP_MOST;
   return lin_run(p, &lp, stream);
@@ -257,8 +258,8 @@ ikbo_status_t ikbo_linattn_backward(ikbo_plan_t p, const void* Q, const void* K,
     j.s_out = s_out;
     j.s_in_turned = turned;
     j.reverse = reverse;
-    j.s_in_factor = reverse ? 1.f / scale : 1.f;
-    j.s_out_factor = reverse ? scale : 1.f;
+    j.add = reverse ? scale : 1.f;
+    j.read = reverse ? 1.f : scale;
   };
   if (dQ) add(3, 2, 1, dQ, 4, state_in, true, nullptr, false);
   if (dK) add(2, 3, 0, dK, 5, d_state_out, true, nullptr, true);

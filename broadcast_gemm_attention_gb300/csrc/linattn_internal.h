@@ -19,18 +19,19 @@ constexpr int LIN_STEP_MOST = 8;              // rows of a user up to which sing
 
 
 // One scan: with queries x, keys y and values z,
-//   S <- decay S + y_t z_t^T,   out_t = scale x_t S
+//   S <- decay S + add y_t z_t^T,   out_t = read x_t S,   add read = scale
 // from the first row of a user to the last, or (reverse) from the last to the
 // first.  A reverse scan's start has been decayed already: its first step
-// takes it as it is, and its end is decayed once more.
+// takes it as it is, and its end is decayed once more.  The scale is in what rows add where
+// the state is a gradient, which the start and the end are too (a state without it
+// would have to begin with the start divided by the scale, and may not hold that).
 struct LinJob {
   const uint16_t *x, *y, *z;  // x null: no outputs
   uint16_t* out;
   int64_t xs, ys, zs, os;     // row strides in elements
   const float* s_in;          // [n_users][H][128][128], rows of y's elements; null: zero
   float* s_out;               // the same, or null; may be s_in
-  float s_in_factor;          // of the start
-  float s_out_factor;         // of the end
+  float add, read;
   int s_in_turned;            // s_in has rows of z's elements
   int reverse;
 };

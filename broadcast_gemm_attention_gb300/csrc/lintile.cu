@@ -11,6 +11,7 @@
 //                         decay to the chunk's end, as two bf16 parts in shared
 //                         memory (2^-16), so two products
 //   out = scale (O2 + decay^(i+1) O1)
+// Of a scan whose state is a gradient the scale is in w, not in O1's factor.
 //
 // Per CTA (persistent, one per SM, 32 warps):
 //   warp 0       loads x, y, z by TMA; warp 1 issues A, O1, O2; warp 2 issues S
@@ -61,7 +62,7 @@ struct Aux {
   uint64_t a_full, p_full, o_full, o_empty, s_full, s_empty, w_full[2], m_full, m_begun, w_empty[2], drain[2], group[2];
   float4 near[4];             // a 16-column block's decays to its nearest column
   float power[LT_CHUNK + 4];  // decay^n of the current item
-  uint2 parts[LT_CHUNK];      // decay^n as a bf16 pair of the same, and what that lacks
+  uint2 parts[LT_CHUNK];      // decay^n (and the scale, in a gradient's state) as a bf16 pair of the same, and what that lacks
   uint32_t tmem_slot, abort;
 };
 constexpr uint32_t LT_SMEM_USED = AUX_AT + sizeof(Aux);
@@ -504,7 +505,7 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t t
     const float log2_decay = log2f(__ldcg(p.decay + it.h));
     for (int c = 0; c < it.chunks; ++c, ++g) {
       const int rows = it.rows(c);
-      const float w1 = decay_power(log2_decay, max(it.reverse ? rows - i_row - (c == 0 ? it.early : 0) : i_row + 1, 0)) * p.scale;
+      const float w1 = decay_power(log2_decay, max(it.reverse ? rows - i_row - (c == 0 ? it.early : 0) : i_row + 1, 0)) * job.read;
       const bool stores = quarter * 32 < rows && job.out;
       uint8_t* stage = sm + (g & 1u ? X1_AT : X_AT) + (warp - OUT_WARP0) * OUT_BYTES;  // x's place: its products have ended
       if (!warp_wait(&x.o_full, g & 1u, x, p)) return;
@@ -565,9 +566,8 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tm
     const int64_t ws = ((static_cast<int64_t>(it.job) * p.n_users + it.u) * p.H + it.h) * p.segs;
     bool turned;
     const float* from = state_from<kLocal>(p, it, turned);
-    const float factor = it.segs > 1 ? 1.f : job.s_in_factor;
     float* to = kLocal ? p.ws + (ws + it.seg) * LIN_STATE : (it.seg + 1 == it.segs && job.s_out ? job.s_out + state : nullptr);
-    const float up = kLocal ? 1.f : (it.reverse && !it.whole_user_empty ? job.s_out_factor * decay_power(log2_decay, 1) : job.s_out_factor);
+    const float up = !kLocal && it.reverse && !it.whole_user_empty ? decay_power(log2_decay, 1) : 1.f;
     // The start to tensor memory.  Rows of a state are 512 bytes apart, a lane's place is a row: eight lanes load a row's
     // 128 bytes, by way of the warp's place in the image (a load of 16 bytes of each of 32 rows took 18000 cycles in all).
     if (kOutputs && !warp_wait(&x.s_empty, (g & 1u) ^ 1u, x, p)) return;
@@ -585,15 +585,15 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tm
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float4 r = *reinterpret_cast<const float4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4));
-          v[4 * k] = __float_as_uint(r.x * factor);
-          v[4 * k + 1] = __float_as_uint(r.y * factor);
-          v[4 * k + 2] = __float_as_uint(r.z * factor);
-          v[4 * k + 3] = __float_as_uint(r.w * factor);
+          v[4 * k] = __float_as_uint(r.x);
+          v[4 * k + 1] = __float_as_uint(r.y);
+          v[4 * k + 2] = __float_as_uint(r.z);
+          v[4 * k + 3] = __float_as_uint(r.w);
         }
         __syncwarp();
       } else {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(from ? __ldcg(from + (64 * half + 32 * b + k) * LIN_D + e_row) * factor : 0.f);
+        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(from ? __ldcg(from + (64 * half + 32 * b + k) * LIN_D + e_row) : 0.f);
       }
       tmem_st32(St + 32 * b, v);
     }
@@ -674,7 +674,7 @@ __device__ void parts_warps(const LinParams& p, uint8_t* sm, Aux& x) {
       const int rows = it.rows(c);
       if (c == 0 || !kOutputs) {  // the decays: to the chunk's end, or to the scan's
         if (!group_sync(&x.group[1], meet, x, p)) return;
-        const float w = decay_power(log2_decay, tid + (kOutputs ? 0 : it.n - c * LT_CHUNK - rows));
+        const float w = decay_power(log2_decay, tid + (kOutputs ? 0 : it.n - c * LT_CHUNK - rows)) * p.job[it.job].add;
         const uint32_t hi = pack_bf16x2(w, w);
         const float rest = w - bf16_lo(hi);
         x.parts[tid] = make_uint2(hi, pack_bf16x2(rest, rest));
