@@ -60,6 +60,29 @@ struct LinShared {
   float power[LIN_CHUNK + 1];  // decay^n
 };
 
+// What z's infinities and NaN in rows up to a row's own add to it: o's rows are `row` and row + 8, its columns 16 warp + 8 e + 2 t
+// (+ 1), of z's rows below `rows`.
+__device__ __noinline__ void add_odd(float (&o)[2][4], uint32_t probs, uint32_t z_at, int row, int rows, int warp, int t) {
+#pragma unroll 1
+  for (int j = 0; j < rows; ++j) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t z;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(z) : "r"(z_at + tile_at(j, 2 * warp + e) + 4 * t) : "memory");
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = row + 8 * k;
+        if (r < j) continue;
+        uint16_t p;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p) : "r"(probs + r * 128 + (((j >> 3) ^ (r & 7)) << 4) + 2 * (j & 7)) : "memory");
+        const float w = __uint_as_float(static_cast<uint32_t>(p) << 16), lo = bf16_lo(z), hi = bf16_hi(z);
+        if (!is_finite(lo)) o[e][2 * k] += w * lo;
+        if (!is_finite(hi)) o[e][2 * k + 1] += w * hi;
+      }
+    }
+  }
+}
+
 // The scan in registers, for histories of a few chunks: 16x8x16 products, a CTA a scan,
 // the turned state as accumulators (their layout is the next product's B operand).
 // Bound: those products (603 TFLOP/s at most on this part, 117 kFLOP a row and head with
@@ -159,10 +182,25 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
     }
     // z's columns 16 warp .. of 16 rows each: A of the state's product, B of the outputs'
     uint32_t zf[4][4];
+    bool any_odd = false;
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)  // matrices: (columns 0-7, rows 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
       ldsm4_t(zf[kb], z_at + tile_at(16 * kb + (lane & 7) + 8 * (lane >> 4), 2 * warp + ((lane >> 3) & 1)));
     if (kOutputs) {
+      // z's infinities and NaN stay out of the outputs' product, where they would reach rows that do not read them (0
+      // times infinity), and are added behind it
+      uint32_t odd = 0;
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) odd |= not_finite(zf[kb][k]);
+      any_odd = __any_sync(0xffffffffu, (odd & 0x80008000u) != 0);
+      if (any_odd) {
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) zf[kb][k] = finite_part(zf[kb][k]);
+      }
       uint32_t sb[16][2];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -197,6 +235,7 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
           mma_16816(o[0], pf, zf[kb][0], zf[kb][2]);
           mma_16816(o[1], pf, zf[kb][1], zf[kb][3]);
         }
+        if (any_odd) add_odd(o, probs, z_at, row, 16 * mt + 16, warp, t);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int r = row + 8 * k;
@@ -207,7 +246,12 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
         }
       }
     }
-    // the state: decayed, and z^T y with each row's decay on z, to 16 bits of mantissa
+    // the state: decayed, and z^T y with each row's decay on z, to 16 bits of mantissa (z as it is)
+    if (any_odd) {
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb)
+        ldsm4_t(zf[kb], z_at + tile_at(16 * kb + (lane & 7) + 8 * (lane >> 4), 2 * warp + ((lane >> 3) & 1)));
+    }
     const float down = sh.power[rows];
 #pragma unroll
     for (int i = 0; i < 16; ++i)

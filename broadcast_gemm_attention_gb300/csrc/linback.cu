@@ -132,6 +132,28 @@ __device__ __forceinline__ void times(float (&c)[2][4], float (&d)[2][4], const 
   }
 }
 
+// What Y's infinities and NaN add to the rows that read them.
+__device__ __noinline__ void add_odd(float (&c)[2][4], const uint32_t (&pr)[4], bool later, uint32_t y_at, int piece, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+  for (int j = 0; j < LB_ROWS; ++j) {
+    uint32_t y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y[i]) : "r"(y_at + place(j, piece + i) + 4 * t) : "memory");
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t p = __shfl_sync(0xffffffffu, j < 8 ? pr[k] : pr[2 + k], (lane & ~3) | ((j & 7) >> 1));
+      const float w = j & 1 ? bf16_hi(p) : bf16_lo(p);
+      if (later ? j < g + 8 * k : j > g + 8 * k) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!is_finite(bf16_lo(y[i]))) c[i][2 * k] += w * bf16_lo(y[i]);
+        if (!is_finite(bf16_hi(y[i]))) c[i][2 * k + 1] += w * bf16_hi(y[i]);
+      }
+    }
+  }
+}
+
 // c <- w c + P Y for the warp's 16 columns of Y, P = scale d with its rows' decays to each other, rounded to bf16:
 // row t reads rows up to t, or (later) from t on.
 __device__ __forceinline__ void among(float (&c)[2][4], const float (&d)[2][4], const float* power, float w0, float w1, float scale, bool later,
@@ -152,8 +174,15 @@ __device__ __forceinline__ void among(float (&c)[2][4], const float (&d)[2][4], 
     c[i][3] *= w1;
   }
   ldsm4_t(y, y_at + place(lane & 15, piece + (lane >> 4)));
+  // Y's infinities and NaN stay out of the product, where they would reach rows that do not read them (0 times infinity)
+  const bool odd = __any_sync(0xffffffffu, ((not_finite(y[0]) | not_finite(y[1]) | not_finite(y[2]) | not_finite(y[3])) & 0x80008000u) != 0);
+  if (odd) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = finite_part(y[k]);
+  }
   mma_16816(c[0], pr, y[0], y[1]);
   mma_16816(c[1], pr, y[2], y[3]);
+  if (odd) add_odd(c, pr, later, y_at, piece, lane);
 }
 
 // Asks for a state in L2.

@@ -492,6 +492,63 @@ __device__ void decay_warps(const LinParams& p, Aux& x, uint32_t tmem) {
 }
 
 // ----------------------------------------------------------------- outputs
+// 8 columns of the lane's row from tensor memory.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Outputs again, in plain arithmetic, where one is infinite or NaN whose part from the state is not: an infinity or NaN in
+// z reaches rows of its chunk that do not read it, as 0 times infinity.  8 columns of the lane's row i of a chunk
+// (`row0` its first row, `rows` of them) at a time, from the inputs; o1 is x S of them, `to` the row's place.
+// (Behind that chunk the state has it, so that of a column one chunk is slow: 0.7 ms, 6 where all columns are.
+// Looking for it in all chunks takes 1 to 1.5% of a call: 15 histories 51.6 -> 52.0 us, their gradient 73.2 -> 74.4.)
+__device__ __forceinline__ void plain_outputs(const LinParams& p, const LinJob& job, int64_t row0, int rows, int at, int i, int column, float log2_decay,
+                                              float w1, uint32_t o1, uint8_t* to) {
+  uint32_t a[8];
+  tmem_ld8(o1, a);
+  uint4* piece = reinterpret_cast<uint4*>(to + ((((column & 63) >> 3) ^ (i & 7)) << 4));
+  const uint4 now = *piece;
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t w = k < 4 ? (k < 2 ? now.x : now.y) : (k < 6 ? now.z : now.w);
+    any |= is_finite(__uint_as_float(a[k])) && (not_finite(w) & (k & 1 ? 0x80000000u : 0x8000u));
+  }
+  if (!__any_sync(0xffffffffu, any && i < rows)) return;
+  float acc[8] = {};
+#pragma unroll 1
+  for (int j = 0; j < rows; ++j) {
+    const int gap = job.reverse ? j - i : i - j;
+    if (gap < 0 || i >= rows) continue;
+    const uint16_t *x = job.x + (row0 + i) * job.xs + at, *y = job.y + (row0 + j) * job.ys + at;
+    float w = 0.f;
+#pragma unroll 1
+    for (int e = 0; e < LIN_D; e += 2) {
+      const uint32_t f = *reinterpret_cast<const uint32_t*>(x + e), g = *reinterpret_cast<const uint32_t*>(y + e);
+      w = fmaf(bf16_lo(f), bf16_lo(g), fmaf(bf16_hi(f), bf16_hi(g), w));
+    }
+    w = bf16_lo(pack_bf16x2(w * (decay_power(log2_decay, gap) * p.scale), 0.f));
+    const uint16_t* z = job.z + (row0 + j) * job.zs + at + column;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(z + 2 * k);
+      acc[2 * k] = fmaf(w, bf16_lo(v), acc[2 * k]);
+      acc[2 * k + 1] = fmaf(w, bf16_hi(v), acc[2 * k + 1]);
+    }
+  }
+  __syncwarp();
+  tmem_ld8(o1, a);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    a[k] = pack_bf16x2(fmaf(__uint_as_float(a[2 * k]), w1, acc[2 * k]), fmaf(__uint_as_float(a[2 * k + 1]), w1, acc[2 * k + 1]));
+  *piece = make_uint4(a[0], a[1], a[2], a[3]);
+}
+
 template <bool kLocal>
 __device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t tmem) {
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(lane_id());
@@ -510,6 +567,7 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t t
       uint8_t* stage = sm + (g & 1u ? X1_AT : X_AT) + (warp - OUT_WARP0) * OUT_BYTES;  // x's place: its products have ended
       if (!warp_wait(&x.o_full, g & 1u, x, p)) return;
       tc_fence_after();
+      float odd0 = 0.f, odd1 = 0.f;  // NaN where an output is infinite or NaN
 #pragma unroll 1
       for (int b = 0; b < 4 && stores; ++b) {
         uint32_t a[16], o[16], out[8];
@@ -522,11 +580,17 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Aux& x, uint32_t t
           float u, v;
           fma2v(u, v, __uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]), w1, __uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
           out[j] = pack_bf16x2(u, v);
+          fma2v(odd0, odd1, u, v, 0.f, odd0, odd1);
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * b + q) ^ (lane & 7)) << 4)) =
               make_uint4(out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]);
+      }
+      if (__builtin_expect(__any_sync(0xffffffffu, stores && i_row < rows && !(odd0 + odd1 == 0.f)), 0)) {
+#pragma unroll 1
+        for (int b = 0; b < 8; ++b)
+          plain_outputs(p, job, it.first(c), rows, it.h * LIN_D, i_row, half * 64 + 8 * b, log2_decay, w1, O1 + 8 * b, stage + lane * 128);
       }
       tc_fence_before();
       warp_arrive(&x.o_empty);

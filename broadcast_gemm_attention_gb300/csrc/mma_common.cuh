@@ -51,6 +51,17 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uin
   hi = pack_bf16x2(a, b);
   lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
 }
+// Bits 15 and 31: whether the halves of x, a bf16 pair, are infinite or NaN (the exponent's carry).
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; }
+__device__ __forceinline__ uint32_t not_finite(const uint4& x) {
+  return not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
+}
+// x without its halves that are infinite or NaN (0 in their place).
+__device__ __forceinline__ uint32_t finite_part(uint32_t x) {
+  const uint32_t odd = not_finite(x) & 0x80008000u;
+  return x & ~((odd >> 15) * 0xffffu);
+}
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < INFINITY; }
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 

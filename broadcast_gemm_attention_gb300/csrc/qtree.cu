@@ -36,13 +36,6 @@ constexpr int TR_SHARED_CTAS = 3;  // an SM
 
 __device__ __forceinline__ uint32_t word(const uint4& x, int i) { return i == 0 ? x.x : (i == 1 ? x.y : (i == 2 ? x.z : x.w)); }
 
-// Bits 15 and 31: whether the halves of x are infinite or NaN (the exponent's
-// carry).
-__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; }
-__device__ __forceinline__ uint32_t not_finite(const uint4& x) {
-  return not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
-}
-
 struct Tree {
   uint4 sees[TR_MOST];  // rows that a row reads, itself among them
   int up[2][TR_MOST];   // the row above, -1: none, -2: the row is not there

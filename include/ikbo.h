@@ -554,9 +554,10 @@ ikbo_status_t ikbo_attn_qcache_tree_forward(ikbo_plan_t p, const void* Q, const 
  * length; up to 8 rows a user they are taken one by one, in fp32, else in chunks of
  * 64 or (from 129 rows, the states alone from 257) 128 on the tensor cores: decayed
  * keys or values in two bf16 parts (2^-16) for the state, the products q_i.k_j with
- * their decays and, for O, the state rounded to bf16 (2^-8 each), fp32 sums.  A row
- * that holds an infinity or NaN makes its user's O of that head undefined from 127 rows
- * before it on; other users' are not touched.  O must not overlap inputs.  Histories far
+ * their decays and, for O, the state rounded to bf16 (2^-8 each), fp32 sums.  An
+ * infinity or NaN in a row reaches the outputs of its head that read the row, which are then
+ * not defined, and no others; one in V its column alone (where chunks have 128 rows such a call
+ * takes up to some milliseconds longer).  O must not overlap inputs.  Histories far
  * longer than a CTA's share are cut into segments (two launches more, and a workspace of
  * the plan's of up to 1 GiB, as described at ikbo_attn_qcache_forward).  Results repeat
  * bit for bit.  Of a call in which a bounded wait ran out (IKBO_ERR_TIMEOUT) the outputs
@@ -573,7 +574,8 @@ ikbo_status_t ikbo_linattn_forward(ikbo_plan_t p, const void* Q, const void* K, 
  * Only inputs are read: the states are formed again from state_in.  dQ, dK, dV
  * bf16, d_state_in fp32, overwritten; any may be NULL, and none may overlap an
  * input.  row_strides: 7 values, of Q, K, V, dO, dQ, dK, dV.  The decays are
- * constants.  Up to 64 rows a user one pass over both states, in blocks of 16 rows (the
+ * constants.  An infinity or NaN in a row reaches gradients that the formulas above have it
+ * in, and no others.  Up to 64 rows a user one pass over both states, in blocks of 16 rows (the
  * same roundings, and 2^-17 for the states' parts), else three scans in chunks of 128; a
  * gradient does not depend on which others are asked for.  Else as above. */
 ikbo_status_t ikbo_linattn_backward(ikbo_plan_t p, const void* Q, const void* K, const void* V, const void* dO,
