@@ -515,7 +515,7 @@ ikbo_status_t ikbo_attn_qcache_tree_forward(ikbo_plan_t p, const void* Q, const 
   if (!K_new || !V_new || !aligned16(K_new) || !aligned16(V_new) || !aligned4(d_parents) || !Q || Q == O)
     return IKBO_ERR_INVALID_ARG;
   if (H_kv < 1 || row_stride < static_cast<int64_t>(H_kv) * QC_D) return IKBO_ERR_INVALID_ARG;
-  if (row_stride % 8 != 0) return IKBO_ERR_UNSUPPORTED;
+  if (row_stride % 8 != 0 || H_kv > TREE_MOST_HEADS) return IKBO_ERR_UNSUPPORTED;
   ikbo_status_t st = check_attn(p, Q, data, n_pages, page, H_kv, d_table, max_blocks, d_lens, O, lse, Lkv, d, scale);
   if (st != IKBO_OK) return st;
   float* hist = lse;

@@ -107,6 +107,7 @@ struct QcAttnParams {
 };
 
 // The drafted rows' part of attention over a tree (qtree.cu).
+constexpr int TREE_MOST_HEADS = 65535;  // of K and V: a dimension of its grid
 struct QcTreeParams {
   const uint16_t* Q;
   const uint16_t* K;        // [n_cand][Lq] rows of [H_kv][128], row_stride apart

@@ -513,6 +513,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
  *                 rows row_stride elements apart (>= H_kv * 128, a multiple of 8):
  *                 rows as ikbo_qcache_append takes them, which stores the
  *                 accepted ones once their slots are known
+ *                 (H_kv <= 65535)
  *   d_parents     int32 [n_cand][Lq]: the row above row l, in [0, l); -1: none
  *                 (a child of the history); below -1: row l is not there, so a
  *                 draft may have fewer rows than Lq.  NULL: chains, row l below

@@ -62,3 +62,19 @@ def test_a_refused_call_under_capture_says_why():
         graph.replay()
         torch.cuda.synchronize()
         assert float(x) == 1.0 and torch.all(c.o == 3.0) and p.status() == B.IKBO_OK
+
+
+def test_more_heads_than_a_grid_has_are_refused_before_any_launch():
+    H = 65536
+    st = QC.Store(4, [0], 1, 16)
+    table, ln = st.cuda()[1:]
+    data = torch.zeros((1, H, 1, 2560), dtype=torch.uint8, device="cuda")
+    x = torch.zeros((1, H, 24, 128), dtype=torch.bfloat16, device="cuda")
+    kv, o, m = torch.zeros((1, 24, H, 128), dtype=torch.bfloat16, device="cuda"), torch.full_like(x, 3.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+    with B.Plan(1, 1, H) as p:
+        p.plan(m, 1, H, 24)
+        with pytest.raises(B.IkboError) as e:
+            p.attn_qcache_tree_forward(x, data, 16, table, ln, kv, kv, None, o)
+        assert e.value.code == UNSUPPORTED and p.launches() == 1
+        torch.cuda.synchronize()
+        assert torch.all(o == 3.0) and p.status() == B.IKBO_OK
