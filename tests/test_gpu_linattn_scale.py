@@ -46,3 +46,17 @@ def test_any_scale(lens, size, scale):
             BD.near(got, w, m, name)
         BD.near_state(dS, want[3], mass[3])
         assert p.status() == B.IKBO_OK
+
+
+def test_no_user_has_rows():
+    """In tiles too: states pass through, rows of no user are left alone."""
+    d = Data(42, [0, 0, 0], 3, spare=200)
+    Q, K, V, decay, off = d.cuda()
+    with plan() as p:
+        for queries in (True, False):
+            O, S = torch.full_like(Q, -7.0), torch.full((3, 3, 128, 128), float("nan"), device="cuda")
+            p.linattn_forward(Q if queries else None, K, V, decay, O if queries else None, state_in=f32(d.S), state_out=S, offsets=off, max_len=200)
+            assert np.array_equal(S.cpu().numpy(), d.S) and torch.all(O == -7.0)
+        outs, dS = gradients(p, d, 0.5, 200)
+        assert np.array_equal(dS.cpu().numpy(), d.dS) and all(torch.all(t == -7.0) for t in outs)
+        assert p.status() == B.IKBO_OK
