@@ -451,6 +451,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
     c.d = d;
     c.H_kv = H_kv;
     c.scale = scale;
+    // (An ordinary launch, here and below, as launch_qtree needs: it begins when all before it has ended.)
     return attn_launch(p, c, stream);
   }
 
@@ -501,6 +502,7 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
   ap.sixteen = QC_SIXTEEN;
   ap.debug = p->debug;
   ap.timeout_ns = p->timeout_ns;
+  // (Ordinary launches: the drafts' kernel behind them, launch_qtree, reads its inputs before they have ended.)
   if ((few ? launch_qattn(ap, eight, solo, stream) : launch_qattn_tile(ap, stream)) != cudaSuccess)
     return IKBO_ERR_CUDA;
   p->launches++;

@@ -328,6 +328,10 @@ __global__ void __launch_bounds__(TR_THREADS, kShared ? TR_SHARED_CTAS : 2) qtre
 
 }  // namespace
 
+// The kernel reads the map, the parents and Q, K and V ahead of its wait, by the read-only path.  That is sound because
+// the launch before it in the stream is the history's, an ordinary one that writes none of these: it has begun when
+// all before it had ended and could be seen.  Behind a kernel that is itself set up early (launch_behind), or one
+// that writes one of these, every load has to move behind the wait.
 cudaError_t launch_qtree(const QcTreeParams& p, int num_sms, cudaStream_t s) {
   const bool shared = p.Lq > 16;
   const int heads = shared ? p.H_kv : 1, items = ((p.group * p.Lq + 15) / 16) * (shared ? 1 : p.H_kv);
