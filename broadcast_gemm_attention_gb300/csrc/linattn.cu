@@ -17,6 +17,8 @@
 // is kept from the forward pass.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "launch.cuh"
 #include "linattn_internal.h"
 #include "mma_common.cuh"
@@ -60,24 +62,24 @@ struct LinShared {
   float power[LIN_CHUNK + 1];  // decay^n
 };
 
-// What z's infinities and NaN in rows up to a row's own add to it: o's rows are `row` and row + 8, its columns 16 warp + 8 e + 2 t
-// (+ 1), of z's rows below `rows`.
-__device__ __noinline__ void add_odd(float (&o)[2][4], uint32_t probs, uint32_t z_at, int row, int rows, int warp, int t) {
+// o += the rows' weights of z's rows that they read, without the matrix instruction: o's rows are `row` and row + 8, its
+// columns 16 warp + 8 e + 2 t (+ 1); z's rows are those below `rows`.
+__device__ __forceinline__ void one_by_one(float (&o)[2][4], uint32_t probs, uint32_t z_at, int row, int rows, int warp, int t) {
 #pragma unroll 1
   for (int j = 0; j < rows; ++j) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t z;
-      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(z) : "r"(z_at + tile_at(j, 2 * warp + e) + 4 * t) : "memory");
+    for (int k = 0; k < 2; ++k) {
+      const int r = row + 8 * k;
+      if (r < j) continue;
+      uint16_t p;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p) : "r"(probs + r * 128 + (((j >> 3) ^ (r & 7)) << 4) + 2 * (j & 7)) : "memory");
+      const float w = __uint_as_float(static_cast<uint32_t>(p) << 16);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = row + 8 * k;
-        if (r < j) continue;
-        uint16_t p;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p) : "r"(probs + r * 128 + (((j >> 3) ^ (r & 7)) << 4) + 2 * (j & 7)) : "memory");
-        const float w = __uint_as_float(static_cast<uint32_t>(p) << 16), lo = bf16_lo(z), hi = bf16_hi(z);
-        if (!is_finite(lo)) o[e][2 * k] += w * lo;
-        if (!is_finite(hi)) o[e][2 * k + 1] += w * hi;
+      for (int e = 0; e < 2; ++e) {
+        uint32_t z;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(z) : "r"(z_at + tile_at(j, 2 * warp + e) + 4 * t) : "memory");
+        o[e][2 * k] = fmaf(w, bf16_lo(z), o[e][2 * k]);
+        o[e][2 * k + 1] = fmaf(w, bf16_hi(z), o[e][2 * k + 1]);
       }
     }
   }
@@ -182,76 +184,69 @@ __global__ void __launch_bounds__(LIN_THREADS, kOutputs ? 1 : 2) lin_chunk_kerne
     }
     // z's columns 16 warp .. of 16 rows each: A of the state's product, B of the outputs'
     uint32_t zf[4][4];
-    bool any_odd = false;
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb)  // matrices: (columns 0-7, rows 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
       ldsm4_t(zf[kb], z_at + tile_at(16 * kb + (lane & 7) + 8 * (lane >> 4), 2 * warp + ((lane >> 3) & 1)));
     if (kOutputs) {
-      // z's infinities and NaN stay out of the outputs' product, where they would reach rows that do not read them (0
-      // times infinity), and are added behind it
+      // z's infinities and NaN would reach rows that do not read them in the product, as 0 times infinity: such chunks go
+      // without it.  (Looking for them, 400 users' 24 rows 129.5 -> 131.5 us, 128 rows 245 -> 249; a branch at each product 251.)
       uint32_t odd = 0;
 #pragma unroll
-      for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) odd |= not_finite(zf[kb][k]);
-      any_odd = __any_sync(0xffffffffu, (odd & 0x80008000u) != 0);
-      if (any_odd) {
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) zf[kb][k] = finite_part(zf[kb][k]);
-      }
+      for (int kb = 0; kb < 4; ++kb) odd |= times_zero(zf[kb]);
+      const bool any_odd = __any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0);
       uint32_t sb[16][2];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         sb[i][0] = pack_bf16x2(s[i][0], s[i][1]);
         sb[i][1] = pack_bf16x2(s[i][2], s[i][3]);
       }
+      const auto outputs = [&](auto kOdd) {
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        if (16 * mt >= rows) break;
-        float o[2][4] = {};
+        for (int mt = 0; mt < 4; ++mt) {
+          if (16 * mt >= rows) break;
+          float o[2][4] = {};
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          uint32_t xf[4];
-          ldsm4(xf, x_at + tile_at(16 * mt + (lane & 15), 2 * kk + (lane >> 4)));
-          mma_16816(o[0], xf, sb[2 * kk][0], sb[2 * kk + 1][0]);
-          mma_16816(o[1], xf, sb[2 * kk][1], sb[2 * kk + 1][1]);
+          for (int kk = 0; kk < 8; ++kk) {
+            uint32_t xf[4];
+            ldsm4(xf, x_at + tile_at(16 * mt + (lane & 15), 2 * kk + (lane >> 4)));
+            mma_16816(o[0], xf, sb[2 * kk][0], sb[2 * kk + 1][0]);
+            mma_16816(o[1], xf, sb[2 * kk][1], sb[2 * kk + 1][1]);
+          }
+          const int row = 16 * mt + g;
+          const float w0 = sh.power[row + 1], w1 = sh.power[row + 9];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            o[e][0] *= w0;
+            o[e][1] *= w0;
+            o[e][2] *= w1;
+            o[e][3] *= w1;
+          }
+          if constexpr (kOdd.value) {
+            one_by_one(o, probs, z_at, row, min(rows, 16 * mt + 16), warp, t);
+          } else {
+#pragma unroll
+            for (int kb = 0; kb <= mt; ++kb) {
+              uint32_t pf[4];
+              const int r = 16 * mt + (lane & 15);
+              ldsm4(pf, probs + r * 128 + (((2 * kb + (lane >> 4)) ^ (r & 7)) << 4));
+              mma_16816(o[0], pf, zf[kb][0], zf[kb][2]);
+              mma_16816(o[1], pf, zf[kb][1], zf[kb][3]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int r = row + 8 * k;
+            if (r >= rows) continue;
+            uint16_t* dst = job.out + (row_at + c0 + r) * job.os + h * LIN_D + 16 * warp + 2 * t;
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0][2 * k] * p.scale, o[0][2 * k + 1] * p.scale);
+            *reinterpret_cast<uint32_t*>(dst + 8) = pack_bf16x2(o[1][2 * k] * p.scale, o[1][2 * k + 1] * p.scale);
+          }
         }
-        const int row = 16 * mt + g;
-        const float w0 = sh.power[row + 1], w1 = sh.power[row + 9];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          o[e][0] *= w0;
-          o[e][1] *= w0;
-          o[e][2] *= w1;
-          o[e][3] *= w1;
-        }
-#pragma unroll
-        for (int kb = 0; kb <= mt; ++kb) {
-          uint32_t pf[4];
-          const int r = 16 * mt + (lane & 15);
-          ldsm4(pf, probs + r * 128 + (((2 * kb + (lane >> 4)) ^ (r & 7)) << 4));
-          mma_16816(o[0], pf, zf[kb][0], zf[kb][2]);
-          mma_16816(o[1], pf, zf[kb][1], zf[kb][3]);
-        }
-        if (any_odd) add_odd(o, probs, z_at, row, 16 * mt + 16, warp, t);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = row + 8 * k;
-          if (r >= rows) continue;
-          uint16_t* dst = job.out + (row_at + c0 + r) * job.os + h * LIN_D + 16 * warp + 2 * t;
-          *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0][2 * k] * p.scale, o[0][2 * k + 1] * p.scale);
-          *reinterpret_cast<uint32_t*>(dst + 8) = pack_bf16x2(o[1][2 * k] * p.scale, o[1][2 * k + 1] * p.scale);
-        }
-      }
+      };
+      if (any_odd) outputs(std::true_type());
+      else outputs(std::false_type());
     }
-    // the state: decayed, and z^T y with each row's decay on z, to 16 bits of mantissa (z as it is)
-    if (any_odd) {
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb)
-        ldsm4_t(zf[kb], z_at + tile_at(16 * kb + (lane & 7) + 8 * (lane >> 4), 2 * warp + ((lane >> 3) & 1)));
-    }
+    // the state: decayed, and z^T y with each row's decay on z, to 16 bits of mantissa
     const float down = sh.power[rows];
 #pragma unroll
     for (int i = 0; i < 16; ++i)

@@ -44,6 +44,7 @@ struct BackShared {
   uint8_t rows[4][LB_TILE];
   float sums[8][LB_ROWS][LB_SUM];  // R^T k_t over a warp's rows
   float power[LB_ROWS + 1];        // decay^n
+  int odd;                         // some row so far holds an infinity or NaN
 };
 
 __device__ __forceinline__ uint32_t place(int r, int c) { return static_cast<uint32_t>(r * 256 + ((c ^ (r & 7)) << 4)); }
@@ -63,8 +64,9 @@ __device__ __forceinline__ int user_rows(const LinBackParams& p, int u, int& fir
 }
 
 // Rows first .. first + n - 1 of the four, zeros behind them.  v's and do's pairs of each 16
-// columns: 0 2 4 6 1 3 5 7.
+// columns: 0 2 4 6 1 3 5 7.  Notes where one holds an infinity or NaN.
 __device__ __forceinline__ void load_rows(const LinBackParams& p, BackShared& sh, int64_t first, int n, int h) {
+  uint32_t odd = 0;  // 0 times all of them
 #pragma unroll
   for (int i = threadIdx.x; i < 4 * LB_ROWS * 8; i += LB_THREADS) {
     const int t = i >> 7, r = (i >> 3) & 15, c = i & 7;
@@ -76,10 +78,12 @@ __device__ __forceinline__ void load_rows(const LinBackParams& p, BackShared& sh
       a = __ldcg(from);
       b = __ldcg(from + 1);
     }
+    odd |= times_zero(a) | times_zero(b);
     const bool mixed = t >= LB_V;
     *reinterpret_cast<uint4*>(sh.rows[t] + place(r, 2 * c)) = mixed ? make_uint4(a.x, a.z, b.x, b.z) : a;
     *reinterpret_cast<uint4*>(sh.rows[t] + place(r, 2 * c + 1)) = mixed ? make_uint4(a.y, a.w, b.y, b.w) : b;
   }
+  if (odd & 0x7fff7fffu) sh.odd = 1;
 }
 
 // s[2 i], s[2 i + 1]: a lane's rows 16 warp + g (+ 8), columns 16 i + 4 t .. + 3.
@@ -132,32 +136,13 @@ __device__ __forceinline__ void times(float (&c)[2][4], float (&d)[2][4], const 
   }
 }
 
-// What Y's infinities and NaN add to the rows that read them.
-__device__ __noinline__ void add_odd(float (&c)[2][4], const uint32_t (&pr)[4], bool later, uint32_t y_at, int piece, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll 1
-  for (int j = 0; j < LB_ROWS; ++j) {
-    uint32_t y[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y[i]) : "r"(y_at + place(j, piece + i) + 4 * t) : "memory");
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t p = __shfl_sync(0xffffffffu, j < 8 ? pr[k] : pr[2 + k], (lane & ~3) | ((j & 7) >> 1));
-      const float w = j & 1 ? bf16_hi(p) : bf16_lo(p);
-      if (later ? j < g + 8 * k : j > g + 8 * k) continue;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (!is_finite(bf16_lo(y[i]))) c[i][2 * k] += w * bf16_lo(y[i]);
-        if (!is_finite(bf16_hi(y[i]))) c[i][2 * k + 1] += w * bf16_hi(y[i]);
-      }
-    }
-  }
-}
-
 // c <- w c + P Y for the warp's 16 columns of Y, P = scale d with its rows' decays to each other, rounded to bf16:
-// row t reads rows up to t, or (later) from t on.
+// row t reads rows up to t, or (later) from t on.  odd: Y may hold infinities and NaN, which in the product would reach rows
+// that do not read them, as 0 times infinity.  They stay out of it, a second product counts how many of them each
+// row reads, and where that is any the result is NaN.  (Looking for them where rows are loaded takes 1 to 2%: 400 users' 16 rows
+// 151.2 -> 152.8 us, 64 rows 418 -> 425; where each product takes them 6%.)
 __device__ __forceinline__ void among(float (&c)[2][4], const float (&d)[2][4], const float* power, float w0, float w1, float scale, bool later,
-                                      uint32_t y_at, int piece, int lane) {
+                                      uint32_t y_at, int piece, int lane, bool odd) {
   const int g = lane >> 2, t = lane & 3;
   uint32_t pr[4], y[4];
 #pragma unroll
@@ -174,15 +159,26 @@ __device__ __forceinline__ void among(float (&c)[2][4], const float (&d)[2][4], 
     c[i][3] *= w1;
   }
   ldsm4_t(y, y_at + place(lane & 15, piece + (lane >> 4)));
-  // Y's infinities and NaN stay out of the product, where they would reach rows that do not read them (0 times infinity)
-  const bool odd = __any_sync(0xffffffffu, ((not_finite(y[0]) | not_finite(y[1]) | not_finite(y[2]) | not_finite(y[3])) & 0x80008000u) != 0);
-  if (odd) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = finite_part(y[k]);
+  if (!odd) {
+    mma_16816(c[0], pr, y[0], y[1]);
+    mma_16816(c[1], pr, y[2], y[3]);
+    return;
   }
-  mma_16816(c[0], pr, y[0], y[1]);
-  mma_16816(c[1], pr, y[2], y[3]);
-  if (odd) add_odd(c, pr, later, y_at, piece, lane);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float bad[4] = {};
+    uint32_t reads[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = g + 8 * (k & 1), col = 8 * (k >> 1) + 2 * t, gap = later ? col - row : row - col, next = later ? gap + 1 : gap - 1;
+      reads[k] = (gap >= 0 ? 0x3f80u : 0u) | (next >= 0 ? 0x3f800000u : 0u);
+    }
+    mma_16816(bad, reads, odd_ones(y[2 * i]), odd_ones(y[2 * i + 1]));
+    mma_16816(c[i], pr, finite_part(y[2 * i]), finite_part(y[2 * i + 1]));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (bad[k] > 0.f) c[i][k] = __int_as_float(0x7fffffff);
+  }
 }
 
 // Asks for a state in L2.
@@ -216,7 +212,10 @@ __global__ void __launch_bounds__(LB_THREADS, 2) lin_back_kernel(const __grid_co
     const int64_t stride = of == LB_Q ? p.qs : (of == LB_K ? p.ks : (of == LB_V ? p.vs : p.d_os));
     asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (static_cast<int64_t>(first) + (i >> 3)) * stride + h * LIN_D + 64 * (i & 1)) : "memory");
   }
-  const float log2_decay = log2f(__ldcg(p.decay + h));
+  const float decay = __ldcg(p.decay + h);
+  if (tid == 0) sh.odd = 0;
+  __syncthreads();
+  const float log2_decay = log2f(decay);
   if (tid <= LB_ROWS) sh.power[tid] = tid == 0 ? 1.f : exp2f(static_cast<float>(tid) * log2_decay);
   const auto power = [&](int n) { return n >= 0 ? sh.power[n] : 0.f; };
 #pragma unroll 1
@@ -224,9 +223,10 @@ __global__ void __launch_bounds__(LB_THREADS, 2) lin_back_kernel(const __grid_co
     const int n = min(LB_ROWS, len - r0);
     load_rows(p, sh, static_cast<int64_t>(first) + r0, n, h);
     __syncthreads();
+    const bool odd = sh.odd != 0;
     float c[2][4] = {}, d[2][4] = {};
     times(c, d, s, do_at, v_at, lane);
-    among(c, d, sh.power, sh.power[g + 1] * p.scale, sh.power[g + 9] * p.scale, p.scale, false, k_at, 2 * warp, lane);
+    among(c, d, sh.power, sh.power[g + 1] * p.scale, sh.power[g + 9] * p.scale, p.scale, false, k_at, 2 * warp, lane, odd);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (g + 8 * k >= n) continue;
@@ -251,11 +251,12 @@ __global__ void __launch_bounds__(LB_THREADS, 2) lin_back_kernel(const __grid_co
       load_rows(p, sh, row0, n, h);
       __syncthreads();
     }
+    const bool odd = sh.odd != 0;
     const float w0 = power(n - 1 - g), w1 = power(n - 9 - g);
     if (p.dk) {
       float c[2][4] = {}, d[2][4] = {};
       times(c, d, s, v_at, do_at, lane);
-      among(c, d, sh.power, w0, w1, p.scale, true, q_at, 2 * warp, lane);
+      among(c, d, sh.power, w0, w1, p.scale, true, q_at, 2 * warp, lane, odd);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (g + 8 * k >= n) continue;
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(LB_THREADS, 2) lin_back_kernel(const __grid_co
             c[i][2 * k] += v.x;
             c[i][2 * k + 1] += v.y;
           }
-      among(c, d, sh.power, w0, w1, p.scale, true, do_at, 2 * warp, lane);
+      among(c, d, sh.power, w0, w1, p.scale, true, do_at, 2 * warp, lane, odd);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         if (g + 8 * k < n)

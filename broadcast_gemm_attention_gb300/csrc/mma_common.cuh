@@ -56,10 +56,20 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x) { return (x & 0x7f807
 __device__ __forceinline__ uint32_t not_finite(const uint4& x) {
   return not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
 }
-// x without its halves that are infinite or NaN (0 in their place).
-__device__ __forceinline__ uint32_t finite_part(uint32_t x) {
-  const uint32_t odd = not_finite(x) & 0x80008000u;
-  return x & ~((odd >> 15) * 0xffffu);
+// x without its halves that are infinite or NaN, and ones where they are.
+__device__ __forceinline__ uint32_t finite_part(uint32_t x) { return x & ~(((not_finite(x) & 0x80008000u) >> 15) * 0xffffu); }
+__device__ __forceinline__ uint32_t odd_ones(uint32_t x) { return ((not_finite(x) & 0x80008000u) >> 15) * 0x3f80u; }
+// 0 times the halves of bf16 pairs: 0, of either sign, where none is infinite or NaN, else NaN; `or`ed.
+__device__ __forceinline__ uint32_t times_zero(uint32_t x) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0u));
+  return r;
+}
+__device__ __forceinline__ uint32_t times_zero(const uint4& x) {
+  return times_zero(x.x) | times_zero(x.y) | times_zero(x.z) | times_zero(x.w);
+}
+__device__ __forceinline__ uint32_t times_zero(const uint32_t (&x)[4]) {
+  return times_zero(x[0]) | times_zero(x[1]) | times_zero(x[2]) | times_zero(x[3]);
 }
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < INFINITY; }
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
