@@ -63,23 +63,29 @@ ikbo_status_t lin_params(ikbo_plan_t p, const int32_t* d_offsets, int n_users, i
 // others'.  In us, of a scan of L rows 6 + 0.0195 L whole, 13 + 0.041 seg + 0.07 (states between
 // segments) cut; the states alone 5 + 0.012 L and 10.8 + 0.0265 seg + 0.072 states (measured from 400 to
 // 6000 rows and 4 to 76 scans: 16 scans of 1152 rows 29 and 29, of 4096 86 and 43; 40 of 2048 48 and 56, of
-// 6000 126 and 104; 60 of 4096 89 and 122).  At most LIN_MOST_STATES states lie between segments, and with more than
-// LIN_MOST_CUT users none is cut (each item looks for its place among all users').
+// 6000 126 and 104; 60 of 4096 89 and 122).  The gradient, which has three scans for one and begins at both ends, goes
+// by the same: of 3 to 72 scans of 400 to 6000 rows it takes the faster way or one within 3% (12 scans of 1024 rows whole 26.7,
+// cut 26.3; 24 of 1024 26.8 and 31.0, of 2048 47.7 and 39.4; 48 of 6000 127.8 and 124.1; 72 of 6000 128 and 212).  At most
+// LIN_MOST_STATES states lie between segments, and with more than LIN_MOST_CUT users none is cut (each item looks for its place among all users').
 constexpr int64_t LIN_MOST_STATES = 16384;  // 1 GiB
 constexpr int LIN_LEAST_SEGMENT = 256;
 constexpr int LIN_MOST_CUT = 256;
 
-// The variant, from the bound on a user's rows (every variant takes any length).  Measured, 8 heads (us):
-//   forward, rows           15 users:  4     8    16    32    64   128   160   256   100 users: 8    16   128   160   256
-//   row by row                       4.3   5.7   8.3  13.7                                   28.4  40.6
-//   chunks, in registers                   6.0   6.1   6.9   8.2  12.1  14.7  20.3           31.9  32.9  70.3  85.9 118.3
-//   chunks, tensor memory                 13.6  13.6  13.9  14.1  14.1  14.0  14.6           75.5  81.6  90.2  75.8  80.9
-//   the states alone:  row by row 3.9 4.4 5.8 8.6, in registers 5.3 (8 rows) .. 8.3 (128) 12.0 (256) 18.7 (512), tensor
-//   memory 10.8 (8) .. 10.9 (128) 12.5 (256) 15.6 (512)
-constexpr int LIN_TILES_FROM[2] = {129, 257};  // forward, states alone
+// The variant, from the bound on a user's rows (every variant takes any length).  Measured, 8 heads, with states, among other
+// calls on the GPU (us):
+//   forward, rows           15 users:  4     8    16    64    96   128   160   256   100 users: 8    16    64    96   128   256
+//   row by row                       4.3   5.6   8.1  24.4        46.1  56.9  89.5           29.2  40.8             247   476
+//   chunks, in registers             6.1   6.1   6.1   8.2  10.9  12.3  15.0  20.5           33.3  33.6  48.4  63.5  71.2 120
+//   chunks, tensor memory           10.7  10.7  10.8  11.1  11.4  11.4  13.7  13.9           51.6  52.4  53.4  55.6  59.6  84.0
+//     (1 user 80 rows 10.0 and 9.2, 96 10.6 and 9.3; 40 users 80 27.9 and 24.7; 400 users 64 166 and 173, 80 206 and 175, 128 248 and 194)
+//   the states alone, rows  15 users:  8   128   192   224   256   320   100 users: 128   192   224   256   320
+//   chunks, in registers             4.9   7.6   9.4  10.6  11.2  13.0             35.6  44.9  51.1  55.1  64.3
+//   chunks, tensor memory            7.7   7.8   9.4   9.5   9.0  10.8             39.8  50.1  51.3  52.2  60.8
+//     (row by row, 15 users: 4 rows 4.3, 16 5.6; 400 users in chunks: 192 149 and 164, 224 170 and 168, 256 184 and 163)
+constexpr int LIN_TILES_FROM[2] = {96, 225};  // forward, states alone
 //   gradient, rows             15 users: 1    16    32    48    64    96   400 users: 1    16    32    48    64    96
-//   in one pass                        8.0   8.3  14.0  19.0  24.0  34.1          128.7 146.1 257.5 336.5 425.5 608.5
-//   chunks, tensor memory                         24.8  24.9  25.1  25.4                       432  433.3 438.2 448.1
+//   in one pass                        8.4   8.7  14.7  20.0  25.2  35.7            132   153   246   333   426   614
+//   chunks, tensor memory             24.6  24.9  25.4  25.4  25.6  25.9            436   437   442   443   444   452
 constexpr int LIN_BACK_MOST = 64;
 
 void cut_segments(LinParams* lp, int num_sms) {

@@ -553,7 +553,7 @@ ikbo_status_t ikbo_attn_qcache_tree_forward(ikbo_plan_t p, const void* Q, const 
  * n_users <= 8192, H <= 1024, d == 128; scale > 0, and so that 1 / scale is
  * finite; no ikbo_plan is needed.  States are held in fp32.  Any variant takes any
  * length; up to 8 rows a user they are taken one by one, in fp32, else in chunks of
- * 64 or (from 129 rows, the states alone from 257) 128 on the tensor cores: decayed
+ * 64 or (from 96 rows, the states alone from 225) 128 on the tensor cores: decayed
  * keys or values in two bf16 parts (2^-16) for the state, the products q_i.k_j with
  * their decays and, for O, the state rounded to bf16 (2^-8 each), fp32 sums.  An
  * infinity or NaN in a row reaches the outputs of its head that read the row, which are then

@@ -11,7 +11,7 @@ from test_gpu_linattn import SCALE, Data, bf, f32, plan, run_forward
 pytestmark = pytest.mark.gpu
 
 # rows of the first user, the row that is spoiled, and what the second user has
-VARIANTS = {"row_by_row": ([8, 5], 3), "registers": ([120, 64], 50), "registers_second_chunk": ([120, 64], 90), "one_pass": ([60, 64], 21),
+VARIANTS = {"row_by_row": ([8, 5], 3), "registers": ([90, 64], 50), "registers_second_chunk": ([90, 64], 80), "one_pass": ([60, 64], 21),
             "tiles": ([300, 130], 70), "tiles_second_chunk": ([300, 130], 181), "tiles_last_row": ([300, 130], 299), "cut": ([2600, 130], 1500)}
 COLUMNS = [0, 3, 17, 64, 126, 127]
 

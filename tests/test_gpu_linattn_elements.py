@@ -29,7 +29,7 @@ def skewed(users, long, seed):
     return [int(n) for n in lens]
 
 
-VARIANTS = [([5, 8, 0, 3], 8, 1), ([64, 20, 0, 65, 100], 128, 1), ([40, 64, 1, 33, 16, 17], 64, 1), ([130, 0, 300, 128, 1, 400], 400, 1),
+VARIANTS = [([5, 8, 0, 3], 8, 1), ([64, 20, 0, 65, 95], 95, 1), ([40, 64, 1, 33, 16, 17], 64, 1), ([130, 0, 300, 128, 1, 400], 400, 1),
             ([500] * 60 + [120, 0] * 20, 500, 1), ([2500, 300], 2500, 3)]
 
 
