@@ -90,7 +90,7 @@ __device__ __forceinline__ void one_by_one(float (&o)[2][4], uint32_t probs, uin
 // Bound: those products (603 TFLOP/s at most on this part, 117 kFLOP a row and head with
 // queries) and each chunk's chain; no state to set up in tensor memory, so the shorter
 // histories are its own.  Measured: the states of 15 users' 0 to 24 new rows, 8 heads,
-// 5.5 us; 15 histories of 1200 to 2048 rows 142 us (lintile.cu: 51.4).
+// 5.5 us; 15 histories of 1200 to 2048 rows 142 us (lintile.cu: 52).
 //
 // kOutputs: with queries; else the states alone.
 template <bool kOutputs>
@@ -414,7 +414,7 @@ cudaError_t launch_chunks(const LinParams& p, cudaStream_t s) {
 cudaError_t launch_lin_tiles(const LinParams& p, bool local, int num_sms, cudaStream_t s);
 
 // Launches: one, or three where histories are cut into segments (two users' 20000
-// and 30001 rows 83.9 us).
+// and 30001 rows 84.6 us).
 cudaError_t launch_linattn(const LinParams& p, int num_sms, cudaStream_t s, int* launches) {
   *launches = 0;
   const bool outputs = p.job[0].x != nullptr;

@@ -21,9 +21,9 @@
 // histories' is; sums and states are fp32.
 //
 // Bound: memory, with two CTAs on an SM whose chains (5.4 us alone) take turns.
-// 400 users, 8 heads: 16 rows 146 us, 4.6 TB/s (three scans in registers 348), one row
-// 129 (334); 15 users of 16 rows 8.3 us (14.6).  With the vector units and one row after
-// the other one row took 93, 4 rows 113 (134 here), 8 rows 171 (138), 16 rows 346.
+// 400 users, 8 heads: 16 rows 153 us, 4.4 TB/s (three scans in registers 348), one row
+// 132 (334); 15 users of 16 rows 8.7 us (14.6).  With the vector units and one row after
+// the other one row took 93, 4 rows 113 (for 134), 8 rows 171 (138), 16 rows 346.
 #include <cuda_bf16.h>
 
 #include "launch.cuh"

@@ -26,11 +26,11 @@
 // the outputs leave by way of the one whose products have ended (54.2 us with a place of
 // their own, 53.7 so; two buffers for z instead of x 55.0).
 //
-// Bound: shared memory, 576 KB a chunk, 4500 of the 4950 cycles that a chunk takes
-// (products 288, parts 96, image 32, outputs 64, loads 96).  15 histories of 1200 to
-// 2048 rows, 8 heads, bf16: 51.4 us, 12 of them start and end, 3.9 TB/s of the tensors'
-// bytes, 0.36 of the tensor pipe's cycles; with 16x8x16 products in registers
-// (linattn.cu) 142 us.  Their gradient at 524 to 1024 rows: 72.8 us (178).
+// Bound: a chunk of one scan takes 2.55 us, 5280 cycles, of which shared memory's 576 KB take 4608 (products 288,
+// parts 96, image 32, outputs 64, loads 96).  120 scans at a time move 6.05 TB/s (2.60 us), and 152 6.8, memory's
+// rate (2.92).  15 histories of 1200 to 2048 rows, 8 heads, bf16: 52.0 us, the longest's 16 chunks and 11 of start
+// and end, 3.9 TB/s of the tensors' bytes, 0.34 of the tensor pipe's cycles; with 16x8x16 products in registers
+// (linattn.cu) 142 us.  Their gradient at 524 to 1024 rows: 74 us (178).
 //
 // A reverse scan keeps the rows' order in its tiles and turns masks and decays around
 // instead (row j reaches i <= j, and the chunk's first row is its end).
