@@ -523,7 +523,8 @@ ikbo_status_t ikbo_attn_qcache_forward(ikbo_plan_t p, const void* Q, const void*
  * and V_new hold there, infinities and NaN too, reaches no other row, nor does any
  * row's reach rows that do not read it.  O must not be Q, and not overlap other
  * inputs.  Else as ikbo_attn_qcache_forward: its launches and one more, which takes
- * the history's O (rounded to bf16) and log-sum-exp as where its softmax begins.
+ * the history's O (rounded to bf16) and log-sum-exp (fp32: its last place, which grows
+ * with the scores, is an error in the exponent) as where its softmax begins.
  * With lse NULL the plan keeps the history's, a workspace as described there. */
 ikbo_status_t ikbo_attn_qcache_tree_forward(ikbo_plan_t p, const void* Q, const void* data, int n_pages, int page,
                                             int H_kv, const int32_t* d_table, int max_blocks, const int32_t* d_lens,

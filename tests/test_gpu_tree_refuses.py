@@ -42,7 +42,7 @@ def test_a_refused_call_allocates_nothing():
         free = torch.cuda.mem_get_info()[0]
         for other, code in BAD:
             assert call(p, c, **other) == code, other
-        assert torch.cuda.mem_get_info()[0] == free  # (the log-sum-exp takes 4 MB)
+        assert torch.cuda.mem_get_info()[0] >= free  # (the log-sum-exp takes 4 MB)
         assert p.launches() == 1 and torch.all(c.o == 3.0) and p.status() == B.IKBO_OK
 
 
